@@ -106,6 +106,7 @@ typedef enum { RSSM_ROUND_NEAREST = 0, RSSM_ROUND_STOCHASTIC = 1 } rssm_rounding
 #define RSSM_ERRBIT_SEQLEN 2u  /* a row's token count (cu_seqlens) < 0 or > T */
 #define RSSM_ERRBIT_ACCEPT 4u  /* accepted < 0 or > the row's token count */
 #define RSSM_ERRBIT_TIMEOUT 8u /* a kernel gave up waiting on its own copy pipeline */
+#define RSSM_ERRBIT_TOKEN 16u  /* rssm_verify: a drafted token id outside the vocabulary, or a row with no mass */
 
 /*
  * The cache of all slots.  Layouts follow the ring-buffer cache contract of
@@ -403,6 +404,146 @@ rssm_status rssm_step_static_scratch(const rssm_cache *cache, const void *x, con
                                      const void *B, const void *C, const float *D, const float *dt_bias,
                                      const int32_t *slot_idx, const int32_t *pnat, const int32_t *cu_seqlens,
                                      int32_t batch, int32_t T, void *out, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Operators of the layers next to the state update: the gated delta rule
+ * (the recurrence of the linear-attention layers that hybrid models mix with
+ * Mamba-2 layers), the verification of drafted tokens, and the norms between
+ * a state update and the projections around it.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * The gated delta rule's cache.  Per (slot, value head) a state
+ * S[dvalue][dkey] and, for each slot, the drafts of its last step, which wait
+ * for their verification in two halves that the steps use in turn:
+ * value head h uses key head h / (nvheads / nkheads).  Strides are in
+ * elements between slots, as in rssm_cache.
+ */
+typedef struct {
+  int32_t num_slots;   /* including padding slot 0 */
+  int32_t nkheads;     /* heads of q and k */
+  int32_t nvheads;     /* heads of v, g, beta and the state; a multiple of nkheads */
+  int32_t dkey;        /* 64 or 128 */
+  int32_t dvalue;      /* a multiple of 16, at most 1024 */
+  int32_t npredicted;  /* most tokens a step has, 1..8 */
+  int32_t state_dtype; /* RSSM_F32 or RSSM_BF16 (rounded to nearest when stored; all arithmetic is in fp32) */
+  void *state;   int64_t state_slot_stride;  /* [slot][nvheads][dvalue][dkey] */
+  void *pend_k;  int64_t pend_k_slot_stride; /* bf16 [slot][2][nkheads][npredicted][dkey]: keys as given */
+  float *pend_w; int64_t pend_w_slot_stride; /* f32 [slot][2][nvheads][npredicted][dvalue]: corrections u_t (over |k_t| with l2norm) */
+  float *pend_c; int64_t pend_c_slot_stride; /* f32 [slot][2][nvheads][npredicted]: running sums of g over the step */
+  int32_t *pend;       /* [slot][2]: the half that holds the last step's drafts, and how many they are; 8-byte aligned */
+  uint32_t *error_word;
+} rssm_delta_cache;
+
+/* Bytes of scratch rssm_delta_step and rssm_delta_prefill need for `batch`
+ * rows and `tokens` tokens in all; 0 for an invalid cache.  Zero the buffer
+ * once when it is allocated (its first `batch` words are counters that every
+ * call leaves at zero).  One buffer serves both calls and every smaller one. */
+size_t rssm_delta_scratch_bytes(const rssm_delta_cache *cache, int32_t batch, int64_t tokens);
+
+/*
+ * One decode step of the gated delta rule.  For row b (slot s, T_b tokens) and
+ * value head h, first the accepted drafts of the slot's last step enter the
+ * state, j < a = accepted[b] (NULL: none):
+ *   S <- e^{c_{a-1}} S + sum_j e^{c_{a-1} - c_j} w_j (outer) k_j
+ * written back in the state format if a > 0 (a row of T_b = 0 tokens does only
+ * this).  Then the new tokens, from the unrounded S, which they do not change:
+ *   S_t = e^{g_t} S_{t-1} + u_t (outer) k_t,  u_t = beta_t (v_t - e^{g_t} S_{t-1} k_t),
+ *   out_t = scale S_t q_t, rounded to bf16
+ * and their (k_t, u_t, running sum of g) wait in the slot's other half.
+ * l2norm = 1: q_t and k_t are divided by sqrt(|.|^2 + 1e-6) first.  Log decays
+ * below -100 count as -100.
+ *   q, k bf16 [tok][nkheads][dkey], v bf16 [tok][nvheads][dvalue]: *_stride
+ *        elements between tokens (multiples of 8; 16-byte aligned pointers),
+ *        heads contiguous
+ *   g, beta f32 [tok][nvheads]; out bf16 [tok][nvheads][dvalue], dense
+ *   slot_idx, accepted [batch] i32; cu_seqlens [batch+1] i32 or NULL (T a row)
+ *   T 1..npredicted: most tokens of a row;  tokens: token rows of q, k, v, out
+ * Rows of slot ids <= 0 or >= num_slots get zero outputs.  accepted < 0 or
+ * more than the waiting drafts: RSSM_ERRBIT_ACCEPT, zero outputs, the slot
+ * untouched.  Token bounds that are negative, longer than T or past `tokens`:
+ * RSSM_ERRBIT_SEQLEN, the row is skipped.
+ */
+rssm_status rssm_delta_step(const rssm_delta_cache *cache, const void *q, int64_t q_stride, const void *k,
+                            int64_t k_stride, const void *v, int64_t v_stride, const float *g, const float *beta,
+                            float scale, int32_t l2norm, const int32_t *slot_idx, const int32_t *accepted,
+                            const int32_t *cu_seqlens, int32_t batch, int32_t T, int64_t tokens, void *out,
+                            void *scratch, size_t scratch_bytes, void *stream);
+
+/*
+ * The gated delta rule over whole prompts: outputs of every token, and the
+ * state after the last one in each row's slot (no drafts wait afterwards).
+ * Arguments as in rssm_delta_step, and
+ *   cu_seqlens [batch+1] i32: the prompts' bounds (any lengths, 0 too)
+ *   initial [batch] i32 or NULL: nonzero rows start from their slot's state
+ *           (a prompt that comes in parts), the others from zero
+ * Drafts that wait in a slot are dropped.
+ */
+rssm_status rssm_delta_prefill(const rssm_delta_cache *cache, const void *q, int64_t q_stride, const void *k,
+                               int64_t k_stride, const void *v, int64_t v_stride, const float *g, const float *beta,
+                               float scale, int32_t l2norm, const int32_t *slot_idx, const int32_t *cu_seqlens,
+                               const int32_t *initial, int32_t batch, int64_t tokens, void *out, void *scratch,
+                               size_t scratch_bytes, void *stream);
+
+/*
+ * Verification of drafted tokens, from given random numbers.  Row b was fed
+ * T_b tokens: the last sampled one and T_b - 1 drafts.  target[tok] are the
+ * target's probabilities after token tok, draft[tok] those that draft tok was
+ * drawn from (a row's first is not read); draft = NULL: drafts that are
+ * certain (a lookup's).  Draft t = 1, 2, .. is accepted while
+ *   u[t] * draft[t][token_t] < target[t-1][token_t]
+ * (one fp32 product; draft = 1 if NULL).  With t drafts accepted,
+ * accepted[b] = t + 1 tokens join the live prefix -- what rssm_accept,
+ * rssm_accept_flush and rssm_delta_step take -- and next[b] is drawn from
+ *   max(target[t] - draft[t+1], 0)  after a rejected draft (draft is 1 at a
+ *                                   certain one's id), or target[t] if
+ *                                   nothing of that is left
+ *   target[t]                       if every draft was accepted
+ * by inversion: weights w_i = floor(2^36 min(r_i, 1)) (negative and NaN: 0),
+ * W = sum w, next = the first i with w_0 + .. + w_i > floor(W u24 2^-24), u24 =
+ * floor(2^24 u_next[b]).  All of it is integer or single fp32 operations: the
+ * same result whatever the grid.
+ *   target, draft [tok] rows of vocab values of prob_dtype (F32, BF16, F16),
+ *        *_stride elements between rows;  tokens [ntok] i32, u [ntok] f32
+ *   u_next, accepted, next [batch];  T 1..32;  error_word may be NULL
+ * A row with T_b = 0: accepted 0, next -1.  Bad bounds: the same, and
+ * RSSM_ERRBIT_SEQLEN.  A draft id outside the vocabulary is rejected
+ * (RSSM_ERRBIT_TOKEN); a row with no mass at all: next -1, RSSM_ERRBIT_TOKEN.
+ */
+rssm_status rssm_verify(const void *target, int64_t target_stride, const void *draft, int64_t draft_stride,
+                        int32_t prob_dtype, int32_t vocab, const int32_t *tokens, const float *u, const float *u_next,
+                        const int32_t *cu_seqlens, int32_t batch, int32_t T, int64_t ntok, int32_t *accepted,
+                        int32_t *next, uint32_t *error_word, void *stream);
+
+/*
+ * The norm after a mixer with its silu gate, over groups of `group` channels
+ * (Mamba-2: dim / ngroups; per head: the head's width):
+ *   norm_first = 0:  y = x silu(z);  out = y / sqrt(mean(y^2) + eps) * weight
+ *   norm_first = 1:  out = x / sqrt(mean(x^2) + eps) * weight * silu(z)
+ * in fp32, rounded once.  x, z, out [rows][dim] of dtype (F32, BF16, F16),
+ * *_stride elements between rows; weight f32 [dim], or [group] for all groups
+ * (shared_weight = 1).  out may be x.
+ */
+rssm_status rssm_gated_norm(const void *x, int64_t x_stride, const void *z, int64_t z_stride, int32_t dtype,
+                            const float *weight, int32_t shared_weight, int64_t rows, int32_t dim, int32_t group,
+                            float eps, int32_t norm_first, void *out, int64_t out_stride, void *stream);
+
+/*
+ * Between two blocks: the norm after the block (post_weight, or NULL: none),
+ * its residual scale (per channel, or NULL: 1; times alpha), the residual add
+ * and the norm before the next block:
+ *   m = x / sqrt(mean(x^2) + eps) * post_weight   (x without post_weight)
+ *   h = residual + alpha * scale * m              -> residual_out
+ *   out = h / sqrt(mean(h^2) + eps) * weight      (from the unrounded h)
+ * x, out of dtype (F32, BF16, F16); residual, residual_out of residual_dtype
+ * (F32 or dtype); post_weight, scale, weight f32 [dim].  residual_out may be
+ * residual, and out may be x.
+ */
+rssm_status rssm_residual_norm(const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                               int32_t dtype, int32_t residual_dtype, const float *post_weight, const float *scale,
+                               float alpha, const float *weight, int64_t rows, int32_t dim, float eps,
+                               void *residual_out, int64_t residual_out_stride, void *out, int64_t out_stride,
+                               void *stream);
 
 #ifdef __cplusplus
 }

@@ -32,9 +32,25 @@ class RssmCacheStruct(ctypes.Structure):
     ]
 
 
+class RssmDeltaCacheStruct(ctypes.Structure):
+    """Mirror of `rssm_delta_cache` in include/rssm.h."""
+
+    _fields_ = [
+        ("num_slots", ctypes.c_int32), ("nkheads", ctypes.c_int32), ("nvheads", ctypes.c_int32),
+        ("dkey", ctypes.c_int32), ("dvalue", ctypes.c_int32), ("npredicted", ctypes.c_int32),
+        ("state_dtype", ctypes.c_int32),
+        ("state", ctypes.c_void_p), ("state_slot_stride", ctypes.c_int64),
+        ("pend_k", ctypes.c_void_p), ("pend_k_slot_stride", ctypes.c_int64),
+        ("pend_w", ctypes.c_void_p), ("pend_w_slot_stride", ctypes.c_int64),
+        ("pend_c", ctypes.c_void_p), ("pend_c_slot_stride", ctypes.c_int64),
+        ("pend", ctypes.c_void_p), ("error_word", ctypes.c_void_p),
+    ]
+
+
 EXPORTS = ("rssm_scratch_bytes", "rssm_init_state", "rssm_flush", "rssm_step", "rssm_step_precompute",
            "rssm_step_readout", "rssm_step_gated", "rssm_step_readout_gated", "rssm_flush_step", "rssm_flush_step_classify", "rssm_flush_step_main", "rssm_accept", "rssm_accept_flush", "rssm_eval_spec_math", "rssm_selftest_wait_timeout",
-           "rssm_status_string")
+           "rssm_status_string", "rssm_delta_scratch_bytes", "rssm_delta_step", "rssm_delta_prefill", "rssm_verify",
+           "rssm_gated_norm", "rssm_residual_norm")
 
 
 def load(path: str | None = None):
@@ -75,6 +91,21 @@ def load(path: str | None = None):
         lib.rssm_eval_spec_math.argtypes = [vp, vp, vp, i64, vp]
         lib.rssm_selftest_wait_timeout.restype = ctypes.c_int
         lib.rssm_selftest_wait_timeout.argtypes = [vp, i32, vp]
+        f32, dp = ctypes.c_float, ctypes.POINTER(RssmDeltaCacheStruct)
+        lib.rssm_delta_scratch_bytes.restype = sz
+        lib.rssm_delta_scratch_bytes.argtypes = [dp, i32, i64]
+        tok_args = [dp, vp, i64, vp, i64, vp, i64, vp, vp, f32, i32, vp]  # cache, q, k, v, g, beta, scale, l2norm, slots
+        lib.rssm_delta_step.restype = ctypes.c_int
+        lib.rssm_delta_step.argtypes = tok_args + [vp, vp, i32, i32, i64, vp, vp, sz, vp]
+        lib.rssm_delta_prefill.restype = ctypes.c_int
+        lib.rssm_delta_prefill.argtypes = tok_args + [vp, vp, i32, i64, vp, vp, sz, vp]
+        lib.rssm_verify.restype = ctypes.c_int
+        lib.rssm_verify.argtypes = [vp, i64, vp, i64, i32, i32, vp, vp, vp, vp, i32, i32, i64, vp, vp, vp, vp]
+        lib.rssm_gated_norm.restype = ctypes.c_int
+        lib.rssm_gated_norm.argtypes = [vp, i64, vp, i64, i32, vp, i32, i64, i32, i32, f32, i32, vp, i64, vp]
+        lib.rssm_residual_norm.restype = ctypes.c_int
+        lib.rssm_residual_norm.argtypes = [vp, i64, vp, i64, i32, i32, vp, vp, f32, vp, i64, i32, f32, vp, i64, vp, i64,
+                                           vp]
         lib.rssm_status_string.restype = ctypes.c_char_p
         lib.rssm_status_string.argtypes = [ctypes.c_int]
         _lib = lib

@@ -15,7 +15,7 @@ from . import _lib
 
 F32, BF16, F16, I8, E4M3, NVFP4 = 0, 1, 2, 3, 4, 5
 NEAREST, STOCHASTIC = 0, 1
-ERRBIT_PNAT, ERRBIT_SEQLEN, ERRBIT_ACCEPT, ERRBIT_TIMEOUT = 1, 2, 4, 8
+ERRBIT_PNAT, ERRBIT_SEQLEN, ERRBIT_ACCEPT, ERRBIT_TIMEOUT, ERRBIT_TOKEN = 1, 2, 4, 8, 16
 DIM, DSTATE = 64, 128
 STATE_TORCH = {F32: torch.float32, BF16: torch.int16, F16: torch.int16, I8: torch.int8, E4M3: torch.uint8,
                NVFP4: torch.uint8}
@@ -267,3 +267,229 @@ def rssm_selftest_wait_timeout(error_word, wait_ms=50, stream=None):
     """Diagnostics: one bounded mbarrier wait that runs out (sets ERRBIT_TIMEOUT)."""
     _check("rssm_selftest_wait_timeout", _lib.load().rssm_selftest_wait_timeout(_ptr(error_word), wait_ms,
                                                                                 _stream(stream)))
+
+
+# --------------------------------------------------------------------------
+# Operators of the layers next to the state update: the gated delta rule,
+# verification of drafted tokens, and the norms around a block.  Activations
+# are torch tensors of their own types here (bf16, f16, f32); the checks below
+# read no device data.
+# --------------------------------------------------------------------------
+_DTYPE = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+
+
+def _need(fn, ok, text):
+    if not ok:
+        raise ValueError(f"{fn}: {text}")
+
+
+def _ids(fn, name, t, n):
+    _need(fn, t.dtype is torch.int32 and t.is_contiguous() and t.numel() >= n,
+          f"{name} must be a contiguous int32 tensor of at least {n} values")
+
+
+def _f32(fn, name, t, n):
+    _need(fn, t.dtype is torch.float32 and t.is_contiguous() and t.numel() >= n,
+          f"{name} must be a contiguous float32 tensor of at least {n} values")
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _s(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+class DeltaCache:
+    """The gated delta rule's cache (rssm_delta_cache): states [S][Hv][dv][dk] in f32 or bf16, and the drafts of every
+    slot's last step (`pend_*`, two halves).  Tensors that a program already has can be given instead of new ones; a
+    slot's part must be contiguous, slots may be further apart.
+    """
+
+    def __init__(self, num_slots, k_heads, v_heads, key_dim, value_dim, npredicted, state_dtype=F32, device="cuda",
+                 state=None, pend_k=None, pend_w=None, pend_c=None, pend=None, error_word=None):
+        fn = "DeltaCache"
+        _need(fn, state_dtype in (F32, BF16), "state_dtype must be F32 or BF16")
+        self.S, self.Hk, self.Hv, self.dk, self.dv, self.Tmax = num_slots, k_heads, v_heads, key_dim, value_dim, npredicted
+        self.state_dtype = state_dtype
+        dev = torch.device(device)
+
+        def make(name, t, shape, dtype):
+            if t is None:
+                return torch.zeros(shape, dtype=dtype, device=dev)
+            dense = [1] * len(shape)
+            for i in range(len(shape) - 2, 0, -1):
+                dense[i] = dense[i + 1] * shape[i + 1]
+            fits = all(n == 1 or x == d for n, x, d in zip(shape[1:], t.stride()[1:], dense[1:]))
+            _need(fn, tuple(t.shape) == shape and t.dtype is dtype and fits,
+                  f"{name} must be {dtype} {list(shape)}, contiguous within a slot")
+            return t
+
+        self.state = make("state", state, (num_slots, v_heads, value_dim, key_dim),
+                          torch.float32 if state_dtype == F32 else torch.bfloat16)
+        self.pend_k = make("pend_k", pend_k, (num_slots, 2, k_heads, npredicted, key_dim), torch.bfloat16)
+        self.pend_w = make("pend_w", pend_w, (num_slots, 2, v_heads, npredicted, value_dim), torch.float32)
+        self.pend_c = make("pend_c", pend_c, (num_slots, 2, v_heads, npredicted), torch.float32)
+        self.pend = make("pend", pend, (num_slots, 2), torch.int32)
+        _need(fn, self.pend.is_contiguous(), "pend must be contiguous")
+        self.error_word = make("error_word", error_word, (1,), torch.int32)
+        c = _lib.RssmDeltaCacheStruct()
+        c.num_slots, c.nkheads, c.nvheads, c.dkey, c.dvalue = num_slots, k_heads, v_heads, key_dim, value_dim
+        c.npredicted, c.state_dtype = npredicted, state_dtype
+        for name in ("state", "pend_k", "pend_w", "pend_c"):
+            t = getattr(self, name)
+            setattr(c, name, t.data_ptr())
+            setattr(c, name + "_slot_stride", t.stride(0))
+        c.pend, c.error_word = self.pend.data_ptr(), self.error_word.data_ptr()
+        self._struct = c
+        self._ref = ctypes.byref(c)
+
+    def struct(self):
+        return self._ref
+
+
+def rssm_delta_scratch_bytes(cache: DeltaCache, batch: int, tokens: int) -> int:
+    return int(_lib.load().rssm_delta_scratch_bytes(cache.struct(), batch, tokens))
+
+
+def alloc_delta_scratch(cache: DeltaCache, batch: int, tokens: int) -> torch.Tensor:
+    """Scratch for steps and prompts of up to `batch` rows and `tokens` tokens."""
+    n = rssm_delta_scratch_bytes(cache, batch, tokens)
+    if n == 0:
+        raise RssmError("rssm_delta_scratch_bytes", 1)
+    return torch.zeros(n, dtype=torch.uint8, device=cache.state.device)  # its counters start at zero
+
+
+def _delta_tokens(fn, cache, q, k, v, g, beta, out):
+    bf16, n = torch.bfloat16, q.shape[0]
+    for name, t, h, d in (("q", q, cache.Hk, cache.dk), ("k", k, cache.Hk, cache.dk), ("v", v, cache.Hv, cache.dv),
+                          ("out", out, cache.Hv, cache.dv)):
+        _need(fn, t.dtype is bf16 and t.shape == (n, h, d) and (n == 0 or h * d == 0 or t.stride(2) == 1) and
+              (h == 1 or t.stride(1) == d), f"{name} must be bfloat16 [{n}, {h}, {d}] with contiguous heads")
+    _need(fn, out.is_contiguous(), "out must be contiguous")
+    _f32(fn, "g", g, n * cache.Hv)
+    _f32(fn, "beta", beta, n * cache.Hv)
+    return n
+
+
+def _row_stride(t, row):
+    """Elements between the rows of t; a single row has no stride that matters."""
+    return t.stride(0) if t.shape[0] > 1 else row
+
+
+def rssm_delta_step(cache, q, k, v, g, beta, slot_idx, accepted, T, out, scratch, cu_seqlens=None, scale=None,
+                    l2norm=False, stream=None):
+    """One decode step of the gated delta rule: commits the accepted drafts of the last step, then runs the new tokens.
+
+    q, k [tok, k_heads, key_dim], v and out [tok, v_heads, value_dim] bf16 (q, k, v may be columns of one projection);
+    g, beta [tok, v_heads] f32; `scale` defaults to key_dim ** -0.5."""
+    fn = "rssm_delta_step"
+    n = _delta_tokens(fn, cache, q, k, v, g, beta, out)
+    batch = slot_idx.numel()
+    _ids(fn, "slot_idx", slot_idx, batch)
+    if accepted is not None:
+        _ids(fn, "accepted", accepted, batch)
+    if cu_seqlens is not None:
+        _ids(fn, "cu_seqlens", cu_seqlens, batch + 1)
+    status = _lib.load().rssm_delta_step(
+        cache.struct(), q.data_ptr(), _row_stride(q, cache.Hk * cache.dk), k.data_ptr(),
+        _row_stride(k, cache.Hk * cache.dk), v.data_ptr(), _row_stride(v, cache.Hv * cache.dv), g.data_ptr(),
+        beta.data_ptr(), cache.dk ** -0.5 if scale is None else scale, int(l2norm), slot_idx.data_ptr(), _p(accepted),
+        _p(cu_seqlens), batch, T, n, out.data_ptr(), scratch.data_ptr(), scratch.numel(), _s(stream))
+    if status:
+        raise RssmError(fn, status)
+
+
+def rssm_delta_prefill(cache, q, k, v, g, beta, slot_idx, cu_seqlens, out, scratch, initial=None, scale=None,
+                       l2norm=False, stream=None):
+    """The gated delta rule over whole prompts (tensors as in rssm_delta_step): outputs, and each slot's state after
+    its prompt.  initial [batch] int32: nonzero rows go on from their slot's state."""
+    fn = "rssm_delta_prefill"
+    n = _delta_tokens(fn, cache, q, k, v, g, beta, out)
+    batch = slot_idx.numel()
+    _ids(fn, "slot_idx", slot_idx, batch)
+    _ids(fn, "cu_seqlens", cu_seqlens, batch + 1)
+    if initial is not None:
+        _ids(fn, "initial", initial, batch)
+    status = _lib.load().rssm_delta_prefill(
+        cache.struct(), q.data_ptr(), _row_stride(q, cache.Hk * cache.dk), k.data_ptr(),
+        _row_stride(k, cache.Hk * cache.dk), v.data_ptr(), _row_stride(v, cache.Hv * cache.dv), g.data_ptr(),
+        beta.data_ptr(), cache.dk ** -0.5 if scale is None else scale, int(l2norm), slot_idx.data_ptr(),
+        cu_seqlens.data_ptr(), _p(initial), batch, n, out.data_ptr(), scratch.data_ptr(), scratch.numel(), _s(stream))
+    if status:
+        raise RssmError(fn, status)
+
+
+def rssm_verify(target, tokens, u, u_next, T, accepted, next_token, draft=None, cu_seqlens=None, error_word=None,
+                stream=None):
+    """Accepted counts and next tokens of a speculative step; target (and draft) [tok, vocab] probabilities."""
+    fn = "rssm_verify"
+    ntok, vocab = target.shape
+    batch = u_next.numel()
+    _need(fn, target.dtype in _DTYPE and (vocab == 1 or target.stride(1) == 1), "target must be f32, bf16 or f16 rows")
+    if draft is not None:
+        _need(fn, draft.dtype is target.dtype and draft.shape == target.shape and (vocab == 1 or draft.stride(1) == 1),
+              "draft must have target's type and shape")
+    _ids(fn, "tokens", tokens, ntok)
+    _f32(fn, "u", u, ntok)
+    _f32(fn, "u_next", u_next, batch)
+    _ids(fn, "accepted", accepted, batch)
+    _ids(fn, "next_token", next_token, batch)
+    if cu_seqlens is not None:
+        _ids(fn, "cu_seqlens", cu_seqlens, batch + 1)
+    status = _lib.load().rssm_verify(
+        target.data_ptr(), _row_stride(target, vocab), _p(draft), 0 if draft is None else _row_stride(draft, vocab),
+        _DTYPE[target.dtype], vocab, tokens.data_ptr(), u.data_ptr(), u_next.data_ptr(), _p(cu_seqlens), batch, T, ntok,
+        accepted.data_ptr(), next_token.data_ptr(), _p(error_word), _s(stream))
+    if status:
+        raise RssmError(fn, status)
+
+
+def _rows(fn, name, t, dtype, shape):
+    _need(fn, t.dtype is dtype and t.shape == shape and (shape[1] == 1 or t.stride(1) == 1),
+          f"{name} must be {dtype} {list(shape)} with contiguous rows")
+
+
+def rssm_gated_norm(x, z, weight, out, group=None, eps=1e-5, norm_first=False, stream=None):
+    """RMS norm over groups of channels with the silu gate z, before the norm or (norm_first) after it; x, z, out
+    [rows, dim], weight f32 [dim], or [group] for every group."""
+    fn = "rssm_gated_norm"
+    rows, dim = x.shape
+    group = dim if group is None else group
+    _need(fn, x.dtype in _DTYPE, "x must be f32, bf16 or f16")
+    _rows(fn, "x", x, x.dtype, x.shape)
+    _rows(fn, "z", z, x.dtype, x.shape)
+    _rows(fn, "out", out, x.dtype, x.shape)
+    _need(fn, weight.numel() in (dim, group), f"weight must hold {dim} or {group} values")
+    _f32(fn, "weight", weight, 1)
+    status = _lib.load().rssm_gated_norm(
+        x.data_ptr(), _row_stride(x, dim), z.data_ptr(), _row_stride(z, dim), _DTYPE[x.dtype], weight.data_ptr(),
+        int(weight.numel() != dim), rows, dim, group, eps, int(norm_first), out.data_ptr(), _row_stride(out, dim),
+        _s(stream))
+    if status:
+        raise RssmError(fn, status)
+
+
+def rssm_residual_norm(x, residual, weight, out, residual_out, post_weight=None, scale=None, alpha=1.0, eps=1e-5,
+                       stream=None):
+    """residual_out = residual + alpha scale [norm](x), out = norm(residual_out) weight; [rows, dim] each, the
+    residual in x's type or f32, weights f32 [dim]."""
+    fn = "rssm_residual_norm"
+    rows, dim = x.shape
+    _need(fn, x.dtype in _DTYPE and residual.dtype in (torch.float32, x.dtype), "types must be f32, bf16 or f16, the "
+          "residual's f32 or x's")
+    _rows(fn, "x", x, x.dtype, x.shape)
+    _rows(fn, "out", out, x.dtype, x.shape)
+    _rows(fn, "residual", residual, residual.dtype, x.shape)
+    _rows(fn, "residual_out", residual_out, residual.dtype, x.shape)
+    for name, t in (("weight", weight), ("post_weight", post_weight), ("scale", scale)):
+        if t is not None:
+            _need(fn, t.numel() == dim, f"{name} must hold {dim} values")
+            _f32(fn, name, t, dim)
+    status = _lib.load().rssm_residual_norm(
+        x.data_ptr(), _row_stride(x, dim), residual.data_ptr(), _row_stride(residual, dim), _DTYPE[x.dtype],
+        _DTYPE[residual.dtype], _p(post_weight), _p(scale), alpha, weight.data_ptr(), rows, dim, eps,
+        residual_out.data_ptr(), _row_stride(residual_out, dim), out.data_ptr(), _row_stride(out, dim), _s(stream))
+    if status:
+        raise RssmError(fn, status)

@@ -1,0 +1,402 @@
+// rssm_norm.cu -- the norms around a block: the mixer's output norm with its
+// silu gate, and the residual add between the norm after a block and the one
+// before the next.
+#include "rssm_device.cuh"
+
+namespace rssm {
+namespace {
+
+template <typename E>
+struct Elem;
+template <>
+struct Elem<float> {
+  static __device__ __forceinline__ float to(float x) { return x; }
+  static __device__ __forceinline__ float from(float x) { return x; }
+};
+template <>
+struct Elem<__nv_bfloat16> {
+  static __device__ __forceinline__ float to(__nv_bfloat16 x) { return __bfloat162float(x); }
+  static __device__ __forceinline__ __nv_bfloat16 from(float x) { return __float2bfloat16_rn(x); }
+};
+template <>
+struct Elem<__half> {
+  static __device__ __forceinline__ float to(__half x) { return __half2float(x); }
+  static __device__ __forceinline__ __half from(float x) { return __float2half_rn(x); }
+};
+
+// VEC elements of type E as floats, in 16-byte pieces (one element where VEC is 1)
+template <typename E, int VEC>
+__device__ __forceinline__ void load_vec(const E* p, float (&f)[VEC]) {
+  if constexpr (VEC == 1) {
+    f[0] = Elem<E>::to(*p);
+  } else {
+    constexpr int W = VEC * sizeof(E) / 16, N = 16 / sizeof(E);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const uint4 raw = reinterpret_cast<const uint4*>(p)[w];
+      const E* e = reinterpret_cast<const E*>(&raw);
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[w * N + i] = Elem<E>::to(e[i]);
+    }
+  }
+}
+template <typename E, int VEC>
+__device__ __forceinline__ void store_vec(E* p, const float (&f)[VEC]) {
+  if constexpr (VEC == 1) {
+    *p = Elem<E>::from(f[0]);
+  } else {
+    constexpr int W = VEC * sizeof(E) / 16, N = 16 / sizeof(E);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      uint4 raw;
+      E* e = reinterpret_cast<E*>(&raw);
+#pragma unroll
+      for (int i = 0; i < N; ++i) e[i] = Elem<E>::from(f[w * N + i]);
+      reinterpret_cast<uint4*>(p)[w] = raw;
+    }
+  }
+}
+
+__device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+
+// Sum over a team of TEAM lanes of a warp, or over the block (TEAM 0).
+template <int TEAM>
+__device__ __forceinline__ float team_sum(float v, float* sh) {
+  constexpr int W = TEAM == 0 ? 32 : TEAM;
+#pragma unroll
+  for (int o = W / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (TEAM == 0) {
+    const int warps = blockDim.x >> 5;
+    __syncthreads();  // an earlier sum's parts are read
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.0f;
+    for (int w = 0; w < warps; ++w) v += sh[w];
+  }
+  return v;
+}
+
+struct GatedNormArgs {
+  const void* x;
+  const void* z;
+  const float* w;
+  void* out;
+  long long x_stride, z_stride, out_stride;
+  long long rows;
+  int groups, group, w_group;  // w_group: weights between groups (0: one set for all)
+  float eps;
+  int norm_first;
+};
+
+// A team of lanes (TEAM of a warp, or a block) per (row, group), the group's
+// values in NV vectors a lane; NV 0: groups too long for that, read twice.
+template <typename E, int VEC, int TEAM, int NV>
+__global__ void __launch_bounds__(TEAM == 0 ? 1024 : 256) gated_norm_kernel(const GatedNormArgs a) {
+  __shared__ float sh[32];
+  pdl_wait();
+  pdl_trigger();
+  const int width = TEAM == 0 ? static_cast<int>(blockDim.x) : TEAM;
+  const long long item = TEAM == 0 ? blockIdx.x : (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / (TEAM ? TEAM : 1);
+  const int lane = TEAM == 0 ? threadIdx.x : threadIdx.x % (TEAM ? TEAM : 1);
+  const bool live = item < a.rows * a.groups;
+  const long long row = live ? item / a.groups : 0;
+  const int grp = live ? static_cast<int>(item - row * a.groups) : 0;
+  const E* x = static_cast<const E*>(a.x) + row * a.x_stride + static_cast<long long>(grp) * a.group;
+  const E* z = static_cast<const E*>(a.z) + row * a.z_stride + static_cast<long long>(grp) * a.group;
+  E* out = static_cast<E*>(a.out) + row * a.out_stride + static_cast<long long>(grp) * a.group;
+  const float* w = a.w + static_cast<long long>(grp) * a.w_group;
+  const int n = live ? a.group : 0;
+  float sum = 0.0f;
+  if constexpr (NV > 0) {
+    float fx[NV][VEC], fz[NV][VEC];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int i = (v * width + lane) * VEC;
+      if (i < n) {
+        load_vec<E, VEC>(x + i, fx[v]);
+        load_vec<E, VEC>(z + i, fz[v]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) fx[v][e] = fz[v][e] = 0.0f;
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        fz[v][e] = silu(fz[v][e]);
+        if (!a.norm_first) fx[v][e] *= fz[v][e];
+        sum = fmaf(fx[v][e], fx[v][e], sum);
+      }
+    sum = team_sum<TEAM>(sum, sh);
+    const float r = rsqrtf(sum / a.group + a.eps);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int i = (v * width + lane) * VEC;
+      if (i < n) {
+        float fw[VEC];
+        load_vec<float, VEC>(w + i, fw);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          fw[e] *= fx[v][e] * r;
+          if (a.norm_first) fw[e] *= fz[v][e];
+        }
+        store_vec<E, VEC>(out + i, fw);
+      }
+    }
+  } else {
+    for (int i = lane * VEC; i < n; i += width * VEC) {
+      float fx[VEC], fz[VEC];
+      load_vec<E, VEC>(x + i, fx);
+      if (!a.norm_first) load_vec<E, VEC>(z + i, fz);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        if (!a.norm_first) fx[e] *= silu(fz[e]);
+        sum = fmaf(fx[e], fx[e], sum);
+      }
+    }
+    sum = team_sum<TEAM>(sum, sh);
+    const float r = rsqrtf(sum / a.group + a.eps);
+    for (int i = lane * VEC; i < n; i += width * VEC) {
+      float fx[VEC], fz[VEC], fw[VEC];
+      load_vec<E, VEC>(x + i, fx);
+      load_vec<E, VEC>(z + i, fz);
+      load_vec<float, VEC>(w + i, fw);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) fw[e] = a.norm_first ? fx[e] * r * fw[e] * silu(fz[e]) : fx[e] * silu(fz[e]) * r * fw[e];
+      store_vec<E, VEC>(out + i, fw);
+    }
+  }
+}
+
+struct ResidualNormArgs {
+  const void* x;
+  const void* residual;
+  const float* post;
+  const float* scale;
+  const float* w;
+  void* residual_out;
+  void* out;
+  long long x_stride, residual_stride, residual_out_stride, out_stride;
+  int dim;
+  float alpha, eps;
+};
+
+// One block per row, the row's values in NV vectors a thread; NV 0: rows too
+// long for that, read once per sum and once more to write.
+template <typename E, typename R, int VEC, int NV>
+__global__ void __launch_bounds__(1024) residual_norm_kernel(const ResidualNormArgs a) {
+  __shared__ float sh[32];
+  pdl_wait();
+  pdl_trigger();
+  const long long row = blockIdx.x;
+  const E* x = static_cast<const E*>(a.x) + row * a.x_stride;
+  const R* res = static_cast<const R*>(a.residual) + row * a.residual_stride;
+  R* res_out = static_cast<R*>(a.residual_out) + row * a.residual_out_stride;
+  E* out = static_cast<E*>(a.out) + row * a.out_stride;
+  const int tid = threadIdx.x, width = blockDim.x;
+  if constexpr (NV > 0) {
+    float h[NV][VEC], f[NV][VEC];
+    float sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int i = (v * width + tid) * VEC;
+      if (i < a.dim) {
+        load_vec<E, VEC>(x + i, f[v]);
+        load_vec<R, VEC>(res + i, h[v]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f[v][e] = h[v][e] = 0.0f;
+      }
+    }
+    float r = a.alpha;
+    if (a.post) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sum = fmaf(f[v][e], f[v][e], sum);
+      sum = team_sum<0>(sum, sh);
+      r *= rsqrtf(sum / a.dim + a.eps);
+      sum = 0.0f;
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int i = (v * width + tid) * VEC;
+      if (i < a.dim) {
+        float fw[VEC];
+        if (a.post) {
+          load_vec<float, VEC>(a.post + i, fw);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) f[v][e] *= fw[e];
+        }
+        if (a.scale) {
+          load_vec<float, VEC>(a.scale + i, fw);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) f[v][e] *= fw[e];
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          h[v][e] = fmaf(r, f[v][e], h[v][e]);
+          sum = fmaf(h[v][e], h[v][e], sum);
+        }
+        store_vec<R, VEC>(res_out + i, h[v]);
+      }
+    }
+    sum = team_sum<0>(sum, sh);
+    const float s = rsqrtf(sum / a.dim + a.eps);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int i = (v * width + tid) * VEC;
+      if (i < a.dim) {
+        float fw[VEC];
+        load_vec<float, VEC>(a.w + i, fw);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) fw[e] *= h[v][e] * s;
+        store_vec<E, VEC>(out + i, fw);
+      }
+    }
+  } else {
+    float r = a.alpha, sum = 0.0f;
+    if (a.post) {
+      for (int i = tid * VEC; i < a.dim; i += width * VEC) {
+        float f[VEC];
+        load_vec<E, VEC>(x + i, f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sum = fmaf(f[e], f[e], sum);
+      }
+      sum = team_sum<0>(sum, sh);
+      r *= rsqrtf(sum / a.dim + a.eps);
+      sum = 0.0f;
+    }
+    const auto stream = [&](int i, float (&h)[VEC]) {
+      float f[VEC], fw[VEC];
+      load_vec<E, VEC>(x + i, f);
+      load_vec<R, VEC>(res + i, h);
+      if (a.post) {
+        load_vec<float, VEC>(a.post + i, fw);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f[e] *= fw[e];
+      }
+      if (a.scale) {
+        load_vec<float, VEC>(a.scale + i, fw);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f[e] *= fw[e];
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) h[e] = fmaf(r, f[e], h[e]);
+    };
+    for (int i = tid * VEC; i < a.dim; i += width * VEC) {
+      float h[VEC];
+      stream(i, h);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) sum = fmaf(h[e], h[e], sum);
+    }
+    sum = team_sum<0>(sum, sh);
+    const float s = rsqrtf(sum / a.dim + a.eps);
+    for (int i = tid * VEC; i < a.dim; i += width * VEC) {
+      float h[VEC], fw[VEC];
+      stream(i, h);
+      load_vec<float, VEC>(a.w + i, fw);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) fw[e] *= h[e] * s;
+      store_vec<R, VEC>(res_out + i, h);
+      store_vec<E, VEC>(out + i, fw);
+    }
+  }
+}
+
+bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool on4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+template <typename E, int VEC>
+cudaError_t launch_gated(const GatedNormArgs& a, cudaStream_t st) {
+  const long long items = a.rows * a.groups;
+  const int vecs = (a.group + VEC - 1) / VEC;
+  const auto blocks = [&](int team) { return dim3(static_cast<unsigned>((items * team + 255) / 256)); };
+  if (vecs <= 8) return launch_pdl(gated_norm_kernel<E, VEC, 8, 1>, blocks(8), dim3(256), 0, st, a);
+  if (vecs <= 16) return launch_pdl(gated_norm_kernel<E, VEC, 16, 1>, blocks(16), dim3(256), 0, st, a);
+  if (vecs <= 32) return launch_pdl(gated_norm_kernel<E, VEC, 32, 1>, blocks(32), dim3(256), 0, st, a);
+  if (vecs <= 64) return launch_pdl(gated_norm_kernel<E, VEC, 32, 2>, blocks(32), dim3(256), 0, st, a);
+  if (vecs <= 128) return launch_pdl(gated_norm_kernel<E, VEC, 32, 4>, blocks(32), dim3(256), 0, st, a);
+  const dim3 grid(static_cast<unsigned>(items));
+  if (vecs <= 2048) return launch_pdl(gated_norm_kernel<E, VEC, 0, 2>, grid, dim3((vecs + 63) / 64 * 32), 0, st, a);
+  return launch_pdl(gated_norm_kernel<E, VEC, 0, 0>, grid, dim3(1024), 0, st, a);
+}
+
+template <typename E, typename R, int VEC>
+cudaError_t launch_residual(const ResidualNormArgs& a, long long rows, cudaStream_t st) {
+  const int vecs = (a.dim + VEC - 1) / VEC;
+  const dim3 grid(static_cast<unsigned>(rows));
+  if (vecs <= 512) return launch_pdl(residual_norm_kernel<E, R, VEC, 1>, grid, dim3((vecs + 31) / 32 * 32), 0, st, a);
+  if (vecs <= 2048) return launch_pdl(residual_norm_kernel<E, R, VEC, 2>, grid, dim3((vecs + 63) / 64 * 32), 0, st, a);
+  return launch_pdl(residual_norm_kernel<E, R, VEC, 0>, grid, dim3(1024), 0, st, a);
+}
+
+template <typename E>
+cudaError_t residual_of(const ResidualNormArgs& a, bool f32, bool vec, long long rows, cudaStream_t st) {
+  constexpr int V = 16 / static_cast<int>(sizeof(E));
+  if (f32) return vec ? launch_residual<E, float, V>(a, rows, st) : launch_residual<E, float, 1>(a, rows, st);
+  return vec ? launch_residual<E, E, V>(a, rows, st) : launch_residual<E, E, 1>(a, rows, st);
+}
+
+}  // namespace
+}  // namespace rssm
+
+using namespace rssm;
+
+extern "C" rssm_status rssm_gated_norm(const void* x, int64_t x_stride, const void* z, int64_t z_stride, int32_t dtype,
+                                       const float* weight, int32_t shared_weight, int64_t rows, int32_t dim,
+                                       int32_t group, float eps, int32_t norm_first, void* out, int64_t out_stride,
+                                       void* stream) {
+  if (rows < 0 || dim < 1 || group < 1 || dim % group || !(eps >= 0.0f)) return RSSM_ERR_INVALID_ARGUMENT;
+  if ((shared_weight != 0 && shared_weight != 1) || (norm_first != 0 && norm_first != 1)) return RSSM_ERR_INVALID_ARGUMENT;
+  if (dtype != RSSM_F32 && dtype != RSSM_BF16 && dtype != RSSM_F16) return RSSM_ERR_INVALID_ARGUMENT;
+  if (x_stride < dim || z_stride < dim || out_stride < dim) return RSSM_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return RSSM_OK;
+  const int esz = dtype == RSSM_F32 ? 4 : 2, V = 16 / esz;
+  if (!x || !z || !out || !weight || !on4(weight) || reinterpret_cast<uintptr_t>(x) % esz ||
+      reinterpret_cast<uintptr_t>(z) % esz || reinterpret_cast<uintptr_t>(out) % esz)
+    return RSSM_ERR_INVALID_ARGUMENT;
+  GatedNormArgs a = {x, z, weight, out, x_stride, z_stride, out_stride, rows, dim / group, group, shared_weight ? 0 : group, eps, norm_first};
+  if (rows > (1ll << 30) / a.groups) return RSSM_ERR_UNSUPPORTED;
+  const bool vec = on16(x) && on16(z) && on16(out) && on16(weight) && x_stride % V == 0 && z_stride % V == 0 &&
+                   out_stride % V == 0 && group % V == 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (dtype == RSSM_F32)
+    e = vec ? launch_gated<float, 4>(a, st) : launch_gated<float, 1>(a, st);
+  else if (dtype == RSSM_BF16)
+    e = vec ? launch_gated<__nv_bfloat16, 8>(a, st) : launch_gated<__nv_bfloat16, 1>(a, st);
+  else
+    e = vec ? launch_gated<__half, 8>(a, st) : launch_gated<__half, 1>(a, st);
+  return e == cudaSuccess ? RSSM_OK : RSSM_ERR_CUDA;
+}
+
+extern "C" rssm_status rssm_residual_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                                          int32_t dtype, int32_t residual_dtype, const float* post_weight,
+                                          const float* scale, float alpha, const float* weight, int64_t rows,
+                                          int32_t dim, float eps, void* residual_out, int64_t residual_out_stride,
+                                          void* out, int64_t out_stride, void* stream) {
+  if (rows < 0 || dim < 1 || !(eps >= 0.0f)) return RSSM_ERR_INVALID_ARGUMENT;
+  if (dtype != RSSM_F32 && dtype != RSSM_BF16 && dtype != RSSM_F16) return RSSM_ERR_INVALID_ARGUMENT;
+  if (residual_dtype != RSSM_F32 && residual_dtype != dtype) return RSSM_ERR_INVALID_ARGUMENT;
+  if (x_stride < dim || residual_stride < dim || residual_out_stride < dim || out_stride < dim) return RSSM_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return RSSM_OK;
+  const int esz = dtype == RSSM_F32 ? 4 : 2, rsz = residual_dtype == RSSM_F32 ? 4 : 2, V = 16 / esz;
+  if (!x || !residual || !residual_out || !out || !weight || !on4(weight) || !on4(post_weight) || !on4(scale) ||
+      reinterpret_cast<uintptr_t>(x) % esz || reinterpret_cast<uintptr_t>(out) % esz ||
+      reinterpret_cast<uintptr_t>(residual) % rsz || reinterpret_cast<uintptr_t>(residual_out) % rsz)
+    return RSSM_ERR_INVALID_ARGUMENT;
+  if (rows > 0x7fffffffll) return RSSM_ERR_UNSUPPORTED;
+  ResidualNormArgs a = {x, residual, post_weight, scale, weight, residual_out, out, x_stride, residual_stride,
+                        residual_out_stride, out_stride, dim, alpha, eps};
+  const bool vec = on16(x) && on16(residual) && on16(residual_out) && on16(out) && on16(weight) && on16(post_weight) &&
+                   on16(scale) && dim % V == 0 && x_stride % V == 0 && out_stride % V == 0 && residual_stride % V == 0 &&
+                   residual_out_stride % V == 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool f32 = residual_dtype == RSSM_F32;
+  const cudaError_t e = dtype == RSSM_F32    ? residual_of<float>(a, true, vec, rows, st)
+                        : dtype == RSSM_BF16 ? residual_of<__nv_bfloat16>(a, f32, vec, rows, st)
+                                             : residual_of<__half>(a, f32, vec, rows, st);
+  return e == cudaSuccess ? RSSM_OK : RSSM_ERR_CUDA;
+}
