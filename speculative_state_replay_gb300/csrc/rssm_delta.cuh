@@ -25,6 +25,10 @@
 namespace rssm {
 
 constexpr int kDeltaT = 8;       // tokens a block holds
+// bytes between a block's keys (queries) in shared memory: 32 past the row, so
+// that the four rows half a warp reads at a time fall on distinct banks
+template <int DK>
+constexpr int kTokenRow = DK * 2 + 32;
 constexpr float kMinLog = -100.0f;  // log decays are held at this and above: e^-100 is zero to fp32 sums of O(1) values,
                                     // and a finite floor keeps differences of running sums defined (g = -inf resets a state)
 
@@ -73,18 +77,23 @@ __device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t& hi, uin
   lo = cvt_bf16x2(a - bf16lo(hi), b - bf16hi(hi));
 }
 
+// (x, y) += a * (p, q), two fp32 FMAs in one instruction
+__device__ __forceinline__ void fma2(float& x, float& y, float2 a, float p, float q) {
+  float2 d = make_float2(x, y);
+  const float2 b = make_float2(p, q);
+  asm("fma.rn.f32x2 %0, %1, %2, %0;"
+      : "+l"(*reinterpret_cast<unsigned long long*>(&d))
+      : "l"(*reinterpret_cast<const unsigned long long*>(&a)), "l"(*reinterpret_cast<const unsigned long long*>(&b)));
+  x = d.x;
+  y = d.y;
+}
+
 // the state rows of one warp
 template <int DK>
 struct DeltaState {
   static constexpr int KS = DK / 16;
   float4 s[2][KS];
 
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int x = 0; x < KS; ++x) s[i][x] = make_float4(0.f, 0.f, 0.f, 0.f);
-  }
   // `head`: element offset of the warp's first row
   __device__ __forceinline__ void load(const void* state, long long head, int dtype, int lane) {
     const int m = lane >> 2, c = lane & 3;
@@ -134,21 +143,16 @@ struct DeltaState {
         s[i][x].w *= e;
       }
   }
-  // S += (u0, u1) k^T for rows m and m + 8; `k`: the key's first element
-  __device__ __forceinline__ void add(float u0, float u1, const uint16_t* k, int lane) {
-    const int c = lane & 3;
+  // S += (u0, u1) k^T for rows m and m + 8; `k`: the key in fp32, in shared memory
+  __device__ __forceinline__ void add(float u0, float u1, const float* k, int lane) {
+    const float2 a = make_float2(u0, u0), b = make_float2(u1, u1);
 #pragma unroll
     for (int x = 0; x < KS; ++x) {
-      const uint2 w = *reinterpret_cast<const uint2*>(k + 16 * x + 4 * c);
-      const float k0 = bf16lo(w.x), k1 = bf16hi(w.x), k2 = bf16lo(w.y), k3 = bf16hi(w.y);
-      s[0][x].x = fmaf(u0, k0, s[0][x].x);
-      s[0][x].y = fmaf(u0, k1, s[0][x].y);
-      s[0][x].z = fmaf(u0, k2, s[0][x].z);
-      s[0][x].w = fmaf(u0, k3, s[0][x].w);
-      s[1][x].x = fmaf(u1, k0, s[1][x].x);
-      s[1][x].y = fmaf(u1, k1, s[1][x].y);
-      s[1][x].z = fmaf(u1, k2, s[1][x].z);
-      s[1][x].w = fmaf(u1, k3, s[1][x].w);
+      const float4 w = *reinterpret_cast<const float4*>(k + 16 * x + 4 * (lane & 3));
+      fma2(s[0][x].x, s[0][x].y, a, w.x, w.y);
+      fma2(s[0][x].z, s[0][x].w, a, w.z, w.w);
+      fma2(s[1][x].x, s[1][x].y, b, w.x, w.y);
+      fma2(s[1][x].z, s[1][x].w, b, w.z, w.w);
     }
   }
 };
@@ -164,29 +168,28 @@ struct DeltaBlock {
   float A[2], P[2];   // coefficients of u_j in u_t and o_t for j = 2 (lane % 4) + {0, 1}
   float u[2][2];      // u_t of value rows r0 + 8 i + 2 (lane % 4) + {0, 1}
 
-  // tokens [tok0, tok0 + T) of key head hk, value head h; rows past T are zero
-  __device__ __forceinline__ void load(const DeltaTokens& tk, long long tok0, int T, int hk, int h, int Hv, int lane) {
+  // the block's tokens: keys and queries in shared memory, rows of DK bf16 at kTokenRow<DK> bytes
+  __device__ __forceinline__ void load(const uint8_t* keys, const uint8_t* queries, int T, int lane) {
     const int t = lane >> 2, cc = lane & 3;
     const bool live = t < T;
-    const uint16_t* kp = tk.k + (tok0 + t) * tk.k_stride + hk * DK + 4 * cc;
-    const uint16_t* qp = tk.q + (tok0 + t) * tk.q_stride + hk * DK + 4 * cc;
+    const uint8_t *kp = keys + t * kTokenRow<DK> + 8 * cc, *qp = queries + t * kTokenRow<DK> + 8 * cc;
 #pragma unroll
     for (int x = 0; x < KS; ++x) {
-      const uint2 kw = live ? *reinterpret_cast<const uint2*>(kp + 16 * x) : make_uint2(0u, 0u);
-      const uint2 qw = live ? *reinterpret_cast<const uint2*>(qp + 16 * x) : make_uint2(0u, 0u);
+      const uint2 kw = live ? *reinterpret_cast<const uint2*>(kp + 32 * x) : make_uint2(0u, 0u);
+      const uint2 qw = live ? *reinterpret_cast<const uint2*>(qp + 32 * x) : make_uint2(0u, 0u);
       a[x][0] = kw.x;
       a[x][1] = qw.x;
       a[x][2] = kw.y;
       a[x][3] = qw.y;
     }
-    c = live ? fmaxf(tk.g[(tok0 + t) * Hv + h], kMinLog) : 0.0f;
-    beta = live ? tk.beta[(tok0 + t) * Hv + h] : 0.0f;
   }
 
   // running decays, norms and the coefficients among the block's own tokens
-  __device__ __forceinline__ void prepare(const DeltaTokens& tk, int lane) {
+  __device__ __forceinline__ void prepare(const DeltaTokens& tk, float g, float b, int lane) {
     const int t = lane >> 2, cc = lane & 3;
     const unsigned full = 0xffffffffu;
+    c = g;
+    beta = b;
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       const float y = __shfl_up_sync(full, c, o);
@@ -217,10 +220,9 @@ struct DeltaBlock {
   }
 
   // products of the state rows with the keys and queries, then the triangular
-  // solve; `v`: the first of the warp's 16 value columns of token tok0; o gets
-  // the outputs of the lane's token and value rows
-  __device__ __forceinline__ void solve(const DeltaState<DK>& S, const uint16_t* v, long long v_stride, int T, int lane,
-                                        float (&o)[2][2]) {
+  // solve; vw: the lane's token's values of value rows r0 + 8 i + 2 (lane % 4)
+  // + {0, 1}; o gets the outputs of the same rows
+  __device__ __forceinline__ void solve(const DeltaState<DK>& S, const uint32_t (&vw)[2], int T, int lane, float (&o)[2][2]) {
     const int t = lane >> 2, cc = lane & 3;
     const unsigned full = 0xffffffffu;
     const float ec = expf(c);
@@ -236,9 +238,8 @@ struct DeltaBlock {
         mma_bf16(d, a[x], h0, h1);
         mma_bf16(d, a[x], l0, l1);
       }
-      const uint32_t vw = t < T ? *reinterpret_cast<const uint32_t*>(v + t * v_stride + 8 * i + 2 * cc) : 0u;
-      u[i][0] = fmaf(fu, d[0], beta * bf16lo(vw));
-      u[i][1] = fmaf(fu, d[1], beta * bf16hi(vw));
+      u[i][0] = fmaf(fu, d[0], beta * bf16lo(vw[i]));
+      u[i][1] = fmaf(fu, d[1], beta * bf16hi(vw[i]));
       o[i][0] = fo * d[2];
       o[i][1] = fo * d[3];
     }
@@ -257,15 +258,6 @@ struct DeltaBlock {
           if (t >= j) o[i][e] = fmaf(Pj, uj, o[i][e]);
         }
     }
-  }
-
-  // (u_j of value rows m and m + 8) for this lane's state rows
-  __device__ __forceinline__ float2 rows_of(int j, int lane) const {
-    const unsigned full = 0xffffffffu;
-    const int m = lane >> 2, from = j * 4 + (m >> 1);
-    const float x0 = __shfl_sync(full, u[0][0], from), x1 = __shfl_sync(full, u[0][1], from);
-    const float y0 = __shfl_sync(full, u[1][0], from), y1 = __shfl_sync(full, u[1][1], from);
-    return (m & 1) ? make_float2(x1, y1) : make_float2(x0, y0);
   }
 
   __device__ __forceinline__ void store_out(const float (&o)[2][2], uint16_t* out, long long stride, int T, int lane) const {

@@ -17,83 +17,120 @@ struct DeltaStepArgs {
   unsigned* ticket;  // scratch [batch]: blocks that have read the row's `pend` (zero between calls)
 };
 
-constexpr int kStepWarps = 4;  // 64 value rows a block
+constexpr int kStepWarps = 4;
+constexpr int kStepRows = kStepWarps * 16;  // value rows of a block
 
 // One warp per 16 value rows of a (row, value head): reads its part of S once,
 // adds the accepted drafts of the step before, writes it back if there were
-// any, and forms the new drafts' outputs and corrections from registers.
+// any, and forms the new drafts' outputs and corrections from registers.  The
+// block's loads go out in three rounds -- the row's scalars; the state, the new
+// tokens and `pend`; the waiting drafts -- and only the first two are waited for
+// one after another: the state's, the longest, covers the third.
 template <int DK>
-__global__ void __launch_bounds__(kStepWarps * 32) delta_step_kernel(const DeltaStepArgs a) {
+__global__ void __launch_bounds__(kStepWarps * 32, 4) delta_step_kernel(const DeltaStepArgs a) {
   __shared__ int sh[2];
+  __shared__ __align__(16) uint8_t s_k[kDeltaT * kTokenRow<DK>], s_q[kDeltaT * kTokenRow<DK>];
+  __shared__ __align__(16) float s_p[kDeltaT * DK], s_w[kDeltaT * kStepRows], s_c[kDeltaT];  // the waiting drafts
+  constexpr int CH = DK / 8;
   pdl_wait();
   pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, m = lane >> 2, cc = lane & 3;
   const int tile = blockIdx.x % a.tiles;
   const int h = (blockIdx.x / a.tiles) % a.c.Hv;
   const int b = blockIdx.x / a.tiles / a.c.Hv;
   const int s = a.slot_idx[b];
   const long long tok0 = a.cu ? a.cu[b] : static_cast<long long>(b) * a.T;
   const int n = a.cu ? a.cu[b + 1] - a.cu[b] : a.T;
-  const bool first = blockIdx.x % (a.tiles * a.c.Hv) == 0;
+  const int acc = a.accepted ? a.accepted[b] : 0;
   if (n < 0 || n > a.T || tok0 < 0 || tok0 + n > a.tokens) {  // the row's tokens are not known: nothing to write
-    if (first && threadIdx.x == 0) set_error(a.c.err, RSSM_ERRBIT_SEQLEN);
+    if (tid == 0 && blockIdx.x % (a.tiles * a.c.Hv) == 0) set_error(a.c.err, RSSM_ERRBIT_SEQLEN);
     return;
   }
-  const int r0 = (tile * kStepWarps + warp) * 16;
-  const bool mine = r0 < a.c.dv;
-  const int acc = a.accepted ? a.accepted[b] : 0;
-  bool ok = s > 0 && s < a.c.S;
-  int side = 0;
-  if (ok) {
-    // every block of the row reads (side, count) and takes a ticket; the last
-    // one knows that all have and turns the sides
-    if (threadIdx.x == 0) {
-      const int2 p = __ldcg(reinterpret_cast<const int2*>(a.c.pend) + s);
-      sh[0] = p.x;
-      sh[1] = p.y;
-      __threadfence();
-      const unsigned blocks = static_cast<unsigned>(a.tiles * a.c.Hv);
-      if (atomicInc(a.ticket + b, blocks - 1u) == blocks - 1u) {
-        if (acc >= 0 && acc <= p.y)
-          reinterpret_cast<int2*>(a.c.pend)[s] = make_int2(p.x ^ 1, n);
-        else
-          set_error(a.c.err, RSSM_ERRBIT_ACCEPT);
-      }
-    }
-    __syncthreads();
-    side = sh[0] & 1;
-    ok = acc >= 0 && acc <= sh[1];
-  }
-  if (!mine) return;
-  const int dv = a.c.dv, Hv = a.c.Hv, np = a.c.np;
+  const int dv = a.c.dv, Hv = a.c.Hv, np = a.c.np, hk = h / a.c.rep;
+  const int r0 = tile * kStepRows + warp * 16;
+  const bool mine = r0 < dv;
   const long long ostride = static_cast<long long>(Hv) * dv;
   uint16_t* out = a.tk.out + tok0 * ostride + h * dv + r0;
   DeltaBlock<DK> blk;
   float o[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-  if (!ok) {
-    blk.store_out(o, out, ostride, n, lane);
+  if (s <= 0 || s >= a.c.S) {
+    if (mine) blk.store_out(o, out, ostride, n, lane);
     return;
   }
-  const int m = lane >> 2, cc = lane & 3, hk = h / a.c.rep;
   DeltaState<DK> S;
   const long long head = s * a.c.state_stride + (static_cast<long long>(h) * dv + r0) * DK;
-  S.load(a.c.state, head, a.c.dtype, lane);
-  blk.load(a.tk, tok0, n, hk, h, Hv, lane);
+  if (mine) S.load(a.c.state, head, a.c.dtype, lane);
+  for (int i = tid; i < n * CH; i += kStepWarps * 32) {
+    const int t = i / CH, ch = i % CH;
+    cp_async16(s_k + t * kTokenRow<DK> + ch * 16, a.tk.k + (tok0 + t) * a.tk.k_stride + hk * DK + ch * 8);
+    cp_async16(s_q + t * kTokenRow<DK> + ch * 16, a.tk.q + (tok0 + t) * a.tk.q_stride + hk * DK + ch * 8);
+  }
+  float g = 0.0f, beta = 0.0f;
+  uint32_t vw[2] = {0u, 0u};
+  if (mine && m < n) {
+    g = fmaxf(a.tk.g[(tok0 + m) * Hv + h], kMinLog);
+    beta = a.tk.beta[(tok0 + m) * Hv + h];
+    const uint16_t* v = a.tk.v + (tok0 + m) * a.tk.v_stride + h * dv + r0 + 2 * cc;
+    vw[0] = *reinterpret_cast<const uint32_t*>(v);
+    vw[1] = *reinterpret_cast<const uint32_t*>(v + 8);
+  }
+  if (tid == 0) {
+    const int2 p = __ldcg(reinterpret_cast<const int2*>(a.c.pend) + s);
+    sh[0] = p.x;
+    sh[1] = p.y;
+  }
+  __syncthreads();
+  const int side = sh[0] & 1;
+  const bool ok = acc >= 0 && acc <= sh[1];
+  // every block of the row takes a ticket once it has read (side, count); the
+  // last one knows that all have, and turns the sides
+  if (tid == 0) {
+    __threadfence();
+    const unsigned blocks = static_cast<unsigned>(a.tiles * Hv);
+    if (atomicInc(a.ticket + b, blocks - 1u) == blocks - 1u) {
+      if (ok)
+        reinterpret_cast<int2*>(a.c.pend)[s] = make_int2(side ^ 1, n);
+      else
+        set_error(a.c.err, RSSM_ERRBIT_ACCEPT);
+    }
+  }
+  if (!ok) {
+    cp_async_wait_all();
+    if (mine) blk.store_out(o, out, ostride, n, lane);
+    return;
+  }
   if (acc > 0) {
     const float* pc = a.c.pend_c + s * a.c.pend_c_stride + (static_cast<long long>(side) * Hv + h) * np;
-    const float* pw = a.c.pend_w + s * a.c.pend_w_stride + (static_cast<long long>(side) * Hv + h) * np * dv + r0 + m;
+    const float* pw = a.c.pend_w + s * a.c.pend_w_stride + (static_cast<long long>(side) * Hv + h) * np * dv + tile * kStepRows;
     const uint16_t* pk = a.c.pend_k + s * a.c.pend_k_stride + (static_cast<long long>(side) * a.c.Hk + hk) * np * DK;
-    const float end = pc[acc - 1];
+    if (tid < acc) cp_async4(s_c + tid, pc + tid);
+    for (int i = tid; i < acc * (kStepRows / 4); i += kStepWarps * 32) {
+      const int j = i / (kStepRows / 4), r = i % (kStepRows / 4) * 4;
+      if (tile * kStepRows + r < dv) cp_async16(s_w + j * kStepRows + r, pw + static_cast<long long>(j) * dv + r);
+    }
+    for (int i = tid; i < acc * CH; i += kStepWarps * 32) {
+      const uint4 x = *reinterpret_cast<const uint4*>(pk + i * 8);
+      float4* to = reinterpret_cast<float4*>(s_p + i * 8);
+      to[0] = make_float4(bf16lo(x.x), bf16hi(x.x), bf16lo(x.y), bf16hi(x.y));
+      to[1] = make_float4(bf16lo(x.z), bf16hi(x.z), bf16lo(x.w), bf16hi(x.w));
+    }
+  }
+  cp_async_wait_all();
+  __syncthreads();
+  if (!mine) return;
+  if (acc > 0) {
+    const float end = s_c[acc - 1];
     S.decay(expf(end));
     for (int j = 0; j < acc; ++j) {
-      const float e = expf(end - pc[j]);
-      S.add(e * pw[static_cast<long long>(j) * dv], e * pw[static_cast<long long>(j) * dv + 8], pk + j * DK, lane);
+      const float e = expf(end - s_c[j]);
+      S.add(e * s_w[j * kStepRows + warp * 16 + m], e * s_w[j * kStepRows + warp * 16 + m + 8], s_p + j * DK, lane);
     }
     S.store(a.c.state, head, a.c.dtype, lane);
   }
   if (n == 0) return;
-  blk.prepare(a.tk, lane);
-  blk.solve(S, a.tk.v + tok0 * a.tk.v_stride + h * dv + r0, a.tk.v_stride, n, lane, o);
+  blk.load(s_k, s_q, n, lane);
+  blk.prepare(a.tk, g, beta, lane);
+  blk.solve(S, vw, n, lane, o);
   blk.store_out(o, out, ostride, n, lane);
   // the new drafts wait in the other half
   if (m < n) {
@@ -205,7 +242,7 @@ extern "C" rssm_status rssm_delta_step(const rssm_delta_cache* cache, const void
   a.batch = batch;
   a.T = T;
   a.tokens = tokens;
-  a.tiles = (a.c.dv + kStepWarps * 16 - 1) / (kStepWarps * 16);
+  a.tiles = (a.c.dv + kStepRows - 1) / kStepRows;
   a.ticket = static_cast<unsigned*>(scratch);
   const long long blocks = static_cast<long long>(batch) * a.c.Hv * a.tiles;
   if (blocks > 0x7fffffffll) return RSSM_ERR_UNSUPPORTED;

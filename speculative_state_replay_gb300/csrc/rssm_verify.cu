@@ -27,6 +27,8 @@ struct VerifyArgs {
 
 constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kMaxParts = 8;  // blocks of a cluster (the portable most)
+constexpr int kRuns = 8;      // a warp's part of a row is summed in 8 runs
 
 template <typename P>
 __device__ __forceinline__ float prob(P x);
@@ -43,12 +45,25 @@ __device__ __forceinline__ float prob<__half>(__half x) {
   return __half2float(x);
 }
 
-// Sampling weight in fixed point, 36 fraction bits: sums of integers do not
+// Sampling weights in fixed point, 36 fraction bits: sums of integers do not
 // depend on their order, so the drawn token is a function of the inputs
-// whatever the grid.  Comparisons send NaN to zero.
-__device__ __forceinline__ unsigned long long weight(float r) {
-  return r > 0.0f ? static_cast<unsigned long long>(__float2ll_rz(fminf(r, 1.0f) * 68719476736.0f)) : 0ull;
-}
+// whatever the grid.  floor(2^36 r) of r in [0, 1] comes from two additions
+// rounded toward zero: r + 32, whose last bit is 2^-18, leaves floor(2^18 r)
+// in its fraction, and the remainder (exact) + 2^-13 the next 18 bits; the
+// 64-bit conversion instruction runs at a fraction of their rate.
+struct Weight {
+  uint32_t hi, lo;  // in units of 2^-18 and 2^-36
+  __device__ __forceinline__ void add(float r) {
+    r = fminf(fmaxf(r, 0.0f), 1.0f);  // NaN: 0
+    const float t = __fadd_rz(r, 32.0f);
+    const float rest = __fsub_rn(r, __fsub_rn(t, 32.0f));
+    hi += __float_as_uint(t) - __float_as_uint(32.0f);
+    lo += __float_as_uint(__fadd_rz(rest, 1.220703125e-4f)) - __float_as_uint(1.220703125e-4f);
+  }
+  __device__ __forceinline__ unsigned long long value() const {
+    return (static_cast<unsigned long long>(hi) << 18) + lo;
+  }
+};
 
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 #pragma unroll
@@ -57,61 +72,84 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 }
 
 // One row's distribution to draw from: max(p - q, 0), q from the draft's row,
-// or 1 at the draft's token (certain drafts), or nothing.
+// or 1 at the draft's token (certain drafts), or nothing.  Pieces of VEC values
+// start on 16 bytes of p's row: positions j are counted from `off` values
+// before its first, so that rows of any alignment are read 16 bytes a lane.
 template <typename P>
 struct Residual {
+  static constexpr int VEC = 16 / sizeof(P);
   const P* p;
   const P* q;
-  int token;
-  template <int VEC>
-  __device__ __forceinline__ unsigned long long sum(int i) const {
-    P a[VEC];
-    unsigned long long w = 0;
-    if constexpr (VEC == 1) {
-      return at(i);
-    } else {
-      *reinterpret_cast<uint4*>(a) = *reinterpret_cast<const uint4*>(p + i);
-      if (q) {
-        P c[VEC];
-        *reinterpret_cast<uint4*>(c) = *reinterpret_cast<const uint4*>(q + i);
+  int token, vocab, off;
+  bool q_same;  // q's row has p's alignment
+
+  __device__ __forceinline__ void set(const P* target, const P* draft, int tok, int v) {
+    p = target;
+    q = draft;
+    token = tok;
+    vocab = v;
+    off = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(P));
+    q_same = q && (reinterpret_cast<uintptr_t>(q) & 15u) == (reinterpret_cast<uintptr_t>(p) & 15u);
+  }
+  __device__ __forceinline__ void one(Weight& w, int i) const {
+    w.add(prob<P>(p[i]) - (q ? prob<P>(q[i]) : (i == token ? 1.0f : 0.0f)));
+  }
+  // weight of the piece at position j
+  __device__ __forceinline__ unsigned long long piece(int j) const {
+    Weight w = {0u, 0u};
+    const int i = j - off;
+    if (i >= 0 && i + VEC <= vocab) {
+      P a[VEC], c[VEC];
+      *reinterpret_cast<uint4*>(a) = __ldcs(reinterpret_cast<const uint4*>(p + i));
+      if (!q) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) w += weight(prob<P>(a[e]) - prob<P>(c[e]));
+        for (int e = 0; e < VEC; ++e) w.add(prob<P>(a[e]) - (i + e == token ? 1.0f : 0.0f));
+        return w.value();
+      }
+      if (q_same) {
+        *reinterpret_cast<uint4*>(c) = __ldcs(reinterpret_cast<const uint4*>(q + i));
       } else {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) w += weight(prob<P>(a[e]) - (i + e == token ? 1.0f : 0.0f));
+        for (int e = 0; e < VEC; ++e) c[e] = q[i + e];
       }
-      return w;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) w.add(prob<P>(a[e]) - prob<P>(c[e]));
+    } else {
+      for (int e = max(i, 0); e < min(i + VEC, vocab); ++e) one(w, e);
     }
-  }
-  __device__ __forceinline__ unsigned long long at(int i) const {
-    const float b = q ? prob<P>(q[i]) : (i == token ? 1.0f : 0.0f);
-    return weight(prob<P>(p[i]) - b);
+    return w.value();
   }
 };
 
 // One cluster per row.  The row's tests come from single values; then the one
 // row of the target (and of the draft) the next token is drawn from is read
-// once in slices, one per CTA and warp, and summed; the CTA whose slice holds
-// the drawn mass reads it again, in ever smaller parts, to find the token.
-template <typename P, int VEC>
+// once, a part per block and warp, and summed in 64 bits; the sums of a
+// warp's 8 runs stay in its lanes, so the warp that holds the drawn mass finds
+// the run, then the piece and the value, from them and a second look at that
+// run alone.
+template <typename P>
 __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs a) {
+  constexpr int VEC = Residual<P>::VEC, kStep = 32 * VEC;
   __shared__ unsigned long long part[kVerifyWarps];
-  __shared__ unsigned long long cta_sum;
+  __shared__ unsigned long long sums[2][kMaxParts];
   __shared__ int sh_count, sh_bad;
   cg::cluster_group cl = cg::this_cluster();
   const int parts = cl.num_blocks(), rank = cl.block_rank();
   const int b = blockIdx.x / parts;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (parts > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this block runs: its sums can be written
   pdl_wait();
   pdl_trigger();
   const long long tok0 = a.cu ? a.cu[b] : static_cast<long long>(b) * a.T;
   const int n = a.cu ? a.cu[b + 1] - a.cu[b] : a.T;
-  if (n <= 0 || n > a.T || tok0 < 0 || tok0 + n > a.ntok) {  // the same in every CTA of the cluster
+  const bool empty = n <= 0 || n > a.T || tok0 < 0 || tok0 + n > a.ntok;  // the same in every block of the cluster
+  if (empty) {
     if (rank == 0 && threadIdx.x == 0) {
       a.accepted[b] = 0;
       a.next[b] = -1;
       if (n != 0) set_error(a.err, RSSM_ERRBIT_SEQLEN);
     }
+    if (parts > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     return;
   }
   const P* target = static_cast<const P*>(a.target);
@@ -121,11 +159,12 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs
     bool pass = lane == 0, bad = false;
     if (lane > 0 && lane < n) {
       const int tok = a.tokens[tok0 + lane];
+      const float u = a.u[tok0 + lane];
       bad = tok < 0 || tok >= a.vocab;
       if (!bad) {
         const float p = prob<P>(target[(tok0 + lane - 1) * a.target_stride + tok]);
         const float q = draft ? prob<P>(draft[(tok0 + lane) * a.draft_stride + tok]) : 1.0f;
-        pass = __fmul_rn(a.u[tok0 + lane], q) < p;
+        pass = __fmul_rn(u, q) < p;
       }
     }
     const unsigned failed = ~__ballot_sync(0xffffffffu, pass);
@@ -138,45 +177,53 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs
   __syncthreads();
   const int count = sh_count;
   Residual<P> res;
-  res.p = target + (tok0 + count - 1) * a.target_stride;
-  res.q = draft && count < n ? draft + (tok0 + count) * a.draft_stride : nullptr;
-  res.token = !draft && count < n ? a.tokens[tok0 + count] : -1;
+  res.set(target + (tok0 + count - 1) * a.target_stride,
+          draft && count < n ? draft + (tok0 + count) * a.draft_stride : nullptr,
+          !draft && count < n ? a.tokens[tok0 + count] : -1, a.vocab);
   if (rank == 0 && threadIdx.x == 0 && sh_bad) set_error(a.err, RSSM_ERRBIT_TOKEN);
 
-  // slices in whole vectors, the last one ragged
-  const int step = kVerifyWarps * VEC * 32;
-  const int slice = (a.vocab + parts * step - 1) / (parts * step) * step;  // a multiple of every warp's 32 vectors
-  unsigned long long total = 0, before = 0, mine = 0;
+  // a warp's part: kRuns runs of `len` steps of 32 pieces
+  const int len = (a.vocab + res.off + parts * kVerifyWarps * kRuns * kStep - 1) / (parts * kVerifyWarps * kRuns * kStep);
+  const int span = kRuns * len * kStep, first = (rank * kVerifyWarps + warp) * span, end = a.vocab + res.off;
+  unsigned long long total = 0, before = 0, run[kRuns];
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
-    const int lo = rank * slice + warp * (slice / kVerifyWarps), hi = min(lo + slice / kVerifyWarps, a.vocab);
-    unsigned long long w = 0;
-#pragma unroll 4
-    for (int i = lo + lane * VEC; i < hi; i += 32 * VEC) {
-      if (i + VEC <= hi) {
-        w += res.template sum<VEC>(i);
-      } else {
-        for (int e = i; e < hi; ++e) w += res.at(e);
-      }
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r) run[r] = 0;
+    if (first < end) {
+#pragma unroll 1
+      for (int k = 0; k < len; ++k)
+#pragma unroll
+        for (int r = 0; r < kRuns; ++r) {
+          const int j = first + (r * len + k) * kStep + lane * VEC;
+          if (j < end) run[r] += res.piece(j);
+        }
     }
+    unsigned long long w = 0;
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r) w += run[r];
     w = warp_sum(w);
     if (lane == 0) part[warp] = w;
     __syncthreads();
-    mine = 0;
-#pragma unroll
-    for (int x = 0; x < kVerifyWarps; ++x) mine += part[x];
     if (parts == 1) {
-      total = mine;
+      total = 0;
+#pragma unroll
+      for (int x = 0; x < kVerifyWarps; ++x) total += part[x];
     } else {
-      if (threadIdx.x == 0) cta_sum = mine;
+      if (pass == 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+      if (threadIdx.x < parts) {
+        unsigned long long mine = 0;
+#pragma unroll
+        for (int x = 0; x < kVerifyWarps; ++x) mine += part[x];
+        *cl.map_shared_rank(&sums[pass][rank], threadIdx.x) = mine;
+      }
       cl.sync();
       total = before = 0;
       for (int x = 0; x < parts; ++x) {
-        const unsigned long long y = *cl.map_shared_rank(&cta_sum, x);
+        const unsigned long long y = sums[pass][x];
         total += y;
         if (x < rank) before += y;
       }
-      cl.sync();  // nobody leaves, or writes its sum again, before all have read
     }
     if (total || (!res.q && res.token < 0)) break;
     // nothing left of the target above the draft: draw from the target itself
@@ -195,63 +242,58 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs
   // floor(total * u) with u in 24 bits
   const unsigned long long u24 = static_cast<unsigned long long>(__float2ll_rz(fminf(fmaxf(a.u_next[b], 0.0f), 0.99999994f) * 16777216.0f));
   const unsigned long long aim = (total >> 24) * u24 + (((total & 0xffffffull) * u24) >> 24);
-  if (aim < before || aim >= before + mine) return;
-  // this CTA's slice holds the token: the warp's part that does, then parts of parts
+  for (int x = 0; x < warp; ++x) before += part[x];
+  if (aim < before || aim >= before + part[warp]) return;
+  // this warp's part holds the token: the run that does, then the step of 32 pieces
   unsigned long long left = aim - before;
-  int lo = rank * slice, width = slice / kVerifyWarps;
-  while (true) {
-    int x = 0;
-    while (x < kVerifyWarps - 1 && left >= part[x]) left -= part[x++];
-    lo += x * width;
-    if (width <= 32 * VEC) break;
-    __syncthreads();  // part is read
-    const int next_width = (width + step - 1) / step * (step / kVerifyWarps);
-    const int l = lo + warp * next_width, h = min(min(l + next_width, lo + width), a.vocab);
-    unsigned long long w = 0;
-    for (int i = l + lane * VEC; i < h; i += 32 * VEC) {
-      if (i + VEC <= h) {
-        w += res.template sum<VEC>(i);
+  int at = first;
+  bool found = false;
+#pragma unroll
+  for (int r = 0; r < kRuns; ++r) {
+    const unsigned long long w = warp_sum(run[r]);
+    if (!found) {
+      if (left < w) {
+        found = true;
+        at = first + r * len * kStep;
       } else {
-        for (int e = i; e < h; ++e) w += res.at(e);
+        left -= w;
       }
     }
-    w = warp_sum(w);
-    if (lane == 0) part[warp] = w;
-    __syncthreads();
-    width = next_width;
   }
-  if (warp == 0) {
-    const int i0 = lo + lane * VEC, i1 = min(i0 + VEC, a.vocab);
-    unsigned long long w[VEC], own = 0;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      w[e] = i0 + e < i1 ? res.at(i0 + e) : 0ull;
-      own += w[e];
-    }
+#pragma unroll 4
+  for (int k = 0; k < len; ++k) {
+    const int j = at + k * kStep + lane * VEC;
+    const unsigned long long own = j < end ? res.piece(j) : 0ull;
     unsigned long long upto = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const unsigned long long y = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += y;
     }
+    const unsigned long long all = __shfl_sync(0xffffffffu, upto, 31);
+    if (left >= all) {
+      left -= all;
+      continue;
+    }
     unsigned long long base = upto - own;
     if (left >= base && left < upto) {
-      int e = 0;
-#pragma unroll
-      for (int x = 0; x < VEC - 1; ++x) {
-        if (e == x && left >= base + w[x]) {
-          base += w[x];
-          e = x + 1;
+      for (int i = max(j - res.off, 0); i < min(j - res.off + VEC, a.vocab); ++i) {
+        Weight w = {0u, 0u};
+        res.one(w, i);
+        base += w.value();
+        if (left < base) {
+          a.accepted[b] = count;
+          a.next[b] = i;
+          break;
         }
       }
-      a.accepted[b] = count;
-      a.next[b] = i0 + e;
     }
+    break;
   }
 }
 
 template <typename P>
-cudaError_t launch_verify(const VerifyArgs& a, bool vec, int parts, cudaStream_t st) {
+cudaError_t launch_verify(const VerifyArgs& a, int parts, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * parts);
   cfg.blockDim = dim3(kVerifyThreads);
@@ -264,8 +306,7 @@ cudaError_t launch_verify(const VerifyArgs& a, bool vec, int parts, cudaStream_t
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (vec) return cudaLaunchKernelEx(&cfg, verify_kernel<P, 16 / static_cast<int>(sizeof(P))>, a);
-  return cudaLaunchKernelEx(&cfg, verify_kernel<P, 1>, a);
+  return cudaLaunchKernelEx(&cfg, verify_kernel<P>, a);
 }
 
 }  // namespace
@@ -306,14 +347,11 @@ extern "C" rssm_status rssm_verify(const void* target, int64_t target_stride, co
   a.accepted = accepted;
   a.next = next;
   a.err = error_word;
-  // rows that start on 16 bytes are read 16 bytes a lane
-  const bool vec = reinterpret_cast<uintptr_t>(target) % 16 == 0 && target_stride * esz % 16 == 0 &&
-                   (!draft || (reinterpret_cast<uintptr_t>(draft) % 16 == 0 && draft_stride * esz % 16 == 0));
   int parts = 1;
   while (parts < 8 && batch * parts < 304 && vocab > parts * 4096) parts *= 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = prob_dtype == RSSM_F32    ? launch_verify<float>(a, vec, parts, st)
-                        : prob_dtype == RSSM_BF16 ? launch_verify<__nv_bfloat16>(a, vec, parts, st)
-                                                  : launch_verify<__half>(a, vec, parts, st);
+  const cudaError_t e = prob_dtype == RSSM_F32    ? launch_verify<float>(a, parts, st)
+                        : prob_dtype == RSSM_BF16 ? launch_verify<__nv_bfloat16>(a, parts, st)
+                                                  : launch_verify<__half>(a, parts, st);
   return e == cudaSuccess ? RSSM_OK : RSSM_ERR_CUDA;
 }
