@@ -10,14 +10,18 @@
 // so S0 is read once for all of them and S after a of them is
 //     e^{c_{a-1}} S0 + sum_{j<a} e^{c_{a-1}-c_j} u_j k_j^T.
 //
-// A warp owns 16 value rows of S and all DK key columns, in registers, as
-// mma.sync fragments: lane (m = lane / 4, c = lane % 4) holds rows m and m + 8,
-// and of each 16 columns the four 4c..4c+3 (the contraction index of a step of
-// 16 is permuted so that each lane's part is contiguous; keys and queries are
-// loaded with the same permutation).  The first operand's 16 rows are the 8
-// keys and the 8 queries, so one instruction serves both products; the Gram
-// products k.k and q.k come from the same registers.  No shared memory and no
-// barriers are involved.
+// The drafts that wait from the step before enter the same way, without
+// forming the new state first: with E = e^{c_end} and e_j = e^{c_end - c_j},
+//     S0' k = E (S0 k) + sum_j e_j w_j (k_j . k).
+//
+// A warp owns 16 value rows of S and all DK key columns as mma.sync fragments:
+// lane (m = lane / 4, c = lane % 4) holds rows m and m + 8, and of each 32
+// columns the eight 8c..8c+7 (the contraction index of two steps of 16 is
+// permuted so that each lane's part is contiguous; keys and queries are loaded
+// with the same permutation).  The first operand's 16 rows are the 8 keys and
+// the 8 queries, so one instruction serves both products; the Gram products
+// come from the same registers.  2-byte states go into the products as they
+// are; fp32 states as bf16 hi + lo.
 #pragma once
 
 #include "rssm_device.cuh"
@@ -25,16 +29,16 @@
 namespace rssm {
 
 constexpr int kDeltaT = 8;       // tokens a block holds
-// bytes between a block's keys (queries) in shared memory: 32 past the row, so
-// that the four rows half a warp reads at a time fall on distinct banks
+// bytes between a block's keys (queries) in shared memory: 64 past the row, so
+// that the two rows a quarter of a warp reads at a time fall on distinct banks
 template <int DK>
-constexpr int kTokenRow = DK * 2 + 32;
+constexpr int kTokenRow = DK * 2 + 64;
 constexpr float kMinLog = -100.0f;  // log decays are held at this and above: e^-100 is zero to fp32 sums of O(1) values,
                                     // and a finite floor keeps differences of running sums defined (g = -inf resets a state)
 
 struct DeltaCacheView {
   int S, Hk, Hv, rep, dv, np;
-  int dtype;
+  int dtype, wide;  // wide: state rows start on 32 bytes
   void* state;
   long long state_stride;
   uint16_t* pend_k;
@@ -60,7 +64,7 @@ struct DeltaTokens {
 };
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -77,129 +81,175 @@ __device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t& hi, uin
   lo = cvt_bf16x2(a - bf16lo(hi), b - bf16hi(hi));
 }
 
-// (x, y) += a * (p, q), two fp32 FMAs in one instruction
-__device__ __forceinline__ void fma2(float& x, float& y, float2 a, float p, float q) {
-  float2 d = make_float2(x, y);
-  const float2 b = make_float2(p, q);
-  asm("fma.rn.f32x2 %0, %1, %2, %0;"
-      : "+l"(*reinterpret_cast<unsigned long long*>(&d))
-      : "l"(*reinterpret_cast<const unsigned long long*>(&a)), "l"(*reinterpret_cast<const unsigned long long*>(&b)));
-  x = d.x;
-  y = d.y;
+// Two fp32 values in one 64-bit register pair: packed instructions take and
+// leave pairs, so values that go through them stay in this form.
+using pair = unsigned long long;
+__device__ __forceinline__ pair pack2(float lo, float hi) {
+  pair d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpack2(pair d, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(d)); }
+__device__ __forceinline__ void fma2(pair& d, pair a, pair b) { asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b)); }
+__device__ __forceinline__ void mul2(pair& d, pair a) { asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(a)); }
+__device__ __forceinline__ uint32_t cvt_bf16x2(pair d) {
+  float lo, hi;
+  unpack2(d, lo, hi);
+  return cvt_bf16x2(lo, hi);
+}
+__device__ __forceinline__ void split_bf16x2(pair d, uint32_t& h, uint32_t& l) {
+  float lo, hi;
+  unpack2(d, lo, hi);
+  split_bf16x2(lo, hi, h, l);
 }
 
-// the state rows of one warp
-template <int DK>
-struct DeltaState {
+// Rows m (or m + 8) of a warp's state: a lane's 2 KS pairs of columns.
+template <int DK, bool F32>
+struct DeltaRow {
   static constexpr int KS = DK / 16;
-  float4 s[2][KS];
+  ulonglong2 s[KS];  // fp32 values; 2-byte states keep their words in `w` until they are needed as such
+  uint4 w[KS / 2];
 
-  // `head`: element offset of the warp's first row
-  __device__ __forceinline__ void load(const void* state, long long head, int dtype, int lane) {
-    const int m = lane >> 2, c = lane & 3;
-    if (dtype == RSSM_F32) {
-      const float* p = static_cast<const float*>(state) + head + m * DK + 4 * c;
+  // from the warp's rows in shared memory
+  __device__ __forceinline__ void read(const uint8_t* buf, int row, int c) {
+    if constexpr (F32) {
+      const float* p = reinterpret_cast<const float*>(buf) + row * DK + 8 * c;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int x = 0; x < KS; ++x) s[i][x] = *reinterpret_cast<const float4*>(p + i * 8 * DK + 16 * x);
+      for (int x = 0; x < KS; ++x) s[x] = *reinterpret_cast<const ulonglong2*>(p + 32 * (x >> 1) + 4 * (x & 1));
     } else {
-      const uint16_t* p = static_cast<const uint16_t*>(state) + head + m * DK + 4 * c;
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(buf) + row * DK + 8 * c;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int x = 0; x < KS; ++x) {
-          const uint2 w = *reinterpret_cast<const uint2*>(p + i * 8 * DK + 16 * x);
-          s[i][x] = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
-        }
+      for (int y = 0; y < KS / 2; ++y) w[y] = *reinterpret_cast<const uint4*>(p + 32 * y);
     }
   }
-  __device__ __forceinline__ void store(void* state, long long head, int dtype, int lane) const {
-    const int m = lane >> 2, c = lane & 3;
-    if (dtype == RSSM_F32) {
-      float* p = static_cast<float*>(state) + head + m * DK + 4 * c;
+  // d = (keys; queries) times these rows, in short chains of products
+  __device__ __forceinline__ void product(const uint32_t (&a)[KS][4], float (&d)[4]) const {
+    float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (F32) {
+      float l0[4] = {0.f, 0.f, 0.f, 0.f}, l1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int x = 0; x < KS; x += 2) {
+        uint32_t h[4], l[4];
+        split_bf16x2(s[x].x, h[0], l[0]);
+        split_bf16x2(s[x].y, h[1], l[1]);
+        split_bf16x2(s[x + 1].x, h[2], l[2]);
+        split_bf16x2(s[x + 1].y, h[3], l[3]);
+        mma_bf16(d0, a[x], h[0], h[1]);
+        mma_bf16(l0, a[x], l[0], l[1]);
+        mma_bf16(d1, a[x + 1], h[2], h[3]);
+        mma_bf16(l1, a[x + 1], l[2], l[3]);
+      }
 #pragma unroll
-        for (int x = 0; x < KS; ++x) *reinterpret_cast<float4*>(p + i * 8 * DK + 16 * x) = s[i][x];
+      for (int e = 0; e < 4; ++e) d[e] = (d0[e] + d1[e]) + (l0[e] + l1[e]);
     } else {
-      uint16_t* p = static_cast<uint16_t*>(state) + head + m * DK + 4 * c;
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int y = 0; y < KS / 2; ++y) {
+        mma_bf16(d0, a[2 * y], w[y].x, w[y].y);
+        mma_bf16(d1, a[2 * y + 1], w[y].z, w[y].w);
+      }
 #pragma unroll
-        for (int x = 0; x < KS; ++x)
-          *reinterpret_cast<uint2*>(p + i * 8 * DK + 16 * x) =
-              make_uint2(cvt_bf16x2(s[i][x].x, s[i][x].y), cvt_bf16x2(s[i][x].z, s[i][x].w));
+      for (int e = 0; e < 4; ++e) d[e] = d0[e] + d1[e];
     }
   }
   __device__ __forceinline__ void decay(float e) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int x = 0; x < KS; ++x) {
-        s[i][x].x *= e;
-        s[i][x].y *= e;
-        s[i][x].z *= e;
-        s[i][x].w *= e;
-      }
-  }
-  // S += (u0, u1) k^T for rows m and m + 8; `k`: the key in fp32, in shared memory
-  __device__ __forceinline__ void add(float u0, float u1, const float* k, int lane) {
-    const float2 a = make_float2(u0, u0), b = make_float2(u1, u1);
+    const pair a = pack2(e, e);
 #pragma unroll
     for (int x = 0; x < KS; ++x) {
-      const float4 w = *reinterpret_cast<const float4*>(k + 16 * x + 4 * (lane & 3));
-      fma2(s[0][x].x, s[0][x].y, a, w.x, w.y);
-      fma2(s[0][x].z, s[0][x].w, a, w.z, w.w);
-      fma2(s[1][x].x, s[1][x].y, b, w.x, w.y);
-      fma2(s[1][x].z, s[1][x].w, b, w.z, w.w);
+      if constexpr (!F32) {
+        const uint32_t p = (x & 1) ? w[x >> 1].z : w[x >> 1].x, q = (x & 1) ? w[x >> 1].w : w[x >> 1].y;
+        s[x].x = pack2(bf16lo(p), bf16hi(p));
+        s[x].y = pack2(bf16lo(q), bf16hi(q));
+      }
+      mul2(s[x].x, a);
+      mul2(s[x].y, a);
+    }
+  }
+  // += u k^T; `k`: the key in fp32, in shared memory
+  __device__ __forceinline__ void add(float u, const float* k, int c) {
+    const pair a = pack2(u, u);
+#pragma unroll
+    for (int x = 0; x < KS; ++x) {
+      const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(k + 32 * (x >> 1) + 8 * c + 4 * (x & 1));
+      fma2(s[x].x, a, y.x);
+      fma2(s[x].y, a, y.y);
+    }
+  }
+  // to memory; `p`: the lane's first column.  wide: rows start on 32 bytes,
+  // and a lane writes a whole sector at a time
+  __device__ __forceinline__ void store(void* p, bool wide) const {
+    if constexpr (F32) {
+#pragma unroll
+      for (int y = 0; y < KS / 2; ++y) {
+        float* to = static_cast<float*>(p) + 32 * y;
+        if (wide) {
+          asm volatile("st.global.v4.b64 [%0], {%1,%2,%3,%4};" ::"l"(to), "l"(s[2 * y].x), "l"(s[2 * y].y), "l"(s[2 * y + 1].x),
+                       "l"(s[2 * y + 1].y)
+                       : "memory");
+        } else {
+          *reinterpret_cast<ulonglong2*>(to) = s[2 * y];
+          *reinterpret_cast<ulonglong2*>(to + 4) = s[2 * y + 1];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int y = 0; y < KS / 2; ++y)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + 32 * y) =
+            make_uint4(cvt_bf16x2(s[2 * y].x), cvt_bf16x2(s[2 * y].y), cvt_bf16x2(s[2 * y + 1].x), cvt_bf16x2(s[2 * y + 1].y));
     }
   }
 };
 
-// A block of up to 8 tokens against the warp's state rows.
+// A block of up to 8 tokens, and the drafts that wait before it.  Lane (t =
+// lane / 4, c = lane % 4) has token t and, of pairs of tokens, j = 2c + {0, 1}.
 template <int DK>
 struct DeltaBlock {
   static constexpr int KS = DK / 16;
   uint32_t a[KS][4];  // first operand: rows 0-7 keys, rows 8-15 queries
-  float c;            // running sum of g at this lane's token t = lane / 4
-  float r, rq;        // 1 / |k_t|, scale / |q_t| (1 and scale without normalisation)
-  float beta;
-  float A[2], P[2];   // coefficients of u_j in u_t and o_t for j = 2 (lane % 4) + {0, 1}
-  float u[2][2];      // u_t of value rows r0 + 8 i + 2 (lane % 4) + {0, 1}
+  float kk[4];        // k_t.k_j and q_t.k_j among the block's tokens, normalised and scaled
+  float wk[4];        // k_t.k_j and q_t.k_j with the waiting keys, times 1 / |k_t| and scale / |q_t|
+  float r;            // 1 / |k_t| (1 without normalisation)
 
-  // the block's tokens: keys and queries in shared memory, rows of DK bf16 at kTokenRow<DK> bytes
+  // keys and queries in shared memory, rows of DK bf16 at kTokenRow<DK> bytes
   __device__ __forceinline__ void load(const uint8_t* keys, const uint8_t* queries, int T, int lane) {
     const int t = lane >> 2, cc = lane & 3;
     const bool live = t < T;
-    const uint8_t *kp = keys + t * kTokenRow<DK> + 8 * cc, *qp = queries + t * kTokenRow<DK> + 8 * cc;
+    const uint8_t *kp = keys + t * kTokenRow<DK> + 16 * cc, *qp = queries + t * kTokenRow<DK> + 16 * cc;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-    for (int x = 0; x < KS; ++x) {
-      const uint2 kw = live ? *reinterpret_cast<const uint2*>(kp + 32 * x) : make_uint2(0u, 0u);
-      const uint2 qw = live ? *reinterpret_cast<const uint2*>(qp + 32 * x) : make_uint2(0u, 0u);
-      a[x][0] = kw.x;
-      a[x][1] = qw.x;
-      a[x][2] = kw.y;
-      a[x][3] = qw.y;
+    for (int y = 0; y < KS / 2; ++y) {
+      const uint4 kw = live ? *reinterpret_cast<const uint4*>(kp + 64 * y) : zero;
+      const uint4 qw = live ? *reinterpret_cast<const uint4*>(qp + 64 * y) : zero;
+      a[2 * y][0] = kw.x;
+      a[2 * y][1] = qw.x;
+      a[2 * y][2] = kw.y;
+      a[2 * y][3] = qw.y;
+      a[2 * y + 1][0] = kw.z;
+      a[2 * y + 1][1] = qw.z;
+      a[2 * y + 1][2] = kw.w;
+      a[2 * y + 1][3] = qw.w;
     }
   }
 
-  // running decays, norms and the coefficients among the block's own tokens
-  __device__ __forceinline__ void prepare(const DeltaTokens& tk, float g, float b, int lane) {
+  // the Gram products, the same for every value head of the key head;
+  // `waiting`: the waiting keys, as `keys` of load()
+  __device__ __forceinline__ void gram(const DeltaTokens& tk, const uint8_t* waiting, int acc, int lane) {
     const int t = lane >> 2, cc = lane & 3;
     const unsigned full = 0xffffffffu;
-    c = g;
-    beta = b;
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      const float y = __shfl_up_sync(full, c, o);
-      if (lane >= o) c += y;
-    }
-    float kk[4] = {0.f, 0.f, 0.f, 0.f};  // k_t.k_j, then q_t.k_j, j = 2 cc + {0, 1}
+    for (int i = 0; i < 4; ++i) kk[i] = wk[i] = 0.0f;
 #pragma unroll
     for (int x = 0; x < KS; ++x) mma_bf16(kk, a[x], a[x][0], a[x][2]);
+    if (acc > 0) {
+#pragma unroll
+      for (int y = 0; y < KS / 2; ++y) {
+        const uint4 w = t < acc ? *reinterpret_cast<const uint4*>(waiting + t * kTokenRow<DK> + 16 * cc + 64 * y)
+                                : make_uint4(0u, 0u, 0u, 0u);
+        mma_bf16(wk, a[2 * y], w.x, w.y);
+        mma_bf16(wk, a[2 * y + 1], w.z, w.w);
+      }
+    }
+    float rq = tk.scale;
     r = 1.0f;
-    rq = tk.scale;
     if (tk.l2norm) {
       float qq[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -211,63 +261,15 @@ struct DeltaBlock {
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int j = 2 * cc + i;
-      const float cj = __shfl_sync(full, c, j * 4), rj = __shfl_sync(full, r, j * 4);
-      const float e = j <= t ? expf(c - cj) * rj : 0.0f;
-      A[i] = j < t ? beta * r * e * kk[i] : 0.0f;
-      P[i] = e * rq * kk[2 + i];
+      const float rj = __shfl_sync(full, r, (2 * cc + i) * 4);
+      kk[i] *= r * rj;
+      kk[2 + i] *= rq * rj;
+      wk[i] *= r;
+      wk[2 + i] *= rq;
     }
+    kq = rq;
   }
-
-  // products of the state rows with the keys and queries, then the triangular
-  // solve; vw: the lane's token's values of value rows r0 + 8 i + 2 (lane % 4)
-  // + {0, 1}; o gets the outputs of the same rows
-  __device__ __forceinline__ void solve(const DeltaState<DK>& S, const uint32_t (&vw)[2], int T, int lane, float (&o)[2][2]) {
-    const int t = lane >> 2, cc = lane & 3;
-    const unsigned full = 0xffffffffu;
-    const float ec = expf(c);
-    const float fu = -beta * ec * r, fo = ec * rq;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int x = 0; x < KS; ++x) {
-        uint32_t h0, l0, h1, l1;
-        split_bf16x2(S.s[i][x].x, S.s[i][x].y, h0, l0);
-        split_bf16x2(S.s[i][x].z, S.s[i][x].w, h1, l1);
-        mma_bf16(d, a[x], h0, h1);
-        mma_bf16(d, a[x], l0, l1);
-      }
-      u[i][0] = fmaf(fu, d[0], beta * bf16lo(vw[i]));
-      u[i][1] = fmaf(fu, d[1], beta * bf16hi(vw[i]));
-      o[i][0] = fo * d[2];
-      o[i][1] = fo * d[3];
-    }
-#pragma unroll
-    for (int j = 0; j < kDeltaT; ++j) {
-      if (j >= T) break;
-      // u_j is final in the lanes of token j once every earlier token's share is in
-      const float Aj = __shfl_sync(full, A[j & 1], t * 4 + (j >> 1)), Pj = __shfl_sync(full, P[j & 1], t * 4 + (j >> 1));
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float uj = __shfl_sync(full, u[i][e], j * 4 + cc);
-          // selected, not multiplied by zero: a later token's NaN stays out of the earlier ones
-          if (t > j) u[i][e] = fmaf(-Aj, uj, u[i][e]);
-          if (t >= j) o[i][e] = fmaf(Pj, uj, o[i][e]);
-        }
-    }
-  }
-
-  __device__ __forceinline__ void store_out(const float (&o)[2][2], uint16_t* out, long long stride, int T, int lane) const {
-    const int t = lane >> 2, cc = lane & 3;
-    if (t < T) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        *reinterpret_cast<uint32_t*>(out + t * stride + 8 * i + 2 * cc) = cvt_bf16x2(o[i][0], o[i][1]);
-    }
-  }
+  float kq;  // scale / |q_t|
 };
 
 // host side

@@ -13,66 +13,116 @@ struct DeltaStepArgs {
   const int* cu;
   int batch, T;
   long long tokens;
-  int tiles;         // blocks per (row, value head)
+  int tiles;         // kStepRows value rows a head has
+  int items, per;    // (value head, tile) items of a key head, and how many of them a block takes
   unsigned* ticket;  // scratch [batch]: blocks that have read the row's `pend` (zero between calls)
 };
 
 constexpr int kStepWarps = 4;
-constexpr int kStepRows = kStepWarps * 16;  // value rows of a block
+constexpr int kStepRows = kStepWarps * 16;  // value rows of a tile
 
-// One warp per 16 value rows of a (row, value head): reads its part of S once,
-// adds the accepted drafts of the step before, writes it back if there were
-// any, and forms the new drafts' outputs and corrections from registers.  The
-// block's loads go out in three rounds -- the row's scalars; the state, the new
-// tokens and `pend`; the waiting drafts -- and only the first two are waited for
-// one after another: the state's, the longest, covers the third.
-template <int DK>
-__global__ void __launch_bounds__(kStepWarps * 32, 4) delta_step_kernel(const DeltaStepArgs a) {
+// A warp's item on its way from memory: its state rows (a bulk copy) and, for
+// this item and the next in turn, of the waiting drafts the corrections of these
+// rows and the running sums, of the new tokens the values of these rows, log
+// decays and rates.
+template <int DK, bool F32>
+struct alignas(128) StepWarp {
+  uint8_t s[16 * DK * (F32 ? 4 : 2)];
+  struct alignas(16) Small {
+    float w[kDeltaT][16];
+    uint16_t v[kDeltaT][16];
+    float c[kDeltaT], g[kDeltaT], beta[kDeltaT];
+  } x[2];
+  uint64_t bar;  // the state rows have landed
+};
+template <int DK, bool F32>
+struct alignas(128) StepSmem {
+  StepWarp<DK, F32> warp[kStepWarps];
+  alignas(16) uint8_t k[kDeltaT * kTokenRow<DK>];  // the new tokens' keys and queries
+  alignas(16) uint8_t q[kDeltaT * kTokenRow<DK>];
+  alignas(16) uint8_t pk[kDeltaT * kTokenRow<DK>];  // the waiting drafts' keys, and in fp32
+  alignas(16) float p[kDeltaT * DK];
+};
+// every destination of a 16-byte or bulk copy starts on 16 bytes
+static_assert(sizeof(StepWarp<64, false>) % 128 == 0 && sizeof(StepWarp<128, true>) % 128 == 0, "a warp's part keeps the next one's alignment");
+static_assert(sizeof(StepWarp<64, false>::Small) % 16 == 0 && kTokenRow<64> % 16 == 0 && kTokenRow<128> % 16 == 0, "rows start on 16 bytes");
+
+// A block takes `per` items -- 64 value rows of a value head each -- of a (row,
+// key head); the tokens' keys and queries, their Gram products and the waiting
+// keys serve all of them.  One warp per 16 value rows reads its part of S once
+// (one bulk copy: the rows are contiguous), and with the rows in registers sends
+// for its next item's; it forms the new drafts' outputs and corrections, adds the
+// accepted drafts of the step before and writes the rows back if there were any.
+template <int DK, bool F32>
+__global__ void __launch_bounds__(kStepWarps * 32, 3) delta_step_kernel(const DeltaStepArgs a) {
+  extern __shared__ __align__(128) uint8_t raw[];
+  StepSmem<DK, F32>& sm = *reinterpret_cast<StepSmem<DK, F32>*>(raw);
   __shared__ int sh[2];
-  __shared__ __align__(16) uint8_t s_k[kDeltaT * kTokenRow<DK>], s_q[kDeltaT * kTokenRow<DK>];
-  __shared__ __align__(16) float s_p[kDeltaT * DK], s_w[kDeltaT * kStepRows], s_c[kDeltaT];  // the waiting drafts
-  constexpr int CH = DK / 8;
+  constexpr int CH = DK / 8, kRow = DK * (F32 ? 4 : 2);
+  constexpr unsigned full = 0xffffffffu;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, t = lane >> 2, cc = lane & 3;
+  StepWarp<DK, F32>& wm = sm.warp[warp];
+  if (lane == 0) {
+    mbar_init(&wm.bar, 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  const int groups = (a.items + a.per - 1) / a.per;
+  const int b = blockIdx.x / (a.c.Hk * groups), hk = blockIdx.x / groups % a.c.Hk;
+  const int item0 = blockIdx.x % groups * a.per;
+  int left = min(a.per, a.items - item0);
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, m = lane >> 2, cc = lane & 3;
-  const int tile = blockIdx.x % a.tiles;
-  const int h = (blockIdx.x / a.tiles) % a.c.Hv;
-  const int b = blockIdx.x / a.tiles / a.c.Hv;
   const int s = a.slot_idx[b];
   const long long tok0 = a.cu ? a.cu[b] : static_cast<long long>(b) * a.T;
-  const int n = a.cu ? a.cu[b + 1] - a.cu[b] : a.T;
+  const int n = a.cu ? a.cu[b + 1] - static_cast<int>(tok0) : a.T;
   const int acc = a.accepted ? a.accepted[b] : 0;
   if (n < 0 || n > a.T || tok0 < 0 || tok0 + n > a.tokens) {  // the row's tokens are not known: nothing to write
-    if (tid == 0 && blockIdx.x % (a.tiles * a.c.Hv) == 0) set_error(a.c.err, RSSM_ERRBIT_SEQLEN);
+    if (tid == 0 && blockIdx.x % (a.c.Hk * groups) == 0) set_error(a.c.err, RSSM_ERRBIT_SEQLEN);
     return;
   }
-  const int dv = a.c.dv, Hv = a.c.Hv, np = a.c.np, hk = h / a.c.rep;
-  const int r0 = tile * kStepRows + warp * 16;
-  const bool mine = r0 < dv;
-  const long long ostride = static_cast<long long>(Hv) * dv;
-  uint16_t* out = a.tk.out + tok0 * ostride + h * dv + r0;
-  DeltaBlock<DK> blk;
-  float o[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+  const int dv = a.c.dv, Hv = a.c.Hv, np = a.c.np;
+  const bool live = t < n;
+  // the item: value head hv, and the warp's first value row in it
+  int hv = hk * a.c.rep + item0 / a.tiles, r0 = item0 % a.tiles * kStepRows + warp * 16;
+  const auto step_on = [&](int& h, int& r) {
+    r += kStepRows;
+    if (r - warp * 16 >= dv) {
+      r = warp * 16;
+      ++h;
+    }
+  };
+  uint16_t* out = a.tk.out + (tok0 + t) * Hv * dv + 2 * cc;
+  const auto zeros = [&]() {
+    for (; left > 0; --left, step_on(hv, r0))
+      if (r0 < dv && live) {
+        *reinterpret_cast<uint32_t*>(out + hv * dv + r0) = 0u;
+        *reinterpret_cast<uint32_t*>(out + hv * dv + r0 + 8) = 0u;
+      }
+  };
   if (s <= 0 || s >= a.c.S) {
-    if (mine) blk.store_out(o, out, ostride, n, lane);
+    zeros();
     return;
   }
-  DeltaState<DK> S;
-  const long long head = s * a.c.state_stride + (static_cast<long long>(h) * dv + r0) * DK;
-  if (mine) S.load(a.c.state, head, a.c.dtype, lane);
+  uint8_t* state = static_cast<uint8_t*>(a.c.state) + s * a.c.state_stride * (F32 ? 4 : 2);
+  const uint16_t* vp = a.tk.v + (tok0 + t) * a.tk.v_stride + 8 * (cc & 1);
+  const float* gp = (lane < 8 ? a.tk.g : a.tk.beta) + (tok0 + (lane & 7)) * Hv;
+  int turn = 0;
+  // an item's state rows, and the new tokens' part
+  const auto fetch = [&](int h, int r, int x) {
+    if (r >= dv) return;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&wm.bar, 16 * kRow);
+      bulk_g2s(wm.s, state + static_cast<long long>(h * dv + r) * kRow, 16 * kRow, &wm.bar);
+    }
+    if (live && cc < 2) cp_async16(&wm.x[x].v[t][8 * cc], vp + h * dv + r);
+    if (lane < 16 && (lane & 7) < n) cp_async4(lane < 8 ? &wm.x[x].g[lane] : &wm.x[x].beta[lane & 7], gp + h);
+  };
+  fetch(hv, r0, 0);
   for (int i = tid; i < n * CH; i += kStepWarps * 32) {
-    const int t = i / CH, ch = i % CH;
-    cp_async16(s_k + t * kTokenRow<DK> + ch * 16, a.tk.k + (tok0 + t) * a.tk.k_stride + hk * DK + ch * 8);
-    cp_async16(s_q + t * kTokenRow<DK> + ch * 16, a.tk.q + (tok0 + t) * a.tk.q_stride + hk * DK + ch * 8);
-  }
-  float g = 0.0f, beta = 0.0f;
-  uint32_t vw[2] = {0u, 0u};
-  if (mine && m < n) {
-    g = fmaxf(a.tk.g[(tok0 + m) * Hv + h], kMinLog);
-    beta = a.tk.beta[(tok0 + m) * Hv + h];
-    const uint16_t* v = a.tk.v + (tok0 + m) * a.tk.v_stride + h * dv + r0 + 2 * cc;
-    vw[0] = *reinterpret_cast<const uint32_t*>(v);
-    vw[1] = *reinterpret_cast<const uint32_t*>(v + 8);
+    const int r = i / CH, ch = i % CH;
+    cp_async16(sm.k + r * kTokenRow<DK> + ch * 16, a.tk.k + (tok0 + r) * a.tk.k_stride + hk * DK + ch * 8);
+    cp_async16(sm.q + r * kTokenRow<DK> + ch * 16, a.tk.q + (tok0 + r) * a.tk.q_stride + hk * DK + ch * 8);
   }
   if (tid == 0) {
     const int2 p = __ldcg(reinterpret_cast<const int2*>(a.c.pend) + s);
@@ -80,72 +130,190 @@ __global__ void __launch_bounds__(kStepWarps * 32, 4) delta_step_kernel(const De
     sh[1] = p.y;
   }
   __syncthreads();
-  const int side = sh[0] & 1;
-  const bool ok = acc >= 0 && acc <= sh[1];
+  const int side = sh[0] & 1, to = side ^ 1;
+  const bool ok = acc >= 0 && acc <= sh[1] && acc <= np;
   // every block of the row takes a ticket once it has read (side, count); the
   // last one knows that all have, and turns the sides
   if (tid == 0) {
     __threadfence();
-    const unsigned blocks = static_cast<unsigned>(a.tiles * Hv);
+    const unsigned blocks = static_cast<unsigned>(a.c.Hk * groups);
     if (atomicInc(a.ticket + b, blocks - 1u) == blocks - 1u) {
       if (ok)
-        reinterpret_cast<int2*>(a.c.pend)[s] = make_int2(side ^ 1, n);
+        reinterpret_cast<int2*>(a.c.pend)[s] = make_int2(to, n);
       else
         set_error(a.c.err, RSSM_ERRBIT_ACCEPT);
     }
   }
   if (!ok) {
     cp_async_wait_all();
-    if (mine) blk.store_out(o, out, ostride, n, lane);
+    if (r0 < dv) mbar_wait(&wm.bar, 0);  // nothing is in flight at the end
+    zeros();
     return;
   }
+  const float* pw = a.c.pend_w + s * a.c.pend_w_stride + 4 * cc;
+  const float* pc = a.c.pend_c + s * a.c.pend_c_stride + lane;
+  const auto fetch_waiting = [&](int h, int r, int x) {
+    const int at = (side * Hv + h) * np;
+    if (r < dv && t < acc) cp_async16(&wm.x[x].w[t][4 * cc], pw + static_cast<long long>(at + t) * dv + r);
+    if (lane < acc) cp_async4(&wm.x[x].c[lane], pc + at);
+  };
   if (acc > 0) {
-    const float* pc = a.c.pend_c + s * a.c.pend_c_stride + (static_cast<long long>(side) * Hv + h) * np;
-    const float* pw = a.c.pend_w + s * a.c.pend_w_stride + (static_cast<long long>(side) * Hv + h) * np * dv + tile * kStepRows;
+    fetch_waiting(hv, r0, 0);
     const uint16_t* pk = a.c.pend_k + s * a.c.pend_k_stride + (static_cast<long long>(side) * a.c.Hk + hk) * np * DK;
-    if (tid < acc) cp_async4(s_c + tid, pc + tid);
-    for (int i = tid; i < acc * (kStepRows / 4); i += kStepWarps * 32) {
-      const int j = i / (kStepRows / 4), r = i % (kStepRows / 4) * 4;
-      if (tile * kStepRows + r < dv) cp_async16(s_w + j * kStepRows + r, pw + static_cast<long long>(j) * dv + r);
-    }
     for (int i = tid; i < acc * CH; i += kStepWarps * 32) {
       const uint4 x = *reinterpret_cast<const uint4*>(pk + i * 8);
-      float4* to = reinterpret_cast<float4*>(s_p + i * 8);
-      to[0] = make_float4(bf16lo(x.x), bf16hi(x.x), bf16lo(x.y), bf16hi(x.y));
-      to[1] = make_float4(bf16lo(x.z), bf16hi(x.z), bf16lo(x.w), bf16hi(x.w));
+      *reinterpret_cast<uint4*>(sm.pk + i / CH * kTokenRow<DK> + i % CH * 16) = x;
+      float4* d = reinterpret_cast<float4*>(sm.p + i * 8);
+      d[0] = make_float4(bf16lo(x.x), bf16hi(x.x), bf16lo(x.y), bf16hi(x.y));
+      d[1] = make_float4(bf16lo(x.z), bf16hi(x.z), bf16lo(x.w), bf16hi(x.w));
     }
   }
   cp_async_wait_all();
   __syncthreads();
-  if (!mine) return;
-  if (acc > 0) {
-    const float end = s_c[acc - 1];
-    S.decay(expf(end));
-    for (int j = 0; j < acc; ++j) {
-      const float e = expf(end - s_c[j]);
-      S.add(e * s_w[j * kStepRows + warp * 16 + m], e * s_w[j * kStepRows + warp * 16 + m + 8], s_p + j * DK, lane);
-    }
-    S.store(a.c.state, head, a.c.dtype, lane);
-  }
-  if (n == 0) return;
-  blk.load(s_k, s_q, n, lane);
-  blk.prepare(a.tk, g, beta, lane);
-  blk.solve(S, vw, n, lane, o);
-  blk.store_out(o, out, ostride, n, lane);
-  // the new drafts wait in the other half
-  if (m < n) {
-    const int to = side ^ 1;
-    float* pw = a.c.pend_w + s * a.c.pend_w_stride + ((static_cast<long long>(to) * Hv + h) * np + m) * dv + r0 + 2 * cc;
+  DeltaBlock<DK> blk;
+  blk.load(sm.k, sm.q, n, lane);
+  blk.gram(a.tk, sm.pk, acc, lane);
+  if (item0 == 0 && warp == 0 && live) {  // the new drafts wait in the other half
+    uint16_t* pk = a.c.pend_k + s * a.c.pend_k_stride + ((static_cast<long long>(to) * a.c.Hk + hk) * np + t) * DK + 8 * cc;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<float2*>(pw + 8 * i) = make_float2(blk.u[i][0] * blk.r, blk.u[i][1] * blk.r);
-    if (r0 == 0 && cc == 0) a.c.pend_c[s * a.c.pend_c_stride + (static_cast<long long>(to) * Hv + h) * np + m] = blk.c;
-    if (r0 == 0 && h % a.c.rep == 0) {
-      uint16_t* pk = a.c.pend_k + s * a.c.pend_k_stride + ((static_cast<long long>(to) * a.c.Hk + hk) * np + m) * DK + 4 * cc;
+    for (int y = 0; y < DK / 32; ++y)
+      *reinterpret_cast<uint4*>(pk + 32 * y) =
+          make_uint4(blk.a[2 * y][0], blk.a[2 * y][2], blk.a[2 * y + 1][0], blk.a[2 * y + 1][2]);
+  }
+  float* nw = a.c.pend_w + s * a.c.pend_w_stride + static_cast<long long>(to * Hv * np + t) * dv + 2 * cc;
+  float* nc = a.c.pend_c + s * a.c.pend_c_stride + to * Hv * np + t;
+  state += (t * DK + 8 * cc) * (F32 ? 4 : 2);
+  uint32_t parity = 0;
+  int head = -1;
+  float beta = 0.0f, c = 0.0f, ec = 0.0f, E = 1.0f, ew = 0.0f, A[2], P[2], gk[2], gq[2];
+#pragma unroll 1
+  for (; left > 0; --left, turn ^= 1) {
+    const typename StepWarp<DK, F32>::Small& x = wm.x[turn];
+    const int h = hv, r = r0;
+    step_on(hv, r0);
+    cp_async_wait_all();
+    __syncwarp();  // the other lanes' copies have landed too
+    if (r >= dv) {
+      if (left > 1) {
+        fetch(hv, r0, turn ^ 1);
+        if (acc > 0) fetch_waiting(hv, r0, turn ^ 1);
+      }
+      continue;
+    }
+    if (!__all_sync(full, mbar_wait(&wm.bar, parity))) {
+      if (lane == 0) set_error(a.c.err, RSSM_ERRBIT_TIMEOUT);
+      return;
+    }
+    parity ^= 1;
+    DeltaRow<DK, F32> S[2];
+    S[0].read(wm.s, t, cc);
+    S[1].read(wm.s, t + 8, cc);
+    __syncwarp();  // the rows are read
+    if (left > 1) {
+      fetch(hv, r0, turn ^ 1);
+      if (acc > 0) fetch_waiting(hv, r0, turn ^ 1);
+    }
+    if (h != head) {  // what the head's items share
+      head = h;
+      beta = live ? x.beta[t] : 0.0f;
+      // running sums and the coefficients among the block's own tokens
+      c = live ? fmaxf(x.g[t], kMinLog) : 0.0f;
 #pragma unroll
-      for (int x = 0; x < DK / 16; ++x) *reinterpret_cast<uint2*>(pk + 16 * x) = make_uint2(blk.a[x][0], blk.a[x][2]);
+      for (int o = 4; o < 32; o <<= 1) {
+        const float y = __shfl_up_sync(full, c, o);
+        if (lane >= o) c += y;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = 2 * cc + i;
+        const float d = c - __shfl_sync(full, c, j * 4);
+        const float e = j <= t ? __expf(d) : 0.0f;
+        A[i] = j < t ? beta * e * blk.kk[i] : 0.0f;
+        P[i] = e * blk.kk[2 + i];
+      }
+      ec = __expf(c);
+      if (acc > 0) {
+        const float end = x.c[acc - 1];
+        E = __expf(end);
+        ew = lane < acc ? __expf(end - x.c[lane]) : 0.0f;
+        const float e0 = __shfl_sync(full, ew, 2 * cc), e1 = __shfl_sync(full, ew, 2 * cc + 1);
+        gk[0] = blk.wk[0] * e0;
+        gk[1] = blk.wk[1] * e1;
+        gq[0] = blk.wk[2] * e0;
+        gq[1] = blk.wk[3] * e1;
+      }
+    }
+    // what the waiting drafts add to S0 k_t and S0 q_t
+    float wu[2][2] = {{0.f, 0.f}, {0.f, 0.f}}, wo[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+    if (acc > 0) {
+#pragma unroll
+      for (int j = 0; j < kDeltaT; ++j) {
+        if (j >= acc) break;
+        const float xk = __shfl_sync(full, gk[j & 1], t * 4 + (j >> 1)), xq = __shfl_sync(full, gq[j & 1], t * 4 + (j >> 1));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 w = *reinterpret_cast<const float2*>(&x.w[j][8 * i + 2 * cc]);
+          wu[i][0] = fmaf(xk, w.x, wu[i][0]);
+          wu[i][1] = fmaf(xk, w.y, wu[i][1]);
+          wo[i][0] = fmaf(xq, w.x, wo[i][0]);
+          wo[i][1] = fmaf(xq, w.y, wo[i][1]);
+        }
+      }
+    }
+    const float fk = E * blk.r, fq = E * blk.kq, be = beta * ec;
+    float u[2][2], o[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float d[4];
+      S[i].product(blk.a, d);
+      const uint32_t vw = live ? *reinterpret_cast<const uint32_t*>(&x.v[t][8 * i + 2 * cc]) : 0u;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        u[i][e] = fmaf(-be, fmaf(fk, d[e], wu[i][e]), beta * (e ? bf16hi(vw) : bf16lo(vw)));
+        o[i][e] = ec * fmaf(fq, d[2 + e], wo[i][e]);
+      }
+    }
+    if (acc > 0) {
+      uint8_t* mine = state + static_cast<long long>(h * dv + r) * kRow;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        S[i].decay(E);
+        for (int j = 0; j < acc; ++j) S[i].add(__shfl_sync(full, ew, j) * x.w[j][t + 8 * i], sm.p + j * DK, cc);
+        S[i].store(mine + 8 * i * kRow, a.c.wide);
+      }
+    }
+    if (n == 0) continue;
+#pragma unroll
+    for (int j = 0; j < kDeltaT; ++j) {
+      if (j >= n) break;
+      // u_j is final in the lanes of token j once every earlier token's share is in
+      const float Aj = __shfl_sync(full, A[j & 1], t * 4 + (j >> 1)), Pj = __shfl_sync(full, P[j & 1], t * 4 + (j >> 1));
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float uj = __shfl_sync(full, u[i][e], j * 4 + cc);
+          // selected, not multiplied by zero: a later token's NaN stays out of the earlier ones
+          if (t > j) u[i][e] = fmaf(-Aj, uj, u[i][e]);
+          if (t >= j) o[i][e] = fmaf(Pj, uj, o[i][e]);
+        }
+    }
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        *reinterpret_cast<uint32_t*>(out + h * dv + r + 8 * i) = cvt_bf16x2(o[i][0], o[i][1]);
+        *reinterpret_cast<float2*>(nw + static_cast<long long>(h * np) * dv + r + 8 * i) = make_float2(u[i][0] * blk.r, u[i][1] * blk.r);
+      }
+      if (r == 0 && cc == 0) nc[h * np] = c;
     }
   }
+}
+
+template <int DK, bool F32>
+cudaError_t launch_step(const DeltaStepArgs& a, unsigned blocks, cudaStream_t st) {
+  constexpr size_t smem = sizeof(StepSmem<DK, F32>);
+  const cudaError_t e = cudaFuncSetAttribute(delta_step_kernel<DK, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  return e == cudaSuccess ? launch_pdl(delta_step_kernel<DK, F32>, dim3(blocks), dim3(kStepWarps * 32), smem, st, a) : e;
 }
 
 bool al(const void* p, unsigned n) { return p && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -187,6 +355,7 @@ bool delta_view(const rssm_delta_cache* c, DeltaCacheView* o, rssm_status* st) {
   o->pend_c_stride = c->pend_c_slot_stride;
   o->pend = c->pend;
   o->err = c->error_word;
+  o->wide = al(c->state, 32) && c->state_slot_stride * esz % 32 == 0;
   *st = RSSM_OK;
   return true;
 }
@@ -244,11 +413,21 @@ extern "C" rssm_status rssm_delta_step(const rssm_delta_cache* cache, const void
   a.tokens = tokens;
   a.tiles = (a.c.dv + kStepRows - 1) / kStepRows;
   a.ticket = static_cast<unsigned*>(scratch);
-  const long long blocks = static_cast<long long>(batch) * a.c.Hv * a.tiles;
-  if (blocks > 0x7fffffffll) return RSSM_ERR_UNSUPPORTED;
+  a.items = a.c.rep * a.tiles;
+  // Items a block takes: as few as give one wave of blocks, all of a key head's
+  // where there are more -- then what the items share is worth more than the
+  // spread.  (64 rows of 16 key heads with 4 items, fp32: 1 an item 82 us, 4 an
+  // item 61 us; one row: 28 us against 32 us with the host's part.)
+  const long long wave = 3ll * num_sms();
+  if (wave == 0) return RSSM_ERR_CUDA;
+  const auto grid_of = [&](int per) { return static_cast<long long>(batch) * a.c.Hk * ((a.items + per - 1) / per); };
+  a.per = 1;
+  while (a.per < a.items && grid_of(a.per) > wave) a.per = a.per * 2 < a.items ? a.per * 2 : a.items;
+  if (grid_of(1) > 0x7fffffffll) return RSSM_ERR_UNSUPPORTED;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = cache->dkey == 128
-                            ? launch_pdl(delta_step_kernel<128>, dim3(static_cast<unsigned>(blocks)), dim3(kStepWarps * 32), 0, cs, a)
-                            : launch_pdl(delta_step_kernel<64>, dim3(static_cast<unsigned>(blocks)), dim3(kStepWarps * 32), 0, cs, a);
+  const unsigned grid = static_cast<unsigned>(grid_of(a.per));
+  const bool f32 = a.c.dtype == RSSM_F32;
+  const cudaError_t e = cache->dkey == 128 ? (f32 ? launch_step<128, true>(a, grid, cs) : launch_step<128, false>(a, grid, cs))
+                                           : (f32 ? launch_step<64, true>(a, grid, cs) : launch_step<64, false>(a, grid, cs));
   return e == cudaSuccess ? RSSM_OK : RSSM_ERR_CUDA;
 }

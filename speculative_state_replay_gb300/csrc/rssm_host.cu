@@ -9,6 +9,32 @@
 #include "rssm.h"
 #include "rssm_internal.h"
 
+namespace rssm {
+
+// SMs the persistent kernels size their grids for: the current device's SM
+// count (cached per device), capped by the environment variable
+// RSSM_SM_LIMIT when it holds a positive integer (read at every call, so a
+// caller can leave SMs to concurrent work; results do not depend on it)
+int num_sms() {
+  static std::mutex mu;
+  static int cache[64] = {0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+  int n = dev < 64 ? cache[dev] : 0;
+  if (!n) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    std::lock_guard<std::mutex> g(mu);
+    if (dev < 64) cache[dev] = n;
+  }
+  if (const char* lim = getenv("RSSM_SM_LIMIT")) {
+    const long v = strtol(lim, nullptr, 10);
+    if (v > 0 && v < n) n = static_cast<int>(v);
+  }
+  return n;
+}
+
+}  // namespace rssm
+
 using namespace rssm;
 
 namespace {
@@ -102,28 +128,6 @@ rssm_status check_cache(const rssm_cache* c, Cache* out) {
     if (fp4) v.read_scale = nullptr;
   }
   return RSSM_OK;
-}
-
-// SMs the persistent kernels size their grids for: the current device's SM
-// count (cached per device), capped by the environment variable
-// RSSM_SM_LIMIT when it holds a positive integer (read at every call, so a
-// caller can leave SMs to concurrent work; results do not depend on it)
-int num_sms() {
-  static std::mutex mu;
-  static int cache[64] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
-  int n = dev < 64 ? cache[dev] : 0;
-  if (!n) {
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    std::lock_guard<std::mutex> g(mu);
-    if (dev < 64) cache[dev] = n;
-  }
-  if (const char* lim = getenv("RSSM_SM_LIMIT")) {
-    const long v = strtol(lim, nullptr, 10);
-    if (v > 0 && v < n) n = static_cast<int>(v);
-  }
-  return n;
 }
 
 rssm_status step_common(const rssm_cache* cache, const void* x, const float* dt, const float* A, const void* B,
