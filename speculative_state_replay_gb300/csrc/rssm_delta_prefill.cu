@@ -422,7 +422,7 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_
   return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
          (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) | (swizzle << 61);
 }
-constexpr uint64_t kSw128 = 2, kSw64 = 4;
+constexpr uint64_t kSw128 = 2;
 // kind::f16, bf16 operands, fp32 accumulators, M = 128
 __host__ __device__ constexpr uint32_t instruction(int n, bool a_mn, bool b_mn) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
@@ -441,22 +441,18 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
 }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_ld16(float* v, uint32_t addr) {
+__device__ __forceinline__ void tc_ld8(float* v, uint32_t addr) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(addr)
-      : "memory");
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr)
+               : "memory");
 }
-__device__ __forceinline__ void tc_st16(uint32_t addr, const float* v) {
+__device__ __forceinline__ void tc_st8(uint32_t addr, const float* v) {
   const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -471,6 +467,11 @@ __device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x,
 
 // --------------------------------------------------------------------------
 // delta_scan_kernel: one block per (prompt, value head, NDV value columns).
+//
+// A product's time here is its operands' way out of shared memory (128 bytes a
+// cycle: 32 cycles for the 128 rows of a step of 16), so the hi and lo parts of
+// S, R and U stand side by side and one instruction takes both: X, U and S have
+// a column for each part, added when they are read.
 // --------------------------------------------------------------------------
 template <int DK, int NDV>
 struct ScanSmem {
@@ -479,34 +480,33 @@ struct ScanSmem {
   static constexpr int kKQ = 0;  // per 64 key columns: K (64 rows of 128 bytes), then Q
   static constexpr int kHi = kKQ + kHalves * 16384;
   static constexpr int kLo = kHi + kImgHi;
-  static constexpr int kV = kLo + 16384;
+  static constexpr int kV = kLo + kImgHi;
   static constexpr int kVecs = kV + kC * NDV * 2;
   static constexpr int kStage = kVecs + kVec;
-  static constexpr int kOps = kStages * kStage;
-  static constexpr int kSh = kOps, kSl = kSh + DK * NDV * 2;
-  static constexpr int kRh = kSl + DK * NDV * 2, kRl = kRh + kC * NDV * 2;
-  static constexpr int kUh = kRl + kC * NDV * 2, kUl = kUh + kC * NDV * 2;
-  static constexpr int kBars = kUl + kC * NDV * 2;
+  // operands: rows of 128 bytes, for 32 columns hi and lo in one row, for 64 in one block each
+  static constexpr int kBlocks = NDV / 32;
+  static constexpr int kS = kStages * kStage;
+  static constexpr int kR = kS + kBlocks * DK * 128;  // R, then U in its place
+  static constexpr int kBars = kR + kBlocks * kC * 128;
   static constexpr int kBytes = kBars + 128 + 1024;  // barriers, and room to start on 1024 bytes
   static constexpr uint32_t kTx = kHalves * 16384 + kImg + kC * NDV * 2 + kVec;
 };
 
-constexpr int kWorkWarps = 8;
+constexpr int kWorkWarps = 16;
 
-// Roles.  Warps 0-7 turn accumulators into the next product's operands: warp w
-// reads TMEM lanes 32 (w % 4) .. + 31, and half of the value columns by w / 4.
-// In X and U the first 64 lanes are the chunk's tokens (warps with w % 4 < 2
-// make R, then U), the other 64 the same tokens' outputs (the other warps
-// store them); of S a lane is a key column.  Warp 8 issues the copies, warp 9
-// the products.
+// Roles.  Warps 0-15 turn accumulators into the next product's operands: warp w
+// reads TMEM lanes 32 (w % 4) .. + 31, and a quarter of the value columns by
+// w / 4.  In X and U the first 64 lanes are the chunk's tokens (warps with
+// w % 4 < 2 make R, then U), the other 64 the same tokens' outputs (the other
+// warps store them); of S a lane is a key column.  Warp 16 issues the copies,
+// warp 17 the products.
 template <int DK, int NDV>
 __global__ void __launch_bounds__(kWorkWarps * 32 + 64, 1)
     delta_scan_kernel(const DeltaPrefillArgs a, const __grid_constant__ CUtensorMap mq,
                       const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
   using L = ScanSmem<DK, NDV>;
-  constexpr int RB = NDV * 2, CN = NDV / 2;
-  constexpr uint64_t kSwB = NDV == 32 ? kSw64 : kSw128;
-  constexpr int kTmem = NDV == 32 ? 128 : 256;
+  constexpr int CN = NDV / 4;
+  constexpr int kTmem = NDV == 32 ? 256 : 512;
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
   __shared__ uint32_t tmem_base;
@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kWorkWarps * 32 + 64, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBars);
   uint64_t *b_full = bars, *b_empty = bars + L::kStages, *b_s = bars + 2 * L::kStages, *b_x = b_s + 1, *b_r = b_s + 2,
            *b_u = b_s + 3, *b_up = b_s + 4, *b_new = b_s + 5;
-  if (warp == 9) {
+  if (warp == kWorkWarps + 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)),
                  "n"(kTmem)
                  : "memory");
@@ -548,20 +548,23 @@ __global__ void __launch_bounds__(kWorkWarps * 32 + 64, 1)
       mbar_init(b_full + i, 1);
       mbar_init(b_empty + i, 1);
     }
-    mbar_init(b_s, kWorkWarps);  // S is split, and scaled in place
-    mbar_init(b_x, 1);           // X, Y
-    mbar_init(b_r, kWorkWarps / 2);
-    mbar_init(b_u, 1);
-    mbar_init(b_up, kWorkWarps / 2);
-    mbar_init(b_new, 1);  // S of the next chunk
+    mbar_init(b_s, kWorkWarps);       // S as an operand
+    mbar_init(b_x, 1);                // X, and Y under it
+    mbar_init(b_r, kWorkWarps / 2);   // R as an operand
+    mbar_init(b_u, 1);                // U, and the outputs' part under it
+    mbar_init(b_up, kWorkWarps);      // U as an operand, and S decayed in place
+    mbar_init(b_new, 1);              // S after the chunk
     fence_barrier_init();
   }
   tc_before();
   __syncthreads();
   tc_after();
-  const uint32_t tm_s = tmem_base, tm_x = tm_s + NDV, tm_u = tm_s + 2 * NDV;
+  const uint32_t tm_s = tmem_base, tm_x = tm_s + 2 * NDV, tm_u = tm_s + 4 * NDV;
   const int chunks = (n + kC - 1) / kC;
+  // the chain is a few hundred cycles long between waits: poll before sleeping
   const auto wait = [&](uint64_t* bar, uint32_t parity) {
+    for (int i = 0; i < 4096; ++i)
+      if (mbar_test(bar, parity)) return true;
     if (dead) return false;
     if (mbar_wait(bar, parity)) return true;
     dead = 1;
@@ -571,7 +574,7 @@ __global__ void __launch_bounds__(kWorkWarps * 32 + 64, 1)
   const auto wait_warp = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
   const uint8_t* units = a.units + (static_cast<long long>(start / kC + b) * a.c.Hv + h) * kUnit;
 
-  if (warp == 8) {
+  if (warp == kWorkWarps) {
     if (lane == 0) {
       const int hx = (h / a.c.rep) * DK;
       int c = 0;
@@ -595,67 +598,71 @@ __global__ void __launch_bounds__(kWorkWarps * 32 + 64, 1)
       for (int i = max(0, c - L::kStages); i < c; ++i)  // also after a wait that gave up: no copy is in flight at the end
         mbar_wait(b_full + i % L::kStages, (i / L::kStages) & 1);
     }
-  } else if (warp == 9) {
+  } else if (warp == kWorkWarps + 1) {
     if (lane == 0) {
-      constexpr uint32_t i_x = instruction(NDV, false, true), i_s = instruction(NDV, true, true);
+      constexpr uint32_t i_x = instruction(2 * NDV, false, true), i_lo = instruction(NDV, false, true),
+                         i_s = instruction(2 * NDV, true, true);
       const uint32_t base = smem_addr(sm);
-      const auto rows = [&](int at, int row) { return operand(base + at + row * RB, 16, 8 * RB, kSwB); };
+      // addresses are in the operands' low bits, in units of 16 bytes: offsets are added to them
+      const uint64_t d_s = operand(base + L::kS, DK * 128, 1024, kSw128), d_r = operand(base + L::kR, kC * 128, 1024, kSw128);
+      const uint64_t d_k = operand(base + L::kKQ, 16, 1024, kSw128);
+      // of 64 key columns the second 64 rows of the update are made from the queries, and nobody reads them
+      const uint64_t d_kt = operand(base + L::kKQ, DK == 128 ? 16384 : 8192, 1024, kSw128);
+      const uint64_t d_hi = operand(base + L::kHi, 16, 1024, kSw128), d_lo = operand(base + L::kLo, 16, 1024, kSw128);
       for (int c = 0; c < chunks; ++c) {
         const int st = c % L::kStages;
-        const uint32_t p = base + st * L::kStage;
+        const uint64_t p = static_cast<uint64_t>(st * L::kStage) >> 4;
         if (!wait(b_full + st, (c / L::kStages) & 1) || !wait(b_s, c & 1)) break;
         tc_after();
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int x = 0; x < DK / 16; ++x)
-            tc_mma(tm_x, operand(p + L::kKQ + (x >> 2) * 16384 + (x & 3) * 32, 16, 1024, kSw128),
-                   rows(part ? L::kSl : L::kSh, 16 * x), i_x, part || x);
+        for (int x = 0; x < DK / 16; ++x)
+          tc_mma(tm_x, d_k + p + (((x >> 2) * 16384 + (x & 3) * 32) >> 4), d_s + ((x * 2048) >> 4), i_x, x > 0);
         tc_commit(b_x);
         if (!wait(b_r, c & 1)) break;
         tc_after();
 #pragma unroll
-        for (int part = 0; part < 3; ++part)  // hi hi, lo hi, hi lo
+        for (int x = 0; x < kC / 16; ++x) tc_mma(tm_u, d_hi + p + ((x * 32) >> 4), d_r + ((x * 2048) >> 4), i_x, x > 0);
 #pragma unroll
-          for (int x = 0; x < kC / 16; ++x)
-            tc_mma(tm_u, operand(p + (part == 1 ? L::kLo : L::kHi) + x * 32, 16, 1024, kSw128),
-                   rows(part == 2 ? L::kRl : L::kRh, 16 * x), i_x, part || x);
+        for (int x = 0; x < kC / 16; ++x) tc_mma(tm_u, d_lo + p + ((x * 32) >> 4), d_r + ((x * 2048) >> 4), i_lo, true);
         tc_commit(b_u);
         if (!wait(b_up, c & 1)) break;
         tc_after();
-        // of 64 key columns the second 64 rows of the product are the queries', which nobody reads
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int x = 0; x < kC / 16; ++x)
-            tc_mma(tm_s, operand(p + L::kKQ + x * 2048, DK == 128 ? 16384 : 8192, 1024, kSw128),
-                   rows(part ? L::kUl : L::kUh, 16 * x), i_s, true);
+        for (int x = 0; x < kC / 16; ++x) tc_mma(tm_s, d_kt + p + ((x * 2048) >> 4), d_r + ((x * 2048) >> 4), i_s, true);
         tc_commit(b_new);
         tc_commit(b_empty + st);
       }
     }
   } else {
     const int q = warp & 3, row = 32 * q + lane, c0 = (warp >> 2) * CN;
-    const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
+    const uint32_t at = (static_cast<uint32_t>(32 * q) << 16) + c0;  // this warp's lanes and columns of an accumulator
     const bool is_tok = q < 2, has_s = row < DK;
     const int t = row & 63;
-    const auto piece = [&](int r, int col) {  // 8 columns from `col` of row r of an operand or V
-      const int ch = col >> 3;
-      return r * RB + ((NDV == 32 ? ch ^ ((r >> 1) & 3) : ch ^ (r & 7)) << 4);
+    // v (two sums of parts) from an accumulator's two halves
+    const auto get = [&](float* v, uint32_t from) {
+      float y[CN];
+#pragma unroll
+      for (int i = 0; i < CN; i += 8) {
+        tc_ld8(v + i, from + at + i);
+        tc_ld8(y + i, from + at + NDV + i);
+      }
+      tc_wait_ld();
+#pragma unroll
+      for (int i = 0; i < CN; ++i) v[i] += y[i];
     };
-    const auto put = [&](int hi, int lo, int r, const float* v) {
+    const auto put = [&](int to, int rows, int r, const float* v) {  // as an operand of `rows` rows
 #pragma unroll
       for (int i = 0; i < CN; i += 8) {
         uint32_t hw[4], lw[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) split_bf16x2(v[i + 2 * e], v[i + 2 * e + 1], hw[e], lw[e]);
-        const int to = piece(r, c0 + i);
-        *reinterpret_cast<uint4*>(sm + hi + to) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-        *reinterpret_cast<uint4*>(sm + lo + to) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+        const int ch = (c0 + i) >> 3;
+        uint8_t* p = sm + to;
+        *reinterpret_cast<uint4*>(p + sw128(r, ch)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+        *reinterpret_cast<uint4*>(p + (NDV == 32 ? sw128(r, ch + 4) : rows * 128 + sw128(r, ch))) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
       }
     };
     const auto arrive = [&](uint64_t* bar) {
-      fence_async();
       tc_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
@@ -680,7 +687,6 @@ __global__ void __launch_bounds__(kWorkWarps * 32 + 64, 1)
       ok = wait_warp(b_full + st, (c / L::kStages) & 1);
       ok = ok && (c == 0 || wait_warp(b_new, (c - 1) & 1));
       if (!ok) break;
-      const float w0 = vec[is_tok ? t : 128 + t], w1 = vec[64 + t], ec = vec[192];
       if (live < kC) {  // keys past the prompt's end may be another prompt's: whatever they are, they must not count
         for (int i = tid; i < (kC - live) * L::kHalves * 8; i += kWorkWarps * 32) {
           const int r = live + i / (L::kHalves * 8), x = i % (L::kHalves * 8);
@@ -690,47 +696,65 @@ __global__ void __launch_bounds__(kWorkWarps * 32 + 64, 1)
       if (has_s) {
         if (c > 0) {
           tc_after();
-#pragma unroll
-          for (int i = 0; i < CN; i += 16) tc_ld16(v + i, tm_s + lanes + c0 + i);
-          tc_wait_ld();
+          get(v, tm_s);
         }
-        put(L::kSh, L::kSl, row, v);
+        put(L::kS, DK, row, v);
+      }
+      fence_async();
+      arrive(b_s);
+      // while X is formed: the decayed S in place, and what this thread needs of the decay vectors
+      const float w0 = vec[is_tok ? t : 128 + t], w1 = vec[64 + t], ec = vec[192];
+      if (has_s) {
+        float zero[CN];
 #pragma unroll
-        for (int i = 0; i < CN; ++i) v[i] *= ec;
+        for (int i = 0; i < CN; ++i) {
+          v[i] *= ec;
+          zero[i] = 0.0f;
+        }
 #pragma unroll
-        for (int i = 0; i < CN; i += 16) tc_st16(tm_s + lanes + c0 + i, v + i);
+        for (int i = 0; i < CN; i += 8) {
+          tc_st8(tm_s + at + i, v + i);
+          tc_st8(tm_s + at + NDV + i, zero + i);
+        }
         tc_wait_st();
       }
-      arrive(b_s);
-      if (!(ok = wait_warp(b_x, c & 1))) break;
-      tc_after();
-#pragma unroll
-      for (int i = 0; i < CN; i += 16) tc_ld16(v + i, tm_x + lanes + c0 + i);
-      tc_wait_ld();
+      uint32_t xw[CN / 2];
       if (is_tok) {
 #pragma unroll
         for (int i = 0; i < CN; i += 8) {
-          const uint4 x = *reinterpret_cast<const uint4*>(p + L::kV + piece(t, c0 + i));
-          const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[i + 2 * e] = t < live ? fmaf(-w0, v[i + 2 * e], bf16lo(xw[e])) : 0.0f;
-            v[i + 2 * e + 1] = t < live ? fmaf(-w0, v[i + 2 * e + 1], bf16hi(xw[e])) : 0.0f;
-          }
+          const int ch = (c0 + i) >> 3;
+          const uint4 x = *reinterpret_cast<const uint4*>(
+              p + L::kV + (NDV == 32 ? t * 64 + ((ch ^ ((t >> 1) & 3)) << 4) : static_cast<int>(sw128(t, ch))));
+          xw[i / 2] = x.x;
+          xw[i / 2 + 1] = x.y;
+          xw[i / 2 + 2] = x.z;
+          xw[i / 2 + 3] = x.w;
         }
-        put(L::kRh, L::kRl, t, v);
+      } else {
+        arrive(b_up);
+      }
+      if (!(ok = wait_warp(b_x, c & 1))) break;
+      tc_after();
+      get(v, tm_x);
+      if (is_tok) {
+#pragma unroll
+        for (int i = 0; i < CN; i += 2) {
+          v[i] = t < live ? fmaf(-w0, v[i], bf16lo(xw[i / 2])) : 0.0f;
+          v[i + 1] = t < live ? fmaf(-w0, v[i + 1], bf16hi(xw[i / 2])) : 0.0f;
+        }
+        put(L::kR, kC, t, v);
+        fence_async();
         arrive(b_r);
       }
       if (!(ok = wait_warp(b_u, c & 1))) break;
       tc_after();
       float u[CN];
-#pragma unroll
-      for (int i = 0; i < CN; i += 16) tc_ld16(u + i, tm_u + lanes + c0 + i);
-      tc_wait_ld();
+      get(u, tm_u);
       if (is_tok) {
 #pragma unroll
         for (int i = 0; i < CN; ++i) u[i] *= w1;
-        put(L::kUh, L::kUl, t, u);
+        put(L::kR, kC, t, u);
+        fence_async();
         arrive(b_up);
       } else if (t < live) {
         uint16_t* o = a.tk.out + (start + c * kC + t) * ostride + h * dv + dv0 + c0;
@@ -750,9 +774,7 @@ __global__ void __launch_bounds__(kWorkWarps * 32 + 64, 1)
       ok = wait_warp(b_new, (chunks - 1) & 1);
       if (ok && has_s) {
         tc_after();
-#pragma unroll
-        for (int i = 0; i < CN; i += 16) tc_ld16(v + i, tm_s + lanes + c0 + i);
-        tc_wait_ld();
+        get(v, tm_s);
       }
     }
     if (ok && has_s) {
@@ -769,7 +791,7 @@ __global__ void __launch_bounds__(kWorkWarps * 32 + 64, 1)
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == 9)
+  if (warp == kWorkWarps + 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "n"(kTmem) : "memory");
   if (tid == 0) {
     if (dead) set_error(a.c.err, RSSM_ERRBIT_TIMEOUT);
@@ -870,13 +892,18 @@ extern "C" rssm_status rssm_delta_prefill(const rssm_delta_cache* cache, const v
   a.tokens = tokens;
   a.units = static_cast<uint8_t*>(scratch) + ticket_bytes(batch);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  // Value columns of a block.  A chunk's chain takes little longer for 64 than
+  // for 32, so 32 only where the blocks then still run all at once.
+  const int sms = num_sms();
+  if (sms == 0) return RSSM_ERR_CUDA;
+  const bool narrow = a.c.dv <= 32 || static_cast<long long>(batch) * a.c.Hv * ((a.c.dv + 31) / 32) <= sms;
   cudaError_t e;
   if (cache->dkey == 128) {
     e = launch_chunks<128>(a, cs);
-    if (e == cudaSuccess) e = launch_scan<128, 32>(a, cs);
+    if (e == cudaSuccess) e = narrow ? launch_scan<128, 32>(a, cs) : launch_scan<128, 64>(a, cs);
   } else {
     e = launch_chunks<64>(a, cs);
-    if (e == cudaSuccess) e = launch_scan<64, 32>(a, cs);
+    if (e == cudaSuccess) e = narrow ? launch_scan<64, 32>(a, cs) : launch_scan<64, 64>(a, cs);
   }
   return e == cudaSuccess ? RSSM_OK : RSSM_ERR_CUDA;
 }
