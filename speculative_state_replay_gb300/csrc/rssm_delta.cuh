@@ -91,6 +91,7 @@ __device__ __forceinline__ pair pack2(float lo, float hi) {
 }
 __device__ __forceinline__ void unpack2(pair d, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(d)); }
 __device__ __forceinline__ void fma2(pair& d, pair a, pair b) { asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b)); }
+__device__ __forceinline__ void add2(pair& d, pair a) { asm("add.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(a)); }
 __device__ __forceinline__ void mul2(pair& d, pair a) { asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(a)); }
 __device__ __forceinline__ uint32_t cvt_bf16x2(pair d) {
   float lo, hi;
@@ -98,9 +99,9 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(pair d) {
   return cvt_bf16x2(lo, hi);
 }
 __device__ __forceinline__ void split_bf16x2(pair d, uint32_t& h, uint32_t& l) {
-  float lo, hi;
-  unpack2(d, lo, hi);
-  split_bf16x2(lo, hi, h, l);
+  h = cvt_bf16x2(d);
+  fma2(d, pack2(-1.0f, -1.0f), pack2(bf16lo(h), bf16hi(h)));  // the remainder, exact
+  l = cvt_bf16x2(d);
 }
 
 // Rows m (or m + 8) of a warp's state: a lane's 2 KS pairs of columns.

@@ -4,22 +4,24 @@
 // Within a chunk, with c the running sum of g, r = 1/|k| (1 without
 // normalisation) and the keys as given,
 //     A[i][j] = beta_i e^{c_i - c_j} r_i r_j (k_i . k_j)      (j < i)
-//     T'      = (I + A)^-1 diag(beta)
+//     T       = (I + A)^-1
 //     P[i][j] = scale e^{c_i - c_j} rq_i r_j (q_i . k_j)      (j <= i)
 // and, with S the state before the chunk (X = K S^T, Y = Q S^T),
-//     R = V - diag(e^c r) X,   U = T' R,   O = diag(scale e^c rq) Y + (P T') R
+//     R = diag(beta) (V - diag(e^c r) X),   U = T R,
+//     O = diag(scale e^c rq) Y + (P T) R,
 //     S <- e^{c_end} S + (diag(e^{c_end - c} r) U)^T K.
-// T', P T' and the decay vectors do not depend on the state: delta_chunk_kernel
+// T, P T and the decay vectors do not depend on the state: delta_chunk_kernel
 // forms them for every chunk at once (scratch).  delta_scan_kernel then walks
 // each prompt's chunks in order; its chain per chunk is three products, X (with
-// Y on top: one product of 128 rows), U (with (P T') R on top) and the state's
-// update, on tcgen05 with accumulators in TMEM.
+// Y on top: one product of 128 rows), U (with (P T) R on top) and the state's
+// update.  The large products of both kernels are tcgen05's, with accumulators
+// in TMEM.
 //
 // Precision: products run in bf16 with fp32 accumulation.  Keys, queries and
-// values are exact; fp32 factors (S, T', R, U) are carried as bf16 hi + lo,
-// 16 significant bits, and the product of two lo parts (2^-18 of the term) is
-// dropped: states and outputs keep about 5 decimal digits, and the outputs are
-// rounded to bf16 once.  (P T' rounded to bf16 would save a quarter of the
+// values are exact; fp32 factors (S, A, T, P T, R, U) are carried as bf16 hi +
+// lo, 16 significant bits, and the product of two lo parts (2^-18 of the term)
+// is dropped: states and outputs keep about 5 decimal digits, and the outputs
+// are rounded to bf16 once.  (P T rounded to bf16 would save a quarter of the
 // scratch traffic, but of a prompt of few tokens all outputs would share its
 // error: up to 2^-8 more.)
 #include <cuda.h>
@@ -33,9 +35,9 @@ namespace rssm {
 namespace {
 
 constexpr int kC = 64;                   // tokens of a chunk
-constexpr int kImgHi = 128 * 128;        // bytes: T' (64 rows), then P T' (64 rows), rows of 64 bf16: the hi parts
+constexpr int kImgHi = 128 * 128;        // bytes: T (64 rows), then P T (64 rows), rows of 64 bf16: the hi parts
 constexpr int kImg = 2 * kImgHi;         // and the lo parts
-constexpr int kVec = 1024;               // bytes: e^c r [64], e^{c_end-c} r [64], scale e^c rq [64], e^{c_end}
+constexpr int kVec = 1040;               // bytes: beta e^c r [64], e^{c_end-c} r [64], scale e^c rq [64], beta [64], e^{c_end}
 constexpr int kUnit = kImg + kVec;       // scratch of one (chunk, value head)
 
 struct DeltaPrefillArgs {
@@ -69,6 +71,18 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
+__device__ __forceinline__ void stsm4_t(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3])
+               : "memory");
+}
+// bulk copy shared -> global (16-byte boundaries and multiples), and the wait for this thread's
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_s2g_wait() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+}
 // 16-byte piece `ch` of row r of a matrix with 128-byte rows, 128-byte swizzle
 __device__ __forceinline__ uint32_t sw128(int r, int ch) { return static_cast<uint32_t>(r * 128 + ((ch ^ (r & 7)) << 4)); }
 
@@ -88,330 +102,6 @@ __device__ __forceinline__ void as_operand(const float (&d)[2][4], uint32_t (&h)
   split_bf16x2(d[0][2], d[0][3], h[1], l[1]);
   split_bf16x2(d[1][0], d[1][1], h[2], l[2]);
   split_bf16x2(d[1][2], d[1][3], h[3], l[3]);
-}
-
-// --------------------------------------------------------------------------
-// delta_chunk_kernel: one block of 4 warps per (chunk, key head); warp w has
-// the chunk's tokens 16 w .. 16 w + 15.
-// --------------------------------------------------------------------------
-struct ChunkSmem {
-  static constexpr int kA = 0;                   // A hi, lo: 2 x 8 KB
-  static constexpr int kImage = kA + 2 * 8192;   // as in scratch
-  static constexpr int kD = kImage + kImg;       // inverses of the diagonal blocks, hi and lo: 2 x 4 x 512
-  static constexpr int kF = kD + 4096;           // diagonal blocks in fp32: 4 x 16 x 17, then the inverses
-  static constexpr int kS = kF + 2 * 4 * 16 * 17 * 4;
-  static constexpr int kScalars = kS;            // c hi, c lo, beta, r, rq: 5 x 64 floats
-  static constexpr int kTokens = (kScalars + 5 * 64 * 4 + 127) / 128 * 128;  // K then Q
-};
-
-template <int DK>
-__global__ void __launch_bounds__(128) delta_chunk_kernel(const DeltaPrefillArgs a) {
-  extern __shared__ __align__(1024) uint8_t sm[];
-  __shared__ int sh[3];
-  constexpr int RB = DK * 2, CH = DK / 8, KS = DK / 16;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int hk = blockIdx.y;
-  const unsigned full = 0xffffffffu;
-  pdl_wait();
-  if (tid == 0) sh[0] = -1;
-  __syncthreads();
-  for (int b = tid; b < a.batch; b += 128) {
-    int start, n;
-    if (!row_bounds(a, b, start, n)) continue;
-    const int i = static_cast<int>(blockIdx.x) - (start / kC + b);
-    if (i >= 0 && i < (n + kC - 1) / kC && a.slot_idx[b] > 0 && a.slot_idx[b] < a.c.S) {
-      sh[0] = b;
-      sh[1] = start + i * kC;
-      sh[2] = min(n - i * kC, kC);
-    }
-  }
-  __syncthreads();
-  if (sh[0] < 0) return;  // an unused slot
-  const long long tok0 = sh[1];
-  const int n = sh[2];
-  uint8_t* sk = sm + ChunkSmem::kTokens;
-  uint8_t* sq = sk + kC * RB;
-  float* s_ch = reinterpret_cast<float*>(sm + ChunkSmem::kScalars);
-  float *s_cl = s_ch + 64, *s_beta = s_cl + 64, *s_r = s_beta + 64, *s_rq = s_r + 64;
-  // tokens past the chunk's end are zeros: they add nothing anywhere
-  for (int i = tid; i < kC * CH; i += 128) {
-    const int r = i / CH, ch = i % CH;
-    const uint32_t to = static_cast<uint32_t>(r * RB + ((ch ^ (r & 7)) << 4));
-    if (r < n) {
-      cp_async16(sk + to, a.tk.k + (tok0 + r) * a.tk.k_stride + hk * DK + ch * 8);
-      cp_async16(sq + to, a.tk.q + (tok0 + r) * a.tk.q_stride + hk * DK + ch * 8);
-    } else {
-      *reinterpret_cast<uint4*>(sk + to) = make_uint4(0u, 0u, 0u, 0u);
-      *reinterpret_cast<uint4*>(sq + to) = make_uint4(0u, 0u, 0u, 0u);
-    }
-  }
-  for (int i = tid; i < kImg / 16; i += 128)  // the upper triangles stay zero
-    reinterpret_cast<uint4*>(sm + ChunkSmem::kImage)[i] = make_uint4(0u, 0u, 0u, 0u);
-  cp_async_wait_all();
-  __syncthreads();
-
-  // k.k and q.k of the warp's 16 rows (n-tiles up to its own), q.q of its diagonal tile
-  const int m = lane >> 2, cc = lane & 3;
-  float kk[8][4], qk[8][4], qq[2][4];
-#pragma unroll
-  for (int t = 0; t < 8; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) kk[t][e] = qk[t][e] = 0.0f;
-#pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) qq[t][e] = 0.0f;
-  const uint32_t ak = smem_addr(sk), aq = smem_addr(sq);
-  const auto tok_addr = [&](uint32_t base, int row, int ch) {
-    return base + static_cast<uint32_t>(row * RB + ((ch ^ (row & 7)) << 4));
-  };
-  const int arow = (lane & 7) + ((lane >> 3) & 1) * 8, ach = lane >> 4;   // first operand, or a transposed second one
-  const int brow = (lane & 7) + ((lane >> 4) << 3), bch = (lane >> 3) & 1;  // second operand, two n-tiles
-#pragma unroll
-  for (int x = 0; x < KS; ++x) {
-    uint32_t fk[4], fq[4], b[4];
-    ldsm4(fk, tok_addr(ak, 16 * warp + arow, 2 * x + ach));
-    ldsm4(fq, tok_addr(aq, 16 * warp + arow, 2 * x + ach));
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      if (t <= warp) {
-        ldsm4(b, tok_addr(ak, 16 * t + brow, 2 * x + bch));
-        mma_bf16(kk[2 * t], fk, b[0], b[1]);
-        mma_bf16(kk[2 * t + 1], fk, b[2], b[3]);
-        mma_bf16(qk[2 * t], fq, b[0], b[1]);
-        mma_bf16(qk[2 * t + 1], fq, b[2], b[3]);
-      }
-    }
-    if (a.tk.l2norm) {
-      ldsm4(b, tok_addr(aq, 16 * warp + brow, 2 * x + bch));
-      mma_bf16(qq[0], fq, b[0], b[1]);
-      mma_bf16(qq[1], fq, b[2], b[3]);
-    }
-  }
-  if (cc == (m >> 1)) {  // the lanes that hold the diagonal
-    float k0 = 0.f, k1 = 0.f;
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      if (t == warp) {
-        k0 = (m & 1) ? kk[2 * t][1] : kk[2 * t][0];
-        k1 = (m & 1) ? kk[2 * t + 1][3] : kk[2 * t + 1][2];
-      }
-    const float q0 = (m & 1) ? qq[0][1] : qq[0][0], q1 = (m & 1) ? qq[1][3] : qq[1][2];
-    const int row = 16 * warp + m;
-    s_r[row] = a.tk.l2norm ? rsqrtf(k0 + 1e-6f) : 1.0f;
-    s_r[row + 8] = a.tk.l2norm ? rsqrtf(k1 + 1e-6f) : 1.0f;
-    s_rq[row] = a.tk.scale * (a.tk.l2norm ? rsqrtf(q0 + 1e-6f) : 1.0f);
-    s_rq[row + 8] = a.tk.scale * (a.tk.l2norm ? rsqrtf(q1 + 1e-6f) : 1.0f);
-  }
-
-  const uint32_t a_hi = smem_addr(sm + ChunkSmem::kA), a_lo = a_hi + 8192;
-  const uint32_t img = smem_addr(sm + ChunkSmem::kImage);
-  float* fd = reinterpret_cast<float*>(sm + ChunkSmem::kF) + warp * 16 * 17;  // the warp's diagonal block
-  float* fi = fd + 4 * 16 * 17;                                              // and its inverse
-  const uint32_t d_hi = smem_addr(sm + ChunkSmem::kD) , d_lo = d_hi + 2048;
-
-#pragma unroll 1
-  for (int rep = 0; rep < a.c.rep; ++rep) {
-    const int h = hk * a.c.rep + rep;
-    uint8_t* unit = a.units + (static_cast<long long>(blockIdx.x) * a.c.Hv + h) * kUnit;
-    if (warp == 0) {
-      // running sums of g in fp64, kept as two floats: differences of them are
-      // exponents, and one float's rounding at a sum of 100 would be 2^-18
-      double c[2];
-      float g[2], be[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int i = 2 * lane + e;
-        g[e] = i < n ? fmaxf(a.tk.g[(tok0 + i) * a.c.Hv + h], kMinLog) : 0.0f;
-        be[e] = i < n ? a.tk.beta[(tok0 + i) * a.c.Hv + h] : 0.0f;
-      }
-      c[0] = g[0];
-      c[1] = static_cast<double>(g[0]) + g[1];
-      double run = c[1];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(full, run, o);
-        if (lane >= o) run += y;
-      }
-      const double before = run - c[1];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const double x = before + c[e];
-        const float hi = static_cast<float>(x);
-        s_ch[2 * lane + e] = hi;
-        s_cl[2 * lane + e] = static_cast<float>(x - hi);
-        s_beta[2 * lane + e] = be[e];
-      }
-    }
-    __syncthreads();
-    if (tid < 64) {
-      float* vec = reinterpret_cast<float*>(unit + kImg);
-      const float ec = expf(s_ch[tid]), ed = expf((s_ch[63] - s_ch[tid]) + (s_cl[63] - s_cl[tid]));
-      vec[tid] = ec * s_r[tid];
-      vec[64 + tid] = ed * s_r[tid];
-      vec[128 + tid] = ec * s_rq[tid];
-      if (tid == 63) vec[192] = ec;
-    }
-    // A and P of the warp's rows
-    uint32_t ph[4][4], pl[4][4];
-    {
-      const int i0 = 16 * warp + m, i1 = i0 + 8;
-      const float ch0 = s_ch[i0], cl0 = s_cl[i0], ch1 = s_ch[i1], cl1 = s_cl[i1];
-      const float br0 = s_beta[i0] * s_r[i0], br1 = s_beta[i1] * s_r[i1], rq0 = s_rq[i0], rq1 = s_rq[i1];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        if (t > warp) break;
-        float p[2][4];
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const int j = 16 * t + 8 * y + 2 * cc;
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int i = e < 2 ? i0 : i1, jj = j + (e & 1);
-            const float dc = (e < 2 ? ch0 : ch1) - s_ch[jj] + ((e < 2 ? cl0 : cl1) - s_cl[jj]);
-            const float w = jj <= i ? __expf(dc) * s_r[jj] : 0.0f;
-            v[e] = jj < i ? (e < 2 ? br0 : br1) * w * kk[2 * t + y][e] : 0.0f;
-            p[y][e] = jj <= i ? (e < 2 ? rq0 : rq1) * w * qk[2 * t + y][e] : 0.0f;
-          }
-          if (t == warp) {  // the diagonal block in fp32
-            fd[m * 17 + 8 * y + 2 * cc] = v[0];
-            fd[m * 17 + 8 * y + 2 * cc + 1] = v[1];
-            fd[(m + 8) * 17 + 8 * y + 2 * cc] = v[2];
-            fd[(m + 8) * 17 + 8 * y + 2 * cc + 1] = v[3];
-          } else {
-            uint32_t h0, l0, h1, l1;
-            split_bf16x2(v[0], v[1], h0, l0);
-            split_bf16x2(v[2], v[3], h1, l1);
-            const uint32_t o0 = sw128(i0, 2 * t + y) + 4 * cc, o1 = sw128(i1, 2 * t + y) + 4 * cc;
-            *reinterpret_cast<uint32_t*>(sm + ChunkSmem::kA + o0) = h0;
-            *reinterpret_cast<uint32_t*>(sm + ChunkSmem::kA + o1) = h1;
-            *reinterpret_cast<uint32_t*>(sm + ChunkSmem::kA + 8192 + o0) = l0;
-            *reinterpret_cast<uint32_t*>(sm + ChunkSmem::kA + 8192 + o1) = l1;
-          }
-        }
-        as_operand(p, ph[t], pl[t]);
-      }
-    }
-    __syncwarp();
-    // inverse of the warp's unit lower triangular diagonal block: a lane per column
-    if (lane < 16) {
-      float x[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float s0 = i == lane ? 1.0f : 0.0f, s1 = 0.0f;
-#pragma unroll
-        for (int j = 0; j < i; ++j) {
-          if (j & 1)
-            s1 = fmaf(-fd[i * 17 + j], x[j], s1);
-          else
-            s0 = fmaf(-fd[i * 17 + j], x[j], s0);
-        }
-        x[i] = s0 + s1;
-        fi[i * 17 + lane] = x[i];
-      }
-    }
-    __syncwarp();
-    // its bf16 parts, rows of 32 bytes, and its transpose as this warp's first operand
-    uint32_t yh[4][4], yl[4][4];
-    {
-      const int r = lane >> 1, c0 = (lane & 1) * 8;
-      uint32_t hw[4], lw[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) split_bf16x2(fi[r * 17 + c0 + 2 * e], fi[r * 17 + c0 + 2 * e + 1], hw[e], lw[e]);
-      const uint32_t to = static_cast<uint32_t>(warp * 512 + r * 32 + c0 * 2);
-      *reinterpret_cast<uint4*>(sm + ChunkSmem::kD + to) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-      *reinterpret_cast<uint4*>(sm + ChunkSmem::kD + 2048 + to) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
-    }
-    float yd[2][4];  // D^T: row = column m of D, column = row of D
-#pragma unroll
-    for (int y = 0; y < 2; ++y)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) yd[y][e] = fi[(8 * y + 2 * cc + (e & 1)) * 17 + m + (e >> 1) * 8];
-    __syncthreads();
-    // column block `warp` of the inverse, transposed: Y_i = -(sum_l Y_l A_il^T) D_i^T, l from the diagonal down
-    const float bt0 = s_beta[16 * warp + m], bt1 = s_beta[16 * warp + m + 8];
-    uint8_t* im = sm + ChunkSmem::kImage;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i < warp) continue;
-      if (i > warp) {
-        float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-        for (int l = 0; l < 3; ++l) {
-          if (l < warp || l >= i) continue;
-          uint32_t bh[4], bl[4];
-          ldsm4(bh, a_hi + sw128(16 * i + brow, 2 * l + bch));
-          ldsm4(bl, a_lo + sw128(16 * i + brow, 2 * l + bch));
-          mma_split(acc, yh[l], yl[l], bh, bl);
-        }
-        uint32_t h[4], l4[4], bh[4], bl[4];
-        as_operand(acc, h, l4);
-        ldsm4(bh, d_hi + i * 512 + brow * 32 + bch * 16);
-        ldsm4(bl, d_lo + i * 512 + brow * 32 + bch * 16);
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) yd[y][e] = 0.0f;
-        mma_split(yd, h, l4, bh, bl);
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) yd[y][e] = -yd[y][e];
-      }
-      as_operand(yd, yh[i], yl[i]);
-      // T'[row][column] = Y[column][row] beta[column]
-#pragma unroll
-      for (int y = 0; y < 2; ++y)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int row = 16 * i + 8 * y + 2 * cc + (e & 1), col = 16 * warp + m + (e >> 1) * 8;
-          const float v = yd[y][e] * (e < 2 ? bt0 : bt1);
-          const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-          const uint32_t to = sw128(row, col >> 3) + (col & 7) * 2;
-          *reinterpret_cast<__nv_bfloat16*>(im + to) = hi;
-          *reinterpret_cast<__nv_bfloat16*>(im + kImgHi + to) = __float2bfloat16_rn(v - __bfloat162float(hi));
-        }
-    }
-    __syncthreads();
-    // P T' of the warp's rows
-    {
-      float o[8][4];
-#pragma unroll
-      for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[t][e] = 0.0f;
-#pragma unroll
-      for (int l = 0; l < 4; ++l) {
-        if (l > warp) break;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          if (t > l) break;
-          uint32_t bh[4], bl[4];
-          ldsm4_t(bh, img + sw128(16 * l + arow, 2 * t + ach));
-          ldsm4_t(bl, img + kImgHi + sw128(16 * l + arow, 2 * t + ach));
-          float(&d)[2][4] = *reinterpret_cast<float(*)[2][4]>(&o[2 * t]);
-          mma_split(d, ph[l], pl[l], bh, bl);
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        if (t > 2 * warp + 1) break;
-        uint32_t h0, l0, h1, l1;
-        split_bf16x2(o[t][0], o[t][1], h0, l0);
-        split_bf16x2(o[t][2], o[t][3], h1, l1);
-        const uint32_t o0 = sw128(64 + 16 * warp + m, t) + 4 * cc, o1 = sw128(64 + 16 * warp + m + 8, t) + 4 * cc;
-        *reinterpret_cast<uint32_t*>(im + o0) = h0;
-        *reinterpret_cast<uint32_t*>(im + o1) = h1;
-        *reinterpret_cast<uint32_t*>(im + kImgHi + o0) = l0;
-        *reinterpret_cast<uint32_t*>(im + kImgHi + o1) = l1;
-      }
-    }
-    __syncthreads();
-    for (int i = tid; i < kImg / 16; i += 128) reinterpret_cast<uint4*>(unit)[i] = reinterpret_cast<const uint4*>(im)[i];
-    __syncthreads();
-  }
-  pdl_trigger();
 }
 
 // --------------------------------------------------------------------------
@@ -441,17 +131,24 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
 }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_ld8(float* v, uint32_t addr) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+// 8 columns of the warp's lanes: the registers hold them only after
+// tc_wait_ld and are not to be touched before (tc_landed)
+__device__ __forceinline__ void tc_ld8(uint32_t (&r)[8], uint32_t addr) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ void tc_st8(uint32_t addr, const float* v) {
-  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+// after tc_wait_ld: uses of r stay behind it
+__device__ __forceinline__ void tc_landed(uint32_t (&r)[8]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]));
+}
+__device__ __forceinline__ void tc_st8(uint32_t addr, const pair* v) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpack2(v[i], f[2 * i], f[2 * i + 1]);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "f"(f[0]), "f"(f[1]),
+               "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
                : "memory");
 }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -463,6 +160,365 @@ __device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x,
           smem_addr(dst)),
       "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
       : "memory");
+}
+
+// --------------------------------------------------------------------------
+// delta_chunk_kernel: one block of 4 warps per (chunk, value head).
+//
+// The Gram products of the keys and of the queries with the keys are one
+// product of 128 rows; a thread then has a row of A (threads 0-63) or of P.
+// The inverse goes by blocks of 16: the diagonal ones by substitution, then
+// joined twice, [T1 0; -T2 A21 T1  T2].  The block chain is a string of small
+// dependent steps, so what matters is how many blocks an SM holds: three, for
+// which T and P T take the place of the keys and queries in shared memory.
+// --------------------------------------------------------------------------
+struct ChunkSmem {
+  static constexpr int kImage = 0;              // K and Q per 64 columns as in the scan, then T and P T as in scratch
+  static constexpr int kHi = kImg;              // A (64 rows), P (64 rows): the hi parts
+  static constexpr int kLo = kHi + kImgHi;      // and the lo parts
+  static constexpr int kDiag = kLo + kImgHi;    // diagonal blocks of A in fp32, then their inverses: 4 x 16 x 20
+  static constexpr int kScalars = kDiag + 4 * 16 * 20 * 4;  // c hi, c lo, beta, r, rq, column factors: 6 x 64 floats
+  static constexpr int kBars = kScalars + 6 * 64 * 4;
+  static constexpr int kBytes = kBars + 64 + 1024;
+};
+
+template <int DK>
+__global__ void __launch_bounds__(128, 3)
+    delta_chunk_kernel(const DeltaPrefillArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk) {
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+  __shared__ int sh[3];
+  __shared__ uint32_t tmem_base;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.y, hk = h / a.c.rep;
+  const unsigned full = 0xffffffffu;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + ChunkSmem::kBars);  // copies, Gram products, P T
+  if (tid == 0) {
+    sh[0] = -1;
+    mbar_init(bars, 1);
+    mbar_init(bars + 1, 1);
+    mbar_init(bars + 2, 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  for (int b = tid; b < a.batch; b += 128) {
+    int start, n;
+    if (!row_bounds(a, b, start, n)) continue;
+    const int i = static_cast<int>(blockIdx.x) - (start / kC + b);
+    if (i >= 0 && i < (n + kC - 1) / kC && a.slot_idx[b] > 0 && a.slot_idx[b] < a.c.S) {
+      sh[0] = b;
+      sh[1] = start + i * kC;
+      sh[2] = min(n - i * kC, kC);
+    }
+  }
+  __syncthreads();
+  if (sh[0] < 0) return;  // an unused slot
+  const int tok0 = sh[1], n = sh[2];
+  float* s_ch = reinterpret_cast<float*>(sm + ChunkSmem::kScalars);
+  float *s_cl = s_ch + 64, *s_beta = s_cl + 64, *s_r = s_beta + 64, *s_rq = s_r + 64, *s_col = s_rq + 64;
+  uint8_t* im = sm + ChunkSmem::kImage;
+  const uint32_t base = smem_addr(sm);
+  if (tid == 0) {
+    mbar_arrive_expect_tx(bars, DK * 2 * 128);
+#pragma unroll
+    for (int x = 0; x < DK / 64; ++x) {
+      tma_2d(im + x * 16384, &mk, hk * DK + 64 * x, tok0, bars);
+      tma_2d(im + x * 16384 + 8192, &mq, hk * DK + 64 * x, tok0, bars);
+    }
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)), "n"(128) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else if (warp == 2) {
+    // running sums of g in fp64, kept as two floats: differences of them are
+    // exponents, and one float's rounding at a sum of 100 would be 2^-18
+    double c[2];
+    float g[2], be[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = 2 * lane + e;
+      g[e] = i < n ? fmaxf(a.tk.g[static_cast<long long>(tok0 + i) * a.c.Hv + h], kMinLog) : 0.0f;
+      be[e] = i < n ? a.tk.beta[static_cast<long long>(tok0 + i) * a.c.Hv + h] : 0.0f;
+    }
+    c[0] = g[0];
+    c[1] = static_cast<double>(g[0]) + g[1];
+    double run = c[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double y = __shfl_up_sync(full, run, o);
+      if (lane >= o) run += y;
+    }
+    const double before = run - c[1];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const double x = before + c[e];
+      const float hi = static_cast<float>(x);
+      s_ch[2 * lane + e] = hi;
+      s_cl[2 * lane + e] = static_cast<float>(x - hi);
+      s_beta[2 * lane + e] = be[e];
+    }
+  }
+  bool ok = mbar_wait(bars, 0);
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tm = tmem_base;
+  constexpr uint32_t i_gram = instruction(64, false, false), i_pt = instruction(64, false, true);
+  if (tid == 0 && ok) {
+    const uint64_t d = operand(base + ChunkSmem::kImage, 16, 1024, kSw128);
+#pragma unroll
+    for (int x = 0; x < DK / 16; ++x) {
+      const uint64_t k = d + (((x >> 2) * 16384 + (x & 3) * 32) >> 4);
+      tc_mma(tm, k, k, i_gram, x > 0);
+    }
+    tc_commit(bars + 1);
+  }
+  // meanwhile the norm of the thread's key (query)
+  const int i = tid & 63;
+  const bool is_key = tid < 64, live = i < n;
+  {
+    float ss = 0.0f, s1 = 0.0f;
+    if (a.tk.l2norm) {
+#pragma unroll
+      for (int x = 0; x < DK / 64; ++x)
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) {
+          const uint4 w = *reinterpret_cast<const uint4*>(im + x * 16384 + sw128(tid, ch));
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            ss = fmaf(bf16lo(u[e]), bf16lo(u[e]), ss);
+            s1 = fmaf(bf16hi(u[e]), bf16hi(u[e]), s1);
+          }
+        }
+    }
+    float r = a.tk.l2norm ? rsqrtf(ss + s1 + 1e-6f) : 1.0f;
+    if (!live) r = 0.0f;  // whatever is past the chunk's end must not count
+    if (is_key) {
+      s_r[i] = r;
+      // decays go through the end of the column's block: both factors are at most 1
+      const int end = i | 15;
+      s_col[i] = live ? __expf((s_ch[end] - s_ch[i]) + (s_cl[end] - s_cl[i])) * r : 0.0f;
+    } else {
+      s_rq[i] = a.tk.scale * r;
+    }
+  }
+  __syncthreads();
+  uint8_t* unit = a.units + (static_cast<long long>(blockIdx.x) * a.c.Hv + h) * kUnit;
+  const float ch = s_ch[i], cl = s_cl[i];
+  if (is_key) {
+    float* vec = reinterpret_cast<float*>(unit + kImg);
+    const float ec = __expf(ch);
+    vec[i] = s_beta[i] * ec * s_r[i];
+    vec[64 + i] = __expf((s_ch[63] - ch) + (s_cl[63] - cl)) * s_r[i];
+    vec[128 + i] = ec * s_rq[i];
+    vec[192 + i] = s_beta[i];
+    if (i == 63) vec[256] = ec;
+  }
+  ok = ok && mbar_wait(bars + 1, 0);
+  tc_after();
+  // the thread's row of A (P), in blocks of 16 columns
+  {
+    const float rf = live ? (is_key ? s_beta[i] * s_r[i] : s_rq[i]) : 0.0f;
+    float* fd = reinterpret_cast<float*>(sm + ChunkSmem::kDiag) + i * 20;
+    const uint32_t lanes = tm + (static_cast<uint32_t>(32 * warp) << 16);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      pair v[8];
+      if (b <= ((32 * warp + 31) & 63) / 16) {  // some row of the warp reaches the block
+        uint32_t x[2][8];
+        tc_ld8(x[0], lanes + 16 * b);
+        tc_ld8(x[1], lanes + 16 * b + 8);
+        tc_wait_ld();
+        tc_landed(x[0]);
+        tc_landed(x[1]);
+        if (16 * b + 16 <= i) {
+          const float f = __expf((ch - s_ch[16 * b + 15]) + (cl - s_cl[16 * b + 15])) * rf;
+          const pair f2 = pack2(f, f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[e] = *reinterpret_cast<const pair*>(s_col + 16 * b + 2 * e);
+            mul2(v[e], f2);
+            mul2(v[e], pack2(__uint_as_float(x[e >> 2][2 * (e & 3)]), __uint_as_float(x[e >> 2][2 * (e & 3) + 1])));
+          }
+        } else {
+          // the row's diagonal block (or one past it: nothing)
+          float y[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int j = 16 * b + e;
+            const float w = __expf((ch - s_ch[j]) + (cl - s_cl[j])) * (rf * s_r[j]);
+            y[e] = live && (is_key ? j < i : j <= i) ? w * __uint_as_float(x[e >> 3][e & 7]) : 0.0f;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = pack2(y[2 * e], y[2 * e + 1]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0ull;
+      }
+      if (!live) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 0ull;
+      }
+      if (is_key && b == (i >> 4)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<ulonglong2*>(fd + 4 * e) = make_ulonglong2(v[2 * e], v[2 * e + 1]);
+      }
+      uint32_t hw[8], lw[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) split_bf16x2(v[e], hw[e], lw[e]);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t to = sw128(tid, 2 * b + e);
+        *reinterpret_cast<uint4*>(sm + ChunkSmem::kHi + to) = make_uint4(hw[4 * e], hw[4 * e + 1], hw[4 * e + 2], hw[4 * e + 3]);
+        *reinterpret_cast<uint4*>(sm + ChunkSmem::kLo + to) = make_uint4(lw[4 * e], lw[4 * e + 1], lw[4 * e + 2], lw[4 * e + 3]);
+      }
+    }
+  }
+  // the Gram products are done with the keys and queries: T takes their place, zero above its diagonal
+  for (int x = tid; x < 64 * 8; x += 128) {
+    *reinterpret_cast<uint4*>(im + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+    *reinterpret_cast<uint4*>(im + kImgHi + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __syncthreads();
+  {
+    // inverse of the warp's unit lower triangular diagonal block: a lane per column
+    float* fd = reinterpret_cast<float*>(sm + ChunkSmem::kDiag) + warp * 16 * 20;
+    float x[16];
+    if (lane < 16) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        float s0 = r == lane ? 1.0f : 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int j = 0; j < r; j += 4) {
+          const float4 w = *reinterpret_cast<const float4*>(fd + r * 20 + j);
+          s0 = fmaf(-w.x, x[j], s0);
+          if (j + 1 < r) s1 = fmaf(-w.y, x[j + 1], s1);
+          if (j + 2 < r) s0 = fmaf(-w.z, x[j + 2], s0);
+          if (j + 3 < r) s1 = fmaf(-w.w, x[j + 3], s1);
+        }
+        x[r] = s0 + s1;
+      }
+    }
+    __syncwarp();
+    if (lane < 16) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) fd[r * 20 + lane] = x[r];
+    }
+    __syncwarp();
+    const int r = lane >> 1, c0 = (lane & 1) * 8;
+    uint32_t hw[4], lw[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split_bf16x2(fd[r * 20 + c0 + 2 * e], fd[r * 20 + c0 + 2 * e + 1], hw[e], lw[e]);
+    const uint32_t to = sw128(16 * warp + r, 2 * warp + (lane & 1));
+    *reinterpret_cast<uint4*>(im + to) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+    *reinterpret_cast<uint4*>(im + kImgHi + to) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+  }
+  // block (br, bc) of a 64 x 64 matrix as a second operand (its transpose: rows of it are columns), or, with .trans,
+  // its transpose as a first operand; the same addresses store a transposed accumulator
+  const auto block = [&](uint32_t m, int br, int bc) {
+    return m + sw128(16 * br + (lane & 7) + ((lane >> 4) << 3), 2 * bc + ((lane >> 3) & 1));
+  };
+  const uint32_t t_hi = base + ChunkSmem::kImage, t_lo = t_hi + kImgHi, a_hi = base + ChunkSmem::kHi, a_lo = base + ChunkSmem::kLo;
+  // d += (T_lc)^T (A_il)^T for one l
+  const auto first = [&](float (&d)[2][4], int l, int c, int r) {
+    uint32_t th[4], tl[4], bh[4], bl[4];
+    ldsm4_t(th, block(t_hi, l, c));
+    ldsm4_t(tl, block(t_lo, l, c));
+    ldsm4(bh, block(a_hi, r, l));
+    ldsm4(bl, block(a_lo, r, l));
+    mma_split(d, th, tl, bh, bl);
+  };
+  // d -= y (T_rl)^T
+  const auto second = [&](float (&d)[2][4], const uint32_t (&yh)[4], const uint32_t (&yl)[4], int r, int l) {
+    uint32_t bh[4], bl[4];
+    ldsm4(bh, block(t_hi, r, l));
+    ldsm4(bl, block(t_lo, r, l));
+    mma_split(d, yh, yl, bh, bl);
+  };
+  const auto save = [&](float (&d)[2][4], int r, int c) {
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[y][e] = -d[y][e];
+    uint32_t h4[4], l4[4];
+    as_operand(d, h4, l4);
+    stsm4_t(block(t_hi, r, c), h4);
+    stsm4_t(block(t_lo, r, c), l4);
+  };
+  __syncthreads();
+  if (warp < 2) {  // blocks (1, 0) and (3, 2)
+    const int c = 2 * warp;
+    float y[2][4] = {}, z[2][4] = {};
+    uint32_t yh[4], yl[4];
+    first(y, c, c, c + 1);
+    as_operand(y, yh, yl);
+    second(z, yh, yl, c + 1, c + 1);
+    save(z, c + 1, c);
+  }
+  __syncthreads();
+  if (warp < 2) {  // blocks (2, c) and (3, c): the lower left 32 x 32, a column of blocks each
+    const int c = warp;
+    uint32_t yh[2][4], yl[2][4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float y[2][4] = {};
+      if (c == 0) first(y, 0, c, 2 + r);
+      first(y, 1, c, 2 + r);
+      as_operand(y, yh[r], yl[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float z[2][4] = {};
+      second(z, yh[0], yl[0], 2 + r, 2);
+      if (r == 1) second(z, yh[1], yl[1], 3, 3);
+      save(z, 2 + r, c);
+    }
+  }
+  fence_async();
+  tc_before();
+  __syncthreads();
+  tc_after();
+  // P T: P is rows 64-127 of its operand, so that the result is in the lanes of the threads that store it
+  if (tid == 0 && ok) {
+    const uint64_t ph = operand(a_hi, 16, 1024, kSw128), pl = operand(a_lo, 16, 1024, kSw128);
+    const uint64_t bh = operand(t_hi, 16, 1024, kSw128), bl = operand(t_lo, 16, 1024, kSw128);
+#pragma unroll
+    for (int part = 0; part < 3; ++part)
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        tc_mma(tm + 64, (part == 1 ? pl : ph) + ((x * 32) >> 4), (part == 2 ? bl : bh) + ((x * 2048) >> 4), i_pt, part || x);
+    tc_commit(bars + 2);
+  }
+  ok = ok && mbar_wait(bars + 2, 0);
+  tc_after();
+  if (warp >= 2) {
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      uint32_t x[8], hw[4], lw[4];
+      tc_ld8(x, tm + 64 + (static_cast<uint32_t>(32 * warp) << 16) + 8 * b);
+      tc_wait_ld();
+      tc_landed(x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) split_bf16x2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]), hw[e], lw[e]);
+      const uint32_t to = sw128(tid, b);
+      *reinterpret_cast<uint4*>(im + to) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+      *reinterpret_cast<uint4*>(im + kImgHi + to) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+    }
+  }
+  fence_async();
+  tc_before();
+  const bool all_ok = __syncthreads_and(ok) != 0;
+  tc_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(128) : "memory");
+  if (tid == 0) {
+    if (!all_ok) set_error(a.c.err, RSSM_ERRBIT_TIMEOUT);
+    bulk_s2g(unit, im, kImg);
+    bulk_s2g_wait();
+  }
+  pdl_trigger();
 }
 
 // --------------------------------------------------------------------------
@@ -482,7 +538,7 @@ struct ScanSmem {
   static constexpr int kLo = kHi + kImgHi;
   static constexpr int kV = kLo + kImgHi;
   static constexpr int kVecs = kV + kC * NDV * 2;
-  static constexpr int kStage = kVecs + kVec;
+  static constexpr int kStage = kVecs + 2048;  // the next one starts on 1024 bytes too
   // operands: rows of 128 bytes, for 32 columns hi and lo in one row, for 64 in one block each
   static constexpr int kBlocks = NDV / 32;
   static constexpr int kS = kStages * kStage;
@@ -638,24 +694,32 @@ __global__ void __launch_bounds__(kWorkWarps * 32 + 64, 1)
     const uint32_t at = (static_cast<uint32_t>(32 * q) << 16) + c0;  // this warp's lanes and columns of an accumulator
     const bool is_tok = q < 2, has_s = row < DK;
     const int t = row & 63;
-    // v (two sums of parts) from an accumulator's two halves
-    const auto get = [&](float* v, uint32_t from) {
-      float y[CN];
+    // CN values as pairs, an accumulator's two halves added
+    const auto get = [&](pair* v, uint32_t from) {
+      uint32_t x[CN / 8][8], y[CN / 8][8];
 #pragma unroll
-      for (int i = 0; i < CN; i += 8) {
-        tc_ld8(v + i, from + at + i);
-        tc_ld8(y + i, from + at + NDV + i);
+      for (int i = 0; i < CN / 8; ++i) {
+        tc_ld8(x[i], from + at + 8 * i);
+        tc_ld8(y[i], from + at + NDV + 8 * i);
       }
       tc_wait_ld();
 #pragma unroll
-      for (int i = 0; i < CN; ++i) v[i] += y[i];
+      for (int i = 0; i < CN / 8; ++i) {
+        tc_landed(x[i]);
+        tc_landed(y[i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[4 * i + e] = pack2(__uint_as_float(x[i][2 * e]), __uint_as_float(x[i][2 * e + 1]));
+          add2(v[4 * i + e], pack2(__uint_as_float(y[i][2 * e]), __uint_as_float(y[i][2 * e + 1])));
+        }
+      }
     };
-    const auto put = [&](int to, int rows, int r, const float* v) {  // as an operand of `rows` rows
+    const auto put = [&](int to, int rows, int r, const pair* v) {  // as an operand of `rows` rows
 #pragma unroll
       for (int i = 0; i < CN; i += 8) {
         uint32_t hw[4], lw[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split_bf16x2(v[i + 2 * e], v[i + 2 * e + 1], hw[e], lw[e]);
+        for (int e = 0; e < 4; ++e) split_bf16x2(v[i / 2 + e], hw[e], lw[e]);
         const int ch = (c0 + i) >> 3;
         uint8_t* p = sm + to;
         *reinterpret_cast<uint4*>(p + sw128(r, ch)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
@@ -669,15 +733,23 @@ __global__ void __launch_bounds__(kWorkWarps * 32 + 64, 1)
     };
     const long long head = s * a.c.state_stride + (static_cast<long long>(h) * dv + dv0 + c0) * DK + row;
     const int cols = min(CN, dv - dv0 - c0);  // of this warp's columns those that exist (may be negative)
-    float v[CN];
+    pair v[CN / 2];
     const bool go_on = a.initial && a.initial[b] != 0;
+    const auto state_in = [&](int i) {
+      if (!go_on || !has_s || i >= cols) return 0.0f;
+      const long long x = head + static_cast<long long>(i) * DK;
+      return a.c.dtype == RSSM_F32 ? static_cast<const float*>(a.c.state)[x] : bf16f(static_cast<const uint16_t*>(a.c.state)[x]);
+    };
+    const auto state_out = [&](int i, float y) {
+      if (i >= cols) return;
+      const long long x = head + static_cast<long long>(i) * DK;
+      if (a.c.dtype == RSSM_F32)
+        static_cast<float*>(a.c.state)[x] = y;
+      else
+        static_cast<__nv_bfloat16*>(a.c.state)[x] = __float2bfloat16_rn(y);
+    };
 #pragma unroll
-    for (int i = 0; i < CN; ++i) {
-      v[i] = 0.0f;
-      if (go_on && has_s && i < cols)
-        v[i] = a.c.dtype == RSSM_F32 ? static_cast<const float*>(a.c.state)[head + static_cast<long long>(i) * DK]
-                                     : bf16f(static_cast<const uint16_t*>(a.c.state)[head + static_cast<long long>(i) * DK]);
-    }
+    for (int i = 0; i < CN / 2; ++i) v[i] = pack2(state_in(2 * i), state_in(2 * i + 1));
     bool ok = true;
     for (int c = 0; c < chunks; ++c) {
       const int st = c % L::kStages;
@@ -687,12 +759,13 @@ __global__ void __launch_bounds__(kWorkWarps * 32 + 64, 1)
       ok = wait_warp(b_full + st, (c / L::kStages) & 1);
       ok = ok && (c == 0 || wait_warp(b_new, (c - 1) & 1));
       if (!ok) break;
-      if (live < kC) {  // keys past the prompt's end may be another prompt's: whatever they are, they must not count
+      if (live < kC) {  // rows past the prompt's end may be another prompt's: whatever they are, they must not count
         for (int i = tid; i < (kC - live) * L::kHalves * 8; i += kWorkWarps * 32) {
           const int r = live + i / (L::kHalves * 8), x = i % (L::kHalves * 8);
           *reinterpret_cast<uint4*>(p + L::kKQ + (x >> 3) * 16384 + r * 128 + (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
       }
+      const bool past = t >= live;
       if (has_s) {
         if (c > 0) {
           tc_after();
@@ -703,32 +776,29 @@ __global__ void __launch_bounds__(kWorkWarps * 32 + 64, 1)
       fence_async();
       arrive(b_s);
       // while X is formed: the decayed S in place, and what this thread needs of the decay vectors
-      const float w0 = vec[is_tok ? t : 128 + t], w1 = vec[64 + t], ec = vec[192];
+      const float w0 = vec[is_tok ? t : 128 + t], w1 = vec[64 + t], be = vec[192 + t], ec = vec[256];
       if (has_s) {
-        float zero[CN];
+        const pair e2 = pack2(ec, ec);
+        const pair zero[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-        for (int i = 0; i < CN; ++i) {
-          v[i] *= ec;
-          zero[i] = 0.0f;
-        }
+        for (int i = 0; i < CN / 2; ++i) mul2(v[i], e2);
 #pragma unroll
         for (int i = 0; i < CN; i += 8) {
-          tc_st8(tm_s + at + i, v + i);
-          tc_st8(tm_s + at + NDV + i, zero + i);
+          tc_st8(tm_s + at + i, v + i / 2);
+          tc_st8(tm_s + at + NDV + i, zero);
         }
         tc_wait_st();
       }
-      uint32_t xw[CN / 2];
+      pair val[CN / 2];
       if (is_tok) {
 #pragma unroll
         for (int i = 0; i < CN; i += 8) {
           const int ch = (c0 + i) >> 3;
           const uint4 x = *reinterpret_cast<const uint4*>(
               p + L::kV + (NDV == 32 ? t * 64 + ((ch ^ ((t >> 1) & 3)) << 4) : static_cast<int>(sw128(t, ch))));
-          xw[i / 2] = x.x;
-          xw[i / 2 + 1] = x.y;
-          xw[i / 2 + 2] = x.z;
-          xw[i / 2 + 3] = x.w;
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) val[i / 2 + e] = past ? 0ull : pack2(bf16lo(xw[e]), bf16hi(xw[e]));
         }
       } else {
         arrive(b_up);
@@ -737,36 +807,37 @@ __global__ void __launch_bounds__(kWorkWarps * 32 + 64, 1)
       tc_after();
       get(v, tm_x);
       if (is_tok) {
+        const pair m = pack2(-w0, -w0), m1 = pack2(be, be);
 #pragma unroll
-        for (int i = 0; i < CN; i += 2) {
-          v[i] = t < live ? fmaf(-w0, v[i], bf16lo(xw[i / 2])) : 0.0f;
-          v[i + 1] = t < live ? fmaf(-w0, v[i + 1], bf16hi(xw[i / 2])) : 0.0f;
+        for (int i = 0; i < CN / 2; ++i) {
+          mul2(val[i], m1);
+          fma2(val[i], m, v[i]);  // past the end X is zero: its key was
         }
-        put(L::kR, kC, t, v);
+        put(L::kR, kC, t, val);
         fence_async();
         arrive(b_r);
       }
       if (!(ok = wait_warp(b_u, c & 1))) break;
       tc_after();
-      float u[CN];
+      pair u[CN / 2];
       get(u, tm_u);
       if (is_tok) {
+        const pair m = pack2(w1, w1);
 #pragma unroll
-        for (int i = 0; i < CN; ++i) u[i] *= w1;
+        for (int i = 0; i < CN / 2; ++i) mul2(u[i], m);
         put(L::kR, kC, t, u);
         fence_async();
         arrive(b_up);
       } else if (t < live) {
+        const pair m = pack2(w0, w0);
+#pragma unroll
+        for (int i = 0; i < CN / 2; ++i) fma2(u[i], m, v[i]);
         uint16_t* o = a.tk.out + (start + c * kC + t) * ostride + h * dv + dv0 + c0;
 #pragma unroll
         for (int i = 0; i < CN; i += 8) {
-          if (i < cols) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = cvt_bf16x2(fmaf(w0, v[i + 2 * e], u[i + 2 * e]), fmaf(w0, v[i + 2 * e + 1], u[i + 2 * e + 1]));
-            *reinterpret_cast<uint4*>(o + i) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          if (i < cols)
+            *reinterpret_cast<uint4*>(o + i) =
+                make_uint4(cvt_bf16x2(u[i / 2]), cvt_bf16x2(u[i / 2 + 1]), cvt_bf16x2(u[i / 2 + 2]), cvt_bf16x2(u[i / 2 + 3]));
         }
       }
     }
@@ -779,12 +850,11 @@ __global__ void __launch_bounds__(kWorkWarps * 32 + 64, 1)
     }
     if (ok && has_s) {
 #pragma unroll
-      for (int i = 0; i < CN; ++i) {
-        if (i >= cols) break;
-        if (a.c.dtype == RSSM_F32)
-          static_cast<float*>(a.c.state)[head + static_cast<long long>(i) * DK] = v[i];
-        else
-          static_cast<__nv_bfloat16*>(a.c.state)[head + static_cast<long long>(i) * DK] = __float2bfloat16_rn(v[i]);
+      for (int i = 0; i < CN / 2; ++i) {
+        float lo, hi;
+        unpack2(v[i], lo, hi);
+        state_out(2 * i, lo);
+        state_out(2 * i + 1, hi);
       }
     }
   }
@@ -833,10 +903,14 @@ cudaError_t grow_smem(K kernel, size_t bytes) {
 
 template <int DK>
 cudaError_t launch_chunks(const DeltaPrefillArgs& a, cudaStream_t st) {
-  constexpr size_t smem = ChunkSmem::kTokens + 2 * kC * DK * 2;
-  const cudaError_t e = grow_smem(delta_chunk_kernel<DK>, smem);
+  CUtensorMap mq, mk;
+  if (a.tokens == 0) return cudaSuccess;
+  if (!token_map(&mq, a.tk.q, a.c.Hk * DK, a.tokens, a.tk.q_stride, 64) || !token_map(&mk, a.tk.k, a.c.Hk * DK, a.tokens, a.tk.k_stride, 64))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = grow_smem(delta_chunk_kernel<DK>, ChunkSmem::kBytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(delta_chunk_kernel<DK>, dim3(static_cast<unsigned>(a.tokens / kC + a.batch), a.c.Hk), dim3(128), smem, st, a);
+  return launch_pdl(delta_chunk_kernel<DK>, dim3(static_cast<unsigned>(a.tokens / kC + a.batch), a.c.Hv), dim3(128), ChunkSmem::kBytes, st,
+                    a, mq, mk);
 }
 
 template <int DK, int NDV>
@@ -884,7 +958,7 @@ extern "C" rssm_status rssm_delta_prefill(const rssm_delta_cache* cache, const v
     if (st != RSSM_OK) return st;
   }
   if (scratch_bytes < rssm_delta_scratch_bytes(cache, batch, tokens)) return RSSM_ERR_SCRATCH_TOO_SMALL;
-  if (static_cast<long long>(batch) * a.c.Hv * ((a.c.dv + 31) / 32) > 0x7fffffffll || a.c.Hk > 65535) return RSSM_ERR_UNSUPPORTED;
+  if (static_cast<long long>(batch) * a.c.Hv * ((a.c.dv + 31) / 32) > 0x7fffffffll || a.c.Hv > 65535) return RSSM_ERR_UNSUPPORTED;
   a.slot_idx = slot_idx;
   a.cu = cu_seqlens;
   a.initial = initial;
