@@ -36,6 +36,9 @@ constexpr int kTokenRow = DK * 2 + 64;
 constexpr float kMinLog = -100.0f;  // log decays are held at this and above: e^-100 is zero to fp32 sums of O(1) values,
                                     // and a finite floor keeps differences of running sums defined (g = -inf resets a state)
 
+constexpr float kMaxLog = 1000.0f;         // and at this and below (e^89 is infinite)
+constexpr float kFix = 1099511627776.0f;   // 2^40: one of running sums in fixed point
+
 struct DeltaCacheView {
   int S, Hk, Hv, rep, dv, np;
   int dtype, wide;  // wide: state rows start on 32 bytes

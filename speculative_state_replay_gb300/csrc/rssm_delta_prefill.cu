@@ -76,12 +76,12 @@ __device__ __forceinline__ void stsm4_t(uint32_t addr, const uint32_t (&r)[4]) {
                "r"(r[3])
                : "memory");
 }
-// bulk copy shared -> global (16-byte boundaries and multiples), and the wait for this thread's
+// bulk copy shared -> global (16-byte boundaries and multiples), and the wait until this thread's have left shared memory
 __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_addr(src)), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void bulk_s2g_wait() {
-  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 // 16-byte piece `ch` of row r of a matrix with 128-byte rows, 128-byte swizzle
 __device__ __forceinline__ uint32_t sw128(int r, int ch) { return static_cast<uint32_t>(r * 128 + ((ch ^ (r & 7)) << 4)); }
@@ -202,6 +202,10 @@ __global__ void __launch_bounds__(128, 3)
   }
   __syncthreads();
   pdl_wait();
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)), "n"(128) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
   for (int b = tid; b < a.batch; b += 128) {
     int start, n;
     if (!row_bounds(a, b, start, n)) continue;
@@ -212,8 +216,17 @@ __global__ void __launch_bounds__(128, 3)
       sh[2] = min(n - i * kC, kC);
     }
   }
+  tc_before();
   __syncthreads();
-  if (sh[0] < 0) return;  // an unused slot
+  tc_after();
+  const uint32_t tm = tmem_base;
+  const auto release = [&]() {
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(128) : "memory");
+  };
+  if (sh[0] < 0) {  // an unused slot
+    release();
+    return;
+  }
   const int tok0 = sh[1], n = sh[2];
   float* s_ch = reinterpret_cast<float*>(sm + ChunkSmem::kScalars);
   float *s_cl = s_ch + 64, *s_beta = s_cl + 64, *s_r = s_beta + 64, *s_rq = s_r + 64, *s_col = s_rq + 64;
@@ -227,45 +240,39 @@ __global__ void __launch_bounds__(128, 3)
       tma_2d(im + x * 16384 + 8192, &mq, hk * DK + 64 * x, tok0, bars);
     }
   }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)), "n"(128) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  } else if (warp == 2) {
-    // running sums of g in fp64, kept as two floats: differences of them are
-    // exponents, and one float's rounding at a sum of 100 would be 2^-18
-    double c[2];
-    float g[2], be[2];
+  constexpr uint32_t i_gram = instruction(64, false, false), i_pt = instruction(64, false, true);
+  if (warp == 2) {
+    // Running sums of g in fixed point, 40 fraction bits, and as two floats:
+    // differences of them are exponents, and one float's rounding at a sum of
+    // 100 would be 2^-18.  (fp64 takes several times as long here.)
+    long long c[2];
+    float be[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int i = 2 * lane + e;
-      g[e] = i < n ? fmaxf(a.tk.g[static_cast<long long>(tok0 + i) * a.c.Hv + h], kMinLog) : 0.0f;
-      be[e] = i < n ? a.tk.beta[static_cast<long long>(tok0 + i) * a.c.Hv + h] : 0.0f;
+      const long long at = static_cast<long long>(tok0 + i) * a.c.Hv + h;
+      c[e] = i < n ? __float2ll_rn(fminf(fmaxf(a.tk.g[at], kMinLog), kMaxLog) * kFix) : 0ll;
+      be[e] = i < n ? a.tk.beta[at] : 0.0f;
     }
-    c[0] = g[0];
-    c[1] = static_cast<double>(g[0]) + g[1];
-    double run = c[1];
+    c[1] += c[0];
+    long long run = c[1];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(full, run, o);
+      const long long y = __shfl_up_sync(full, run, o);
       if (lane >= o) run += y;
     }
-    const double before = run - c[1];
+    const long long before = run - c[1];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const double x = before + c[e];
-      const float hi = static_cast<float>(x);
-      s_ch[2 * lane + e] = hi;
-      s_cl[2 * lane + e] = static_cast<float>(x - hi);
+      const long long x = before + c[e];
+      const float hi = __ll2float_rn(x);
+      s_ch[2 * lane + e] = hi * (1.0f / kFix);
+      s_cl[2 * lane + e] = __ll2float_rn(x - __float2ll_rn(hi)) * (1.0f / kFix);
       s_beta[2 * lane + e] = be[e];
     }
   }
   bool ok = mbar_wait(bars, 0);
-  tc_before();
-  __syncthreads();
-  tc_after();
-  const uint32_t tm = tmem_base;
-  constexpr uint32_t i_gram = instruction(64, false, false), i_pt = instruction(64, false, true);
-  if (tid == 0 && ok) {
+  if (tid == 32 && ok) {
     const uint64_t d = operand(base + ChunkSmem::kImage, 16, 1024, kSw128);
 #pragma unroll
     for (int x = 0; x < DK / 16; ++x) {
@@ -274,6 +281,7 @@ __global__ void __launch_bounds__(128, 3)
     }
     tc_commit(bars + 1);
   }
+  __syncwarp();
   // meanwhile the norm of the thread's key (query)
   const int i = tid & 63;
   const bool is_key = tid < 64, live = i < n;
@@ -295,19 +303,15 @@ __global__ void __launch_bounds__(128, 3)
     }
     float r = a.tk.l2norm ? rsqrtf(ss + s1 + 1e-6f) : 1.0f;
     if (!live) r = 0.0f;  // whatever is past the chunk's end must not count
-    if (is_key) {
-      s_r[i] = r;
-      // decays go through the end of the column's block: both factors are at most 1
-      const int end = i | 15;
-      s_col[i] = live ? __expf((s_ch[end] - s_ch[i]) + (s_cl[end] - s_cl[i])) * r : 0.0f;
-    } else {
-      s_rq[i] = a.tk.scale * r;
-    }
+    (is_key ? s_r : s_rq)[i] = is_key ? r : a.tk.scale * r;
   }
   __syncthreads();
   uint8_t* unit = a.units + (static_cast<long long>(blockIdx.x) * a.c.Hv + h) * kUnit;
   const float ch = s_ch[i], cl = s_cl[i];
   if (is_key) {
+    // decays of a row go through the end of the column's block: a factor of the column, at most 1, and one of the row
+    const int end = i | 15;
+    s_col[i] = live ? __expf((s_ch[end] - ch) + (s_cl[end] - cl)) * s_r[i] : 0.0f;
     float* vec = reinterpret_cast<float*>(unit + kImg);
     const float ec = __expf(ch);
     vec[i] = s_beta[i] * ec * s_r[i];
@@ -316,6 +320,7 @@ __global__ void __launch_bounds__(128, 3)
     vec[192 + i] = s_beta[i];
     if (i == 63) vec[256] = ec;
   }
+  __syncthreads();
   ok = ok && mbar_wait(bars + 1, 0);
   tc_after();
   // the thread's row of A (P), in blocks of 16 columns
@@ -333,26 +338,34 @@ __global__ void __launch_bounds__(128, 3)
         tc_wait_ld();
         tc_landed(x[0]);
         tc_landed(x[1]);
-        if (16 * b + 16 <= i) {
-          const float f = __expf((ch - s_ch[16 * b + 15]) + (cl - s_cl[16 * b + 15])) * rf;
-          const pair f2 = pack2(f, f);
+        // the row's factor is at most 1 past the block, and in its own block as
+        // large as the block's decay is small: up to e^60 the factors serve there too
+        const float up = (ch - s_ch[16 * b + 15]) + (cl - s_cl[16 * b + 15]);
+        const float f = __expf(up) * rf;
+        const pair f2 = pack2(f, f);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            v[e] = *reinterpret_cast<const pair*>(s_col + 16 * b + 2 * e);
-            mul2(v[e], f2);
-            mul2(v[e], pack2(__uint_as_float(x[e >> 2][2 * (e & 3)]), __uint_as_float(x[e >> 2][2 * (e & 3) + 1])));
-          }
-        } else {
-          // the row's diagonal block (or one past it: nothing)
+        for (int e = 0; e < 8; ++e) {
+          v[e] = *reinterpret_cast<const pair*>(s_col + 16 * b + 2 * e);
+          mul2(v[e], f2);
+          mul2(v[e], pack2(__uint_as_float(x[e >> 2][2 * (e & 3)]), __uint_as_float(x[e >> 2][2 * (e & 3) + 1])));
+        }
+        const int d = i - 16 * b;  // the row's diagonal column
+        if (d < 16) {
           float y[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int j = 16 * b + e;
-            const float w = __expf((ch - s_ch[j]) + (cl - s_cl[j])) * (rf * s_r[j]);
-            y[e] = live && (is_key ? j < i : j <= i) ? w * __uint_as_float(x[e >> 3][e & 7]) : 0.0f;
-          }
+          for (int e = 0; e < 8; ++e) unpack2(v[e], y[2 * e], y[2 * e + 1]);
+          if (up > 60.0f && d >= 0) {
+#pragma unroll 1
+            for (int e = 0; e < 16; ++e) {
+              const float w = __expf((ch - s_ch[16 * b + e]) + (cl - s_cl[16 * b + e])) * (rf * s_r[16 * b + e]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = pack2(y[2 * e], y[2 * e + 1]);
+              for (int k = 0; k < 16; ++k)
+                if (k == e) y[k] = w * __uint_as_float(x[k >> 3][k & 7]);
+            }
+          }
+          const int last = is_key ? d : d + 1;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = pack2(2 * e < last ? y[2 * e] : 0.0f, 2 * e + 1 < last ? y[2 * e + 1] : 0.0f);
         }
       } else {
 #pragma unroll
@@ -512,7 +525,7 @@ __global__ void __launch_bounds__(128, 3)
   tc_before();
   const bool all_ok = __syncthreads_and(ok) != 0;
   tc_after();
-  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(128) : "memory");
+  release();
   if (tid == 0) {
     if (!all_ok) set_error(a.c.err, RSSM_ERRBIT_TIMEOUT);
     bulk_s2g(unit, im, kImg);
