@@ -505,7 +505,7 @@ rssm_status rssm_delta_prefill(const rssm_delta_cache *cache, const void *q, int
  * same result whatever the grid.
  *   target, draft [tok] rows of vocab values of prob_dtype (F32, BF16, F16),
  *        *_stride elements between rows;  tokens [ntok] i32, u [ntok] f32
- *   u_next, accepted, next [batch];  T 1..32;  error_word may be NULL
+ *   vocab 1..2^25;  u_next, accepted, next [batch];  T 1..32;  error_word may be NULL
  * A row with T_b = 0: accepted 0, next -1.  Bad bounds: the same, and
  * RSSM_ERRBIT_SEQLEN.  A draft id outside the vocabulary is rejected
  * (RSSM_ERRBIT_TOKEN); a row with no mass at all: next -1, RSSM_ERRBIT_TOKEN.

@@ -56,6 +56,8 @@ EXPORTS = ("rssm_scratch_bytes", "rssm_init_state", "rssm_flush", "rssm_step", "
 def load(path: str | None = None):
     """Load librssm.so; raises if it has not been built (no fallback exists)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -278,27 +278,29 @@ def rssm_selftest_wait_timeout(error_word, wait_ms=50, stream=None):
 _DTYPE = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 
-def _need(fn, ok, text):
-    if not ok:
-        raise ValueError(f"{fn}: {text}")
+def _refuse(fn, text):
+    raise ValueError(f"{fn}: {text}")
 
 
+# (messages are made only when a check fails: a decode step's calls are short)
 def _ids(fn, name, t, n):
-    _need(fn, t.dtype is torch.int32 and t.is_contiguous() and t.numel() >= n,
-          f"{name} must be a contiguous int32 tensor of at least {n} values")
+    if t.dtype is not torch.int32 or t.numel() < n or not t.is_contiguous():
+        _refuse(fn, f"{name} must be a contiguous int32 tensor of at least {n} values")
 
 
 def _f32(fn, name, t, n):
-    _need(fn, t.dtype is torch.float32 and t.is_contiguous() and t.numel() >= n,
-          f"{name} must be a contiguous float32 tensor of at least {n} values")
+    if t.dtype is not torch.float32 or t.numel() < n or not t.is_contiguous():
+        _refuse(fn, f"{name} must be a contiguous float32 tensor of at least {n} values")
 
 
 def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _s(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _s(stream, t):
+    """The stream's handle: the current one of t's device where none is given (torch.cuda.current_stream() costs a
+    small call 3 us)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 class DeltaCache:
@@ -310,7 +312,8 @@ class DeltaCache:
     def __init__(self, num_slots, k_heads, v_heads, key_dim, value_dim, npredicted, state_dtype=F32, device="cuda",
                  state=None, pend_k=None, pend_w=None, pend_c=None, pend=None, error_word=None):
         fn = "DeltaCache"
-        _need(fn, state_dtype in (F32, BF16), "state_dtype must be F32 or BF16")
+        if state_dtype not in (F32, BF16):
+            _refuse(fn, "state_dtype must be F32 or BF16")
         self.S, self.Hk, self.Hv, self.dk, self.dv, self.Tmax = num_slots, k_heads, v_heads, key_dim, value_dim, npredicted
         self.state_dtype = state_dtype
         dev = torch.device(device)
@@ -322,8 +325,8 @@ class DeltaCache:
             for i in range(len(shape) - 2, 0, -1):
                 dense[i] = dense[i + 1] * shape[i + 1]
             fits = all(n == 1 or x == d for n, x, d in zip(shape[1:], t.stride()[1:], dense[1:]))
-            _need(fn, tuple(t.shape) == shape and t.dtype is dtype and fits,
-                  f"{name} must be {dtype} {list(shape)}, contiguous within a slot")
+            if tuple(t.shape) != shape or t.dtype is not dtype or not fits:
+                _refuse(fn, f"{name} must be {dtype} {list(shape)}, contiguous within a slot")
             return t
 
         self.state = make("state", state, (num_slots, v_heads, value_dim, key_dim),
@@ -332,7 +335,8 @@ class DeltaCache:
         self.pend_w = make("pend_w", pend_w, (num_slots, 2, v_heads, npredicted, value_dim), torch.float32)
         self.pend_c = make("pend_c", pend_c, (num_slots, 2, v_heads, npredicted), torch.float32)
         self.pend = make("pend", pend, (num_slots, 2), torch.int32)
-        _need(fn, self.pend.is_contiguous(), "pend must be contiguous")
+        if not self.pend.is_contiguous():
+            _refuse(fn, "pend must be contiguous")
         self.error_word = make("error_word", error_word, (1,), torch.int32)
         c = _lib.RssmDeltaCacheStruct()
         c.num_slots, c.nkheads, c.nvheads, c.dkey, c.dvalue = num_slots, k_heads, v_heads, key_dim, value_dim
@@ -361,16 +365,24 @@ def alloc_delta_scratch(cache: DeltaCache, batch: int, tokens: int) -> torch.Ten
     return torch.zeros(n, dtype=torch.uint8, device=cache.state.device)  # its counters start at zero
 
 
+def _heads(fn, name, t, n, h, d):
+    """Elements between the tokens of t [n, h, d]."""
+    if t.dtype is torch.bfloat16 and t.dim() == 3:
+        st = t.stride()
+        if t.shape == (n, h, d) and (n == 0 or ((d == 1 or st[2] == 1) and (h == 1 or st[1] == d))):
+            return st[0] if n > 1 else h * d
+    _refuse(fn, f"{name} must be bfloat16 [{n}, {h}, {d}] with contiguous heads")
+
+
 def _delta_tokens(fn, cache, q, k, v, g, beta, out):
-    bf16, n = torch.bfloat16, q.shape[0]
-    for name, t, h, d in (("q", q, cache.Hk, cache.dk), ("k", k, cache.Hk, cache.dk), ("v", v, cache.Hv, cache.dv),
-                          ("out", out, cache.Hv, cache.dv)):
-        _need(fn, t.dtype is bf16 and t.shape == (n, h, d) and (n == 0 or h * d == 0 or t.stride(2) == 1) and
-              (h == 1 or t.stride(1) == d), f"{name} must be bfloat16 [{n}, {h}, {d}] with contiguous heads")
-    _need(fn, out.is_contiguous(), "out must be contiguous")
+    n = q.shape[0]
+    sq, sk = _heads(fn, "q", q, n, cache.Hk, cache.dk), _heads(fn, "k", k, n, cache.Hk, cache.dk)
+    sv = _heads(fn, "v", v, n, cache.Hv, cache.dv)
+    if out.dtype is not torch.bfloat16 or out.shape != v.shape or not out.is_contiguous():
+        _refuse(fn, f"out must be contiguous bfloat16 {list(v.shape)}")
     _f32(fn, "g", g, n * cache.Hv)
     _f32(fn, "beta", beta, n * cache.Hv)
-    return n
+    return n, sq, sk, sv
 
 
 def _row_stride(t, row):
@@ -385,7 +397,7 @@ def rssm_delta_step(cache, q, k, v, g, beta, slot_idx, accepted, T, out, scratch
     q, k [tok, k_heads, key_dim], v and out [tok, v_heads, value_dim] bf16 (q, k, v may be columns of one projection);
     g, beta [tok, v_heads] f32; `scale` defaults to key_dim ** -0.5."""
     fn = "rssm_delta_step"
-    n = _delta_tokens(fn, cache, q, k, v, g, beta, out)
+    n, sq, sk, sv = _delta_tokens(fn, cache, q, k, v, g, beta, out)
     batch = slot_idx.numel()
     _ids(fn, "slot_idx", slot_idx, batch)
     if accepted is not None:
@@ -393,10 +405,9 @@ def rssm_delta_step(cache, q, k, v, g, beta, slot_idx, accepted, T, out, scratch
     if cu_seqlens is not None:
         _ids(fn, "cu_seqlens", cu_seqlens, batch + 1)
     status = _lib.load().rssm_delta_step(
-        cache.struct(), q.data_ptr(), _row_stride(q, cache.Hk * cache.dk), k.data_ptr(),
-        _row_stride(k, cache.Hk * cache.dk), v.data_ptr(), _row_stride(v, cache.Hv * cache.dv), g.data_ptr(),
-        beta.data_ptr(), cache.dk ** -0.5 if scale is None else scale, int(l2norm), slot_idx.data_ptr(), _p(accepted),
-        _p(cu_seqlens), batch, T, n, out.data_ptr(), scratch.data_ptr(), scratch.numel(), _s(stream))
+        cache._ref, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, g.data_ptr(), beta.data_ptr(),
+        cache.dk ** -0.5 if scale is None else scale, int(l2norm), slot_idx.data_ptr(), _p(accepted),
+        _p(cu_seqlens), batch, T, n, out.data_ptr(), scratch.data_ptr(), scratch.numel(), _s(stream, q))
     if status:
         raise RssmError(fn, status)
 
@@ -406,7 +417,7 @@ def rssm_delta_prefill(cache, q, k, v, g, beta, slot_idx, cu_seqlens, out, scrat
     """The gated delta rule over whole prompts (tensors as in rssm_delta_step): outputs, and each slot's state after
     its prompt.  initial [batch] int32: nonzero rows go on from their slot's state."""
     fn = "rssm_delta_prefill"
-    n = _delta_tokens(fn, cache, q, k, v, g, beta, out)
+    n, sq, sk, sv = _delta_tokens(fn, cache, q, k, v, g, beta, out)
     batch = slot_idx.numel()
     _ids(fn, "slot_idx", slot_idx, batch)
     _ids(fn, "cu_seqlens", cu_seqlens, batch + 1)
@@ -416,7 +427,7 @@ def rssm_delta_prefill(cache, q, k, v, g, beta, slot_idx, cu_seqlens, out, scrat
         cache.struct(), q.data_ptr(), _row_stride(q, cache.Hk * cache.dk), k.data_ptr(),
         _row_stride(k, cache.Hk * cache.dk), v.data_ptr(), _row_stride(v, cache.Hv * cache.dv), g.data_ptr(),
         beta.data_ptr(), cache.dk ** -0.5 if scale is None else scale, int(l2norm), slot_idx.data_ptr(),
-        cu_seqlens.data_ptr(), _p(initial), batch, n, out.data_ptr(), scratch.data_ptr(), scratch.numel(), _s(stream))
+        cu_seqlens.data_ptr(), _p(initial), batch, n, out.data_ptr(), scratch.data_ptr(), scratch.numel(), _s(stream, q))
     if status:
         raise RssmError(fn, status)
 
@@ -427,10 +438,11 @@ def rssm_verify(target, tokens, u, u_next, T, accepted, next_token, draft=None, 
     fn = "rssm_verify"
     ntok, vocab = target.shape
     batch = u_next.numel()
-    _need(fn, target.dtype in _DTYPE and (vocab == 1 or target.stride(1) == 1), "target must be f32, bf16 or f16 rows")
-    if draft is not None:
-        _need(fn, draft.dtype is target.dtype and draft.shape == target.shape and (vocab == 1 or draft.stride(1) == 1),
-              "draft must have target's type and shape")
+    if target.dtype not in _DTYPE or (vocab > 1 and target.stride(1) != 1):
+        _refuse(fn, "target must be f32, bf16 or f16 rows")
+    if draft is not None and (draft.dtype is not target.dtype or draft.shape != target.shape or
+                              (vocab > 1 and draft.stride(1) != 1)):
+        _refuse(fn, "draft must have target's type and shape")
     _ids(fn, "tokens", tokens, ntok)
     _f32(fn, "u", u, ntok)
     _f32(fn, "u_next", u_next, batch)
@@ -441,14 +453,18 @@ def rssm_verify(target, tokens, u, u_next, T, accepted, next_token, draft=None, 
     status = _lib.load().rssm_verify(
         target.data_ptr(), _row_stride(target, vocab), _p(draft), 0 if draft is None else _row_stride(draft, vocab),
         _DTYPE[target.dtype], vocab, tokens.data_ptr(), u.data_ptr(), u_next.data_ptr(), _p(cu_seqlens), batch, T, ntok,
-        accepted.data_ptr(), next_token.data_ptr(), _p(error_word), _s(stream))
+        accepted.data_ptr(), next_token.data_ptr(), _p(error_word), _s(stream, target))
     if status:
         raise RssmError(fn, status)
 
 
 def _rows(fn, name, t, dtype, shape):
-    _need(fn, t.dtype is dtype and t.shape == shape and (shape[1] == 1 or t.stride(1) == 1),
-          f"{name} must be {dtype} {list(shape)} with contiguous rows")
+    """Elements between the rows of t."""
+    if t.dtype is dtype and t.shape == shape:
+        st = t.stride()
+        if st[1] == 1 or shape[1] == 1:
+            return st[0] if shape[0] > 1 else shape[1]
+    _refuse(fn, f"{name} must be {dtype} {list(shape)} with contiguous rows")
 
 
 def rssm_gated_norm(x, z, weight, out, group=None, eps=1e-5, norm_first=False, stream=None):
@@ -457,16 +473,17 @@ def rssm_gated_norm(x, z, weight, out, group=None, eps=1e-5, norm_first=False, s
     fn = "rssm_gated_norm"
     rows, dim = x.shape
     group = dim if group is None else group
-    _need(fn, x.dtype in _DTYPE, "x must be f32, bf16 or f16")
-    _rows(fn, "x", x, x.dtype, x.shape)
-    _rows(fn, "z", z, x.dtype, x.shape)
-    _rows(fn, "out", out, x.dtype, x.shape)
-    _need(fn, weight.numel() in (dim, group), f"weight must hold {dim} or {group} values")
+    dtype, shape = x.dtype, x.shape
+    if dtype not in _DTYPE:
+        _refuse(fn, "x must be f32, bf16 or f16")
+    sx, sz, so = _rows(fn, "x", x, dtype, shape), _rows(fn, "z", z, dtype, shape), _rows(fn, "out", out, dtype, shape)
+    weights = weight.numel()
+    if weights != dim and weights != group:
+        _refuse(fn, f"weight must hold {dim} or {group} values")
     _f32(fn, "weight", weight, 1)
-    status = _lib.load().rssm_gated_norm(
-        x.data_ptr(), _row_stride(x, dim), z.data_ptr(), _row_stride(z, dim), _DTYPE[x.dtype], weight.data_ptr(),
-        int(weight.numel() != dim), rows, dim, group, eps, int(norm_first), out.data_ptr(), _row_stride(out, dim),
-        _s(stream))
+    status = _lib.load().rssm_gated_norm(x.data_ptr(), sx, z.data_ptr(), sz, _DTYPE[dtype], weight.data_ptr(),
+                                         int(weights != dim), rows, dim, group, eps, int(norm_first), out.data_ptr(), so,
+                                         _s(stream, x))
     if status:
         raise RssmError(fn, status)
 
@@ -477,19 +494,16 @@ def rssm_residual_norm(x, residual, weight, out, residual_out, post_weight=None,
     residual in x's type or f32, weights f32 [dim]."""
     fn = "rssm_residual_norm"
     rows, dim = x.shape
-    _need(fn, x.dtype in _DTYPE and residual.dtype in (torch.float32, x.dtype), "types must be f32, bf16 or f16, the "
-          "residual's f32 or x's")
-    _rows(fn, "x", x, x.dtype, x.shape)
-    _rows(fn, "out", out, x.dtype, x.shape)
-    _rows(fn, "residual", residual, residual.dtype, x.shape)
-    _rows(fn, "residual_out", residual_out, residual.dtype, x.shape)
+    dtype, shape, rtype = x.dtype, x.shape, residual.dtype
+    if dtype not in _DTYPE or (rtype is not torch.float32 and rtype is not dtype):
+        _refuse(fn, "types must be f32, bf16 or f16, the residual's f32 or x's")
+    sx, so = _rows(fn, "x", x, dtype, shape), _rows(fn, "out", out, dtype, shape)
+    sr, sro = _rows(fn, "residual", residual, rtype, shape), _rows(fn, "residual_out", residual_out, rtype, shape)
     for name, t in (("weight", weight), ("post_weight", post_weight), ("scale", scale)):
-        if t is not None:
-            _need(fn, t.numel() == dim, f"{name} must hold {dim} values")
-            _f32(fn, name, t, dim)
+        if t is not None and (t.numel() != dim or t.dtype is not torch.float32 or not t.is_contiguous()):
+            _refuse(fn, f"{name} must hold {dim} contiguous float32 values")
     status = _lib.load().rssm_residual_norm(
-        x.data_ptr(), _row_stride(x, dim), residual.data_ptr(), _row_stride(residual, dim), _DTYPE[x.dtype],
-        _DTYPE[residual.dtype], _p(post_weight), _p(scale), alpha, weight.data_ptr(), rows, dim, eps,
-        residual_out.data_ptr(), _row_stride(residual_out, dim), out.data_ptr(), _row_stride(out, dim), _s(stream))
+        x.data_ptr(), sx, residual.data_ptr(), sr, _DTYPE[dtype], _DTYPE[rtype], _p(post_weight), _p(scale), alpha,
+        weight.data_ptr(), rows, dim, eps, residual_out.data_ptr(), sro, out.data_ptr(), so, _s(stream, x))
     if status:
         raise RssmError(fn, status)

@@ -82,8 +82,8 @@ struct GatedNormArgs {
   const float* w;
   void* out;
   long long x_stride, z_stride, out_stride;
-  long long rows;
-  int groups, group, w_group;  // w_group: weights between groups (0: one set for all)
+  unsigned items, groups;  // groups of all rows (below 2^30), and of one
+  int group, w_group;  // w_group: weights between groups (0: one set for all)
   float eps;
   int norm_first;
 };
@@ -96,15 +96,15 @@ __global__ void __launch_bounds__(TEAM == 0 ? 1024 : 256) gated_norm_kernel(cons
   pdl_wait();
   pdl_trigger();
   const int width = TEAM == 0 ? static_cast<int>(blockDim.x) : TEAM;
-  const long long item = TEAM == 0 ? blockIdx.x : (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / (TEAM ? TEAM : 1);
+  const unsigned item = TEAM == 0 ? blockIdx.x : blockIdx.x * (256 / (TEAM ? TEAM : 1)) + threadIdx.x / (TEAM ? TEAM : 1);
   const int lane = TEAM == 0 ? threadIdx.x : threadIdx.x % (TEAM ? TEAM : 1);
-  const bool live = item < a.rows * a.groups;
-  const long long row = live ? item / a.groups : 0;
-  const int grp = live ? static_cast<int>(item - row * a.groups) : 0;
-  const E* x = static_cast<const E*>(a.x) + row * a.x_stride + static_cast<long long>(grp) * a.group;
-  const E* z = static_cast<const E*>(a.z) + row * a.z_stride + static_cast<long long>(grp) * a.group;
-  E* out = static_cast<E*>(a.out) + row * a.out_stride + static_cast<long long>(grp) * a.group;
-  const float* w = a.w + static_cast<long long>(grp) * a.w_group;
+  const bool live = item < a.items;
+  const unsigned row = live ? item / a.groups : 0;
+  const unsigned grp = live ? item - row * a.groups : 0;
+  const E* x = static_cast<const E*>(a.x) + row * a.x_stride + grp * a.group;
+  const E* z = static_cast<const E*>(a.z) + row * a.z_stride + grp * a.group;
+  E* out = static_cast<E*>(a.out) + row * a.out_stride + grp * a.group;
+  const float* w = a.w + grp * a.w_group;
   const int n = live ? a.group : 0;
   float sum = 0.0f;
   if constexpr (NV > 0) {
@@ -310,7 +310,7 @@ bool on4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 template <typename E, int VEC>
 cudaError_t launch_gated(const GatedNormArgs& a, cudaStream_t st) {
-  const long long items = a.rows * a.groups;
+  const long long items = a.items;
   const int vecs = (a.group + VEC - 1) / VEC;
   const auto blocks = [&](int team) { return dim3(static_cast<unsigned>((items * team + 255) / 256)); };
   if (vecs <= 8) return launch_pdl(gated_norm_kernel<E, VEC, 8, 1>, blocks(8), dim3(256), 0, st, a);
@@ -357,8 +357,10 @@ extern "C" rssm_status rssm_gated_norm(const void* x, int64_t x_stride, const vo
   if (!x || !z || !out || !weight || !on4(weight) || reinterpret_cast<uintptr_t>(x) % esz ||
       reinterpret_cast<uintptr_t>(z) % esz || reinterpret_cast<uintptr_t>(out) % esz)
     return RSSM_ERR_INVALID_ARGUMENT;
-  GatedNormArgs a = {x, z, weight, out, x_stride, z_stride, out_stride, rows, dim / group, group, shared_weight ? 0 : group, eps, norm_first};
-  if (rows > (1ll << 30) / a.groups) return RSSM_ERR_UNSUPPORTED;
+  const int groups = dim / group;
+  if (rows > (1ll << 30) / groups) return RSSM_ERR_UNSUPPORTED;
+  GatedNormArgs a = {x, z, weight, out, x_stride, z_stride, out_stride, static_cast<unsigned>(rows * groups), static_cast<unsigned>(groups),
+                     group, shared_weight ? 0 : group, eps, norm_first};
   const bool vec = on16(x) && on16(z) && on16(out) && on16(weight) && x_stride % V == 0 && z_stride % V == 0 &&
                    out_stride % V == 0 && group % V == 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

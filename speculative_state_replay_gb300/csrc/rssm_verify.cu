@@ -25,10 +25,12 @@ struct VerifyArgs {
   unsigned* err;
 };
 
-constexpr int kVerifyThreads = 512;
+constexpr int kVerifyThreads = 256;
+constexpr int kVerifyBlocks = 4;  // an SM: 12 us where 3 take 15 (64 rows), 48 where 3 take 64 (512 rows)
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxParts = 8;  // blocks of a cluster (the portable most)
 constexpr int kRuns = 8;      // a warp's part of a row is summed in 8 runs
+constexpr int kMaxVocab = 1 << 25;  // 8 warps' lanes then sum at most 2^14 values in a run
 
 template <typename P>
 __device__ __forceinline__ float prob(P x);
@@ -49,16 +51,33 @@ __device__ __forceinline__ float prob<__half>(__half x) {
 // depend on their order, so the drawn token is a function of the inputs
 // whatever the grid.  floor(2^36 r) of r in [0, 1] comes from two additions
 // rounded toward zero: r + 32, whose last bit is 2^-18, leaves floor(2^18 r)
-// in its fraction, and the remainder (exact) + 2^-13 the next 18 bits; the
-// 64-bit conversion instruction runs at a fraction of their rate.
+// in its fraction, and the remainder (exact) + 2^-13 the next 18 bits.  The
+// sums' words are added as they are, two values an instruction, and the
+// constants' bits taken off at the end: a lane's part of a row has fewer than
+// 2^14 values (kMaxVocab), so neither sum passes 32 bits.  (The 64-bit
+// conversion instruction runs at a fraction of these rates.)
+using pair = unsigned long long;
+__device__ __forceinline__ pair pack2(float lo, float hi) {
+  pair d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
 struct Weight {
-  uint32_t hi, lo;  // in units of 2^-18 and 2^-36
-  __device__ __forceinline__ void add(float r) {
-    r = fminf(fmaxf(r, 0.0f), 1.0f);  // NaN: 0
-    const float t = __fadd_rz(r, 32.0f);
-    const float rest = __fsub_rn(r, __fsub_rn(t, 32.0f));
-    hi += __float_as_uint(t) - __float_as_uint(32.0f);
-    lo += __float_as_uint(__fadd_rz(rest, 1.220703125e-4f)) - __float_as_uint(1.220703125e-4f);
+  uint32_t hi = 0, lo = 0;  // in units of 2^-18 and 2^-36, less the constants' bits
+  __device__ __forceinline__ void add(float r0, float r1) {  // both in [0, 1]
+    const pair r = pack2(r0, r1), c = pack2(32.0f, 32.0f), f = pack2(1.220703125e-4f, 1.220703125e-4f), m = pack2(-1.0f, -1.0f);
+    pair t, d;
+    asm("add.rz.f32x2 %0, %1, %2;" : "=l"(t) : "l"(r), "l"(c));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(t), "l"(m), "l"(c));
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(r));
+    asm("add.rz.f32x2 %0, %0, %1;" : "+l"(d) : "l"(f));
+    hi += static_cast<uint32_t>(t) + static_cast<uint32_t>(t >> 32) - 2u * 0x42000000u;
+    lo += static_cast<uint32_t>(d) + static_cast<uint32_t>(d >> 32) - 2u * 0x39000000u;
+  }
+  __device__ __forceinline__ void add(float r) { add(r, 0.0f); }
+  __device__ __forceinline__ void add(const Weight& w) {
+    hi += w.hi;
+    lo += w.lo;
   }
   __device__ __forceinline__ unsigned long long value() const {
     return (static_cast<unsigned long long>(hi) << 18) + lo;
@@ -91,33 +110,63 @@ struct Residual {
     off = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(P));
     q_same = q && (reinterpret_cast<uintptr_t>(q) & 15u) == (reinterpret_cast<uintptr_t>(p) & 15u);
   }
-  __device__ __forceinline__ void one(Weight& w, int i) const {
-    w.add(prob<P>(p[i]) - (q ? prob<P>(q[i]) : (i == token ? 1.0f : 0.0f)));
+  // a value of the distribution: NaN and what is negative are 0, at most 1
+  __device__ __forceinline__ float at(int i) const {
+    return __saturatef(prob<P>(p[i]) - (q ? prob<P>(q[i]) : (i == token ? 1.0f : 0.0f)));
   }
-  // weight of the piece at position j
-  __device__ __forceinline__ unsigned long long piece(int j) const {
-    Weight w = {0u, 0u};
+  // weight of the piece at position j, any of it past the row's ends left out
+  __device__ __forceinline__ Weight piece(int j) const {
+    Weight w;
     const int i = j - off;
-    if (i >= 0 && i + VEC <= vocab) {
-      P a[VEC], c[VEC];
-      *reinterpret_cast<uint4*>(a) = __ldcs(reinterpret_cast<const uint4*>(p + i));
-      if (!q) {
+    for (int e = max(i, 0); e < min(i + VEC, vocab); ++e) w.add(at(e));
+    return w;
+  }
+  // whether the 32 pieces from position j on can be read as they are
+  __device__ __forceinline__ bool plain(int j) const {
+    const int i = j - off;
+    return i >= 0 && i + 32 * VEC <= vocab && static_cast<unsigned>(token - i) >= 32u * VEC && (!q || q_same);
+  }
+  __device__ __forceinline__ void load(int j, uint4& a, uint4& c) const {
+    a = __ldcs(reinterpret_cast<const uint4*>(p + (j - off)));
+    if (q) c = __ldcs(reinterpret_cast<const uint4*>(q + (j - off)));
+  }
+  __device__ __forceinline__ void add(Weight& w, const uint4& a, const uint4& c) const {
+    const P *x = reinterpret_cast<const P*>(&a), *y = reinterpret_cast<const P*>(&c);
+    if (q) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) w.add(prob<P>(a[e]) - (i + e == token ? 1.0f : 0.0f));
-        return w.value();
-      }
-      if (q_same) {
-        *reinterpret_cast<uint4*>(c) = __ldcs(reinterpret_cast<const uint4*>(q + i));
-      } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) c[e] = q[i + e];
-      }
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) w.add(prob<P>(a[e]) - prob<P>(c[e]));
+      for (int e = 0; e < VEC; e += 2)
+        w.add(__saturatef(prob<P>(x[e]) - prob<P>(y[e])), __saturatef(prob<P>(x[e + 1]) - prob<P>(y[e + 1])));
     } else {
-      for (int e = max(i, 0); e < min(i + VEC, vocab); ++e) one(w, e);
+#pragma unroll
+      for (int e = 0; e < VEC; e += 2) w.add(__saturatef(prob<P>(x[e])), __saturatef(prob<P>(x[e + 1])));
     }
-    return w.value();
+  }
+  // weights of the lane's pieces of N steps, `gap` positions apart: their loads first, then the sums
+  template <int N>
+  __device__ __forceinline__ void steps(Weight (&w)[N], int j, int gap, int lane, int end) const {
+    bool all = true;
+#pragma unroll
+    for (int x = 0; x < N; ++x) all = all && plain(j + x * gap);
+    if (all) {
+      uint4 a[N], c[N];
+#pragma unroll
+      for (int x = 0; x < N; ++x) load(j + x * gap + lane * VEC, a[x], c[x]);
+#pragma unroll
+      for (int x = 0; x < N; ++x) add(w[x], a[x], c[x]);
+    } else {
+#pragma unroll
+      for (int x = 0; x < N; ++x) {
+        const int k = j + x * gap;
+        if (k >= end) continue;
+        if (plain(k)) {
+          uint4 a, c;
+          load(k + lane * VEC, a, c);
+          add(w[x], a, c);
+        } else {
+          w[x].add(piece(k + lane * VEC));
+        }
+      }
+    }
   }
 };
 
@@ -128,7 +177,7 @@ struct Residual {
 // the run, then the piece and the value, from them and a second look at that
 // run alone.
 template <typename P>
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kVerifyThreads, kVerifyBlocks) verify_kernel(const VerifyArgs a) {
   constexpr int VEC = Residual<P>::VEC, kStep = 32 * VEC;
   __shared__ unsigned long long part[kVerifyWarps];
   __shared__ unsigned long long sums[2][kMaxParts];
@@ -185,23 +234,21 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs
   // a warp's part: kRuns runs of `len` steps of 32 pieces
   const int len = (a.vocab + res.off + parts * kVerifyWarps * kRuns * kStep - 1) / (parts * kVerifyWarps * kRuns * kStep);
   const int span = kRuns * len * kStep, first = (rank * kVerifyWarps + warp) * span, end = a.vocab + res.off;
-  unsigned long long total = 0, before = 0, run[kRuns];
+  unsigned long long total = 0, before = 0;
+  Weight run[kRuns / 4][4];
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll
-    for (int r = 0; r < kRuns; ++r) run[r] = 0;
+    for (int r = 0; r < kRuns; ++r) run[r / 4][r % 4] = Weight();
     if (first < end) {
 #pragma unroll 1
       for (int k = 0; k < len; ++k)
 #pragma unroll
-        for (int r = 0; r < kRuns; ++r) {
-          const int j = first + (r * len + k) * kStep + lane * VEC;
-          if (j < end) run[r] += res.piece(j);
-        }
+        for (int r = 0; r < kRuns / 4; ++r) res.steps(run[r], first + (4 * r * len + k) * kStep, len * kStep, lane, end);
     }
     unsigned long long w = 0;
 #pragma unroll
-    for (int r = 0; r < kRuns; ++r) w += run[r];
+    for (int r = 0; r < kRuns; ++r) w += run[r / 4][r % 4].value();
     w = warp_sum(w);
     if (lane == 0) part[warp] = w;
     __syncthreads();
@@ -250,7 +297,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs
   bool found = false;
 #pragma unroll
   for (int r = 0; r < kRuns; ++r) {
-    const unsigned long long w = warp_sum(run[r]);
+    const unsigned long long w = warp_sum(run[r / 4][r % 4].value());
     if (!found) {
       if (left < w) {
         found = true;
@@ -260,35 +307,42 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs
       }
     }
   }
-#pragma unroll 4
-  for (int k = 0; k < len; ++k) {
-    const int j = at + k * kStep + lane * VEC;
-    const unsigned long long own = j < end ? res.piece(j) : 0ull;
-    unsigned long long upto = own;
+#pragma unroll 1
+  for (int k0 = 0; k0 < len; k0 += 4) {  // four steps' values on their way at a time
+    Weight part4[4];
+    res.steps(part4, at + k0 * kStep, kStep, lane, min(end, at + len * kStep));
+    unsigned long long own[4];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long y = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += y;
-    }
-    const unsigned long long all = __shfl_sync(0xffffffffu, upto, 31);
-    if (left >= all) {
-      left -= all;
-      continue;
-    }
-    unsigned long long base = upto - own;
-    if (left >= base && left < upto) {
-      for (int i = max(j - res.off, 0); i < min(j - res.off + VEC, a.vocab); ++i) {
-        Weight w = {0u, 0u};
-        res.one(w, i);
-        base += w.value();
-        if (left < base) {
-          a.accepted[b] = count;
-          a.next[b] = i;
-          break;
+    for (int x = 0; x < 4; ++x) own[x] = part4[x].value();
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const unsigned long long all = warp_sum(own[x]);
+      if (left >= all) {
+        left -= all;
+        continue;
+      }
+      unsigned long long upto = own[x];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      unsigned long long base = upto - own[x];
+      if (left >= base && left < upto) {
+        const int i0 = at + (k0 + x) * kStep + lane * VEC - res.off;
+        for (int i = max(i0, 0); i < min(i0 + VEC, a.vocab); ++i) {
+          Weight w;
+          w.add(res.at(i));
+          base += w.value();
+          if (left < base) {
+            a.accepted[b] = count;
+            a.next[b] = i;
+            break;
+          }
         }
       }
+      return;
     }
-    break;
   }
 }
 
@@ -321,7 +375,7 @@ extern "C" rssm_status rssm_verify(const void* target, int64_t target_stride, co
   const auto al4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
   if (batch < 0 || T < 1 || vocab < 1 || ntok < 0) return RSSM_ERR_INVALID_ARGUMENT;
   if (prob_dtype != RSSM_F32 && prob_dtype != RSSM_BF16 && prob_dtype != RSSM_F16) return RSSM_ERR_INVALID_ARGUMENT;
-  if (T > 32 || vocab > (1 << 28)) return RSSM_ERR_UNSUPPORTED;
+  if (T > 32 || vocab > kMaxVocab) return RSSM_ERR_UNSUPPORTED;
   if (batch == 0) return RSSM_OK;
   if ((ntok > 0 && (!target || !tokens || !u)) || !u_next || !accepted || !next) return RSSM_ERR_INVALID_ARGUMENT;
   if (!al4(tokens) || !al4(u) || !al4(u_next) || !al4(cu_seqlens) || !al4(accepted) || !al4(next) || !al4(error_word))
@@ -347,8 +401,11 @@ extern "C" rssm_status rssm_verify(const void* target, int64_t target_stride, co
   a.accepted = accepted;
   a.next = next;
   a.err = error_word;
+  // blocks of a row: as many as still run all at once, each with 4096 values at least
+  const int sms = num_sms();
+  if (sms == 0) return RSSM_ERR_CUDA;
   int parts = 1;
-  while (parts < 8 && batch * parts < 304 && vocab > parts * 4096) parts *= 2;
+  while (parts < kMaxParts && static_cast<long long>(batch) * parts * 2 <= kVerifyBlocks * sms && vocab > parts * 4096) parts *= 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = prob_dtype == RSSM_F32    ? launch_verify<float>(a, parts, st)
                         : prob_dtype == RSSM_BF16 ? launch_verify<__nv_bfloat16>(a, parts, st)
