@@ -12,31 +12,86 @@ template <>
 struct Elem<float> {
   static __device__ __forceinline__ float to(float x) { return x; }
   static __device__ __forceinline__ float from(float x) { return x; }
+  static __device__ __forceinline__ uint32_t from2(float, float) { return 0u; }  // (4-byte values are stored as they are)
 };
 template <>
 struct Elem<__nv_bfloat16> {
   static __device__ __forceinline__ float to(__nv_bfloat16 x) { return __bfloat162float(x); }
   static __device__ __forceinline__ __nv_bfloat16 from(float x) { return __float2bfloat16_rn(x); }
+  static __device__ __forceinline__ float2 to2(uint32_t w) { return make_float2(bf16lo(w), bf16hi(w)); }
+  static __device__ __forceinline__ uint32_t from2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
 };
 template <>
 struct Elem<__half> {
   static __device__ __forceinline__ float to(__half x) { return __half2float(x); }
   static __device__ __forceinline__ __half from(float x) { return __float2half_rn(x); }
+  static __device__ __forceinline__ float2 to2(uint32_t w) { return h2f2(w); }
+  static __device__ __forceinline__ uint32_t from2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
 };
 
-// VEC elements of type E as floats, in 16-byte pieces (one element where VEC is 1)
+// VEC elements of type E, in 16-byte pieces (one element where VEC is 1): as
+// they come, as floats, and back.  Activations are read once (no L1 line is
+// kept for them: the weights' stay).
+template <typename E, int VEC>
+struct Raw {
+  static constexpr int W = VEC == 1 ? 1 : VEC * static_cast<int>(sizeof(E)) / 16;
+  uint4 w[W];
+  __device__ __forceinline__ void load(const E* p) {
+    if constexpr (VEC == 1) {
+      *reinterpret_cast<E*>(w) = *p;
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ void floats(float (&f)[VEC]) const {
+    const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+    if constexpr (VEC == 1) {
+      f[0] = Elem<E>::to(*reinterpret_cast<const E*>(w));
+    } else if constexpr (sizeof(E) == 4) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) f[i] = __uint_as_float(u[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC / 2; ++i) {
+        const float2 d = Elem<E>::to2(u[i]);
+        f[2 * i] = d.x;
+        f[2 * i + 1] = d.y;
+      }
+    }
+  }
+};
 template <typename E, int VEC>
 __device__ __forceinline__ void load_vec(const E* p, float (&f)[VEC]) {
+  Raw<E, VEC> r;
+  r.load(p);
+  r.floats(f);
+}
+// weights: read by every row
+template <int VEC>
+__device__ __forceinline__ void load_weight(const float* p, float (&f)[VEC]) {
   if constexpr (VEC == 1) {
-    f[0] = Elem<E>::to(*p);
+    f[0] = __ldg(p);
   } else {
-    constexpr int W = VEC * sizeof(E) / 16, N = 16 / sizeof(E);
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const uint4 raw = reinterpret_cast<const uint4*>(p)[w];
-      const E* e = reinterpret_cast<const E*>(&raw);
-#pragma unroll
-      for (int i = 0; i < N; ++i) f[w * N + i] = Elem<E>::to(e[i]);
+    for (int i = 0; i < VEC; i += 4) {
+      const float4 w = __ldg(reinterpret_cast<const float4*>(p + i));
+      f[i] = w.x;
+      f[i + 1] = w.y;
+      f[i + 2] = w.z;
+      f[i + 3] = w.w;
     }
   }
 }
@@ -45,21 +100,28 @@ __device__ __forceinline__ void store_vec(E* p, const float (&f)[VEC]) {
   if constexpr (VEC == 1) {
     *p = Elem<E>::from(f[0]);
   } else {
-    constexpr int W = VEC * sizeof(E) / 16, N = 16 / sizeof(E);
+    constexpr int N = 16 / sizeof(E);
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
+    for (int w = 0; w < VEC / N; ++w) {
       uint4 raw;
-      E* e = reinterpret_cast<E*>(&raw);
+      uint32_t* u = reinterpret_cast<uint32_t*>(&raw);
 #pragma unroll
-      for (int i = 0; i < N; ++i) e[i] = Elem<E>::from(f[w * N + i]);
-      reinterpret_cast<uint4*>(p)[w] = raw;
+      for (int i = 0; i < 4; ++i) u[i] = sizeof(E) == 4 ? __float_as_uint(f[w * N + i]) : Elem<E>::from2(f[(w * N + 2 * i) % VEC], f[(w * N + 2 * i + 1) % VEC]);
+      __stcs(reinterpret_cast<uint4*>(p) + w, raw);
     }
   }
 }
 
-__device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+// z / (1 + e^-z) by the hardware's exponential and reciprocal, a few 2^-22 off
+__device__ __forceinline__ float silu(float z) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return z * r;
+}
 
-// Sum over a team of TEAM lanes of a warp, or over the block (TEAM 0).
+// Sum over a team of TEAM lanes of a warp, or over the block (TEAM 0; `sh`: 32
+// floats that no earlier sum of the kernel used).
 template <int TEAM>
 __device__ __forceinline__ float team_sum(float v, float* sh) {
   constexpr int W = TEAM == 0 ? 32 : TEAM;
@@ -67,7 +129,6 @@ __device__ __forceinline__ float team_sum(float v, float* sh) {
   for (int o = W / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if constexpr (TEAM == 0) {
     const int warps = blockDim.x >> 5;
-    __syncthreads();  // an earlier sum's parts are read
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
     __syncthreads();
     v = 0.0f;
@@ -89,63 +150,89 @@ struct GatedNormArgs {
 };
 
 // A team of lanes (TEAM of a warp, or a block) per (row, group), the group's
-// values in NV vectors a lane; NV 0: groups too long for that, read twice.
-template <typename E, int VEC, int TEAM, int NV>
+// values in NV vectors a lane; IT groups one after another, their loads first
+// (short groups: a lane would have two loads on their way otherwise).  NV 0:
+// groups too long for that, read twice.
+template <typename E, int VEC, int TEAM, int NV, int IT>
 __global__ void __launch_bounds__(TEAM == 0 ? 1024 : 256) gated_norm_kernel(const GatedNormArgs a) {
   __shared__ float sh[32];
   pdl_wait();
   pdl_trigger();
   const int width = TEAM == 0 ? static_cast<int>(blockDim.x) : TEAM;
-  const unsigned item = TEAM == 0 ? blockIdx.x : blockIdx.x * (256 / (TEAM ? TEAM : 1)) + threadIdx.x / (TEAM ? TEAM : 1);
+  constexpr int kTeams = TEAM == 0 ? 1 : 256 / TEAM;
+  const unsigned first = blockIdx.x * (kTeams * IT) + (TEAM == 0 ? 0 : threadIdx.x / (TEAM ? TEAM : 1));
   const int lane = TEAM == 0 ? threadIdx.x : threadIdx.x % (TEAM ? TEAM : 1);
-  const bool live = item < a.items;
-  const unsigned row = live ? item / a.groups : 0;
-  const unsigned grp = live ? item - row * a.groups : 0;
-  const E* x = static_cast<const E*>(a.x) + row * a.x_stride + grp * a.group;
-  const E* z = static_cast<const E*>(a.z) + row * a.z_stride + grp * a.group;
-  E* out = static_cast<E*>(a.out) + row * a.out_stride + grp * a.group;
-  const float* w = a.w + grp * a.w_group;
-  const int n = live ? a.group : 0;
-  float sum = 0.0f;
+  const auto row_of = [&](unsigned item, unsigned& grp) {
+    const unsigned row = item / a.groups;
+    grp = item - row * a.groups;
+    return row;
+  };
   if constexpr (NV > 0) {
-    float fx[NV][VEC], fz[NV][VEC];
+    Raw<E, VEC> rx[IT][NV], rz[IT][NV];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int i = (v * width + lane) * VEC;
-      if (i < n) {
-        load_vec<E, VEC>(x + i, fx[v]);
-        load_vec<E, VEC>(z + i, fz[v]);
-      } else {
+    for (int it = 0; it < IT; ++it) {
+      const unsigned item = first + it * kTeams;
+      unsigned grp;
+      const unsigned row = row_of(item < a.items ? item : 0, grp);
+      const E* x = static_cast<const E*>(a.x) + row * a.x_stride + grp * a.group;
+      const E* z = static_cast<const E*>(a.z) + row * a.z_stride + grp * a.group;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) fx[v][e] = fz[v][e] = 0.0f;
+      for (int v = 0; v < NV; ++v) {
+        const int i = (v * width + lane) * VEC;
+        if (item < a.items && i < a.group) {
+          rx[it][v].load(x + i);
+          rz[it][v].load(z + i);
+        } else {
+          rx[it][v].zero();
+          rz[it][v].zero();
+        }
       }
     }
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int it = 0; it < IT; ++it) {
+      const unsigned item = first + it * kTeams;
+      unsigned grp;
+      const unsigned row = row_of(item < a.items ? item : 0, grp);
+      E* out = static_cast<E*>(a.out) + row * a.out_stride + grp * a.group;
+      const float* w = a.w + grp * a.w_group;
+      float fx[NV][VEC], fz[NV][VEC], sum = 0.0f;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        fz[v][e] = silu(fz[v][e]);
-        if (!a.norm_first) fx[v][e] *= fz[v][e];
-        sum = fmaf(fx[v][e], fx[v][e], sum);
-      }
-    sum = team_sum<TEAM>(sum, sh);
-    const float r = rsqrtf(sum / a.group + a.eps);
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int i = (v * width + lane) * VEC;
-      if (i < n) {
-        float fw[VEC];
-        load_vec<float, VEC>(w + i, fw);
+      for (int v = 0; v < NV; ++v) {
+        rx[it][v].floats(fx[v]);
+        rz[it][v].floats(fz[v]);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          fw[e] *= fx[v][e] * r;
-          if (a.norm_first) fw[e] *= fz[v][e];
+          fz[v][e] = silu(fz[v][e]);
+          if (!a.norm_first) fx[v][e] *= fz[v][e];
+          sum = fmaf(fx[v][e], fx[v][e], sum);
         }
-        store_vec<E, VEC>(out + i, fw);
+      }
+      sum = team_sum<TEAM>(sum, sh);
+      const float r = rsqrtf(sum / a.group + a.eps);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int i = (v * width + lane) * VEC;
+        if (item < a.items && i < a.group) {
+          float fw[VEC];
+          load_weight<VEC>(w + i, fw);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            fw[e] *= fx[v][e] * r;
+            if (a.norm_first) fw[e] *= fz[v][e];
+          }
+          store_vec<E, VEC>(out + i, fw);
+        }
       }
     }
   } else {
-    for (int i = lane * VEC; i < n; i += width * VEC) {
+    unsigned grp;
+    const unsigned row = row_of(first, grp);
+    const E* x = static_cast<const E*>(a.x) + row * a.x_stride + grp * a.group;
+    const E* z = static_cast<const E*>(a.z) + row * a.z_stride + grp * a.group;
+    E* out = static_cast<E*>(a.out) + row * a.out_stride + grp * a.group;
+    const float* w = a.w + grp * a.w_group;
+    float sum = 0.0f;
+    for (int i = lane * VEC; i < a.group; i += width * VEC) {
       float fx[VEC], fz[VEC];
       load_vec<E, VEC>(x + i, fx);
       if (!a.norm_first) load_vec<E, VEC>(z + i, fz);
@@ -157,11 +244,11 @@ __global__ void __launch_bounds__(TEAM == 0 ? 1024 : 256) gated_norm_kernel(cons
     }
     sum = team_sum<TEAM>(sum, sh);
     const float r = rsqrtf(sum / a.group + a.eps);
-    for (int i = lane * VEC; i < n; i += width * VEC) {
+    for (int i = lane * VEC; i < a.group; i += width * VEC) {
       float fx[VEC], fz[VEC], fw[VEC];
       load_vec<E, VEC>(x + i, fx);
       load_vec<E, VEC>(z + i, fz);
-      load_vec<float, VEC>(w + i, fw);
+      load_weight<VEC>(w + i, fw);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) fw[e] = a.norm_first ? fx[e] * r * fw[e] * silu(fz[e]) : fx[e] * silu(fz[e]) * r * fw[e];
       store_vec<E, VEC>(out + i, fw);
@@ -178,36 +265,46 @@ struct ResidualNormArgs {
   void* residual_out;
   void* out;
   long long x_stride, residual_stride, residual_out_stride, out_stride;
+  unsigned rows;
   int dim;
   float alpha, eps;
 };
 
-// One block per row, the row's values in NV vectors a thread; NV 0: rows too
-// long for that, read once per sum and once more to write.
+// A block per row, the row's values in NV vectors a thread; NV 0: rows too long
+// for that, read once per sum and once more to write.  (Blocks that go through
+// rows with the next one's loads on their way are slower, 103 us for 92: they
+// hold more registers, and two fit an SM instead of three.)
 template <typename E, typename R, int VEC, int NV>
 __global__ void __launch_bounds__(1024) residual_norm_kernel(const ResidualNormArgs a) {
-  __shared__ float sh[32];
+  __shared__ float sh[64];
   pdl_wait();
   pdl_trigger();
-  const long long row = blockIdx.x;
-  const E* x = static_cast<const E*>(a.x) + row * a.x_stride;
-  const R* res = static_cast<const R*>(a.residual) + row * a.residual_stride;
-  R* res_out = static_cast<R*>(a.residual_out) + row * a.residual_out_stride;
-  E* out = static_cast<E*>(a.out) + row * a.out_stride;
   const int tid = threadIdx.x, width = blockDim.x;
   if constexpr (NV > 0) {
+    const long long row = blockIdx.x;
+    const E* x = static_cast<const E*>(a.x) + row * a.x_stride;
+    const R* res = static_cast<const R*>(a.residual) + row * a.residual_stride;
+    R* res_out = static_cast<R*>(a.residual_out) + row * a.residual_out_stride;
+    E* out = static_cast<E*>(a.out) + row * a.out_stride;
+    Raw<E, VEC> rx[NV];
+    Raw<R, VEC> rr[NV];
     float h[NV][VEC], f[NV][VEC];
     float sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int i = (v * width + tid) * VEC;
       if (i < a.dim) {
-        load_vec<E, VEC>(x + i, f[v]);
-        load_vec<R, VEC>(res + i, h[v]);
+        rx[v].load(x + i);
+        rr[v].load(res + i);
       } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) f[v][e] = h[v][e] = 0.0f;
+        rx[v].zero();
+        rr[v].zero();
       }
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      rx[v].floats(f[v]);
+      rr[v].floats(h[v]);
     }
     float r = a.alpha;
     if (a.post) {
@@ -225,12 +322,12 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const ResidualNormA
       if (i < a.dim) {
         float fw[VEC];
         if (a.post) {
-          load_vec<float, VEC>(a.post + i, fw);
+          load_weight<VEC>(a.post + i, fw);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) f[v][e] *= fw[e];
         }
         if (a.scale) {
-          load_vec<float, VEC>(a.scale + i, fw);
+          load_weight<VEC>(a.scale + i, fw);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) f[v][e] *= fw[e];
         }
@@ -242,20 +339,25 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const ResidualNormA
         store_vec<R, VEC>(res_out + i, h[v]);
       }
     }
-    sum = team_sum<0>(sum, sh);
+    sum = team_sum<0>(sum, sh + 32);
     const float s = rsqrtf(sum / a.dim + a.eps);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int i = (v * width + tid) * VEC;
       if (i < a.dim) {
         float fw[VEC];
-        load_vec<float, VEC>(a.w + i, fw);
+        load_weight<VEC>(a.w + i, fw);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) fw[e] *= h[v][e] * s;
         store_vec<E, VEC>(out + i, fw);
       }
     }
   } else {
+    const unsigned row = blockIdx.x;
+    const E* x = static_cast<const E*>(a.x) + row * a.x_stride;
+    const R* res = static_cast<const R*>(a.residual) + row * a.residual_stride;
+    R* res_out = static_cast<R*>(a.residual_out) + row * a.residual_out_stride;
+    E* out = static_cast<E*>(a.out) + row * a.out_stride;
     float r = a.alpha, sum = 0.0f;
     if (a.post) {
       for (int i = tid * VEC; i < a.dim; i += width * VEC) {
@@ -273,12 +375,12 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const ResidualNormA
       load_vec<E, VEC>(x + i, f);
       load_vec<R, VEC>(res + i, h);
       if (a.post) {
-        load_vec<float, VEC>(a.post + i, fw);
+        load_weight<VEC>(a.post + i, fw);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) f[e] *= fw[e];
       }
       if (a.scale) {
-        load_vec<float, VEC>(a.scale + i, fw);
+        load_weight<VEC>(a.scale + i, fw);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) f[e] *= fw[e];
       }
@@ -291,12 +393,12 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const ResidualNormA
 #pragma unroll
       for (int e = 0; e < VEC; ++e) sum = fmaf(h[e], h[e], sum);
     }
-    sum = team_sum<0>(sum, sh);
+    sum = team_sum<0>(sum, sh + 32);
     const float s = rsqrtf(sum / a.dim + a.eps);
     for (int i = tid * VEC; i < a.dim; i += width * VEC) {
       float h[VEC], fw[VEC];
       stream(i, h);
-      load_vec<float, VEC>(a.w + i, fw);
+      load_weight<VEC>(a.w + i, fw);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) fw[e] *= h[e] * s;
       store_vec<R, VEC>(res_out + i, h);
@@ -308,35 +410,43 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const ResidualNormA
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool on4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+template <typename E, int VEC, int TEAM, int NV>
+cudaError_t launch_teams(const GatedNormArgs& a, cudaStream_t st) {
+  constexpr int teams = 256 / TEAM;
+  // Two groups a team once one would make over three waves of blocks: 64 us
+  // where one takes 71, and three 64 (524288 groups of 128, bf16).
+  if (NV <= 2 && a.items >= (1u << 20) / TEAM)
+    return launch_pdl(gated_norm_kernel<E, VEC, TEAM, NV, NV <= 2 ? 2 : 1>, dim3((a.items + 2 * teams - 1) / (2 * teams)), dim3(256), 0, st, a);
+  return launch_pdl(gated_norm_kernel<E, VEC, TEAM, NV, 1>, dim3((a.items + teams - 1) / teams), dim3(256), 0, st, a);
+}
+
 template <typename E, int VEC>
 cudaError_t launch_gated(const GatedNormArgs& a, cudaStream_t st) {
-  const long long items = a.items;
   const int vecs = (a.group + VEC - 1) / VEC;
-  const auto blocks = [&](int team) { return dim3(static_cast<unsigned>((items * team + 255) / 256)); };
-  if (vecs <= 8) return launch_pdl(gated_norm_kernel<E, VEC, 8, 1>, blocks(8), dim3(256), 0, st, a);
-  if (vecs <= 16) return launch_pdl(gated_norm_kernel<E, VEC, 16, 1>, blocks(16), dim3(256), 0, st, a);
-  if (vecs <= 32) return launch_pdl(gated_norm_kernel<E, VEC, 32, 1>, blocks(32), dim3(256), 0, st, a);
-  if (vecs <= 64) return launch_pdl(gated_norm_kernel<E, VEC, 32, 2>, blocks(32), dim3(256), 0, st, a);
-  if (vecs <= 128) return launch_pdl(gated_norm_kernel<E, VEC, 32, 4>, blocks(32), dim3(256), 0, st, a);
-  const dim3 grid(static_cast<unsigned>(items));
-  if (vecs <= 2048) return launch_pdl(gated_norm_kernel<E, VEC, 0, 2>, grid, dim3((vecs + 63) / 64 * 32), 0, st, a);
-  return launch_pdl(gated_norm_kernel<E, VEC, 0, 0>, grid, dim3(1024), 0, st, a);
+  if (vecs <= 8) return launch_teams<E, VEC, 8, 1>(a, st);
+  if (vecs <= 16) return launch_teams<E, VEC, 16, 1>(a, st);
+  if (vecs <= 32) return launch_teams<E, VEC, 32, 1>(a, st);
+  if (vecs <= 64) return launch_teams<E, VEC, 32, 2>(a, st);
+  if (vecs <= 128) return launch_teams<E, VEC, 32, 4>(a, st);
+  const dim3 grid(a.items);
+  if (vecs <= 2048) return launch_pdl(gated_norm_kernel<E, VEC, 0, 2, 1>, grid, dim3((vecs + 63) / 64 * 32), 0, st, a);
+  return launch_pdl(gated_norm_kernel<E, VEC, 0, 0, 1>, grid, dim3(1024), 0, st, a);
 }
 
 template <typename E, typename R, int VEC>
-cudaError_t launch_residual(const ResidualNormArgs& a, long long rows, cudaStream_t st) {
+cudaError_t launch_residual(const ResidualNormArgs& a, cudaStream_t st) {
   const int vecs = (a.dim + VEC - 1) / VEC;
-  const dim3 grid(static_cast<unsigned>(rows));
-  if (vecs <= 512) return launch_pdl(residual_norm_kernel<E, R, VEC, 1>, grid, dim3((vecs + 31) / 32 * 32), 0, st, a);
+  const dim3 grid(a.rows);
+  if (vecs <= 1024) return launch_pdl(residual_norm_kernel<E, R, VEC, 1>, grid, dim3((vecs + 31) / 32 * 32), 0, st, a);
   if (vecs <= 2048) return launch_pdl(residual_norm_kernel<E, R, VEC, 2>, grid, dim3((vecs + 63) / 64 * 32), 0, st, a);
   return launch_pdl(residual_norm_kernel<E, R, VEC, 0>, grid, dim3(1024), 0, st, a);
 }
 
 template <typename E>
-cudaError_t residual_of(const ResidualNormArgs& a, bool f32, bool vec, long long rows, cudaStream_t st) {
+cudaError_t residual_of(const ResidualNormArgs& a, bool f32, bool vec, cudaStream_t st) {
   constexpr int V = 16 / static_cast<int>(sizeof(E));
-  if (f32) return vec ? launch_residual<E, float, V>(a, rows, st) : launch_residual<E, float, 1>(a, rows, st);
-  return vec ? launch_residual<E, E, V>(a, rows, st) : launch_residual<E, E, 1>(a, rows, st);
+  if (f32) return vec ? launch_residual<E, float, V>(a, st) : launch_residual<E, float, 1>(a, st);
+  return vec ? launch_residual<E, E, V>(a, st) : launch_residual<E, E, 1>(a, st);
 }
 
 }  // namespace
@@ -391,14 +501,14 @@ extern "C" rssm_status rssm_residual_norm(const void* x, int64_t x_stride, const
     return RSSM_ERR_INVALID_ARGUMENT;
   if (rows > 0x7fffffffll) return RSSM_ERR_UNSUPPORTED;
   ResidualNormArgs a = {x, residual, post_weight, scale, weight, residual_out, out, x_stride, residual_stride,
-                        residual_out_stride, out_stride, dim, alpha, eps};
+                        residual_out_stride, out_stride, static_cast<unsigned>(rows), dim, alpha, eps};
   const bool vec = on16(x) && on16(residual) && on16(residual_out) && on16(out) && on16(weight) && on16(post_weight) &&
                    on16(scale) && dim % V == 0 && x_stride % V == 0 && out_stride % V == 0 && residual_stride % V == 0 &&
                    residual_out_stride % V == 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool f32 = residual_dtype == RSSM_F32;
-  const cudaError_t e = dtype == RSSM_F32    ? residual_of<float>(a, true, vec, rows, st)
-                        : dtype == RSSM_BF16 ? residual_of<__nv_bfloat16>(a, f32, vec, rows, st)
-                                             : residual_of<__half>(a, f32, vec, rows, st);
+  const cudaError_t e = dtype == RSSM_F32    ? residual_of<float>(a, true, vec, st)
+                        : dtype == RSSM_BF16 ? residual_of<__nv_bfloat16>(a, f32, vec, st)
+                                             : residual_of<__half>(a, f32, vec, st);
   return e == cudaSuccess ? RSSM_OK : RSSM_ERR_CUDA;
 }
