@@ -169,21 +169,22 @@ __device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x,
 // product of 128 rows; a thread then has a row of A (threads 0-63) or of P.
 // The inverse goes by blocks of 16: the diagonal ones by substitution, then
 // joined twice, [T1 0; -T2 A21 T1  T2].  The block chain is a string of small
-// dependent steps, so what matters is how many blocks an SM holds: three, for
-// which T and P T take the place of the keys and queries in shared memory.
+// dependent steps, so what matters is how many blocks an SM holds: four, for
+// which A and P take the place of the keys and queries in shared memory, and
+// P T that of A.
 // --------------------------------------------------------------------------
 struct ChunkSmem {
-  static constexpr int kImage = 0;              // K and Q per 64 columns as in the scan, then T and P T as in scratch
-  static constexpr int kHi = kImg;              // A (64 rows), P (64 rows): the hi parts
-  static constexpr int kLo = kHi + kImgHi;      // and the lo parts
-  static constexpr int kDiag = kLo + kImgHi;    // diagonal blocks of A in fp32, then their inverses: 4 x 16 x 20
+  static constexpr int kHi = 0;                   // K and Q per 64 columns as in the scan; A (64 rows) and P, the hi parts,
+  static constexpr int kLo = kImgHi;              // and the lo parts; P T for A
+  static constexpr int kT = 2 * kImgHi;           // T (64 rows), hi and lo parts
+  static constexpr int kDiag = kT + 2 * 8192;     // diagonal blocks of A in fp32, then their inverses: 4 x 16 x 20
   static constexpr int kScalars = kDiag + 4 * 16 * 20 * 4;  // c hi, c lo, beta, r, rq, column factors: 6 x 64 floats
   static constexpr int kBars = kScalars + 6 * 64 * 4;
   static constexpr int kBytes = kBars + 64 + 1024;
 };
 
 template <int DK>
-__global__ void __launch_bounds__(128, 3)
+__global__ void __launch_bounds__(128, 4)
     delta_chunk_kernel(const DeltaPrefillArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk) {
   extern __shared__ uint8_t raw[];
   uint8_t* sm = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
@@ -230,14 +231,14 @@ __global__ void __launch_bounds__(128, 3)
   const int tok0 = sh[1], n = sh[2];
   float* s_ch = reinterpret_cast<float*>(sm + ChunkSmem::kScalars);
   float *s_cl = s_ch + 64, *s_beta = s_cl + 64, *s_r = s_beta + 64, *s_rq = s_r + 64, *s_col = s_rq + 64;
-  uint8_t* im = sm + ChunkSmem::kImage;
+  uint8_t *kq = sm, *s_t = sm + ChunkSmem::kT;  // T
   const uint32_t base = smem_addr(sm);
   if (tid == 0) {
     mbar_arrive_expect_tx(bars, DK * 2 * 128);
 #pragma unroll
     for (int x = 0; x < DK / 64; ++x) {
-      tma_2d(im + x * 16384, &mk, hk * DK + 64 * x, tok0, bars);
-      tma_2d(im + x * 16384 + 8192, &mq, hk * DK + 64 * x, tok0, bars);
+      tma_2d(kq + x * 16384, &mk, hk * DK + 64 * x, tok0, bars);
+      tma_2d(kq + x * 16384 + 8192, &mq, hk * DK + 64 * x, tok0, bars);
     }
   }
   constexpr uint32_t i_gram = instruction(64, false, false), i_pt = instruction(64, false, true);
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(128, 3)
   }
   bool ok = mbar_wait(bars, 0);
   if (tid == 32 && ok) {
-    const uint64_t d = operand(base + ChunkSmem::kImage, 16, 1024, kSw128);
+    const uint64_t d = operand(base, 16, 1024, kSw128);
 #pragma unroll
     for (int x = 0; x < DK / 16; ++x) {
       const uint64_t k = d + (((x >> 2) * 16384 + (x & 3) * 32) >> 4);
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(128, 3)
       for (int x = 0; x < DK / 64; ++x)
 #pragma unroll
         for (int ch = 0; ch < 8; ++ch) {
-          const uint4 w = *reinterpret_cast<const uint4*>(im + x * 16384 + sw128(tid, ch));
+          const uint4 w = *reinterpret_cast<const uint4*>(kq + x * 16384 + sw128(tid, ch));
           const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -390,11 +391,8 @@ __global__ void __launch_bounds__(128, 3)
       }
     }
   }
-  // the Gram products are done with the keys and queries: T takes their place, zero above its diagonal
-  for (int x = tid; x < 64 * 8; x += 128) {
-    *reinterpret_cast<uint4*>(im + x * 16) = make_uint4(0u, 0u, 0u, 0u);
-    *reinterpret_cast<uint4*>(im + kImgHi + x * 16) = make_uint4(0u, 0u, 0u, 0u);
-  }
+  // T is zero above its diagonal
+  for (int x = tid; x < 2 * 64 * 8; x += 128) *reinterpret_cast<uint4*>(s_t + x * 16) = make_uint4(0u, 0u, 0u, 0u);
   __syncthreads();
   {
     // inverse of the warp's unit lower triangular diagonal block: a lane per column
@@ -426,15 +424,15 @@ __global__ void __launch_bounds__(128, 3)
 #pragma unroll
     for (int e = 0; e < 4; ++e) split_bf16x2(fd[r * 20 + c0 + 2 * e], fd[r * 20 + c0 + 2 * e + 1], hw[e], lw[e]);
     const uint32_t to = sw128(16 * warp + r, 2 * warp + (lane & 1));
-    *reinterpret_cast<uint4*>(im + to) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-    *reinterpret_cast<uint4*>(im + kImgHi + to) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+    *reinterpret_cast<uint4*>(s_t + to) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+    *reinterpret_cast<uint4*>(s_t + 8192 + to) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
   }
   // block (br, bc) of a 64 x 64 matrix as a second operand (its transpose: rows of it are columns), or, with .trans,
   // its transpose as a first operand; the same addresses store a transposed accumulator
   const auto block = [&](uint32_t m, int br, int bc) {
     return m + sw128(16 * br + (lane & 7) + ((lane >> 4) << 3), 2 * bc + ((lane >> 3) & 1));
   };
-  const uint32_t t_hi = base + ChunkSmem::kImage, t_lo = t_hi + kImgHi, a_hi = base + ChunkSmem::kHi, a_lo = base + ChunkSmem::kLo;
+  const uint32_t t_hi = base + ChunkSmem::kT, t_lo = t_hi + 8192, a_hi = base + ChunkSmem::kHi, a_lo = base + ChunkSmem::kLo;
   // d += (T_lc)^T (A_il)^T for one l
   const auto first = [&](float (&d)[2][4], int l, int c, int r) {
     uint32_t th[4], tl[4], bh[4], bl[4];
@@ -516,9 +514,9 @@ __global__ void __launch_bounds__(128, 3)
       tc_landed(x);
 #pragma unroll
       for (int e = 0; e < 4; ++e) split_bf16x2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]), hw[e], lw[e]);
-      const uint32_t to = sw128(tid, b);
-      *reinterpret_cast<uint4*>(im + to) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-      *reinterpret_cast<uint4*>(im + kImgHi + to) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+      const uint32_t to = sw128(i, b);
+      *reinterpret_cast<uint4*>(sm + ChunkSmem::kHi + to) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+      *reinterpret_cast<uint4*>(sm + ChunkSmem::kLo + to) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
     }
   }
   fence_async();
@@ -528,7 +526,10 @@ __global__ void __launch_bounds__(128, 3)
   release();
   if (tid == 0) {
     if (!all_ok) set_error(a.c.err, RSSM_ERRBIT_TIMEOUT);
-    bulk_s2g(unit, im, kImg);
+    bulk_s2g(unit, s_t, 8192);
+    bulk_s2g(unit + 8192, sm + ChunkSmem::kHi, 8192);
+    bulk_s2g(unit + kImgHi, s_t + 8192, 8192);
+    bulk_s2g(unit + kImgHi + 8192, sm + ChunkSmem::kLo, 8192);
     bulk_s2g_wait();
   }
   pdl_trigger();
