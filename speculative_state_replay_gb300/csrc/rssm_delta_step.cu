@@ -14,7 +14,8 @@ struct DeltaStepArgs {
   int batch, T;
   long long tokens;
   int tiles;         // kStepRows value rows a head has
-  int items, per;    // (value head, tile) items of a key head, and how many of them a block takes
+  int items;         // (value head, tile) items of a (row, key head)
+  int whole, per;    // blocks that take all items of theirs; the (row, key head)s after them go `per` items to a block
   unsigned* ticket;  // scratch [batch]: blocks that have read the row's `pend` (zero between calls)
 };
 
@@ -47,8 +48,8 @@ struct alignas(128) StepSmem {
 static_assert(sizeof(StepWarp<64, false>) % 128 == 0 && sizeof(StepWarp<128, true>) % 128 == 0, "a warp's part keeps the next one's alignment");
 static_assert(sizeof(StepWarp<64, false>::Small) % 16 == 0 && kTokenRow<64> % 16 == 0 && kTokenRow<128> % 16 == 0, "rows start on 16 bytes");
 
-// A block takes `per` items -- 64 value rows of a value head each -- of a (row,
-// key head); the tokens' keys and queries, their Gram products and the waiting
+// A block takes items -- 64 value rows of a value head each -- of a (row, key
+// head); the tokens' keys and queries, their Gram products and the waiting
 // keys serve all of them.  One warp per 16 value rows reads its part of S once
 // (one bulk copy: the rows are contiguous), and with the rows in registers sends
 // for its next item's; it forms the new drafts' outputs and corrections, adds the
@@ -67,10 +68,15 @@ __global__ void __launch_bounds__(kStepWarps * 32, 3) delta_step_kernel(const De
     fence_barrier_init();
   }
   __syncwarp();
+  int unit = blockIdx.x, item0 = 0, left = a.items;
   const int groups = (a.items + a.per - 1) / a.per;
-  const int b = blockIdx.x / (a.c.Hk * groups), hk = blockIdx.x / groups % a.c.Hk;
-  const int item0 = blockIdx.x % groups * a.per;
-  int left = min(a.per, a.items - item0);
+  if (unit >= a.whole) {
+    const int x = unit - a.whole;
+    unit = a.whole + x / groups;
+    item0 = x % groups * a.per;
+    left = min(a.per, a.items - item0);
+  }
+  const int b = unit / a.c.Hk, hk = unit - b * a.c.Hk;
   pdl_wait();
   pdl_trigger();
   const int s = a.slot_idx[b];
@@ -78,7 +84,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, 3) delta_step_kernel(const De
   const int n = a.cu ? a.cu[b + 1] - static_cast<int>(tok0) : a.T;
   const int acc = a.accepted ? a.accepted[b] : 0;
   if (n < 0 || n > a.T || tok0 < 0 || tok0 + n > a.tokens) {  // the row's tokens are not known: nothing to write
-    if (tid == 0 && blockIdx.x % (a.c.Hk * groups) == 0) set_error(a.c.err, RSSM_ERRBIT_SEQLEN);
+    if (tid == 0 && hk == 0 && item0 == 0) set_error(a.c.err, RSSM_ERRBIT_SEQLEN);
     return;
   }
   const int dv = a.c.dv, Hv = a.c.Hv, np = a.c.np;
@@ -136,7 +142,8 @@ __global__ void __launch_bounds__(kStepWarps * 32, 3) delta_step_kernel(const De
   // last one knows that all have, and turns the sides
   if (tid == 0) {
     __threadfence();
-    const unsigned blocks = static_cast<unsigned>(a.c.Hk * groups);
+    const int wholes = min(max(a.whole - b * a.c.Hk, 0), a.c.Hk);  // of the row's blocks
+    const unsigned blocks = static_cast<unsigned>(wholes + (a.c.Hk - wholes) * groups);
     if (atomicInc(a.ticket + b, blocks - 1u) == blocks - 1u) {
       if (ok)
         reinterpret_cast<int2*>(a.c.pend)[s] = make_int2(to, n);
@@ -414,18 +421,21 @@ extern "C" rssm_status rssm_delta_step(const rssm_delta_cache* cache, const void
   a.tiles = (a.c.dv + kStepRows - 1) / kStepRows;
   a.ticket = static_cast<unsigned*>(scratch);
   a.items = a.c.rep * a.tiles;
-  // Items a block takes: as few as give one wave of blocks, all of a key head's
-  // where there are more -- then what the items share is worth more than the
-  // spread.  (64 rows of 16 key heads with 4 items, fp32: 1 an item 82 us, 4 an
-  // item 61 us; one row: 28 us against 32 us with the host's part.)
-  const long long wave = 3ll * num_sms();
+  // Items a block takes: all of a (row, key head)'s for as many whole waves of
+  // blocks as there are -- what the items share is worth more than the spread
+  // (64 rows of 16 key heads with 4 items, fp32: 1 an item 82 us, 4 an item 61
+  // us) -- and of the rest as few as give one more wave, so that it does not
+  // take as long as a whole one (55 us).
+  const long long wave = 3ll * num_sms(), units = static_cast<long long>(batch) * a.c.Hk;
   if (wave == 0) return RSSM_ERR_CUDA;
-  const auto grid_of = [&](int per) { return static_cast<long long>(batch) * a.c.Hk * ((a.items + per - 1) / per); };
+  if (units * a.items > 0x7fffffffll) return RSSM_ERR_UNSUPPORTED;
+  a.whole = static_cast<int>(units / wave * wave);
+  const long long rest = units - a.whole;
+  const auto spread = [&](int per) { return rest * ((a.items + per - 1) / per); };
   a.per = 1;
-  while (a.per < a.items && grid_of(a.per) > wave) a.per = a.per * 2 < a.items ? a.per * 2 : a.items;
-  if (grid_of(1) > 0x7fffffffll) return RSSM_ERR_UNSUPPORTED;
+  while (a.per < a.items && spread(a.per) > wave) a.per = a.per * 2 < a.items ? a.per * 2 : a.items;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const unsigned grid = static_cast<unsigned>(grid_of(a.per));
+  const unsigned grid = static_cast<unsigned>(a.whole + spread(a.per));
   const bool f32 = a.c.dtype == RSSM_F32;
   const cudaError_t e = cache->dkey == 128 ? (f32 ? launch_step<128, true>(a, grid, cs) : launch_step<128, false>(a, grid, cs))
                                            : (f32 ? launch_step<64, true>(a, grid, cs) : launch_step<64, false>(a, grid, cs));
