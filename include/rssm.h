@@ -435,10 +435,13 @@ typedef struct {
   uint32_t *error_word;
 } rssm_delta_cache;
 
-/* Bytes of scratch rssm_delta_step and rssm_delta_prefill need for `batch`
- * rows and `tokens` tokens in all; 0 for an invalid cache.  Zero the buffer
- * once when it is allocated (its first `batch` words are counters that every
- * call leaves at zero).  One buffer serves both calls and every smaller one. */
+/* Bytes of scratch for `batch` rows and `tokens` tokens in all; 0 for an
+ * invalid cache.  rssm_delta_prefill needs that much (33 KB per 64 tokens and
+ * value head, and a prompt's last chunk counts as a whole one), rssm_delta_step
+ * the first 256 KB: its counters.  Zero the buffer once when it is allocated;
+ * every call leaves the counters at zero.  One buffer serves both calls and all
+ * smaller ones, in any order on one stream; calls that overlap on the GPU need
+ * scratch of their own. */
 size_t rssm_delta_scratch_bytes(const rssm_delta_cache *cache, int32_t batch, int64_t tokens);
 
 /*
@@ -459,7 +462,8 @@ size_t rssm_delta_scratch_bytes(const rssm_delta_cache *cache, int32_t batch, in
  *   g, beta f32 [tok][nvheads]; out bf16 [tok][nvheads][dvalue], dense
  *   slot_idx, accepted [batch] i32; cu_seqlens [batch+1] i32 or NULL (T a row)
  *   T 1..npredicted: most tokens of a row;  tokens: token rows of q, k, v, out
- * Rows of slot ids <= 0 or >= num_slots get zero outputs.  accepted < 0 or
+ * batch at most 65536.  Rows of slot ids <= 0 or >= num_slots get zero
+ * outputs (active ids in one call must be unique).  accepted < 0 or
  * more than the waiting drafts: RSSM_ERRBIT_ACCEPT, zero outputs, the slot
  * untouched.  Token bounds that are negative, longer than T or past `tokens`:
  * RSSM_ERRBIT_SEQLEN, the row is skipped.

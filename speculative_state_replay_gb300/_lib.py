@@ -9,6 +9,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "librssm.so")
 _lock = threading.Lock()
 _lib = None
+_fast = None
 
 
 class RssmCacheStruct(ctypes.Structure):
@@ -112,3 +113,15 @@ def load(path: str | None = None):
         lib.rssm_status_string.argtypes = [ctypes.c_int]
         _lib = lib
         return lib
+
+
+def fast():
+    """The C module that calls librssm with checked arguments (csrc/rssm_call.c); the library is loaded first, so that
+    a missing build is reported as in load()."""
+    global _fast
+    if _fast is None:
+        load()
+        from . import _call
+
+        _fast = _call
+    return _fast

@@ -347,7 +347,7 @@ class DeltaCache:
             setattr(c, name + "_slot_stride", t.stride(0))
         c.pend, c.error_word = self.pend.data_ptr(), self.error_word.data_ptr()
         self._struct = c
-        self._ref = ctypes.byref(c)
+        self._ref, self._addr = ctypes.byref(c), ctypes.addressof(c)
 
     def struct(self):
         return self._ref
@@ -367,9 +367,9 @@ def alloc_delta_scratch(cache: DeltaCache, batch: int, tokens: int) -> torch.Ten
 
 def _heads(fn, name, t, n, h, d):
     """Elements between the tokens of t [n, h, d]."""
-    if t.dtype is torch.bfloat16 and t.dim() == 3:
+    if t.dtype is torch.bfloat16 and t.shape == (n, h, d):
         st = t.stride()
-        if t.shape == (n, h, d) and (n == 0 or ((d == 1 or st[2] == 1) and (h == 1 or st[1] == d))):
+        if n == 0 or ((d == 1 or st[2] == 1) and (h == 1 or st[1] == d)):
             return st[0] if n > 1 else h * d
     _refuse(fn, f"{name} must be bfloat16 [{n}, {h}, {d}] with contiguous heads")
 
@@ -383,11 +383,6 @@ def _delta_tokens(fn, cache, q, k, v, g, beta, out):
     _f32(fn, "g", g, n * cache.Hv)
     _f32(fn, "beta", beta, n * cache.Hv)
     return n, sq, sk, sv
-
-
-def _row_stride(t, row):
-    """Elements between the rows of t; a single row has no stride that matters."""
-    return t.stride(0) if t.shape[0] > 1 else row
 
 
 def rssm_delta_step(cache, q, k, v, g, beta, slot_idx, accepted, T, out, scratch, cu_seqlens=None, scale=None,
@@ -404,8 +399,8 @@ def rssm_delta_step(cache, q, k, v, g, beta, slot_idx, accepted, T, out, scratch
         _ids(fn, "accepted", accepted, batch)
     if cu_seqlens is not None:
         _ids(fn, "cu_seqlens", cu_seqlens, batch + 1)
-    status = _lib.load().rssm_delta_step(
-        cache._ref, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, g.data_ptr(), beta.data_ptr(),
+    status = _lib.fast().rssm_delta_step(
+        cache._addr, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, g.data_ptr(), beta.data_ptr(),
         cache.dk ** -0.5 if scale is None else scale, int(l2norm), slot_idx.data_ptr(), _p(accepted),
         _p(cu_seqlens), batch, T, n, out.data_ptr(), scratch.data_ptr(), scratch.numel(), _s(stream, q))
     if status:
@@ -423,37 +418,10 @@ def rssm_delta_prefill(cache, q, k, v, g, beta, slot_idx, cu_seqlens, out, scrat
     _ids(fn, "cu_seqlens", cu_seqlens, batch + 1)
     if initial is not None:
         _ids(fn, "initial", initial, batch)
-    status = _lib.load().rssm_delta_prefill(
-        cache.struct(), q.data_ptr(), _row_stride(q, cache.Hk * cache.dk), k.data_ptr(),
-        _row_stride(k, cache.Hk * cache.dk), v.data_ptr(), _row_stride(v, cache.Hv * cache.dv), g.data_ptr(),
-        beta.data_ptr(), cache.dk ** -0.5 if scale is None else scale, int(l2norm), slot_idx.data_ptr(),
-        cu_seqlens.data_ptr(), _p(initial), batch, n, out.data_ptr(), scratch.data_ptr(), scratch.numel(), _s(stream, q))
-    if status:
-        raise RssmError(fn, status)
-
-
-def rssm_verify(target, tokens, u, u_next, T, accepted, next_token, draft=None, cu_seqlens=None, error_word=None,
-                stream=None):
-    """Accepted counts and next tokens of a speculative step; target (and draft) [tok, vocab] probabilities."""
-    fn = "rssm_verify"
-    ntok, vocab = target.shape
-    batch = u_next.numel()
-    if target.dtype not in _DTYPE or (vocab > 1 and target.stride(1) != 1):
-        _refuse(fn, "target must be f32, bf16 or f16 rows")
-    if draft is not None and (draft.dtype is not target.dtype or draft.shape != target.shape or
-                              (vocab > 1 and draft.stride(1) != 1)):
-        _refuse(fn, "draft must have target's type and shape")
-    _ids(fn, "tokens", tokens, ntok)
-    _f32(fn, "u", u, ntok)
-    _f32(fn, "u_next", u_next, batch)
-    _ids(fn, "accepted", accepted, batch)
-    _ids(fn, "next_token", next_token, batch)
-    if cu_seqlens is not None:
-        _ids(fn, "cu_seqlens", cu_seqlens, batch + 1)
-    status = _lib.load().rssm_verify(
-        target.data_ptr(), _row_stride(target, vocab), _p(draft), 0 if draft is None else _row_stride(draft, vocab),
-        _DTYPE[target.dtype], vocab, tokens.data_ptr(), u.data_ptr(), u_next.data_ptr(), _p(cu_seqlens), batch, T, ntok,
-        accepted.data_ptr(), next_token.data_ptr(), _p(error_word), _s(stream, target))
+    status = _lib.fast().rssm_delta_prefill(
+        cache._addr, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, g.data_ptr(), beta.data_ptr(),
+        cache.dk ** -0.5 if scale is None else scale, int(l2norm), slot_idx.data_ptr(), cu_seqlens.data_ptr(),
+        _p(initial), batch, n, out.data_ptr(), scratch.data_ptr(), scratch.numel(), _s(stream, q))
     if status:
         raise RssmError(fn, status)
 
@@ -465,6 +433,31 @@ def _rows(fn, name, t, dtype, shape):
         if st[1] == 1 or shape[1] == 1:
             return st[0] if shape[0] > 1 else shape[1]
     _refuse(fn, f"{name} must be {dtype} {list(shape)} with contiguous rows")
+
+
+def rssm_verify(target, tokens, u, u_next, T, accepted, next_token, draft=None, cu_seqlens=None, error_word=None,
+                stream=None):
+    """Accepted counts and next tokens of a speculative step; target (and draft) [tok, vocab] probabilities."""
+    fn = "rssm_verify"
+    ntok, vocab = target.shape
+    batch = u_next.numel()
+    dtype = target.dtype
+    if dtype not in _DTYPE:
+        _refuse(fn, "target must be f32, bf16 or f16")
+    st = _rows(fn, "target", target, dtype, target.shape)
+    sd = 0 if draft is None else _rows(fn, "draft", draft, dtype, target.shape)
+    _ids(fn, "tokens", tokens, ntok)
+    _f32(fn, "u", u, ntok)
+    _f32(fn, "u_next", u_next, batch)
+    _ids(fn, "accepted", accepted, batch)
+    _ids(fn, "next_token", next_token, batch)
+    if cu_seqlens is not None:
+        _ids(fn, "cu_seqlens", cu_seqlens, batch + 1)
+    status = _lib.fast().rssm_verify(
+        target.data_ptr(), st, _p(draft), sd, _DTYPE[dtype], vocab, tokens.data_ptr(), u.data_ptr(), u_next.data_ptr(),
+        _p(cu_seqlens), batch, T, ntok, accepted.data_ptr(), next_token.data_ptr(), _p(error_word), _s(stream, target))
+    if status:
+        raise RssmError(fn, status)
 
 
 def rssm_gated_norm(x, z, weight, out, group=None, eps=1e-5, norm_first=False, stream=None):
@@ -481,7 +474,7 @@ def rssm_gated_norm(x, z, weight, out, group=None, eps=1e-5, norm_first=False, s
     if weights != dim and weights != group:
         _refuse(fn, f"weight must hold {dim} or {group} values")
     _f32(fn, "weight", weight, 1)
-    status = _lib.load().rssm_gated_norm(x.data_ptr(), sx, z.data_ptr(), sz, _DTYPE[dtype], weight.data_ptr(),
+    status = _lib.fast().rssm_gated_norm(x.data_ptr(), sx, z.data_ptr(), sz, _DTYPE[dtype], weight.data_ptr(),
                                          int(weights != dim), rows, dim, group, eps, int(norm_first), out.data_ptr(), so,
                                          _s(stream, x))
     if status:
@@ -502,7 +495,7 @@ def rssm_residual_norm(x, residual, weight, out, residual_out, post_weight=None,
     for name, t in (("weight", weight), ("post_weight", post_weight), ("scale", scale)):
         if t is not None and (t.numel() != dim or t.dtype is not torch.float32 or not t.is_contiguous()):
             _refuse(fn, f"{name} must hold {dim} contiguous float32 values")
-    status = _lib.load().rssm_residual_norm(
+    status = _lib.fast().rssm_residual_norm(
         x.data_ptr(), sx, residual.data_ptr(), sr, _DTYPE[dtype], _DTYPE[rtype], _p(post_weight), _p(scale), alpha,
         weight.data_ptr(), rows, dim, eps, residual_out.data_ptr(), sro, out.data_ptr(), so, _s(stream, x))
     if status:

@@ -276,6 +276,11 @@ struct DeltaBlock {
   float kq;  // scale / |q_t|
 };
 
+// Scratch: counters of the steps' rows first, of a fixed number of rows, so that
+// no prompt's data reaches them whatever the sizes of the calls that share it.
+constexpr int kDeltaRows = 65536;
+constexpr size_t kDeltaHead = kDeltaRows * sizeof(unsigned);
+
 // host side
 bool delta_view(const rssm_delta_cache* c, DeltaCacheView* out, rssm_status* st);
 rssm_status delta_tokens(const DeltaCacheView& c, int dk, const void* q, const void* k, const void* v, int64_t q_stride,

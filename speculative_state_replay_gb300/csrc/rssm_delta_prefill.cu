@@ -942,8 +942,6 @@ cudaError_t launch_scan(DeltaPrefillArgs a, cudaStream_t st) {
                     dim3(kWorkWarps * 32 + 64), smem, st, a, mq, mk, mv);
 }
 
-size_t ticket_bytes(int batch) { return align_up(static_cast<size_t>(batch) * sizeof(unsigned) + 1, 256); }
-
 }  // namespace
 }  // namespace rssm
 
@@ -953,7 +951,7 @@ extern "C" size_t rssm_delta_scratch_bytes(const rssm_delta_cache* cache, int32_
   DeltaCacheView c;
   rssm_status st;
   if (!delta_view(cache, &c, &st) || batch < 0 || tokens < 0) return 0;
-  return ticket_bytes(batch) + static_cast<size_t>(tokens / kC + batch) * c.Hv * kUnit;
+  return kDeltaHead + static_cast<size_t>(tokens / kC + batch) * c.Hv * kUnit;
 }
 
 extern "C" rssm_status rssm_delta_prefill(const rssm_delta_cache* cache, const void* q, int64_t q_stride, const void* k,
@@ -978,7 +976,7 @@ extern "C" rssm_status rssm_delta_prefill(const rssm_delta_cache* cache, const v
   a.initial = initial;
   a.batch = batch;
   a.tokens = tokens;
-  a.units = static_cast<uint8_t*>(scratch) + ticket_bytes(batch);
+  a.units = static_cast<uint8_t*>(scratch) + kDeltaHead;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   // Value columns of a block.  A chunk's chain takes little longer for 64 than
   // for 32, so 32 only where the blocks then still run all at once.

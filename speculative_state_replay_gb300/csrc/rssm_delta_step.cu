@@ -402,7 +402,7 @@ extern "C" rssm_status rssm_delta_step(const rssm_delta_cache* cache, const void
   rssm_status st;
   if (!delta_view(cache, &a.c, &st)) return st;
   if (batch < 0 || T < 1 || tokens < 0) return RSSM_ERR_INVALID_ARGUMENT;
-  if (T > a.c.np) return RSSM_ERR_UNSUPPORTED;
+  if (T > a.c.np || batch > kDeltaRows) return RSSM_ERR_UNSUPPORTED;
   if (!cu_seqlens && tokens < static_cast<int64_t>(batch) * T) return RSSM_ERR_INVALID_ARGUMENT;
   if (batch == 0) return RSSM_OK;
   if (tokens > 0) {
@@ -411,7 +411,7 @@ extern "C" rssm_status rssm_delta_step(const rssm_delta_cache* cache, const void
   }
   if (!al(slot_idx, 4) || (accepted && !al(accepted, 4)) || (cu_seqlens && !al(cu_seqlens, 4)) || !al(scratch, 16))
     return RSSM_ERR_INVALID_ARGUMENT;
-  if (scratch_bytes < static_cast<size_t>(batch) * sizeof(unsigned)) return RSSM_ERR_SCRATCH_TOO_SMALL;
+  if (scratch_bytes < kDeltaHead) return RSSM_ERR_SCRATCH_TOO_SMALL;
   a.slot_idx = slot_idx;
   a.accepted = accepted;
   a.cu = cu_seqlens;

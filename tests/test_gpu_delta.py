@@ -333,3 +333,21 @@ def test_slots_past_32_bits(gen):
     api.rssm_delta_step(cache, *tk, slots, None, T, out, scratch, l2norm=True)
     close(out, delta_tokens(S0, *tk, dk**-0.5, True)[0])
     assert (cache.state[: S - 1].view(torch.int16).amax() == 0) and int(cache.error_word) == 0
+
+
+def test_scratch_is_shared_by_calls_of_other_sizes(gen):
+    """A small prompt between the steps of a larger batch, on one buffer: the steps' counters stay at zero."""
+    hk, hv, dk, dv, T, B = 1, 2, 64, 32, 2, 300
+    cache = api.DeltaCache(B + 1, hk, hv, dk, dv, T)
+    scratch = torch.zeros(max(api.rssm_delta_scratch_bytes(cache, B, B * T), api.rssm_delta_scratch_bytes(cache, 1, 500)),
+                          dtype=torch.uint8, device="cuda")
+    slots = torch.arange(1, B + 1, dtype=torch.int32, device="cuda")
+    acc = torch.zeros(B, dtype=torch.int32, device="cuda")
+    out = torch.empty(B * T, hv, dv, dtype=BF, device="cuda")
+    for step in range(3):
+        api.rssm_delta_step(cache, *tokens(B * T, hk, hv, dk, dv, gen), slots, acc, T, out, scratch, l2norm=True)
+        assert cache.pend[1:].tolist() == [[(step + 1) % 2, T]] * B
+        o = torch.empty(500, hv, dv, dtype=BF, device="cuda")
+        other = api.DeltaCache(2, hk, hv, dk, dv, T)
+        api.rssm_delta_prefill(other, *tokens(500, hk, hv, dk, dv, gen), slots[:1], cu_of([500], "cuda"), o, scratch, l2norm=True)
+    assert int(cache.error_word) == 0 and (scratch[: 4 * 65536] == 0).all()

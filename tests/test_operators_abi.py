@@ -129,3 +129,28 @@ def test_binding_checks():
         kw.update(bad)
         with pytest.raises(ValueError):
             api.rssm_residual_norm(**kw)
+
+
+def test_fast_calls_are_the_abi_calls(lib):
+    """The binding's C module makes the library's calls: the same statuses, and refuses what is no argument."""
+    f, p, c = _lib.fast(), 1 << 20, cache()
+    struct = c._obj
+    addr = ctypes.addressof(struct)
+    step_args = [addr, p, 256, p, 256, p, 256, p, p, 1.0, 1, p, p, None, 0, 4, 8, p, p, 1 << 20, 0]
+    assert f.rssm_delta_step(*step_args) == 0  # empty batch
+    step_args[14:16] = [2, 9]
+    assert f.rssm_delta_step(*step_args) == 2
+    step_args[14:16] = [2, 4]
+    step_args[1] = p + 2
+    assert f.rssm_delta_step(*step_args) == 1
+    prefill_args = [addr, p, 256, p, 256, p, 256, p, p, 1.0, 1, p, p, None, 2, 8, p, p, 8, 0]
+    assert f.rssm_delta_prefill(*prefill_args) == 3
+    assert f.rssm_verify(p, 100, p, 100, 0, 100, p, p, p, None, 2, 33, 99, p, p, None, 0) == 2
+    assert f.rssm_verify(p, 99, p, 100, 0, 100, p, p, p, None, 2, 3, 99, p, p, None, 0) == 1
+    assert f.rssm_gated_norm(p, 64, p, 64, 0, p, 0, 0, 64, 32, 1e-5, 0, p, 64, 0) == 0
+    assert f.rssm_gated_norm(p, 64, p, 64, 0, p, 0, 4, 64, 48, 1e-5, 0, p, 64, 0) == 1
+    assert f.rssm_residual_norm(p, 64, p, 64, 1, 0, None, None, 1.0, p, 0, 64, 1e-5, p, 64, p, 64, 0) == 0
+    assert f.rssm_residual_norm(p, 64, p, 64, 1, 2, None, None, 1.0, p, 4, 64, 1e-5, p, 64, p, 64, 0) == 1
+    for bad in (step_args[:-1], ["x"] + step_args[1:], step_args[:14] + [1 << 40] + step_args[15:], step_args[:9] + [None] + step_args[10:]):
+        with pytest.raises((TypeError, OverflowError)):
+            f.rssm_delta_step(*bad)
