@@ -631,10 +631,10 @@ __global__ void __launch_bounds__(kWorkWarps * 32 + 64, 1)
   tc_after();
   const uint32_t tm_s = tmem_base, tm_x = tm_s + 2 * NDV, tm_u = tm_s + 4 * NDV;
   const int chunks = (n + kC - 1) / kC;
-  // the chain is a few hundred cycles long between waits: poll before sleeping
+  // (polling with test_wait instead of try_wait, or by one lane for its warp, is slower: 618 and 639 us where this takes 602)
   const auto wait = [&](uint64_t* bar, uint32_t parity) {
-    for (int i = 0; i < 4096; ++i)
-      if (mbar_test(bar, parity)) return true;
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
     if (dead) return false;
     if (mbar_wait(bar, parity)) return true;
     dead = 1;
