@@ -126,35 +126,6 @@ struct DeltaRow {
       for (int y = 0; y < KS / 2; ++y) w[y] = *reinterpret_cast<const uint4*>(p + 32 * y);
     }
   }
-  // d = (keys; queries) times these rows, in short chains of products
-  __device__ __forceinline__ void product(const uint32_t (&a)[KS][4], float (&d)[4]) const {
-    float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (F32) {
-      float l0[4] = {0.f, 0.f, 0.f, 0.f}, l1[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int x = 0; x < KS; x += 2) {
-        uint32_t h[4], l[4];
-        split_bf16x2(s[x].x, h[0], l[0]);
-        split_bf16x2(s[x].y, h[1], l[1]);
-        split_bf16x2(s[x + 1].x, h[2], l[2]);
-        split_bf16x2(s[x + 1].y, h[3], l[3]);
-        mma_bf16(d0, a[x], h[0], h[1]);
-        mma_bf16(l0, a[x], l[0], l[1]);
-        mma_bf16(d1, a[x + 1], h[2], h[3]);
-        mma_bf16(l1, a[x + 1], l[2], l[3]);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) d[e] = (d0[e] + d1[e]) + (l0[e] + l1[e]);
-    } else {
-#pragma unroll
-      for (int y = 0; y < KS / 2; ++y) {
-        mma_bf16(d0, a[2 * y], w[y].x, w[y].y);
-        mma_bf16(d1, a[2 * y + 1], w[y].z, w[y].w);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) d[e] = d0[e] + d1[e];
-    }
-  }
   __device__ __forceinline__ void decay(float e) {
     const pair a = pack2(e, e);
 #pragma unroll
@@ -205,75 +176,130 @@ struct DeltaRow {
 
 // A block of up to 8 tokens, and the drafts that wait before it.  Lane (t =
 // lane / 4, c = lane % 4) has token t and, of pairs of tokens, j = 2c + {0, 1}.
+// Keys and queries stay in shared memory, rows of DK bf16 at kTokenRow<DK>
+// bytes, zeros past the last token, and come from there as the first operand of
+// two steps of 16 at a time: 8 loads an item for 32 registers less.
 template <int DK>
 struct DeltaBlock {
   static constexpr int KS = DK / 16;
-  uint32_t a[KS][4];  // first operand: rows 0-7 keys, rows 8-15 queries
-  float kk[4];        // k_t.k_j and q_t.k_j among the block's tokens, normalised and scaled
-  float wk[4];        // k_t.k_j and q_t.k_j with the waiting keys, times 1 / |k_t| and scale / |q_t|
-  float r;            // 1 / |k_t| (1 without normalisation)
+  const uint8_t *k, *q;  // this lane's part of its token's key and query
+  float kk[4];           // k_t.k_j and q_t.k_j among the block's tokens, normalised and scaled
+  float wk[4];           // k_t.k_j and q_t.k_j with the waiting keys, times 1 / |k_t| and scale / |q_t|
+  float r, kq;           // 1 / |k_t| and scale / |q_t| (1 and scale without normalisation)
 
-  // keys and queries in shared memory, rows of DK bf16 at kTokenRow<DK> bytes
-  __device__ __forceinline__ void load(const uint8_t* keys, const uint8_t* queries, int T, int lane) {
-    const int t = lane >> 2, cc = lane & 3;
-    const bool live = t < T;
-    const uint8_t *kp = keys + t * kTokenRow<DK> + 16 * cc, *qp = queries + t * kTokenRow<DK> + 16 * cc;
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-    for (int y = 0; y < KS / 2; ++y) {
-      const uint4 kw = live ? *reinterpret_cast<const uint4*>(kp + 64 * y) : zero;
-      const uint4 qw = live ? *reinterpret_cast<const uint4*>(qp + 64 * y) : zero;
-      a[2 * y][0] = kw.x;
-      a[2 * y][1] = qw.x;
-      a[2 * y][2] = kw.y;
-      a[2 * y][3] = qw.y;
-      a[2 * y + 1][0] = kw.z;
-      a[2 * y + 1][1] = qw.z;
-      a[2 * y + 1][2] = kw.w;
-      a[2 * y + 1][3] = qw.w;
-    }
+  __device__ __forceinline__ void set(const uint8_t* keys, const uint8_t* queries, int lane) {
+    const int at = (lane >> 2) * kTokenRow<DK> + 16 * (lane & 3);
+    k = keys + at;
+    q = queries + at;
+  }
+  // first operands of steps 2 y and 2 y + 1: rows 0-7 keys, rows 8-15 queries
+  __device__ __forceinline__ void operands(int y, uint32_t (&a)[4], uint32_t (&b)[4]) const {
+    const uint4 kw = *reinterpret_cast<const uint4*>(k + 64 * y), qw = *reinterpret_cast<const uint4*>(q + 64 * y);
+    a[0] = kw.x;
+    a[1] = qw.x;
+    a[2] = kw.y;
+    a[3] = qw.y;
+    b[0] = kw.z;
+    b[1] = qw.z;
+    b[2] = kw.w;
+    b[3] = qw.w;
   }
 
   // the Gram products, the same for every value head of the key head;
-  // `waiting`: the waiting keys, as `keys` of load()
+  // `waiting`: the waiting keys, laid out like the keys
   __device__ __forceinline__ void gram(const DeltaTokens& tk, const uint8_t* waiting, int acc, int lane) {
     const int t = lane >> 2, cc = lane & 3;
     const unsigned full = 0xffffffffu;
+    float qq[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 4; ++i) kk[i] = wk[i] = 0.0f;
 #pragma unroll
-    for (int x = 0; x < KS; ++x) mma_bf16(kk, a[x], a[x][0], a[x][2]);
-    if (acc > 0) {
-#pragma unroll
-      for (int y = 0; y < KS / 2; ++y) {
+    for (int y = 0; y < KS / 2; ++y) {
+      uint32_t a[4], b[4];
+      operands(y, a, b);
+      mma_bf16(kk, a, a[0], a[2]);
+      mma_bf16(kk, b, b[0], b[2]);
+      if (tk.l2norm) {
+        mma_bf16(qq, a, a[1], a[3]);
+        mma_bf16(qq, b, b[1], b[3]);
+      }
+      if (acc > 0) {
         const uint4 w = t < acc ? *reinterpret_cast<const uint4*>(waiting + t * kTokenRow<DK> + 16 * cc + 64 * y)
                                 : make_uint4(0u, 0u, 0u, 0u);
-        mma_bf16(wk, a[2 * y], w.x, w.y);
-        mma_bf16(wk, a[2 * y + 1], w.z, w.w);
+        mma_bf16(wk, a, w.x, w.y);
+        mma_bf16(wk, b, w.z, w.w);
       }
     }
-    float rq = tk.scale;
+    kq = tk.scale;
     r = 1.0f;
     if (tk.l2norm) {
-      float qq[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int x = 0; x < KS; ++x) mma_bf16(qq, a[x], a[x][1], a[x][3]);
       // the diagonal element (t, t) is in lane 4 t + t / 2, register t & 1
       const float dk = (t & 1) ? kk[1] : kk[0], dq = (t & 1) ? qq[3] : qq[2];
       r = rsqrtf(__shfl_sync(full, dk, t * 4 + (t >> 1)) + 1e-6f);
-      rq = tk.scale * rsqrtf(__shfl_sync(full, dq, t * 4 + (t >> 1)) + 1e-6f);
+      kq = tk.scale * rsqrtf(__shfl_sync(full, dq, t * 4 + (t >> 1)) + 1e-6f);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float rj = __shfl_sync(full, r, (2 * cc + i) * 4);
       kk[i] *= r * rj;
-      kk[2 + i] *= rq * rj;
+      kk[2 + i] *= kq * rj;
       wk[i] *= r;
-      wk[2 + i] *= rq;
+      wk[2 + i] *= kq;
     }
-    kq = rq;
   }
-  float kq;  // scale / |q_t|
+
+  // d[i] = (keys; queries) times rows i of the warp's state, in short chains of products
+  template <bool F32>
+  __device__ __forceinline__ void product(const DeltaRow<DK, F32> (&S)[2], float (&d)[2][4]) const {
+    float d1[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[i][e] = d1[i][e] = 0.0f;
+    if constexpr (F32) {
+      float l[2][4], l1[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) l[i][e] = l1[i][e] = 0.0f;
+#pragma unroll
+      for (int y = 0; y < KS / 2; ++y) {
+        uint32_t a[4], b[4];
+        operands(y, a, b);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t h[4], lo[4];
+          split_bf16x2(S[i].s[2 * y].x, h[0], lo[0]);
+          split_bf16x2(S[i].s[2 * y].y, h[1], lo[1]);
+          split_bf16x2(S[i].s[2 * y + 1].x, h[2], lo[2]);
+          split_bf16x2(S[i].s[2 * y + 1].y, h[3], lo[3]);
+          mma_bf16(d[i], a, h[0], h[1]);
+          mma_bf16(l[i], a, lo[0], lo[1]);
+          mma_bf16(d1[i], b, h[2], h[3]);
+          mma_bf16(l1[i], b, lo[2], lo[3]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[i][e] = (d[i][e] + d1[i][e]) + (l[i][e] + l1[i][e]);
+    } else {
+#pragma unroll
+      for (int y = 0; y < KS / 2; ++y) {
+        uint32_t a[4], b[4];
+        operands(y, a, b);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          mma_bf16(d[i], a, S[i].w[y].x, S[i].w[y].y);
+          mma_bf16(d1[i], b, S[i].w[y].z, S[i].w[y].w);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[i][e] += d1[i][e];
+    }
+  }
 };
 
 // Scratch: counters of the steps' rows first, of a fixed number of rows, so that

@@ -21,6 +21,9 @@ struct DeltaStepArgs {
 
 constexpr int kStepWarps = 4;
 constexpr int kStepRows = kStepWarps * 16;  // value rows of a tile
+// blocks an SM: 2-byte states 431 us with 4, 452 with 3 (1024 rows); fp32 states
+// keep 64 values a lane and spill with 4: 82 us, 54 with 3 (64 rows)
+constexpr int step_blocks(bool f32) { return f32 ? 3 : 4; }
 
 // A warp's item on its way from memory: its state rows (a bulk copy) and, for
 // this item and the next in turn, of the waiting drafts the corrections of these
@@ -55,7 +58,7 @@ static_assert(sizeof(StepWarp<64, false>::Small) % 16 == 0 && kTokenRow<64> % 16
 // for its next item's; it forms the new drafts' outputs and corrections, adds the
 // accepted drafts of the step before and writes the rows back if there were any.
 template <int DK, bool F32>
-__global__ void __launch_bounds__(kStepWarps * 32, 3) delta_step_kernel(const DeltaStepArgs a) {
+__global__ void __launch_bounds__(kStepWarps * 32, step_blocks(F32)) delta_step_kernel(const DeltaStepArgs a) {
   extern __shared__ __align__(128) uint8_t raw[];
   StepSmem<DK, F32>& sm = *reinterpret_cast<StepSmem<DK, F32>*>(raw);
   __shared__ int sh[2];
@@ -125,10 +128,14 @@ __global__ void __launch_bounds__(kStepWarps * 32, 3) delta_step_kernel(const De
     if (lane < 16 && (lane & 7) < n) cp_async4(lane < 8 ? &wm.x[x].g[lane] : &wm.x[x].beta[lane & 7], gp + h);
   };
   fetch(hv, r0, 0);
-  for (int i = tid; i < n * CH; i += kStepWarps * 32) {
-    const int r = i / CH, ch = i % CH;
-    cp_async16(sm.k + r * kTokenRow<DK> + ch * 16, a.tk.k + (tok0 + r) * a.tk.k_stride + hk * DK + ch * 8);
-    cp_async16(sm.q + r * kTokenRow<DK> + ch * 16, a.tk.q + (tok0 + r) * a.tk.q_stride + hk * DK + ch * 8);
+  for (int i = tid; i < kDeltaT * CH; i += kStepWarps * 32) {
+    const int r = i / CH, ch = i % CH, to = r * kTokenRow<DK> + ch * 16;
+    if (r < n) {
+      cp_async16(sm.k + to, a.tk.k + (tok0 + r) * a.tk.k_stride + hk * DK + ch * 8);
+      cp_async16(sm.q + to, a.tk.q + (tok0 + r) * a.tk.q_stride + hk * DK + ch * 8);
+    } else {
+      *reinterpret_cast<uint4*>(sm.k + to) = *reinterpret_cast<uint4*>(sm.q + to) = make_uint4(0u, 0u, 0u, 0u);
+    }
   }
   if (tid == 0) {
     const int2 p = __ldcg(reinterpret_cast<const int2*>(a.c.pend) + s);
@@ -178,14 +185,12 @@ __global__ void __launch_bounds__(kStepWarps * 32, 3) delta_step_kernel(const De
   cp_async_wait_all();
   __syncthreads();
   DeltaBlock<DK> blk;
-  blk.load(sm.k, sm.q, n, lane);
+  blk.set(sm.k, sm.q, lane);
   blk.gram(a.tk, sm.pk, acc, lane);
   if (item0 == 0 && warp == 0 && live) {  // the new drafts wait in the other half
     uint16_t* pk = a.c.pend_k + s * a.c.pend_k_stride + ((static_cast<long long>(to) * a.c.Hk + hk) * np + t) * DK + 8 * cc;
 #pragma unroll
-    for (int y = 0; y < DK / 32; ++y)
-      *reinterpret_cast<uint4*>(pk + 32 * y) =
-          make_uint4(blk.a[2 * y][0], blk.a[2 * y][2], blk.a[2 * y + 1][0], blk.a[2 * y + 1][2]);
+    for (int y = 0; y < DK / 32; ++y) *reinterpret_cast<uint4*>(pk + 32 * y) = *reinterpret_cast<const uint4*>(blk.k + 64 * y);
   }
   float* nw = a.c.pend_w + s * a.c.pend_w_stride + static_cast<long long>(to * Hv * np + t) * dv + 2 * cc;
   float* nc = a.c.pend_c + s * a.c.pend_c_stride + to * Hv * np + t;
@@ -268,16 +273,15 @@ __global__ void __launch_bounds__(kStepWarps * 32, 3) delta_step_kernel(const De
       }
     }
     const float fk = E * blk.r, fq = E * blk.kq, be = beta * ec;
-    float u[2][2], o[2][2];
+    float u[2][2], o[2][2], d[2][4];
+    blk.product(S, d);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float d[4];
-      S[i].product(blk.a, d);
       const uint32_t vw = live ? *reinterpret_cast<const uint32_t*>(&x.v[t][8 * i + 2 * cc]) : 0u;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        u[i][e] = fmaf(-be, fmaf(fk, d[e], wu[i][e]), beta * (e ? bf16hi(vw) : bf16lo(vw)));
-        o[i][e] = ec * fmaf(fq, d[2 + e], wo[i][e]);
+        u[i][e] = fmaf(-be, fmaf(fk, d[i][e], wu[i][e]), beta * (e ? bf16hi(vw) : bf16lo(vw)));
+        o[i][e] = ec * fmaf(fq, d[i][2 + e], wo[i][e]);
       }
     }
     if (acc > 0) {
@@ -423,10 +427,10 @@ extern "C" rssm_status rssm_delta_step(const rssm_delta_cache* cache, const void
   a.items = a.c.rep * a.tiles;
   // Items a block takes: all of a (row, key head)'s for as many whole waves of
   // blocks as there are -- what the items share is worth more than the spread
-  // (64 rows of 16 key heads with 4 items, fp32: 1 an item 82 us, 4 an item 61
-  // us) -- and of the rest as few as give one more wave, so that it does not
+  // (64 rows of 16 key heads with 4 items, fp32: 82 us with 1 item a block, 61
+  // with 4) -- and of the rest as few as give one more wave, so that it does not
   // take as long as a whole one (55 us).
-  const long long wave = 3ll * num_sms(), units = static_cast<long long>(batch) * a.c.Hk;
+  const long long wave = static_cast<long long>(step_blocks(a.c.dtype == RSSM_F32)) * num_sms(), units = static_cast<long long>(batch) * a.c.Hk;
   if (wave == 0) return RSSM_ERR_CUDA;
   if (units * a.items > 0x7fffffffll) return RSSM_ERR_UNSUPPORTED;
   a.whole = static_cast<int>(units / wave * wave);
