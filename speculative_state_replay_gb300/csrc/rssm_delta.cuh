@@ -25,6 +25,7 @@
 #pragma once
 
 #include "rssm_device.cuh"
+#include "rssm_host.h"
 
 namespace rssm {
 

@@ -105,10 +105,6 @@ __device__ __forceinline__ void bulk_g2s(void* smem_dst, const void* gmem_src, u
       "l"(gmem_src), "r"(bytes), "r"(smem_addr(bar))
       : "memory");
 }
-// hint: bring `bytes` (a multiple of 16, 16-byte aligned) at `src` into L2
-__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
-}
 // Per-thread asynchronous copies global -> shared (16 bytes through L2 only,
 // or 4 bytes), all of a thread's copies completed by cp_async_wait_all().
 __device__ __forceinline__ void cp_async16(void* smem_dst, const void* gmem_src) {

@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "rssm.h"
+#include "rssm_host.h"
 #include "rssm_internal.h"
 
 namespace rssm {

@@ -128,8 +128,6 @@ struct InitArgs {
   unsigned long long seed;
 };
 
-int num_sms();  // SMs a persistent grid is sized for (rssm_host.cu); 0: no device
-
 __host__ __device__ inline int ring_pad(int L) { return (L + 3) & ~3; }
 inline int t_pad(int T) { return T <= 4 ? 4 : 8; }
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }

@@ -97,6 +97,11 @@ __host__ __device__ inline ReadLayout read_layout(int dtype, int TP, int ns, int
   return f;
 }
 
+// hint: bring `bytes` (a multiple of 16, 16-byte aligned) at `src` into L2
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int c0, int c1, int c2,
                                             uint64_t* bar) {
   asm volatile(

@@ -3,6 +3,7 @@
 #include <cooperative_groups.h>
 
 #include "rssm_device.cuh"
+#include "rssm_host.h"
 
 namespace cg = cooperative_groups;
 
