@@ -95,41 +95,52 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 // or 1 at the draft's token (certain drafts), or nothing.  Pieces of VEC values
 // start on 16 bytes of p's row: positions j are counted from `off` values
 // before its first, so that rows of any alignment are read 16 bytes a lane.
+// A row of q with another alignment (an odd vocabulary's) is read 16 bytes a
+// lane as well, and a piece cut out of the two that hold it (94 rows of 15635
+// fp16 values and their drafts': 11.9 us, value by value 16.8).
 template <typename P>
 struct Residual {
   static constexpr int VEC = 16 / sizeof(P);
   const P* p;
   const P* q;
   int token, vocab, off;
-  bool q_same;  // q's row has p's alignment
+  Weight certain;  // the target's weight at `token`
+  int skew;  // values of q's 16 bytes before a piece: 0 if q's row has p's alignment
 
-  __device__ __forceinline__ void set(const P* target, const P* draft, int tok, int v) {
+  __device__ __forceinline__ void set(const P* target, const P* draft, int tok, float at_tok, int v) {
     p = target;
     q = draft;
     token = tok;
+    certain.add(__saturatef(at_tok));
     vocab = v;
     off = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(P));
-    q_same = q && (reinterpret_cast<uintptr_t>(q) & 15u) == (reinterpret_cast<uintptr_t>(p) & 15u);
+    skew = q ? static_cast<int>((reinterpret_cast<uintptr_t>(q - off) & 15u) / sizeof(P)) : 0;
   }
-  // a value of the distribution: NaN and what is negative are 0, at most 1
-  __device__ __forceinline__ float at(int i) const {
-    return __saturatef(prob<P>(p[i]) - (q ? prob<P>(q[i]) : (i == token ? 1.0f : 0.0f)));
+  // the target's row without anything taken off
+  __device__ __forceinline__ void alone() {
+    q = nullptr;
+    token = -1;
+    skew = 0;
   }
-  // weight of the piece at position j, any of it past the row's ends left out
-  __device__ __forceinline__ Weight piece(int j) const {
-    Weight w;
+  // weights of the piece at position j, value by value: what lies past the
+  // row's ends is 0, as NaN and what is negative are; at most 1
+  __device__ __forceinline__ void values(int j, float (&r)[VEC]) const {
     const int i = j - off;
-    for (int e = max(i, 0); e < min(i + VEC, vocab); ++e) w.add(at(e));
-    return w;
+    P x[VEC], y[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const bool in = static_cast<unsigned>(i + e) < static_cast<unsigned>(vocab);
+      x[e] = in ? p[i + e] : P(0.0f);
+      y[e] = in && q ? q[i + e] : P(i + e == token ? 1.0f : 0.0f);
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) r[e] = __saturatef(prob<P>(x[e]) - prob<P>(y[e]));
   }
-  // whether the 32 pieces from position j on can be read as they are
+  // whether the 32 pieces from position j on can be read 16 bytes a lane: all of
+  // them (and of what lies around q's) is in the row
   __device__ __forceinline__ bool plain(int j) const {
     const int i = j - off;
-    return i >= 0 && i + 32 * VEC <= vocab && static_cast<unsigned>(token - i) >= 32u * VEC && (!q || q_same);
-  }
-  __device__ __forceinline__ void load(int j, uint4& a, uint4& c) const {
-    a = __ldcs(reinterpret_cast<const uint4*>(p + (j - off)));
-    if (q) c = __ldcs(reinterpret_cast<const uint4*>(q + (j - off)));
+    return i >= skew && i + 32 * VEC + (skew ? VEC - skew : 0) <= vocab;
   }
   __device__ __forceinline__ void add(Weight& w, const uint4& a, const uint4& c) const {
     const P *x = reinterpret_cast<const P*>(&a), *y = reinterpret_cast<const P*>(&c);
@@ -142,47 +153,90 @@ struct Residual {
       for (int e = 0; e < VEC; e += 2) w.add(__saturatef(prob<P>(x[e])), __saturatef(prob<P>(x[e + 1])));
     }
   }
-  // weights of the lane's pieces of N steps, `gap` positions apart: their loads first, then the sums
-  template <int N>
-  __device__ __forceinline__ void steps(Weight (&w)[N], int j, int gap, int lane, int end) const {
-    bool all = true;
+  // the 16 bytes that start `skew` values into lo, hi
+  __device__ __forceinline__ uint4 cut(const uint4& lo, const uint4& hi) const {
+    const int bytes = skew * static_cast<int>(sizeof(P));
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-    for (int x = 0; x < N; ++x) all = all && plain(j + x * gap);
-    if (all) {
-      uint4 a[N], c[N];
+    for (int k = 0; k < 6; ++k) w[k] = bytes & 8 ? w[k + 2] : w[k];
 #pragma unroll
-      for (int x = 0; x < N; ++x) load(j + x * gap + lane * VEC, a[x], c[x]);
+    for (int k = 0; k < 5; ++k) w[k] = bytes & 4 ? w[k + 1] : w[k];
+    const int bits = bytes % 4 * 8;
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+  }
+  __device__ __forceinline__ static uint4 read(const P* at) { return __ldcs(reinterpret_cast<const uint4*>(at)); }
+  // Weights of the lane's pieces of four steps that are `gap` positions apart:
+  // their loads first, then the sums; where the row ends, one step at a time.
+  __device__ __forceinline__ void steps(Weight (&w)[4], int j, int gap, int lane, int end) const {
+    const int i = j - off + lane * VEC;
+    const bool all = j + 3 * gap < end && plain(j) && plain(j + 3 * gap);
+    if (all && skew == 0) {
+      uint4 a[4], c[4];
 #pragma unroll
-      for (int x = 0; x < N; ++x) add(w[x], a[x], c[x]);
-    } else {
+      for (int x = 0; x < 4; ++x) {
+        a[x] = read(p + i + x * gap);
+        if (q) c[x] = read(q + i + x * gap);
+      }
 #pragma unroll
-      for (int x = 0; x < N; ++x) {
-        const int k = j + x * gap;
-        if (k >= end) continue;
-        if (plain(k)) {
-          uint4 a, c;
-          load(k + lane * VEC, a, c);
-          add(w[x], a, c);
-        } else {
-          w[x].add(piece(k + lane * VEC));
+      for (int x = 0; x < 4; ++x) add(w[x], a[x], c[x]);
+    } else if (all) {
+#pragma unroll
+      for (int x0 = 0; x0 < 4; x0 += 2) {
+        uint4 a[2], lo[2], hi[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const P* at = q + i + (x0 + x) * gap - skew;
+          a[x] = read(p + i + (x0 + x) * gap);
+          lo[x] = *reinterpret_cast<const uint4*>(at);
+          hi[x] = *reinterpret_cast<const uint4*>(at + VEC);
         }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) add(w[x0 + x], a[x], cut(lo[x], hi[x]));
+      }
+    } else {
+#pragma unroll 1
+      for (int x = 0; x < 4; ++x) {
+        const int k = j + x * gap;
+        if (k >= end) break;
+        Weight v;
+        if (skew == 0 && plain(k)) {
+          const uint4 a = read(p + i + x * gap);
+          add(v, a, q ? read(q + i + x * gap) : a);
+        } else {
+          float r[VEC];
+          values(k + lane * VEC, r);
+#pragma unroll
+          for (int e = 0; e < VEC; e += 2) v.add(r[e], r[e + 1]);
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          if (y == x) w[y].add(v);
       }
     }
+  }
+  // what to take off the lane's weight of the step at position j that holds a
+  // certain draft's token, whose weight is 0: steps() does not look for it
+  // where it reads 16 bytes a lane
+  __device__ __forceinline__ unsigned long long taken(int j, int lane) const {
+    const bool mine = static_cast<unsigned>(token - (j - off + lane * VEC)) < static_cast<unsigned>(VEC);
+    return token >= 0 && mine && plain(j) ? certain.value() : 0ull;
   }
 };
 
 // One cluster per row.  The row's tests come from single values; then the one
 // row of the target (and of the draft) the next token is drawn from is read
 // once, a part per block and warp, and summed in 64 bits; the sums of a
-// warp's 8 runs stay in its lanes, so the warp that holds the drawn mass finds
+// warp's 8 runs are kept lane by lane, so the warp that holds the drawn mass finds
 // the run, then the piece and the value, from them and a second look at that
 // run alone.
 template <typename P>
 __global__ void __launch_bounds__(kVerifyThreads, kVerifyBlocks) verify_kernel(const VerifyArgs a) {
   constexpr int VEC = Residual<P>::VEC, kStep = 32 * VEC;
-  __shared__ unsigned long long part[kVerifyWarps];
+  __shared__ unsigned long long part[kVerifyWarps], runs[kRuns][kVerifyThreads];
   __shared__ unsigned long long sums[2][kMaxParts];
-  __shared__ int sh_count, sh_bad;
+  __shared__ int sh_count, sh_bad, sh_token;
+  __shared__ float sh_p;
   cg::cluster_group cl = cg::this_cluster();
   const int parts = cl.num_blocks(), rank = cl.block_rank();
   const int b = blockIdx.x / parts;
@@ -204,24 +258,32 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyBlocks) verify_kernel(c
   }
   const P* target = static_cast<const P*>(a.target);
   const P* draft = static_cast<const P*>(a.draft);
+  const float u_next = a.u_next[b];
   if (warp == 0) {
     // draft t is tested against the target's probabilities after token t - 1
     bool pass = lane == 0, bad = false;
+    int tok = -1;
+    float p = 0.0f;
     if (lane > 0 && lane < n) {
-      const int tok = a.tokens[tok0 + lane];
+      tok = a.tokens[tok0 + lane];
       const float u = a.u[tok0 + lane];
       bad = tok < 0 || tok >= a.vocab;
       if (!bad) {
-        const float p = prob<P>(target[(tok0 + lane - 1) * a.target_stride + tok]);
+        p = prob<P>(target[(tok0 + lane - 1) * a.target_stride + tok]);
         const float q = draft ? prob<P>(draft[(tok0 + lane) * a.draft_stride + tok]) : 1.0f;
         pass = __fmul_rn(u, q) < p;
       }
     }
     const unsigned failed = ~__ballot_sync(0xffffffffu, pass);
     const unsigned any_bad = __ballot_sync(0xffffffffu, bad);
+    const int count = failed ? __ffs(failed) - 1 : 32;
     if (lane == 0) {
-      sh_count = failed ? __ffs(failed) - 1 : 32;
+      sh_count = count;
       sh_bad = any_bad != 0u;
+    }
+    if (lane == count) {
+      sh_token = tok;
+      sh_p = p;
     }
   }
   __syncthreads();
@@ -229,27 +291,30 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyBlocks) verify_kernel(c
   Residual<P> res;
   res.set(target + (tok0 + count - 1) * a.target_stride,
           draft && count < n ? draft + (tok0 + count) * a.draft_stride : nullptr,
-          !draft && count < n ? a.tokens[tok0 + count] : -1, a.vocab);
+          !draft && count < n ? sh_token : -1, !draft && count < n ? sh_p : 0.0f, a.vocab);
   if (rank == 0 && threadIdx.x == 0 && sh_bad) set_error(a.err, RSSM_ERRBIT_TOKEN);
 
   // a warp's part: kRuns runs of `len` steps of 32 pieces
   const int len = (a.vocab + res.off + parts * kVerifyWarps * kRuns * kStep - 1) / (parts * kVerifyWarps * kRuns * kStep);
   const int span = kRuns * len * kStep, first = (rank * kVerifyWarps + warp) * span, end = a.vocab + res.off;
   unsigned long long total = 0, before = 0;
-  Weight run[kRuns / 4][4];
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
-#pragma unroll
-    for (int r = 0; r < kRuns; ++r) run[r / 4][r % 4] = Weight();
-    if (first < end) {
-#pragma unroll 1
-      for (int k = 0; k < len; ++k)
-#pragma unroll
-        for (int r = 0; r < kRuns / 4; ++r) res.steps(run[r], first + (4 * r * len + k) * kStep, len * kStep, lane, end);
-    }
     unsigned long long w = 0;
+    const int place = res.token + res.off - first, held = place / kStep;  // the part's step that holds a certain token
+    const unsigned long long off = place >= 0 && place < span ? res.taken(first + held * kStep, lane) : 0ull;
+#pragma unroll 1
+    for (int r = 0; r < kRuns; r += 4) {
+      Weight run[4];
+#pragma unroll 1
+      for (int k = 0; k < len; ++k) res.steps(run, first + (r * len + k) * kStep, len * kStep, lane, end);
 #pragma unroll
-    for (int r = 0; r < kRuns; ++r) w += run[r / 4][r % 4].value();
+      for (int x = 0; x < 4; ++x) {
+        const unsigned long long y = run[x].value() - (held / len == r + x ? off : 0ull);
+        runs[r + x][threadIdx.x] = y;
+        w += y;
+      }
+    }
     w = warp_sum(w);
     if (lane == 0) part[warp] = w;
     __syncthreads();
@@ -275,8 +340,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyBlocks) verify_kernel(c
     }
     if (total || (!res.q && res.token < 0)) break;
     // nothing left of the target above the draft: draw from the target itself
-    res.q = nullptr;
-    res.token = -1;
+    res.alone();
     __syncthreads();
   }
   if (total == 0) {
@@ -288,7 +352,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyBlocks) verify_kernel(c
     return;
   }
   // floor(total * u) with u in 24 bits
-  const unsigned long long u24 = static_cast<unsigned long long>(__float2ll_rz(fminf(fmaxf(a.u_next[b], 0.0f), 0.99999994f) * 16777216.0f));
+  const unsigned long long u24 = static_cast<unsigned long long>(__float2ll_rz(fminf(fmaxf(u_next, 0.0f), 0.99999994f) * 16777216.0f));
   const unsigned long long aim = (total >> 24) * u24 + (((total & 0xffffffull) * u24) >> 24);
   for (int x = 0; x < warp; ++x) before += part[x];
   if (aim < before || aim >= before + part[warp]) return;
@@ -298,7 +362,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyBlocks) verify_kernel(c
   bool found = false;
 #pragma unroll
   for (int r = 0; r < kRuns; ++r) {
-    const unsigned long long w = warp_sum(run[r / 4][r % 4].value());
+    const unsigned long long w = warp_sum(runs[r][threadIdx.x]);
     if (!found) {
       if (left < w) {
         found = true;
@@ -314,7 +378,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyBlocks) verify_kernel(c
     res.steps(part4, at + k0 * kStep, kStep, lane, min(end, at + len * kStep));
     unsigned long long own[4];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) own[x] = part4[x].value();
+    for (int x = 0; x < 4; ++x) own[x] = part4[x].value() - (k0 + x < len ? res.taken(at + (k0 + x) * kStep, lane) : 0ull);
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       const unsigned long long all = warp_sum(own[x]);
@@ -330,17 +394,19 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyBlocks) verify_kernel(c
       }
       unsigned long long base = upto - own[x];
       if (left >= base && left < upto) {
-        const int i0 = at + (k0 + x) * kStep + lane * VEC - res.off;
-        for (int i = max(i0, 0); i < min(i0 + VEC, a.vocab); ++i) {
+        const int j = at + (k0 + x) * kStep + lane * VEC;
+        float r[VEC];
+        res.values(j, r);
+        int e = 0;  // the first value whose running sum passes `left`; the piece's last one does
+#pragma unroll
+        for (int y = 0; y < VEC; ++y) {
           Weight w;
-          w.add(res.at(i));
+          w.add(r[y]);
           base += w.value();
-          if (left < base) {
-            a.accepted[b] = count;
-            a.next[b] = i;
-            break;
-          }
+          e += left >= base;
         }
+        a.accepted[b] = count;
+        a.next[b] = j - res.off + e;
       }
       return;
     }

@@ -100,6 +100,49 @@ def test_nothing_left_and_odd_values():
     check([2] * 6, 2, target, None, tokens, u, un, err=api.ERRBIT_TOKEN)
 
 
+@pytest.mark.parametrize("left", [True, False])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_rows_of_two_alignments(dtype, left):
+    """Long rows of the draft that start elsewhere in 16 bytes than the target's, with and without anything left above
+    them."""
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    V, B = 20011, 3
+    target, draft, tokens, u, un = inputs(gen, [2] * B, V, dtype)
+    if not left:
+        draft[1::2] = target[::2]
+        tokens[1::2] = torch.tensor([0, 9999, V - 1], dtype=torch.int32, device="cuda")
+        draft[1::2].scatter_(1, tokens[1::2, None].long(), 2.0)
+    u[1::2] = 0.999999
+    n = 16 // target.element_size()
+    first = None
+    for shift in range(n):
+        wide = torch.full((2 * B, V + n + (-V) % n), 0.5, dtype=dtype, device="cuda")
+        wide[:, shift : shift + V] = draft
+        got = check([2] * B, 2, target, wide[:, shift : shift + V], tokens, u, un)
+        first = first or got
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+
+
+@pytest.mark.parametrize("rows", [1, 200])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_certain_token_anywhere(dtype, rows):
+    """A lookup's rejected token holds half of the target's mass, which is not drawn, wherever in the row it stands."""
+    gen = torch.Generator(device="cuda").manual_seed(13)
+    V = 17001
+    places = [0, 1, 7, 8, 127, 128, 255, 256, 1023, 1024, 2047, 2048, 4100, 8191, 8192, 12345, V - 2, V - 1]
+    base = torch.softmax(torch.randn(rows * 2, V, generator=gen, device="cuda"), -1) * 0.5
+    tokens = torch.tensor([places[b // 2 % len(places)] for b in range(2 * rows)], dtype=torch.int32, device="cuda")
+    un = torch.rand(rows, generator=gen, device="cuda")
+    u = torch.full((2 * rows,), 0.999, device="cuda")
+    for i in range(len(places) if rows == 1 else 1):
+        if rows == 1:
+            tokens[:] = places[i]
+        target = base.clone()
+        target.scatter_(1, tokens[:, None].long(), 0.5)
+        accepted, nxt = check([2] * rows, 2, target.to(dtype), None, tokens, u, un)
+        assert int(accepted.max()) == 1 and not (nxt == tokens[1::2]).any()
+
+
 def test_strides_alignment_and_bounds():
     gen = torch.Generator(device="cuda").manual_seed(9)
     V = 5001
