@@ -152,9 +152,11 @@ struct GatedNormArgs {
 // A team of lanes (TEAM of a warp, or a block) per (row, group), the group's
 // values in NV vectors a lane; IT groups one after another, their loads first
 // (short groups: a lane would have two loads on their way otherwise).  NV 0:
-// groups too long for that, read twice.
+// groups too long for that, read twice.  Where a lane has four vectors at a time
+// registers are for four blocks of 256: groups of 1000 (bf16, 46 M values) take
+// 44 us, 54 with two blocks.
 template <typename E, int VEC, int TEAM, int NV, int IT>
-__global__ void __launch_bounds__(TEAM == 0 ? 1024 : 256) gated_norm_kernel(const GatedNormArgs a) {
+__global__ void __launch_bounds__(TEAM == 0 ? 1024 : 256, NV * IT == 4 && TEAM != 0 ? 4 : 1) gated_norm_kernel(const GatedNormArgs a) {
   __shared__ float sh[32];
   pdl_wait();
   pdl_trigger();
@@ -195,17 +197,18 @@ __global__ void __launch_bounds__(TEAM == 0 ? 1024 : 256) gated_norm_kernel(cons
       const unsigned row = row_of(item < a.items ? item : 0, grp);
       E* out = static_cast<E*>(a.out) + row * a.out_stride + grp * a.group;
       const float* w = a.w + grp * a.w_group;
-      float fx[NV][VEC], fz[NV][VEC], sum = 0.0f;
+      float fx[NV][VEC], sum = 0.0f;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         rx[it][v].floats(fx[v]);
-        rz[it][v].floats(fz[v]);
+        if (!a.norm_first) {
+          float fz[VEC];
+          rz[it][v].floats(fz);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          fz[v][e] = silu(fz[v][e]);
-          if (!a.norm_first) fx[v][e] *= fz[v][e];
-          sum = fmaf(fx[v][e], fx[v][e], sum);
+          for (int e = 0; e < VEC; ++e) fx[v][e] *= silu(fz[e]);
         }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sum = fmaf(fx[v][e], fx[v][e], sum);
       }
       sum = team_sum<TEAM>(sum, sh);
       const float r = rsqrtf(sum / a.group + a.eps);
@@ -216,9 +219,12 @@ __global__ void __launch_bounds__(TEAM == 0 ? 1024 : 256) gated_norm_kernel(cons
           float fw[VEC];
           load_weight<VEC>(w + i, fw);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            fw[e] *= fx[v][e] * r;
-            if (a.norm_first) fw[e] *= fz[v][e];
+          for (int e = 0; e < VEC; ++e) fw[e] *= fx[v][e] * r;
+          if (a.norm_first) {
+            float fz[VEC];
+            rz[it][v].floats(fz);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) fw[e] *= silu(fz[e]);
           }
           store_vec<E, VEC>(out + i, fw);
         }
@@ -271,11 +277,15 @@ struct ResidualNormArgs {
 };
 
 // A block per row, the row's values in NV vectors a thread; NV 0: rows too long
-// for that, read once per sum and once more to write.  (Blocks that go through
-// rows with the next one's loads on their way are slower, 103 us for 92: they
-// hold more registers, and two fit an SM instead of three.)
+// for that, read once per sum and once more to write.  Several small blocks an
+// SM keep loads on their way while others wait for their two sums: rows of 8192
+// (bf16, fp32 residual, 42 M values) take 78 us with 256 threads of 4 vectors,
+// 83 with 512 of 2 and 102 with 1024 of one; 80 registers a thread are for three
+// blocks of 256 (83 us with 88).  Blocks that go through rows with the next
+// one's loads on their way took 103 us.
+constexpr int residual_regs(int vec, int nv) { return nv == 1 ? 32 : nv == 4 && vec == 8 ? 80 : 64; }
 template <typename E, typename R, int VEC, int NV>
-__global__ void __launch_bounds__(1024) residual_norm_kernel(const ResidualNormArgs a) {
+__global__ void __maxnreg__(residual_regs(VEC, NV)) residual_norm_kernel(const ResidualNormArgs a) {
   __shared__ float sh[64];
   pdl_wait();
   pdl_trigger();
@@ -288,8 +298,7 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const ResidualNormA
     E* out = static_cast<E*>(a.out) + row * a.out_stride;
     Raw<E, VEC> rx[NV];
     Raw<R, VEC> rr[NV];
-    float h[NV][VEC], f[NV][VEC];
-    float sum = 0.0f;
+    float h[NV][VEC], sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int i = (v * width + tid) * VEC;
@@ -301,17 +310,15 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const ResidualNormA
         rr[v].zero();
       }
     }
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      rx[v].floats(f[v]);
-      rr[v].floats(h[v]);
-    }
     float r = a.alpha;
     if (a.post) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
+      for (int v = 0; v < NV; ++v) {
+        float f[VEC];
+        rx[v].floats(f);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) sum = fmaf(f[v][e], f[v][e], sum);
+        for (int e = 0; e < VEC; ++e) sum = fmaf(f[e], f[e], sum);
+      }
       sum = team_sum<0>(sum, sh);
       r *= rsqrtf(sum / a.dim + a.eps);
       sum = 0.0f;
@@ -320,20 +327,22 @@ __global__ void __launch_bounds__(1024) residual_norm_kernel(const ResidualNormA
     for (int v = 0; v < NV; ++v) {
       const int i = (v * width + tid) * VEC;
       if (i < a.dim) {
-        float fw[VEC];
+        float f[VEC], fw[VEC];
+        rx[v].floats(f);
+        rr[v].floats(h[v]);
         if (a.post) {
           load_weight<VEC>(a.post + i, fw);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) f[v][e] *= fw[e];
+          for (int e = 0; e < VEC; ++e) f[e] *= fw[e];
         }
         if (a.scale) {
           load_weight<VEC>(a.scale + i, fw);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) f[v][e] *= fw[e];
+          for (int e = 0; e < VEC; ++e) f[e] *= fw[e];
         }
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          h[v][e] = fmaf(r, f[v][e], h[v][e]);
+          h[v][e] = fmaf(r, f[e], h[v][e]);
           sum = fmaf(h[v][e], h[v][e], sum);
         }
         store_vec<R, VEC>(res_out + i, h[v]);
@@ -429,7 +438,10 @@ cudaError_t launch_gated(const GatedNormArgs& a, cudaStream_t st) {
   if (vecs <= 64) return launch_teams<E, VEC, 32, 2>(a, st);
   if (vecs <= 128) return launch_teams<E, VEC, 32, 4>(a, st);
   const dim3 grid(a.items);
-  if (vecs <= 2048) return launch_pdl(gated_norm_kernel<E, VEC, 0, 2, 1>, grid, dim3((vecs + 63) / 64 * 32), 0, st, a);
+  // as few threads as hold the group in 4 vectors: several blocks an SM have
+  // loads on their way while one sums (5784 groups of 8192, bf16: 45 us with
+  // 256 threads, 58 with 512 of 2 vectors, 97 with 1024 of one)
+  if (vecs <= 4096) return launch_pdl(gated_norm_kernel<E, VEC, 0, 4, 1>, grid, dim3((vecs + 127) / 128 * 32), 0, st, a);
   return launch_pdl(gated_norm_kernel<E, VEC, 0, 0, 1>, grid, dim3(1024), 0, st, a);
 }
 
@@ -437,8 +449,11 @@ template <typename E, typename R, int VEC>
 cudaError_t launch_residual(const ResidualNormArgs& a, cudaStream_t st) {
   const int vecs = (a.dim + VEC - 1) / VEC;
   const dim3 grid(a.rows);
-  if (vecs <= 1024) return launch_pdl(residual_norm_kernel<E, R, VEC, 1>, grid, dim3((vecs + 31) / 32 * 32), 0, st, a);
-  if (vecs <= 2048) return launch_pdl(residual_norm_kernel<E, R, VEC, 2>, grid, dim3((vecs + 63) / 64 * 32), 0, st, a);
+  // blocks of 256 threads at most, where 4 vectors a thread hold the row
+  if (vecs <= 256) return launch_pdl(residual_norm_kernel<E, R, VEC, 1>, grid, dim3((vecs + 31) / 32 * 32), 0, st, a);
+  if (vecs <= 512) return launch_pdl(residual_norm_kernel<E, R, VEC, 2>, grid, dim3((vecs + 63) / 64 * 32), 0, st, a);
+  if (vecs <= (VEC == 8 ? 2048 : 4096))
+    return launch_pdl(residual_norm_kernel<E, R, VEC, 4>, grid, dim3((vecs + 127) / 128 * 32), 0, st, a);
   return launch_pdl(residual_norm_kernel<E, R, VEC, 0>, grid, dim3(1024), 0, st, a);
 }
 
