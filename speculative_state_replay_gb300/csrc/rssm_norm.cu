@@ -40,13 +40,23 @@ struct Elem<__half> {
 // VEC elements of type E, in 16-byte pieces (one element where VEC is 1): as
 // they come, as floats, and back.  Activations are read once (no L1 line is
 // kept for them: the weights' stay).
+using pair = unsigned long long;
+__device__ __forceinline__ uint32_t low(pair d) { return static_cast<uint32_t>(d); }
+__device__ __forceinline__ uint32_t high(pair d) { return static_cast<uint32_t>(d >> 32); }
 template <typename E, int VEC>
 struct Raw {
   static constexpr int W = VEC == 1 ? 1 : VEC * static_cast<int>(sizeof(E)) / 16;
   uint4 w[W];
-  __device__ __forceinline__ void load(const E* p) {
+  // wide: p is on 32 bytes, and they are read by one instruction (lanes that
+  // read 16 bytes 32 apart pass the L1 in twice as many)
+  __device__ __forceinline__ void load(const E* p, bool wide = false) {
     if constexpr (VEC == 1) {
       *reinterpret_cast<E*>(w) = *p;
+    } else if (W == 2 && wide) {
+      pair d[4];
+      asm volatile("ld.global.cs.v4.b64 {%0, %1, %2, %3}, [%4];" : "=l"(d[0]), "=l"(d[1]), "=l"(d[2]), "=l"(d[3]) : "l"(p));
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = make_uint4(low(d[2 * i]), high(d[2 * i]), low(d[2 * i + 1]), high(d[2 * i + 1]));
     } else {
 #pragma unroll
       for (int i = 0; i < W; ++i) w[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
@@ -81,9 +91,14 @@ __device__ __forceinline__ void load_vec(const E* p, float (&f)[VEC]) {
 }
 // weights: read by every row
 template <int VEC>
-__device__ __forceinline__ void load_weight(const float* p, float (&f)[VEC]) {
+__device__ __forceinline__ void load_weight(const float* p, float (&f)[VEC], bool wide = false) {
   if constexpr (VEC == 1) {
     f[0] = __ldg(p);
+  } else if (VEC == 8 && wide) {
+    pair d[4];
+    asm("ld.global.nc.v4.b64 {%0, %1, %2, %3}, [%4];" : "=l"(d[0]), "=l"(d[1]), "=l"(d[2]), "=l"(d[3]) : "l"(p));
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) f[i] = __uint_as_float(i & 1 ? high(d[i / 2 % 4]) : low(d[i / 2 % 4]));
   } else {
 #pragma unroll
     for (int i = 0; i < VEC; i += 4) {
@@ -96,9 +111,14 @@ __device__ __forceinline__ void load_weight(const float* p, float (&f)[VEC]) {
   }
 }
 template <typename E, int VEC>
-__device__ __forceinline__ void store_vec(E* p, const float (&f)[VEC]) {
+__device__ __forceinline__ void store_vec(E* p, const float (&f)[VEC], bool wide = false) {
   if constexpr (VEC == 1) {
     *p = Elem<E>::from(f[0]);
+  } else if (VEC * sizeof(E) == 32 && wide) {
+    pair d[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] = static_cast<pair>(__float_as_uint(f[(2 * i + 1) % VEC])) << 32 | __float_as_uint(f[2 * i % VEC]);
+    asm volatile("st.global.cs.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(p), "l"(d[0]), "l"(d[1]), "l"(d[2]), "l"(d[3]) : "memory");
   } else {
     constexpr int N = 16 / sizeof(E);
 #pragma unroll
@@ -274,6 +294,7 @@ struct ResidualNormArgs {
   unsigned rows;
   int dim;
   float alpha, eps;
+  bool wide;  // fp32 rows and weights are on 32 bytes
 };
 
 // A block per row, the row's values in NV vectors a thread; NV 0: rows too long
@@ -281,7 +302,9 @@ struct ResidualNormArgs {
 // SM keep loads on their way while others wait for their two sums: rows of 8192
 // (bf16, fp32 residual, 42 M values) take 78 us with 256 threads of 4 vectors,
 // 83 with 512 of 2 and 102 with 1024 of one; 80 registers a thread are for three
-// blocks of 256 (83 us with 88).  Blocks that go through rows with the next
+// blocks of 256 (83 us with 88).  fp32 rows and weights on 32 bytes are read and
+// written 32 bytes a lane, 76 us (with a post norm and a scale, 8192 rows of
+// 5120, 84 us where 16 bytes a lane take 88).  Blocks that go through rows with the next
 // one's loads on their way took 103 us.
 constexpr int residual_regs(int vec, int nv) { return nv == 1 ? 32 : nv == 4 && vec == 8 ? 80 : 64; }
 template <typename E, typename R, int VEC, int NV>
@@ -304,7 +327,7 @@ __global__ void __maxnreg__(residual_regs(VEC, NV)) residual_norm_kernel(const R
       const int i = (v * width + tid) * VEC;
       if (i < a.dim) {
         rx[v].load(x + i);
-        rr[v].load(res + i);
+        rr[v].load(res + i, a.wide);
       } else {
         rx[v].zero();
         rr[v].zero();
@@ -331,12 +354,12 @@ __global__ void __maxnreg__(residual_regs(VEC, NV)) residual_norm_kernel(const R
         rx[v].floats(f);
         rr[v].floats(h[v]);
         if (a.post) {
-          load_weight<VEC>(a.post + i, fw);
+          load_weight<VEC>(a.post + i, fw, a.wide);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) f[e] *= fw[e];
         }
         if (a.scale) {
-          load_weight<VEC>(a.scale + i, fw);
+          load_weight<VEC>(a.scale + i, fw, a.wide);
 #pragma unroll
           for (int e = 0; e < VEC; ++e) f[e] *= fw[e];
         }
@@ -345,7 +368,7 @@ __global__ void __maxnreg__(residual_regs(VEC, NV)) residual_norm_kernel(const R
           h[v][e] = fmaf(r, f[e], h[v][e]);
           sum = fmaf(h[v][e], h[v][e], sum);
         }
-        store_vec<R, VEC>(res_out + i, h[v]);
+        store_vec<R, VEC>(res_out + i, h[v], a.wide);
       }
     }
     sum = team_sum<0>(sum, sh + 32);
@@ -355,7 +378,7 @@ __global__ void __maxnreg__(residual_regs(VEC, NV)) residual_norm_kernel(const R
       const int i = (v * width + tid) * VEC;
       if (i < a.dim) {
         float fw[VEC];
-        load_weight<VEC>(a.w + i, fw);
+        load_weight<VEC>(a.w + i, fw, a.wide);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) fw[e] *= h[v][e] * s;
         store_vec<E, VEC>(out + i, fw);
@@ -417,6 +440,7 @@ __global__ void __maxnreg__(residual_regs(VEC, NV)) residual_norm_kernel(const R
 }
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool on32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 bool on4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 template <typename E, int VEC, int TEAM, int NV>
@@ -516,12 +540,14 @@ extern "C" rssm_status rssm_residual_norm(const void* x, int64_t x_stride, const
     return RSSM_ERR_INVALID_ARGUMENT;
   if (rows > 0x7fffffffll) return RSSM_ERR_UNSUPPORTED;
   ResidualNormArgs a = {x, residual, post_weight, scale, weight, residual_out, out, x_stride, residual_stride,
-                        residual_out_stride, out_stride, static_cast<unsigned>(rows), dim, alpha, eps};
+                        residual_out_stride, out_stride, static_cast<unsigned>(rows), dim, alpha, eps, false};
   const bool vec = on16(x) && on16(residual) && on16(residual_out) && on16(out) && on16(weight) && on16(post_weight) &&
                    on16(scale) && dim % V == 0 && x_stride % V == 0 && out_stride % V == 0 && residual_stride % V == 0 &&
                    residual_out_stride % V == 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool f32 = residual_dtype == RSSM_F32;
+  a.wide = vec && on32(weight) && on32(post_weight) && on32(scale) &&
+           (!f32 || (on32(residual) && on32(residual_out) && residual_stride % 8 == 0 && residual_out_stride % 8 == 0));
   const cudaError_t e = dtype == RSSM_F32    ? residual_of<float>(a, true, vec, st)
                         : dtype == RSSM_BF16 ? residual_of<__nv_bfloat16>(a, f32, vec, st)
                                              : residual_of<__half>(a, f32, vec, st);

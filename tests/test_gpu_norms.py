@@ -123,3 +123,43 @@ def test_stream_and_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[2])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("group", [255, 1025, 2047, 4001, 4097, 2056, 8200, 32768, 32776])
+def test_gated_norm_long_groups(group, dtype):
+    """Lengths on both sides of what a thread's vectors hold, odd ones value by value."""
+    gen = torch.Generator(device="cuda").manual_seed(group)
+    for rows, first in ((1, False), (5, True)):
+        x, z = rnd(gen, rows, 2 * group).to(dtype), (2.0 * rnd(gen, rows, 2 * group)).to(dtype)
+        w = 1.0 + 0.2 * rnd(gen, group)
+        out = torch.empty_like(x)
+        api.rssm_gated_norm(x, z, w, out, group, eps=1e-5, norm_first=first)
+        close(out, gated_norm(x, z, w, group, 1e-5, first), dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("shift", [0, 4, 8, 1])
+@pytest.mark.parametrize("dim", [1001, 2048, 4001, 8192, 16384, 16392])
+def test_residual_norm_alignment(dim, shift, dtype):
+    """fp32 residuals and weights on 32 bytes, on 16, and on neither, give the same rows."""
+    gen = torch.Generator(device="cuda").manual_seed(dim)
+    R = 3
+    x = rnd(gen, R, dim).to(dtype)
+    full = 2.0 * rnd(gen, R * (dim + 8))
+    vec = [1.0 + 0.2 * rnd(gen, dim) for _ in range(3)]
+    res = full[: R * dim].view(R, dim).contiguous()
+    w, post, scale = vec
+    want, rwant = torch.empty_like(x), torch.empty_like(res)
+    api.rssm_residual_norm(x, res, w, want, rwant, post_weight=post, scale=scale, alpha=0.7, eps=1e-5)
+    pad = torch.empty(R * dim + 16, device="cuda")
+    moved = pad[shift : shift + R * dim].view(R, dim).copy_(res)
+    wv = [torch.empty(dim + 16, device="cuda")[shift : shift + dim].copy_(v) for v in vec]
+    out, rout = torch.empty_like(x), torch.empty(R * dim + 16, device="cuda")[shift : shift + R * dim].view(R, dim)
+    api.rssm_residual_norm(x, moved, wv[0], out, rout, post_weight=wv[1], scale=wv[2], alpha=0.7, eps=1e-5)
+    h, o = residual_norm(x, res, w, post, scale, 0.7, 1e-5)
+    rms = o.pow(2).mean(-1, keepdim=True).sqrt()
+    for a, r in ((want, rwant), (out, rout)):
+        size = res.double().abs() + (h - res.double()).abs()
+        assert ((r.double() - h).abs() <= 4e-6 * size).all()
+        assert ((a.double() - o).abs() <= ULP[dtype] * o.abs() + 1e-5 * (o.abs() + rms) + 2.0**-24).all()
