@@ -37,12 +37,13 @@ struct Elem<__half> {
   }
 };
 
-// VEC elements of type E, in 16-byte pieces (one element where VEC is 1): as
-// they come, as floats, and back.  Activations are read once (no L1 line is
-// kept for them: the weights' stay).
 using pair = unsigned long long;
 __device__ __forceinline__ uint32_t low(pair d) { return static_cast<uint32_t>(d); }
 __device__ __forceinline__ uint32_t high(pair d) { return static_cast<uint32_t>(d >> 32); }
+
+// VEC elements of type E, in 16-byte pieces (one element where VEC is 1): as
+// they come, as floats, and back.  Activations are read once (no L1 line is
+// kept for them: the weights' stay).
 template <typename E, int VEC>
 struct Raw {
   static constexpr int W = VEC == 1 ? 1 : VEC * static_cast<int>(sizeof(E)) / 16;
