@@ -39,7 +39,7 @@ namespace rssm {
 namespace {
 
 constexpr int kC = 64;                   // tokens of a chunk
-constexpr int kImgHi = 128 * 128;        // bytes: T (64 rows), then P T (64 rows), rows of 64 bf16: the hi parts
+constexpr int kImgHi = 128 * 128;        // bytes: T (fp32 states: T - I; 64 rows), then P T (64 rows), rows of 64 bf16: the hi parts
 constexpr int kImg = 2 * kImgHi;         // and the lo parts
 constexpr int kVec = 1040;               // bytes: beta e^c r [64], e^{c_end-c} r [64], scale e^c rq [64], beta [64], e^{c_end}
 constexpr int kUnit = kImg + kVec;       // scratch of one (chunk, value head)
