@@ -27,7 +27,7 @@ struct VerifyArgs {
 };
 
 constexpr int kVerifyThreads = 256;
-constexpr int kVerifyBlocks = 4;  // an SM: 12 us where 3 take 15 (64 rows), 48 where 3 take 64 (512 rows)
+constexpr int kVerifyBlocks = 4;  // an SM: 3 took 15 us for 12 (64 rows) and 64 for 48 (512 rows, now 42)
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxParts = 8;  // blocks of a cluster (the portable most)
 constexpr int kRuns = 8;      // a warp's part of a row is summed in 8 runs
