@@ -21,7 +21,9 @@
 // with the same permutation).  The first operand's 16 rows are the 8 keys and
 // the 8 queries, so one instruction serves both products; the Gram products
 // come from the same registers.  2-byte states go into the products as they
-// are; fp32 states as bf16 hi + lo.
+// are; fp32 states as three bf16 parts, which is all 24 bits of them: u = v - S k
+// is what is left of values that the state predicts, and two parts (16 bits)
+// leave 2^-18 of |S| |k| in it.
 #pragma once
 
 #include "rssm_device.cuh"
@@ -105,6 +107,14 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(pair d) {
 __device__ __forceinline__ void split_bf16x2(pair d, uint32_t& h, uint32_t& l) {
   h = cvt_bf16x2(d);
   fma2(d, pack2(-1.0f, -1.0f), pack2(bf16lo(h), bf16hi(h)));  // the remainder, exact
+  l = cvt_bf16x2(d);
+}
+// and as three parts, whose sum is the value
+__device__ __forceinline__ void split_bf16x2(pair d, uint32_t& h, uint32_t& m, uint32_t& l) {
+  h = cvt_bf16x2(d);
+  fma2(d, pack2(-1.0f, -1.0f), pack2(bf16lo(h), bf16hi(h)));
+  m = cvt_bf16x2(d);
+  fma2(d, pack2(-1.0f, -1.0f), pack2(bf16lo(m), bf16hi(m)));
   l = cvt_bf16x2(d);
 }
 
@@ -269,14 +279,16 @@ struct DeltaBlock {
         operands(y, a, b);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          uint32_t h[4], lo[4];
-          split_bf16x2(S[i].s[2 * y].x, h[0], lo[0]);
-          split_bf16x2(S[i].s[2 * y].y, h[1], lo[1]);
-          split_bf16x2(S[i].s[2 * y + 1].x, h[2], lo[2]);
-          split_bf16x2(S[i].s[2 * y + 1].y, h[3], lo[3]);
+          uint32_t h[4], m[4], lo[4];
+          split_bf16x2(S[i].s[2 * y].x, h[0], m[0], lo[0]);
+          split_bf16x2(S[i].s[2 * y].y, h[1], m[1], lo[1]);
+          split_bf16x2(S[i].s[2 * y + 1].x, h[2], m[2], lo[2]);
+          split_bf16x2(S[i].s[2 * y + 1].y, h[3], m[3], lo[3]);
           mma_bf16(d[i], a, h[0], h[1]);
-          mma_bf16(l[i], a, lo[0], lo[1]);
+          mma_bf16(l[i], a, m[0], m[1]);
           mma_bf16(d1[i], b, h[2], h[3]);
+          mma_bf16(l1[i], b, m[2], m[3]);
+          mma_bf16(l[i], a, lo[0], lo[1]);
           mma_bf16(l1[i], b, lo[2], lo[3]);
         }
       }

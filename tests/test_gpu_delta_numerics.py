@@ -1,0 +1,63 @@
+"""The gated delta rule where fp32 arithmetic shows: states that need all of their 24 bits, strong decays in mid-step,
+decay factors by themselves, and a log decay that is NaN.
+
+Every bound below is derived in its test from the operations that the rule needs in fp32: a sum of n products is off by
+at most a few 2^-23 of the sum of their magnitudes (the tensor cores add 16 products at a time, four such sums one after
+another), an exponential by 2 units in the last place.
+"""
+import math
+
+import pytest
+import torch
+
+from operators_plain import delta_tokens
+from speculative_state_replay_gb300 import api
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+SHAPES = [(1, 1, 64, 16), (2, 4, 128, 64), (1, 3, 128, 80), (2, 2, 64, 256), (4, 8, 128, 128)]
+
+
+@pytest.fixture
+def gen():
+    return torch.Generator(device="cuda").manual_seed(20261207)
+
+
+def ones(*shape, dtype=BF):
+    return torch.ones(shape, dtype=dtype, device="cuda")
+
+
+def rnd(gen, *shape):
+    return torch.randn(shape, generator=gen, device="cuda")
+
+
+def off(x, ref):
+    return float((x.double() - ref.double()).norm() / ref.double().norm())
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+def test_step_takes_a_state_as_it_is(gen, shape):
+    """Values of 1 + 2^-10 + 2^-18 that all add up: the last bit is 2^-18 of S k.  One token, so that u = v - S k, which
+    is what is left of values that the state predicts.  S k is off by at most 5 2^-23 of sum |S k| (four sums of 16
+    products, two more additions), v and the subtraction by 2^-24 each: 2^-20 of it."""
+    hk, hv, dk, dv = shape
+    B = 3
+    cache = api.DeltaCache(B + 1, hk, hv, dk, dv, 1)
+    sign = torch.where(rnd(gen, hv, dk) > 0, 1.0, -1.0)
+    size = torch.exp2(torch.randint(-2, 3, (B + 1, hv, dv, 1), generator=gen, device="cuda").float())
+    cache.state.copy_((1.0 + 2.0**-10 + 2.0**-18) * size * sign[:, None, :])
+    k = (rnd(gen, B, hk, dk).abs() + 0.5).to(BF) * sign.view(hk, hv // hk, dk)[:, 0].to(BF)
+    for h in range(hv):  # value heads of one key head share its signs
+        cache.state[:, h] = cache.state[:, h].abs() * sign[h // (hv // hk) * (hv // hk)]
+    S = cache.state[1:].double()
+    kd = k.double().repeat_interleave(hv // hk, 1)
+    Sk = torch.einsum("bhvk,bhk->bhv", S, kd)
+    v = Sk.to(BF)
+    g, beta = torch.zeros(B, hv, device="cuda"), torch.ones(B, hv, device="cuda")
+    out = torch.empty(B, hv, dv, dtype=BF, device="cuda")
+    slots = torch.arange(1, B + 1, dtype=torch.int32, device="cuda")
+    api.rssm_delta_step(cache, k, k, v, g, beta, slots, None, 1, out, api.alloc_delta_scratch(cache, B, B))
+    u = v.double() - Sk
+    got = cache.pend_w[1:, 1, :, 0].double()
+    size = torch.einsum("bhvk,bhk->bhv", S.abs(), kd.abs())
+    assert ((got - u).abs() <= 2.0**-20 * size).all(), float(((got - u).abs() / size).max())
