@@ -478,7 +478,9 @@ rssm_status rssm_delta_step(const rssm_delta_cache *cache, const void *q, int64_
  * The gated delta rule over whole prompts: outputs of every token, and the
  * state after the last one in each row's slot (no drafts wait afterwards).
  * Arguments as in rssm_delta_step, and
- *   cu_seqlens [batch+1] i32: the prompts' bounds (any lengths, 0 too)
+ *   cu_seqlens [batch+1] i32: the prompts' bounds (any lengths, 0 too).  Rows whose
+ *           bounds are negative, fall or pass `tokens`, and rows that begin before
+ *           an earlier row's bound, are skipped (RSSM_ERRBIT_SEQLEN)
  *   initial [batch] i32 or NULL: nonzero rows start from their slot's state
  *           (a prompt that comes in parts), the others from zero
  * Drafts that wait in a slot are dropped.

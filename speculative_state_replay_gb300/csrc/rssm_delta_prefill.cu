@@ -55,12 +55,21 @@ struct DeltaPrefillArgs {
   uint8_t* units;  // scratch [chunk slot][Hv][kUnit]
 };
 
-// A prompt's chunks are in scratch from slot cu / 64 + b on: no two prompts
-// share a slot, and the last slot is below tokens / 64 + batch.
+// A prompt's chunks are in scratch from slot cu / 64 + b on: of bounds that never
+// fall no two prompts share a slot, and the last slot is below tokens / 64 +
+// batch.  Where bounds fall, a row that begins before an earlier bound is skipped
+// (begins_inside), so that what is left of them never falls either.
 __device__ __forceinline__ bool row_bounds(const DeltaPrefillArgs& a, int b, int& start, int& n) {
   start = a.cu[b];
-  n = a.cu[b + 1] - start;
-  return start >= 0 && n >= 0 && start + static_cast<long long>(n) <= a.tokens;
+  const long long m = static_cast<long long>(a.cu[b + 1]) - start;
+  n = static_cast<int>(m);
+  return start >= 0 && m >= 0 && start + m <= a.tokens;
+}
+// whether one of the bounds i0, i0 + step, .. up to row b's own lies past its start (bounds that are none do not count)
+__device__ __forceinline__ bool begins_inside(const DeltaPrefillArgs& a, int b, int start, int i0, int step) {
+  bool inside = false;
+  for (int i = i0; i < b; i += step) inside |= a.cu[i] > start && a.cu[i] <= a.tokens;
+  return inside;
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -211,18 +220,33 @@ __global__ void __launch_bounds__(128, 4)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)), "n"(128) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  const auto holds = [&](int b, int& start, int& n) {  // whether this slot is one of row b's
+    if (!row_bounds(a, b, start, n)) return false;
+    const int i = static_cast<int>(blockIdx.x) - (start / kC + b);
+    return i >= 0 && i < (n + kC - 1) / kC && a.slot_idx[b] > 0 && a.slot_idx[b] < a.c.S;
+  };
+  const auto take = [&](int b, int start, int n) {
+    const int i = static_cast<int>(blockIdx.x) - (start / kC + b);
+    sh[0] = b;
+    sh[1] = start + i * kC;
+    sh[2] = min(n - i * kC, kC);
+  };
+  bool malformed = false;
   for (int b = tid; b < a.batch; b += 128) {
     int start, n;
-    if (!row_bounds(a, b, start, n)) continue;
-    const int i = static_cast<int>(blockIdx.x) - (start / kC + b);
-    if (i >= 0 && i < (n + kC - 1) / kC && a.slot_idx[b] > 0 && a.slot_idx[b] < a.c.S) {
-      sh[0] = b;
-      sh[1] = start + i * kC;
-      sh[2] = min(n - i * kC, kC);
-    }
+    if (holds(b, start, n)) take(b, start, n);
+    malformed |= !row_bounds(a, b, start, n);
   }
   tc_before();
-  __syncthreads();
+  if (__syncthreads_or(malformed)) {  // more than one row may have taken the slot: the one that is not skipped has it
+    if (tid == 0) sh[0] = -1;
+    __syncthreads();
+    for (int b = tid; b < a.batch; b += 128) {
+      int start, n;
+      if (holds(b, start, n) && !begins_inside(a, b, start, 0, 1)) take(b, start, n);
+    }
+    __syncthreads();
+  }
   tc_after();
   const uint32_t tm = tmem_base;
   const auto release = [&]() {
@@ -600,7 +624,7 @@ __global__ void __launch_bounds__(kWorkWarps * 32 + 64, 1)
   const int s = a.slot_idx[b];
   const int dv = a.c.dv, dv0 = tile * NDV;
   const long long ostride = static_cast<long long>(a.c.Hv) * dv;
-  if (!fits) {
+  if (__syncthreads_or(begins_inside(a, b, start, tid, blockDim.x)) || !fits) {
     if (h == 0 && tile == 0 && tid == 0) set_error(a.c.err, RSSM_ERRBIT_SEQLEN);
     return;
   }
