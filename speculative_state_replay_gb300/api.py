@@ -8,6 +8,7 @@ Layouts and semantics are those of include/rssm.h.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -297,10 +298,32 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _s(stream, t):
-    """The stream's handle: the current one of t's device where none is given (torch.cuda.current_stream() costs a
-    small call 3 us)."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+def _s(fn, stream, d):
+    """The stream's handle: the current one of device d where none is given (torch.cuda.current_stream() costs a small
+    call 3 us).  d: the device of all of a call's tensors, by _lib.fast().device(..).  A launch goes to the current
+    device with the tensors' addresses, so all of them have to be there; an address of another device or of the host
+    would fault the GPU."""
+    if d < 0:
+        _refuse(fn, "all tensors must be on one CUDA device")
+    if (d != 0 or _devices() > 1) and d != torch._C._cuda_getDevice():
+        _refuse(fn, f"the tensors' device, {d}, is not the current one")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(d)
+    if stream.device_index != d:
+        _refuse(fn, "the stream is another device's")
+    return stream.cuda_stream
+
+
+@functools.cache
+def _devices():
+    return torch.cuda.device_count()
+
+
+def _scratch(fn, t):
+    """Bytes of a scratch buffer."""
+    if not t.is_contiguous():
+        _refuse(fn, "scratch must be contiguous")
+    return t.numel()
 
 
 class DeltaCache:
@@ -338,6 +361,8 @@ class DeltaCache:
         if not self.pend.is_contiguous():
             _refuse(fn, "pend must be contiguous")
         self.error_word = make("error_word", error_word, (1,), torch.int32)
+        if len({t.device for t in (self.state, self.pend_k, self.pend_w, self.pend_c, self.pend, self.error_word)}) > 1:
+            _refuse(fn, "tensors on different devices")
         c = _lib.RssmDeltaCacheStruct()
         c.num_slots, c.nkheads, c.nvheads, c.dkey, c.dvalue = num_slots, k_heads, v_heads, key_dim, value_dim
         c.npredicted, c.state_dtype = npredicted, state_dtype
@@ -399,10 +424,12 @@ def rssm_delta_step(cache, q, k, v, g, beta, slot_idx, accepted, T, out, scratch
         _ids(fn, "accepted", accepted, batch)
     if cu_seqlens is not None:
         _ids(fn, "cu_seqlens", cu_seqlens, batch + 1)
-    status = _lib.fast().rssm_delta_step(
+    lib = _lib.fast()
+    status = lib.rssm_delta_step(
         cache._addr, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, g.data_ptr(), beta.data_ptr(),
         cache.dk ** -0.5 if scale is None else scale, int(l2norm), slot_idx.data_ptr(), _p(accepted),
-        _p(cu_seqlens), batch, T, n, out.data_ptr(), scratch.data_ptr(), scratch.numel(), _s(stream, q))
+        _p(cu_seqlens), batch, T, n, out.data_ptr(), scratch.data_ptr(), _scratch(fn, scratch),
+        _s(fn, stream, lib.device(q, k, v, g, beta, slot_idx, accepted, cu_seqlens, out, scratch, cache.state)))
     if status:
         raise RssmError(fn, status)
 
@@ -418,10 +445,12 @@ def rssm_delta_prefill(cache, q, k, v, g, beta, slot_idx, cu_seqlens, out, scrat
     _ids(fn, "cu_seqlens", cu_seqlens, batch + 1)
     if initial is not None:
         _ids(fn, "initial", initial, batch)
-    status = _lib.fast().rssm_delta_prefill(
+    lib = _lib.fast()
+    status = lib.rssm_delta_prefill(
         cache._addr, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, g.data_ptr(), beta.data_ptr(),
         cache.dk ** -0.5 if scale is None else scale, int(l2norm), slot_idx.data_ptr(), cu_seqlens.data_ptr(),
-        _p(initial), batch, n, out.data_ptr(), scratch.data_ptr(), scratch.numel(), _s(stream, q))
+        _p(initial), batch, n, out.data_ptr(), scratch.data_ptr(), _scratch(fn, scratch),
+        _s(fn, stream, lib.device(q, k, v, g, beta, slot_idx, cu_seqlens, initial, out, scratch, cache.state)))
     if status:
         raise RssmError(fn, status)
 
@@ -453,9 +482,13 @@ def rssm_verify(target, tokens, u, u_next, T, accepted, next_token, draft=None, 
     _ids(fn, "next_token", next_token, batch)
     if cu_seqlens is not None:
         _ids(fn, "cu_seqlens", cu_seqlens, batch + 1)
-    status = _lib.fast().rssm_verify(
+    if error_word is not None and (error_word.element_size() != 4 or error_word.numel() < 1):
+        _refuse(fn, "error_word must be a tensor of one 32-bit word")
+    lib = _lib.fast()
+    status = lib.rssm_verify(
         target.data_ptr(), st, _p(draft), sd, _DTYPE[dtype], vocab, tokens.data_ptr(), u.data_ptr(), u_next.data_ptr(),
-        _p(cu_seqlens), batch, T, ntok, accepted.data_ptr(), next_token.data_ptr(), _p(error_word), _s(stream, target))
+        _p(cu_seqlens), batch, T, ntok, accepted.data_ptr(), next_token.data_ptr(), _p(error_word),
+        _s(fn, stream, lib.device(target, draft, tokens, u, u_next, cu_seqlens, accepted, next_token, error_word)))
     if status:
         raise RssmError(fn, status)
 
@@ -474,9 +507,10 @@ def rssm_gated_norm(x, z, weight, out, group=None, eps=1e-5, norm_first=False, s
     if weights != dim and weights != group:
         _refuse(fn, f"weight must hold {dim} or {group} values")
     _f32(fn, "weight", weight, 1)
-    status = _lib.fast().rssm_gated_norm(x.data_ptr(), sx, z.data_ptr(), sz, _DTYPE[dtype], weight.data_ptr(),
+    lib = _lib.fast()
+    status = lib.rssm_gated_norm(x.data_ptr(), sx, z.data_ptr(), sz, _DTYPE[dtype], weight.data_ptr(),
                                          int(weights != dim), rows, dim, group, eps, int(norm_first), out.data_ptr(), so,
-                                         _s(stream, x))
+                                         _s(fn, stream, lib.device(x, z, weight, out)))
     if status:
         raise RssmError(fn, status)
 
@@ -495,8 +529,10 @@ def rssm_residual_norm(x, residual, weight, out, residual_out, post_weight=None,
     for name, t in (("weight", weight), ("post_weight", post_weight), ("scale", scale)):
         if t is not None and (t.numel() != dim or t.dtype is not torch.float32 or not t.is_contiguous()):
             _refuse(fn, f"{name} must hold {dim} contiguous float32 values")
-    status = _lib.fast().rssm_residual_norm(
+    lib = _lib.fast()
+    status = lib.rssm_residual_norm(
         x.data_ptr(), sx, residual.data_ptr(), sr, _DTYPE[dtype], _DTYPE[rtype], _p(post_weight), _p(scale), alpha,
-        weight.data_ptr(), rows, dim, eps, residual_out.data_ptr(), sro, out.data_ptr(), so, _s(stream, x))
+        weight.data_ptr(), rows, dim, eps, residual_out.data_ptr(), sro, out.data_ptr(), so,
+        _s(fn, stream, lib.device(x, residual, weight, out, residual_out, post_weight, scale)))
     if status:
         raise RssmError(fn, status)
