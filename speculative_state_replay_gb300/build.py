@@ -2,8 +2,8 @@
 
 Each .cu file is compiled in parallel to an object, then linked into a shared
 library next to this file.  The CUDA runtime is linked statically, so the
-library needs only the driver at run time.  The binding's fast path (_call.so,
-plain C against the CPython API) is compiled next to it.
+library needs only the driver at run time.  The binding's fast path (the module
+_call, plain C against the CPython API) is compiled next to it.
 """
 from __future__ import annotations
 
@@ -20,7 +20,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "librssm.so")
-CALL = os.path.join(HERE, "_call.so")
+CALL = os.path.join(HERE, "_call" + sysconfig.get_config_var("EXT_SUFFIX"))  # an interpreter imports its own
 CALL_SRC = os.path.join(CSRC, "rssm_call.c")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
