@@ -29,10 +29,13 @@ static int32_t as_i32(PyObject *o) {
     PyErr_Format(PyExc_TypeError, "%d arguments expected, got %zd", (n), nargs);       \
     return NULL;                                                                       \
   }
+/* other threads run meanwhile: a launch may wait (for room in the queue, or behind a host callback that needs the lock) */
 #define GIVE(call)                                                                     \
   do {                                                                                 \
+    long status;                                                                       \
     if (PyErr_Occurred()) return NULL;                                                 \
-    return PyLong_FromLong((long)(call));                                              \
+    Py_BEGIN_ALLOW_THREADS status = (long)(call);                                      \
+    Py_END_ALLOW_THREADS return PyLong_FromLong(status);                               \
   } while (0)
 
 static PyObject *delta_step(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
