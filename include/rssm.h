@@ -433,6 +433,10 @@ typedef struct {
   float *pend_c; int64_t pend_c_slot_stride; /* f32 [slot][2][nvheads][npredicted]: running sums of g over the step */
   int32_t *pend;       /* [slot][2]: the half that holds the last step's drafts, and how many they are; 8-byte aligned */
   uint32_t *error_word;
+  /* f32 [slot][2][nvheads][npredicted], laid out like pend_c: what its rounding to
+   * fp32 leaves of the sums (up to 2^-18 after a decay of -100, which is as much
+   * of the factors of the drafts after it).  NULL: not kept */
+  float *pend_cl; int64_t pend_cl_slot_stride;
 } rssm_delta_cache;
 
 /* Bytes of scratch for `batch` rows and `tokens` tokens in all; 0 for an

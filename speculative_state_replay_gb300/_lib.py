@@ -45,6 +45,7 @@ class RssmDeltaCacheStruct(ctypes.Structure):
         ("pend_w", ctypes.c_void_p), ("pend_w_slot_stride", ctypes.c_int64),
         ("pend_c", ctypes.c_void_p), ("pend_c_slot_stride", ctypes.c_int64),
         ("pend", ctypes.c_void_p), ("error_word", ctypes.c_void_p),
+        ("pend_cl", ctypes.c_void_p), ("pend_cl_slot_stride", ctypes.c_int64),
     ]
 
 

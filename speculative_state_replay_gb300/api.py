@@ -333,7 +333,7 @@ class DeltaCache:
     """
 
     def __init__(self, num_slots, k_heads, v_heads, key_dim, value_dim, npredicted, state_dtype=F32, device="cuda",
-                 state=None, pend_k=None, pend_w=None, pend_c=None, pend=None, error_word=None):
+                 state=None, pend_k=None, pend_w=None, pend_c=None, pend=None, error_word=None, pend_cl=None):
         fn = "DeltaCache"
         if state_dtype not in (F32, BF16):
             _refuse(fn, "state_dtype must be F32 or BF16")
@@ -357,16 +357,17 @@ class DeltaCache:
         self.pend_k = make("pend_k", pend_k, (num_slots, 2, k_heads, npredicted, key_dim), torch.bfloat16)
         self.pend_w = make("pend_w", pend_w, (num_slots, 2, v_heads, npredicted, value_dim), torch.float32)
         self.pend_c = make("pend_c", pend_c, (num_slots, 2, v_heads, npredicted), torch.float32)
+        self.pend_cl = make("pend_cl", pend_cl, (num_slots, 2, v_heads, npredicted), torch.float32)
         self.pend = make("pend", pend, (num_slots, 2), torch.int32)
         if not self.pend.is_contiguous():
             _refuse(fn, "pend must be contiguous")
         self.error_word = make("error_word", error_word, (1,), torch.int32)
-        if len({t.device for t in (self.state, self.pend_k, self.pend_w, self.pend_c, self.pend, self.error_word)}) > 1:
+        if len({t.device for t in (self.state, self.pend_k, self.pend_w, self.pend_c, self.pend_cl, self.pend, self.error_word)}) > 1:
             _refuse(fn, "tensors on different devices")
         c = _lib.RssmDeltaCacheStruct()
         c.num_slots, c.nkheads, c.nvheads, c.dkey, c.dvalue = num_slots, k_heads, v_heads, key_dim, value_dim
         c.npredicted, c.state_dtype = npredicted, state_dtype
-        for name in ("state", "pend_k", "pend_w", "pend_c"):
+        for name in ("state", "pend_k", "pend_w", "pend_c", "pend_cl"):
             t = getattr(self, name)
             setattr(c, name, t.data_ptr())
             setattr(c, name + "_slot_stride", t.stride(0))

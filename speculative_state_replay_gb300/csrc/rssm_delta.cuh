@@ -42,6 +42,22 @@ constexpr float kMinLog = -100.0f;  // log decays are held at this and above: e^
 constexpr float kMaxLog = 1000.0f;         // and at this and below (e^89 is infinite)
 constexpr float kFix = 1099511627776.0f;   // 2^40: one of running sums in fixed point
 
+// A sum as two floats, hi + lo: differences of running sums are exponents, and
+// one float's rounding at a sum of 100 would be 2^-18.
+struct LongSum {
+  float hi, lo;
+  __device__ __forceinline__ void add(float h, float l) {
+    const float s = hi + h, b = s - hi;
+    lo += l + ((hi - (s - b)) + (h - b));  // what the addition rounded off, exactly (Knuth's two-sum)
+    hi = s;
+  }
+  __device__ __forceinline__ void settle() {  // hi: the sum rounded
+    const float s = hi + lo;
+    lo += hi - s;
+    hi = s;
+  }
+};
+
 struct DeltaCacheView {
   int S, Hk, Hv, rep, dv, np;
   int dtype, wide;  // wide: state rows start on 32 bytes
@@ -53,6 +69,8 @@ struct DeltaCacheView {
   long long pend_w_stride;
   float* pend_c;
   long long pend_c_stride;
+  float* pend_cl;  // or null
+  long long pend_cl_stride;
   int* pend;
   unsigned* err;
 };

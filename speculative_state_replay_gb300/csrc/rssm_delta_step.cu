@@ -22,7 +22,7 @@ struct DeltaStepArgs {
 constexpr int kStepWarps = 4;
 constexpr int kStepRows = kStepWarps * 16;  // value rows of a tile
 // blocks an SM: 2-byte states 431 us with 4, 452 with 3 (1024 rows); fp32 states
-// keep 64 values a lane and spill with 4: 82 us, 57 with 3 (64 rows)
+// keep 64 values a lane and spill with 4: 82 us, 54 with 3 (64 rows)
 constexpr int step_blocks(bool f32) { return f32 ? 3 : 4; }
 
 // A warp's item on its way from memory: its state rows (a bulk copy) and, for
@@ -35,7 +35,7 @@ struct alignas(128) StepWarp {
   struct alignas(16) Small {
     float w[kDeltaT][16];
     uint16_t v[kDeltaT][16];
-    float c[kDeltaT], g[kDeltaT], beta[kDeltaT];
+    float c[kDeltaT], cl[kDeltaT], g[kDeltaT], beta[kDeltaT];
   } x[2];
   uint64_t bar;  // the state rows have landed
 };
@@ -169,7 +169,13 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(F32)) delta_step_
   const auto fetch_waiting = [&](int h, int r, int x) {
     const int at = (side * Hv + h) * np;
     if (r < dv && t < acc) cp_async16(&wm.x[x].w[t][4 * cc], pw + static_cast<long long>(at + t) * dv + r);
-    if (lane < acc) cp_async4(&wm.x[x].c[lane], pc + at);
+    if (lane < acc) {
+      cp_async4(&wm.x[x].c[lane], pc + at);
+      if (a.c.pend_cl)
+        cp_async4(&wm.x[x].cl[lane], a.c.pend_cl + s * a.c.pend_cl_stride + at + lane);
+      else
+        wm.x[x].cl[lane] = 0.0f;
+    }
   };
   if (acc > 0) {
     fetch_waiting(hv, r0, 0);
@@ -197,7 +203,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(F32)) delta_step_
   state += (t * DK + 8 * cc) * (F32 ? 4 : 2);
   uint32_t parity = 0;
   int head = -1;
-  float beta = 0.0f, c = 0.0f, ec = 0.0f, E = 1.0f, ew = 0.0f, A[2], P[2], gk[2], gq[2];
+  float beta = 0.0f, ec = 0.0f, E = 1.0f, ew = 0.0f, A[2], P[2], gk[2], gq[2];
 #pragma unroll 1
   for (; left > 0; --left, turn ^= 1) {
     const typename StepWarp<DK, F32>::Small& x = wm.x[turn];
@@ -229,25 +235,30 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(F32)) delta_step_
       head = h;
       beta = live ? x.beta[t] : 0.0f;
       // running sums and the coefficients among the block's own tokens
-      c = live ? fmaxf(x.g[t], kMinLog) : 0.0f;
+      LongSum c = {live ? fminf(fmaxf(x.g[t], kMinLog), kMaxLog) : 0.0f, 0.0f};
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
-        const float y = __shfl_up_sync(full, c, o);
-        if (lane >= o) c += y;
+        const float yh = __shfl_up_sync(full, c.hi, o), yl = __shfl_up_sync(full, c.lo, o);
+        if (lane >= o) c.add(yh, yl);
       }
+      c.settle();
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int j = 2 * cc + i;
-        const float d = c - __shfl_sync(full, c, j * 4);
+        const float d = (c.hi - __shfl_sync(full, c.hi, j * 4)) + (c.lo - __shfl_sync(full, c.lo, j * 4));
         const float e = j <= t ? __expf(d) : 0.0f;
         A[i] = j < t ? beta * e * blk.kk[i] : 0.0f;
         P[i] = e * blk.kk[2 + i];
       }
-      ec = __expf(c);
+      ec = __expf(c.hi);
+      if (r == 0 && live && cc == 0) {  // they wait with the drafts
+        nc[h * np] = c.hi;
+        if (a.c.pend_cl) a.c.pend_cl[s * a.c.pend_cl_stride + (to * Hv + h) * np + t] = c.lo;
+      }
       if (acc > 0) {
-        const float end = x.c[acc - 1];
+        const float end = x.c[acc - 1], rest = x.cl[acc - 1];
         E = __expf(end);
-        ew = lane < acc ? __expf(end - x.c[lane]) : 0.0f;
+        ew = lane < acc ? __expf((end - x.c[lane]) + (rest - x.cl[lane])) : 0.0f;
         const float e0 = __shfl_sync(full, ew, 2 * cc), e1 = __shfl_sync(full, ew, 2 * cc + 1);
         gk[0] = blk.wk[0] * e0;
         gk[1] = blk.wk[1] * e1;
@@ -315,7 +326,6 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(F32)) delta_step_
         *reinterpret_cast<uint32_t*>(out + h * dv + r + 8 * i) = cvt_bf16x2(o[i][0], o[i][1]);
         *reinterpret_cast<float2*>(nw + static_cast<long long>(h * np) * dv + r + 8 * i) = make_float2(u[i][0] * blk.r, u[i][1] * blk.r);
       }
-      if (r == 0 && cc == 0) nc[h * np] = c;
     }
   }
 }
@@ -348,6 +358,7 @@ bool delta_view(const rssm_delta_cache* c, DeltaCacheView* o, rssm_status* st) {
   if (c->state_slot_stride < static_cast<int64_t>(c->nvheads) * c->dvalue * c->dkey || c->pend_k_slot_stride < kl ||
       c->pend_w_slot_stride < cl * c->dvalue || c->pend_c_slot_stride < cl)
     return false;
+  if (c->pend_cl && (!al(c->pend_cl, 4) || c->pend_cl_slot_stride < cl)) return false;
   if (c->state_slot_stride * esz % 16 || c->pend_k_slot_stride % 8 || c->pend_w_slot_stride % 4) return false;
   o->S = c->num_slots;
   o->Hk = c->nkheads;
@@ -364,6 +375,8 @@ bool delta_view(const rssm_delta_cache* c, DeltaCacheView* o, rssm_status* st) {
   o->pend_w_stride = c->pend_w_slot_stride;
   o->pend_c = c->pend_c;
   o->pend_c_stride = c->pend_c_slot_stride;
+  o->pend_cl = c->pend_cl;
+  o->pend_cl_stride = c->pend_cl_slot_stride;
   o->pend = c->pend;
   o->err = c->error_word;
   o->wide = al(c->state, 32) && c->state_slot_stride * esz % 32 == 0;

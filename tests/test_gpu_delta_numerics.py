@@ -61,3 +61,41 @@ def test_step_takes_a_state_as_it_is(gen, shape):
     got = cache.pend_w[1:, 1, :, 0].double()
     size = torch.einsum("bhvk,bhk->bhv", S.abs(), kd.abs())
     assert ((got - u).abs() <= 2.0**-20 * size).all(), float(((got - u).abs() / size).max())
+
+
+def many_resets(gen, n, hv):
+    """Log decays with resets (-inf), near ones and ordinary ones in every order."""
+    g = -0.5 * torch.rand(n, hv, generator=gen, device="cuda")
+    kind = torch.rand(n, hv, generator=gen, device="cuda")
+    g = torch.where(kind < 0.3, torch.full_like(g, -math.inf), g)
+    return torch.where((kind >= 0.3) & (kind < 0.5), g - 60.0, g)
+
+
+@pytest.mark.parametrize("T", [2, 5, 8])
+def test_resets_in_mid_step(gen, T):
+    """Resets and decays of -60 among a step's tokens, then a commit.  What a later token's factors need is a difference
+    of running sums that is O(1), whatever the sums are: corrections, and the state after the commit, are fp32 sums of
+    at most 136 terms with factors that are a few 2^-23 off: 1e-6 of their norm."""
+    hk, hv, dk, dv, B = 2, 4, 128, 64, 12
+    cache = api.DeltaCache(B + 1, hk, hv, dk, dv, T)
+    cache.state.copy_(0.3 * rnd(gen, *cache.state.shape))
+    scratch = api.alloc_delta_scratch(cache, B, B * T)
+    slots = torch.arange(1, B + 1, dtype=torch.int32, device="cuda")
+    before = cache.state.clone()
+    q, k, v = rnd(gen, B * T, hk, dk).to(BF), rnd(gen, B * T, hk, dk).to(BF), rnd(gen, B * T, hv, dv).to(BF)
+    g, beta = many_resets(gen, B * T, hv), torch.rand(B * T, hv, generator=gen, device="cuda")
+    out = torch.empty(B * T, hv, dv, dtype=BF, device="cuda")
+    api.rssm_delta_step(cache, q, k, v, g, beta, slots, None, T, out, scratch, l2norm=True)
+    acc = torch.tensor([b % T + 1 for b in range(B)], dtype=torch.int32, device="cuda")
+    want, us = [], []
+    for b in range(B):
+        part = slice(b * T, b * T + T)
+        _, u, S = delta_tokens(before[b + 1], q[part], k[part], v[part], g[part], beta[part], dk**-0.5, True, keep=int(acc[b]))
+        want.append(S)
+        us.append(u * (k[part].double().pow(2).sum(-1) + 1e-6).rsqrt().repeat_interleave(hv // hk, 1)[..., None])
+    assert off(cache.pend_w[1:, 1].transpose(1, 2), torch.stack(us)) <= 1e-6
+    none = [x[:0] for x in (q, k, v, g, beta)]
+    api.rssm_delta_step(cache, *none, slots, acc, T, out[:0], scratch, l2norm=True,
+                        cu_seqlens=torch.zeros(B + 1, dtype=torch.int32, device="cuda"))
+    for b in range(B):
+        assert off(cache.state[b + 1], want[b]) <= 1e-6, b

@@ -68,3 +68,17 @@ for name, a in args.items():
     r = subprocess.run([sys.executable, "-c", code, str(tmp_path)], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0, r.stderr
     assert r.stdout.splitlines() == [f"{f} 7 True True" for f in FUNCTIONS]
+
+
+def test_low_parts_of_the_sums():
+    """pend_cl may be missing; what is given is checked like pend_c."""
+    import ctypes
+
+    lib, at = _lib.load(), 1 << 20
+    c = _lib.RssmDeltaCacheStruct(num_slots=4, nkheads=2, nvheads=4, dkey=128, dvalue=64, npredicted=4, state_dtype=0, state=at,
+                                  state_slot_stride=4 * 64 * 128, pend_k=at, pend_k_slot_stride=2 * 2 * 4 * 128, pend_w=at,
+                                  pend_w_slot_stride=2 * 4 * 4 * 64, pend_c=at, pend_c_slot_stride=2 * 4 * 4, pend=at, error_word=at)
+    assert lib.rssm_delta_scratch_bytes(ctypes.byref(c), 1, 1) > 0
+    for pointer, stride, ok in ((at, 32, True), (at + 4, 40, True), (at + 2, 32, False), (at, 31, False), (at, -32, False)):
+        c.pend_cl, c.pend_cl_slot_stride = pointer, stride
+        assert (lib.rssm_delta_scratch_bytes(ctypes.byref(c), 1, 1) > 0) == ok
