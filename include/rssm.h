@@ -459,7 +459,10 @@ size_t rssm_delta_scratch_bytes(const rssm_delta_cache *cache, int32_t batch, in
  *   out_t = scale S_t q_t, rounded to bf16
  * and their (k_t, u_t, running sum of g) wait in the slot's other half.
  * l2norm = 1: q_t and k_t are divided by sqrt(|.|^2 + 1e-6) first.  Log decays
- * below -100 count as -100.
+ * below -100 count as -100, those above 1000 as 1000; where the running sums of a
+ * step (of a prompt's 64 tokens) rise by more than 88 anywhere, factors pass
+ * fp32's range.  A decay that is NaN makes its head's outputs NaN from its token
+ * on, and the state once the token is in it.
  *   q, k bf16 [tok][nkheads][dkey], v bf16 [tok][nvheads][dvalue]: *_stride
  *        elements between tokens (multiples of 8; 16-byte aligned pointers),
  *        heads contiguous
@@ -487,7 +490,9 @@ rssm_status rssm_delta_step(const rssm_delta_cache *cache, const void *q, int64_
  *           an earlier row's bound, are skipped (RSSM_ERRBIT_SEQLEN)
  *   initial [batch] i32 or NULL: nonzero rows start from their slot's state
  *           (a prompt that comes in parts), the others from zero
- * Drafts that wait in a slot are dropped.
+ * Drafts that wait in a slot are dropped.  What is not finite reaches all of the
+ * 64 tokens of a prompt that are worked on together, and those after them; no
+ * other head and no other prompt.
  */
 rssm_status rssm_delta_prefill(const rssm_delta_cache *cache, const void *q, int64_t q_stride, const void *k,
                                int64_t k_stride, const void *v, int64_t v_stride, const float *g, const float *beta,

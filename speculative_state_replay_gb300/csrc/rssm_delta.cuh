@@ -40,7 +40,7 @@ constexpr float kMinLog = -100.0f;  // log decays are held at this and above: e^
                                     // and a finite floor keeps differences of running sums defined (g = -inf resets a state)
 
 constexpr float kMaxLog = 1000.0f;         // and at this and below (e^89 is infinite)
-constexpr float kFix = 1099511627776.0f;   // 2^40: one of running sums in fixed point
+__device__ __forceinline__ float held_log(float g) { return g < kMinLog ? kMinLog : g > kMaxLog ? kMaxLog : g; }  // NaN stays NaN
 
 // A sum as two floats, hi + lo: differences of running sums are exponents, and
 // one float's rounding at a sum of 100 would be 2^-18.

@@ -271,34 +271,31 @@ __global__ void __launch_bounds__(128, 4)
   }
   constexpr uint32_t i_gram = instruction(64, false, false), i_pt = instruction(64, false, true);
   if (warp == 2) {
-    // Running sums of g in fixed point, 40 fraction bits, and as two floats:
-    // differences of them are exponents, and one float's rounding at a sum of
-    // 100 would be 2^-18.  (fp64 takes several times as long here.)
-    long long c[2];
-    float be[2];
+    // running sums of g, two tokens a lane
+    float g[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int i = 2 * lane + e;
       const long long at = static_cast<long long>(tok0 + i) * a.c.Hv + h;
-      c[e] = i < n ? __float2ll_rn(fminf(fmaxf(a.tk.g[at], kMinLog), kMaxLog) * kFix) : 0ll;
-      be[e] = i < n ? a.tk.beta[at] : 0.0f;
+      g[e] = i < n ? held_log(a.tk.g[at]) : 0.0f;
+      s_beta[i] = i < n ? a.tk.beta[at] : 0.0f;
     }
-    c[1] += c[0];
-    long long run = c[1];
+    LongSum run = {g[0], 0.0f};
+    run.add(g[1], 0.0f);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(full, run, o);
-      if (lane >= o) run += y;
+      const float yh = __shfl_up_sync(full, run.hi, o), yl = __shfl_up_sync(full, run.lo, o);
+      if (lane >= o) run.add(yh, yl);
     }
-    const long long before = run - c[1];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const long long x = before + c[e];
-      const float hi = __ll2float_rn(x);
-      s_ch[2 * lane + e] = hi * (1.0f / kFix);
-      s_cl[2 * lane + e] = __ll2float_rn(x - __float2ll_rn(hi)) * (1.0f / kFix);
-      s_beta[2 * lane + e] = be[e];
-    }
+    LongSum c = {__shfl_up_sync(full, run.hi, 1), __shfl_up_sync(full, run.lo, 1)};
+    if (lane == 0) c = {0.0f, 0.0f};
+    c.add(g[0], 0.0f);
+    c.settle();
+    run.settle();
+    s_ch[2 * lane] = c.hi;
+    s_cl[2 * lane] = c.lo;
+    s_ch[2 * lane + 1] = run.hi;
+    s_cl[2 * lane + 1] = run.lo;
   }
   bool ok = mbar_wait(bars, 0);
   if (tid == 32 && ok) {

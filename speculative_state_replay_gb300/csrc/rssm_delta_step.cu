@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(F32)) delta_step_
       head = h;
       beta = live ? x.beta[t] : 0.0f;
       // running sums and the coefficients among the block's own tokens
-      LongSum c = {live ? fminf(fmaxf(x.g[t], kMinLog), kMaxLog) : 0.0f, 0.0f};
+      LongSum c = {live ? held_log(x.g[t]) : 0.0f, 0.0f};
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
         const float yh = __shfl_up_sync(full, c.hi, o), yl = __shfl_up_sync(full, c.lo, o);

@@ -99,3 +99,53 @@ def test_resets_in_mid_step(gen, T):
                         cu_seqlens=torch.zeros(B + 1, dtype=torch.int32, device="cuda"))
     for b in range(B):
         assert off(cache.state[b + 1], want[b]) <= 1e-6, b
+
+
+def test_a_nan_decay_in_a_step(gen):
+    """One head's log decay of token 2 is NaN: its outputs are NaN from there on, and so is its state once that token is
+    accepted; earlier tokens and the other head do not know."""
+    hk, hv, dk, dv, T, B = 1, 2, 64, 32, 5, 2
+    cache = api.DeltaCache(B + 1, hk, hv, dk, dv, T)
+    cache.state.copy_(0.3 * rnd(gen, *cache.state.shape))
+    before = cache.state.clone()
+    scratch = api.alloc_delta_scratch(cache, B, B * T)
+    slots = torch.arange(1, B + 1, dtype=torch.int32, device="cuda")
+    q, k, v = rnd(gen, B * T, hk, dk).to(BF), rnd(gen, B * T, hk, dk).to(BF), rnd(gen, B * T, hv, dv).to(BF)
+    g, beta = -torch.rand(B * T, hv, generator=gen, device="cuda"), torch.rand(B * T, hv, generator=gen, device="cuda")
+    g[[2, T + 2], 1] = math.nan
+    out = torch.empty(B * T, hv, dv, dtype=BF, device="cuda")
+    api.rssm_delta_step(cache, q, k, v, g, beta, slots, None, T, out, scratch, l2norm=True)
+    clean = g.nan_to_num(nan=-0.1)
+    ref = [delta_tokens(before[b + 1], *(x[b * T : b * T + T] for x in (q, k, v, clean, beta)), dk**-0.5, True, keep=[2, 4][b])
+           for b in range(B)]
+    for b in range(B):
+        o = out[b * T : b * T + T]
+        assert torch.isnan(o[2:, 1]).all()
+        assert off(o[:, 0], ref[b][0][:, 0]) <= 2.0**-8 and off(o[:2, 1], ref[b][0][:2, 1]) <= 2.0**-8
+        assert torch.isnan(cache.pend_c[b + 1, 1, 1, 2:]).all() and torch.isfinite(cache.pend_c[b + 1, 1, 1, :2]).all()
+    api.rssm_delta_step(cache, q, k, v, clean, beta, slots, torch.tensor([2, 4], dtype=torch.int32, device="cuda"), T, out, scratch,
+                        l2norm=True)
+    assert off(cache.state[1], ref[0][2]) <= 1e-5 and off(cache.state[2, 0], ref[1][2][0]) <= 1e-5
+    assert torch.isnan(cache.state[2, 1]).all()
+
+
+def test_a_nan_decay_in_a_prompt(gen):
+    """The head's outputs are NaN from the token on, its state too; the chunks before, the other head and the other
+    prompt do not know."""
+    hk, hv, dk, dv = 1, 2, 128, 64
+    lens = [150, 90]
+    tot = sum(lens)
+    q, k, v = rnd(gen, tot, hk, dk).to(BF), rnd(gen, tot, hk, dk).to(BF), rnd(gen, tot, hv, dv).to(BF)
+    g, beta = -torch.rand(tot, hv, generator=gen, device="cuda"), torch.rand(tot, hv, generator=gen, device="cuda")
+    ref = [delta_tokens(torch.zeros(hv, dv, dk, device="cuda"), *(x[a : a + n] for x in (q, k, v, g, beta)), dk**-0.5, True)
+           for a, n in ((0, 150), (150, 90))]
+    g[100, 1] = math.nan
+    cache = api.DeltaCache(3, hk, hv, dk, dv, 2)
+    out = torch.empty(tot, hv, dv, dtype=BF, device="cuda")
+    api.rssm_delta_prefill(cache, q, k, v, g, beta, torch.tensor([1, 2], dtype=torch.int32, device="cuda"),
+                           torch.tensor([0, 150, 240], dtype=torch.int32, device="cuda"), out, api.alloc_delta_scratch(cache, 2, tot),
+                           l2norm=True)
+    assert torch.isnan(out[100:150, 1]).all() and torch.isnan(cache.state[1, 1]).all()
+    assert off(out[:150, 0], ref[0][0][:, 0]) <= 2.0**-8 and off(out[:64, 1], ref[0][0][:64, 1]) <= 2.0**-8
+    assert off(out[150:], ref[1][0]) <= 2.0**-8
+    assert off(cache.state[1, 0], ref[0][2][0]) <= 1e-5 and off(cache.state[2], ref[1][2]) <= 1e-5
