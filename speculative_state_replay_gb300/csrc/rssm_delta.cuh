@@ -58,6 +58,10 @@ struct LongSum {
   }
 };
 
+// e^(hi + lo), lo what the rounding of hi left: expf's 2 units in the last place and one more, whatever hi (an infinite
+// one stays infinite).  The hardware's power of two alone would be |hi| 2^-24 off, and a state keeps that of every commit.
+__device__ __forceinline__ float exp_sum(float hi, float lo) { return expf(hi) * (1.0f + lo); }
+
 struct DeltaCacheView {
   int S, Hk, Hv, rep, dv, np;
   int dtype, wide;  // wide: state rows start on 32 bytes

@@ -337,11 +337,11 @@ __global__ void __launch_bounds__(128, 4)
   if (is_key) {
     // decays of a row go through the end of the column's block: a factor of the column, at most 1, and one of the row
     const int end = i | 15;
-    s_col[i] = live ? __expf((s_ch[end] - ch) + (s_cl[end] - cl)) * s_r[i] : 0.0f;
+    s_col[i] = live ? expf((s_ch[end] - ch) + (s_cl[end] - cl)) * s_r[i] : 0.0f;
     float* vec = reinterpret_cast<float*>(unit + kImg);
-    const float ec = __expf(ch);
+    const float ec = exp_sum(ch, cl);
     vec[i] = s_beta[i] * ec * s_r[i];
-    vec[64 + i] = __expf((s_ch[63] - ch) + (s_cl[63] - cl)) * s_r[i];
+    vec[64 + i] = expf((s_ch[63] - ch) + (s_cl[63] - cl)) * s_r[i];
     vec[128 + i] = ec * s_rq[i];
     vec[192 + i] = s_beta[i];
     if (i == 63) vec[256] = ec;
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(128, 4)
         // the row's factor is at most 1 past the block, and in its own block as
         // large as the block's decay is small: up to e^60 the factors serve there too
         const float up = (ch - s_ch[16 * b + 15]) + (cl - s_cl[16 * b + 15]);
-        const float f = __expf(up) * rf;
+        const float f = expf(up) * rf;
         const pair f2 = pack2(f, f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(128, 4)
           if (up > 60.0f && d >= 0) {
 #pragma unroll 1
             for (int e = 0; e < 16; ++e) {
-              const float w = __expf((ch - s_ch[16 * b + e]) + (cl - s_cl[16 * b + e])) * (rf * s_r[16 * b + e]);
+              const float w = expf((ch - s_ch[16 * b + e]) + (cl - s_cl[16 * b + e])) * (rf * s_r[16 * b + e]);
 #pragma unroll
               for (int k = 0; k < 16; ++k)
                 if (k == e) y[k] = w * __uint_as_float(x[k >> 3][k & 7]);

@@ -246,19 +246,19 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(F32)) delta_step_
       for (int i = 0; i < 2; ++i) {
         const int j = 2 * cc + i;
         const float d = (c.hi - __shfl_sync(full, c.hi, j * 4)) + (c.lo - __shfl_sync(full, c.lo, j * 4));
-        const float e = j <= t ? __expf(d) : 0.0f;
+        const float e = j <= t ? expf(d) : 0.0f;
         A[i] = j < t ? beta * e * blk.kk[i] : 0.0f;
         P[i] = e * blk.kk[2 + i];
       }
-      ec = __expf(c.hi);
+      ec = exp_sum(c.hi, c.lo);
       if (r == 0 && live && cc == 0) {  // they wait with the drafts
         nc[h * np] = c.hi;
         if (a.c.pend_cl) a.c.pend_cl[s * a.c.pend_cl_stride + (to * Hv + h) * np + t] = c.lo;
       }
       if (acc > 0) {
         const float end = x.c[acc - 1], rest = x.cl[acc - 1];
-        E = __expf(end);
-        ew = lane < acc ? __expf((end - x.c[lane]) + (rest - x.cl[lane])) : 0.0f;
+        E = exp_sum(end, rest);
+        ew = lane < acc ? expf((end - x.c[lane]) + (rest - x.cl[lane])) : 0.0f;
         const float e0 = __shfl_sync(full, ew, 2 * cc), e1 = __shfl_sync(full, ew, 2 * cc + 1);
         gk[0] = blk.wk[0] * e0;
         gk[1] = blk.wk[1] * e1;

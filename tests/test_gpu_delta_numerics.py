@@ -101,6 +101,31 @@ def test_resets_in_mid_step(gen, T):
         assert off(cache.state[b + 1], want[b]) <= 1e-6, b
 
 
+@pytest.mark.parametrize("how", ["step", "prompt"])
+def test_decay_of_a_state(gen, how):
+    """Keys of zero: the state is multiplied by e^c and nothing else.  expf is at most 2 units (2^-22) off and the
+    product half a one: 5 2^-24."""
+    hk, hv, dk, dv, B = 4, 8, 64, 32, 8
+    cache = api.DeltaCache(B + 1, hk, hv, dk, dv, 2)
+    cache.state.copy_(rnd(gen, *cache.state.shape))
+    before = cache.state[1:].double()
+    c = -8.0 - 8.0 * torch.rand(B, hv, generator=gen, device="cuda")
+    slots = torch.arange(1, B + 1, dtype=torch.int32, device="cuda")
+    zero = torch.zeros(B, hk, dk, dtype=BF, device="cuda")
+    v, beta = torch.zeros(B, hv, dv, dtype=BF, device="cuda"), torch.ones(B, hv, device="cuda")
+    out = torch.empty_like(v)
+    scratch = api.alloc_delta_scratch(cache, B, B)
+    if how == "prompt":
+        api.rssm_delta_prefill(cache, zero, zero, v, c, beta, slots, torch.arange(B + 1, dtype=torch.int32, device="cuda"), out,
+                               scratch, initial=torch.ones(B, dtype=torch.int32, device="cuda"))
+    else:
+        api.rssm_delta_step(cache, zero, zero, v, c, beta, slots, None, 1, out, scratch)
+        api.rssm_delta_step(cache, zero, zero, v, c, beta, slots, torch.ones(B, dtype=torch.int32, device="cuda"), 1, out, scratch)
+    want = before * torch.exp(c.double())[..., None, None]
+    worst = float(((cache.state[1:].double() - want).abs() / want.abs()).max())
+    assert worst <= 5 * 2.0**-24, worst
+
+
 def test_a_nan_decay_in_a_step(gen):
     """One head's log decay of token 2 is NaN: its outputs are NaN from there on, and so is its state once that token is
     accepted; earlier tokens and the other head do not know."""
