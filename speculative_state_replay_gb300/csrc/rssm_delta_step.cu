@@ -117,17 +117,18 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(F32)) delta_step_
   const uint16_t* vp = a.tk.v + (tok0 + t) * a.tk.v_stride + 8 * (cc & 1);
   const float* gp = (lane < 8 ? a.tk.g : a.tk.beta) + (tok0 + (lane & 7)) * Hv;
   int turn = 0;
-  // an item's state rows, and the new tokens' part
-  const auto fetch = [&](int h, int r, int x) {
+  // an item's state rows, and the new tokens' part; a head's decays, rates and (below) running sums come with the first
+  // of its items that the warp has
+  const auto fetch = [&](int h, int r, int x, bool new_head) {
     if (r >= dv) return;
     if (lane == 0) {
       mbar_arrive_expect_tx(&wm.bar, 16 * kRow);
       bulk_g2s(wm.s, state + static_cast<long long>(h * dv + r) * kRow, 16 * kRow, &wm.bar);
     }
     if (live && cc < 2) cp_async16(&wm.x[x].v[t][8 * cc], vp + h * dv + r);
-    if (lane < 16 && (lane & 7) < n) cp_async4(lane < 8 ? &wm.x[x].g[lane] : &wm.x[x].beta[lane & 7], gp + h);
+    if (new_head && lane < 16 && (lane & 7) < n) cp_async4(lane < 8 ? &wm.x[x].g[lane] : &wm.x[x].beta[lane & 7], gp + h);
   };
-  fetch(hv, r0, 0);
+  fetch(hv, r0, 0, true);
   for (int i = tid; i < kDeltaT * CH; i += kStepWarps * 32) {
     const int r = i / CH, ch = i % CH, to = r * kTokenRow<DK> + ch * 16;
     if (r < n) {
@@ -166,10 +167,10 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(F32)) delta_step_
   }
   const float* pw = a.c.pend_w + s * a.c.pend_w_stride + 4 * cc;
   const float* pc = a.c.pend_c + s * a.c.pend_c_stride + lane;
-  const auto fetch_waiting = [&](int h, int r, int x) {
+  const auto fetch_waiting = [&](int h, int r, int x, bool new_head) {
     const int at = (side * Hv + h) * np;
     if (r < dv && t < acc) cp_async16(&wm.x[x].w[t][4 * cc], pw + static_cast<long long>(at + t) * dv + r);
-    if (lane < acc) {
+    if (new_head && lane < acc) {
       cp_async4(&wm.x[x].c[lane], pc + at);
       if (a.c.pend_cl)
         cp_async4(&wm.x[x].cl[lane], a.c.pend_cl + s * a.c.pend_cl_stride + at + lane);
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(F32)) delta_step_
     }
   };
   if (acc > 0) {
-    fetch_waiting(hv, r0, 0);
+    fetch_waiting(hv, r0, 0, true);
     const uint16_t* pk = a.c.pend_k + s * a.c.pend_k_stride + (static_cast<long long>(side) * a.c.Hk + hk) * np * DK;
     for (int i = tid; i < acc * CH; i += kStepWarps * 32) {
       const uint4 x = *reinterpret_cast<const uint4*>(pk + i * 8);
@@ -213,8 +214,8 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(F32)) delta_step_
     __syncwarp();  // the other lanes' copies have landed too
     if (r >= dv) {
       if (left > 1) {
-        fetch(hv, r0, turn ^ 1);
-        if (acc > 0) fetch_waiting(hv, r0, turn ^ 1);
+        fetch(hv, r0, turn ^ 1, r0 == warp * 16);
+        if (acc > 0) fetch_waiting(hv, r0, turn ^ 1, r0 == warp * 16);
       }
       continue;
     }
@@ -228,8 +229,8 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(F32)) delta_step_
     S[1].read(wm.s, t + 8, cc);
     __syncwarp();  // the rows are read
     if (left > 1) {
-      fetch(hv, r0, turn ^ 1);
-      if (acc > 0) fetch_waiting(hv, r0, turn ^ 1);
+      fetch(hv, r0, turn ^ 1, r0 == warp * 16);
+      if (acc > 0) fetch_waiting(hv, r0, turn ^ 1, r0 == warp * 16);
     }
     if (h != head) {  // what the head's items share
       head = h;
