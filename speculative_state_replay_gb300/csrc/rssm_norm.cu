@@ -133,10 +133,20 @@ __device__ __forceinline__ void store_vec(E* p, const float (&f)[VEC], bool wide
   }
 }
 
-// z / (1 + e^-z) by the hardware's exponential and reciprocal, a few 2^-22 off
+// z / (1 + e^-z), the reciprocal by the hardware's, 2^-23 off.  2-byte values
+// take its power of two as well, |z| 2^-24 and 2^-22 off: 2^-18 at z = -85, and
+// below -87 it is 0, against 2^-9 or 2^-12 of the output's rounding.  fp32
+// values: e^-|z| by expf, exact to 2 units whatever z, on the side where it is
+// at most 1, so that gates below -87 are what they are too.
+template <typename E>
 __device__ __forceinline__ float silu(float z) {
   float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+  if constexpr (sizeof(E) == 4) {
+    e = expf(-fabsf(z));
+    z = z < 0.0f ? z * e : z;
+  } else {
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+  }
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
   return z * r;
 }
@@ -226,7 +236,7 @@ __global__ void __launch_bounds__(TEAM == 0 ? 1024 : 256, NV * IT == 4 && TEAM !
           float fz[VEC];
           rz[it][v].floats(fz);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) fx[v][e] *= silu(fz[e]);
+          for (int e = 0; e < VEC; ++e) fx[v][e] *= silu<E>(fz[e]);
         }
 #pragma unroll
         for (int e = 0; e < VEC; ++e) sum = fmaf(fx[v][e], fx[v][e], sum);
@@ -245,7 +255,7 @@ __global__ void __launch_bounds__(TEAM == 0 ? 1024 : 256, NV * IT == 4 && TEAM !
             float fz[VEC];
             rz[it][v].floats(fz);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) fw[e] *= silu(fz[e]);
+            for (int e = 0; e < VEC; ++e) fw[e] *= silu<E>(fz[e]);
           }
           store_vec<E, VEC>(out + i, fw);
         }
@@ -265,7 +275,7 @@ __global__ void __launch_bounds__(TEAM == 0 ? 1024 : 256, NV * IT == 4 && TEAM !
       if (!a.norm_first) load_vec<E, VEC>(z + i, fz);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        if (!a.norm_first) fx[e] *= silu(fz[e]);
+        if (!a.norm_first) fx[e] *= silu<E>(fz[e]);
         sum = fmaf(fx[e], fx[e], sum);
       }
     }
@@ -277,7 +287,7 @@ __global__ void __launch_bounds__(TEAM == 0 ? 1024 : 256, NV * IT == 4 && TEAM !
       load_vec<E, VEC>(z + i, fz);
       load_weight<VEC>(w + i, fw);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) fw[e] = a.norm_first ? fx[e] * r * fw[e] * silu(fz[e]) : fx[e] * silu(fz[e]) * r * fw[e];
+      for (int e = 0; e < VEC; ++e) fw[e] = a.norm_first ? fx[e] * r * fw[e] * silu<E>(fz[e]) : fx[e] * silu<E>(fz[e]) * r * fw[e];
       store_vec<E, VEC>(out + i, fw);
     }
   }
