@@ -31,7 +31,8 @@ constexpr int kVerifyBlocks = 4;  // an SM: 3 took 15 us for 12 (64 rows) and 64
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxParts = 8;  // blocks of a cluster (the portable most)
 constexpr int kRuns = 8;      // a warp's part of a row is summed in 8 runs
-constexpr int kMaxVocab = 1 << 25;  // 8 warps' lanes then sum at most 2^14 values in a run
+constexpr int kMaxVocab = 1 << 25;
+constexpr int kMaxPart = 1 << 24;  // values of a block: its 8 warps' lanes then sum about 2^13 in a run, fewer than 2^14
 
 template <typename P>
 __device__ __forceinline__ float prob(P x);
@@ -55,8 +56,8 @@ __device__ __forceinline__ float prob<__half>(__half x) {
 // in its fraction, and the remainder (exact) + 2^-13 the next 18 bits.  The
 // sums' words are added as they are, two values an instruction, and the
 // constants' bits taken off at the end: a lane's part of a row has fewer than
-// 2^14 values (kMaxVocab), so neither sum passes 32 bits.  (The 64-bit
-// conversion instruction runs at a fraction of these rates.)
+// 2^14 values (kMaxPart), so neither sum passes 32 bits even where all are 1.
+// (The 64-bit conversion instruction runs at a fraction of these rates.)
 using pair = unsigned long long;
 __device__ __forceinline__ pair pack2(float lo, float hi) {
   pair d;
@@ -468,11 +469,13 @@ extern "C" rssm_status rssm_verify(const void* target, int64_t target_stride, co
   a.accepted = accepted;
   a.next = next;
   a.err = error_word;
-  // blocks of a row: as many as still run all at once, each with 4096 values at least
+  // blocks of a row: as many as still run all at once, each with 4096 values at
+  // least; and two where one would have more than kMaxPart
   const int sms = num_sms();
   if (sms == 0) return RSSM_ERR_CUDA;
   int parts = 1;
   while (parts < kMaxParts && static_cast<long long>(batch) * parts * 2 <= kVerifyBlocks * sms && vocab > parts * 4096) parts *= 2;
+  if (vocab > kMaxPart && parts == 1) parts = 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = prob_dtype == RSSM_F32    ? launch_verify<float>(a, parts, st)
                         : prob_dtype == RSSM_BF16 ? launch_verify<__nv_bfloat16>(a, parts, st)
