@@ -105,14 +105,17 @@ struct Residual {
   const P* p;
   const P* q;
   int token, vocab, off;
-  Weight certain;  // the target's weight at `token`
+  unsigned long long certain;  // what a certain draft takes off the target's weight at `token`: all of it, of an entry up to 1
   int skew;  // values of q's 16 bytes before a piece: 0 if q's row has p's alignment
 
   __device__ __forceinline__ void set(const P* target, const P* draft, int tok, float at_tok, int v) {
     p = target;
     q = draft;
     token = tok;
-    certain.add(__saturatef(at_tok));
+    Weight all, left;
+    all.add(__saturatef(at_tok));
+    left.add(__saturatef(at_tok - 1.0f));
+    certain = all.value() - left.value();
     vocab = v;
     off = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(P));
     skew = q ? static_cast<int>((reinterpret_cast<uintptr_t>(q - off) & 15u) / sizeof(P)) : 0;
@@ -217,11 +220,11 @@ struct Residual {
     }
   }
   // what to take off the lane's weight of the step at position j that holds a
-  // certain draft's token, whose weight is 0: steps() does not look for it
-  // where it reads 16 bytes a lane
+  // certain draft's token: steps() does not look for it where it reads 16 bytes
+  // a lane
   __device__ __forceinline__ unsigned long long taken(int j, int lane) const {
     const bool mine = static_cast<unsigned>(token - (j - off + lane * VEC)) < static_cast<unsigned>(VEC);
-    return token >= 0 && mine && plain(j) ? certain.value() : 0ull;
+    return token >= 0 && mine && plain(j) ? certain : 0ull;
   }
 };
 

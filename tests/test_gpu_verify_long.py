@@ -61,3 +61,24 @@ def test_weights_of_one(monkeypatch):
     assert got == ([1] * B, [int(x * V) for x in un])
     wide = torch.ones(B, V + 8, dtype=torch.bfloat16, device="cuda")[:, 5 : V + 5]  # rows that do not start on 16 bytes
     assert verify(wide, None, zero, torch.zeros(B, device="cuda"), torch.tensor(un, device="cuda"), 1) == got
+
+
+@pytest.mark.parametrize("rows", [1, 200])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_certain_draft_above_one(dtype, rows):
+    """A rejected certain draft whose entry is 3: what is left of it is 2, a weight of one, wherever it stands."""
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    V = 17001
+    places = [0, 7, 128, 1023, 4100, 8192, 12345, V - 1]
+    for i in range(len(places) if rows == 1 else 1):
+        tokens = torch.tensor([places[(b // 2 + i) % len(places)] for b in range(2 * rows)], dtype=torch.int32, device="cuda")
+        target = torch.softmax(torch.randn(rows * 2, V, generator=gen, device="cuda"), -1)
+        target.scatter_(1, tokens[:, None].long(), 3.0)
+        target = target.to(dtype)
+        un = torch.rand(rows, generator=gen, device="cuda")
+        u = torch.full((2 * rows,), 4.0, device="cuda")
+        accepted, nxt = verify(target, None, tokens, u, un, 2)
+        t = target.float().cpu()
+        for b in range(rows):
+            want = verify_row(t[2 * b : 2 * b + 2], None, tokens[2 * b : 2 * b + 2].cpu(), u[:2].cpu(), un[b].cpu())
+            assert (accepted[b], nxt[b]) == want, b
