@@ -550,6 +550,11 @@ __global__ void __launch_bounds__(128, 4)
   fence_async();
   tc_before();
   const bool all_ok = __syncthreads_and(ok) != 0;
+  if (!all_ok) {  // once more, with their limits: neither copies nor products must outlive the block
+    if (tid == 0)
+      for (int x = 0; x < 3; ++x) mbar_wait(bars + x, 0);
+    __syncthreads();
+  }
   tc_after();
   release();
   if (tid == 0) {

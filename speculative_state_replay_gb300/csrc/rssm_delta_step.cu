@@ -161,7 +161,10 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(F32)) delta_step_
   }
   if (!ok) {
     cp_async_wait_all();
-    if (r0 < dv) mbar_wait(&wm.bar, 0);  // nothing is in flight at the end
+    if (r0 < dv && !mbar_wait(&wm.bar, 0)) {  // nothing is in flight at the end
+      if (lane == 0) set_error(a.c.err, RSSM_ERRBIT_TIMEOUT);
+      mbar_wait(&wm.bar, 0);
+    }
     zeros();
     return;
   }
@@ -221,6 +224,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, step_blocks(F32)) delta_step_
     }
     if (!__all_sync(full, mbar_wait(&wm.bar, parity))) {
       if (lane == 0) set_error(a.c.err, RSSM_ERRBIT_TIMEOUT);
+      mbar_wait(&wm.bar, parity);  // once more, with its limit: the copy must not outlive the block
       return;
     }
     parity ^= 1;
