@@ -426,7 +426,10 @@ typedef struct {
   int32_t dkey;        /* 64 or 128 */
   int32_t dvalue;      /* a multiple of 16, at most 1024 */
   int32_t npredicted;  /* most tokens a step has, 1..8 */
-  int32_t state_dtype; /* RSSM_F32 or RSSM_BF16 (rounded to nearest when stored; all arithmetic is in fp32) */
+  /* RSSM_F32 or RSSM_BF16 (rounded to nearest when stored).  Sums, decays and the
+   * state while a call works on it are fp32; products take bf16 inputs as they
+   * are, an fp32 state whole in rssm_delta_step, and for rssm_delta_prefill see there */
+  int32_t state_dtype;
   void *state;   int64_t state_slot_stride;  /* [slot][nvheads][dvalue][dkey] */
   void *pend_k;  int64_t pend_k_slot_stride; /* bf16 [slot][2][nkheads][npredicted][dkey]: keys as given */
   float *pend_w; int64_t pend_w_slot_stride; /* f32 [slot][2][nvheads][npredicted][dvalue]: corrections u_t (over |k_t| with l2norm) */
@@ -490,6 +493,13 @@ rssm_status rssm_delta_step(const rssm_delta_cache *cache, const void *q, int64_
  *           an earlier row's bound, are skipped (RSSM_ERRBIT_SEQLEN)
  *   initial [batch] i32 or NULL: nonzero rows start from their slot's state
  *           (a prompt that comes in parts), the others from zero
+ * Precision: products take factors that are not bf16 inputs -- the state, the
+ * solve within 64 tokens, its right sides -- in 16 significant bits and sum in
+ * fp32.  Outputs do not show it.  An fp32 state ends 3e-7 of its norm from the
+ * exact one where keys are random, and up to 1.5e-5 where they are alike
+ * (correlation 0.95), rates near 1 and decays near none; token by token in fp32
+ * it would be 1e-7 to 4e-7.  A caller who needs that can give the prompt to
+ * rssm_delta_step, eight accepted tokens at a time.
  * Drafts that wait in a slot are dropped.  What is not finite reaches all of the
  * 64 tokens of a prompt that are worked on together, and those after them; no
  * other head and no other prompt.

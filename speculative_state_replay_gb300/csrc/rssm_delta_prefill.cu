@@ -20,14 +20,19 @@
 // Precision: products run in bf16 with fp32 accumulation.  Keys, queries and
 // values are exact; fp32 factors (S, A, T, P T, R, U) are carried as bf16 hi +
 // lo, 16 significant bits, and the product of two lo parts (2^-18 of the term)
-// is dropped.  For an fp32 state U is R + (T - I) R, R added in fp32, so that of
-// random keys only a quarter of U has these errors, and U, which the state sums,
-// goes in three parts, which is all of it: of a prompt of 16384 random tokens
-// the state is 2.0e-7 of its norm off, 644 us.  Without both it was 3e-6 off in
-// 602 us, which is enough for a bf16 state: that is rounded to 2^-9.  Outputs
-// are rounded to bf16 once.  (P T rounded to bf16 would save a quarter of the
-// scratch traffic, but of a prompt of few tokens all outputs would share its
-// error: up to 2^-8 more.)
+// is dropped.  For an fp32 state U is R + (T - I) R, R added in fp32, and U, which
+// the state sums, goes in three parts, which is all of it.  Of a prompt of 16384
+// tokens with random keys the state is then 2.0e-7 of its norm off, 637 us; without
+// both it was 3e-6 off in 602 us, which is enough for a bf16 state: that is rounded
+// to 2^-9.  What is left comes from T - I, R and S alike, and grows with T - I:
+// 1000 tokens whose keys are correlated by 0.7 (0.95) leave the state 1.5e-6
+// (2e-6) off, and with rates above 0.9 and hardly a decay 6e-6 (1.5e-5), where
+// fp32 token by token is 1e-7 .. 3e-7.  Three parts of all of them would be as
+// exact, with half as many operand bytes again for the chain and 32 KB more shared
+// memory, which blocks of 64 value columns do not have: rssm_delta_step is the call
+// for that.  Outputs are rounded to bf16 once.  (P T rounded to bf16 would save a
+// quarter of the scratch traffic, but of a prompt of few tokens all outputs would
+// share its error: up to 2^-8 more.)
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

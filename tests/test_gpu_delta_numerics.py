@@ -174,3 +174,42 @@ def test_a_nan_decay_in_a_prompt(gen):
     assert off(out[:150, 0], ref[0][0][:, 0]) <= 2.0**-8 and off(out[:64, 1], ref[0][0][:64, 1]) <= 2.0**-8
     assert off(out[150:], ref[1][0]) <= 2.0**-8
     assert off(cache.state[1, 0], ref[0][2][0]) <= 1e-5 and off(cache.state[2], ref[1][2]) <= 1e-5
+
+
+@pytest.mark.parametrize("n", [77, 300])
+@pytest.mark.parametrize("corr", [0.7, 0.95])
+def test_prompts_of_correlated_keys(gen, n, corr):
+    """Prompts take fp32 factors in 16 significant bits (include/rssm.h): a factor is at most 2^-17 off, a product of two
+    2^-16, and the solve multiplies that by its own size, about one where keys are normalised and rates below one.
+    2^-15 of an fp32 state's norm; outputs do not show it (2^-8 as everywhere)."""
+    hk, hv, dk, dv = 2, 4, 128, 64
+    q, k = ((corr * rnd(gen, 1, hk, dk) + math.sqrt(1 - corr * corr) * rnd(gen, n, hk, dk)).to(BF) for _ in range(2))
+    v = rnd(gen, n, hv, dv).to(BF)
+    g, beta = -0.02 * torch.rand(n, hv, generator=gen, device="cuda"), 0.9 + 0.1 * torch.rand(n, hv, generator=gen, device="cuda")
+    cache = api.DeltaCache(2, hk, hv, dk, dv, 2)
+    out = torch.empty(n, hv, dv, dtype=BF, device="cuda")
+    api.rssm_delta_prefill(cache, q, k, v, g, beta, torch.ones(1, dtype=torch.int32, device="cuda"),
+                           torch.tensor([0, n], dtype=torch.int32, device="cuda"), out, api.alloc_delta_scratch(cache, 1, n), l2norm=True)
+    o, _, S = delta_tokens(torch.zeros(hv, dv, dk, device="cuda"), q, k, v, g, beta, dk**-0.5, True)
+    assert off(out, o) <= 2.0**-8 and off(cache.state[1], S) <= 2.0**-15
+
+
+@pytest.mark.parametrize("corr", [0.0, 0.95])
+def test_steps_of_correlated_keys(gen, corr):
+    """The same tokens by steps of 8, all accepted, keep fp32: 136 terms a product and a decay a commit, each a few 2^-24
+    off, over 19 commits: 2e-6."""
+    hk, hv, dk, dv, n = 2, 4, 128, 64, 152
+    q, k = ((corr * rnd(gen, 1, hk, dk) + math.sqrt(1 - corr * corr) * rnd(gen, n, hk, dk)).to(BF) for _ in range(2))
+    v = rnd(gen, n, hv, dv).to(BF)
+    g, beta = -0.02 * torch.rand(n, hv, generator=gen, device="cuda"), 0.9 + 0.1 * torch.rand(n, hv, generator=gen, device="cuda")
+    cache = api.DeltaCache(2, hk, hv, dk, dv, 8)
+    scratch, slot = api.alloc_delta_scratch(cache, 1, 8), torch.ones(1, dtype=torch.int32, device="cuda")
+    out = torch.empty(n, hv, dv, dtype=BF, device="cuda")
+    for at in range(0, n, 8):
+        x = [t[at : at + 8] for t in (q, k, v, g, beta)]
+        api.rssm_delta_step(cache, *x, slot, slot * (8 if at else 0), 8, out[at : at + 8], scratch, l2norm=True)
+    none = [t[:0] for t in (q, k, v, g, beta)]
+    api.rssm_delta_step(cache, *none, slot, slot * 8, 8, out[:0], scratch, l2norm=True,
+                        cu_seqlens=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    o, _, S = delta_tokens(torch.zeros(hv, dv, dk, device="cuda"), q, k, v, g, beta, dk**-0.5, True)
+    assert off(out, o) <= 2.0**-8 and off(cache.state[1], S) <= 2e-6
