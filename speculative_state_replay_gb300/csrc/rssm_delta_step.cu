@@ -21,8 +21,8 @@ struct DeltaStepArgs {
 
 constexpr int kStepWarps = 4;
 constexpr int kStepRows = kStepWarps * 16;  // value rows of a tile
-// blocks an SM: 2-byte states 431 us with 4, 452 with 3 (1024 rows); fp32 states
-// keep 64 values a lane and spill with 4: 82 us, 54 with 3 (64 rows)
+// blocks an SM: 2-byte states 438 us with 4, 464 with 3, 454 with 5 (1024 rows);
+// fp32 states keep 64 values a lane and spill with 4: 81 us, 58 with 3 (64 rows)
 constexpr int step_blocks(bool f32) { return f32 ? 3 : 4; }
 
 // A warp's item on its way from memory: its state rows (a bulk copy) and, for
