@@ -496,10 +496,10 @@ rssm_status rssm_delta_step(const rssm_delta_cache *cache, const void *q, int64_
  * Precision: products take factors that are not bf16 inputs -- the state, the
  * solve within 64 tokens, its right sides -- in 16 significant bits and sum in
  * fp32.  Outputs do not show it.  An fp32 state ends 3e-7 of its norm from the
- * exact one where keys are random, and up to 1.5e-5 where they are alike
- * (correlation 0.95), rates near 1 and decays near none; token by token in fp32
- * it would be 1e-7 to 4e-7.  A caller who needs that can give the prompt to
- * rssm_delta_step, eight accepted tokens at a time.
+ * exact one where keys are random (2e-6 if rates are near 1 and decays near none),
+ * and up to 1.5e-5 where keys are alike as well (correlation 0.95); token by token
+ * in fp32 it would be 1e-7 to 4e-7.  A caller who needs that can give the prompt
+ * to rssm_delta_step, eight accepted tokens at a time.
  * Drafts that wait in a slot are dropped.  What is not finite reaches all of the
  * 64 tokens of a prompt that are worked on together, and those after them; no
  * other head and no other prompt.

@@ -309,7 +309,7 @@ def _s(fn, stream, d):
         _refuse(fn, f"the tensors' device, {d}, is not the current one")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(d)
-    if stream.device_index != d:
+    if getattr(stream, "device_index", d) != d:  # (any object with a handle is a stream)
         _refuse(fn, "the stream is another device's")
     return stream.cuda_stream
 

@@ -111,3 +111,31 @@ def test_scratch(library):
     with pytest.raises(ValueError):
         f(**tensors, **rest)
     assert library.calls == 0
+
+
+class Handle:
+    cuda_stream = 0
+
+
+def test_streams(library):
+    """Any object with a handle is a stream, as for the other calls."""
+    for i in range(5):
+        f, tensors, rest = calls()[i]
+        f(**tensors, **rest, stream=Handle())
+    assert library.calls == 5
+
+
+@pytest.mark.gpu
+def test_a_given_stream():
+    x = torch.randn(40, 512, device="cuda")
+    w, out, here = torch.ones(512, device="cuda"), torch.empty_like(x), torch.empty_like(x)
+    api.rssm_gated_norm(x, x, w, here)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    api.rssm_gated_norm(x, x, w, out, stream=st)
+    st.synchronize()
+    assert torch.equal(out, here)
+    with pytest.raises(ValueError):
+        api.rssm_gated_norm(x.cpu(), x, w, out)
+    with pytest.raises(ValueError):
+        api.rssm_gated_norm(x, x, w.cpu(), out)
