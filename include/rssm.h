@@ -107,6 +107,8 @@ typedef enum { RSSM_ROUND_NEAREST = 0, RSSM_ROUND_STOCHASTIC = 1 } rssm_rounding
 #define RSSM_ERRBIT_ACCEPT 4u  /* accepted < 0 or > the row's token count */
 #define RSSM_ERRBIT_TIMEOUT 8u /* a kernel gave up waiting on its own copy pipeline */
 #define RSSM_ERRBIT_TOKEN 16u  /* rssm_verify: a drafted token id outside the vocabulary, or a row with no mass */
+#define RSSM_ERRBIT_TREE 32u   /* a drafted token whose parent is not one of the tokens before it in its row */
+#define RSSM_ERRBIT_PAGE 64u   /* a position past a row's page table, or a page id outside the cache */
 
 /*
  * The cache of all slots.  Layouts follow the ring-buffer cache contract of
@@ -569,6 +571,188 @@ rssm_status rssm_residual_norm(const void *x, int64_t x_stride, const void *resi
                                float alpha, const float *weight, int64_t rows, int32_t dim, float eps,
                                void *residual_out, int64_t residual_out_stride, void *out, int64_t out_stride,
                                void *stream);
+
+/* ------------------------------------------------------------------------
+ * Operators of a hybrid model's attention layers and of its sampler: a paged
+ * cache of keys and values, attention of drafted tokens over it, the commit of
+ * the drafts that a verification accepted, and the step from logits to the
+ * probabilities that rssm_verify takes.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * The keys and values of all attention layers, in pages of page_size tokens.
+ * A page belongs to one row at a time and has the same id in every layer.
+ * Strides are in elements; a page's part of a layer is dense:
+ *   k, v             [layer][page][nheads][page_size][head_dim] of `format`
+ *   k_scale, v_scale f32 [layer][page][nheads][page_size] (8-bit formats)
+ * A value is code * scale, one fp32 rounding.  Codes are written with scale = amax
+ * times 1/127 (int8) or 1/448 (e4m3), amax that of a token's head (scale 1 where
+ * it is below 2^-100), and code = nearest of x * (1 / scale), ties to even, each
+ * operation and constant rounded to fp32.  A token's head
+ * with a value that is not finite gets the scale NaN and the codes 0: it reads
+ * back as NaN throughout.  e4m3 codes that a caller writes must not be NaN.
+ *
+ * Rows find their pages in a table, pages [batch][pages_stride] i32, whose first
+ * max_pages entries of a row are its pages in order: the token at position i is
+ * token i % page_size of page pages[b][i / page_size].  Entries past a row's last
+ * token are not read.  lengths [batch] i32 are the committed tokens: a step's new
+ * tokens lie at lengths[b], lengths[b] + 1, .. until an acceptance has moved those
+ * that stay, and the caller then adds `accepted` to lengths, once for all layers.
+ * Rows of lengths[b] < 0 are padding.
+ */
+typedef struct {
+  int32_t num_pages;
+  int32_t nlayers;
+  int32_t nheads;    /* heads of keys and values */
+  int32_t head_dim;  /* 64, 128 or 256 */
+  int32_t page_size; /* a multiple of 16, at most 65536 */
+  int32_t format;    /* RSSM_BF16, RSSM_I8 or RSSM_E4M3 */
+  void *k;        int64_t k_layer_stride, k_page_stride;
+  void *v;        int64_t v_layer_stride, v_page_stride;
+  float *k_scale; int64_t k_scale_layer_stride, k_scale_page_stride;
+  float *v_scale; int64_t v_scale_layer_stride, v_scale_page_stride;
+  uint32_t *error_word;
+} rssm_kv_cache;
+
+/*
+ * Writes the keys and values of new tokens: token t of row b goes to position
+ * lengths[b] + t of layer `layer`.
+ *   k, v bf16 [tok][nheads][head_dim]: *_stride elements between tokens (multiples
+ *        of 8; 16-byte aligned pointers), heads contiguous
+ *   cu_seqlens [batch+1] i32 or NULL (T tokens a row);  T: most tokens of a row
+ *   tokens: token rows of k and v;  max_pages: entries of a row of `pages`
+ * Tokens behind the last row are not written.  Token counts that are negative or
+ * more than T, and bounds past `tokens`: RSSM_ERRBIT_SEQLEN, the row is skipped.
+ * Positions past the page table and pages outside the cache: RSSM_ERRBIT_PAGE,
+ * the token is skipped.  Two tokens of a call must not meet in one place of a page.
+ */
+rssm_status rssm_kv_append(const rssm_kv_cache *cache, int32_t layer, const void *k, int64_t k_stride, const void *v,
+                           int64_t v_stride, const int32_t *pages, int64_t pages_stride, int32_t max_pages,
+                           const int32_t *lengths, const int32_t *cu_seqlens, int32_t batch, int32_t T, int64_t tokens,
+                           void *stream);
+
+/*
+ * Reads tokens back: token i of row b is the one at position starts[b] + i (i if
+ * starts is NULL), as the value it stands for, rounded once to out_dtype.
+ *   cu_seqlens [batch+1] i32: the rows' tokens among the outputs
+ *   k_out, v_out [tok][nheads][head_dim] of out_dtype (F32, BF16, F16),
+ *        *_stride elements between tokens (16-byte aligned rows); tokens: their rows
+ * Rows of starts[b] < 0 are padding: their outputs and those of tokens that lie
+ * past the page table or in no page (RSSM_ERRBIT_PAGE) are zeros.  Outputs behind
+ * the last row, and those of rows whose bounds fall or pass `tokens`
+ * (RSSM_ERRBIT_SEQLEN), stay as they are.
+ */
+rssm_status rssm_kv_read(const rssm_kv_cache *cache, int32_t layer, const int32_t *pages, int64_t pages_stride,
+                         int32_t max_pages, const int32_t *starts, const int32_t *cu_seqlens, int32_t batch,
+                         int64_t tokens, int32_t out_dtype, void *k_out, int64_t k_stride, void *v_out,
+                         int64_t v_stride, void *stream);
+
+/* Bytes of scratch for rssm_tree_attention with nqheads heads of queries, whatever
+ * the batch and the lengths; 0 for an invalid cache.  Zero the buffer once when it
+ * is allocated; every call leaves its counters at zero.  One buffer serves all
+ * layers and calls on one stream; calls that overlap on the GPU, captured ones too,
+ * need scratch of their own. */
+size_t rssm_attention_scratch_bytes(const rssm_kv_cache *cache, int32_t nqheads);
+
+/*
+ * Attention of a row's new tokens over its cached ones, which hold the new tokens
+ * themselves (rssm_kv_append first).  For token t of row b and query head h, over
+ * keys and values of head h / (nqheads / nheads):
+ *   out = sum_i p_i v_i,  p = softmax over the tokens that t sees of scale q . k_i
+ * t sees the committed tokens, itself, and of the new tokens before it
+ *   parents NULL   all (a chain of drafts, or a part of a prompt)
+ *   parents        those on its path: parents[tok] is the place in the row of the
+ *                  token that tok comes after, -1: it follows the committed ones.
+ *                  Trees have up to 64 tokens a row; a parent that is not before
+ *                  its token: RSSM_ERRBIT_TREE and zeros for the row
+ *   q, out bf16 [tok][nqheads][head_dim]: *_stride elements between tokens
+ *        (multiples of 8; 16-byte aligned), heads contiguous
+ *   T: most tokens of a row (at most 64 with parents);  tokens: rows of q and out
+ * Scores, statistics and sums are fp32; the probabilities enter the product with
+ * the values in 8 significant bits for a bf16 cache, in 11 for 8-bit ones.  Rows
+ * of lengths[b] < 0 get zeros; rows past their page table get zeros and
+ * RSSM_ERRBIT_PAGE; tokens in a page outside the cache are not seen
+ * (RSSM_ERRBIT_PAGE).  Bad token counts: RSSM_ERRBIT_SEQLEN, outputs untouched, as
+ * are those behind the last row.  What a token does not see does not reach it,
+ * whatever it holds.  How the work is cut, and so the order of sums, follows from
+ * the batch's lengths and the grid; the same call gives the same bits.
+ */
+rssm_status rssm_tree_attention(const rssm_kv_cache *cache, int32_t layer, const void *q, int64_t q_stride,
+                                int32_t nqheads, float scale, const int32_t *pages, int64_t pages_stride,
+                                int32_t max_pages, const int32_t *lengths, const int32_t *parents,
+                                const int32_t *cu_seqlens, int32_t batch, int32_t T, int64_t tokens, void *out,
+                                int64_t out_stride, void *scratch, size_t scratch_bytes, void *stream);
+
+/*
+ * Verification of a tree of drafts by the target's own draws, and the commit of
+ * what it accepts.  drawn[tok] is the token drawn from the target's distribution
+ * after tok (rssm_verify with one token a row draws it; the arg max if greedy).
+ * From the row's first token, which is always accepted, the walk goes on to the
+ * first token whose parent is the current one and whose id was drawn there, until
+ * there is none:
+ *   accepted[b]  tokens on the path;  next[b]  what was drawn after the last of them
+ *   path [batch][T] i32: their places in the row, -1 after the last
+ * and in every layer of `cache` (NULL: no cache) the keys and values at lengths[b] +
+ * path[j] move to lengths[b] + j, codes and scales as they are.  T is 1..64.
+ * parents NULL: a chain.  Padding rows (lengths[b] < 0) and rows without tokens:
+ * accepted 0, next -1.  So are rows of bad token counts (RSSM_ERRBIT_SEQLEN), of
+ * parents that are not before their token (RSSM_ERRBIT_TREE), and rows that pass
+ * their page table or have an accepted token in a page outside the cache
+ * (RSSM_ERRBIT_PAGE); nothing of theirs moves.
+ * Without a cache pages and lengths may be NULL, and errors go to error_word (NULL:
+ * nowhere); with one they go to the cache's and error_word is not used.
+ */
+rssm_status rssm_tree_accept(const rssm_kv_cache *cache, const int32_t *pages, int64_t pages_stride, int32_t max_pages,
+                             const int32_t *lengths, const int32_t *tokens, const int32_t *parents,
+                             const int32_t *drawn, const int32_t *cu_seqlens, int32_t batch, int32_t T, int64_t ntok,
+                             int32_t *accepted, int32_t *next, int32_t *path, uint32_t *error_word, void *stream);
+
+/*
+ * From logits to the probabilities that rssm_verify takes.  Row tok (of request b)
+ * with logits x; c_i is how often id i is in the request's output, history
+ * [prompt_len[b], history_len[b]) and the fed tokens on tok's path, and i was seen
+ * if that or the prompt, history [0, prompt_len[b]), holds it:
+ *   x_i <- x_i > 0 ? x_i / repetition : x_i * repetition      if i was seen
+ *   x_i <- x_i - (presence + frequency * c_i)                  if c_i > 0
+ *   x_i <- x_i + bias of i in request b (entries of one id add up, in order)
+ *   x_i <- -inf where bit i % 32 of mask word i / 32 is 0, or x_i is NaN
+ *   x_i <- x_i / temperature
+ *   probs = 1: out = softmax(x), 0: out = x
+ * in fp32, rounded once.  Temperature 0 (probs = 1): 1 at the largest x_i, the
+ * lowest id of equal ones; with probs = 0 nothing is divided.  Entries of +inf share
+ * the probability evenly.  A row of which nothing is left gets zeros.
+ *   logits, out [tok] rows of vocab values (F32, BF16, F16 each), *_stride elements
+ *        between rows; out may be logits if type and stride are the same
+ *   vocab 1..2^18;  T 1..64: most tokens of a request;  ntok: rows of logits
+ *   temperature, repetition, presence, frequency f32 [batch] or NULL (1, 1, 0, 0);
+ *        a repetition of 0 or less, a temperature below 0, or one that is NaN counts as 1
+ *   history i32 [batch][history_stride], of which a row's first history_max may be
+ *        tokens; history_len, prompt_len i32 [batch]; NULL: none, no prompt.  Lengths
+ *        are held to 0 .. history_max, a prompt's to its history's; ids outside the
+ *        vocabulary are not counted
+ *   tokens i32 [ntok] or NULL: the fed tokens;  parents as in rssm_tree_attention
+ *   bias_start i32 [batch+1], bias_id i32, bias_value f32 [biases], or NULL; entries
+ *        outside the vocabulary, and past `biases`, are left out
+ *   mask u32 [tok][mask_stride] or NULL
+ * Bad token counts: RSSM_ERRBIT_SEQLEN, the request's rows untouched, as are rows
+ * behind the last.  Bad parents: RSSM_ERRBIT_TREE, only the token itself counts of
+ * the fed ones.  error_word may be NULL.
+ */
+typedef struct {
+  const void *logits;         int64_t logits_stride; int32_t logits_dtype;
+  void *out;                  int64_t out_stride;    int32_t out_dtype;
+  int32_t vocab, batch, T, probs;
+  int64_t ntok;
+  const int32_t *cu_seqlens;
+  const float *temperature, *repetition, *presence, *frequency;
+  const int32_t *history;     int64_t history_stride; int32_t history_max;
+  const int32_t *history_len, *prompt_len;
+  const int32_t *tokens, *parents;
+  const int32_t *bias_start, *bias_id; const float *bias_value; int64_t biases;
+  const uint32_t *mask;       int64_t mask_stride;
+  uint32_t *error_word;
+} rssm_logits_args;
+rssm_status rssm_logits(const rssm_logits_args *args, void *stream);
 
 #ifdef __cplusplus
 }

@@ -10,6 +10,7 @@ LIB_PATH = os.path.join(HERE, "librssm.so")
 _lock = threading.Lock()
 _lib = None
 _fast = None
+_fast_kv = None
 
 
 class RssmCacheStruct(ctypes.Structure):
@@ -49,10 +50,44 @@ class RssmDeltaCacheStruct(ctypes.Structure):
     ]
 
 
+class RssmKvCacheStruct(ctypes.Structure):
+    """Mirror of `rssm_kv_cache` in include/rssm.h."""
+
+    _fields_ = [
+        ("num_pages", ctypes.c_int32), ("nlayers", ctypes.c_int32), ("nheads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32), ("format", ctypes.c_int32),
+        ("k", ctypes.c_void_p), ("k_layer_stride", ctypes.c_int64), ("k_page_stride", ctypes.c_int64),
+        ("v", ctypes.c_void_p), ("v_layer_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64),
+        ("k_scale", ctypes.c_void_p), ("k_scale_layer_stride", ctypes.c_int64), ("k_scale_page_stride", ctypes.c_int64),
+        ("v_scale", ctypes.c_void_p), ("v_scale_layer_stride", ctypes.c_int64), ("v_scale_page_stride", ctypes.c_int64),
+        ("error_word", ctypes.c_void_p),
+    ]
+
+
+class RssmLogitsArgs(ctypes.Structure):
+    """Mirror of `rssm_logits_args` in include/rssm.h."""
+
+    _fields_ = [
+        ("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_int64), ("logits_dtype", ctypes.c_int32),
+        ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64), ("out_dtype", ctypes.c_int32),
+        ("vocab", ctypes.c_int32), ("batch", ctypes.c_int32), ("T", ctypes.c_int32), ("probs", ctypes.c_int32),
+        ("ntok", ctypes.c_int64), ("cu_seqlens", ctypes.c_void_p),
+        ("temperature", ctypes.c_void_p), ("repetition", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+        ("frequency", ctypes.c_void_p),
+        ("history", ctypes.c_void_p), ("history_stride", ctypes.c_int64), ("history_max", ctypes.c_int32),
+        ("history_len", ctypes.c_void_p),
+        ("prompt_len", ctypes.c_void_p), ("tokens", ctypes.c_void_p), ("parents", ctypes.c_void_p),
+        ("bias_start", ctypes.c_void_p), ("bias_id", ctypes.c_void_p), ("bias_value", ctypes.c_void_p),
+        ("biases", ctypes.c_int64), ("mask", ctypes.c_void_p), ("mask_stride", ctypes.c_int64),
+        ("error_word", ctypes.c_void_p),
+    ]
+
+
 EXPORTS = ("rssm_scratch_bytes", "rssm_init_state", "rssm_flush", "rssm_step", "rssm_step_precompute",
            "rssm_step_readout", "rssm_step_gated", "rssm_step_readout_gated", "rssm_flush_step", "rssm_flush_step_classify", "rssm_flush_step_main", "rssm_accept", "rssm_accept_flush", "rssm_eval_spec_math", "rssm_selftest_wait_timeout",
            "rssm_status_string", "rssm_delta_scratch_bytes", "rssm_delta_step", "rssm_delta_prefill", "rssm_verify",
-           "rssm_gated_norm", "rssm_residual_norm")
+           "rssm_gated_norm", "rssm_residual_norm", "rssm_kv_append", "rssm_kv_read", "rssm_attention_scratch_bytes",
+           "rssm_tree_attention", "rssm_tree_accept", "rssm_logits")
 
 
 def load(path: str | None = None):
@@ -110,6 +145,19 @@ def load(path: str | None = None):
         lib.rssm_residual_norm.restype = ctypes.c_int
         lib.rssm_residual_norm.argtypes = [vp, i64, vp, i64, i32, i32, vp, vp, f32, vp, i64, i32, f32, vp, i64, vp, i64,
                                            vp]
+        kp = ctypes.POINTER(RssmKvCacheStruct)
+        lib.rssm_kv_append.restype = ctypes.c_int
+        lib.rssm_kv_append.argtypes = [kp, i32, vp, i64, vp, i64, vp, i64, i32, vp, vp, i32, i32, i64, vp]
+        lib.rssm_kv_read.restype = ctypes.c_int
+        lib.rssm_kv_read.argtypes = [kp, i32, vp, i64, i32, vp, vp, i32, i64, i32, vp, i64, vp, i64, vp]
+        lib.rssm_attention_scratch_bytes.restype = sz
+        lib.rssm_attention_scratch_bytes.argtypes = [kp, i32]
+        lib.rssm_tree_attention.restype = ctypes.c_int
+        lib.rssm_tree_attention.argtypes = [kp, i32, vp, i64, i32, f32, vp, i64, i32, vp, vp, vp, i32, i32, i64, vp, i64, vp, sz, vp]
+        lib.rssm_tree_accept.restype = ctypes.c_int
+        lib.rssm_tree_accept.argtypes = [kp, vp, i64, i32, vp, vp, vp, vp, vp, i32, i32, i64, vp, vp, vp, vp, vp]
+        lib.rssm_logits.restype = ctypes.c_int
+        lib.rssm_logits.argtypes = [ctypes.POINTER(RssmLogitsArgs), vp]
         lib.rssm_status_string.restype = ctypes.c_char_p
         lib.rssm_status_string.argtypes = [ctypes.c_int]
         _lib = lib
@@ -126,3 +174,14 @@ def fast():
 
         _fast = _call
     return _fast
+
+
+def fast_kv():
+    """The same for the calls of attention layers and of the sampler (csrc/rssm_call_kv.c)."""
+    global _fast_kv
+    if _fast_kv is None:
+        load()
+        from . import _call_kv
+
+        _fast_kv = _call_kv
+    return _fast_kv

@@ -16,7 +16,7 @@ from . import _lib
 
 F32, BF16, F16, I8, E4M3, NVFP4 = 0, 1, 2, 3, 4, 5
 NEAREST, STOCHASTIC = 0, 1
-ERRBIT_PNAT, ERRBIT_SEQLEN, ERRBIT_ACCEPT, ERRBIT_TIMEOUT, ERRBIT_TOKEN = 1, 2, 4, 8, 16
+ERRBIT_PNAT, ERRBIT_SEQLEN, ERRBIT_ACCEPT, ERRBIT_TIMEOUT, ERRBIT_TOKEN, ERRBIT_TREE, ERRBIT_PAGE = 1, 2, 4, 8, 16, 32, 64
 DIM, DSTATE = 64, 128
 STATE_TORCH = {F32: torch.float32, BF16: torch.int16, F16: torch.int16, I8: torch.int8, E4M3: torch.uint8,
                NVFP4: torch.uint8}
@@ -535,5 +535,245 @@ def rssm_residual_norm(x, residual, weight, out, residual_out, post_weight=None,
         x.data_ptr(), sx, residual.data_ptr(), sr, _DTYPE[dtype], _DTYPE[rtype], _p(post_weight), _p(scale), alpha,
         weight.data_ptr(), rows, dim, eps, residual_out.data_ptr(), sro, out.data_ptr(), so,
         _s(fn, stream, lib.device(x, residual, weight, out, residual_out, post_weight, scale)))
+    if status:
+        raise RssmError(fn, status)
+
+
+# --------------------------------------------------------------------------
+# Operators of attention layers and of the sampler: the paged cache of keys and
+# values, attention over it, the commit of a tree's accepted drafts, and the step
+# from logits to probabilities.
+# --------------------------------------------------------------------------
+_KV_TORCH = {BF16: torch.bfloat16, I8: torch.int8, E4M3: torch.uint8}
+
+
+class KVCache:
+    """Keys and values of all attention layers in pages (rssm_kv_cache): k, v [layers][pages][heads][page_size][head_dim]
+    in bf16, or 8-bit codes (I8: int8, E4M3: uint8) with f32 scales [layers][pages][heads][page_size].  Tensors that a
+    program already has can be given instead of new ones; a page's part of a layer must be contiguous.  New scales are 1."""
+
+    def __init__(self, num_pages, kv_heads, head_dim, page_size, format=BF16, layers=1, device="cuda", k=None, v=None, k_scale=None,
+                 v_scale=None, error_word=None):
+        fn = "KVCache"
+        if format not in _KV_TORCH:
+            _refuse(fn, "format must be BF16, I8 or E4M3")
+        self.pages, self.H, self.D, self.page_size, self.format, self.layers = num_pages, kv_heads, head_dim, page_size, format, layers
+        dev = torch.device(device)
+        shape = (layers, num_pages, kv_heads, page_size, head_dim)
+
+        def make(name, t, shape, dtype, fill):
+            if t is None:
+                return torch.full(shape, fill, dtype=dtype, device=dev)
+            dense = [1] * len(shape)
+            for i in range(len(shape) - 2, 1, -1):
+                dense[i] = dense[i + 1] * shape[i + 1]
+            fits = tuple(t.shape) == shape and all(n == 1 or x == d for n, x, d in zip(shape[2:], t.stride()[2:], dense[2:]))
+            if t.dtype is not dtype or not fits:
+                _refuse(fn, f"{name} must be {dtype} {list(shape)}, contiguous within a page")
+            return t
+
+        self.k, self.v = make("k", k, shape, _KV_TORCH[format], 0), make("v", v, shape, _KV_TORCH[format], 0)
+        self.k_scale = self.v_scale = None
+        if format != BF16:
+            self.k_scale = make("k_scale", k_scale, shape[:-1], torch.float32, 1.0)
+            self.v_scale = make("v_scale", v_scale, shape[:-1], torch.float32, 1.0)
+        elif k_scale is not None or v_scale is not None:
+            _refuse(fn, "a bf16 cache has no scales")
+        if error_word is None:
+            error_word = torch.zeros(1, dtype=torch.int32, device=dev)
+        if error_word.element_size() != 4 or error_word.numel() < 1:
+            _refuse(fn, "error_word must be a tensor of one 32-bit word")
+        self.error_word = error_word
+        tensors = [t for t in (self.k, self.v, self.k_scale, self.v_scale, self.error_word) if t is not None]
+        if len({t.device for t in tensors}) > 1:
+            _refuse(fn, "tensors on different devices")
+        c = _lib.RssmKvCacheStruct()
+        c.num_pages, c.nlayers, c.nheads, c.head_dim, c.page_size, c.format = num_pages, layers, kv_heads, head_dim, page_size, format
+        for name in ("k", "v", "k_scale", "v_scale"):
+            t = getattr(self, name)
+            if t is not None:
+                # (a stride of a dimension of one element may be anything)
+                page = t.stride(1) if num_pages > 1 else t[0, 0].numel()
+                setattr(c, name, t.data_ptr())
+                setattr(c, name + "_page_stride", page)
+                setattr(c, name + "_layer_stride", t.stride(0) if layers > 1 else page * num_pages)
+        c.error_word = self.error_word.data_ptr()
+        self._struct = c
+        self._ref, self._addr = ctypes.byref(c), ctypes.addressof(c)
+
+    def struct(self):
+        return self._ref
+
+
+def _table(fn, pages, batch):
+    """Entries between the rows of a page table, and of a row."""
+    if pages.dtype is not torch.int32 or pages.dim() != 2 or pages.shape[0] < batch or (pages.shape[1] > 1 and pages.stride(1) != 1):
+        _refuse(fn, f"pages must be int32 [{batch}, pages of a row] with contiguous rows")
+    n = pages.shape[1]
+    return (pages.stride(0) if pages.shape[0] > 1 else n), n
+
+
+def _tokens(fn, name, t, dtype, n, h, d):
+    """Elements between the tokens of t [n, h, d]."""
+    if t.dtype is dtype and t.shape == (n, h, d):
+        st = t.stride()
+        if n == 0 or ((d == 1 or st[2] == 1) and (h == 1 or st[1] == d)):
+            return st[0] if n > 1 else h * d
+    _refuse(fn, f"{name} must be {dtype} [{n}, {h}, {d}] with contiguous heads")
+
+
+def rssm_kv_append(cache, k, v, pages, lengths, T, cu_seqlens=None, layer=0, stream=None):
+    """Writes new tokens' keys and values, bf16 [tok, kv_heads, head_dim], to the positions behind each row's `lengths`."""
+    fn = "rssm_kv_append"
+    n, batch = k.shape[0], lengths.numel()
+    sk, sv = _tokens(fn, "k", k, torch.bfloat16, n, cache.H, cache.D), _tokens(fn, "v", v, torch.bfloat16, n, cache.H, cache.D)
+    _ids(fn, "lengths", lengths, batch)
+    if cu_seqlens is not None:
+        _ids(fn, "cu_seqlens", cu_seqlens, batch + 1)
+    sp, np_ = _table(fn, pages, batch)
+    status = _lib.fast_kv().rssm_kv_append(
+        cache._addr, layer, k.data_ptr(), sk, v.data_ptr(), sv, pages.data_ptr(), sp, np_, lengths.data_ptr(), _p(cu_seqlens), batch, T, n,
+        _s(fn, stream, _lib.fast().device(k, v, pages, lengths, cu_seqlens, cache.k)))
+    if status:
+        raise RssmError(fn, status)
+
+
+def rssm_kv_read(cache, pages, cu_seqlens, k_out, v_out, starts=None, layer=0, stream=None):
+    """Reads tokens back, from position starts[b] (0) on: k_out, v_out [tok, kv_heads, head_dim] f32, bf16 or f16."""
+    fn = "rssm_kv_read"
+    n, batch, dtype = k_out.shape[0], cu_seqlens.numel() - 1, k_out.dtype
+    if dtype not in _DTYPE:
+        _refuse(fn, "k_out must be f32, bf16 or f16")
+    if batch < 0:
+        _refuse(fn, "cu_seqlens must hold one value at least")
+    sk, sv = _tokens(fn, "k_out", k_out, dtype, n, cache.H, cache.D), _tokens(fn, "v_out", v_out, dtype, n, cache.H, cache.D)
+    _ids(fn, "cu_seqlens", cu_seqlens, batch + 1)
+    if starts is not None:
+        _ids(fn, "starts", starts, batch)
+    sp, np_ = _table(fn, pages, batch)
+    status = _lib.fast_kv().rssm_kv_read(
+        cache._addr, layer, pages.data_ptr(), sp, np_, _p(starts), cu_seqlens.data_ptr(), batch, n, _DTYPE[dtype], k_out.data_ptr(), sk,
+        v_out.data_ptr(), sv, _s(fn, stream, _lib.fast().device(pages, cu_seqlens, k_out, v_out, starts, cache.k)))
+    if status:
+        raise RssmError(fn, status)
+
+
+def rssm_attention_scratch_bytes(cache: KVCache, query_heads: int) -> int:
+    return int(_lib.load().rssm_attention_scratch_bytes(cache.struct(), query_heads))
+
+
+def alloc_attention_scratch(cache: KVCache, query_heads: int) -> torch.Tensor:
+    """Scratch for rssm_tree_attention, whatever the batch and the lengths."""
+    n = rssm_attention_scratch_bytes(cache, query_heads)
+    if n == 0:
+        raise RssmError("rssm_attention_scratch_bytes", 1)
+    return torch.zeros(n, dtype=torch.uint8, device=cache.k.device)  # its counters start at zero
+
+
+def rssm_tree_attention(cache, q, pages, lengths, T, out, scratch, parents=None, cu_seqlens=None, scale=None, layer=0, stream=None):
+    """Attention of new tokens, which rssm_kv_append has written, over each row's cached ones: q, out bf16 [tok, heads, head_dim];
+    `parents` [tok] int32 for a tree of drafts (None: a chain); `scale` defaults to head_dim ** -0.5."""
+    fn = "rssm_tree_attention"
+    n, heads, batch = q.shape[0], q.shape[1], lengths.numel()
+    sq, so = _tokens(fn, "q", q, torch.bfloat16, n, heads, cache.D), _tokens(fn, "out", out, torch.bfloat16, n, heads, cache.D)
+    _ids(fn, "lengths", lengths, batch)
+    if parents is not None:
+        _ids(fn, "parents", parents, n)
+    if cu_seqlens is not None:
+        _ids(fn, "cu_seqlens", cu_seqlens, batch + 1)
+    sp, np_ = _table(fn, pages, batch)
+    status = _lib.fast_kv().rssm_tree_attention(
+        cache._addr, layer, q.data_ptr(), sq, heads, cache.D ** -0.5 if scale is None else scale, pages.data_ptr(), sp, np_,
+        lengths.data_ptr(), _p(parents), _p(cu_seqlens), batch, T, n, out.data_ptr(), so, scratch.data_ptr(), _scratch(fn, scratch),
+        _s(fn, stream, _lib.fast().device(q, pages, lengths, parents, cu_seqlens, out, scratch, cache.k)))
+    if status:
+        raise RssmError(fn, status)
+
+
+def rssm_tree_accept(cache, pages, lengths, tokens, parents, drawn, T, accepted, next_token, path, cu_seqlens=None, error_word=None,
+                     stream=None):
+    """Walks each row's tree of drafts along what was drawn after its tokens, and moves the accepted tokens' keys and values
+    of all layers into place; cache None (with pages, lengths None): the walk alone.  path [batch, T] int32."""
+    fn = "rssm_tree_accept"
+    n, batch = tokens.numel(), accepted.numel()
+    _ids(fn, "tokens", tokens, n)
+    _ids(fn, "drawn", drawn, n)
+    _ids(fn, "accepted", accepted, batch)
+    _ids(fn, "next_token", next_token, batch)
+    _ids(fn, "path", path, batch * T)
+    if parents is not None:
+        _ids(fn, "parents", parents, n)
+    if cu_seqlens is not None:
+        _ids(fn, "cu_seqlens", cu_seqlens, batch + 1)
+    if lengths is not None:
+        _ids(fn, "lengths", lengths, batch)
+    if cache is not None:
+        if pages is None or lengths is None:
+            _refuse(fn, "a cache needs pages and lengths")
+        sp, np_ = _table(fn, pages, batch)
+        at = cache.k
+    else:
+        pages, sp, np_, at = None, 0, 0, None
+        if error_word is not None and (error_word.element_size() != 4 or error_word.numel() < 1):
+            _refuse(fn, "error_word must be a tensor of one 32-bit word")
+    status = _lib.fast_kv().rssm_tree_accept(
+        None if cache is None else cache._addr, _p(pages), sp, np_, _p(lengths), tokens.data_ptr(), _p(parents), drawn.data_ptr(), _p(cu_seqlens),
+        batch, T, n, accepted.data_ptr(), next_token.data_ptr(), path.data_ptr(), None if cache is not None else _p(error_word),
+        _s(fn, stream, _lib.fast().device(tokens, drawn, accepted, next_token, path, parents, cu_seqlens, lengths, pages, at, error_word)))
+    if status:
+        raise RssmError(fn, status)
+
+
+def rssm_logits(logits, T, out, temperature=None, repetition=None, presence=None, frequency=None, history=None, history_len=None,
+                prompt_len=None, tokens=None, parents=None, bias_start=None, bias_id=None, bias_value=None, mask=None, cu_seqlens=None,
+                batch=None, probs=True, error_word=None, stream=None):
+    """Penalties, biases, grammar masks and temperature on logits [tok, vocab]; out: the probabilities that rssm_verify takes, or
+    (probs False) the processed logits.  `temperature` .. `frequency` [batch] f32; `history` [batch, most] int32 with `history_len`
+    and `prompt_len` [batch]; `tokens`, `parents` [tok]; biases by request: `bias_start` [batch + 1], `bias_id`, `bias_value`;
+    `mask` [tok, words of 32 ids] int32.  Without cu_seqlens and `batch`, requests of T tokens each."""
+    fn = "rssm_logits"
+    ntok, vocab = logits.shape
+    if logits.dtype not in _DTYPE or out.dtype not in _DTYPE:
+        _refuse(fn, "logits and out must be f32, bf16 or f16")
+    sl, so = _rows(fn, "logits", logits, logits.dtype, logits.shape), _rows(fn, "out", out, out.dtype, logits.shape)
+    if batch is None:
+        batch = cu_seqlens.numel() - 1 if cu_seqlens is not None else ntok // T if T > 0 else 0
+    if cu_seqlens is not None:
+        _ids(fn, "cu_seqlens", cu_seqlens, batch + 1)
+    for name, t in (("temperature", temperature), ("repetition", repetition), ("presence", presence), ("frequency", frequency)):
+        if t is not None:
+            _f32(fn, name, t, batch)
+    sh = width = 0
+    if history is not None:
+        if history_len is None:
+            _refuse(fn, "history needs history_len")
+        sh, width = _table(fn, history, batch)
+        _ids(fn, "history_len", history_len, batch)
+        if prompt_len is not None:
+            _ids(fn, "prompt_len", prompt_len, batch)
+    for name, t in (("tokens", tokens), ("parents", parents)):
+        if t is not None:
+            _ids(fn, name, t, ntok)
+    biases = 0
+    if bias_id is not None:
+        if bias_start is None or bias_value is None:
+            _refuse(fn, "bias_id needs bias_start and bias_value")
+        biases = bias_id.numel()
+        _ids(fn, "bias_start", bias_start, batch + 1)
+        _ids(fn, "bias_id", bias_id, biases)
+        _f32(fn, "bias_value", bias_value, biases)
+    sm = 0
+    if mask is not None:
+        if mask.dtype is not torch.int32 or mask.dim() != 2 or mask.shape[0] < ntok or 32 * mask.shape[1] < vocab or mask.stride(1) != 1:
+            _refuse(fn, f"mask must be int32 [{ntok}, {(vocab + 31) // 32}] with contiguous rows")
+        sm = mask.stride(0) if mask.shape[0] > 1 else mask.shape[1]
+    if error_word is not None and (error_word.element_size() != 4 or error_word.numel() < 1):
+        _refuse(fn, "error_word must be a tensor of one 32-bit word")
+    status = _lib.fast_kv().rssm_logits(
+        logits.data_ptr(), sl, _DTYPE[logits.dtype], out.data_ptr(), so, _DTYPE[out.dtype], vocab, batch, T, int(probs), ntok, _p(cu_seqlens),
+        _p(temperature), _p(repetition), _p(presence), _p(frequency), _p(history), sh, width, _p(history_len), _p(prompt_len), _p(tokens), _p(parents),
+        _p(bias_start), _p(bias_id), _p(bias_value), biases, _p(mask), sm, _p(error_word),
+        _s(fn, stream, _lib.fast().device(logits, out, temperature, repetition, presence, frequency, history, history_len, prompt_len, tokens,
+                                          parents, bias_start, bias_id, bias_value, mask, cu_seqlens, error_word)))
     if status:
         raise RssmError(fn, status)

@@ -2,8 +2,8 @@
 
 Each .cu file is compiled in parallel to an object, then linked into a shared
 library next to this file.  The CUDA runtime is linked statically, so the
-library needs only the driver at run time.  The binding's fast path (the module
-_call, plain C against the CPython API) is compiled next to it.
+library needs only the driver at run time.  The binding's fast path (the modules
+_call and _call_kv, plain C against the CPython API) is compiled next to it.
 """
 from __future__ import annotations
 
@@ -22,6 +22,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "librssm.so")
 CALL = os.path.join(HERE, "_call" + sysconfig.get_config_var("EXT_SUFFIX"))  # an interpreter imports its own
 CALL_SRC = os.path.join(CSRC, "rssm_call.c")
+CALL_KV = os.path.join(HERE, "_call_kv" + sysconfig.get_config_var("EXT_SUFFIX"))
+CALL_KV_SRC = os.path.join(CSRC, "rssm_call_kv.c")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]
@@ -40,14 +42,15 @@ def _sources():
 
 
 def _deps():
-    return _sources() + [CALL_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + [
+    return _sources() + [CALL_SRC, CALL_KV_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + [
         os.path.join(ROOT, "include", "rssm.h"), __file__]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALL):
+    built = (LIB, CALL, CALL_KV)
+    if not all(os.path.exists(p) for p in built):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALL))
+    t = min(os.path.getmtime(p) for p in built)
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -76,13 +79,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    tmp = CALL + ".tmp"
-    cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-Wall", "-I" + sysconfig.get_paths()["include"],
-           "-I" + os.path.join(ROOT, "include"), CALL_SRC, "-o", tmp, "-L" + HERE, "-l:librssm.so", "-Wl,-rpath,$ORIGIN"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"the binding's C module failed to compile:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALL)
+    for module, src in ((CALL, CALL_SRC), (CALL_KV, CALL_KV_SRC)):
+        tmp = module + ".tmp"
+        cmd = [os.environ.get("CC", "gcc"), "-O2", "-shared", "-fPIC", "-Wall", "-I" + sysconfig.get_paths()["include"],
+               "-I" + os.path.join(ROOT, "include"), src, "-o", tmp, "-L" + HERE, "-l:librssm.so", "-Wl,-rpath,$ORIGIN"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"the binding's C module failed to compile:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, module)
     return LIB
 
 

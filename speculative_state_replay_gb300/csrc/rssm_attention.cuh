@@ -1,0 +1,256 @@
+// rssm_attention.cuh -- attention's arguments, how its work is cut, and how the
+// pieces of a shared segment are joined.
+//
+// The queries of a (row, key head) are its new tokens times the heads of its group,
+// `group` consecutive ones a token.  A segment is a tile of them over all of the
+// row's tokens; a unit is a segment's part of one tile of tokens.
+#pragma once
+
+#include "rssm_kv.cuh"
+
+namespace rssm {
+
+constexpr float kShift8 = 9.3132257461547852e-10f;  // 2^-30: 1 / (a value's scale) is summed times this
+
+struct AttnArgs {
+  KvView c;
+  KvRows r;
+  const uint16_t* q;
+  long long q_stride;
+  uint16_t* out;
+  long long out_stride;
+  const int* parents;  // or null: a chain
+  int group;
+  float scale2;  // scale log2(e)
+  unsigned* ticket;  // [blocks]
+  float* partial;    // [blocks][2][rows of a tile x (head_dim + 2)]
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two codes (the bytes of a 16-bit half of w that `sel` picks) as two fp16 values, exactly.
+// int8: with the sign bit turned, code + 128 under the exponent of 1024 is 1152 + code.
+template <int FMT>
+__device__ __forceinline__ uint32_t codes_f16(uint32_t w, uint32_t sel_i8, uint32_t sel_e4m3) {
+  if constexpr (FMT == RSSM_I8) {
+    const uint32_t h = __byte_perm(w, 0x64646464u, sel_i8);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&h), __float2half2_rn(1152.0f));
+    return *reinterpret_cast<const uint32_t*>(&y);
+  } else {
+    const uint32_t h = __byte_perm(w, 0u, sel_e4m3);
+    uint32_t y;
+    asm("{\n\t.reg .b16 x, z;\n\tmov.b32 {x, z}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(y) : "r"(h));
+    return y;
+  }
+}
+
+// 16 (4) bytes to shared memory, zeros if not `have`
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool have) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool have) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(have ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Eight values of a query for an 8-bit cache: fp16, times a power of two that takes the row's largest to
+// 2^14 .. 2^15 (smaller ones keep all their bits down to 2^-28 of it).  G lanes hold a row; `back`: its inverse.
+template <int G>
+__device__ __forceinline__ uint4 query_f16(const uint4& x, float& back) {
+  uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+#pragma unroll
+  for (int o = 1; o < G; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const int e = static_cast<int>(max(m & 0xffffu, m >> 16) >> 7);  // exponent of the largest, 255: not finite
+  const int by = e == 0 || e == 255 ? 0 : 141 - e, h1 = by / 2, h2 = by - h1;  // two factors, for exponents of any size
+  const float f1 = __uint_as_float(static_cast<uint32_t>(127 + h1) << 23), f2 = __uint_as_float(static_cast<uint32_t>(127 + h2) << 23);
+  back = __uint_as_float(static_cast<uint32_t>(127 - h1) << 23) * __uint_as_float(static_cast<uint32_t>(127 - h2) << 23);
+  const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+  uint32_t z[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) z[i] = pack_f16(bf16lo(y[i]) * f1 * f2, bf16hi(y[i]) * f1 * f2);
+  return make_uint4(z[0], z[1], z[2], z[3]);
+}
+
+// bf16 values that are not finite become zeros; whether there was one
+__device__ __forceinline__ bool take_out_odd(uint4& x) {
+  uint32_t z[4] = {x.x, x.y, x.z, x.w};
+  bool odd = false;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if ((z[e] & 0x7f80u) == 0x7f80u) z[e] &= 0xffff0000u, odd = true;
+    if ((z[e] & 0x7f800000u) == 0x7f800000u) z[e] &= 0xffffu, odd = true;
+  }
+  x = make_uint4(z[0], z[1], z[2], z[3]);
+  return odd;
+}
+
+struct RowWork {
+  RowSpan s;
+  int len;    // committed tokens; < 0: nothing to see, zeros (-2: past the page table)
+  int tiles;  // of tokens
+  int mtiles; // of queries
+};
+
+template <int kRows, int kTile>
+__device__ __forceinline__ RowWork row_work(const AttnArgs& a, int b) {
+  RowWork w;
+  w.s = row_span(a.r, b);
+  w.tiles = w.mtiles = 0;
+  w.len = -1;
+  if (w.s.count <= 0) return w;
+  w.len = a.r.lengths[b];
+  w.tiles = 1;
+  w.mtiles = static_cast<int>((static_cast<long long>(w.s.count) * a.group + kRows - 1) / kRows);
+  if (w.len >= 0) {
+    const long long end = static_cast<long long>(w.len) + w.s.count;
+    if (end > static_cast<long long>(a.r.max_pages) * a.c.page_size) w.len = -2;
+    else w.tiles = static_cast<int>((end + kTile - 1) / kTile);
+  }
+  return w;
+}
+
+// A block's part of the line of all units, ordered by row, query tile, head and token tile: units lo .. hi of
+// `share` a block, which begin in row b, whose units begin at `base`.  All threads of the block call it.
+struct Line {
+  long long lo, hi, share, base;
+  int b;
+};
+template <int kRows, int kTile, int kThreads>
+__device__ __forceinline__ Line cut_line(const AttnArgs& a) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ long long scan[kWarps], sh_base;
+  __shared__ int sh_row;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (a.r.batch + kThreads - 1) / kThreads;
+  const int r0 = min(a.r.batch, static_cast<int>(threadIdx.x) * per), r1 = min(a.r.batch, r0 + per);
+  long long sum = 0;
+  for (int i = r0; i < r1; ++i) {
+    const RowWork w = row_work<kRows, kTile>(a, i);
+    sum += static_cast<long long>(w.tiles) * w.mtiles * a.c.heads;
+    if (blockIdx.x == 0) {
+      if (w.s.count < 0) set_error(a.c.err, RSSM_ERRBIT_SEQLEN);
+      if (w.len == -2) set_error(a.c.err, RSSM_ERRBIT_PAGE);
+    }
+  }
+  long long upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) scan[warp] = upto;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int x = 0; x < kWarps; ++x) {
+    if (x < warp) upto += scan[x];
+    total += scan[x];
+  }
+  Line l;
+  l.share = (total + gridDim.x - 1) / gridDim.x;
+  l.lo = l.share * blockIdx.x;
+  l.hi = min(total, l.lo + l.share);
+  long long at = upto - sum;
+  if (l.lo < l.hi && l.lo >= at && l.lo < upto) {
+    int i = r0;
+    for (; i < r1; ++i) {
+      const RowWork w = row_work<kRows, kTile>(a, i);
+      const long long n = static_cast<long long>(w.tiles) * w.mtiles * a.c.heads;
+      if (l.lo < at + n) break;
+      at += n;
+    }
+    sh_row = i;
+    sh_base = at;
+  }
+  __syncthreads();
+  l.b = sh_row;
+  l.base = sh_base;
+  return l;
+}
+
+// What values that are not finite add to four columns from x4 on of the query at new token t: the kernels take
+// them out of the products from position `from` on, where tokens are that not every query sees, since they must not
+// meet the weight 0 of one that does not.
+__device__ __forceinline__ void add_odd(const AttnArgs& a, const RowWork& w, const int* table, const uint8_t* vbase, int row_bytes, long long from,
+                                        long long to, int t, unsigned long long path, int x4, float (&y)[4]) {
+  for (long long p = from; p < to; ++p) {
+    const long long j = p - w.len;
+    if (j >= 0 && !(a.parents ? path >> (j & 63) & 1 : j <= t)) continue;
+    const unsigned pos = static_cast<unsigned>(p), page = pos / static_cast<unsigned>(a.c.page_size);
+    const int pg = table[page];
+    if (pg < 0 || pg >= a.c.pages) continue;
+    const uint2 v = *reinterpret_cast<const uint2*>(vbase + pg * a.c.v_page + static_cast<long long>(pos - page * a.c.page_size) * row_bytes + x4 * 2);
+    const float f[4] = {bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y)};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (!isfinite(f[e])) y[e] += f[e];
+  }
+}
+
+__device__ __forceinline__ void write_out(const AttnArgs& a, const RowWork& w, int head, int query, int D, int x4, const float (&y)[4], float inv) {
+  const int t = query / a.group, h = head * a.group + query - t * a.group;
+  *reinterpret_cast<uint2*>(a.out + (w.s.first + t) * a.out_stride + static_cast<long long>(h) * D + x4) =
+      make_uint2(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv));
+}
+
+// A segment that several blocks share: each leaves its sums, and whoever leaves the last joins them, in the
+// segment's order.  A piece is kRows x D sums, then the rows' maxima and the rows' sums of weights; a block has two
+// places, for a segment that began before it and for one that goes on after it.
+template <int kRows, int D>
+__device__ __forceinline__ float* piece_place(const AttnArgs& a, int block, bool begins) {
+  return a.partial + (static_cast<long long>(block) * 2 + begins) * (kRows * (D + 2));
+}
+template <int kRows, int D, int kThreads>
+__device__ __forceinline__ void join_pieces(const AttnArgs& a, const RowWork& w, int head, int row0, int rows, long long seg0, long long share, float unit) {
+  __shared__ int last;
+  const int first = static_cast<int>(seg0 / share), pieces = static_cast<int>((seg0 + w.tiles - 1) / share) - first + 1;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    last = atomicAdd(a.ticket + first, 1u) == static_cast<unsigned>(pieces - 1);
+    if (last) a.ticket[first] = 0u;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  constexpr int D4 = D / 4;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < rows * D4; i += kThreads) {
+    const int r = i / D4, x4 = (i - r * D4) * 4;
+    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f}, z = 0.0f, top = -INFINITY;
+#pragma unroll 4
+    for (int x = 0; x < pieces; ++x) {
+      const float* p = piece_place<kRows, D>(a, first + x, x == 0);
+      const float mx = __ldcg(p + kRows * D + r), lx = __ldcg(p + kRows * D + kRows + r);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(p + r * D + x4));
+      const float now = fmaxf(top, mx), ref = now == -INFINITY ? 0.0f : now;
+      const float f = exp2_fast(top - ref), e = exp2_fast(mx - ref);
+      top = now;
+      y[0] = y[0] * f + v.x * e;
+      y[1] = y[1] * f + v.y * e;
+      y[2] = y[2] * f + v.z * e;
+      y[3] = y[3] * f + v.w * e;
+      z = z * f + lx * e;
+    }
+    write_out(a, w, head, row0 + r, D, x4, y, z == 0.0f ? 0.0f : unit / z);
+  }
+}
+
+}  // namespace rssm
