@@ -525,7 +525,8 @@ cudaError_t run_format(const AttnArgs& a, int sms, cudaStream_t st) {
 constexpr size_t kHead = 4096;  // bytes of tickets before the pieces
 size_t scratch_need(const KvView& c, int sms) {
   const int rows = c.dim == 256 ? 16 : 32;
-  return kHead + static_cast<size_t>(kBlocks) * sms * 2 * rows * (c.dim + 2) * sizeof(float);
+  const size_t narrow = static_cast<size_t>(kBlocks) * sms * 2 * rows * (c.dim + 2) * sizeof(float), wide = wide_scratch(c, sms);
+  return kHead + (narrow > wide ? narrow : wide);
 }
 static_assert(kBlocks * kMaxSms * sizeof(unsigned) <= kHead, "a ticket a block");
 
@@ -538,7 +539,8 @@ extern "C" size_t rssm_attention_scratch_bytes(const rssm_kv_cache* cache, int32
   KvView c;
   if (kv_view(cache, 0, &c) != RSSM_OK || nqheads < 1 || nqheads % c.heads) return 0;
   const int sms = num_sms();
-  return scratch_need(c, sms > 0 && sms < kMaxSms ? sms : kMaxSms);
+  const int n = sms > 0 && sms < kMaxSms ? sms : kMaxSms;
+  return scratch_need(c, n);
 }
 
 extern "C" rssm_status rssm_tree_attention(const rssm_kv_cache* cache, int32_t layer, const void* q, int64_t q_stride, int32_t nqheads, float scale,
@@ -574,6 +576,8 @@ extern "C" rssm_status rssm_tree_attention(const rssm_kv_cache* cache, int32_t l
   a.ticket = static_cast<unsigned*>(scratch);
   a.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + kHead);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = a.c.dim == 64 ? run_format<64>(a, sms, s) : a.c.dim == 128 ? run_format<128>(a, sms, s) : run_format<256>(a, sms, s);
+  a.whole = 0;
+  const cudaError_t e = wide_takes(a.c, static_cast<int64_t>(T) * a.group) ? run_wide(a, sms, s)
+                        : a.c.dim == 64 ? run_format<64>(a, sms, s) : a.c.dim == 128 ? run_format<128>(a, sms, s) : run_format<256>(a, sms, s);
   return e == cudaSuccess ? RSSM_OK : RSSM_ERR_CUDA;
 }

@@ -1,5 +1,5 @@
-// rssm_attention.cuh -- attention's arguments, how its work is cut, and how the
-// pieces of a shared segment are joined.
+// rssm_attention.cuh -- what the two attention kernels share: arguments, how the
+// work is cut, and how the pieces of a shared segment are joined.
 //
 // The queries of a (row, key head) are its new tokens times the heads of its group,
 // `group` consecutive ones a token.  A segment is a tile of them over all of the
@@ -22,6 +22,7 @@ struct AttnArgs {
   const int* parents;  // or null: a chain
   int group;
   float scale2;  // scale log2(e)
+  int whole;     // a block takes one segment, the longest first, instead of an equal part of the line
   unsigned* ticket;  // [blocks]
   float* partial;    // [blocks][2][rows of a tile x (head_dim + 2)]
 };
@@ -252,5 +253,10 @@ __device__ __forceinline__ void join_pieces(const AttnArgs& a, const RowWork& w,
     write_out(a, w, head, row0 + r, D, x4, y, z == 0.0f ? 0.0f : unit / z);
   }
 }
+
+// host side: the kernel for many queries of a head (rssm_attention_wide.cu)
+bool wide_takes(const KvView& c, int64_t queries);
+size_t wide_scratch(const KvView& c, int sms);
+cudaError_t run_wide(const AttnArgs& a, int sms, cudaStream_t st);
 
 }  // namespace rssm

@@ -39,6 +39,7 @@
 #include <mutex>
 
 #include "rssm_delta.cuh"
+#include "rssm_tcgen05.cuh"
 
 namespace rssm {
 namespace {
@@ -122,45 +123,6 @@ __device__ __forceinline__ void as_operand(const float (&d)[2][4], uint32_t (&h)
   split_bf16x2(d[1][2], d[1][3], h[3], l[3]);
 }
 
-// --------------------------------------------------------------------------
-// tcgen05 (PTX ISA: 5th generation tensor core instructions)
-// --------------------------------------------------------------------------
-// Shared-memory operand: start address, leading and stride byte offsets in 16-byte units, version 1, swizzle mode.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_t sbo, uint64_t swizzle) {
-  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
-         (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) | (swizzle << 61);
-}
-constexpr uint64_t kSw128 = 2;
-// kind::f16, bf16 operands, fp32 accumulators, M = 128
-__host__ __device__ constexpr uint32_t instruction(int n, bool a_mn, bool b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
-         (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
-}
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
-      : "memory");
-}
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// 8 columns of the warp's lanes: the registers hold them only after
-// tc_wait_ld and are not to be touched before (tc_landed)
-__device__ __forceinline__ void tc_ld8(uint32_t (&r)[8], uint32_t addr) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(addr)
-               : "memory");
-}
-// after tc_wait_ld: uses of r stay behind it
-__device__ __forceinline__ void tc_landed(uint32_t (&r)[8]) {
-  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]));
-}
 __device__ __forceinline__ void tc_st8(uint32_t addr, const pair* v) {
   float f[8];
 #pragma unroll
@@ -169,9 +131,6 @@ __device__ __forceinline__ void tc_st8(uint32_t addr, const pair* v) {
                "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
                : "memory");
 }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(

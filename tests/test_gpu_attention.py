@@ -94,6 +94,10 @@ CASES = [
     ("E4M3", 128, 12, 4, 64, [65, 0], [97, 150], False),
     ("I8", 64, 2, 2, 16, [3000], [65], False),
     ("BF16", 128, 8, 1, 64, [4000, -1, 90], [48, 3, 20], True),
+    ("I8", 128, 32, 8, 16, [7 * b for b in range(40)], [9 - b % 3 for b in range(40)], True),
+    ("BF16", 64, 20, 4, 32, [300, 0, -1, 129], [70, 300, 2, 0], False),
+    ("E4M3", 128, 2, 2, 16, [120] * 3, [130, 127, 1], False),
+    ("I8", 64, 8, 8, 16, [11 * b for b in range(20)], [300 if b == 3 else b for b in range(20)], False),
 ]
 
 
