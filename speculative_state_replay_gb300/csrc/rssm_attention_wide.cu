@@ -7,9 +7,11 @@
 // S's place, O += P V with O in tensor memory throughout.  Keys and values come in
 // turn through a ring of shared-memory buffers, 8-bit codes as fp16, exactly.  The two
 // tiles alternate: while one's scores are turned into weights the products of the other
-// run.  The running maximum that weights are taken against follows the true one only
-// when that is more than 2^4 times past it, so that O is rarely touched (weights are
-// then at most 2^4: of a bf16 cache as bf16; fp16 ones are times 2^11).
+// run.  Where a segment has 128 queries or fewer, both take the same ones and every
+// other step of tokens, and are added at the end.  The running maximum that weights are
+// taken against follows the true one only when that is more than 2^4 times past it, so
+// that O is rarely touched (weights are then at most 2^4: of a bf16 cache as bf16; fp16
+// ones are times 2^11).
 //
 // Work is cut as in rssm_attention.cu, or, where there are segments enough for all
 // blocks, a segment a block with the longest first: a prompt's late queries see more.
@@ -24,11 +26,11 @@ constexpr int kTiles = 2;                  // tiles of a block
 constexpr int kRows = kTiles * kQ;
 constexpr int kTok = 128;                  // tokens of a step
 constexpr int kSoftWarps = 4 * kTiles;     // a thread has a query
-constexpr int kLoadWarps = 4;
+constexpr int kLoadWarps = 3;
+constexpr int kLoaders = kLoadWarps * 32;
 constexpr int kThreads = (kSoftWarps + kLoadWarps + 1) * 32;
-constexpr int kRing = 4;                   // buffers of a tile of keys or values
-constexpr int kInfo = 3;                   // and what goes with them: K of step j + 3 waits until K of j + 1 is used, which
-                                           // is after the weights of j
+constexpr int kInfo = 4;                   // places of what goes with a step of tokens: K of step j + 4 waits for a buffer that is
+                                           // free once the scores of j + 2 are made, which is after the weights of j
 constexpr float kLazy = 4.0f;              // log2 of how far the true maximum may be past the one in use
 constexpr float kShift = 11.0f;            // fp16 weights are times 2^11: 2^15 at most
 constexpr int kTmem = 512;                 // columns: two of S, two of O
@@ -52,10 +54,14 @@ struct Shape {
   static constexpr int RB = D * (Q8 ? 1 : 2);     // bytes of a cached head
   static constexpr int NC = RB / 16;              // and its 16-byte chunks
   static constexpr int kTile = kTok * D * 2;      // bytes of a tile as an operand: per 64 dimensions, rows of 128 bytes
+  static constexpr int kRing = Q8 ? 3 : 4;        // buffers of a tile of keys or values
+  static constexpr int kRaw = Q8 ? 3 : 0;         // 8-bit: tiles as they come, on their way to be converted
   static constexpr int kRingAt = kTiles * kTile;  // queries first
-  static constexpr int kInfoAt = kRingAt + kRing * kTile;
+  static constexpr int kRawAt = kRingAt + kRing * kTile;
+  static constexpr int kInfoAt = kRawAt + kRaw * kTok * RB;
   static constexpr int kBarsAt = kInfoAt + (Q8 ? kInfo * 3 * kTok * 4 : 0);
   static constexpr int kSmem = kBarsAt + 256 + 1024;  // and room to start on 1024 bytes
+  static_assert(kSmem <= 227 * 1024 && kRing * kTile >= kQ * D * 4, "fits, and a tile's sums fit the ring");
 };
 
 __device__ __forceinline__ uint32_t sw(int r, int ch) { return static_cast<uint32_t>(r * 128 + ((ch ^ (r & 7)) << 4)); }
@@ -78,6 +84,12 @@ __device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t addr) {
       : "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void tc_ld16(uint32_t (&r)[16], uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : R8(r, 0), R8(r, 8)
+               : "r"(addr)
+               : "memory");
+}
 __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,"
@@ -91,15 +103,42 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) 
 }
 #undef R8
 #undef S8
-// after tc_wait_ld: uses of r stay behind it
+// what was asked for has landed; uses of r stay behind
 __device__ __forceinline__ void landed(uint32_t (&r)[32]) {
+  tc_wait_ld();
 #pragma unroll
   for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+// Two fp32 values in one 64-bit register pair
+using pair = unsigned long long;
+__device__ __forceinline__ pair pack2(float lo, float hi) {
+  pair d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpack2(pair d, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(d)); }
+__device__ __forceinline__ void add2(pair& d, pair a) { asm("add.rn.f32x2 %0, %0, %1;" : "+l"(d) : "l"(a)); }
+__device__ __forceinline__ void fma2(pair& d, pair a, pair b) { asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b)); }
+__device__ __forceinline__ pair fma2v(pair a, pair b, pair c) {
+  pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+// two scores times the query's factor and their keys' scales, and the logarithms of their values' scales
+__device__ __forceinline__ void scaled(uint32_t& x0, uint32_t& x1, pair back, pair keys, pair values) {
+  pair y = pack2(__uint_as_float(x0), __uint_as_float(x1));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(y) : "l"(back));
+  y = fma2v(y, keys, values);
+  float y0, y1;
+  unpack2(y, y0, y1);
+  x0 = __float_as_uint(y0);
+  x1 = __float_as_uint(y1);
+}
+
 template <typename S>
 __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
-  constexpr int D = S::D, RB = S::RB, NC = S::NC;
+  constexpr int D = S::D, RB = S::RB, NC = S::NC, kRing = S::kRing;
   constexpr bool Q8 = S::Q8;
   extern __shared__ uint8_t raw[];
   uint8_t* const sm = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
@@ -122,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
   if (tid == 0) {
     dead = 0;
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(b_full + i, kLoadWarps * 32);
+      mbar_init(b_full + i, kLoaders);
       mbar_init(b_empty + i, 1);
     }
     for (int i = 0; i < kTiles; ++i) {
@@ -130,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
       mbar_init(b_p + i, 4);
       mbar_init(b_o + i, 1);
     }
-    for (int i = 0; i < kInfo; ++i) mbar_init(b_info + i, kLoadWarps * 32);
+    for (int i = 0; i < kInfo; ++i) mbar_init(b_info + i, kLoaders);
     fence_barrier_init();
   }
   tc_before();
@@ -185,10 +224,11 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
     u += t1 - t0;
     const int row0 = mtile * kRows, rows = min(kRows, w.s.count * a.group - row0);
     const int nq = rows > kQ ? 2 : 1;
+    const bool alt = nq == 1;  // both tiles have the same queries, and every other step
     __syncthreads();  // the last piece's shared memory is free
     if (tid == 0) sh_bad = sh_odd = 0;
     const bool flip = a.scale2 < 0.0f;  // the maximum is taken before the scale
-    const float scale2 = fabsf(a.scale2);
+    const float scale2 = fmaxf(fabsf(a.scale2), 1e-30f);  // (times -inf it stays that)
     {
       constexpr int G = D / 8, AT = 32 / G;  // lanes of a row, rows of a warp
 #pragma unroll 1
@@ -231,167 +271,265 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
     const uint8_t* kbase = a.c.k + static_cast<long long>(head) * a.c.page_size * RB;
     const uint8_t* vbase = a.c.v + static_cast<long long>(head) * a.c.page_size * RB;
 
-    float ref = -INFINITY, sum = 0.0f;
+    float ref = -INFINITY, sum = 0.0f, join0 = 1.0f, join1 = 0.0f;  // join: what the two tiles' sums are times where both have the same queries
     if (warp < kSoftWarps) {
       // ---- scores into weights
       const int tile = warp >> 2;
-      if (tile < nq) {
-        const int r = tid;  // its query
-        const int t = (row0 + min(r, rows - 1)) / a.group;
-        const unsigned long long path = a.parents ? sh_mask[t & 63] : 0ull;
-        const float back = Q8 ? sh_back[r] : scale2;
-        const uint32_t s_at = tm + tile * kTok + ((warp & 3) << 21), o_at = tm + kTiles * kTok + tile * D + ((warp & 3) << 21);
+      const int r = alt ? tid & (kQ - 1) : tid;  // its query
+      const int t = (row0 + min(r, rows - 1)) / a.group;
+      const unsigned long long path = a.parents ? sh_mask[t & 63] : 0ull;
+      const float back = Q8 ? sh_back[r] : scale2;
+      const uint32_t s_at = tm + tile * kTok + ((warp & 3) << 21), o_at = tm + kTiles * kTok + tile * D + ((warp & 3) << 21);
+      const int step = alt ? 2 : 1;
+      int n = used[tile];
 #pragma unroll 1
-        for (int j = 0; j < nt; ++j) {
-          const int slot = (steps + j) % kInfo;
-          ok = ok && wait(b_info + slot, ((steps + j) / kInfo) & 1);
-          ok = __all_sync(full, ok && wait(b_s + tile, (used[tile] + j) & 1)) != 0;
-          if (!ok) break;
-          tc_after();
-          const long long pos = static_cast<long long>(t0 + j) * kTok;
-          const unsigned valid = sh_valid[slot];
-          const bool edge = pos + kTok > some || valid != 0xffu;
-          const float* ks = reinterpret_cast<const float*>(sm + S::kInfoAt) + slot * 3 * kTok;
-          // scores in units of log2 (8-bit: with their values' scales)
-          auto units_of = [&](uint32_t (&x)[32], int c) {
-            if constexpr (Q8) {
+      for (int j = alt ? tile : 0; j < nt; j += step, ++n) {
+        const int slot = (steps + j) % kInfo;
+        ok = ok && wait(b_info + slot, ((steps + j) / kInfo) & 1);
+        ok = __all_sync(full, ok && wait(b_s + tile, n & 1)) != 0;
+        if (!ok) break;
+        tc_after();
+        const long long pos = static_cast<long long>(t0 + j) * kTok;
+        const unsigned valid = sh_valid[slot];
+        const bool edge = pos + kTok > some || valid != 0xffu;
+        const float* info = reinterpret_cast<const float*>(sm + S::kInfoAt) + slot * 3 * kTok;
+        // the scores go through the registers 32 at a time, the next ones on their way meanwhile: once for the maximum, once for the weights
+        uint32_t x[2][32];
+        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        tc_ld32(x[0], s_at);
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float4 k4 = *reinterpret_cast<const float4*>(ks + 32 * c + i), l4 = *reinterpret_cast<const float4*>(ks + kTok + 32 * c + i);
-                x[i] = __float_as_uint(__uint_as_float(x[i]) * back * k4.x + l4.x);
-                x[i + 1] = __float_as_uint(__uint_as_float(x[i + 1]) * back * k4.y + l4.y);
-                x[i + 2] = __float_as_uint(__uint_as_float(x[i + 2]) * back * k4.z + l4.z);
-                x[i + 3] = __float_as_uint(__uint_as_float(x[i + 3]) * back * k4.w + l4.w);
-              }
+        for (int c = 0; c < kTok / 32; ++c) {
+          uint32_t(&y)[32] = x[c & 1];
+          landed(y);
+          if (c + 1 < kTok / 32) tc_ld32(x[(c + 1) & 1], s_at + 32 * (c + 1));
+          if constexpr (Q8) {  // in units of log2, with their values' scales
+            const pair bb = pack2(back, back);
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(info + 32 * c + i), l4 = *reinterpret_cast<const ulonglong2*>(info + kTok + 32 * c + i);
+              scaled(y[i], y[i + 1], bb, k4.x, l4.x);
+              scaled(y[i + 2], y[i + 3], bb, k4.y, l4.y);
             }
-          };
-          float top = -INFINITY;
+          }
           if (edge) {
-#pragma unroll 1
-            for (int c = 0; c < kTok / 32; ++c) {
-              uint32_t x[32];
-              tc_ld32(x, s_at + 32 * c);
-              tc_wait_ld();
-              landed(x);
-              units_of(x, c);
-              // which of the 32 this query sees
-              const long long j0 = pos + 32 * c - w.len;
-              uint32_t see;
-              if (a.parents) {
-                see = j0 <= -32 ? full : j0 < 0 ? static_cast<uint32_t>(path << -j0) | ((1u << -j0) - 1u) : j0 < 64 ? static_cast<uint32_t>(path >> j0) : 0u;
-              } else {
-                const long long n = t - j0;  // the last one's place
-                see = n >= 31 ? full : n < 0 ? 0u : (2u << n) - 1u;
-              }
-              see &= (valid >> (2 * c) & 1u ? 0xffffu : 0u) | (valid >> (2 * c + 1) & 1u ? 0xffff0000u : 0u);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float y = Q8 ? __uint_as_float(x[i]) : __uint_as_float(x[i]) * back;
-                x[i] = __float_as_uint(see >> i & 1u ? y : -INFINITY);
-                top = fmaxf(top, __uint_as_float(x[i]));
-              }
-              tc_st32(s_at + 32 * c, x);
+            // which of the 32 this query sees
+            const long long j0 = pos + 32 * c - w.len;
+            uint32_t see;
+            if (a.parents) {
+              see = j0 <= -32 ? full : j0 < 0 ? static_cast<uint32_t>(path << -j0) | ((1u << -j0) - 1u) : j0 < 64 ? static_cast<uint32_t>(path >> j0) : 0u;
+            } else {
+              const long long m = t - j0;  // the last one's place
+              see = m >= 31 ? full : m < 0 ? 0u : (2u << m) - 1u;
             }
-            tc_wait_st();
-          } else {
+            see &= (valid >> (2 * c) & 1u ? 0xffffu : 0u) | (valid >> (2 * c + 1) & 1u ? 0xffff0000u : 0u);
 #pragma unroll
-            for (int c = 0; c < kTok / 32; ++c) {
-              uint32_t x[32];
-              tc_ld32(x, s_at + 32 * c);
-              tc_wait_ld();
-              landed(x);
-              units_of(x, c);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) top = fmaxf(top, __uint_as_float(x[i]));
-            }
-            if constexpr (!Q8) top *= back;
+            for (int i = 0; i < 32; ++i) y[i] = see >> i & 1u ? y[i] : 0xff800000u;  // -inf
           }
-          // the maximum in use follows where it has to; the products before this step's are done (its scores came after them)
-          if (__any_sync(full, top > ref + kLazy)) {
-            const float now = fmaxf(ref, top);
-            const float f = now == -INFINITY ? 1.0f : exp2_fast(ref - now);
-            ref = now;
-            sum *= f;
-            if (j > 0) {
-#pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t x[32];
-                tc_ld32(x, o_at + 32 * c);
-                tc_wait_ld();
-                landed(x);
+          if (Q8 || edge) tc_st32(s_at + 32 * c, y);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-                tc_st32(o_at + 32 * c, x);
-              }
+          for (int i = 0; i < 32; ++i) t4[i & 3] = fmaxf(t4[i & 3], __uint_as_float(y[i]));
+        }
+        if (Q8 || edge) tc_wait_st();
+        tc_ld32(x[0], s_at);
+        float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+        if constexpr (!Q8) top = top == -INFINITY ? top : top * back;
+        // the maximum in use follows where it has to; the products before this step's are done (its scores came after them)
+        if (__any_sync(full, top > ref + kLazy)) {
+          const float now = fmaxf(ref, top);
+          const float f = now == -INFINITY ? 1.0f : exp2_fast(ref - now);
+          ref = now;
+          sum *= f;
+          if (n > used[tile]) {
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t y[16];
+              tc_ld16(y, o_at + 16 * c);
+              tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(y[i]));
+#pragma unroll
+              for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+              tc_st16(o_at + 16 * c, y);
             }
           }
-          const float off = (ref == -INFINITY ? 0.0f : ref) - (Q8 ? kShift : 0.0f);
-          float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          auto weights = [&](auto is_edge) {
-            constexpr bool E = decltype(is_edge)::value;
+        }
+        const float lift = (Q8 ? kShift : 0.0f) - (ref == -INFINITY ? 0.0f : ref);
+        const pair lift2 = pack2(lift, lift), scale22 = pack2(back, back);
+        pair s2[2] = {0ull, 0ull};
 #pragma unroll
-            for (int c = 0; c < kTok / 32; ++c) {
-              uint32_t x[32], p[16];
-              tc_ld32(x, s_at + 32 * c);
-              tc_wait_ld();
-              landed(x);
-              if constexpr (!E) units_of(x, c);
+        for (int c = 0; c < kTok / 32; ++c) {
+          uint32_t(&z)[32] = x[c & 1];
+          landed(z);
+          if (c + 1 < kTok / 32) tc_ld32(x[(c + 1) & 1], s_at + 32 * (c + 1));
+          uint32_t p[16];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float y = __uint_as_float(x[i]);
-                x[i] = __float_as_uint(exp2_fast(Q8 || E ? y - off : y * back - off));
+          for (int i = 0; i < 32; i += 2) {
+            pair y = pack2(__uint_as_float(z[i]), __uint_as_float(z[i + 1]));
+            if constexpr (Q8) add2(y, lift2);
+            else y = fma2v(y, scale22, lift2);
+            float y0, y1;
+            unpack2(y, y0, y1);
+            y0 = exp2_fast(y0);
+            y1 = exp2_fast(y1);
+            const pair e = pack2(y0, y1);
+            if constexpr (Q8) {
+              // (a token that is not seen may have no scale: its weight 0 must not meet that)
+              pair v = *reinterpret_cast<const pair*>(info + 2 * kTok + 32 * c + i);
+              if (edge) {
+                float v0, v1;
+                unpack2(v, v0, v1);
+                v = pack2(y0 == 0.0f ? 0.0f : v0, y1 == 0.0f ? 0.0f : v1);
               }
-              if constexpr (Q8) {
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                  const float4 i4 = *reinterpret_cast<const float4*>(ks + 2 * kTok + 32 * c + i);
-                  const float v4[4] = {i4.x, i4.y, i4.z, i4.w};
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    const float y = __uint_as_float(x[i + e]);
-                    if (!E || y > 0.0f) s4[e] += y * v4[e];
-                  }
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) p[i] = pack_f16(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-              } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) s4[i & 3] += __uint_as_float(x[i]);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) p[i] = pack_bf16(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-              }
-              tc_st16(s_at + 16 * c, p);
+              fma2(s2[i >> 1 & 1], e, v);
+              p[i >> 1] = pack_f16(y0, y1);
+            } else {
+              add2(s2[i >> 1 & 1], e);
+              p[i >> 1] = pack_bf16(y0, y1);
             }
-          };
-          if (edge) weights(std::true_type{});
-          else weights(std::false_type{});
-          sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-          tc_wait_st();
-          tc_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(b_p + tile);
+          }
+          tc_st16(s_at + 16 * c, p);
         }
-        if (nt > 0) {
-          ok = __all_sync(full, ok && wait(b_o + tile, done[tile] & 1)) != 0;
-          tc_after();
-        }
+        add2(s2[0], s2[1]);
+        float u0, u1;
+        unpack2(s2[0], u0, u1);
+        sum += u0 + u1;
+        tc_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_p + tile);
+      }
+      if (nt > (alt ? tile : 0)) {
+        ok = __all_sync(full, ok && wait(b_o + tile, done[tile] & 1)) != 0;
+        tc_after();
       }
     } else if (warp < kSoftWarps + kLoadWarps) {
       // ---- keys and values, in turn
       const int lt = tid - kSoftWarps * 32;
-      int pending = -1;  // an item whose copies are on their way
-      bool pending_odd = false;
-      // this thread's copies have landed: its values are looked at where not every query sees them, then the buffer is announced
-      auto announce = [&]() {
-        if (pending < 0) return;
-        const int buf = pending % kRing;
-        if constexpr (!Q8) {
+      constexpr int CHUNKS = kTok * NC;  // of 16 bytes, in order: thread lt takes lt, lt + 96, ..
+      auto page_id = [&](int j) {
+        const long long p = static_cast<long long>(t0 + j) * kTok + 16 * lane;
+        return lane < 8 && j < nt && p < end ? table[static_cast<unsigned>(p) / static_cast<unsigned>(a.c.page_size)] : -1;
+      };
+      int next_id = page_id(0);
+      // lanes 0-7: where the step's slices of 16 tokens are, and how many of them are there
+      long long koff = 0, voff = 0;
+      int live = 0;
+      unsigned missing = 0u, place = 0u;
+      int page = 0;
+      auto find = [&](int j) {
+        const long long mine = static_cast<long long>(t0 + j) * kTok + 16 * lane;
+        const int id = next_id;
+        next_id = page_id(j + 1);
+        const bool wanted = lane < 8 && mine < end, have = wanted && id >= 0 && id < a.c.pages;
+        if (wanted && !have) set_error(a.c.err, RSSM_ERRBIT_PAGE);
+        missing = __ballot_sync(full, wanted && !have);
+        place = static_cast<unsigned>(mine) % static_cast<unsigned>(a.c.page_size);
+        page = have ? id : 0;
+        koff = have ? id * a.c.k_page + static_cast<long long>(place) * RB : 0;
+        voff = have ? id * a.c.v_page + static_cast<long long>(place) * RB : 0;
+        live = have ? static_cast<int>(min(16ll, end - mine)) : 0;
+      };
+      // a tile's copies: chunk i of it goes to dst(row, chunk of the row)
+      auto copy = [&](bool values, auto dst) {
+        const uint8_t* src = values ? vbase : kbase;
+        const long long off = values ? voff : koff;
+#pragma unroll 2
+        for (int x = 0; x < (CHUNKS + kLoaders - 1) / kLoaders; ++x) {
+          const int i = lt + kLoaders * x, r = i / NC, ch = i % NC, sl = (r / 16) & 7;  // (the warp's chunks may lie in two slices)
+          const long long o = __shfl_sync(full, off, sl);
+          const int there = __shfl_sync(full, live, sl);
+          if (i < CHUNKS) copy16(dst(i, r, ch), src + o + (r % 16) * RB + ch * 16, r % 16 < there);
+        }
+        copy_commit();
+      };
+      auto step_info = [&](float (&ksv)[2], float (&vsv)[2]) {  // 8-bit: the scales of tokens lt and lt + 96
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = lt + kLoaders * e, sl = (i / 16) & 7;
+          const long long row = static_cast<long long>(head) * a.c.page_size + __shfl_sync(full, place, sl) + (i & 15);
+          const int pg = __shfl_sync(full, page, sl);
+          const bool there = i < kTok && (i & 15) < __shfl_sync(full, live, sl);
+          ksv[e] = there ? a.c.ks[pg * a.c.ks_page + row] : 0.0f;
+          vsv[e] = there ? a.c.vs[pg * a.c.vs_page + row] : 0.0f;
+        }
+      };
+      if constexpr (Q8) {
+        // raw tiles kRaw items ahead; a thread converts the chunks that it has copied itself
+        float ksv[2] = {0.0f, 0.0f}, vsv[2] = {0.0f, 0.0f};  // of the newest step asked for
+        auto ask = [&](int n) {  // item n of the piece
+          if (n < 2 * nt) {
+            if (!(n & 1)) {
+              find(n >> 1);
+              step_info(ksv, vsv);
+            }
+            const uint32_t raw_at = base + S::kRawAt + (n % S::kRaw) * kTok * RB;
+            copy(n & 1, [&](int i, int, int) { return raw_at + i * 16; });
+          } else {
+            copy_commit();
+          }
+        };
+        ask(0);
+        ask(1);
+#pragma unroll 1
+        for (int n = 0; n < 2 * nt; ++n) {
+          const int item = items + n, buf = item % kRing, j = n >> 1;
+          if (!(n & 1)) {
+            // what goes with the step (asked for with item 2 j, the newest still): its place is free, by the buffer that K waits for
+            ok = ok && (item < kRing || wait(b_empty + buf, (item / kRing - 1) & 1));
+            if (ok) {
+              const int slot = (steps + j) % kInfo;
+              float* info = reinterpret_cast<float*>(sm + S::kInfoAt) + slot * 3 * kTok;
+              if (lt == 0) sh_valid[slot] = 0xffu & ~missing;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int i = lt + kLoaders * e;
+                if (i < kTok) {
+                  const float y = vsv[e] < 7.7037197775489434e-34f ? 7.7037197775489434e-34f : vsv[e];  // 2^-110: a scale of 0 stands for zeros all the same
+                  info[i] = ksv[e];
+                  info[kTok + i] = __log2f(y);
+                  info[2 * kTok + i] = __frcp_rn(y) * kShift8;
+                }
+              }
+              mbar_arrive(b_info + slot);
+            }
+          } else {
+            ok = ok && (item < kRing || wait(b_empty + buf, (item / kRing - 1) & 1));
+          }
+          ok = __all_sync(full, ok) != 0;
+          if (!ok) break;
+          ask(n + 2);
+          copy_wait<2>();
+          const uint32_t raw_at = base + S::kRawAt + (n % S::kRaw) * kTok * RB;
+          uint8_t* to = sm + S::kRingAt + buf * S::kTile;
+#pragma unroll 2
+          for (int i = lt; i < CHUNKS; i += kLoaders) {
+            const int r = i / NC, ch = i % NC;
+            uint32_t c4[4], h[8];
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(c4[0]), "=r"(c4[1]), "=r"(c4[2]), "=r"(c4[3]) : "r"(raw_at + i * 16) : "memory");
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t y = S::FMT == RSSM_I8 ? c4[e] ^ 0x80808080u : c4[e];
+              h[2 * e] = codes_f16<S::FMT>(y, 0x4140u, 0x4410u);
+              h[2 * e + 1] = codes_f16<S::FMT>(y, 0x4342u, 0x4432u);
+            }
+            uint8_t* p = to + (ch / 4) * 16384;
+            *reinterpret_cast<uint4*>(p + sw(r, (2 * ch) % 8)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(p + sw(r, (2 * ch + 1) % 8)) = make_uint4(h[4], h[5], h[6], h[7]);
+          }
+          fence_async();
+          mbar_arrive(b_full + buf);
+        }
+      } else {
+        int pending = -1;  // an item whose copies are on their way
+        bool pending_odd = false;
+        // this thread's copies have landed: its values are looked at where not every query sees them, then the buffer is announced
+        auto announce = [&]() {
+          if (pending < 0) return;
+          const int buf = pending % kRing;
           if (pending_odd) {
             uint8_t* p = sm + S::kRingAt + buf * S::kTile;
-#pragma unroll 4
-            for (int x = 0; x < NC; ++x) {
-              const int i = lt + 128 * x, r = i / NC, ch = i % NC;
-              uint4* q = reinterpret_cast<uint4*>(p + (ch / 8) * 16384 + sw(r, ch % 8));
+            for (int i = lt; i < CHUNKS; i += kLoaders) {
+              uint4* q = reinterpret_cast<uint4*>(p + (i % NC / 8) * 16384 + sw(i / NC, i % NC % 8));
               uint4 y = *q;
               if (take_out_odd(y)) {
                 *q = y;
@@ -399,122 +537,45 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
               }
             }
           }
-        }
-        fence_async();
-        mbar_arrive(b_full + buf);
-        pending = -1;
-      };
-      auto page_id = [&](int j) {
-        const long long p = static_cast<long long>(t0 + j) * kTok + 16 * lane;
-        return lane < 8 && j < nt && p < end ? table[static_cast<unsigned>(p) / static_cast<unsigned>(a.c.page_size)] : -1;
-      };
-      int next_id = page_id(0);
+          fence_async();
+          mbar_arrive(b_full + buf);
+          pending = -1;
+        };
 #pragma unroll 1
-      for (int j = 0; j < nt; ++j) {
-        const long long pos = static_cast<long long>(t0 + j) * kTok;
-        const long long mine = pos + 16 * lane;
-        const int id = next_id;
-        next_id = page_id(j + 1);
-        const bool have = lane < 8 && mine < end && id >= 0 && id < a.c.pages;
-        if (lane < 8 && mine < end && !have) set_error(a.c.err, RSSM_ERRBIT_PAGE);
-        const unsigned missing = __ballot_sync(full, lane < 8 && mine < end && !have) & 0xffu;
-        const unsigned place = static_cast<unsigned>(mine) % static_cast<unsigned>(a.c.page_size);
-        const long long koff = have ? id * a.c.k_page + static_cast<long long>(place) * RB : 0;
-        const long long voff = have ? id * a.c.v_page + static_cast<long long>(place) * RB : 0;
-        const int live = have ? static_cast<int>(min(16ll, end - mine)) : 0;
-        const int slot = (steps + j) % kInfo;
-        float ksv = 0.0f, vsv = 0.0f;
-        if constexpr (Q8) {  // a token a thread
-          const int sl = lt / 16;
-          const long long row = static_cast<long long>(head) * a.c.page_size + __shfl_sync(full, place, sl) + (lt & 15);
-          const int pg = __shfl_sync(full, have ? id : 0, sl);
-          if ((lt & 15) < __shfl_sync(full, live, sl)) {
-            ksv = a.c.ks[pg * a.c.ks_page + row];
-            vsv = a.c.vs[pg * a.c.vs_page + row];
-          }
-        }
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          const int item = items + 2 * j + kv, buf = item % kRing;
-          const uint8_t* src = kv ? vbase : kbase;
-          const long long off = kv ? voff : koff;
-          uint4 codes[Q8 ? NC : 1];
-          if constexpr (Q8) {  // asked for before the buffer is free
-#pragma unroll
-            for (int x = 0; x < NC; ++x) {
-              const int i = lt + 128 * x, r = i / NC, ch = i % NC, sl = r / 16;
-              const long long o = __shfl_sync(full, off, sl);
-              codes[x] = r % 16 < __shfl_sync(full, live, sl) ? __ldcg(reinterpret_cast<const uint4*>(src + o + (r % 16) * RB + ch * 16)) : make_uint4(0u, 0u, 0u, 0u);
-            }
-          }
+        for (int n = 0; n < 2 * nt; ++n) {
+          const int item = items + n, buf = item % kRing, j = n >> 1;
+          if (!(n & 1)) find(j);
           if (item >= kRing && !mbar_try_wait(b_empty + buf, (item / kRing - 1) & 1)) {
-            if constexpr (!Q8) {
-              copy_wait<0>();
-              announce();
-            }
+            copy_wait<0>();
+            announce();
             ok = ok && wait(b_empty + buf, (item / kRing - 1) & 1);
           }
           ok = __all_sync(full, ok) != 0;
           if (!ok) break;
-          uint8_t* to = sm + S::kRingAt + buf * S::kTile;
-          if (kv == 0) {  // what goes with the step: the place is free since K of two steps before is
+          if (!(n & 1)) {
+            const int slot = (steps + j) % kInfo;
             if (lt == 0) sh_valid[slot] = 0xffu & ~missing;
-            if constexpr (Q8) {
-              float* info = reinterpret_cast<float*>(sm + S::kInfoAt) + slot * 3 * kTok;
-              vsv = vsv < 7.7037197775489434e-34f ? 7.7037197775489434e-34f : vsv;  // 2^-110: a scale of 0 stands for zeros all the same
-              info[lt] = ksv;
-              info[kTok + lt] = __log2f(vsv);
-              info[2 * kTok + lt] = __frcp_rn(vsv) * kShift8;
-            }
             mbar_arrive(b_info + slot);
           }
-          if constexpr (Q8) {
-#pragma unroll
-            for (int x = 0; x < NC; ++x) {
-              const int i = lt + 128 * x, r = i / NC, ch = i % NC;
-              const uint32_t c4[4] = {codes[x].x, codes[x].y, codes[x].z, codes[x].w};
-              uint32_t h[8];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t y = S::FMT == RSSM_I8 ? c4[e] ^ 0x80808080u : c4[e];
-                h[2 * e] = codes_f16<S::FMT>(y, 0x4140u, 0x4410u);
-                h[2 * e + 1] = codes_f16<S::FMT>(y, 0x4342u, 0x4432u);
-              }
-              uint8_t* p = to + (ch / 4) * 16384;
-              *reinterpret_cast<uint4*>(p + sw(r, (2 * ch) % 8)) = make_uint4(h[0], h[1], h[2], h[3]);
-              *reinterpret_cast<uint4*>(p + sw(r, (2 * ch + 1) % 8)) = make_uint4(h[4], h[5], h[6], h[7]);
-            }
-            pending = item;
+          const uint32_t to = base + S::kRingAt + buf * S::kTile;
+          copy(n & 1, [&](int, int r, int ch) { return to + (ch / 8) * 16384 + sw(r, ch % 8); });
+          if (pending >= 0) {
+            copy_wait<1>();
             announce();
-          } else {
-#pragma unroll
-            for (int x = 0; x < NC; ++x) {
-              const int i = lt + 128 * x, r = i / NC, ch = i % NC, sl = r / 16;
-              const long long o = __shfl_sync(full, off, sl);
-              copy16(base + S::kRingAt + buf * S::kTile + (ch / 8) * 16384 + sw(r, ch % 8), src + o + (r % 16) * RB + ch * 16,
-                     r % 16 < __shfl_sync(full, live, sl));
-            }
-            copy_commit();
-            if (pending >= 0) {
-              copy_wait<1>();
-              announce();
-            }
-            pending = item;
-            pending_odd = kv && pos + kTok > some;
           }
+          pending = item;
+          pending_odd = (n & 1) && static_cast<long long>(t0 + j + 1) * kTok > some;
         }
-        if (!ok) break;
-      }
-      if constexpr (!Q8) {
         copy_wait<0>();
         announce();
       }
+      copy_wait<0>();
     } else if (lane == 0) {
       // ---- products
       constexpr uint32_t kind = Q8 ? (1u << 7) | (1u << 10) : 0u;  // fp16 operands: without bf16's bits
       constexpr uint32_t i_s = instruction(kTok, false, false) & ~kind, i_o = instruction(D, false, true) & ~kind;
-      auto scores = [&](int tile, int buf) {
-        const uint64_t q = operand(base + tile * S::kTile, 16, 1024, kSw128), k = operand(base + S::kRingAt + buf * S::kTile, 16, 1024, kSw128);
+      auto scores = [&](int tile, int queries, int buf) {
+        const uint64_t q = operand(base + queries * S::kTile, 16, 1024, kSw128), k = operand(base + S::kRingAt + buf * S::kTile, 16, 1024, kSw128);
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
           const uint64_t o = (x / 4) * (16384 / 16) + (x % 4) * 2;
@@ -522,34 +583,67 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
         }
         tc_commit(b_s + tile);
       };
-      if (nt > 0) {
-        const int buf = items % kRing;
-        ok = ok && wait(b_full + buf, (items / kRing) & 1);
-        if (ok) {
-          tc_after();
-          for (int x = 0; x < nq; ++x) scores(x, buf);
-          tc_commit(b_empty + buf);
-        }
-      }
-#pragma unroll 1
-      for (int j = 0; ok && j < nt; ++j) {
-        const int iv = items + 2 * j + 1, bv = iv % kRing, ik = iv + 1, bk = ik % kRing;
-        const bool more = j + 1 < nt;
-        ok = ok && wait(b_full + bv, (iv / kRing) & 1);
-        if (more) ok = ok && wait(b_full + bk, (ik / kRing) & 1);
-        for (int x = 0; x < nq; ++x) {
-          ok = ok && wait(b_p + x, (used[x] + j) & 1);
+      auto sums = [&](int tile, int buf, bool more) {
+        const uint64_t v = operand(base + S::kRingAt + buf * S::kTile, 16384, 1024, kSw128);
+#pragma unroll
+        for (int y = 0; y < kTok / 16; ++y) tc_mma_ts(tm + kTiles * kTok + tile * D, tm + tile * kTok + 8 * y, v + y * (2048 / 16), i_o, more || y > 0);
+      };
+      auto filled = [&](int n) {  // item n of the piece is there
+        const int item = items + n;
+        ok = ok && wait(b_full + item % kRing, (item / kRing) & 1);
+        return item % kRing;
+      };
+      if (alt) {
+        for (int j = 0; ok && j < min(nt, 2); ++j) {
+          const int buf = filled(2 * j);
           if (!ok) break;
           tc_after();
-          const uint64_t v = operand(base + S::kRingAt + bv * S::kTile, 16384, 1024, kSw128);
-#pragma unroll
-          for (int y = 0; y < kTok / 16; ++y) tc_mma_ts(tm + kTiles * kTok + x * D, tm + x * kTok + 8 * y, v + y * (2048 / 16), i_o, j > 0 || y > 0);
-          if (more) scores(x, bk);
-          else tc_commit(b_o + x);
+          scores(j, 0, buf);
+          tc_commit(b_empty + buf);
         }
-        if (ok) {
+#pragma unroll 1
+        for (int j = 0; ok && j < nt; ++j) {
+          const int x = j & 1, bv = filled(2 * j + 1);
+          ok = ok && wait(b_p + x, (used[x] + j / 2) & 1);
+          if (!ok) break;
+          tc_after();
+          sums(x, bv, j > 1);
           tc_commit(b_empty + bv);
-          if (more) tc_commit(b_empty + bk);
+          if (j + 2 < nt) {
+            const int bk = filled(2 * j + 4);
+            if (!ok) break;
+            tc_after();
+            scores(x, 0, bk);
+            tc_commit(b_empty + bk);
+          } else {
+            tc_commit(b_o + x);
+          }
+        }
+      } else {
+        if (nt > 0) {
+          const int buf = filled(0);
+          if (ok) {
+            tc_after();
+            for (int x = 0; x < kTiles; ++x) scores(x, x, buf);
+            tc_commit(b_empty + buf);
+          }
+        }
+#pragma unroll 1
+        for (int j = 0; ok && j < nt; ++j) {
+          const bool more = j + 1 < nt;
+          const int bv = filled(2 * j + 1), bk = more ? filled(2 * j + 2) : 0;
+          for (int x = 0; x < kTiles; ++x) {
+            ok = ok && wait(b_p + x, (used[x] + j) & 1);
+            if (!ok) break;
+            tc_after();
+            sums(x, bv, j > 0);
+            if (more) scores(x, x, bk);
+            else tc_commit(b_o + x);
+          }
+          if (ok) {
+            tc_commit(b_empty + bv);
+            if (more) tc_commit(b_empty + bk);
+          }
         }
       }
     }
@@ -558,8 +652,40 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
     items += 2 * nt;
     steps += nt;
 #pragma unroll
-    for (int x = 0; x < kTiles; ++x)
-      if (x < nq) used[x] += nt, done[x] += nt > 0;
+    for (int x = 0; x < kTiles; ++x) {
+      const int n = alt ? (nt - x + 1) / 2 : nt;
+      used[x] += n;
+      done[x] += n > 0;
+    }
+    if (alt && nt > 1) {
+      // ---- the second tile's sums are the same queries'
+      float* const other = reinterpret_cast<float*>(sm + S::kRingAt);  // [dimension][query]
+      __shared__ float sh_ref[kQ], sh_sum[kQ];
+      if (warp < kSoftWarps && warp >= 4) {
+        const int r = tid - kQ;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          uint32_t x[16];
+          tc_ld16(x, tm + kTiles * kTok + D + ((warp & 3) << 21) + c);
+          tc_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(x[i]));
+#pragma unroll
+          for (int i = 0; i < 16; ++i) other[(c + i) * kQ + r] = __uint_as_float(x[i]);
+        }
+        sh_ref[r] = ref;
+        sh_sum[r] = sum;
+        tc_before();
+      }
+      __syncthreads();
+      if (warp < 4) {
+        const float now = fmaxf(ref, sh_ref[tid]), at0 = now == -INFINITY ? 0.0f : now;
+        join0 = exp2_fast(ref - at0);
+        join1 = exp2_fast(sh_ref[tid] - at0);
+        sum = sum * join0 + sh_sum[tid] * join1;
+        ref = now;
+      }
+    }
 
     // ---- the queries' sums
     const bool whole = t0 == 0 && t1 == w.tiles;
@@ -573,8 +699,12 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
         uint32_t x[32];
         if (nt > 0) {
           tc_ld32(x, tm + kTiles * kTok + tile * D + ((warp & 3) << 21) + 32 * c);
-          tc_wait_ld();
           landed(x);
+          if (alt && nt > 1) {
+            const float* other = reinterpret_cast<const float*>(sm + S::kRingAt) + 32 * c * kQ + r;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * join0 + other[i * kQ] * join1);
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = 0u;

@@ -5,8 +5,10 @@
 // row, each a slice of the vocabulary that it keeps in shared memory, one 32-bit word
 // an id.  A word is first the id's count in the request's text -- every block goes over
 // the whole history and keeps what falls into its slice, integer additions in shared
-// memory, whose order does not matter -- then the processed logit.  Maximum and sum
-// meet through the cluster's shared memory.
+// memory, whose order does not matter -- then the processed logit, then its
+// exponential.  Each block takes them against its own maximum; maxima and sums meet once
+// through the cluster's shared memory.  Rows of any alignment are read 16 bytes a lane:
+// places are counted from the 16-byte boundary before the row's first value.
 #include <cooperative_groups.h>
 
 #include "rssm_kv.cuh"
@@ -16,15 +18,20 @@ namespace cg = cooperative_groups;
 namespace rssm {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kBlocks = 3;              // an SM
 constexpr int kMaxParts = 8;            // blocks of a cluster (the portable most)
-constexpr int kMaxSlice = 1 << 15;      // words of a block: 128 KB
-constexpr int kMaxVocab = kMaxParts * kMaxSlice;
-constexpr unsigned kSeen = 1u << 31;    // a count's bit for ids of the prompt
+constexpr int kMaxVocab = 1 << 18;
+constexpr int kRun = 8;                 // ids of a lane's step
+constexpr int kAhead = 4;               // steps whose loads are on their way at a time
+constexpr int kStride = kThreads * kRun;
+constexpr int kMaxSlice = kMaxVocab / kMaxParts + 32;  // words of a block: 128 KB
+constexpr unsigned kSeen = 1u << 31;    // bits of a count: the prompt holds the id,
+constexpr unsigned kBiased = 1u << 30;  // it has a bias
 
 struct LogitsArgs {
   rssm_logits_args a;
-  int slice;  // ids of a block, a multiple of 32
+  int slice;  // words of a block, a multiple of 32
 };
 
 template <typename P>
@@ -44,41 +51,6 @@ __device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float x) { retur
 template <>
 __device__ __forceinline__ __half rounded<__half>(float x) { return __float2half_rn(x); }
 
-// `N` values from p on, 16 bytes at a time if p allows; those past `n` are zeros (not written)
-template <typename P, int N>
-__device__ __forceinline__ void load(const P* p, int n, bool wide, float (&f)[N]) {
-  constexpr int VEC = 16 / sizeof(P);
-  if (wide && n >= N) {
-#pragma unroll
-    for (int i = 0; i < N; i += VEC) {
-      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(p + i));
-      const P* x = reinterpret_cast<const P*>(&w);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) f[i + e] = value<P>(x[e]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = i < n ? value<P>(p[i]) : 0.0f;
-  }
-}
-template <typename P, int N>
-__device__ __forceinline__ void store(P* p, int n, bool wide, const float (&f)[N]) {
-  constexpr int VEC = 16 / sizeof(P);
-  if (wide && n >= N) {
-#pragma unroll
-    for (int i = 0; i < N; i += VEC) {
-      P x[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) x[e] = rounded<P>(f[i + e]);
-      __stcs(reinterpret_cast<uint4*>(p + i), *reinterpret_cast<const uint4*>(x));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (i < n) p[i] = rounded<P>(f[i]);
-  }
-}
-
 // largest value, and of equal ones the lowest id, as one number that orders like them
 __device__ __forceinline__ unsigned long long top_key(float x, int id) {
   const uint32_t u = __float_as_uint(x == 0.0f ? 0.0f : x);  // -0 is 0
@@ -86,15 +58,14 @@ __device__ __forceinline__ unsigned long long top_key(float x, int id) {
   return static_cast<unsigned long long>(o) << 32 | (0xffffffffu - static_cast<uint32_t>(id));
 }
 
-constexpr int kRun = 8;  // ids of a lane's step
-
 template <typename IN, typename OUT>
-__global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsArgs k) {
+__global__ void __launch_bounds__(kThreads, kBlocks) logits_kernel(const LogitsArgs k) {
+  constexpr int VEC = 16 / sizeof(IN), PIECES = kRun / VEC;  // 16-byte pieces of a step
   extern __shared__ __align__(16) uint32_t word[];  // [slice]
   __shared__ float sh_part[kWarps];
   __shared__ unsigned long long sh_key[kWarps];
-  __shared__ float sh_all[2][kMaxParts];
-  __shared__ unsigned long long sh_top[kMaxParts];
+  __shared__ float sh_top[kMaxParts], sh_sum[kMaxParts];
+  __shared__ unsigned long long sh_best[kMaxParts];
   __shared__ int sh_fed[kTreeT];
   __shared__ int sh_id[kThreads], sh_kept[kWarps];  // a part of the biases: those of this block's ids, in order
   __shared__ float sh_bias[kThreads];
@@ -119,42 +90,46 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsArgs k) {
     n = static_cast<int>(m);
   }
   if (t >= n) return;
+  if (parts > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this block runs: its sums can be written
   const long long tok = first + t;
-  const int from = rank * k.slice, size = min(k.slice, a.vocab - from);  // this block's ids; none: size <= 0
-  const IN* x = static_cast<const IN*>(a.logits) + tok * a.logits_stride + from;
-  OUT* out = static_cast<OUT*>(a.out) + tok * a.out_stride + from;
-  const bool wide_in = (reinterpret_cast<uintptr_t>(x) & 15u) == 0, wide_out = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
+  const IN* x = static_cast<const IN*>(a.logits) + tok * a.logits_stride;
+  OUT* out = static_cast<OUT*>(a.out) + tok * a.out_stride;
+  const int off = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(IN));
+  const int base = rank * k.slice - off;  // the id of word 0
+  const int words = min(k.slice, a.vocab - base);  // up to the last id's; none: <= 0
+  auto holds = [&](int id) { return id >= max(base, 0) && id - base < words; };  // (an id below 0 is none)
+
+  // ---- the first logits, asked for early
+  uint4 raw[kAhead][PIECES];
+  auto ask = [&](int w0) {
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) {
+      const int w = w0 + s * kStride + threadIdx.x * kRun, id = base + w;
+      if (w < words && id >= 0 && w + kRun <= words) {
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) raw[s][i] = __ldcs(reinterpret_cast<const uint4*>(x + id) + i);
+      }
+    }
+  };
+  ask(0);
+
   float temp = a.temperature ? a.temperature[b] : 1.0f;
   if (!(temp >= 0.0f)) temp = 1.0f;
   float rep = a.repetition ? a.repetition[b] : 1.0f;
   if (!(rep > 0.0f)) rep = 1.0f;
   const float presence = a.presence ? a.presence[b] : 0.0f, frequency = a.frequency ? a.frequency[b] : 0.0f;
   const bool counted = rep != 1.0f || presence != 0.0f || frequency != 0.0f;
-
-  // ---- this lane's entry of the first biases, asked for early
-  const bool biased = a.bias_id != nullptr;
   long long bias_lo = 0, bias_hi = 0;
-  int bias_id = -1;
-  float bias_value = 0.0f;
-  auto bias_entry = [&](long long e0) {
-    const long long e = e0 + threadIdx.x;
-    bias_id = -1;
-    if (e < bias_hi) {
-      const int id = a.bias_id[e];
-      bias_id = id >= from ? id - from : -1;
-      bias_value = a.bias_value[e];
-    }
-  };
-  if (biased) {
+  if (a.bias_id) {
     bias_lo = max(0, a.bias_start[b]);
     bias_hi = min(static_cast<long long>(a.bias_start[b + 1]), static_cast<long long>(a.biases));
-    bias_entry(bias_lo);
   }
+  const bool biased = bias_lo < bias_hi, marked = counted || biased;
 
-  // ---- counts
-  if (counted) {
-    for (int i = threadIdx.x; i < k.slice; i += kThreads) word[i] = 0u;
-    if (warp == 0 && a.tokens) {
+  // ---- counts, and marks of ids with a bias
+  if (marked) {
+    for (int i = threadIdx.x * 4; i < k.slice; i += kThreads * 4) *reinterpret_cast<uint4*>(word + i) = make_uint4(0u, 0u, 0u, 0u);
+    if (counted && warp == 0 && a.tokens) {
       // the fed tokens on the path to this one
       unsigned long long mask = (2ull << t) - 1ull;  // a chain: all up to it
       if (a.parents) {
@@ -174,75 +149,88 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsArgs k) {
       }
     }
     __syncthreads();
-    if (a.history) {
+    if (counted && a.history) {
       const int* h = a.history + b * a.history_stride;
       const int len = min(max(a.history_len[b], 0), a.history_max);
       const int prompt = a.prompt_len ? min(max(a.prompt_len[b], 0), len) : 0;
-#pragma unroll 4
-      for (int i = threadIdx.x; i < len; i += kThreads) {
-        const int id = h[i];
-        if (id >= from && id < from + size) {
-          if (i < prompt) atomicOr(word + id - from, kSeen);
-          else atomicAdd(word + id - from, 1u);
+      for (int i0 = threadIdx.x; i0 < len; i0 += 8 * kThreads) {
+        int id[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) id[e] = i0 + e * kThreads < len ? h[i0 + e * kThreads] : -1;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (holds(id[e])) {
+            if (i0 + e * kThreads < prompt) atomicOr(word + id[e] - base, kSeen);
+            else atomicAdd(word + id[e] - base, 1u);
+          }
         }
       }
     }
-    if (a.tokens && threadIdx.x < kTreeT) {
-      const int id = sh_fed[threadIdx.x];  // -1: none
-      if (id >= from && id < from + size) atomicAdd(word + id - from, 1u);
+    if (counted && a.tokens && threadIdx.x < kTreeT && holds(sh_fed[threadIdx.x])) atomicAdd(word + sh_fed[threadIdx.x] - base, 1u);
+    for (long long e = bias_lo + threadIdx.x; e < bias_hi; e += kThreads) {
+      const int id = a.bias_id[e];
+      if (holds(id)) atomicOr(word + id - base, kBiased);
     }
     __syncthreads();
   }
 
-  // ---- the logits with their penalties, into the words
+  // ---- the logits with their penalties, masked, into the words
   const uint32_t* mask = a.mask ? a.mask + tok * a.mask_stride : nullptr;
   float top = -INFINITY;
   unsigned long long key = 0ull;
-  // an id's last steps; a softmax divides by the temperature later, what is left of the largest: that stays in range
-  auto finish = [&](float y, uint32_t allowed) {
-    if (!allowed || y != y) y = -INFINITY;
-    return temp > 0.0f && !a.probs ? __fdiv_rn(y, temp) : y;
-  };
   auto take = [&](float y, int id) {
     top = fmaxf(top, y);
     if (temp == 0.0f && y > -INFINITY) key = max(key, top_key(y, id));
   };
-  auto bits = [&](int i) {  // the mask's bits of ids from + i ..
-    if (!mask) return 0xffffffffu;
-    const int id = from + i;
-    return mask[id >> 5] >> (id & 31);
+  auto allowed = [&](int id) {  // the mask's bits of eight ids, the first of which may be before the row's
+    if (!mask) return 0xffu;
+    if (id < 0) return mask[0] << -id;
+    const uint32_t lo = mask[id >> 5], hi = (id & 31) > 24 && (id | 31) + 1 < a.vocab ? mask[(id >> 5) + 1] : 0u;
+    return __funnelshift_r(lo, hi, id & 31);
   };
-  for (int i = threadIdx.x * kRun; i < size; i += kThreads * kRun) {
-    float f[kRun];
-    load<IN, kRun>(x + i, size - i, wide_in, f);
-    if (counted) {
-      uint32_t w[kRun];
-      *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(word + i);
-      *reinterpret_cast<uint4*>(w + 4) = *reinterpret_cast<const uint4*>(word + i + 4);
+  for (int w0 = 0; w0 < words; w0 += kAhead * kStride) {
+    if (w0) ask(w0);
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) {
+      const int w = w0 + s * kStride + threadIdx.x * kRun, id = base + w;
+      if (w >= words) continue;
+      const bool all = id >= 0 && w + kRun <= words;
+      float f[kRun];
+      if (all) {
+#pragma unroll
+        for (int e = 0; e < kRun; ++e) f[e] = value<IN>(reinterpret_cast<const IN*>(raw[s])[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kRun; ++e) f[e] = id + e >= 0 && w + e < words ? value<IN>(x[id + e]) : -INFINITY;
+      }
+      const uint32_t ok = allowed(id);
+      uint32_t c[kRun];
+      if (marked) {
+        *reinterpret_cast<uint4*>(c) = *reinterpret_cast<const uint4*>(word + w);
+        *reinterpret_cast<uint4*>(c + 4) = *reinterpret_cast<const uint4*>(word + w + 4);
+      }
 #pragma unroll
       for (int e = 0; e < kRun; ++e) {
-        if (w[e]) {
+        if (marked && c[e] & ~kBiased) {
           f[e] = f[e] > 0.0f ? __fdiv_rn(f[e], rep) : f[e] * rep;
-          const unsigned c = w[e] & ~kSeen;
-          if (c) f[e] -= presence + frequency * static_cast<float>(c);
+          const unsigned m = c[e] & ~(kSeen | kBiased);
+          if (m) f[e] -= presence + frequency * static_cast<float>(m);
         }
+        if (!(ok >> e & 1u) || f[e] != f[e]) f[e] = -INFINITY;
+        if (!(marked && c[e] & kBiased)) take(f[e], id + e);
       }
+      *reinterpret_cast<float4*>(word + w) = make_float4(f[0], f[1], f[2], f[3]);
+      *reinterpret_cast<float4*>(word + w + 4) = make_float4(f[4], f[5], f[6], f[7]);
     }
-    if (!biased) {
-      const uint32_t ok = bits(i);
-#pragma unroll
-      for (int e = 0; e < kRun; ++e) {
-        f[e] = i + e < size ? finish(f[e], ok >> e & 1u) : -INFINITY;
-        take(f[e], from + i + e);
-      }
-    }
-    *reinterpret_cast<float4*>(word + i) = make_float4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<float4*>(word + i + 4) = make_float4(f[4], f[5], f[6], f[7]);
   }
+  float* const val = reinterpret_cast<float*>(word);
   if (biased) {
-    for (long long e0 = bias_lo; e0 < bias_hi; e0 += kThreads) {  // (a barrier with the dense pass inside)
-      if (e0 > bias_lo) bias_entry(e0);
-      const bool mine = bias_id >= 0 && bias_id < size;
+    // ---- the biases: those of this block's ids, in order, a part of the entries at a time
+    __syncthreads();
+    for (long long e0 = bias_lo; e0 < bias_hi; e0 += kThreads) {
+      const long long e = e0 + threadIdx.x;
+      const int id = e < bias_hi ? a.bias_id[e] : -1;
+      const bool mine = holds(id);
       const unsigned kept = __ballot_sync(full, mine);
       if (lane == 0) sh_kept[warp] = __popc(kept);
       __syncthreads();
@@ -253,57 +241,70 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsArgs k) {
         all += sh_kept[i];
       }
       if (mine) {
-        sh_id[at] = bias_id;
-        sh_bias[at] = bias_value;
+        sh_id[at] = id - base;
+        sh_bias[at] = a.bias_value[e];
       }
       __syncthreads();
       if (warp == 0) {
-        // of 32 entries at a time, the first lane of those with one id adds them up, in order
-        float* y = reinterpret_cast<float*>(word);
+        // of 32 entries at a time, the first lane of those with one id adds them up
         for (int i0 = 0; i0 < all; i0 += 32) {
           const bool on = i0 + lane < all;
-          const int id = on ? sh_id[i0 + lane] : -1 - lane;
+          const int w = on ? sh_id[i0 + lane] : -1 - lane;
           const float v = on ? sh_bias[i0 + lane] : 0.0f;
-          const unsigned same = __match_any_sync(full, id);
+          const unsigned same = __match_any_sync(full, w);
           const int count = __popc(same), most = __reduce_max_sync(full, count);
-          float sum = on ? y[id] : 0.0f;
+          float sum = on ? val[w] : 0.0f;
           for (int j = 0; j < most; ++j) {
             const float add = __shfl_sync(full, v, j < count ? static_cast<int>(__fns(same, 0, j + 1)) : lane);
             if (j < count) sum += add;
           }
-          if (on && lane == __ffs(same) - 1) y[id] = sum;
+          if (on && lane == __ffs(same) - 1) val[w] = sum;
           __syncwarp();
         }
       }
       __syncthreads();
     }
-    if (bias_lo >= bias_hi) __syncthreads();
-    for (int i = threadIdx.x * kRun; i < size; i += kThreads * kRun) {
-      float f[kRun];
-      *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(word + i);
-      *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(word + i + 4);
-      const uint32_t ok = bits(i);
-#pragma unroll
-      for (int e = 0; e < kRun; ++e) {
-        f[e] = i + e < size ? finish(f[e], ok >> e & 1u) : -INFINITY;
-        take(f[e], from + i + e);
-      }
-      *reinterpret_cast<float4*>(word + i) = make_float4(f[0], f[1], f[2], f[3]);
-      *reinterpret_cast<float4*>(word + i + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    // (entries of one id look at the same value)
+    for (long long e = bias_lo + threadIdx.x; e < bias_hi; e += kThreads) {
+      const int id = a.bias_id[e];
+      if (holds(id) && val[id - base] == val[id - base]) take(val[id - base], id);
     }
   }
-  // (a lane reads back what it wrote itself)
-  if (!a.probs) {
-    for (int i = threadIdx.x * kRun; i < size; i += kThreads * kRun) {
-      float f[kRun];
-      *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(word + i);
-      *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(word + i + 4);
-      store<OUT, kRun>(out + i, size - i, wide_out, f);
+
+  const bool wide = ((reinterpret_cast<uintptr_t>(out) - off * sizeof(OUT)) & 15u) == 0;
+  // the words, times `scale`, to the row: 16 bytes a lane where its alignment goes with the logits', else neighbouring values by neighbouring lanes
+  auto write = [&](auto result) {
+    if (wide) {
+      constexpr int OV = 16 / sizeof(OUT);
+      for (int w = threadIdx.x * kRun; w < words; w += kStride) {
+        const int id = base + w;
+        OUT y[kRun];
+#pragma unroll
+        for (int e = 0; e < kRun; ++e) y[e] = rounded<OUT>(result(w + e));
+        if (id >= 0 && w + kRun <= words) {
+#pragma unroll
+          for (int i = 0; i < kRun; i += OV) __stcs(reinterpret_cast<uint4*>(out + id + i), *reinterpret_cast<const uint4*>(y + i));
+        } else {
+#pragma unroll
+          for (int e = 0; e < kRun; ++e)
+            if (id + e >= 0 && w + e < words) out[id + e] = y[e];
+        }
+      }
+    } else {
+      for (int w = threadIdx.x + max(0, -base); w < words; w += kThreads) out[base + w] = rounded<OUT>(result(w));
     }
+  };
+  if (!a.probs) {
+    __syncthreads();
+    write([&](int w) {
+      const float y = val[w] == val[w] ? val[w] : -INFINITY;
+      return temp > 0.0f ? __fdiv_rn(y, temp) : y;
+    });
+    if (parts > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     return;
   }
 
-  // ---- the row's maximum
+  // ---- the block's maximum, its exponentials and their sum; then the row's
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     top = fmaxf(top, __shfl_xor_sync(full, top, o));
@@ -314,74 +315,63 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsArgs k) {
     sh_key[warp] = key;
   }
   __syncthreads();
-  top = sh_part[lane % kWarps];
-  key = sh_key[lane % kWarps];
 #pragma unroll
-  for (int o = kWarps / 2; o; o >>= 1) {
-    top = fmaxf(top, __shfl_xor_sync(full, top, o));
-    key = max(key, __shfl_xor_sync(full, key, o));
+  for (int i = 0; i < kWarps; ++i) {
+    top = fmaxf(top, sh_part[i]);
+    key = max(key, sh_key[i]);
   }
-  if (parts > 1) {
-    cl.sync();  // all blocks run
-    if (threadIdx.x < parts) {
-      *cl.map_shared_rank(&sh_all[0][rank], threadIdx.x) = top;
-      *cl.map_shared_rank(&sh_top[rank], threadIdx.x) = key;
-    }
-    cl.sync();
-    for (int i = 0; i < parts; ++i) {
-      top = fmaxf(top, sh_all[0][i]);
-      key = max(key, sh_top[i]);
-    }
-  }
-  float scale = 0.0f;
-  if (temp > 0.0f) {
-    // ---- and its sum
-    const float cool = __fdiv_rn(1.0f, temp);
-    float sum = 0.0f;
-    if (top > -INFINITY) {
-      for (int i = threadIdx.x * kRun; i < size; i += kThreads * kRun) {
-        float f[kRun];
-        *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(word + i);
-        *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(word + i + 4);
+  float sum = 0.0f;
+  const float cool = __fdiv_rn(1.0f, temp);  // the temperature divides what is left of the largest: that stays in range
+  auto weight = [&](float y, float most) {   // (infinite ones too, and any temperature; NaN: 0)
+    const float d = y - most;
+    return y == most ? 1.0f : d > -INFINITY ? expf(d * cool) : 0.0f;
+  };
+  if (temp > 0.0f && top > -INFINITY) {
+    for (int w = threadIdx.x * kRun; w < words; w += kStride) {
+      float f[kRun];
+      *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(val + w);
+      *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(val + w + 4);
 #pragma unroll
-        for (int e = 0; e < kRun; ++e) {
-          const float d = f[e] - top;
-          f[e] = f[e] == top ? 1.0f : d == -INFINITY ? 0.0f : expf(d * cool);  // (infinite ones too, and any temperature)
-          sum += f[e];
-        }
-        *reinterpret_cast<float4*>(word + i) = make_float4(f[0], f[1], f[2], f[3]);
-        *reinterpret_cast<float4*>(word + i + 4) = make_float4(f[4], f[5], f[6], f[7]);
+      for (int e = 0; e < kRun; ++e) {
+        f[e] = weight(f[e], top);
+        sum += f[e];
       }
+      *reinterpret_cast<float4*>(val + w) = make_float4(f[0], f[1], f[2], f[3]);
+      *reinterpret_cast<float4*>(val + w + 4) = make_float4(f[4], f[5], f[6], f[7]);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(full, sum, o);
-    __syncthreads();  // sh_part is read
-    if (lane == 0) sh_part[warp] = sum;
-    __syncthreads();
-    sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) sum += sh_part[i];
-    if (parts > 1) {
-      if (threadIdx.x < parts) *cl.map_shared_rank(&sh_all[1][rank], threadIdx.x) = sum;
-      cl.sync();
-      sum = 0.0f;
-      for (int i = 0; i < parts; ++i) sum += sh_all[1][i];
-    }
-    scale = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
   }
-  const int best = key ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(key)) : -1;
-  for (int i = threadIdx.x * kRun; i < size; i += kThreads * kRun) {
-    float f[kRun];
-    if (temp > 0.0f) {
-      *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(word + i);
-      *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(word + i + 4);
+  __syncthreads();  // sh_part is read
+  if (lane == 0) sh_part[warp] = sum;
+  __syncthreads();
+  sum = 0.0f;
 #pragma unroll
-      for (int e = 0; e < kRun; ++e) f[e] = scale == 0.0f ? 0.0f : f[e] * scale;
-    } else {
-#pragma unroll
-      for (int e = 0; e < kRun; ++e) f[e] = from + i + e == best ? 1.0f : 0.0f;
+  for (int i = 0; i < kWarps; ++i) sum += sh_part[i];
+  float most = top;
+  if (parts > 1) {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    if (threadIdx.x < parts) {
+      *cl.map_shared_rank(&sh_top[rank], threadIdx.x) = top;
+      *cl.map_shared_rank(&sh_sum[rank], threadIdx.x) = sum;
+      *cl.map_shared_rank(&sh_best[rank], threadIdx.x) = key;
     }
-    store<OUT, kRun>(out + i, size - i, wide_out, f);
+    cl.sync();
+    for (int i = 0; i < parts; ++i) {
+      most = fmaxf(most, sh_top[i]);
+      key = max(key, sh_best[i]);
+    }
+    sum = 0.0f;
+    for (int i = 0; i < parts; ++i) sum += sh_sum[i] > 0.0f ? sh_sum[i] * weight(sh_top[i], most) : 0.0f;
+  }
+  if (temp > 0.0f) {
+    // (a block whose values are all -inf has them in the words still)
+    const float scale = top > -INFINITY && sum > 0.0f ? weight(top, most) * __fdiv_rn(1.0f, sum) : 0.0f;
+    if (scale > 0.0f) write([&](int w) { return val[w] * scale; });
+    else write([&](int) { return 0.0f; });
+  } else {
+    const int best = key ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(key)) : -1;
+    write([&](int w) { return base + w == best ? 1.0f : 0.0f; });
   }
 }
 
@@ -449,13 +439,13 @@ extern "C" rssm_status rssm_logits(const rssm_logits_args* args, void* stream) {
   if (!a.logits || !a.out) return RSSM_ERR_INVALID_ARGUMENT;
   const int sms = num_sms();
   if (sms == 0) return RSSM_ERR_CUDA;
-  // blocks of a row: while all rows' still run at once, and each has 2048 ids; and as many as a slice's words need
+  // blocks of a row: while all rows' still run at once, and each has 2048 ids; and as many as let three blocks' words be on an SM
   int parts = 1;
-  while (parts < kMaxParts && ((static_cast<int64_t>(a.batch) * a.T * parts * 2 <= 2 * sms && a.vocab > parts * 2048) || a.vocab > parts * (kMaxSlice / 2)))
+  while (parts < kMaxParts && ((static_cast<int64_t>(a.batch) * a.T * parts * 2 <= kBlocks * sms && a.vocab > parts * 2048) || a.vocab > parts * 16384))
     parts *= 2;
   LogitsArgs k;
   k.a = a;
-  k.slice = ((a.vocab + parts - 1) / parts + 31) / 32 * 32;
+  k.slice = ((a.vocab + 7 + parts - 1) / parts + 31) / 32 * 32;  // (a row begins up to seven places in)
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = a.logits_dtype == RSSM_F32    ? launch_out<float>(k, parts, st)
                         : a.logits_dtype == RSSM_BF16 ? launch_out<__nv_bfloat16>(k, parts, st)

