@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attention_kernel(const Attn
             y = y < 7.7037197775489434e-34f ? 7.7037197775489434e-34f : y;  // 2^-110: a scale of 0 stands for zeros all the same
             kf[n][e] = x;
             lv[n][e] = __log2f(y);
-            iv[n][e] = __frcp_rn(y) * kShift8;  // a sum of 2^110 2^14 would pass fp32's range
+            iv[n][e] = y == y ? __frcp_rn(y) * kShift8 : 0.0f;  // a sum of 2^110 2^14 would pass fp32's range; NaN: the weight is that, or 0 if not seen
           }
       }
       uint32_t pa[MT][4];
@@ -324,17 +324,14 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attention_kernel(const Attn
               if constexpr (Q8) y = y * kf[n][e] + lv[n][e];
               v[2 * n + e] = y;
             }
-          unsigned seen = 0xfu;
           if (edge) {
             const int t = (row0 + r) / a.group;  // rows past the tile's last see what it sees
-            seen = 0u;
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int j = pos + 8 * n + 2 * cc + e - w.len;  // which new token this is
                 const bool y = j < 0 || (j < w.s.count && (a.parents ? t < kTreeT && (sh_mask[t] >> (j & 63) & 1) : j <= t));
-                seen |= y ? 1u << (2 * n + e) : 0u;
                 if (!y) v[2 * n + e] = -INFINITY;
               }
           }
@@ -358,13 +355,13 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attention_kernel(const Attn
           for (int y = 0; y < 4; ++y) p[y] = exp2_fast(v[y] - (Q8 ? ref - kShift : ref));
           if constexpr (Q8) {
 #pragma unroll
-            for (int y = 0; y < 4; ++y) l[x][h] += seen >> y & 1 ? p[y] * iv[y >> 1][y & 1] : 0.0f;
-            pa[x][h] = pack_f16(p[0], p[1]);
-            pa[x][2 + h] = pack_f16(p[2], p[3]);
+            for (int y = 0; y < 4; ++y) l[x][h] += p[y] * iv[y >> 1][y & 1];
+            pa[x][h] = f16_pair(p[0], p[1]);
+            pa[x][2 + h] = f16_pair(p[2], p[3]);
           } else {
             l[x][h] += (p[0] + p[1]) + (p[2] + p[3]);
-            pa[x][h] = pack_bf16(p[0], p[1]);
-            pa[x][2 + h] = pack_bf16(p[2], p[3]);
+            pa[x][h] = bf16_pair(p[0], p[1]);
+            pa[x][2 + h] = bf16_pair(p[2], p[3]);
           }
         }
 

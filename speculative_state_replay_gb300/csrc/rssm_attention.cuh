@@ -23,6 +23,7 @@ struct AttnArgs {
   int group;
   float scale2;  // scale log2(e)
   int whole;     // a block takes one segment, the longest first, instead of an equal part of the line
+  int box;           // tokens of one copy (the kernel for many queries)
   unsigned* ticket;  // [blocks]
   float* partial;    // [blocks][2][rows of a tile x (head_dim + 2)]
 };
@@ -32,12 +33,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+__device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
@@ -85,7 +86,7 @@ __device__ __forceinline__ uint4 query_f16(const uint4& x, float& back) {
   const uint32_t y[4] = {x.x, x.y, x.z, x.w};
   uint32_t z[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) z[i] = pack_f16(bf16lo(y[i]) * f1 * f2, bf16hi(y[i]) * f1 * f2);
+  for (int i = 0; i < 4; ++i) z[i] = f16_pair(bf16lo(y[i]) * f1 * f2, bf16hi(y[i]) * f1 * f2);
   return make_uint4(z[0], z[1], z[2], z[3]);
 }
 
@@ -208,7 +209,7 @@ __device__ __forceinline__ void add_odd(const AttnArgs& a, const RowWork& w, con
 __device__ __forceinline__ void write_out(const AttnArgs& a, const RowWork& w, int head, int query, int D, int x4, const float (&y)[4], float inv) {
   const int t = query / a.group, h = head * a.group + query - t * a.group;
   *reinterpret_cast<uint2*>(a.out + (w.s.first + t) * a.out_stride + static_cast<long long>(h) * D + x4) =
-      make_uint2(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv));
+      make_uint2(bf16_pair(y[0] * inv, y[1] * inv), bf16_pair(y[2] * inv, y[3] * inv));
 }
 
 // A segment that several blocks share: each leaves its sums, and whoever leaves the last joins them, in the
@@ -232,25 +233,66 @@ __device__ __forceinline__ void join_pieces(const AttnArgs& a, const RowWork& w,
   if (!last) return;
   __threadfence();
   constexpr int D4 = D / 4;
-#pragma unroll 1
-  for (int i = threadIdx.x; i < rows * D4; i += kThreads) {
-    const int r = i / D4, x4 = (i - r * D4) * 4;
+  struct Sum {
     float y[4] = {0.0f, 0.0f, 0.0f, 0.0f}, z = 0.0f, top = -INFINITY;
-#pragma unroll 4
-    for (int x = 0; x < pieces; ++x) {
-      const float* p = piece_place<kRows, D>(a, first + x, x == 0);
-      const float mx = __ldcg(p + kRows * D + r), lx = __ldcg(p + kRows * D + kRows + r);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(p + r * D + x4));
-      const float now = fmaxf(top, mx), ref = now == -INFINITY ? 0.0f : now;
-      const float f = exp2_fast(top - ref), e = exp2_fast(mx - ref);
+    __device__ __forceinline__ void add(const float4& v, float m, float l) {
+      const float now = fmaxf(top, m), ref = now == -INFINITY ? 0.0f : now;
+      const float f = exp2_fast(top - ref), g = exp2_fast(m - ref);
       top = now;
-      y[0] = y[0] * f + v.x * e;
-      y[1] = y[1] * f + v.y * e;
-      y[2] = y[2] * f + v.z * e;
-      y[3] = y[3] * f + v.w * e;
-      z = z * f + lx * e;
+      y[0] = y[0] * f + v.x * g;
+      y[1] = y[1] * f + v.y * g;
+      y[2] = y[2] * f + v.z * g;
+      y[3] = y[3] * f + v.w * g;
+      z = z * f + l * g;
     }
-    write_out(a, w, head, row0 + r, D, x4, y, z == 0.0f ? 0.0f : unit / z);
+  };
+  auto write = [&](const Sum& s, int r, int x4) { write_out(a, w, head, row0 + r, D, x4, s.y, s.z == 0.0f ? 0.0f : unit / s.z); };
+  auto load = [&](const float* p, int r, int x4, float4& v, float& m, float& l) {
+    m = __ldcg(p + kRows * D + r);
+    l = __ldcg(p + kRows * D + kRows + r);
+    v = __ldcg(reinterpret_cast<const float4*>(p + r * D + x4));
+  };
+  // loads on their way at a time: of eight pieces where a thread has one output or two, else of four outputs
+  if (rows * D4 <= 2 * kThreads) {
+#pragma unroll 1
+    for (int i = threadIdx.x; i < rows * D4; i += kThreads) {
+      const int r = i / D4, x4 = (i - r * D4) * 4;
+      Sum s;
+#pragma unroll 1
+      for (int x0 = 0; x0 < pieces; x0 += 8) {
+        float4 v[8];
+        float m[8], l[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (x0 + e < pieces) load(piece_place<kRows, D>(a, first + x0 + e, x0 + e == 0), r, x4, v[e], m[e], l[e]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (x0 + e < pieces) s.add(v[e], m[e], l[e]);
+      }
+      write(s, r, x4);
+    }
+  } else {
+    constexpr int N = 4;
+#pragma unroll 1
+    for (int i0 = threadIdx.x; i0 < rows * D4; i0 += N * kThreads) {
+      Sum s[N];
+#pragma unroll 1
+      for (int x = 0; x < pieces; ++x) {
+        const float* p = piece_place<kRows, D>(a, first + x, x == 0);
+        float4 v[N];
+        float m[N], l[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const int i = min(i0 + e * kThreads, rows * D4 - 1);
+          load(p, i / D4, i % D4 * 4, v[e], m[e], l[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e) s[e].add(v[e], m[e], l[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (i0 + e * kThreads < rows * D4) write(s[e], (i0 + e * kThreads) / D4, (i0 + e * kThreads) % D4 * 4);
+    }
   }
 }
 

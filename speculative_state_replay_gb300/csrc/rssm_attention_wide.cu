@@ -16,24 +16,23 @@
 // Work is cut as in rssm_attention.cu, or, where there are segments enough for all
 // blocks, a segment a block with the longest first: a prompt's late queries see more.
 #include "rssm_attention.cuh"
+#include "rssm_readout.cuh"
 #include "rssm_tcgen05.cuh"
 
 namespace rssm {
 namespace {
 
-constexpr int kQ = 128;                    // queries of a tile: the product's rows
-constexpr int kTiles = 2;                  // tiles of a block
+constexpr int kQ = 128;                 // queries of a tile: the product's rows
+constexpr int kTiles = 2;               // tiles of a block
 constexpr int kRows = kTiles * kQ;
-constexpr int kTok = 128;                  // tokens of a step
-constexpr int kSoftWarps = 4 * kTiles;     // a thread has a query
-constexpr int kLoadWarps = 3;
-constexpr int kLoaders = kLoadWarps * 32;
-constexpr int kThreads = (kSoftWarps + kLoadWarps + 1) * 32;
-constexpr int kInfo = 4;                   // places of what goes with a step of tokens: K of step j + 4 waits for a buffer that is
-                                           // free once the scores of j + 2 are made, which is after the weights of j
-constexpr float kLazy = 4.0f;              // log2 of how far the true maximum may be past the one in use
-constexpr float kShift = 11.0f;            // fp16 weights are times 2^11: 2^15 at most
-constexpr int kTmem = 512;                 // columns: two of S, two of O
+constexpr int kTok = 128;               // tokens of a step
+constexpr int kSoftWarps = 4 * kTiles;  // a thread has a query
+constexpr int kSoft = kSoftWarps * 32;
+constexpr int kInfo = 4;                // places of what goes with a step of tokens: K of step j + 4 waits for a buffer that is
+                                        // free once the scores of j + 2 are made, which is after the weights of j
+constexpr float kLazy = 4.0f;           // log2 of how far the true maximum may be past the one in use
+constexpr float kShift = 11.0f;         // fp16 weights are times 2^11: 2^15 at most
+constexpr int kTmem = 512;              // columns: two of S, two of O
 
 struct Wait {  // a wait that gives up is for all of the block
   volatile int* dead;
@@ -51,21 +50,33 @@ template <int D_, int FMT_>
 struct Shape {
   static constexpr int D = D_, FMT = FMT_;
   static constexpr bool Q8 = FMT != RSSM_BF16;
+  static constexpr int kLoadWarps = Q8 ? 7 : 3;   // bf16: one of them copies, all look at tiles that not every query sees
+  static constexpr int kLoaders = kLoadWarps * 32;
+  static constexpr int kThreads = kSoft + kLoaders + 32;
   static constexpr int RB = D * (Q8 ? 1 : 2);     // bytes of a cached head
   static constexpr int NC = RB / 16;              // and its 16-byte chunks
   static constexpr int kTile = kTok * D * 2;      // bytes of a tile as an operand: per 64 dimensions, rows of 128 bytes
-  static constexpr int kRing = Q8 ? 3 : 4;        // buffers of a tile of keys or values
-  static constexpr int kRaw = Q8 ? 3 : 0;         // 8-bit: tiles as they come, on their way to be converted
+  static constexpr int kRing = Q8 ? 3 : 4;        // buffers of a tile of keys or values; 8-bit: as many of tiles as they come
   static constexpr int kRingAt = kTiles * kTile;  // queries first
   static constexpr int kRawAt = kRingAt + kRing * kTile;
-  static constexpr int kInfoAt = kRawAt + kRaw * kTok * RB;
+  static constexpr int kInfoAt = kRawAt + (Q8 ? kRing * kTok * RB : 0);
   static constexpr int kBarsAt = kInfoAt + (Q8 ? kInfo * 3 * kTok * 4 : 0);
   static constexpr int kSmem = kBarsAt + 256 + 1024;  // and room to start on 1024 bytes
-  static_assert(kSmem <= 227 * 1024 && kRing * kTile >= kQ * D * 4, "fits, and a tile's sums fit the ring");
+  static_assert(kSmem <= 226 * 1024 && kRing * kTile >= kQ * D * 4, "fits, and a tile's sums fit the ring");
+};
+
+struct Slice {  // 16 tokens of a step
+  long long off[2];       // bytes from the head's first key (value)
+  int page, place, live;  // its page, where it begins there, and how many of the tokens there are
 };
 
 __device__ __forceinline__ uint32_t sw(int r, int ch) { return static_cast<uint32_t>(r * 128 + ((ch ^ (r & 7)) << 4)); }
 
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst), "l"(map),
+               "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+               : "memory");
+}
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {  // first operand in tensor memory
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -136,33 +147,39 @@ __device__ __forceinline__ void scaled(uint32_t& x0, uint32_t& x1, pair back, pa
   x1 = __float_as_uint(y1);
 }
 
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoft) : "memory"); }
+
 template <typename S>
-__global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
-  constexpr int D = S::D, RB = S::RB, NC = S::NC, kRing = S::kRing;
+__global__ void __launch_bounds__(S::kThreads, 1)
+    wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+  constexpr int D = S::D, RB = S::RB, NC = S::NC, kRing = S::kRing, kThreads = S::kThreads, kLoadWarps = S::kLoadWarps, kLoaders = S::kLoaders;
   constexpr bool Q8 = S::Q8;
   extern __shared__ uint8_t raw[];
   uint8_t* const sm = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
   __shared__ uint32_t tmem_base;
   __shared__ volatile int dead;
-  __shared__ int sh_bad, sh_odd;
-  __shared__ unsigned long long sh_mask[kTreeT];
-  __shared__ float sh_back[kRows];
+  __shared__ int sh_odd;  // the last piece (counted from 1) with values that are not finite among its new tokens
+  __shared__ float sh_back[kRows], sh_ref[kQ], sh_sum[kQ];
   __shared__ unsigned sh_valid[kInfo];
+  __shared__ Slice sh_slice[kLoadWarps][2][8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const unsigned full = 0xffffffffu;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(sm + S::kBarsAt);
-  uint64_t *const b_full = bars, *const b_empty = bars + kRing, *const b_s = bars + 2 * kRing, *const b_p = b_s + kTiles, *const b_o = b_p + kTiles,
-           *const b_info = b_o + kTiles;
+  uint64_t *const b_full = bars, *const b_empty = b_full + kRing, *const b_raw = b_empty + kRing, *const b_free = b_raw + kRing,
+           *const b_s = b_free + kRing, *const b_p = b_s + kTiles, *const b_o = b_p + kTiles, *const b_info = b_o + kTiles, *const b_q = b_info + kInfo;
   const uint32_t base = smem_addr(sm);
-  if (warp == kSoftWarps + kLoadWarps) {
+  constexpr int kMmaWarp = kSoftWarps + kLoadWarps;
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)), "n"(kTmem) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (tid == 0) {
-    dead = 0;
+    dead = sh_odd = 0;
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(b_full + i, kLoaders);
+      mbar_init(b_full + i, kLoadWarps);
       mbar_init(b_empty + i, 1);
+      mbar_init(b_raw + i, 1);
+      mbar_init(b_free + i, kLoadWarps);
     }
     for (int i = 0; i < kTiles; ++i) {
       mbar_init(b_s + i, 1);
@@ -170,6 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
       mbar_init(b_o + i, 1);
     }
     for (int i = 0; i < kInfo; ++i) mbar_init(b_info + i, kLoaders);
+    mbar_init(b_q, kSoft);
     fence_barrier_init();
   }
   tc_before();
@@ -204,7 +222,8 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
   }
   int b = line.b;
   long long rbase = line.base;
-  int items = 0, steps = 0, used[kTiles] = {0, 0}, done[kTiles] = {0, 0};  // how often the ring, and what goes with it, the scores, the sums came round
+  // how often things came round so far: items of the ring, steps, pieces, and by tile scores and sums; fixed tiles (bf16)
+  int items = 0, steps = 0, pieces = 0, fixed = 0, used0 = 0, used1 = 0, done0 = 0, done1 = 0;
   bool ok = true;
 
 #pragma unroll 1
@@ -223,65 +242,71 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
     const long long seg0 = u - t0;
     u += t1 - t0;
     const int row0 = mtile * kRows, rows = min(kRows, w.s.count * a.group - row0);
-    const int nq = rows > kQ ? 2 : 1;
-    const bool alt = nq == 1;  // both tiles have the same queries, and every other step
-    __syncthreads();  // the last piece's shared memory is free
-    if (tid == 0) sh_bad = sh_odd = 0;
-    const bool flip = a.scale2 < 0.0f;  // the maximum is taken before the scale
-    const float scale2 = fmaxf(fabsf(a.scale2), 1e-30f);  // (times -inf it stays that)
-    {
-      constexpr int G = D / 8, AT = 32 / G;  // lanes of a row, rows of a warp
-#pragma unroll 1
-      for (int r0 = warp * AT; r0 < nq * kQ; r0 += kThreads / 32 * AT) {
-        const int r = r0 + lane / G, part = lane % G;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows) {
-          const int t = (row0 + r) / a.group, h = head * a.group + (row0 + r) - t * a.group;
-          x = *reinterpret_cast<const uint4*>(a.q + (w.s.first + t) * a.q_stride + static_cast<long long>(h) * D + part * 8);
-          if (flip) x = make_uint4(x.x ^ 0x80008000u, x.y ^ 0x80008000u, x.z ^ 0x80008000u, x.w ^ 0x80008000u);
-        }
-        if constexpr (Q8) {
-          float back;
-          x = query_f16<G>(x, back);
-          if (part == 0) sh_back[r] = scale2 * back;
-        }
-        *reinterpret_cast<uint4*>(sm + (r / kQ) * S::kTile + (part / 8) * 16384 + sw(r % kQ, part % 8)) = x;
-      }
-    }
-    __syncthreads();
-    if (a.parents && warp == 0 && w.len >= 0) {
-      unsigned long long mask[2];
-      const bool fine = tree_masks(a.parents + w.s.first, w.s.count, lane, mask);
-      sh_mask[lane] = mask[0];
-      sh_mask[lane + 32] = mask[1];
-      if (!fine && lane == 0) {
-        sh_bad = 1;
-        set_error(a.c.err, RSSM_ERRBIT_TREE);
-      }
-    }
-    fence_async();
-    __syncthreads();
+    const bool alt = rows <= kQ;  // both tiles have the same queries, and every other step
     const int last = (row0 + rows - 1) / a.group;
-    const long long end = w.len < 0 || sh_bad ? 0 : static_cast<long long>(w.len) + (a.parents ? w.s.count : last + 1);
+    // every warp looks at the row's tree by itself
+    unsigned long long masks[2] = {0ull, 0ull};
+    bool fine = true;
+    if (a.parents && w.len >= 0) fine = tree_masks(a.parents + w.s.first, w.s.count, lane, masks);
+    if (!fine && tid == 0) set_error(a.c.err, RSSM_ERRBIT_TREE);
+    const long long end = w.len < 0 || !fine ? 0 : static_cast<long long>(w.len) + (a.parents ? w.s.count : last + 1);
     // from here on there are tokens that not every query of the tile sees, or none
     const long long some = static_cast<long long>(w.len) + (a.parents ? 0 : row0 / a.group + 1);
     const int stop = static_cast<int>(min(static_cast<long long>(t1), (end + kTok - 1) / kTok));
     const int nt = max(0, stop - t0);
     const int* table = a.r.pages + b * a.r.pages_stride;
-    const uint8_t* kbase = a.c.k + static_cast<long long>(head) * a.c.page_size * RB;
     const uint8_t* vbase = a.c.v + static_cast<long long>(head) * a.c.page_size * RB;
-
     float ref = -INFINITY, sum = 0.0f, join0 = 1.0f, join1 = 0.0f;  // join: what the two tiles' sums are times where both have the same queries
+    int t = 0;                                                      // a thread's query's new token,
+    unsigned long long path = 0ull;                                 // and those it comes after
+    __syncthreads();  // the last piece's shared memory is free
+
     if (warp < kSoftWarps) {
+      // ---- queries
+      const float scale2 = fmaxf(fabsf(a.scale2), 1e-30f);  // (times -inf it stays that)
+      {
+        const bool flip = a.scale2 < 0.0f;           // the maximum is taken before the scale
+        constexpr int G = D / 8, AT = 32 / G, N = 4;  // lanes of a row, rows of a warp; rows on their way at a time
+#pragma unroll 1
+        for (int r0 = warp * AT; r0 < (alt ? kQ : kRows); r0 += N * kSoftWarps * AT) {
+          uint4 x[N];
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int r = r0 + i * kSoftWarps * AT + lane / G;
+            x[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < rows) {
+              const int tq = (row0 + r) / a.group, h = head * a.group + (row0 + r) - tq * a.group;
+              x[i] = *reinterpret_cast<const uint4*>(a.q + (w.s.first + tq) * a.q_stride + static_cast<long long>(h) * D + lane % G * 8);
+              if (flip) x[i] = make_uint4(x[i].x ^ 0x80008000u, x[i].y ^ 0x80008000u, x[i].z ^ 0x80008000u, x[i].w ^ 0x80008000u);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int r = r0 + i * kSoftWarps * AT + lane / G, part = lane % G;
+            if constexpr (Q8) {
+              float back;
+              x[i] = query_f16<G>(x[i], back);
+              if (part == 0) sh_back[r] = scale2 * back;
+            }
+            *reinterpret_cast<uint4*>(sm + (r / kQ) * S::kTile + (part / 8) * 16384 + sw(r % kQ, part % 8)) = x[i];
+          }
+        }
+      }
+      fence_async();
+      mbar_arrive(b_q);
+      if constexpr (Q8) soft_sync();
       // ---- scores into weights
       const int tile = warp >> 2;
       const int r = alt ? tid & (kQ - 1) : tid;  // its query
-      const int t = (row0 + min(r, rows - 1)) / a.group;
-      const unsigned long long path = a.parents ? sh_mask[t & 63] : 0ull;
+      t = (row0 + min(r, rows - 1)) / a.group;
+      if (a.parents) {
+        const unsigned long long m0 = __shfl_sync(full, masks[0], t & 31), m1 = __shfl_sync(full, masks[1], t & 31);
+        path = t < 32 ? m0 : m1;
+      }
       const float back = Q8 ? sh_back[r] : scale2;
       const uint32_t s_at = tm + tile * kTok + ((warp & 3) << 21), o_at = tm + kTiles * kTok + tile * D + ((warp & 3) << 21);
-      const int step = alt ? 2 : 1;
-      int n = used[tile];
+      const int step = alt ? 2 : 1, n0 = tile ? used1 : used0;
+      int n = n0;
 #pragma unroll 1
       for (int j = alt ? tile : 0; j < nt; j += step, ++n) {
         const int slot = (steps + j) % kInfo;
@@ -339,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
           const float f = now == -INFINITY ? 1.0f : exp2_fast(ref - now);
           ref = now;
           sum *= f;
-          if (n > used[tile]) {
+          if (n > n0) {
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
               uint32_t y[16];
@@ -363,28 +388,26 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
           if (c + 1 < kTok / 32) tc_ld32(x[(c + 1) & 1], s_at + 32 * (c + 1));
           uint32_t p[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            pair y = pack2(__uint_as_float(z[i]), __uint_as_float(z[i + 1]));
-            if constexpr (Q8) add2(y, lift2);
-            else y = fma2v(y, scale22, lift2);
-            float y0, y1;
-            unpack2(y, y0, y1);
-            y0 = exp2_fast(y0);
-            y1 = exp2_fast(y1);
-            const pair e = pack2(y0, y1);
-            if constexpr (Q8) {
-              // (a token that is not seen may have no scale: its weight 0 must not meet that)
-              pair v = *reinterpret_cast<const pair*>(info + 2 * kTok + 32 * c + i);
-              if (edge) {
-                float v0, v1;
-                unpack2(v, v0, v1);
-                v = pack2(y0 == 0.0f ? 0.0f : v0, y1 == 0.0f ? 0.0f : v1);
+          for (int i = 0; i < 32; i += 4) {
+            ulonglong2 v4;
+            if constexpr (Q8) v4 = *reinterpret_cast<const ulonglong2*>(info + 2 * kTok + 32 * c + i);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              pair y = pack2(__uint_as_float(z[i + 2 * e]), __uint_as_float(z[i + 2 * e + 1]));
+              if constexpr (Q8) add2(y, lift2);
+              else y = fma2v(y, scale22, lift2);
+              float y0, y1;
+              unpack2(y, y0, y1);
+              y0 = exp2_fast(y0);
+              y1 = exp2_fast(y1);
+              const pair p2 = pack2(y0, y1);
+              if constexpr (Q8) {
+                fma2(s2[e], p2, e ? v4.y : v4.x);
+                p[i / 2 + e] = f16_pair(y0, y1);
+              } else {
+                add2(s2[e], p2);
+                p[i / 2 + e] = bf16_pair(y0, y1);
               }
-              fma2(s2[i >> 1 & 1], e, v);
-              p[i >> 1] = pack_f16(y0, y1);
-            } else {
-              add2(s2[i >> 1 & 1], e);
-              p[i >> 1] = pack_bf16(y0, y1);
             }
           }
           tc_st16(s_at + 16 * c, p);
@@ -399,23 +422,22 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
         if (lane == 0) mbar_arrive(b_p + tile);
       }
       if (nt > (alt ? tile : 0)) {
-        ok = __all_sync(full, ok && wait(b_o + tile, done[tile] & 1)) != 0;
+        ok = __all_sync(full, ok && wait(b_o + tile, (tile ? done1 : done0) & 1)) != 0;
         tc_after();
       }
-    } else if (warp < kSoftWarps + kLoadWarps) {
+    } else if (warp < kMmaWarp) {
       // ---- keys and values, in turn
-      const int lt = tid - kSoftWarps * 32;
-      constexpr int CHUNKS = kTok * NC;  // of 16 bytes, in order: thread lt takes lt, lt + 96, ..
+      const int lt = tid - kSoft, lw = warp - kSoftWarps;
+      // a tile is 128 NC chunks of 16 bytes; thread lt looks at chunk `ch` of rows r0, r0 + R, ..
+      constexpr int R = kLoaders / NC, STEPS = (kTok + R - 1) / R;
+      const int ch = lt % NC, r0 = lt / NC;
       auto page_id = [&](int j) {
         const long long p = static_cast<long long>(t0 + j) * kTok + 16 * lane;
         return lane < 8 && j < nt && p < end ? table[static_cast<unsigned>(p) / static_cast<unsigned>(a.c.page_size)] : -1;
       };
       int next_id = page_id(0);
-      // lanes 0-7: where the step's slices of 16 tokens are, and how many of them are there
-      long long koff = 0, voff = 0;
-      int live = 0;
-      unsigned missing = 0u, place = 0u;
-      int page = 0;
+      unsigned missing = 0u;
+      // where the slices of step j are, for this warp
       auto find = [&](int j) {
         const long long mine = static_cast<long long>(t0 + j) * kTok + 16 * lane;
         const int id = next_id;
@@ -423,134 +445,127 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
         const bool wanted = lane < 8 && mine < end, have = wanted && id >= 0 && id < a.c.pages;
         if (wanted && !have) set_error(a.c.err, RSSM_ERRBIT_PAGE);
         missing = __ballot_sync(full, wanted && !have);
-        place = static_cast<unsigned>(mine) % static_cast<unsigned>(a.c.page_size);
-        page = have ? id : 0;
-        koff = have ? id * a.c.k_page + static_cast<long long>(place) * RB : 0;
-        voff = have ? id * a.c.v_page + static_cast<long long>(place) * RB : 0;
-        live = have ? static_cast<int>(min(16ll, end - mine)) : 0;
-      };
-      // a tile's copies: chunk i of it goes to dst(row, chunk of the row)
-      auto copy = [&](bool values, auto dst) {
-        const uint8_t* src = values ? vbase : kbase;
-        const long long off = values ? voff : koff;
-#pragma unroll 2
-        for (int x = 0; x < (CHUNKS + kLoaders - 1) / kLoaders; ++x) {
-          const int i = lt + kLoaders * x, r = i / NC, ch = i % NC, sl = (r / 16) & 7;  // (the warp's chunks may lie in two slices)
-          const long long o = __shfl_sync(full, off, sl);
-          const int there = __shfl_sync(full, live, sl);
-          if (i < CHUNKS) copy16(dst(i, r, ch), src + o + (r % 16) * RB + ch * 16, r % 16 < there);
+        if (lane < 8) {
+          const unsigned place = static_cast<unsigned>(mine) % static_cast<unsigned>(a.c.page_size);
+          Slice s;
+          s.off[0] = have ? id * a.c.k_page + (static_cast<long long>(head) * a.c.page_size + place) * RB : 0;
+          s.off[1] = have ? id * a.c.v_page + (static_cast<long long>(head) * a.c.page_size + place) * RB : 0;
+          s.page = have ? id : 0;
+          s.place = static_cast<int>(place);
+          s.live = have ? static_cast<int>(min(16ll, end - mine)) : 0;
+          sh_slice[lw][j & 1][lane] = s;
         }
-        copy_commit();
+        __syncwarp();
       };
-      auto step_info = [&](float (&ksv)[2], float (&vsv)[2]) {  // 8-bit: the scales of tokens lt and lt + 96
+      // the copies of item n, by the first of these warps: a lane takes the tokens that neighbour in a page
+      auto copy = [&](int n, uint64_t* bar, uint32_t to) {
+        const Slice* slices = sh_slice[lw][n >> 1 & 1];
+        const int groups = kTok / a.box;
+        const Slice sl = slices[lane < groups ? lane * a.box / 16 : 0];
+        const bool mine = lane < groups && sl.live > 0;
+        const int count = __popc(__ballot_sync(full, mine));
+        if (lane == 0) mbar_arrive_expect_tx(bar, count * a.box * RB);
+        __syncwarp();
+        if (mine) {
+          if constexpr (Q8) {
+            const uint8_t* src = (n & 1 ? a.c.v : a.c.k) + sl.off[n & 1];
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to + lane * a.box * RB), "l"(src),
+                         "r"(a.box * RB), "r"(smem_addr(bar))
+                         : "memory");
+          } else {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int i = lt + kLoaders * e, sl = (i / 16) & 7;
-          const long long row = static_cast<long long>(head) * a.c.page_size + __shfl_sync(full, place, sl) + (i & 15);
-          const int pg = __shfl_sync(full, page, sl);
-          const bool there = i < kTok && (i & 15) < __shfl_sync(full, live, sl);
-          ksv[e] = there ? a.c.ks[pg * a.c.ks_page + row] : 0.0f;
-          vsv[e] = there ? a.c.vs[pg * a.c.vs_page + row] : 0.0f;
+            for (int x = 0; x < D / 64; ++x) tma_4d(to + x * 16384 + lane * a.box * 128, n & 1 ? &map_v : &map_k, 64 * x, sl.place, head, sl.page, bar);
+          }
         }
       };
       if constexpr (Q8) {
-        // raw tiles kRaw items ahead; a thread converts the chunks that it has copied itself
-        float ksv[2] = {0.0f, 0.0f}, vsv[2] = {0.0f, 0.0f};  // of the newest step asked for
+        float ksv[2] = {0.0f, 0.0f}, vsv[2] = {0.0f, 0.0f};  // the scales of tokens lt and lt + kLoaders of the newest step asked for
+        int asked = 0;
         auto ask = [&](int n) {  // item n of the piece
-          if (n < 2 * nt) {
-            if (!(n & 1)) {
-              find(n >> 1);
-              step_info(ksv, vsv);
+          if (n >= 2 * nt) return;
+          const int item = items + n, buf = item % kRing;
+          if (!(n & 1)) {
+            find(n >> 1);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int i = lt + kLoaders * e;
+              const Slice& sl = sh_slice[lw][n >> 1 & 1][(i / 16) & 7];
+              const long long row = static_cast<long long>(head) * a.c.page_size + sl.place + (i & 15);
+              const bool there = i < kTok && (i & 15) < sl.live;
+              ksv[e] = there ? a.c.ks[sl.page * a.c.ks_page + row] : 0.0f;
+              vsv[e] = there ? a.c.vs[sl.page * a.c.vs_page + row] : 0.0f;
             }
-            const uint32_t raw_at = base + S::kRawAt + (n % S::kRaw) * kTok * RB;
-            copy(n & 1, [&](int i, int, int) { return raw_at + i * 16; });
-          } else {
-            copy_commit();
+          }
+          if (lw == 0) {
+            ok = __all_sync(full, ok && (item < kRing || wait(b_free + buf, (item / kRing - 1) & 1))) != 0;
+            if (ok) {
+              copy(n, b_raw + buf, base + S::kRawAt + buf * kTok * RB);
+              asked = n + 1;
+            }
           }
         };
         ask(0);
         ask(1);
+        int n = 0;
 #pragma unroll 1
-        for (int n = 0; n < 2 * nt; ++n) {
+        for (; n < 2 * nt; ++n) {
           const int item = items + n, buf = item % kRing, j = n >> 1;
-          if (!(n & 1)) {
+          ok = ok && (item < kRing || wait(b_empty + buf, (item / kRing - 1) & 1));
+          if (ok && !(n & 1)) {
             // what goes with the step (asked for with item 2 j, the newest still): its place is free, by the buffer that K waits for
-            ok = ok && (item < kRing || wait(b_empty + buf, (item / kRing - 1) & 1));
-            if (ok) {
-              const int slot = (steps + j) % kInfo;
-              float* info = reinterpret_cast<float*>(sm + S::kInfoAt) + slot * 3 * kTok;
-              if (lt == 0) sh_valid[slot] = 0xffu & ~missing;
+            const int slot = (steps + j) % kInfo;
+            float* info = reinterpret_cast<float*>(sm + S::kInfoAt) + slot * 3 * kTok;
+            if (lt == 0) sh_valid[slot] = 0xffu & ~missing;
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int i = lt + kLoaders * e;
-                if (i < kTok) {
-                  const float y = vsv[e] < 7.7037197775489434e-34f ? 7.7037197775489434e-34f : vsv[e];  // 2^-110: a scale of 0 stands for zeros all the same
-                  info[i] = ksv[e];
-                  info[kTok + i] = __log2f(y);
-                  info[2 * kTok + i] = __frcp_rn(y) * kShift8;
-                }
+            for (int e = 0; e < 2; ++e) {
+              const int i = lt + kLoaders * e;
+              if (i < kTok) {
+                const float y = vsv[e] < 7.7037197775489434e-34f ? 7.7037197775489434e-34f : vsv[e];  // 2^-110: a scale of 0 stands for zeros all the same
+                info[i] = ksv[e];
+                info[kTok + i] = __log2f(y);
+                info[2 * kTok + i] = y == y ? __frcp_rn(y) * kShift8 : 0.0f;  // (a weight is NaN as it is, or 0 where the token is not seen)
               }
-              mbar_arrive(b_info + slot);
             }
-          } else {
-            ok = ok && (item < kRing || wait(b_empty + buf, (item / kRing - 1) & 1));
+            mbar_arrive(b_info + slot);
           }
-          ok = __all_sync(full, ok) != 0;
-          if (!ok) break;
           ask(n + 2);
-          copy_wait<2>();
-          const uint32_t raw_at = base + S::kRawAt + (n % S::kRaw) * kTok * RB;
-          uint8_t* to = sm + S::kRingAt + buf * S::kTile;
-#pragma unroll 2
-          for (int i = lt; i < CHUNKS; i += kLoaders) {
-            const int r = i / NC, ch = i % NC;
+          ok = __all_sync(full, ok && wait(b_raw + buf, (item / kRing) & 1)) != 0;
+          if (!ok) break;
+          const uint32_t raw_at = base + S::kRawAt + buf * kTok * RB + ch * 16;
+          uint8_t* const half = sm + S::kRingAt + buf * S::kTile + (ch / 4) * 16384;
+          const Slice* slices = sh_slice[lw][j & 1];
+#pragma unroll
+          for (int x = 0; x < STEPS; ++x) {
+            const int r = r0 + R * x;
+            if (r >= kTok) break;
             uint32_t c4[4], h[8];
-            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(c4[0]), "=r"(c4[1]), "=r"(c4[2]), "=r"(c4[3]) : "r"(raw_at + i * 16) : "memory");
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(c4[0]), "=r"(c4[1]), "=r"(c4[2]), "=r"(c4[3]) : "r"(raw_at + r * RB));
+            const bool there = r % 16 < slices[r / 16].live;  // what lies behind may be anything
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const uint32_t y = S::FMT == RSSM_I8 ? c4[e] ^ 0x80808080u : c4[e];
+              const uint32_t y = !there ? S::FMT == RSSM_I8 ? 0x80808080u : 0u : S::FMT == RSSM_I8 ? c4[e] ^ 0x80808080u : c4[e];
               h[2 * e] = codes_f16<S::FMT>(y, 0x4140u, 0x4410u);
               h[2 * e + 1] = codes_f16<S::FMT>(y, 0x4342u, 0x4432u);
             }
-            uint8_t* p = to + (ch / 4) * 16384;
-            *reinterpret_cast<uint4*>(p + sw(r, (2 * ch) % 8)) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(p + sw(r, (2 * ch + 1) % 8)) = make_uint4(h[4], h[5], h[6], h[7]);
+            *reinterpret_cast<uint4*>(half + sw(r, (2 * ch) % 8)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(half + sw(r, (2 * ch + 1) % 8)) = make_uint4(h[4], h[5], h[6], h[7]);
           }
           fence_async();
-          mbar_arrive(b_full + buf);
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(b_full + buf);
+            mbar_arrive(b_free + buf);
+          }
         }
+        if (!ok && lw == 0)  // no copy is in flight at the end
+          for (; n < asked; ++n) mbar_wait(b_raw + (items + n) % kRing, ((items + n) / kRing) & 1);
       } else {
-        int pending = -1;  // an item whose copies are on their way
-        bool pending_odd = false;
-        // this thread's copies have landed: its values are looked at where not every query sees them, then the buffer is announced
-        auto announce = [&]() {
-          if (pending < 0) return;
-          const int buf = pending % kRing;
-          if (pending_odd) {
-            uint8_t* p = sm + S::kRingAt + buf * S::kTile;
-            for (int i = lt; i < CHUNKS; i += kLoaders) {
-              uint4* q = reinterpret_cast<uint4*>(p + (i % NC / 8) * 16384 + sw(i / NC, i % NC % 8));
-              uint4 y = *q;
-              if (take_out_odd(y)) {
-                *q = y;
-                sh_odd = 1;
-              }
-            }
-          }
-          fence_async();
-          mbar_arrive(b_full + buf);
-          pending = -1;
-        };
+        int n = 0;
 #pragma unroll 1
-        for (int n = 0; n < 2 * nt; ++n) {
+        for (; n < 2 * nt; ++n) {
           const int item = items + n, buf = item % kRing, j = n >> 1;
           if (!(n & 1)) find(j);
-          if (item >= kRing && !mbar_try_wait(b_empty + buf, (item / kRing - 1) & 1)) {
-            copy_wait<0>();
-            announce();
-            ok = ok && wait(b_empty + buf, (item / kRing - 1) & 1);
-          }
-          ok = __all_sync(full, ok) != 0;
+          ok = __all_sync(full, ok && (item < kRing || wait(b_empty + buf, (item / kRing - 1) & 1))) != 0;
           if (!ok) break;
           if (!(n & 1)) {
             const int slot = (steps + j) % kInfo;
@@ -558,18 +573,35 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
             mbar_arrive(b_info + slot);
           }
           const uint32_t to = base + S::kRingAt + buf * S::kTile;
-          copy(n & 1, [&](int, int r, int ch) { return to + (ch / 8) * 16384 + sw(r, ch % 8); });
-          if (pending >= 0) {
-            copy_wait<1>();
-            announce();
+          // values that not every query sees are looked at before the product gets them, and what lies behind the last is zero
+          const bool fix = (n & 1) && (static_cast<long long>(t0 + j + 1) * kTok > some || missing);
+          if (lw == 0) copy(n, fix ? b_raw : b_full + buf, to);
+          if (fix) {
+            ok = __all_sync(full, ok && wait(b_raw, fixed & 1)) != 0;
+            ++fixed;
+            if (!ok) break;
+            uint8_t* p = sm + S::kRingAt + buf * S::kTile + (ch / 8) * 16384;
+            const Slice* slices = sh_slice[lw][j & 1];
+            for (int r = r0; r < kTok; r += R) {
+              uint4* q = reinterpret_cast<uint4*>(p + sw(r, ch % 8));
+              if (r % 16 >= slices[r / 16].live) {
+                *q = make_uint4(0u, 0u, 0u, 0u);
+                continue;
+              }
+              uint4 y = *q;
+              if (take_out_odd(y)) {
+                *q = y;
+                sh_odd = pieces + 1;
+              }
+            }
+            fence_async();
+            __syncwarp();
           }
-          pending = item;
-          pending_odd = (n & 1) && static_cast<long long>(t0 + j + 1) * kTok > some;
+          if (lane == 0 && (fix || lw != 0)) mbar_arrive(b_full + buf);
         }
-        copy_wait<0>();
-        announce();
+        if (!ok && lw == 0)  // no copy is in flight at the end
+          for (int i = max(0, n - kRing); i < n; ++i) mbar_wait(b_full + (items + i) % kRing, ((items + i) / kRing) & 1);
       }
-      copy_wait<0>();
     } else if (lane == 0) {
       // ---- products
       constexpr uint32_t kind = Q8 ? (1u << 7) | (1u << 10) : 0u;  // fp16 operands: without bf16's bits
@@ -593,6 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
         ok = ok && wait(b_full + item % kRing, (item / kRing) & 1);
         return item % kRing;
       };
+      ok = ok && wait(b_q, pieces & 1);
       if (alt) {
         for (int j = 0; ok && j < min(nt, 2); ++j) {
           const int buf = filled(2 * j);
@@ -604,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
 #pragma unroll 1
         for (int j = 0; ok && j < nt; ++j) {
           const int x = j & 1, bv = filled(2 * j + 1);
-          ok = ok && wait(b_p + x, (used[x] + j / 2) & 1);
+          ok = ok && wait(b_p + x, ((x ? used1 : used0) + j / 2) & 1);
           if (!ok) break;
           tc_after();
           sums(x, bv, j > 1);
@@ -620,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
           }
         }
       } else {
-        if (nt > 0) {
+        if (ok && nt > 0) {
           const int buf = filled(0);
           if (ok) {
             tc_after();
@@ -633,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
           const bool more = j + 1 < nt;
           const int bv = filled(2 * j + 1), bk = more ? filled(2 * j + 2) : 0;
           for (int x = 0; x < kTiles; ++x) {
-            ok = ok && wait(b_p + x, (used[x] + j) & 1);
+            ok = ok && wait(b_p + x, ((x ? used1 : used0) + j) & 1);
             if (!ok) break;
             tc_after();
             sums(x, bv, j > 0);
@@ -651,100 +684,121 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
     if (!ok) break;
     items += 2 * nt;
     steps += nt;
-#pragma unroll
-    for (int x = 0; x < kTiles; ++x) {
-      const int n = alt ? (nt - x + 1) / 2 : nt;
-      used[x] += n;
-      done[x] += n > 0;
-    }
-    if (alt && nt > 1) {
-      // ---- the second tile's sums are the same queries'
-      float* const other = reinterpret_cast<float*>(sm + S::kRingAt);  // [dimension][query]
-      __shared__ float sh_ref[kQ], sh_sum[kQ];
-      if (warp < kSoftWarps && warp >= 4) {
-        const int r = tid - kQ;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          uint32_t x[16];
-          tc_ld16(x, tm + kTiles * kTok + D + ((warp & 3) << 21) + c);
-          tc_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(x[i]));
-#pragma unroll
-          for (int i = 0; i < 16; ++i) other[(c + i) * kQ + r] = __uint_as_float(x[i]);
-        }
-        sh_ref[r] = ref;
-        sh_sum[r] = sum;
-        tc_before();
-      }
-      __syncthreads();
-      if (warp < 4) {
-        const float now = fmaxf(ref, sh_ref[tid]), at0 = now == -INFINITY ? 0.0f : now;
-        join0 = exp2_fast(ref - at0);
-        join1 = exp2_fast(sh_ref[tid] - at0);
-        sum = sum * join0 + sh_sum[tid] * join1;
-        ref = now;
-      }
-    }
+    ++pieces;
+    used0 += alt ? (nt + 1) / 2 : nt;
+    used1 += alt ? nt / 2 : nt;
+    done0 += nt > 0;
+    done1 += nt > (alt ? 1 : 0);
 
     // ---- the queries' sums
     const bool whole = t0 == 0 && t1 == w.tiles;
     constexpr float kUnit = Q8 ? kShift8 : 1.0f;
-    if (warp < kSoftWarps && (warp >> 2) < nq) {
-      const int r = tid, tile = warp >> 2, t = (row0 + min(r, rows - 1)) / a.group;
-      float* const left = piece_place<kRows, D>(a, blockIdx.x, t0 == 0);
-      const float inv = sum == 0.0f ? 0.0f : kUnit / sum;
+    if (warp < kSoftWarps) {
+      const int tile = warp >> 2;
+      const uint32_t o_at = tm + kTiles * kTok + tile * D + ((warp & 3) << 21);
+      const bool both = alt && nt > 1;
+      float* const other = reinterpret_cast<float*>(sm + S::kRingAt);  // [dimension][query]
+      if (both) {
+        // the second tile's sums are the same queries'
+        if (tile == 1) {
+          const int r = tid - kQ;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t x[32];
-        if (nt > 0) {
-          tc_ld32(x, tm + kTiles * kTok + tile * D + ((warp & 3) << 21) + 32 * c);
-          landed(x);
-          if (alt && nt > 1) {
-            const float* other = reinterpret_cast<const float*>(sm + S::kRingAt) + 32 * c * kQ + r;
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t x[32];
+            tc_ld32(x, o_at + 32 * c);
+            landed(x);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * join0 + other[i * kQ] * join1);
+            for (int i = 0; i < 32; ++i) other[(32 * c + i) * kQ + r] = __uint_as_float(x[i]);
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = 0u;
+          sh_ref[r] = ref;
+          sh_sum[r] = sum;
         }
-        if (r < rows) {
+        soft_sync();
+        if (tile == 0) {
+          const float now = fmaxf(ref, sh_ref[tid]), at0 = now == -INFINITY ? 0.0f : now;
+          join0 = exp2_fast(ref - at0);
+          join1 = exp2_fast(sh_ref[tid] - at0);
+          sum = sum * join0 + sh_sum[tid] * join1;
+          ref = now;
+        }
+      }
+      if (tile == 0 || !alt) {
+        const int r = tid;
+        float* const left = piece_place<kRows, D>(a, blockIdx.x, t0 == 0);
+        const float inv = sum == 0.0f ? 0.0f : kUnit / sum;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t x[32];
+          if (nt > 0) {
+            tc_ld32(x, o_at + 32 * c);
+            landed(x);
+            if (both) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            float y0[4] = {__uint_as_float(x[i]), __uint_as_float(x[i + 1]), __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])};
-            float y1[4] = {__uint_as_float(x[i + 4]), __uint_as_float(x[i + 5]), __uint_as_float(x[i + 6]), __uint_as_float(x[i + 7])};
+              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * join0 + other[(32 * c + i) * kQ + r] * join1);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = 0u;
+          }
+          if (r < rows) {
             if constexpr (!Q8) {
-              if (sh_odd) {
+              if (sh_odd == pieces) {
                 const long long from = max(static_cast<long long>(t0) * kTok, some / kTok * kTok), to = min(static_cast<long long>(t1) * kTok, end);
-                const unsigned long long path = a.parents ? sh_mask[t & 63] : 0ull;
-                add_odd(a, w, table, vbase, RB, from, to, t, path, 32 * c + i, y0);
-                add_odd(a, w, table, vbase, RB, from, to, t, path, 32 * c + i + 4, y1);
+#pragma unroll 1
+                for (int i = 0; i < 32; i += 4) {
+                  float y[4];
+#pragma unroll
+                  for (int k = 0; k < 32; k += 4)
+                    if (k == i)
+#pragma unroll
+                      for (int e = 0; e < 4; ++e) y[e] = __uint_as_float(x[k + e]);
+                  add_odd(a, w, table, vbase, RB, from, to, t, path, 32 * c + i, y);
+#pragma unroll
+                  for (int k = 0; k < 32; k += 4)
+                    if (k == i)
+#pragma unroll
+                      for (int e = 0; e < 4; ++e) x[k + e] = __float_as_uint(y[e]);
+                }
               }
             }
             if (whole) {
-              const int h = head * a.group + (row0 + r) - t * a.group;
-              *reinterpret_cast<uint4*>(a.out + (w.s.first + t) * a.out_stride + static_cast<long long>(h) * D + 32 * c + i) =
-                  make_uint4(pack_bf16(y0[0] * inv, y0[1] * inv), pack_bf16(y0[2] * inv, y0[3] * inv), pack_bf16(y1[0] * inv, y1[1] * inv),
-                             pack_bf16(y1[2] * inv, y1[3] * inv));
+              // bf16, in the place of the tile's queries: rows leave from there side by side
+              uint8_t* const q = sm + tile * S::kTile + (c / 2) * 16384;
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) {
+                uint32_t y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = bf16_pair(__uint_as_float(x[i + 2 * e]) * inv, __uint_as_float(x[i + 2 * e + 1]) * inv);
+                *reinterpret_cast<uint4*>(q + sw(r % kQ, (c & 1) * 4 + i / 8)) = make_uint4(y[0], y[1], y[2], y[3]);
+              }
             } else {
-              __stcg(reinterpret_cast<float4*>(left + r * D + 32 * c + i), make_float4(y0[0], y0[1], y0[2], y0[3]));
-              __stcg(reinterpret_cast<float4*>(left + r * D + 32 * c + i + 4), make_float4(y1[0], y1[1], y1[2], y1[3]));
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                __stcg(reinterpret_cast<uint4*>(left + r * D + 32 * c + i), make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]));
             }
           }
+          __syncwarp();  // the next load is the whole warp's
         }
-        __syncwarp();  // the next load is the whole warp's
-      }
-      if (!whole && r < rows) {
-        __stcg(left + kRows * D + r, ref);
-        __stcg(left + kRows * D + kRows + r, sum);
+        if (!whole && r < rows) {
+          __stcg(left + kRows * D + r, ref);
+          __stcg(left + kRows * D + kRows + r, sum);
+        }
       }
       tc_before();
+      if (whole) {
+        soft_sync();
+        constexpr int G = D / 8;
+        for (int i = tid; i < rows * G; i += kSoft) {
+          const int r = i / G, ch = i % G, tq = (row0 + r) / a.group, h = head * a.group + (row0 + r) - tq * a.group;
+          *reinterpret_cast<uint4*>(a.out + (w.s.first + tq) * a.out_stride + static_cast<long long>(h) * D + ch * 8) =
+              *reinterpret_cast<const uint4*>(sm + (r / kQ) * S::kTile + (ch / 8) * 16384 + sw(r % kQ, ch % 8));
+        }
+      }
     }
     if (!whole) join_pieces<kRows, D, kThreads>(a, w, head, row0, rows, seg0, line.share, kUnit);
   }
   // a wait that gave up: what was started ends before the memory is given back
-  if (!ok && warp == kSoftWarps + kLoadWarps && lane == 0) {
+  if (!ok && warp == kMmaWarp && lane == 0) {
     mbar_init(b_info, 1);
     fence_barrier_init();
     tc_commit(b_info);
@@ -753,8 +807,21 @@ __global__ void __launch_bounds__(kThreads, 1) wide_kernel(const AttnArgs a) {
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == kSoftWarps + kLoadWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(kTmem) : "memory");
+  if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(kTmem) : "memory");
   if (tid == 0 && dead) set_error(a.c.err, RSSM_ERRBIT_TIMEOUT);
+}
+
+// a layer's keys or values as [page][head][place][dimension], boxes of 64 dimensions of `box` tokens
+bool page_map(const KvView& c, bool values, int box, CUtensorMap* map) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(c.dim) * 2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.dim), static_cast<cuuint64_t>(c.page_size), static_cast<cuuint64_t>(c.heads),
+                              static_cast<cuuint64_t>(c.pages)};
+  const cuuint64_t strides[3] = {row, row * c.page_size, static_cast<cuuint64_t>(values ? c.v_page : c.k_page)};
+  const cuuint32_t shape[4] = {64, static_cast<cuuint32_t>(box), 1, 1}, one[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, values ? c.v : c.k, dims, strides, shape, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D, int FMT>
@@ -769,7 +836,9 @@ cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev] = true;
   }
-  return launch_pdl(wide_kernel<S>, dim3(grid), dim3(kThreads), S::kSmem, st, a);
+  CUtensorMap k = {}, v = {};
+  if (!S::Q8 && (!page_map(a.c, false, a.box, &k) || !page_map(a.c, true, a.box, &v))) return cudaErrorInvalidValue;
+  return launch_pdl(wide_kernel<S>, dim3(grid), dim3(S::kThreads), S::kSmem, st, a, k, v);
 }
 template <int D>
 cudaError_t launch_format(const AttnArgs& a, int grid, cudaStream_t st) {
@@ -787,6 +856,8 @@ cudaError_t run_wide(const AttnArgs& args, int sms, cudaStream_t st) {
   AttnArgs a = args;
   const int64_t mtiles = (static_cast<int64_t>(a.r.T) * a.group + kRows - 1) / kRows, segments = mtiles * a.r.batch * a.c.heads;
   a.whole = segments >= 2 * sms && segments < (1ll << 30);
+  a.box = 16;  // tokens that neighbour in a page, and in a step
+  while (a.box < kTok && a.c.page_size % (2 * a.box) == 0) a.box *= 2;
   const int grid = a.whole ? static_cast<int>(segments) : sms;
   return a.c.dim == 64 ? launch_format<64>(a, grid, st) : launch_format<128>(a, grid, st);
 }
