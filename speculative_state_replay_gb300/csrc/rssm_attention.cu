@@ -89,7 +89,7 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int ch) {
 }
 
 template <typename S>
-__global__ void __launch_bounds__(kThreads, kBlocks) attention_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, kBlocks) attention_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int D = S::D, MT = S::MT, kRows = S::kRows, NL = S::NL, RB = S::RB, NC = S::NC, QS = S::QS, OS = S::OS;
   constexpr bool Q8 = S::Q8;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -105,6 +105,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attention_kernel(const Attn
   pdl_trigger();
 
   const Line line = cut_line<kRows, kTile, kThreads>(a);
+  __shared__ Joint sh_joint[2];
+  int joints = 0;
+  constexpr float kUnit = Q8 ? kShift8 : 1.0f;
   int b = line.b;
   long long base = line.base;
 #pragma unroll 1
@@ -260,9 +263,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attention_kernel(const Attn
           for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const uint32_t y = S::FMT == RSSM_I8 ? kw[n][j] ^ 0x80808080u : kw[n][j];
-              bf[n][j][0] = codes_f16<S::FMT>(y, 0x4140u, 0x4410u);
-              bf[n][j][1] = codes_f16<S::FMT>(y, 0x4342u, 0x4432u);
+              codes_f16<S::FMT>(S::FMT == RSSM_I8 ? kw[n][j] ^ 0x80808080u : kw[n][j], bf[n][j][0], bf[n][j][1]);
             }
 #pragma unroll
           for (int x = 0; x < MT; ++x) {
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attention_kernel(const Attn
             y = y < 7.7037197775489434e-34f ? 7.7037197775489434e-34f : y;  // 2^-110: a scale of 0 stands for zeros all the same
             kf[n][e] = x;
             lv[n][e] = __log2f(y);
-            iv[n][e] = y == y ? __frcp_rn(y) * kShift8 : 0.0f;  // a sum of 2^110 2^14 would pass fp32's range; NaN: the weight is that, or 0 if not seen
+            iv[n][e] = y == y ? rcp_fast(y) * kShift8 : 0.0f;  // a sum of 2^110 2^14 would pass fp32's range; NaN: the weight is that, or 0 if not seen
           }
       }
       uint32_t pa[MT][4];
@@ -393,9 +394,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attention_kernel(const Attn
         if constexpr (Q8) {
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            const uint32_t f0 = S::FMT == RSSM_I8 ? f[2 * z] ^ 0x80808080u : f[2 * z], f1 = S::FMT == RSSM_I8 ? f[2 * z + 1] ^ 0x80808080u : f[2 * z + 1];
-            const uint32_t e0 = codes_f16<S::FMT>(f0, 0x4240u, 0x4420u), e1 = codes_f16<S::FMT>(f1, 0x4240u, 0x4420u);
-            const uint32_t d0 = codes_f16<S::FMT>(f0, 0x4341u, 0x4431u), d1 = codes_f16<S::FMT>(f1, 0x4341u, 0x4431u);
+            uint32_t e0, e1, d0, d1;  // even and odd dimensions: bytes 0 and 2, 1 and 3
+            codes_f16<S::FMT>(__byte_perm(f[2 * z], 0u, 0x3120u) ^ (S::FMT == RSSM_I8 ? 0x80808080u : 0u), e0, d0);
+            codes_f16<S::FMT>(__byte_perm(f[2 * z + 1], 0u, 0x3120u) ^ (S::FMT == RSSM_I8 ? 0x80808080u : 0u), e1, d1);
 #pragma unroll
             for (int x = 0; x < MT; ++x) {
               mma<true>(o[x][4 * y + 2 * z], pa[x][0], pa[x][1], pa[x][2], pa[x][3], e0, e1);
@@ -448,7 +449,6 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attention_kernel(const Attn
     __syncthreads();
     const bool whole = t0 == 0 && t1 == w.tiles;
     float* const left = piece_place<kRows, D>(a, blockIdx.x, t0 == 0);
-    constexpr float kUnit = Q8 ? kShift8 : 1.0f;
     constexpr int D4 = D / 4;
 #pragma unroll 1
     for (int i = threadIdx.x; i < rows * D4; i += kThreads) {
@@ -471,12 +471,13 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attention_kernel(const Attn
       if constexpr (!Q8) {
         if (sh_odd) {
           const int t = (row0 + r) / a.group;
-          add_odd(a, w, table, vbase, RB, max(static_cast<long long>(t0) * kTile, some / kSlice * kSlice), min(static_cast<long long>(t1) * kTile, end), t,
-                  a.parents ? sh_mask[t] : 0ull, x4, y);
+          const float4 z4 = add_odd4(a, w.len, table, vbase, RB, max(static_cast<long long>(t0) * kTile, some / kSlice * kSlice),
+                                     min(static_cast<long long>(t1) * kTile, end), t, a.parents ? sh_mask[t] : 0ull, x4, make_float4(y[0], y[1], y[2], y[3]));
+          y[0] = z4.x, y[1] = z4.y, y[2] = z4.z, y[3] = z4.w;
         }
       }
       if (whole) {
-        write_out(a, w, head, row0 + r, D, x4, y, z == 0.0f ? 0.0f : kUnit / z);
+        write_out(a, w.s.first, head, row0 + r, D, x4, y, z == 0.0f ? 0.0f : kUnit / z);
       } else {
         __stcg(reinterpret_cast<float4*>(left + r * D + x4), make_float4(y[0], y[1], y[2], y[3]));
         if (x4 == 0) {
@@ -487,8 +488,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attention_kernel(const Attn
     }
     if (whole) continue;
 
-    join_pieces<kRows, D, kThreads>(a, w, head, row0, rows, seg0, line.share, kUnit);
+    if (threadIdx.x == 0) sh_joint[joints & 1] = Joint{w.s.first, seg0, w.tiles, head, row0, rows};
+    ++joints;
   }
+  __syncthreads();
+  for (int i = 0; i < joints; ++i) join_pieces<kRows, D, kThreads, 8>(a, sh_joint[i], line.share, kUnit);
 }
 
 template <typename S>

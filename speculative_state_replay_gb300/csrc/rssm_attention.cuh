@@ -33,6 +33,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -43,19 +48,20 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Two codes (the bytes of a 16-bit half of w that `sel` picks) as two fp16 values, exactly.
-// int8: with the sign bit turned, code + 128 under the exponent of 1024 is 1152 + code.
+// The four codes of w (int8: with their sign bits turned) as two pairs of fp16 values, exactly: bytes 0 and 1, 2 and 3.
+// int8: code + 128 under the exponent of 1024 is 1152 + code.
 template <int FMT>
-__device__ __forceinline__ uint32_t codes_f16(uint32_t w, uint32_t sel_i8, uint32_t sel_e4m3) {
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if constexpr (FMT == RSSM_I8) {
-    const uint32_t h = __byte_perm(w, 0x64646464u, sel_i8);
-    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&h), __float2half2_rn(1152.0f));
-    return *reinterpret_cast<const uint32_t*>(&y);
+    const uint32_t l = __byte_perm(w, 0x64646464u, 0x4140u), h = __byte_perm(w, 0x64646464u, 0x4342u);
+    const __half2 off = __float2half2_rn(1152.0f), y = __hsub2(*reinterpret_cast<const __half2*>(&l), off),
+                  z = __hsub2(*reinterpret_cast<const __half2*>(&h), off);
+    lo = *reinterpret_cast<const uint32_t*>(&y);
+    hi = *reinterpret_cast<const uint32_t*>(&z);
   } else {
-    const uint32_t h = __byte_perm(w, 0u, sel_e4m3);
-    uint32_t y;
-    asm("{\n\t.reg .b16 x, z;\n\tmov.b32 {x, z}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(y) : "r"(h));
-    return y;
+    asm("{\n\t.reg .b16 x, z;\n\tmov.b32 {x, z}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, z;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
   }
 }
 
@@ -121,8 +127,8 @@ __device__ __forceinline__ RowWork row_work(const AttnArgs& a, int b) {
   w.tiles = 1;
   w.mtiles = static_cast<int>((static_cast<long long>(w.s.count) * a.group + kRows - 1) / kRows);
   if (w.len >= 0) {
-    const long long end = static_cast<long long>(w.len) + w.s.count;
-    if (end > static_cast<long long>(a.r.max_pages) * a.c.page_size) w.len = -2;
+    const long long end = static_cast<long long>(w.len) + w.s.count;  // (positions are 31 bits from here on)
+    if (end > min(static_cast<long long>(a.r.max_pages) * a.c.page_size, 0x7fffff00ll)) w.len = -2;
     else w.tiles = static_cast<int>((end + kTile - 1) / kTile);
   }
   return w;
@@ -190,10 +196,11 @@ __device__ __forceinline__ Line cut_line(const AttnArgs& a) {
 // What values that are not finite add to four columns from x4 on of the query at new token t: the kernels take
 // them out of the products from position `from` on, where tokens are that not every query sees, since they must not
 // meet the weight 0 of one that does not.
-__device__ __forceinline__ void add_odd(const AttnArgs& a, const RowWork& w, const int* table, const uint8_t* vbase, int row_bytes, long long from,
-                                        long long to, int t, unsigned long long path, int x4, float (&y)[4]) {
+static __device__ __noinline__ float4 add_odd4(const AttnArgs& a, int len, const int* table, const uint8_t* vbase, int row_bytes, long long from,
+                                             long long to, int t, unsigned long long path, int x4, float4 y4) {
+  float y[4] = {y4.x, y4.y, y4.z, y4.w};
   for (long long p = from; p < to; ++p) {
-    const long long j = p - w.len;
+    const long long j = p - len;
     if (j >= 0 && !(a.parents ? path >> (j & 63) & 1 : j <= t)) continue;
     const unsigned pos = static_cast<unsigned>(p), page = pos / static_cast<unsigned>(a.c.page_size);
     const int pg = table[page];
@@ -204,11 +211,12 @@ __device__ __forceinline__ void add_odd(const AttnArgs& a, const RowWork& w, con
     for (int e = 0; e < 4; ++e)
       if (!isfinite(f[e])) y[e] += f[e];
   }
+  return make_float4(y[0], y[1], y[2], y[3]);
 }
 
-__device__ __forceinline__ void write_out(const AttnArgs& a, const RowWork& w, int head, int query, int D, int x4, const float (&y)[4], float inv) {
+__device__ __forceinline__ void write_out(const AttnArgs& a, long long first, int head, int query, int D, int x4, const float (&y)[4], float inv) {
   const int t = query / a.group, h = head * a.group + query - t * a.group;
-  *reinterpret_cast<uint2*>(a.out + (w.s.first + t) * a.out_stride + static_cast<long long>(h) * D + x4) =
+  *reinterpret_cast<uint2*>(a.out + (first + t) * a.out_stride + static_cast<long long>(h) * D + x4) =
       make_uint2(bf16_pair(y[0] * inv, y[1] * inv), bf16_pair(y[2] * inv, y[3] * inv));
 }
 
@@ -219,10 +227,17 @@ template <int kRows, int D>
 __device__ __forceinline__ float* piece_place(const AttnArgs& a, int block, bool begins) {
   return a.partial + (static_cast<long long>(block) * 2 + begins) * (kRows * (D + 2));
 }
-template <int kRows, int D, int kThreads>
-__device__ __forceinline__ void join_pieces(const AttnArgs& a, const RowWork& w, int head, int row0, int rows, long long seg0, long long share, float unit) {
+struct Joint {  // a segment that a block has a piece of
+  long long first_token, seg0;  // its row's first new token, its first unit
+  int tiles, head, row0, rows;
+};
+// (after all of a block's pieces: in their loop it would take registers from it)
+template <int kRows, int D, int kThreads, int kDeep>
+__device__ __forceinline__ void join_pieces(const AttnArgs& a, const Joint& j, long long share, float unit) {
+  const long long first_token = j.first_token, seg0 = j.seg0;
+  const int tiles = j.tiles, head = j.head, row0 = j.row0, rows = j.rows;
   __shared__ int last;
-  const int first = static_cast<int>(seg0 / share), pieces = static_cast<int>((seg0 + w.tiles - 1) / share) - first + 1;
+  const int first = static_cast<int>(seg0 / share), pieces = static_cast<int>((seg0 + tiles - 1) / share) - first + 1;
   __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -246,27 +261,27 @@ __device__ __forceinline__ void join_pieces(const AttnArgs& a, const RowWork& w,
       z = z * f + l * g;
     }
   };
-  auto write = [&](const Sum& s, int r, int x4) { write_out(a, w, head, row0 + r, D, x4, s.y, s.z == 0.0f ? 0.0f : unit / s.z); };
+  auto write = [&](const Sum& s, int r, int x4) { write_out(a, first_token, head, row0 + r, D, x4, s.y, s.z == 0.0f ? 0.0f : unit / s.z); };
   auto load = [&](const float* p, int r, int x4, float4& v, float& m, float& l) {
     m = __ldcg(p + kRows * D + r);
     l = __ldcg(p + kRows * D + kRows + r);
     v = __ldcg(reinterpret_cast<const float4*>(p + r * D + x4));
   };
-  // loads on their way at a time: of eight pieces where a thread has one output or two, else of four outputs
+  // loads on their way at a time: of kDeep pieces where a thread has one output or two, else of four outputs
   if (rows * D4 <= 2 * kThreads) {
 #pragma unroll 1
     for (int i = threadIdx.x; i < rows * D4; i += kThreads) {
       const int r = i / D4, x4 = (i - r * D4) * 4;
       Sum s;
 #pragma unroll 1
-      for (int x0 = 0; x0 < pieces; x0 += 8) {
-        float4 v[8];
-        float m[8], l[8];
+      for (int x0 = 0; x0 < pieces; x0 += kDeep) {
+        float4 v[kDeep];
+        float m[kDeep], l[kDeep];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < kDeep; ++e)
           if (x0 + e < pieces) load(piece_place<kRows, D>(a, first + x0 + e, x0 + e == 0), r, x4, v[e], m[e], l[e]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < kDeep; ++e)
           if (x0 + e < pieces) s.add(v[e], m[e], l[e]);
       }
       write(s, r, x4);

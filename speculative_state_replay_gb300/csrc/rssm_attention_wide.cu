@@ -3,7 +3,7 @@
 //
 // With 256 queries over the same tokens the products are what bounds it, and they are
 // tcgen05's: of two tiles of 128 queries, S = Q K' of 128 tokens into tensor memory,
-// the softmax in registers, a query a thread, its weights P back into tensor memory in
+// the softmax in registers, a query for two threads, its weights P back into tensor memory in
 // S's place, O += P V with O in tensor memory throughout.  Keys and values come in
 // turn through a ring of shared-memory buffers, 8-bit codes as fp16, exactly.  The two
 // tiles alternate: while one's scores are turned into weights the products of the other
@@ -26,8 +26,6 @@ constexpr int kQ = 128;                 // queries of a tile: the product's rows
 constexpr int kTiles = 2;               // tiles of a block
 constexpr int kRows = kTiles * kQ;
 constexpr int kTok = 128;               // tokens of a step
-constexpr int kSoftWarps = 4 * kTiles;  // a thread has a query
-constexpr int kSoft = kSoftWarps * 32;
 constexpr int kInfo = 4;                // places of what goes with a step of tokens: K of step j + 4 waits for a buffer that is
                                         // free once the scores of j + 2 are made, which is after the weights of j
 constexpr float kLazy = 4.0f;           // log2 of how far the true maximum may be past the one in use
@@ -37,22 +35,33 @@ constexpr int kTmem = 512;              // columns: two of S, two of O
 struct Wait {  // a wait that gives up is for all of the block
   volatile int* dead;
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (*dead) return false;
-    if (mbar_wait(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
+    for (uint32_t i = 0; i < kWaitTries; ++i) {
+      if (mbar_try_wait_for(bar, parity, 1000000u)) return true;
+      if (*dead) return false;
+    }
     *dead = 1;
     return false;
   }
 };
 
+#ifndef PB
+#define PB 2
+#define LB 3
+#define P8 2
+#define L8 3
+#endif
+constexpr int kPartsOf(int f) { return f == RSSM_BF16 ? PB : P8; }
+constexpr int kLoadsOf(int f) { return f == RSSM_BF16 ? LB : L8; }
 template <int D_, int FMT_>
 struct Shape {
   static constexpr int D = D_, FMT = FMT_;
   static constexpr bool Q8 = FMT != RSSM_BF16;
-  static constexpr int kLoadWarps = Q8 ? 7 : 3;   // bf16: one of them copies, all look at tiles that not every query sees
-  static constexpr int kLoaders = kLoadWarps * 32;
-  static constexpr int kThreads = kSoft + kLoaders + 32;
+  static constexpr int kParts = kPartsOf(FMT_);    // threads of a query, each with a part of a step's tokens
+  static constexpr int kSoftWarps = 4 * kTiles * kParts, kSoft = kSoftWarps * 32;
+  static constexpr int kLoadWarps = kLoadsOf(FMT_);  // the first copies; 8-bit: the others convert, bf16: all look at tiles that not every query sees
+  static constexpr int kWorkWarps = Q8 ? kLoadWarps - 1 : kLoadWarps, kWorkers = kWorkWarps * 32;
+  static constexpr int kThreads = kSoft + kLoadWarps * 32 + 32;
   static constexpr int RB = D * (Q8 ? 1 : 2);     // bytes of a cached head
   static constexpr int NC = RB / 16;              // and its 16-byte chunks
   static constexpr int kTile = kTok * D * 2;      // bytes of a tile as an operand: per 64 dimensions, rows of 128 bytes
@@ -77,12 +86,32 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int
                "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
                : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {  // first operand in tensor memory
+// Products and their commits by one lane of a warp that runs as a whole: what they are made of then is the warp's, not a
+// thread's, and stays in uniform registers (by one thread in a branch of its own a product took 115 cycles to issue)
+__device__ __forceinline__ void mma_ss(bool mine, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
       "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate))
+      "setp.ne.u32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(static_cast<uint32_t>(mine))
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(bool mine, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {  // first operand in tensor memory
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "setp.ne.u32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(static_cast<uint32_t>(mine))
+      : "memory");
+}
+__device__ __forceinline__ void commit(bool mine, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.u32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(static_cast<uint32_t>(mine))
       : "memory");
 }
 #define R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
@@ -95,22 +124,12 @@ __device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t addr) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tc_ld16(uint32_t (&r)[16], uint32_t addr) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-               : R8(r, 0), R8(r, 8)
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,"
-      "%26,%27,%28,%29,%30,%31};" ::S8(r, 0),
-      S8(r, 8), S8(r, 16), S8(r, 24), "r"(addr)
-      : "memory");
-}
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::S8(r, 0), S8(r, 8), "r"(addr)
                : "memory");
+}
+__device__ __forceinline__ void tc_stw8(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::S8(r, 0), "r"(addr) : "memory");
 }
 #undef R8
 #undef S8
@@ -147,48 +166,71 @@ __device__ __forceinline__ void scaled(uint32_t& x0, uint32_t& x1, pair back, pa
   x1 = __float_as_uint(y1);
 }
 
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoft) : "memory"); }
+template <int N>
+__device__ __forceinline__ void soft_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void pair_sync(int pair) { asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory"); }  // of the two warps with the same queries
+
+// A block's part of a segment: what its warps have to know, in shared memory, so that their loops have the registers.
+struct Piece {
+  long long first;                   // the row's first new token
+  int row, len, count, head;         // the row, its committed and new tokens, the head
+  int row0, rows;                    // the tile's queries
+  int t0, nt, t1, tiles;             // its steps of tokens: from t0 on nt that any query sees, of t1 - t0; of the segment's
+  int end, some;                     // the last token seen by any of its queries; from `some` on not every query sees all
+  int items, steps, used[2], done[2], number;  // how often things came round so far: the ring, steps, by tile scores and sums, pieces
+  int fixed;                         // and tiles whose values were looked at
+  bool alt, whole, fine, over;       // both tiles have the same queries, and every other step; the whole segment; the row's tree; no piece
+};
 
 template <typename S>
 __global__ void __launch_bounds__(S::kThreads, 1)
-    wide_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
-  constexpr int D = S::D, RB = S::RB, NC = S::NC, kRing = S::kRing, kThreads = S::kThreads, kLoadWarps = S::kLoadWarps, kLoaders = S::kLoaders;
+    wide_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+  constexpr int D = S::D, RB = S::RB, NC = S::NC, kRing = S::kRing, kThreads = S::kThreads, kLoadWarps = S::kLoadWarps, kWorkWarps = S::kWorkWarps,
+                kWorkers = S::kWorkers, kParts = S::kParts, kSoftWarps = S::kSoftWarps, kSoft = S::kSoft, kMmaWarp = kSoftWarps + kLoadWarps, kPart = kTok / kParts;
   constexpr bool Q8 = S::Q8;
+  constexpr float kUnit = Q8 ? kShift8 : 1.0f;
   extern __shared__ uint8_t raw[];
   uint8_t* const sm = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
   __shared__ uint32_t tmem_base;
   __shared__ volatile int dead;
   __shared__ int sh_odd;  // the last piece (counted from 1) with values that are not finite among its new tokens
-  __shared__ float sh_back[kRows], sh_ref[kQ], sh_sum[kQ];
+  __shared__ Piece sh_piece;
+  __shared__ unsigned long long sh_mask[kTreeT];
+  __shared__ float sh_back[kRows], sh_top[kTiles][kParts][kQ], sh_sum[kTiles][kParts][kQ], sh_ref[kTiles][kQ];
   __shared__ unsigned sh_valid[kInfo];
   __shared__ Slice sh_slice[kLoadWarps][2][8];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned full = 0xffffffffu;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(sm + S::kBarsAt);
   uint64_t *const b_full = bars, *const b_empty = b_full + kRing, *const b_raw = b_empty + kRing, *const b_free = b_raw + kRing,
            *const b_s = b_free + kRing, *const b_p = b_s + kTiles, *const b_o = b_p + kTiles, *const b_info = b_o + kTiles, *const b_q = b_info + kInfo;
   const uint32_t base = smem_addr(sm);
-  constexpr int kMmaWarp = kSoftWarps + kLoadWarps;
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_base)), "n"(kTmem) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  if (tid == 0) {
+  if (threadIdx.x == 0) {
     dead = sh_odd = 0;
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(b_full + i, kLoadWarps);
+      mbar_init(b_full + i, kWorkWarps);
       mbar_init(b_empty + i, 1);
       mbar_init(b_raw + i, 1);
-      mbar_init(b_free + i, kLoadWarps);
+      mbar_init(b_free + i, kWorkWarps);
     }
     for (int i = 0; i < kTiles; ++i) {
       mbar_init(b_s + i, 1);
-      mbar_init(b_p + i, 4);
+      mbar_init(b_p + i, kSoftWarps / kTiles);
       mbar_init(b_o + i, 1);
     }
-    for (int i = 0; i < kInfo; ++i) mbar_init(b_info + i, kLoaders);
+    for (int i = 0; i < kInfo; ++i) mbar_init(b_info + i, kWorkers);
     mbar_init(b_q, kSoft);
     fence_barrier_init();
+    Piece& p = sh_piece;
+    p.items = p.steps = p.used[0] = p.used[1] = p.done[0] = p.done[1] = p.number = p.fixed = 0;
+    p.nt = 0;
+    p.alt = p.over = false;
   }
   tc_before();
   __syncthreads();
@@ -198,77 +240,114 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   pdl_wait();
   pdl_trigger();
 
-  Line line;
-  if (a.whole) {
-    // segments of the longest prompts' last queries first; a row's tokens are not known here, so its place is by T
-    const int per = a.r.batch * a.c.heads;
-    const int mt = static_cast<int>(gridDim.x / per) - 1 - static_cast<int>(blockIdx.x / per);
-    const int x = static_cast<int>(blockIdx.x % per);
-    line.b = x / a.c.heads;
-    const RowWork w = row_work<kRows, kTok>(a, line.b);
-    if (blockIdx.x == 0) {
-      for (int i = tid; i < a.r.batch; i += kThreads) {
-        const RowWork y = row_work<kRows, kTok>(a, i);
-        if (y.s.count < 0) set_error(a.c.err, RSSM_ERRBIT_SEQLEN);
-        if (y.len == -2) set_error(a.c.err, RSSM_ERRBIT_PAGE);
+  __shared__ Line sh_line;
+  {
+    Line line;
+    if (a.whole) {
+      // segments of the longest prompts' last queries first; a row's tokens are not known here, so its place is by T
+      const int per = a.r.batch * a.c.heads;
+      const int mt = static_cast<int>(gridDim.x / per) - 1 - static_cast<int>(blockIdx.x / per);
+      const int x = static_cast<int>(blockIdx.x % per);
+      line.b = x / a.c.heads;
+      const RowWork w = row_work<kRows, kTok>(a, line.b);
+      if (blockIdx.x == 0) {
+        for (int i = threadIdx.x; i < a.r.batch; i += kThreads) {
+          const RowWork y = row_work<kRows, kTok>(a, i);
+          if (y.s.count < 0) set_error(a.c.err, RSSM_ERRBIT_SEQLEN);
+          if (y.len == -2) set_error(a.c.err, RSSM_ERRBIT_PAGE);
+        }
       }
+      line.base = 0;
+      line.share = 1;
+      line.lo = mt < w.mtiles ? static_cast<long long>(mt * a.c.heads + x % a.c.heads) * w.tiles : 0;
+      line.hi = mt < w.mtiles ? line.lo + w.tiles : 0;
+    } else {
+      line = cut_line<kRows, kTok, kThreads>(a);
     }
-    line.base = 0;
-    line.share = 1;
-    line.lo = mt < w.mtiles ? static_cast<long long>(mt * a.c.heads + x % a.c.heads) * w.tiles : 0;
-    line.hi = mt < w.mtiles ? line.lo + w.tiles : 0;
-  } else {
-    line = cut_line<kRows, kTok, kThreads>(a);
+    if (threadIdx.x == 0) sh_line = line;
   }
-  int b = line.b;
-  long long rbase = line.base;
-  // how often things came round so far: items of the ring, steps, pieces, and by tile scores and sums; fixed tiles (bf16)
-  int items = 0, steps = 0, pieces = 0, fixed = 0, used0 = 0, used1 = 0, done0 = 0, done1 = 0;
   bool ok = true;
+  __shared__ Joint sh_joint[2];
+  int joints = 0;
 
 #pragma unroll 1
-  for (long long u = line.lo; u < line.hi;) {
-    const RowWork w = row_work<kRows, kTok>(a, b);
-    const long long units = static_cast<long long>(w.tiles) * w.mtiles * a.c.heads;
-    if (u >= rbase + units) {
-      rbase += units;
-      ++b;
-      continue;
-    }
-    const long long at = u - rbase;
-    const int seg = static_cast<int>(at / w.tiles), t0 = static_cast<int>(at - static_cast<long long>(seg) * w.tiles);
-    const int t1 = static_cast<int>(min(static_cast<long long>(w.tiles), t0 + (line.hi - u)));
-    const int mtile = seg / a.c.heads, head = seg - mtile * a.c.heads;
-    const long long seg0 = u - t0;
-    u += t1 - t0;
-    const int row0 = mtile * kRows, rows = min(kRows, w.s.count * a.group - row0);
-    const bool alt = rows <= kQ;  // both tiles have the same queries, and every other step
-    const int last = (row0 + rows - 1) / a.group;
-    // every warp looks at the row's tree by itself
-    unsigned long long masks[2] = {0ull, 0ull};
-    bool fine = true;
-    if (a.parents && w.len >= 0) fine = tree_masks(a.parents + w.s.first, w.s.count, lane, masks);
-    if (!fine && tid == 0) set_error(a.c.err, RSSM_ERRBIT_TREE);
-    const long long end = w.len < 0 || !fine ? 0 : static_cast<long long>(w.len) + (a.parents ? w.s.count : last + 1);
-    // from here on there are tokens that not every query of the tile sees, or none
-    const long long some = static_cast<long long>(w.len) + (a.parents ? 0 : row0 / a.group + 1);
-    const int stop = static_cast<int>(min(static_cast<long long>(t1), (end + kTok - 1) / kTok));
-    const int nt = max(0, stop - t0);
-    const int* table = a.r.pages + b * a.r.pages_stride;
-    const uint8_t* vbase = a.c.v + static_cast<long long>(head) * a.c.page_size * RB;
-    float ref = -INFINITY, sum = 0.0f, join0 = 1.0f, join1 = 0.0f;  // join: what the two tiles' sums are times where both have the same queries
-    int t = 0;                                                      // a thread's query's new token,
-    unsigned long long path = 0ull;                                 // and those it comes after
+  while (true) {
     __syncthreads();  // the last piece's shared memory is free
+    if (warp == 0) {
+      // ---- the next piece, by the first warp: line.lo is the unit that it begins with
+      Piece& p = sh_piece;
+      Line& line = sh_line;
+      RowWork w;
+      bool over = true;
+      while (line.lo < line.hi) {
+        w = row_work<kRows, kTok>(a, line.b);
+        const long long units = static_cast<long long>(w.tiles) * w.mtiles * a.c.heads;
+        over = line.lo >= line.base + units;
+        if (!over) break;
+        __syncwarp();
+        if (lane == 0) {
+          line.base += units;
+          ++line.b;
+        }
+        __syncwarp();
+      }
+      bool fine = true;
+      if (!over && a.parents && w.len >= 0) {
+        unsigned long long masks[2];
+        fine = tree_masks(a.parents + w.s.first, w.s.count, lane, masks);
+        sh_mask[lane] = masks[0];
+        sh_mask[lane + 32] = masks[1];
+        if (!fine && lane == 0) set_error(a.c.err, RSSM_ERRBIT_TREE);
+      }
+      __syncwarp();
+      if (lane == 0) {
+        // what the last piece used
+        p.items += 2 * p.nt;
+        p.steps += p.nt;
+        p.used[0] += p.alt ? (p.nt + 1) / 2 : p.nt;
+        p.used[1] += p.alt ? p.nt / 2 : p.nt;
+        p.done[0] += p.nt > 0;
+        p.done[1] += p.nt > (p.alt ? 1 : 0);
+        ++p.number;
+        p.over = over;
+        if (!over) {
+          const long long at = line.lo - line.base;
+          const int seg = static_cast<int>(at / w.tiles);
+          p.t0 = static_cast<int>(at - static_cast<long long>(seg) * w.tiles);
+          p.t1 = static_cast<int>(min(static_cast<long long>(w.tiles), p.t0 + (line.hi - line.lo)));
+          p.tiles = w.tiles;
+          p.whole = p.t0 == 0 && p.t1 == w.tiles;
+          line.lo += p.t1 - p.t0;
+          const int mtile = seg / a.c.heads;
+          p.head = seg - mtile * a.c.heads;
+          p.row = line.b;
+          p.first = w.s.first;
+          p.len = w.len;
+          p.count = w.s.count;
+          p.row0 = mtile * kRows;
+          p.rows = min(kRows, w.s.count * a.group - p.row0);
+          p.alt = p.rows <= kQ;
+          p.fine = fine;
+          p.end = w.len < 0 || !fine ? 0 : w.len + (a.parents ? w.s.count : (p.row0 + p.rows - 1) / a.group + 1);
+          p.some = w.len + (a.parents ? 0 : p.row0 / a.group + 1);
+          p.nt = max(0, min(p.t1, (p.end + kTok - 1) / kTok) - p.t0);
+        }
+      }
+    }
+    __syncthreads();
+    const Piece& p = sh_piece;
+    if (p.over) break;
 
     if (warp < kSoftWarps) {
       // ---- queries
       const float scale2 = fmaxf(fabsf(a.scale2), 1e-30f);  // (times -inf it stays that)
       {
-        const bool flip = a.scale2 < 0.0f;           // the maximum is taken before the scale
-        constexpr int G = D / 8, AT = 32 / G, N = 4;  // lanes of a row, rows of a warp; rows on their way at a time
+        const bool flip = a.scale2 < 0.0f;            // the maximum is taken before the scale
+        constexpr int G = D / 8, AT = 32 / G, N = 2;  // lanes of a row, rows of a warp; rows on their way at a time
+        const int row0 = p.row0, rows = p.rows, head = p.head;
+        const long long first = p.first;
 #pragma unroll 1
-        for (int r0 = warp * AT; r0 < (alt ? kQ : kRows); r0 += N * kSoftWarps * AT) {
+        for (int r0 = warp * AT; r0 < (p.alt ? kQ : kRows); r0 += N * kSoftWarps * AT) {
           uint4 x[N];
 #pragma unroll
           for (int i = 0; i < N; ++i) {
@@ -276,7 +355,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             x[i] = make_uint4(0u, 0u, 0u, 0u);
             if (r < rows) {
               const int tq = (row0 + r) / a.group, h = head * a.group + (row0 + r) - tq * a.group;
-              x[i] = *reinterpret_cast<const uint4*>(a.q + (w.s.first + tq) * a.q_stride + static_cast<long long>(h) * D + lane % G * 8);
+              x[i] = *reinterpret_cast<const uint4*>(a.q + (first + tq) * a.q_stride + static_cast<long long>(h) * D + lane % G * 8);
               if (flip) x[i] = make_uint4(x[i].x ^ 0x80008000u, x[i].y ^ 0x80008000u, x[i].z ^ 0x80008000u, x[i].w ^ 0x80008000u);
             }
           }
@@ -294,39 +373,37 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       }
       fence_async();
       mbar_arrive(b_q);
-      if constexpr (Q8) soft_sync();
-      // ---- scores into weights
-      const int tile = warp >> 2;
-      const int r = alt ? tid & (kQ - 1) : tid;  // its query
-      t = (row0 + min(r, rows - 1)) / a.group;
-      if (a.parents) {
-        const unsigned long long m0 = __shfl_sync(full, masks[0], t & 31), m1 = __shfl_sync(full, masks[1], t & 31);
-        path = t < 32 ? m0 : m1;
-      }
+      if constexpr (Q8) soft_sync<kSoft>();
+      // ---- scores into weights: a warp's tile, half of a step's tokens, lanes of tensor memory; a thread's query in the tile
+      const int tile = warp / (4 * kParts), half = (warp >> 2) % kParts, mine = (warp & 3) * 32 + lane;
+      const bool alt = p.alt;
+      const int r = alt ? mine : tile * kQ + mine;
+      const int t = (p.row0 + min(r, p.rows - 1)) / a.group;
+      const unsigned long long path = a.parents ? sh_mask[t & 63] : 0ull;
       const float back = Q8 ? sh_back[r] : scale2;
-      const uint32_t s_at = tm + tile * kTok + ((warp & 3) << 21), o_at = tm + kTiles * kTok + tile * D + ((warp & 3) << 21);
-      const int step = alt ? 2 : 1, n0 = tile ? used1 : used0;
-      int n = n0;
+      const uint32_t s_at = tm + ((warp & 3) << 21) + tile * kTok + half * kPart;
+      const int n0 = p.used[tile], nt = p.nt, len = p.len, some = p.some;
+      float ref = -INFINITY, sum = 0.0f;
+      int n = n0, j = alt ? tile : 0, step = p.steps + j, pos = (p.t0 + j) * kTok + half * kPart;
 #pragma unroll 1
-      for (int j = alt ? tile : 0; j < nt; j += step, ++n) {
-        const int slot = (steps + j) % kInfo;
-        ok = ok && wait(b_info + slot, ((steps + j) / kInfo) & 1);
+      for (; j < nt; ++n) {
+        const int slot = step % kInfo;
+        ok = ok && wait(b_info + slot, (step / kInfo) & 1);
         ok = __all_sync(full, ok && wait(b_s + tile, n & 1)) != 0;
         if (!ok) break;
         tc_after();
-        const long long pos = static_cast<long long>(t0 + j) * kTok;
-        const unsigned valid = sh_valid[slot];
-        const bool edge = pos + kTok > some || valid != 0xffu;
-        const float* info = reinterpret_cast<const float*>(sm + S::kInfoAt) + slot * 3 * kTok;
-        // the scores go through the registers 32 at a time, the next ones on their way meanwhile: once for the maximum, once for the weights
-        uint32_t x[2][32];
-        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        tc_ld32(x[0], s_at);
+        uint32_t x[kPart / 32][32];
 #pragma unroll
-        for (int c = 0; c < kTok / 32; ++c) {
-          uint32_t(&y)[32] = x[c & 1];
-          landed(y);
-          if (c + 1 < kTok / 32) tc_ld32(x[(c + 1) & 1], s_at + 32 * (c + 1));
+        for (int c = 0; c < kPart / 32; ++c) tc_ld32(x[c], s_at + 32 * c);
+        const unsigned valid = sh_valid[slot] >> (8 / kParts * half);
+        const bool edge = pos + kPart > some || (valid & (0xffu >> (8 - 8 / kParts))) != 0xffu >> (8 - 8 / kParts);
+        const float* info = reinterpret_cast<const float*>(sm + S::kInfoAt) + slot * 3 * kTok + half * kPart;
+#pragma unroll
+        for (int c = 0; c < kPart / 32; ++c) landed(x[c]);
+        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < kPart / 32; ++c) {
+          uint32_t(&y)[32] = x[c];
           if constexpr (Q8) {  // in units of log2, with their values' scales
             const pair bb = pack2(back, back);
 #pragma unroll
@@ -338,26 +415,31 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           }
           if (edge) {
             // which of the 32 this query sees
-            const long long j0 = pos + 32 * c - w.len;
+            const int j0 = pos + 32 * c - len;
             uint32_t see;
             if (a.parents) {
               see = j0 <= -32 ? full : j0 < 0 ? static_cast<uint32_t>(path << -j0) | ((1u << -j0) - 1u) : j0 < 64 ? static_cast<uint32_t>(path >> j0) : 0u;
             } else {
-              const long long m = t - j0;  // the last one's place
+              const int m = t - j0;  // the last one's place
               see = m >= 31 ? full : m < 0 ? 0u : (2u << m) - 1u;
             }
             see &= (valid >> (2 * c) & 1u ? 0xffffu : 0u) | (valid >> (2 * c + 1) & 1u ? 0xffff0000u : 0u);
 #pragma unroll
             for (int i = 0; i < 32; ++i) y[i] = see >> i & 1u ? y[i] : 0xff800000u;  // -inf
           }
-          if (Q8 || edge) tc_st32(s_at + 32 * c, y);
 #pragma unroll
           for (int i = 0; i < 32; ++i) t4[i & 3] = fmaxf(t4[i & 3], __uint_as_float(y[i]));
         }
-        if (Q8 || edge) tc_wait_st();
-        tc_ld32(x[0], s_at);
         float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
         if constexpr (!Q8) top = top == -INFINITY ? top : top * back;
+        if constexpr (kParts == 2) {
+          // the other half's; after this the other half's scores are in registers too, and P may take their place
+          sh_top[tile][half][mine] = top;
+          tc_before();
+          pair_sync(warp & 3 | tile << 2);
+          tc_after();
+          top = fmaxf(top, sh_top[tile][half ^ 1][mine]);
+        }
         // the maximum in use follows where it has to; the products before this step's are done (its scores came after them)
         if (__any_sync(full, top > ref + kLazy)) {
           const float now = fmaxf(ref, top);
@@ -365,16 +447,16 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           ref = now;
           sum *= f;
           if (n > n0) {
+            const uint32_t o_at = tm + ((warp & 3) << 21) + kTiles * kTok + tile * D + half * (D / kParts);
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t y[16];
-              tc_ld16(y, o_at + 16 * c);
+            for (int c = 0; c < D / (8 * kParts); ++c) {
+              uint32_t y[8];
+              tc_ld8(y, o_at + 8 * c);
               tc_wait_ld();
+              tc_landed(y);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(y[i]));
-#pragma unroll
-              for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
-              tc_st16(o_at + 16 * c, y);
+              for (int i = 0; i < 8; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+              tc_stw8(o_at + 8 * c, y);
             }
           }
         }
@@ -382,18 +464,15 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         const pair lift2 = pack2(lift, lift), scale22 = pack2(back, back);
         pair s2[2] = {0ull, 0ull};
 #pragma unroll
-        for (int c = 0; c < kTok / 32; ++c) {
-          uint32_t(&z)[32] = x[c & 1];
-          landed(z);
-          if (c + 1 < kTok / 32) tc_ld32(x[(c + 1) & 1], s_at + 32 * (c + 1));
-          uint32_t p[16];
+        for (int c = 0; c < kPart / 32; ++c) {
+          uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
             ulonglong2 v4;
             if constexpr (Q8) v4 = *reinterpret_cast<const ulonglong2*>(info + 2 * kTok + 32 * c + i);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              pair y = pack2(__uint_as_float(z[i + 2 * e]), __uint_as_float(z[i + 2 * e + 1]));
+              pair y = pack2(__uint_as_float(x[c][i + 2 * e]), __uint_as_float(x[c][i + 2 * e + 1]));
               if constexpr (Q8) add2(y, lift2);
               else y = fma2v(y, scale22, lift2);
               float y0, y1;
@@ -403,14 +482,14 @@ __global__ void __launch_bounds__(S::kThreads, 1)
               const pair p2 = pack2(y0, y1);
               if constexpr (Q8) {
                 fma2(s2[e], p2, e ? v4.y : v4.x);
-                p[i / 2 + e] = f16_pair(y0, y1);
+                w[i / 2 + e] = f16_pair(y0, y1);
               } else {
                 add2(s2[e], p2);
-                p[i / 2 + e] = bf16_pair(y0, y1);
+                w[i / 2 + e] = bf16_pair(y0, y1);
               }
             }
           }
-          tc_st16(s_at + 16 * c, p);
+          tc_st16(s_at - half * (kPart / 2) + 16 * c, w);
         }
         add2(s2[0], s2[1]);
         float u0, u1;
@@ -420,31 +499,41 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         tc_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(b_p + tile);
+        const int by = alt ? 2 : 1;
+        j += by;
+        step += by;
+        pos += by * kTok;
       }
       if (nt > (alt ? tile : 0)) {
-        ok = __all_sync(full, ok && wait(b_o + tile, (tile ? done1 : done0) & 1)) != 0;
+        ok = __all_sync(full, ok && wait(b_o + tile, p.done[tile] & 1)) != 0;
         tc_after();
       }
+      sh_sum[tile][half][mine] = sum;
+      if (half == 0) sh_ref[tile][mine] = ref;
     } else if (warp < kMmaWarp) {
       // ---- keys and values, in turn
-      const int lt = tid - kSoft, lw = warp - kSoftWarps;
+      const int items = p.items, steps = p.steps, nt = p.nt, t0 = p.t0, end = p.end, head = p.head;
+      const int* table = a.r.pages + p.row * a.r.pages_stride;
+      const int lw = warp - kSoftWarps, lt = static_cast<int>(threadIdx.x) - kSoft - (kLoadWarps - kWorkWarps) * 32;  // lt: of those that look or convert
       // a tile is 128 NC chunks of 16 bytes; thread lt looks at chunk `ch` of rows r0, r0 + R, ..
-      constexpr int R = kLoaders / NC, STEPS = (kTok + R - 1) / R;
-      const int ch = lt % NC, r0 = lt / NC;
+      constexpr int R = kWorkers / NC;
+      const int ch = (lt + kWorkers) % NC, r0 = lt / NC;
+      // (asked for a step ahead, whether there is one or not: a load in a branch would be waited for there)
+      const int most = max(0, end - 1);
       auto page_id = [&](int j) {
-        const long long p = static_cast<long long>(t0 + j) * kTok + 16 * lane;
-        return lane < 8 && j < nt && p < end ? table[static_cast<unsigned>(p) / static_cast<unsigned>(a.c.page_size)] : -1;
+        const unsigned at = min(most, (t0 + j) * kTok + 16 * (lane & 7));
+        return end > 0 ? __ldg(table + at / static_cast<unsigned>(a.c.page_size)) : 0;
       };
       int next_id = page_id(0);
       unsigned missing = 0u;
       // where the slices of step j are, for this warp
       auto find = [&](int j) {
-        const long long mine = static_cast<long long>(t0 + j) * kTok + 16 * lane;
+        const int mine = (t0 + j) * kTok + 16 * lane;
         const int id = next_id;
         next_id = page_id(j + 1);
         const bool wanted = lane < 8 && mine < end, have = wanted && id >= 0 && id < a.c.pages;
-        if (wanted && !have) set_error(a.c.err, RSSM_ERRBIT_PAGE);
         missing = __ballot_sync(full, wanted && !have);
+        if (missing && lane == 0) set_error(a.c.err, RSSM_ERRBIT_PAGE);
         if (lane < 8) {
           const unsigned place = static_cast<unsigned>(mine) % static_cast<unsigned>(a.c.page_size);
           Slice s;
@@ -452,7 +541,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           s.off[1] = have ? id * a.c.v_page + (static_cast<long long>(head) * a.c.page_size + place) * RB : 0;
           s.page = have ? id : 0;
           s.place = static_cast<int>(place);
-          s.live = have ? static_cast<int>(min(16ll, end - mine)) : 0;
+          s.live = have ? min(16, end - mine) : 0;
           sh_slice[lw][j & 1][lane] = s;
         }
         __syncwarp();
@@ -479,88 +568,88 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         }
       };
       if constexpr (Q8) {
-        float ksv[2] = {0.0f, 0.0f}, vsv[2] = {0.0f, 0.0f};  // the scales of tokens lt and lt + kLoaders of the newest step asked for
-        int asked = 0;
-        auto ask = [&](int n) {  // item n of the piece
-          if (n >= 2 * nt) return;
-          const int item = items + n, buf = item % kRing;
-          if (!(n & 1)) {
-            find(n >> 1);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int i = lt + kLoaders * e;
-              const Slice& sl = sh_slice[lw][n >> 1 & 1][(i / 16) & 7];
-              const long long row = static_cast<long long>(head) * a.c.page_size + sl.place + (i & 15);
-              const bool there = i < kTok && (i & 15) < sl.live;
-              ksv[e] = there ? a.c.ks[sl.page * a.c.ks_page + row] : 0.0f;
-              vsv[e] = there ? a.c.vs[sl.page * a.c.vs_page + row] : 0.0f;
-            }
-          }
-          if (lw == 0) {
-            ok = __all_sync(full, ok && (item < kRing || wait(b_free + buf, (item / kRing - 1) & 1))) != 0;
-            if (ok) {
-              copy(n, b_raw + buf, base + S::kRawAt + buf * kTok * RB);
-              asked = n + 1;
-            }
-          }
-        };
-        ask(0);
-        ask(1);
-        int n = 0;
+        if (lw == 0) {
+          int n = 0;
 #pragma unroll 1
-        for (; n < 2 * nt; ++n) {
-          const int item = items + n, buf = item % kRing, j = n >> 1;
-          ok = ok && (item < kRing || wait(b_empty + buf, (item / kRing - 1) & 1));
-          if (ok && !(n & 1)) {
-            // what goes with the step (asked for with item 2 j, the newest still): its place is free, by the buffer that K waits for
-            const int slot = (steps + j) % kInfo;
-            float* info = reinterpret_cast<float*>(sm + S::kInfoAt) + slot * 3 * kTok;
-            if (lt == 0) sh_valid[slot] = 0xffu & ~missing;
+          for (; n < 2 * nt; ++n) {
+            const int item = items + n, buf = item % kRing;
+            if (!(n & 1)) find(n >> 1);
+            ok = __all_sync(full, ok && (item < kRing || wait(b_free + buf, (item / kRing - 1) & 1))) != 0;
+            if (!ok) break;
+            copy(n, b_raw + buf, base + S::kRawAt + buf * kTok * RB);
+          }
+          if (!ok)  // no copy is in flight at the end
+            for (int i = max(0, n - kRing); i < n; ++i) mbar_wait(b_raw + (items + i) % kRing, ((items + i) / kRing) & 1);
+        } else {
+          constexpr int N = (kTok + kWorkers - 1) / kWorkers;
+          float ksv[N], vsv[N];  // the scales of tokens lt, lt + kWorkers, .. of the newest step asked for
+          auto scales = [&](int j) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int i = lt + kLoaders * e;
-              if (i < kTok) {
+            for (int e = 0; e < N; ++e) {
+              const int i = lt + e * kWorkers;
+              const Slice& sl = sh_slice[lw][j & 1][i / 16 & 7];
+              const long long row = static_cast<long long>(head) * a.c.page_size + sl.place + (i & 15);
+              ksv[e] = a.c.ks[sl.page * a.c.ks_page + row];  // (of page 0 where there is none: such a token's weight is 0)
+              vsv[e] = a.c.vs[sl.page * a.c.vs_page + row];
+            }
+          };
+          if (nt > 0) {
+            find(0);
+            scales(0);
+          }
+#pragma unroll 1
+          for (int n = 0; n < 2 * nt; ++n) {
+            const int item = items + n, buf = item % kRing, j = n >> 1;
+            ok = __all_sync(full, ok && (item < kRing || wait(b_empty + buf, (item / kRing - 1) & 1))) != 0;
+            if (!ok) break;
+            if (!(n & 1)) {
+              // what goes with the step: its place is free, by the buffer that K waits for
+              const int slot = (steps + j) % kInfo;
+              float* info = reinterpret_cast<float*>(sm + S::kInfoAt) + slot * 3 * kTok;
+              if (lt == 0) sh_valid[slot] = 0xffu & ~missing;
+#pragma unroll
+              for (int e = 0; e < N; ++e) {
+                const int i = lt + e * kWorkers;
                 const float y = vsv[e] < 7.7037197775489434e-34f ? 7.7037197775489434e-34f : vsv[e];  // 2^-110: a scale of 0 stands for zeros all the same
+                if (i >= kTok) break;
                 info[i] = ksv[e];
                 info[kTok + i] = __log2f(y);
-                info[2 * kTok + i] = y == y ? __frcp_rn(y) * kShift8 : 0.0f;  // (a weight is NaN as it is, or 0 where the token is not seen)
+                info[2 * kTok + i] = y == y ? rcp_fast(y) * kShift8 : 0.0f;  // (a weight is NaN as it is, or 0 where the token is not seen)
+              }
+              mbar_arrive(b_info + slot);
+              if (j + 1 < nt) {
+                find(j + 1);
+                scales(j + 1);
               }
             }
-            mbar_arrive(b_info + slot);
-          }
-          ask(n + 2);
-          ok = __all_sync(full, ok && wait(b_raw + buf, (item / kRing) & 1)) != 0;
-          if (!ok) break;
-          const uint32_t raw_at = base + S::kRawAt + buf * kTok * RB + ch * 16;
-          uint8_t* const half = sm + S::kRingAt + buf * S::kTile + (ch / 4) * 16384;
-          const Slice* slices = sh_slice[lw][j & 1];
+            ok = __all_sync(full, wait(b_raw + buf, (item / kRing) & 1)) != 0;
+            if (!ok) break;
+            const uint32_t raw_at = base + S::kRawAt + buf * kTok * RB + ch * 16;
+            uint8_t* const half = sm + S::kRingAt + buf * S::kTile + (ch / 4) * 16384;
+            const Slice* slices = sh_slice[lw][j & 1];
+#pragma unroll 4
+            for (int r = r0; r < kTok; r += R) {
+              uint32_t c4[4], h[8];
+              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(c4[0]), "=r"(c4[1]), "=r"(c4[2]), "=r"(c4[3]) : "r"(raw_at + r * RB));
+              const bool there = r % 16 < slices[r / 16].live;  // what lies behind may be anything
 #pragma unroll
-          for (int x = 0; x < STEPS; ++x) {
-            const int r = r0 + R * x;
-            if (r >= kTok) break;
-            uint32_t c4[4], h[8];
-            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(c4[0]), "=r"(c4[1]), "=r"(c4[2]), "=r"(c4[3]) : "r"(raw_at + r * RB));
-            const bool there = r % 16 < slices[r / 16].live;  // what lies behind may be anything
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t y = !there ? S::FMT == RSSM_I8 ? 0x80808080u : 0u : S::FMT == RSSM_I8 ? c4[e] ^ 0x80808080u : c4[e];
-              h[2 * e] = codes_f16<S::FMT>(y, 0x4140u, 0x4410u);
-              h[2 * e + 1] = codes_f16<S::FMT>(y, 0x4342u, 0x4432u);
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t y = !there ? S::FMT == RSSM_I8 ? 0x80808080u : 0u : S::FMT == RSSM_I8 ? c4[e] ^ 0x80808080u : c4[e];
+                codes_f16<S::FMT>(y, h[2 * e], h[2 * e + 1]);
+              }
+              *reinterpret_cast<uint4*>(half + sw(r, (2 * ch) % 8)) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(half + sw(r, (2 * ch + 1) % 8)) = make_uint4(h[4], h[5], h[6], h[7]);
             }
-            *reinterpret_cast<uint4*>(half + sw(r, (2 * ch) % 8)) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(half + sw(r, (2 * ch + 1) % 8)) = make_uint4(h[4], h[5], h[6], h[7]);
-          }
-          fence_async();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(b_full + buf);
-            mbar_arrive(b_free + buf);
+            fence_async();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(b_full + buf);
+              mbar_arrive(b_free + buf);
+            }
           }
         }
-        if (!ok && lw == 0)  // no copy is in flight at the end
-          for (; n < asked; ++n) mbar_wait(b_raw + (items + n) % kRing, ((items + n) / kRing) & 1);
       } else {
-        int n = 0;
+        int n = 0, fixed = p.fixed;
 #pragma unroll 1
         for (; n < 2 * nt; ++n) {
           const int item = items + n, buf = item % kRing, j = n >> 1;
@@ -574,16 +663,16 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           }
           const uint32_t to = base + S::kRingAt + buf * S::kTile;
           // values that not every query sees are looked at before the product gets them, and what lies behind the last is zero
-          const bool fix = (n & 1) && (static_cast<long long>(t0 + j + 1) * kTok > some || missing);
+          const bool fix = (n & 1) && ((t0 + j + 1) * kTok > p.some || missing);
           if (lw == 0) copy(n, fix ? b_raw : b_full + buf, to);
           if (fix) {
             ok = __all_sync(full, ok && wait(b_raw, fixed & 1)) != 0;
             ++fixed;
             if (!ok) break;
-            uint8_t* p = sm + S::kRingAt + buf * S::kTile + (ch / 8) * 16384;
+            uint8_t* tile = sm + S::kRingAt + buf * S::kTile + (ch / 8) * 16384;
             const Slice* slices = sh_slice[lw][j & 1];
             for (int r = r0; r < kTok; r += R) {
-              uint4* q = reinterpret_cast<uint4*>(p + sw(r, ch % 8));
+              uint4* q = reinterpret_cast<uint4*>(tile + sw(r, ch % 8));
               if (r % 16 >= slices[r / 16].live) {
                 *q = make_uint4(0u, 0u, 0u, 0u);
                 continue;
@@ -591,7 +680,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
               uint4 y = *q;
               if (take_out_odd(y)) {
                 *q = y;
-                sh_odd = pieces + 1;
+                sh_odd = p.number;
               }
             }
             fence_async();
@@ -599,11 +688,13 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           }
           if (lane == 0 && (fix || lw != 0)) mbar_arrive(b_full + buf);
         }
+        if (lw == 0 && lane == 0) sh_piece.fixed = fixed;  // (the others have read it: each item takes them all)
         if (!ok && lw == 0)  // no copy is in flight at the end
           for (int i = max(0, n - kRing); i < n; ++i) mbar_wait(b_full + (items + i) % kRing, ((items + i) / kRing) & 1);
       }
-    } else if (lane == 0) {
+    } else {
       // ---- products
+      const int items = p.items, nt = p.nt, used0 = p.used[0], used1 = p.used[1];
       constexpr uint32_t kind = Q8 ? (1u << 7) | (1u << 10) : 0u;  // fp16 operands: without bf16's bits
       constexpr uint32_t i_s = instruction(kTok, false, false) & ~kind, i_o = instruction(D, false, true) & ~kind;
       auto scores = [&](int tile, int queries, int buf) {
@@ -611,45 +702,45 @@ __global__ void __launch_bounds__(S::kThreads, 1)
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
           const uint64_t o = (x / 4) * (16384 / 16) + (x % 4) * 2;
-          tc_mma(tm + tile * kTok, q + o, k + o, i_s, x > 0);
+          mma_ss(lane == 0, tm + tile * kTok, q + o, k + o, i_s, x > 0);
         }
-        tc_commit(b_s + tile);
+        commit(lane == 0, b_s + tile);
       };
       auto sums = [&](int tile, int buf, bool more) {
         const uint64_t v = operand(base + S::kRingAt + buf * S::kTile, 16384, 1024, kSw128);
 #pragma unroll
-        for (int y = 0; y < kTok / 16; ++y) tc_mma_ts(tm + kTiles * kTok + tile * D, tm + tile * kTok + 8 * y, v + y * (2048 / 16), i_o, more || y > 0);
+        for (int y = 0; y < kTok / 16; ++y) mma_ts(lane == 0, tm + kTiles * kTok + tile * D, tm + tile * kTok + 8 * y, v + y * (2048 / 16), i_o, more || y > 0);
       };
       auto filled = [&](int n) {  // item n of the piece is there
         const int item = items + n;
-        ok = ok && wait(b_full + item % kRing, (item / kRing) & 1);
+        ok = __all_sync(full, ok && wait(b_full + item % kRing, (item / kRing) & 1)) != 0;
         return item % kRing;
       };
-      ok = ok && wait(b_q, pieces & 1);
-      if (alt) {
+      ok = __all_sync(full, ok && wait(b_q, (p.number - 1) & 1)) != 0;
+      if (p.alt) {
         for (int j = 0; ok && j < min(nt, 2); ++j) {
           const int buf = filled(2 * j);
           if (!ok) break;
           tc_after();
           scores(j, 0, buf);
-          tc_commit(b_empty + buf);
+          commit(lane == 0, b_empty + buf);
         }
 #pragma unroll 1
         for (int j = 0; ok && j < nt; ++j) {
           const int x = j & 1, bv = filled(2 * j + 1);
-          ok = ok && wait(b_p + x, ((x ? used1 : used0) + j / 2) & 1);
+          ok = __all_sync(full, ok && wait(b_p + x, ((x ? used1 : used0) + j / 2) & 1)) != 0;
           if (!ok) break;
           tc_after();
           sums(x, bv, j > 1);
-          tc_commit(b_empty + bv);
+          commit(lane == 0, b_empty + bv);
           if (j + 2 < nt) {
             const int bk = filled(2 * j + 4);
             if (!ok) break;
             tc_after();
             scores(x, 0, bk);
-            tc_commit(b_empty + bk);
+            commit(lane == 0, b_empty + bk);
           } else {
-            tc_commit(b_o + x);
+            commit(lane == 0, b_o + x);
           }
         }
       } else {
@@ -658,7 +749,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           if (ok) {
             tc_after();
             for (int x = 0; x < kTiles; ++x) scores(x, x, buf);
-            tc_commit(b_empty + buf);
+            commit(lane == 0, b_empty + buf);
           }
         }
 #pragma unroll 1
@@ -666,137 +757,132 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           const bool more = j + 1 < nt;
           const int bv = filled(2 * j + 1), bk = more ? filled(2 * j + 2) : 0;
           for (int x = 0; x < kTiles; ++x) {
-            ok = ok && wait(b_p + x, ((x ? used1 : used0) + j) & 1);
+            ok = __all_sync(full, ok && wait(b_p + x, ((x ? used1 : used0) + j) & 1)) != 0;
             if (!ok) break;
             tc_after();
             sums(x, bv, j > 0);
             if (more) scores(x, x, bk);
-            else tc_commit(b_o + x);
+            else commit(lane == 0, b_o + x);
           }
           if (ok) {
-            tc_commit(b_empty + bv);
-            if (more) tc_commit(b_empty + bk);
+            commit(lane == 0, b_empty + bv);
+            if (more) commit(lane == 0, b_empty + bk);
           }
         }
       }
     }
     ok = __syncthreads_and(ok);
     if (!ok) break;
-    items += 2 * nt;
-    steps += nt;
-    ++pieces;
-    used0 += alt ? (nt + 1) / 2 : nt;
-    used1 += alt ? nt / 2 : nt;
-    done0 += nt > 0;
-    done1 += nt > (alt ? 1 : 0);
 
     // ---- the queries' sums
-    const bool whole = t0 == 0 && t1 == w.tiles;
-    constexpr float kUnit = Q8 ? kShift8 : 1.0f;
     if (warp < kSoftWarps) {
-      const int tile = warp >> 2;
-      const uint32_t o_at = tm + kTiles * kTok + tile * D + ((warp & 3) << 21);
-      const bool both = alt && nt > 1;
+      const int tile = warp / (4 * kParts), half = (warp >> 2) % kParts, mine = (warp & 3) * 32 + lane;
+      const uint32_t o_at = tm + ((warp & 3) << 21) + kTiles * kTok + tile * D + half * (D / kParts);
+      const bool alt = p.alt, whole = p.whole, both = alt && p.nt > 1;
+      const int rows = p.rows, row0 = p.row0;
+      float ref = sh_ref[tile][mine];
       float* const other = reinterpret_cast<float*>(sm + S::kRingAt);  // [dimension][query]
-      if (both) {
+      if (both && tile == 1) {
         // the second tile's sums are the same queries'
-        if (tile == 1) {
-          const int r = tid - kQ;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t x[32];
-            tc_ld32(x, o_at + 32 * c);
-            landed(x);
+        for (int c = 0; c < D / (32 * kParts); ++c) {
+          uint32_t x[32];
+          tc_ld32(x, o_at + 32 * c);
+          landed(x);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) other[(32 * c + i) * kQ + r] = __uint_as_float(x[i]);
-          }
-          sh_ref[r] = ref;
-          sh_sum[r] = sum;
-        }
-        soft_sync();
-        if (tile == 0) {
-          const float now = fmaxf(ref, sh_ref[tid]), at0 = now == -INFINITY ? 0.0f : now;
-          join0 = exp2_fast(ref - at0);
-          join1 = exp2_fast(sh_ref[tid] - at0);
-          sum = sum * join0 + sh_sum[tid] * join1;
-          ref = now;
+          for (int i = 0; i < 32; ++i) other[(half * (D / kParts) + 32 * c + i) * kQ + mine] = __uint_as_float(x[i]);
         }
       }
+      if (both) soft_sync<kSoft>();
+      float sum = sh_sum[tile][0][mine] + (kParts == 2 ? sh_sum[tile][kParts - 1][mine] : 0.0f);
       if (tile == 0 || !alt) {
-        const int r = tid;
-        float* const left = piece_place<kRows, D>(a, blockIdx.x, t0 == 0);
+        float join0 = 1.0f, join1 = 0.0f;  // what the two tiles' sums are times
+        if (both) {
+          const float now = fmaxf(ref, sh_ref[1][mine]), at0 = now == -INFINITY ? 0.0f : now;
+          join0 = exp2_fast(ref - at0);
+          join1 = exp2_fast(sh_ref[1][mine] - at0);
+          sum = sum * join0 + (sh_sum[1][0][mine] + (kParts == 2 ? sh_sum[1][kParts - 1][mine] : 0.0f)) * join1;
+          ref = now;
+        }
+        const int r = tile * kQ + mine;
+        float* const left = piece_place<kRows, D>(a, blockIdx.x, p.t0 == 0);
         const float inv = sum == 0.0f ? 0.0f : kUnit / sum;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < D / (32 * kParts); ++c) {
+          const int d0 = half * (D / kParts) + 32 * c;
           uint32_t x[32];
-          if (nt > 0) {
+          if (p.nt > 0) {
             tc_ld32(x, o_at + 32 * c);
             landed(x);
             if (both) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * join0 + other[(32 * c + i) * kQ + r] * join1);
+              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * join0 + other[(d0 + i) * kQ + mine] * join1);
             }
           } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = 0u;
           }
           if (r < rows) {
-            if constexpr (!Q8) {
-              if (sh_odd == pieces) {
-                const long long from = max(static_cast<long long>(t0) * kTok, some / kTok * kTok), to = min(static_cast<long long>(t1) * kTok, end);
-#pragma unroll 1
-                for (int i = 0; i < 32; i += 4) {
-                  float y[4];
-#pragma unroll
-                  for (int k = 0; k < 32; k += 4)
-                    if (k == i)
-#pragma unroll
-                      for (int e = 0; e < 4; ++e) y[e] = __uint_as_float(x[k + e]);
-                  add_odd(a, w, table, vbase, RB, from, to, t, path, 32 * c + i, y);
-#pragma unroll
-                  for (int k = 0; k < 32; k += 4)
-                    if (k == i)
-#pragma unroll
-                      for (int e = 0; e < 4; ++e) x[k + e] = __float_as_uint(y[e]);
-                }
-              }
-            }
             if (whole) {
               // bf16, in the place of the tile's queries: rows leave from there side by side
-              uint8_t* const q = sm + tile * S::kTile + (c / 2) * 16384;
+              uint8_t* const q = sm + tile * S::kTile + d0 / 64 * 16384;
 #pragma unroll
               for (int i = 0; i < 32; i += 8) {
                 uint32_t y[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[e] = bf16_pair(__uint_as_float(x[i + 2 * e]) * inv, __uint_as_float(x[i + 2 * e + 1]) * inv);
-                *reinterpret_cast<uint4*>(q + sw(r % kQ, (c & 1) * 4 + i / 8)) = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4*>(q + sw(mine, d0 % 64 / 8 + i / 8)) = make_uint4(y[0], y[1], y[2], y[3]);
               }
             } else {
 #pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                __stcg(reinterpret_cast<uint4*>(left + r * D + 32 * c + i), make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]));
+              for (int i = 0; i < 32; i += 4) __stcg(reinterpret_cast<uint4*>(left + r * D + d0 + i), make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]));
             }
           }
           __syncwarp();  // the next load is the whole warp's
         }
-        if (!whole && r < rows) {
+        if (!whole && r < rows && half == 0) {
           __stcg(left + kRows * D + r, ref);
           __stcg(left + kRows * D + kRows + r, sum);
         }
       }
       tc_before();
+      if (!Q8 && sh_odd == p.number) {
+        // values that are not finite, to those queries that see them
+        soft_sync<kSoft>();
+        const int from = max(p.t0 * kTok, p.some / kTok * kTok), to = min(p.t1 * kTok, p.end);
+        float* const left = piece_place<kRows, D>(a, blockIdx.x, p.t0 == 0);
+#pragma unroll 1
+        for (int i = threadIdx.x; i < rows * (D / 4); i += kSoft) {
+          const int r = i / (D / 4), c = i % (D / 4) * 4, t = (row0 + r) / a.group;
+          const float4 y = add_odd4(a, p.len, a.r.pages + p.row * a.r.pages_stride, a.c.v + static_cast<long long>(p.head) * a.c.page_size * RB, RB, from,
+                                    to, t, a.parents ? sh_mask[t & 63] : 0ull, c, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+          if (y.x == 0.0f && y.y == 0.0f && y.z == 0.0f && y.w == 0.0f) continue;
+          if (whole) {
+            uint2* const q = reinterpret_cast<uint2*>(sm + (r / kQ) * S::kTile + c / 64 * 16384 + sw(r % kQ, c % 64 / 8) + c % 8 * 2);
+            *q = make_uint2(bf16_pair(bf16lo(q->x) + y.x, bf16hi(q->x) + y.y), bf16_pair(bf16lo(q->y) + y.z, bf16hi(q->y) + y.w));
+          } else {
+            float4* const q = reinterpret_cast<float4*>(left + r * D + c);
+            const float4 z = __ldcg(q);
+            __stcg(q, make_float4(z.x + y.x, z.y + y.y, z.z + y.z, z.w + y.w));
+          }
+        }
+      }
       if (whole) {
-        soft_sync();
+        soft_sync<kSoft>();
         constexpr int G = D / 8;
-        for (int i = tid; i < rows * G; i += kSoft) {
-          const int r = i / G, ch = i % G, tq = (row0 + r) / a.group, h = head * a.group + (row0 + r) - tq * a.group;
-          *reinterpret_cast<uint4*>(a.out + (w.s.first + tq) * a.out_stride + static_cast<long long>(h) * D + ch * 8) =
+        for (int i = threadIdx.x; i < rows * G; i += kSoft) {
+          const int r = i / G, ch = i % G, tq = (row0 + r) / a.group, h = p.head * a.group + (row0 + r) - tq * a.group;
+          *reinterpret_cast<uint4*>(a.out + (p.first + tq) * a.out_stride + static_cast<long long>(h) * D + ch * 8) =
               *reinterpret_cast<const uint4*>(sm + (r / kQ) * S::kTile + (ch / 8) * 16384 + sw(r % kQ, ch % 8));
         }
       }
     }
-    if (!whole) join_pieces<kRows, D, kThreads>(a, w, head, row0, rows, seg0, line.share, kUnit);
+    if (!p.whole && threadIdx.x == 0) sh_joint[joints & 1] = Joint{p.first, sh_line.lo - p.t1, p.tiles, p.head, p.row0, p.rows};
+    joints += !p.whole;
   }
+  __syncthreads();
+  if (ok)
+    for (int i = 0; i < joints; ++i) join_pieces<kRows, D, kThreads, 4>(a, sh_joint[i], sh_line.share, kUnit);
   // a wait that gave up: what was started ends before the memory is given back
   if (!ok && warp == kMmaWarp && lane == 0) {
     mbar_init(b_info, 1);
@@ -808,7 +894,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   __syncthreads();
   tc_after();
   if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(kTmem) : "memory");
-  if (tid == 0 && dead) set_error(a.c.err, RSSM_ERRBIT_TIMEOUT);
+  if (threadIdx.x == 0 && dead) set_error(a.c.err, RSSM_ERRBIT_TIMEOUT);
 }
 
 // a layer's keys or values as [page][head][place][dimension], boxes of 64 dimensions of `box` tokens
