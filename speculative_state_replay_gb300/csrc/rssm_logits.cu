@@ -97,6 +97,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) logits_kernel(const LogitsA
   const int off = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(IN));
   const int base = rank * k.slice - off;  // the id of word 0
   const int words = min(k.slice, a.vocab - base);  // up to the last id's; none: <= 0
+  // where word w lies: a step's first four and last four words in planes of their own, so that a warp's 16-byte accesses neighbour
+  const int plane = k.slice / 2;
+  auto at = [&](int w) { return (w >> 3) * 4 + (w & 3) + (w & 4 ? plane : 0); };
   auto holds = [&](int id) { return id >= max(base, 0) && id - base < words; };  // (an id below 0 is none)
 
   // ---- the first logits, asked for early
@@ -117,6 +120,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) logits_kernel(const LogitsA
   if (!(temp >= 0.0f)) temp = 1.0f;
   float rep = a.repetition ? a.repetition[b] : 1.0f;
   if (!(rep > 0.0f)) rep = 1.0f;
+  const float less = __fdiv_rn(1.0f, rep);  // x / repetition is x times this: one rounding more
   const float presence = a.presence ? a.presence[b] : 0.0f, frequency = a.frequency ? a.frequency[b] : 0.0f;
   const bool counted = rep != 1.0f || presence != 0.0f || frequency != 0.0f;
   long long bias_lo = 0, bias_hi = 0;
@@ -160,16 +164,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks) logits_kernel(const LogitsA
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           if (holds(id[e])) {
-            if (i0 + e * kThreads < prompt) atomicOr(word + id[e] - base, kSeen);
-            else atomicAdd(word + id[e] - base, 1u);
+            if (i0 + e * kThreads < prompt) atomicOr(word + at(id[e] - base), kSeen);
+            else atomicAdd(word + at(id[e] - base), 1u);
           }
         }
       }
     }
-    if (counted && a.tokens && threadIdx.x < kTreeT && holds(sh_fed[threadIdx.x])) atomicAdd(word + sh_fed[threadIdx.x] - base, 1u);
+    if (counted && a.tokens && threadIdx.x < kTreeT && holds(sh_fed[threadIdx.x])) atomicAdd(word + at(sh_fed[threadIdx.x] - base), 1u);
     for (long long e = bias_lo + threadIdx.x; e < bias_hi; e += kThreads) {
       const int id = a.bias_id[e];
-      if (holds(id)) atomicOr(word + id - base, kBiased);
+      if (holds(id)) atomicOr(word + at(id - base), kBiased);
     }
     __syncthreads();
   }
@@ -178,9 +182,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) logits_kernel(const LogitsA
   const uint32_t* mask = a.mask ? a.mask + tok * a.mask_stride : nullptr;
   float top = -INFINITY;
   unsigned long long key = 0ull;
+  const bool greedy = temp == 0.0f;
   auto take = [&](float y, int id) {
     top = fmaxf(top, y);
-    if (temp == 0.0f && y > -INFINITY) key = max(key, top_key(y, id));
+    if (greedy && y > -INFINITY) key = max(key, top_key(y, id));
   };
   auto allowed = [&](int id) {  // the mask's bits of eight ids, the first of which may be before the row's
     if (!mask) return 0xffu;
@@ -204,23 +209,35 @@ __global__ void __launch_bounds__(kThreads, kBlocks) logits_kernel(const LogitsA
         for (int e = 0; e < kRun; ++e) f[e] = id + e >= 0 && w + e < words ? value<IN>(x[id + e]) : -INFINITY;
       }
       const uint32_t ok = allowed(id);
-      uint32_t c[kRun];
+      uint4* const p0 = reinterpret_cast<uint4*>(word + (w >> 1));
+      uint4* const p1 = reinterpret_cast<uint4*>(word + plane + (w >> 1));
+      uint32_t later = 0u;  // ids with a bias: their turn comes with that
       if (marked) {
-        *reinterpret_cast<uint4*>(c) = *reinterpret_cast<const uint4*>(word + w);
-        *reinterpret_cast<uint4*>(c + 4) = *reinterpret_cast<const uint4*>(word + w + 4);
+        const uint4 c0 = *p0, c1 = *p1;
+        if (c0.x | c0.y | c0.z | c0.w | c1.x | c1.y | c1.z | c1.w) {
+          const uint32_t c[kRun] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+          for (int e = 0; e < kRun; ++e) {
+            // (no branches: of a warp's 256 ids some mostly count)
+            const unsigned m = c[e] & ~(kSeen | kBiased);
+            const float y = f[e] * (f[e] > 0.0f ? less : rep);
+            f[e] = c[e] & ~kBiased ? y : f[e];
+            f[e] -= m ? presence + frequency * static_cast<float>(m) : 0.0f;
+            later |= (c[e] & kBiased) >> (30 - e);
+          }
+        }
       }
 #pragma unroll
-      for (int e = 0; e < kRun; ++e) {
-        if (marked && c[e] & ~kBiased) {
-          f[e] = f[e] > 0.0f ? __fdiv_rn(f[e], rep) : f[e] * rep;
-          const unsigned m = c[e] & ~(kSeen | kBiased);
-          if (m) f[e] -= presence + frequency * static_cast<float>(m);
-        }
-        if (!(ok >> e & 1u) || f[e] != f[e]) f[e] = -INFINITY;
-        if (!(marked && c[e] & kBiased)) take(f[e], id + e);
+      for (int e = 0; e < kRun; ++e) f[e] = ok >> e & 1u ? f[e] : -INFINITY;
+      *p0 = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+      *p1 = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+      if (later || greedy) {
+#pragma unroll
+        for (int e = 0; e < kRun; ++e)
+          if (!(later >> e & 1u)) take(f[e], id + e);
+      } else {
+        top = fmaxf(fmaxf(fmaxf(top, fmaxf(f[0], f[1])), fmaxf(f[2], f[3])), fmaxf(fmaxf(f[4], f[5]), fmaxf(f[6], f[7])));  // (not of NaN)
       }
-      *reinterpret_cast<float4*>(word + w) = make_float4(f[0], f[1], f[2], f[3]);
-      *reinterpret_cast<float4*>(word + w + 4) = make_float4(f[4], f[5], f[6], f[7]);
     }
   }
   float* const val = reinterpret_cast<float*>(word);
@@ -234,15 +251,15 @@ __global__ void __launch_bounds__(kThreads, kBlocks) logits_kernel(const LogitsA
       const unsigned kept = __ballot_sync(full, mine);
       if (lane == 0) sh_kept[warp] = __popc(kept);
       __syncthreads();
-      int at = __popc(kept & ((1u << lane) - 1u)), all = 0;
+      int place = __popc(kept & ((1u << lane) - 1u)), all = 0;
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) at += sh_kept[i];
+        if (i < warp) place += sh_kept[i];
         all += sh_kept[i];
       }
       if (mine) {
-        sh_id[at] = id - base;
-        sh_bias[at] = a.bias_value[e];
+        sh_id[place] = id - base;
+        sh_bias[place] = a.bias_value[e];
       }
       __syncthreads();
       if (warp == 0) {
@@ -252,13 +269,15 @@ __global__ void __launch_bounds__(kThreads, kBlocks) logits_kernel(const LogitsA
           const int w = on ? sh_id[i0 + lane] : -1 - lane;
           const float v = on ? sh_bias[i0 + lane] : 0.0f;
           const unsigned same = __match_any_sync(full, w);
-          const int count = __popc(same), most = __reduce_max_sync(full, count);
-          float sum = on ? val[w] : 0.0f;
+          const int most = __reduce_max_sync(full, __popc(same));
+          float sum = on ? val[at(w)] : 0.0f;
+          unsigned rest = same;
           for (int j = 0; j < most; ++j) {
-            const float add = __shfl_sync(full, v, j < count ? static_cast<int>(__fns(same, 0, j + 1)) : lane);
-            if (j < count) sum += add;
+            const float add = __shfl_sync(full, v, rest ? __ffs(rest) - 1 : lane);
+            if (rest) sum += add;
+            rest &= rest - 1u;
           }
-          if (on && lane == __ffs(same) - 1) val[w] = sum;
+          if (on && lane == __ffs(same) - 1) val[at(w)] = sum;
           __syncwarp();
         }
       }
@@ -267,20 +286,22 @@ __global__ void __launch_bounds__(kThreads, kBlocks) logits_kernel(const LogitsA
     // (entries of one id look at the same value)
     for (long long e = bias_lo + threadIdx.x; e < bias_hi; e += kThreads) {
       const int id = a.bias_id[e];
-      if (holds(id) && val[id - base] == val[id - base]) take(val[id - base], id);
+      if (holds(id) && val[at(id - base)] == val[at(id - base)]) take(val[at(id - base)], id);
     }
   }
 
   const bool wide = ((reinterpret_cast<uintptr_t>(out) - off * sizeof(OUT)) & 15u) == 0;
   // the words, times `scale`, to the row: 16 bytes a lane where its alignment goes with the logits', else neighbouring values by neighbouring lanes
-  auto write = [&](auto result) {
+  auto write = [&](auto result) {  // result(word, its id)
     if (wide) {
       constexpr int OV = 16 / sizeof(OUT);
       for (int w = threadIdx.x * kRun; w < words; w += kStride) {
         const int id = base + w;
+        const float4 v0 = *reinterpret_cast<const float4*>(val + (w >> 1)), v1 = *reinterpret_cast<const float4*>(val + plane + (w >> 1));
+        const float v[kRun] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
         OUT y[kRun];
 #pragma unroll
-        for (int e = 0; e < kRun; ++e) y[e] = rounded<OUT>(result(w + e));
+        for (int e = 0; e < kRun; ++e) y[e] = rounded<OUT>(result(v[e], id + e));
         if (id >= 0 && w + kRun <= words) {
 #pragma unroll
           for (int i = 0; i < kRun; i += OV) __stcs(reinterpret_cast<uint4*>(out + id + i), *reinterpret_cast<const uint4*>(y + i));
@@ -291,13 +312,13 @@ __global__ void __launch_bounds__(kThreads, kBlocks) logits_kernel(const LogitsA
         }
       }
     } else {
-      for (int w = threadIdx.x + max(0, -base); w < words; w += kThreads) out[base + w] = rounded<OUT>(result(w));
+      for (int w = threadIdx.x + max(0, -base); w < words; w += kThreads) out[base + w] = rounded<OUT>(result(val[at(w)], base + w));
     }
   };
   if (!a.probs) {
     __syncthreads();
-    write([&](int w) {
-      const float y = val[w] == val[w] ? val[w] : -INFINITY;
+    write([&](float y, int) {
+      if (y != y) y = -INFINITY;
       return temp > 0.0f ? __fdiv_rn(y, temp) : y;
     });
     if (parts > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
@@ -327,18 +348,35 @@ __global__ void __launch_bounds__(kThreads, kBlocks) logits_kernel(const LogitsA
     return y == most ? 1.0f : d > -INFINITY ? expf(d * cool) : 0.0f;
   };
   if (temp > 0.0f && top > -INFINITY) {
+    // by the hardware's power of two, of the difference from the maximum: a value of e^x is off by 2^-23 (1 + |x|) of
+    // itself, and what has large |x| is small.  (Of NaN the maximum takes 0.)
+    const float by = cool * 1.4426950408889634f;
+    const bool plain = top < INFINITY && by > 0.0f && by < INFINITY;
+    auto power = [&](float y) {
+      float e;
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"((y - top) * by));
+      return fmaxf(e, 0.0f);
+    };
+    float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int w = threadIdx.x * kRun; w < words; w += kStride) {
-      float f[kRun];
-      *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(val + w);
-      *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(val + w + 4);
-#pragma unroll
-      for (int e = 0; e < kRun; ++e) {
-        f[e] = weight(f[e], top);
-        sum += f[e];
+      float4* const q0 = reinterpret_cast<float4*>(val + (w >> 1));
+      float4* const q1 = reinterpret_cast<float4*>(val + plane + (w >> 1));
+      float4 f = *q0, g = *q1;
+      if (plain) {
+        f = make_float4(power(f.x), power(f.y), power(f.z), power(f.w));
+        g = make_float4(power(g.x), power(g.y), power(g.z), power(g.w));
+      } else {
+        f = make_float4(weight(f.x, top), weight(f.y, top), weight(f.z, top), weight(f.w, top));
+        g = make_float4(weight(g.x, top), weight(g.y, top), weight(g.z, top), weight(g.w, top));
       }
-      *reinterpret_cast<float4*>(val + w) = make_float4(f[0], f[1], f[2], f[3]);
-      *reinterpret_cast<float4*>(val + w + 4) = make_float4(f[4], f[5], f[6], f[7]);
+      s4[0] += f.x + g.x;
+      s4[1] += f.y + g.y;
+      s4[2] += f.z + g.z;
+      s4[3] += f.w + g.w;
+      *q0 = f;
+      *q1 = g;
     }
+    sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(full, sum, o);
   }
@@ -367,11 +405,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) logits_kernel(const LogitsA
   if (temp > 0.0f) {
     // (a block whose values are all -inf has them in the words still)
     const float scale = top > -INFINITY && sum > 0.0f ? weight(top, most) * __fdiv_rn(1.0f, sum) : 0.0f;
-    if (scale > 0.0f) write([&](int w) { return val[w] * scale; });
-    else write([&](int) { return 0.0f; });
+    if (scale > 0.0f) write([&](float y, int) { return y * scale; });
+    else write([&](float, int) { return 0.0f; });
   } else {
     const int best = key ? static_cast<int>(0xffffffffu - static_cast<uint32_t>(key)) : -1;
-    write([&](int w) { return base + w == best ? 1.0f : 0.0f; });
+    write([&](float, int id) { return id == best ? 1.0f : 0.0f; });
   }
 }
 
