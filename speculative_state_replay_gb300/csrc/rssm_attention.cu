@@ -31,7 +31,7 @@ namespace {
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kSlice = 16;              // tokens of a warp's step
 constexpr int kTile = kWarps * kSlice;  // tokens of a unit of work
-constexpr int kBlocks = 2;              // an SM
+constexpr int kBlocks = 3;              // an SM, at most
 constexpr int kMaxSms = 512;
 constexpr float kShift = 14.0f;         // fp16 weights are times 2^14
 
@@ -71,13 +71,17 @@ struct Shape {
   static constexpr int NC = RB / 16;       // and its 16-byte chunks
   static constexpr int NL = NC / 4;        // chunks a lane takes of a key
   static constexpr int QS = D * 2 + (Q8 ? 16 : 64);  // bytes between queries: a quarter of a warp's reads fall on distinct banks
+  // blocks an SM: 8-bit codes are bound by instructions, and eight warps issue in half of the cycles only (64 rows of 8192
+  // tokens, heads of 128, e4m3: two blocks 234 us, three 225; of 64: 187, 150); bf16 keys of 128 are bound by bytes, and three
+  // stages in flight of two blocks are worth more than two of three (332 us, 341)
+  static constexpr int kSm = MT == 1 && D * ESZ <= 128 ? 3 : 2;
   static constexpr int STAGES = Q8 && D < 256 ? 4 : 3;
   static constexpr int SB = 2 * kSlice * RB + (Q8 ? 2 * kSlice * 4 : 0);  // bytes of a stage: keys, values, their scales
   static constexpr int OS = D + (Q8 ? 16 : 8);      // floats between rows where the warps' sums meet
   static constexpr int kStageBytes = kWarps * STAGES * SB;
   static constexpr int kMeetBytes = kWarps * kRows * (OS + 2) * 4;
   static constexpr int kSmem = kRows * QS + (kStageBytes > kMeetBytes ? kStageBytes : kMeetBytes);
-  static constexpr int kGrid = 2 * (kSmem + 2048) <= 227 * 1024 ? 2 : 1;  // blocks an SM
+  static constexpr int kGrid = kSm * (kSmem + 2560) <= 227 * 1024 ? kSm : 2 * (kSmem + 2560) <= 227 * 1024 ? 2 : 1;
 };
 
 // where chunk `ch` of a slice's row lies: eight rows' equal chunks on distinct banks, and
@@ -89,7 +93,7 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int ch) {
 }
 
 template <typename S>
-__global__ void __launch_bounds__(kThreads, kBlocks) attention_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, S::kSm) attention_kernel(const __grid_constant__ AttnArgs a) {
   constexpr int D = S::D, MT = S::MT, kRows = S::kRows, NL = S::NL, RB = S::RB, NC = S::NC, QS = S::QS, OS = S::OS;
   constexpr bool Q8 = S::Q8;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -104,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attention_kernel(const __gr
   pdl_wait();
   pdl_trigger();
 
-  const Line line = cut_line<kRows, kTile, kThreads>(a);
+  const Line line = cut_line<kRows, kTile, kThreads>(a, blockIdx.x, gridDim.x);
   __shared__ Joint sh_joint[2];
   int joints = 0;
   constexpr float kUnit = Q8 ? kShift8 : 1.0f;
@@ -492,11 +496,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) attention_kernel(const __gr
     ++joints;
   }
   __syncthreads();
+  if (a.apart) return;
   for (int i = 0; i < joints; ++i) join_pieces<kRows, D, kThreads, 8>(a, sh_joint[i], line.share, kUnit);
 }
 
 template <typename S>
-cudaError_t run(const AttnArgs& a, int sms, cudaStream_t st) {
+cudaError_t run(const AttnArgs& args, int sms, cudaStream_t st) {
   static bool ready[64] = {};  // per device: the attribute is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -506,7 +511,12 @@ cudaError_t run(const AttnArgs& a, int sms, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev] = true;
   }
-  return launch_pdl(attention_kernel<S>, dim3(S::kGrid * sms), dim3(kThreads), S::kSmem, st, a);
+  AttnArgs a = args;
+  const int grid = S::kGrid * sms;
+  a.apart = static_cast<long long>(a.r.T) * a.group > 8;
+  e = launch_pdl(attention_kernel<S>, dim3(grid), dim3(kThreads), S::kSmem, st, a);
+  if (e != cudaSuccess || !a.apart) return e;
+  return launch_join<S::kRows, kTile, S::D>(a, grid, S::Q8 ? kShift8 : 1.0f, st);
 }
 
 template <int D, int FMT>
@@ -523,7 +533,7 @@ cudaError_t run_format(const AttnArgs& a, int sms, cudaStream_t st) {
                               : run_rows<D, RSSM_E4M3>(a, sms, st);
 }
 
-constexpr size_t kHead = 4096;  // bytes of tickets before the pieces
+constexpr size_t kHead = 8192;  // bytes of tickets before the pieces
 size_t scratch_need(const KvView& c, int sms) {
   const int rows = c.dim == 256 ? 16 : 32;
   const size_t narrow = static_cast<size_t>(kBlocks) * sms * 2 * rows * (c.dim + 2) * sizeof(float), wide = wide_scratch(c, sms);

@@ -3,7 +3,7 @@
 //
 // The queries of a (row, key head) are its new tokens times the heads of its group,
 // `group` consecutive ones a token.  A segment is a tile of them over all of the
-// row's tokens; a unit is a segment's part of one tile of tokens.
+// row's tokens, tile by tile; work is measured in units.
 #pragma once
 
 #include "rssm_kv.cuh"
@@ -24,6 +24,7 @@ struct AttnArgs {
   float scale2;  // scale log2(e)
   int whole;     // a block takes one segment, the longest first, instead of an equal part of the line
   int box;           // tokens of one copy (the kernel for many queries)
+  int apart;         // shared segments are joined by a launch of its own
   unsigned* ticket;  // [blocks]
   float* partial;    // [blocks][2][rows of a tile x (head_dim + 2)]
 };
@@ -114,13 +115,34 @@ struct RowWork {
   int len;    // committed tokens; < 0: nothing to see, zeros (-2: past the page table)
   int tiles;  // of tokens
   int mtiles; // of queries
+  int cost;   // of a tile of tokens, in units
+  int seg;    // units of a segment
+  long long units;  // of the row
 };
+
+// What a segment costs, in units: a tile of tokens, and what is done once.  The kernel for few queries: a tile is a unit.
+// The one for many: a tile of tokens costs about 5000 cycles where both query tiles have queries of their own (3 units),
+// 3500 where they share them (2), and a segment's queries and sums 20000 (16 ragged trees over int8: 204 us with equal
+// tiles, 159 so).  A part is at least what a tile costs, so that none between a segment's first tile and its end is
+// without one.
+template <int kRows>
+constexpr int kOnce = kRows > 32 ? 12 : 0;
+template <int kRows>
+constexpr int kLeast = kRows > 32 ? 4 : 1;
+// the tiles of tokens that begin before unit `at` of a segment
+template <int kRows>
+__device__ __forceinline__ int tiles_before(const RowWork& w, int at) {
+  return at <= kOnce<kRows> ? 0 : (at - kOnce<kRows>) / w.cost;
+}
 
 template <int kRows, int kTile>
 __device__ __forceinline__ RowWork row_work(const AttnArgs& a, int b) {
   RowWork w;
   w.s = row_span(a.r, b);
   w.tiles = w.mtiles = 0;
+  w.cost = kRows > 32 ? 2 : 1;
+  w.seg = 0;
+  w.units = 0;
   w.len = -1;
   if (w.s.count <= 0) return w;
   w.len = a.r.lengths[b];
@@ -131,17 +153,20 @@ __device__ __forceinline__ RowWork row_work(const AttnArgs& a, int b) {
     if (end > min(static_cast<long long>(a.r.max_pages) * a.c.page_size, 0x7fffff00ll)) w.len = -2;
     else w.tiles = static_cast<int>((end + kTile - 1) / kTile);
   }
+  if (kRows > 32 && static_cast<long long>(w.s.count) * a.group > kRows / 2) w.cost = 3;
+  w.seg = kOnce<kRows> + w.tiles * w.cost;
+  w.units = static_cast<long long>(w.seg) * w.mtiles * a.c.heads;
   return w;
 }
 
-// A block's part of the line of all units, ordered by row, query tile, head and token tile: units lo .. hi of
-// `share` a block, which begin in row b, whose units begin at `base`.  All threads of the block call it.
+// Part `block` of `blocks` of the line of all units, ordered by row, query tile, head and token tile: units lo .. hi of
+// `share` a part, which begin in row b, whose units begin at `base`.  All threads of the block call it.
 struct Line {
   long long lo, hi, share, base;
   int b;
 };
 template <int kRows, int kTile, int kThreads>
-__device__ __forceinline__ Line cut_line(const AttnArgs& a) {
+__device__ __forceinline__ Line cut_line(const AttnArgs& a, int block, int blocks) {
   constexpr int kWarps = kThreads / 32;
   __shared__ long long scan[kWarps], sh_base;
   __shared__ int sh_row;
@@ -151,8 +176,8 @@ __device__ __forceinline__ Line cut_line(const AttnArgs& a) {
   long long sum = 0;
   for (int i = r0; i < r1; ++i) {
     const RowWork w = row_work<kRows, kTile>(a, i);
-    sum += static_cast<long long>(w.tiles) * w.mtiles * a.c.heads;
-    if (blockIdx.x == 0) {
+    sum += w.units;
+    if (block == 0) {
       if (w.s.count < 0) set_error(a.c.err, RSSM_ERRBIT_SEQLEN);
       if (w.len == -2) set_error(a.c.err, RSSM_ERRBIT_PAGE);
     }
@@ -172,17 +197,16 @@ __device__ __forceinline__ Line cut_line(const AttnArgs& a) {
     total += scan[x];
   }
   Line l;
-  l.share = (total + gridDim.x - 1) / gridDim.x;
-  l.lo = l.share * blockIdx.x;
+  l.share = max(static_cast<long long>(kLeast<kRows>), (total + blocks - 1) / blocks);
+  l.lo = l.share * block;
   l.hi = min(total, l.lo + l.share);
   long long at = upto - sum;
   if (l.lo < l.hi && l.lo >= at && l.lo < upto) {
     int i = r0;
     for (; i < r1; ++i) {
       const RowWork w = row_work<kRows, kTile>(a, i);
-      const long long n = static_cast<long long>(w.tiles) * w.mtiles * a.c.heads;
-      if (l.lo < at + n) break;
-      at += n;
+      if (l.lo < at + w.units) break;
+      at += w.units;
     }
     sh_row = i;
     sh_base = at;
@@ -220,18 +244,61 @@ __device__ __forceinline__ void write_out(const AttnArgs& a, long long first, in
       make_uint2(bf16_pair(y[0] * inv, y[1] * inv), bf16_pair(y[2] * inv, y[3] * inv));
 }
 
-// A segment that several blocks share: each leaves its sums, and whoever leaves the last joins them, in the
-// segment's order.  A piece is kRows x D sums, then the rows' maxima and the rows' sums of weights; a block has two
+// A segment that several blocks share: each leaves its sums, and they are joined in the segment's order.  A piece is kRows x D sums, then the rows' maxima and the rows' sums of weights; a block has two
 // places, for a segment that began before it and for one that goes on after it.
 template <int kRows, int D>
 __device__ __forceinline__ float* piece_place(const AttnArgs& a, int block, bool begins) {
   return a.partial + (static_cast<long long>(block) * 2 + begins) * (kRows * (D + 2));
 }
+// where row r's columns from x4 on are in a piece: a tile of few rows has them one after another, one of many by four
+// columns (there a thread has a row, and a warp writes 512 bytes that neighbour)
+template <int kRows, int D>
+__device__ __forceinline__ int piece_at(int r, int x4) {
+  return kRows > 32 ? x4 * kRows + r * 4 : r * D + x4;
+}
+// The joined sums of a row's four columns.
+struct JoinSum {
+  float y[4] = {0.0f, 0.0f, 0.0f, 0.0f}, z = 0.0f, top = -INFINITY;
+  __device__ __forceinline__ void add(const float4& v, float m, float l) {
+    const float now = fmaxf(top, m), ref = now == -INFINITY ? 0.0f : now;
+    const float f = exp2_fast(top - ref), g = exp2_fast(m - ref);
+    top = now;
+    y[0] = y[0] * f + v.x * g;
+    y[1] = y[1] * f + v.y * g;
+    y[2] = y[2] * f + v.z * g;
+    y[3] = y[3] * f + v.w * g;
+    z = z * f + l * g;
+  }
+};
+// of row r's columns from x4 on, with the loads of kDeep pieces on their way at a time
+template <int kRows, int D, int kDeep>
+__device__ __forceinline__ JoinSum join_row(const AttnArgs& a, int first, int pieces, int r, int x4) {
+  JoinSum s;
+#pragma unroll 1
+  for (int x0 = 0; x0 < pieces; x0 += kDeep) {
+    float4 v[kDeep];
+    float m[kDeep], l[kDeep];
+#pragma unroll
+    for (int e = 0; e < kDeep; ++e)
+      if (x0 + e < pieces) {
+        const float* p = piece_place<kRows, D>(a, first + x0 + e, x0 + e == 0);
+        m[e] = __ldcg(p + kRows * D + r);
+        l[e] = __ldcg(p + kRows * D + kRows + r);
+        v[e] = __ldcg(reinterpret_cast<const float4*>(p + piece_at<kRows, D>(r, x4)));
+      }
+#pragma unroll
+    for (int e = 0; e < kDeep; ++e)
+      if (x0 + e < pieces) s.add(v[e], m[e], l[e]);
+  }
+  return s;
+}
+
 struct Joint {  // a segment that a block has a piece of
   long long first_token, seg0;  // its row's first new token, its first unit
   int tiles, head, row0, rows;
 };
-// (after all of a block's pieces: in their loop it would take registers from it)
+// Whoever leaves a segment's last piece joins them.  (After all of a block's pieces: in their loop it would take
+// registers from it.)
 template <int kRows, int D, int kThreads, int kDeep>
 __device__ __forceinline__ void join_pieces(const AttnArgs& a, const Joint& j, long long share, float unit) {
   const long long first_token = j.first_token, seg0 = j.seg0;
@@ -248,67 +315,50 @@ __device__ __forceinline__ void join_pieces(const AttnArgs& a, const Joint& j, l
   if (!last) return;
   __threadfence();
   constexpr int D4 = D / 4;
-  struct Sum {
-    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f}, z = 0.0f, top = -INFINITY;
-    __device__ __forceinline__ void add(const float4& v, float m, float l) {
-      const float now = fmaxf(top, m), ref = now == -INFINITY ? 0.0f : now;
-      const float f = exp2_fast(top - ref), g = exp2_fast(m - ref);
-      top = now;
-      y[0] = y[0] * f + v.x * g;
-      y[1] = y[1] * f + v.y * g;
-      y[2] = y[2] * f + v.z * g;
-      y[3] = y[3] * f + v.w * g;
-      z = z * f + l * g;
-    }
-  };
-  auto write = [&](const Sum& s, int r, int x4) { write_out(a, first_token, head, row0 + r, D, x4, s.y, s.z == 0.0f ? 0.0f : unit / s.z); };
-  auto load = [&](const float* p, int r, int x4, float4& v, float& m, float& l) {
-    m = __ldcg(p + kRows * D + r);
-    l = __ldcg(p + kRows * D + kRows + r);
-    v = __ldcg(reinterpret_cast<const float4*>(p + r * D + x4));
-  };
-  // loads on their way at a time: of kDeep pieces where a thread has one output or two, else of four outputs
-  if (rows * D4 <= 2 * kThreads) {
 #pragma unroll 1
-    for (int i = threadIdx.x; i < rows * D4; i += kThreads) {
-      const int r = i / D4, x4 = (i - r * D4) * 4;
-      Sum s;
-#pragma unroll 1
-      for (int x0 = 0; x0 < pieces; x0 += kDeep) {
-        float4 v[kDeep];
-        float m[kDeep], l[kDeep];
-#pragma unroll
-        for (int e = 0; e < kDeep; ++e)
-          if (x0 + e < pieces) load(piece_place<kRows, D>(a, first + x0 + e, x0 + e == 0), r, x4, v[e], m[e], l[e]);
-#pragma unroll
-        for (int e = 0; e < kDeep; ++e)
-          if (x0 + e < pieces) s.add(v[e], m[e], l[e]);
-      }
-      write(s, r, x4);
-    }
-  } else {
-    constexpr int N = 4;
-#pragma unroll 1
-    for (int i0 = threadIdx.x; i0 < rows * D4; i0 += N * kThreads) {
-      Sum s[N];
-#pragma unroll 1
-      for (int x = 0; x < pieces; ++x) {
-        const float* p = piece_place<kRows, D>(a, first + x, x == 0);
-        float4 v[N];
-        float m[N], l[N];
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const int i = min(i0 + e * kThreads, rows * D4 - 1);
-          load(p, i / D4, i % D4 * 4, v[e], m[e], l[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < N; ++e) s[e].add(v[e], m[e], l[e]);
-      }
-#pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (i0 + e * kThreads < rows * D4) write(s[e], (i0 + e * kThreads) / D4, (i0 + e * kThreads) % D4 * 4);
-    }
+  for (int i = threadIdx.x; i < rows * D4; i += kThreads) {
+    const int r = i / D4, x4 = (i - r * D4) * 4;
+    const JoinSum s = join_row<kRows, D, kDeep>(a, first, pieces, r, x4);
+    write_out(a, first_token, head, row0 + r, D, x4, s.y, s.z == 0.0f ? 0.0f : unit / s.z);
   }
+}
+
+// The same by a launch of its own.  A piece has up to 256 x 128 sums, and where few segments meet many blocks, one block
+// that joined all of a segment's pieces would take longer than the pieces themselves (one row's tree of 64 over 4096
+// tokens, 8 heads, groups of 4: 152 us, and 59 so).  Block (x, y): rows 16 y .. of the segment, if any, that cut x of the
+// line is the first to go through.
+constexpr int kJoinRows = 16, kJoinThreads = 256;
+template <int kRows, int kTile, int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnArgs a, int blocks, float unit) {
+  pdl_wait();
+  pdl_trigger();
+  const int cut = blockIdx.x + 1;
+  const Line line = cut_line<kRows, kTile, kJoinThreads>(a, cut, blocks);
+  if (line.lo >= line.hi) return;
+  const RowWork w = row_work<kRows, kTile>(a, line.b);
+  const long long at = line.lo - line.base;
+  const int seg = static_cast<int>(at / w.seg), in = static_cast<int>(at - static_cast<long long>(seg) * w.seg);
+  // the first piece with a tile is of the part that unit `body` is in; this is the cut behind it, or there is nothing to do
+  const long long body = line.lo - in + kOnce<kRows> + w.cost - 1;
+  const int first = cut - 1, pieces = static_cast<int>((line.lo - in + w.seg - 1) / line.share) - first + 1;
+  if (body >= line.lo || body < line.lo - line.share) return;
+  const int mtile = seg / a.c.heads, head = seg - mtile * a.c.heads, row0 = mtile * kRows;
+  const int r0 = blockIdx.y * kJoinRows, rows = min(kJoinRows, min(kRows, w.s.count * a.group - row0) - r0);
+  constexpr int D4 = D / 4;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < kJoinRows * D4; i += kJoinThreads) {
+    // a warp: eight rows, four times four columns, which are 128 bytes that neighbour of a piece, 32 of a row's output
+    const int at = i / (8 * D4) * 8 + (i & 7), r = r0 + at, x4 = i / 8 % D4 * 4;
+    if (at >= rows) continue;
+    const JoinSum s = join_row<kRows, D, 8>(a, first, pieces, r, x4);
+    write_out(a, w.s.first, head, row0 + r, D, x4, s.y, s.z == 0.0f ? 0.0f : unit / s.z);
+  }
+}
+template <int kRows, int kTile, int D>
+cudaError_t launch_join(const AttnArgs& a, int blocks, float unit, cudaStream_t st) {
+  const long long most = static_cast<long long>(a.r.T) * a.group;
+  const int rows = static_cast<int>(most < kRows ? most : kRows);
+  return launch_pdl(join_kernel<kRows, kTile, D>, dim3(blocks - 1, (rows + kJoinRows - 1) / kJoinRows), dim3(kJoinThreads), 0, st, a, blocks, unit);
 }
 
 // host side: the kernel for many queries of a head (rssm_attention_wide.cu)

@@ -26,7 +26,7 @@ constexpr int kQ = 128;                 // queries of a tile: the product's rows
 constexpr int kTiles = 2;               // tiles of a block
 constexpr int kRows = kTiles * kQ;
 constexpr int kTok = 128;               // tokens of a step
-constexpr int kInfo = 4;                // places of what goes with a step of tokens: K of step j + 4 waits for a buffer that is
+constexpr int kInfo = 5;                // places of what goes with a step of tokens: K of step j + 5 waits for a buffer that is
                                         // free once the scores of j + 2 are made, which is after the weights of j
 constexpr float kLazy = 4.0f;           // log2 of how far the true maximum may be past the one in use
 constexpr float kShift = 11.0f;         // fp16 weights are times 2^11: 2^15 at most
@@ -45,21 +45,13 @@ struct Wait {  // a wait that gives up is for all of the block
   }
 };
 
-#ifndef PB
-#define PB 2
-#define LB 3
-#define P8 2
-#define L8 3
-#endif
-constexpr int kPartsOf(int f) { return f == RSSM_BF16 ? PB : P8; }
-constexpr int kLoadsOf(int f) { return f == RSSM_BF16 ? LB : L8; }
 template <int D_, int FMT_>
 struct Shape {
   static constexpr int D = D_, FMT = FMT_;
   static constexpr bool Q8 = FMT != RSSM_BF16;
-  static constexpr int kParts = kPartsOf(FMT_);    // threads of a query, each with a part of a step's tokens
+  static constexpr int kParts = 2;                // threads of a query, each with a part of a step's tokens
   static constexpr int kSoftWarps = 4 * kTiles * kParts, kSoft = kSoftWarps * 32;
-  static constexpr int kLoadWarps = kLoadsOf(FMT_);  // the first copies; 8-bit: the others convert, bf16: all look at tiles that not every query sees
+  static constexpr int kLoadWarps = 3;            // the first copies; 8-bit: the others convert, bf16: all look at tiles that not every query sees
   static constexpr int kWorkWarps = Q8 ? kLoadWarps - 1 : kLoadWarps, kWorkers = kWorkWarps * 32;
   static constexpr int kThreads = kSoft + kLoadWarps * 32 + 32;
   static constexpr int RB = D * (Q8 ? 1 : 2);     // bytes of a cached head
@@ -86,8 +78,8 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int
                "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
                : "memory");
 }
-// Products and their commits by one lane of a warp that runs as a whole: what they are made of then is the warp's, not a
-// thread's, and stays in uniform registers (by one thread in a branch of its own a product took 115 cycles to issue)
+// Products and their commits by one lane of a warp that runs as a whole: the descriptors are the warp's, and no branch
+// stands between two products
 __device__ __forceinline__ void mma_ss(bool mine, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, e;\n\t"
@@ -130,6 +122,27 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) 
 }
 __device__ __forceinline__ void tc_stw8(uint32_t addr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::S8(r, 0), "r"(addr) : "memory");
+}
+// 16 lanes by 64 columns as a fragment: registers 4 n, 4 n + 1 are columns 8 n + 2 (lane % 4), + 1 of lane / 4, the next two those
+// of lane / 4 + 8
+__device__ __forceinline__ void tc_ld64(uint32_t (&r)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,"
+      "%27,%28,%29,%30,%31}, [%32];"
+      : R8(r, 0), R8(r, 8), R8(r, 16), R8(r, 24)
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_ld16(uint32_t (&r)[8], uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : R8(r, 0) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tc_st16f(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::S8(r, 0), "r"(addr) : "memory");
+}
+// and 32 columns: register 2 n is column 4 n + lane % 4 of lane / 4, the next that of lane / 4 + 8
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x8.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::S8(r, 0), S8(r, 8), "r"(addr)
+               : "memory");
 }
 #undef R8
 #undef S8
@@ -177,7 +190,7 @@ struct Piece {
   long long first;                   // the row's first new token
   int row, len, count, head;         // the row, its committed and new tokens, the head
   int row0, rows;                    // the tile's queries
-  int t0, nt, t1, tiles;             // its steps of tokens: from t0 on nt that any query sees, of t1 - t0; of the segment's
+  int t0, nt, t1;                    // its steps of tokens: from t0 on nt that any query sees, of t1 - t0
   int end, some;                     // the last token seen by any of its queries; from `some` on not every query sees all
   int items, steps, used[2], done[2], number;  // how often things came round so far: the ring, steps, by tile scores and sums, pieces
   int fixed;                         // and tiles whose values were looked at
@@ -200,7 +213,8 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   __shared__ unsigned long long sh_mask[kTreeT];
   __shared__ float sh_back[kRows], sh_top[kTiles][kParts][kQ], sh_sum[kTiles][kParts][kQ], sh_ref[kTiles][kQ];
   __shared__ unsigned sh_valid[kInfo];
-  __shared__ Slice sh_slice[kLoadWarps][2][8];
+  constexpr int kFinders = Q8 ? 1 : kLoadWarps, kFound = Q8 ? 4 : 2;  // warps that look up where steps are; steps kept (8-bit: converted up to two steps behind the copies)
+  __shared__ Slice sh_slice[kFinders][kFound][8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned full = 0xffffffffu;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(sm + S::kBarsAt);
@@ -224,7 +238,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       mbar_init(b_p + i, kSoftWarps / kTiles);
       mbar_init(b_o + i, 1);
     }
-    for (int i = 0; i < kInfo; ++i) mbar_init(b_info + i, kWorkers);
+    for (int i = 0; i < kInfo; ++i) mbar_init(b_info + i, Q8 ? 32 : kWorkers);
     mbar_init(b_q, kSoft);
     fence_barrier_init();
     Piece& p = sh_piece;
@@ -259,37 +273,48 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       }
       line.base = 0;
       line.share = 1;
-      line.lo = mt < w.mtiles ? static_cast<long long>(mt * a.c.heads + x % a.c.heads) * w.tiles : 0;
-      line.hi = mt < w.mtiles ? line.lo + w.tiles : 0;
+      line.lo = mt < w.mtiles ? static_cast<long long>(mt * a.c.heads + x % a.c.heads) * w.seg : 0;
+      line.hi = mt < w.mtiles ? line.lo + w.seg : 0;
     } else {
-      line = cut_line<kRows, kTok, kThreads>(a);
+      line = cut_line<kRows, kTok, kThreads>(a, blockIdx.x, gridDim.x);
     }
     if (threadIdx.x == 0) sh_line = line;
   }
   bool ok = true;
-  __shared__ Joint sh_joint[2];
-  int joints = 0;
 
 #pragma unroll 1
   while (true) {
     __syncthreads();  // the last piece's shared memory is free
     if (warp == 0) {
-      // ---- the next piece, by the first warp: line.lo is the unit that it begins with
+      // ---- the next piece, by the first warp: line.lo is the unit that it begins at or before
       Piece& p = sh_piece;
       Line& line = sh_line;
       RowWork w;
       bool over = true;
-      while (line.lo < line.hi) {
-        w = row_work<kRows, kTok>(a, line.b);
-        const long long units = static_cast<long long>(w.tiles) * w.mtiles * a.c.heads;
-        over = line.lo >= line.base + units;
-        if (!over) break;
-        __syncwarp();
-        if (lane == 0) {
-          line.base += units;
-          ++line.b;
+      int seg = 0, t0 = 0, t1 = 0;
+      long long lo = line.lo, row_at = line.base;
+      int row = line.b;
+      while (lo < line.hi) {
+        w = row_work<kRows, kTok>(a, row);
+        if (lo >= row_at + w.units) {
+          row_at += w.units;
+          ++row;
+          continue;
         }
-        __syncwarp();
+        seg = static_cast<int>((lo - row_at) / w.seg);
+        const int in = static_cast<int>(lo - row_at - static_cast<long long>(seg) * w.seg);
+        const int to = static_cast<int>(min(static_cast<long long>(w.seg), in + (line.hi - lo)));
+        t0 = tiles_before<kRows>(w, in);
+        t1 = tiles_before<kRows>(w, to);
+        lo += to - in;
+        over = t0 == t1;  // (only what is done once: that is for who has the first tile)
+        if (!over) break;
+      }
+      __syncwarp();
+      if (lane == 0) {
+        line.lo = lo;
+        line.base = row_at;
+        line.b = row;
       }
       bool fine = true;
       if (!over && a.parents && w.len >= 0) {
@@ -311,16 +336,12 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         ++p.number;
         p.over = over;
         if (!over) {
-          const long long at = line.lo - line.base;
-          const int seg = static_cast<int>(at / w.tiles);
-          p.t0 = static_cast<int>(at - static_cast<long long>(seg) * w.tiles);
-          p.t1 = static_cast<int>(min(static_cast<long long>(w.tiles), p.t0 + (line.hi - line.lo)));
-          p.tiles = w.tiles;
-          p.whole = p.t0 == 0 && p.t1 == w.tiles;
-          line.lo += p.t1 - p.t0;
+          p.t0 = t0;
+          p.t1 = t1;
+          p.whole = t0 == 0 && t1 == w.tiles;
           const int mtile = seg / a.c.heads;
           p.head = seg - mtile * a.c.heads;
-          p.row = line.b;
+          p.row = row;
           p.first = w.s.first;
           p.len = w.len;
           p.count = w.s.count;
@@ -343,11 +364,11 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       const float scale2 = fmaxf(fabsf(a.scale2), 1e-30f);  // (times -inf it stays that)
       {
         const bool flip = a.scale2 < 0.0f;            // the maximum is taken before the scale
-        constexpr int G = D / 8, AT = 32 / G, N = 2;  // lanes of a row, rows of a warp; rows on their way at a time
+        constexpr int G = D / 8, AT = 32 / G, N = kRows / (kSoftWarps * AT);  // lanes of a row, rows of a warp; all rows on their way at a time
         const int row0 = p.row0, rows = p.rows, head = p.head;
         const long long first = p.first;
-#pragma unroll 1
-        for (int r0 = warp * AT; r0 < (p.alt ? kQ : kRows); r0 += N * kSoftWarps * AT) {
+        {
+          const int r0 = warp * AT;
           uint4 x[N];
 #pragma unroll
           for (int i = 0; i < N; ++i) {
@@ -377,139 +398,271 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       // ---- scores into weights: a warp's tile, half of a step's tokens, lanes of tensor memory; a thread's query in the tile
       const int tile = warp / (4 * kParts), half = (warp >> 2) % kParts, mine = (warp & 3) * 32 + lane;
       const bool alt = p.alt;
-      const int r = alt ? mine : tile * kQ + mine;
-      const int t = (p.row0 + min(r, p.rows - 1)) / a.group;
-      const unsigned long long path = a.parents ? sh_mask[t & 63] : 0ull;
-      const float back = Q8 ? sh_back[r] : scale2;
       const uint32_t s_at = tm + ((warp & 3) << 21) + tile * kTok + half * kPart;
       const int n0 = p.used[tile], nt = p.nt, len = p.len, some = p.some;
-      float ref = -INFINITY, sum = 0.0f;
       int n = n0, j = alt ? tile : 0, step = p.steps + j, pos = (p.t0 + j) * kTok + half * kPart;
-#pragma unroll 1
-      for (; j < nt; ++n) {
-        const int slot = step % kInfo;
-        ok = ok && wait(b_info + slot, (step / kInfo) & 1);
-        ok = __all_sync(full, ok && wait(b_s + tile, n & 1)) != 0;
-        if (!ok) break;
-        tc_after();
-        uint32_t x[kPart / 32][32];
-#pragma unroll
-        for (int c = 0; c < kPart / 32; ++c) tc_ld32(x[c], s_at + 32 * c);
-        const unsigned valid = sh_valid[slot] >> (8 / kParts * half);
-        const bool edge = pos + kPart > some || (valid & (0xffu >> (8 - 8 / kParts))) != 0xffu >> (8 - 8 / kParts);
-        const float* info = reinterpret_cast<const float*>(sm + S::kInfoAt) + slot * 3 * kTok + half * kPart;
-#pragma unroll
-        for (int c = 0; c < kPart / 32; ++c) landed(x[c]);
-        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < kPart / 32; ++c) {
-          uint32_t(&y)[32] = x[c];
-          if constexpr (Q8) {  // in units of log2, with their values' scales
-            const pair bb = pack2(back, back);
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(info + 32 * c + i), l4 = *reinterpret_cast<const ulonglong2*>(info + kTok + 32 * c + i);
-              scaled(y[i], y[i + 1], bb, k4.x, l4.x);
-              scaled(y[i + 2], y[i + 3], bb, k4.y, l4.y);
-            }
-          }
-          if (edge) {
-            // which of the 32 this query sees
-            const int j0 = pos + 32 * c - len;
-            uint32_t see;
-            if (a.parents) {
-              see = j0 <= -32 ? full : j0 < 0 ? static_cast<uint32_t>(path << -j0) | ((1u << -j0) - 1u) : j0 < 64 ? static_cast<uint32_t>(path >> j0) : 0u;
-            } else {
-              const int m = t - j0;  // the last one's place
-              see = m >= 31 ? full : m < 0 ? 0u : (2u << m) - 1u;
-            }
-            see &= (valid >> (2 * c) & 1u ? 0xffffu : 0u) | (valid >> (2 * c + 1) & 1u ? 0xffff0000u : 0u);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = see >> i & 1u ? y[i] : 0xff800000u;  // -inf
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) t4[i & 3] = fmaxf(t4[i & 3], __uint_as_float(y[i]));
-        }
-        float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-        if constexpr (!Q8) top = top == -INFINITY ? top : top * back;
-        if constexpr (kParts == 2) {
-          // the other half's; after this the other half's scores are in registers too, and P may take their place
-          sh_top[tile][half][mine] = top;
-          tc_before();
-          pair_sync(warp & 3 | tile << 2);
-          tc_after();
-          top = fmaxf(top, sh_top[tile][half ^ 1][mine]);
-        }
-        // the maximum in use follows where it has to; the products before this step's are done (its scores came after them)
-        if (__any_sync(full, top > ref + kLazy)) {
-          const float now = fmaxf(ref, top);
-          const float f = now == -INFINITY ? 1.0f : exp2_fast(ref - now);
-          ref = now;
-          sum *= f;
-          if (n > n0) {
-            const uint32_t o_at = tm + ((warp & 3) << 21) + kTiles * kTok + tile * D + half * (D / kParts);
-#pragma unroll 1
-            for (int c = 0; c < D / (8 * kParts); ++c) {
-              uint32_t y[8];
-              tc_ld8(y, o_at + 8 * c);
-              tc_wait_ld();
-              tc_landed(y);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
-              tc_stw8(o_at + 8 * c, y);
-            }
-          }
-        }
-        const float lift = (Q8 ? kShift : 0.0f) - (ref == -INFINITY ? 0.0f : ref);
-        const pair lift2 = pack2(lift, lift), scale22 = pack2(back, back);
-        pair s2[2] = {0ull, 0ull};
-#pragma unroll
-        for (int c = 0; c < kPart / 32; ++c) {
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            ulonglong2 v4;
-            if constexpr (Q8) v4 = *reinterpret_cast<const ulonglong2*>(info + 2 * kTok + 32 * c + i);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              pair y = pack2(__uint_as_float(x[c][i + 2 * e]), __uint_as_float(x[c][i + 2 * e + 1]));
-              if constexpr (Q8) add2(y, lift2);
-              else y = fma2v(y, scale22, lift2);
-              float y0, y1;
-              unpack2(y, y0, y1);
-              y0 = exp2_fast(y0);
-              y1 = exp2_fast(y1);
-              const pair p2 = pack2(y0, y1);
-              if constexpr (Q8) {
-                fma2(s2[e], p2, e ? v4.y : v4.x);
-                w[i / 2 + e] = f16_pair(y0, y1);
-              } else {
-                add2(s2[e], p2);
-                w[i / 2 + e] = bf16_pair(y0, y1);
-              }
-            }
-          }
-          tc_st16(s_at - half * (kPart / 2) + 16 * c, w);
-        }
-        add2(s2[0], s2[1]);
-        float u0, u1;
-        unpack2(s2[0], u0, u1);
-        sum += u0 + u1;
-        tc_wait_st();
-        tc_before();
+      // lanes without queries only keep step: what the products make of their lanes goes nowhere
+      const bool idle = (alt ? 0 : tile * kQ) + (warp & 3) * 32 >= p.rows;
+      auto pass = [&] {
         __syncwarp();
         if (lane == 0) mbar_arrive(b_p + tile);
         const int by = alt ? 2 : 1;
         j += by;
         step += by;
         pos += by * kTok;
+      };
+      if constexpr (!Q8) {
+        const int r = alt ? mine : tile * kQ + mine;
+        const int t = (p.row0 + min(r, p.rows - 1)) / a.group;
+        const unsigned long long path = a.parents ? sh_mask[t & 63] : 0ull;
+        float ref = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+        for (; j < nt; ++n) {
+          const int slot = step % kInfo;
+          ok = ok && wait(b_info + slot, (step / kInfo) & 1);
+          ok = __all_sync(full, ok && wait(b_s + tile, n & 1)) != 0;
+          if (!ok) break;
+          tc_after();
+          if (idle) {
+            pass();
+            continue;
+          }
+          uint32_t x[kPart / 32][32];
+#pragma unroll
+          for (int c = 0; c < kPart / 32; ++c) tc_ld32(x[c], s_at + 32 * c);
+          const unsigned valid = sh_valid[slot] >> (8 / kParts * half);
+          const bool edge = pos + kPart > some || (valid & (0xffu >> (8 - 8 / kParts))) != 0xffu >> (8 - 8 / kParts);
+#pragma unroll
+          for (int c = 0; c < kPart / 32; ++c) landed(x[c]);
+          float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < kPart / 32; ++c) {
+            uint32_t(&y)[32] = x[c];
+            if (edge) {
+              // which of the 32 this query sees
+              const int j0 = pos + 32 * c - len;
+              uint32_t see;
+              if (a.parents) {
+                see = j0 <= -32 ? full : j0 < 0 ? static_cast<uint32_t>(path << -j0) | ((1u << -j0) - 1u) : j0 < 64 ? static_cast<uint32_t>(path >> j0) : 0u;
+              } else {
+                const int m = t - j0;  // the last one's place
+                see = m >= 31 ? full : m < 0 ? 0u : (2u << m) - 1u;
+              }
+              see &= (valid >> (2 * c) & 1u ? 0xffffu : 0u) | (valid >> (2 * c + 1) & 1u ? 0xffff0000u : 0u);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) y[i] = see >> i & 1u ? y[i] : 0xff800000u;  // -inf
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) t4[i & 3] = fmaxf(t4[i & 3], __uint_as_float(y[i]));
+          }
+          float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+          top = top == -INFINITY ? top : top * scale2;
+          // the other half's; after this the other half's scores are in registers too, and P may take their place
+          sh_top[tile][half][mine] = top;
+          tc_before();
+          pair_sync(warp & 3 | tile << 2);
+          tc_after();
+          top = fmaxf(top, sh_top[tile][half ^ 1][mine]);
+          // the maximum in use follows where it has to; the products before this step's are done (its scores came after them)
+          if (__any_sync(full, top > ref + kLazy)) {
+            const float now = fmaxf(ref, top);
+            const float f = now == -INFINITY ? 1.0f : exp2_fast(ref - now);
+            ref = now;
+            sum *= f;
+            if (n > n0) {
+              const uint32_t o_at = tm + ((warp & 3) << 21) + kTiles * kTok + tile * D + half * (D / kParts);
+#pragma unroll 1
+              for (int c = 0; c < D / (8 * kParts); ++c) {
+                uint32_t y[8];
+                tc_ld8(y, o_at + 8 * c);
+                tc_wait_ld();
+                tc_landed(y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+                tc_stw8(o_at + 8 * c, y);
+              }
+            }
+          }
+          const float lift = ref == -INFINITY ? 0.0f : -ref;
+          const pair lift2 = pack2(lift, lift), scale22 = pack2(scale2, scale2);
+          pair s2[2] = {0ull, 0ull};
+#pragma unroll
+          for (int c = 0; c < kPart / 32; ++c) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                pair y = pack2(__uint_as_float(x[c][i + 2 * e]), __uint_as_float(x[c][i + 2 * e + 1]));
+                y = fma2v(y, scale22, lift2);
+                float y0, y1;
+                unpack2(y, y0, y1);
+                y0 = exp2_fast(y0);
+                y1 = exp2_fast(y1);
+                add2(s2[e], pack2(y0, y1));
+                w[i / 2 + e] = bf16_pair(y0, y1);
+              }
+            }
+            tc_st16(s_at - half * (kPart / 2) + 16 * c, w);
+          }
+          add2(s2[0], s2[1]);
+          float u0, u1;
+          unpack2(s2[0], u0, u1);
+          sum += u0 + u1;
+          tc_wait_st();
+          tc_before();
+          pass();
+        }
+        sh_sum[tile][half][mine] = sum;
+        if (half == 0) sh_ref[tile][mine] = ref;
+      } else {
+        // A thread has a quarter of the half's tokens, of four queries: what goes with a token is read from shared memory once
+        // for the four (a query a thread would read 12 bytes for every score, 3100 cycles of shared memory a step of 256 queries)
+        const int g = lane >> 2, c2 = 2 * (lane & 3), r0 = (warp & 3) * 32 + g;  // queries r0 + 8 i
+        float back[4], ref[4];
+        pair s2[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          back[i] = sh_back[(alt ? 0 : tile * kQ) + r0 + 8 * i];
+          ref[i] = -INFINITY;
+          s2[i] = 0ull;
+        }
+#pragma unroll 1
+        for (; j < nt; ++n) {
+          const int slot = step % kInfo;
+          ok = ok && wait(b_info + slot, (step / kInfo) & 1);
+          ok = __all_sync(full, ok && wait(b_s + tile, n & 1)) != 0;
+          if (!ok) break;
+          tc_after();
+          if (idle) {
+            pass();
+            continue;
+          }
+          uint32_t x[2][32];  // of query i token 8 y + c2 + e: [i / 2][4 y + 2 (i % 2) + e]
+          tc_ld64(x[0], s_at);
+          tc_ld64(x[1], s_at + (16u << 16));
+          const unsigned valid = sh_valid[slot] >> (4 * half);
+          const bool edge = pos + kPart > some || (valid & 0xfu) != 0xfu;
+          const float* info = reinterpret_cast<const float*>(sm + S::kInfoAt) + slot * 3 * kTok + half * kPart + c2;
+          landed(x[0]);
+          landed(x[1]);
+          // in units of log2, with their values' scales
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const pair k2 = *reinterpret_cast<const pair*>(info + 8 * y), l2 = *reinterpret_cast<const pair*>(info + kTok + 8 * y);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) scaled(x[i / 2][4 * y + 2 * (i & 1)], x[i / 2][4 * y + 2 * (i & 1) + 1], pack2(back[i], back[i]), k2, l2);
+          }
+          if (edge) {
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              const int t = (p.row0 + min((alt ? 0 : tile * kQ) + r0 + 8 * i, p.rows - 1)) / a.group;
+              const unsigned long long path = a.parents ? sh_mask[t & 63] : 0ull;
+              uint32_t see = 0u;
+#pragma unroll
+              for (int y = 0; y < 16; ++y) {
+                const int q = pos + 8 * (y >> 1) + c2 + (y & 1) - len;  // which new token this is
+                const bool seen = (valid >> (y >> 2) & 1u) && (q < 0 || (a.parents ? q < 64 && (path >> (q & 63) & 1) : q <= t));
+                see |= seen ? 1u << y : 0u;
+              }
+              // (i is not known to the compiler, and registers have no index)
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                if (z == i) {
+#pragma unroll
+                  for (int y = 0; y < 16; ++y) {
+                    uint32_t& v = x[z / 2][4 * (y >> 1) + 2 * (z & 1) + (y & 1)];
+                    v = see >> y & 1u ? v : 0xff800000u;  // -inf
+                  }
+                }
+            }
+          }
+          float top[4];
+          bool up = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float t2[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int y = 0; y < 16; ++y) t2[y & 1] = fmaxf(t2[y & 1], __uint_as_float(x[i / 2][4 * (y >> 1) + 2 * (i & 1) + (y & 1)]));
+            top[i] = fmaxf(t2[0], t2[1]);
+            top[i] = fmaxf(top[i], __shfl_xor_sync(full, top[i], 1));
+            top[i] = fmaxf(top[i], __shfl_xor_sync(full, top[i], 2));
+            if ((lane & 3) == 0) sh_top[tile][half][r0 + 8 * i] = top[i];
+          }
+          // the other half's; after this the other half's scores are in registers too, and P may take their place
+          tc_before();
+          pair_sync(warp & 3 | tile << 2);
+          tc_after();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            top[i] = fmaxf(top[i], sh_top[tile][half ^ 1][r0 + 8 * i]);
+            up = up || top[i] > ref[i] + kLazy;
+          }
+          // the maximum in use follows where it has to; the products before this step's are done (its scores came after them)
+          if (__any_sync(full, up)) {
+            float f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float now = fmaxf(ref[i], top[i]);
+              f[i] = now == -INFINITY ? 1.0f : exp2_fast(ref[i] - now);
+              ref[i] = now;
+              s2[i] = fma2v(s2[i], pack2(f[i], f[i]), 0ull);
+            }
+            if (n > n0) {
+              const uint32_t o_at = tm + ((warp & 3) << 21) + kTiles * kTok + tile * D + half * (D / kParts);
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll 1
+                for (int c = 0; c < D / (16 * kParts); ++c) {
+                  uint32_t y[8];
+                  const uint32_t at = o_at + (static_cast<uint32_t>(16 * h) << 16) + 16 * c;
+                  tc_ld16(y, at);
+                  tc_wait_ld();
+                  tc_landed(y);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f[2 * h + (i >> 1 & 1)]);
+                  tc_st16f(at, y);
+                }
+            }
+          }
+          float lift[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) lift[i] = kShift - (ref[i] == -INFINITY ? 0.0f : ref[i]);
+          uint32_t w[2][16];
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const pair v2 = *reinterpret_cast<const pair*>(info + 2 * kTok + 8 * y);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float y0 = exp2_fast(__uint_as_float(x[i / 2][4 * y + 2 * (i & 1)]) + lift[i]);
+              const float y1 = exp2_fast(__uint_as_float(x[i / 2][4 * y + 2 * (i & 1) + 1]) + lift[i]);
+              fma2(s2[i], pack2(y0, y1), v2);
+              w[i / 2][2 * y + (i & 1)] = f16_pair(y0, y1);
+            }
+          }
+          tc_st32(s_at - half * (kPart / 2), w[0]);
+          tc_st32(s_at - half * (kPart / 2) + (16u << 16), w[1]);
+          tc_wait_st();
+          tc_before();
+          pass();
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float u0, u1;
+          unpack2(s2[i], u0, u1);
+          u0 += u1;
+          u0 += __shfl_xor_sync(full, u0, 1);
+          u0 += __shfl_xor_sync(full, u0, 2);
+          if ((lane & 3) == 0) {
+            sh_sum[tile][half][r0 + 8 * i] = u0;
+            if (half == 0) sh_ref[tile][r0 + 8 * i] = ref[i];
+          }
+        }
       }
       if (nt > (alt ? tile : 0)) {
         ok = __all_sync(full, ok && wait(b_o + tile, p.done[tile] & 1)) != 0;
         tc_after();
       }
-      sh_sum[tile][half][mine] = sum;
-      if (half == 0) sh_ref[tile][mine] = ref;
     } else if (warp < kMmaWarp) {
       // ---- keys and values, in turn
       const int items = p.items, steps = p.steps, nt = p.nt, t0 = p.t0, end = p.end, head = p.head;
@@ -542,13 +695,13 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           s.page = have ? id : 0;
           s.place = static_cast<int>(place);
           s.live = have ? min(16, end - mine) : 0;
-          sh_slice[lw][j & 1][lane] = s;
+          sh_slice[lw][j % kFound][lane] = s;
         }
         __syncwarp();
       };
       // the copies of item n, by the first of these warps: a lane takes the tokens that neighbour in a page
       auto copy = [&](int n, uint64_t* bar, uint32_t to) {
-        const Slice* slices = sh_slice[lw][n >> 1 & 1];
+        const Slice* slices = sh_slice[lw][(n >> 1) % kFound];
         const int groups = kTok / a.box;
         const Slice sl = slices[lane < groups ? lane * a.box / 16 : 0];
         const bool mine = lane < groups && sl.live > 0;
@@ -570,75 +723,94 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       if constexpr (Q8) {
         if (lw == 0) {
           int n = 0;
+          float ksv[4], vsv[4];  // the scales of the step's tokens lane + 32 e
 #pragma unroll 1
           for (; n < 2 * nt; ++n) {
-            const int item = items + n, buf = item % kRing;
-            if (!(n & 1)) find(n >> 1);
+            const int item = items + n, buf = item % kRing, j = n >> 1;
+            if (!(n & 1)) {
+              find(j);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const Slice& sl = sh_slice[0][j % kFound][lane / 16 + 2 * e];
+                const long long row = static_cast<long long>(head) * a.c.page_size + sl.place + (lane & 15);
+                ksv[e] = __ldg(a.c.ks + sl.page * a.c.ks_page + row);  // (of page 0 where there is none: such a token's weight is 0)
+                vsv[e] = __ldg(a.c.vs + sl.page * a.c.vs_page + row);
+              }
+            }
             ok = __all_sync(full, ok && (item < kRing || wait(b_free + buf, (item / kRing - 1) & 1))) != 0;
             if (!ok) break;
             copy(n, b_raw + buf, base + S::kRawAt + buf * kTok * RB);
+            if (n & 1) {
+              // what goes with the step: its place is free, by the buffer that K waited for
+              const int slot = (steps + j) % kInfo;
+              float* info = reinterpret_cast<float*>(sm + S::kInfoAt) + slot * 3 * kTok + lane;
+              if (lane == 0) sh_valid[slot] = 0xffu & ~missing;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float y = vsv[e] < 7.7037197775489434e-34f ? 7.7037197775489434e-34f : vsv[e];  // 2^-110: a scale of 0 stands for zeros all the same
+                info[32 * e] = ksv[e];
+                info[kTok + 32 * e] = __log2f(y);
+                info[2 * kTok + 32 * e] = y == y ? rcp_fast(y) * kShift8 : 0.0f;  // (a weight is NaN as it is, or 0 where the token is not seen)
+              }
+              mbar_arrive(b_info + slot);
+            }
           }
           if (!ok)  // no copy is in flight at the end
             for (int i = max(0, n - kRing); i < n; ++i) mbar_wait(b_raw + (items + i) % kRing, ((items + i) / kRing) & 1);
         } else {
-          constexpr int N = (kTok + kWorkers - 1) / kWorkers;
-          float ksv[N], vsv[N];  // the scales of tokens lt, lt + kWorkers, .. of the newest step asked for
-          auto scales = [&](int j) {
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-              const int i = lt + e * kWorkers;
-              const Slice& sl = sh_slice[lw][j & 1][i / 16 & 7];
-              const long long row = static_cast<long long>(head) * a.c.page_size + sl.place + (i & 15);
-              ksv[e] = a.c.ks[sl.page * a.c.ks_page + row];  // (of page 0 where there is none: such a token's weight is 0)
-              vsv[e] = a.c.vs[sl.page * a.c.vs_page + row];
-            }
+          // a row's 16 codes of chunk ch
+          static_assert(R % 4 == 0, "the swizzle of row r0 + k R follows from r0's");
+          const uint32_t to0 = (ch / 4) * 16384 + r0 * 128 + (((2 * ch % 8) ^ (r0 & 7)) << 4);
+          auto fetch = [&](uint32_t (&c4)[4], uint32_t from, int k) {
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(c4[0]), "=r"(c4[1]), "=r"(c4[2]), "=r"(c4[3]) : "r"(from + k * R * RB));
           };
-          if (nt > 0) {
-            find(0);
-            scales(0);
-          }
+          auto store = [&](const uint32_t (&c4)[4], uint8_t* tile, int k, bool there) {
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t y = !there ? S::FMT == RSSM_I8 ? 0x80808080u : 0u : S::FMT == RSSM_I8 ? c4[e] ^ 0x80808080u : c4[e];
+              codes_f16<S::FMT>(y, h[2 * e], h[2 * e + 1]);
+            }
+            uint8_t* const to = tile + k * R * 128;
+            const uint32_t x = to0 ^ ((R * k & 4) << 4);
+            *reinterpret_cast<uint4*>(to + x) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(to + (x ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
+          };
 #pragma unroll 1
           for (int n = 0; n < 2 * nt; ++n) {
-            const int item = items + n, buf = item % kRing, j = n >> 1;
+            const int item = items + n, buf = item % kRing;
             ok = __all_sync(full, ok && (item < kRing || wait(b_empty + buf, (item / kRing - 1) & 1))) != 0;
             if (!ok) break;
-            if (!(n & 1)) {
-              // what goes with the step: its place is free, by the buffer that K waits for
-              const int slot = (steps + j) % kInfo;
-              float* info = reinterpret_cast<float*>(sm + S::kInfoAt) + slot * 3 * kTok;
-              if (lt == 0) sh_valid[slot] = 0xffu & ~missing;
-#pragma unroll
-              for (int e = 0; e < N; ++e) {
-                const int i = lt + e * kWorkers;
-                const float y = vsv[e] < 7.7037197775489434e-34f ? 7.7037197775489434e-34f : vsv[e];  // 2^-110: a scale of 0 stands for zeros all the same
-                if (i >= kTok) break;
-                info[i] = ksv[e];
-                info[kTok + i] = __log2f(y);
-                info[2 * kTok + i] = y == y ? rcp_fast(y) * kShift8 : 0.0f;  // (a weight is NaN as it is, or 0 where the token is not seen)
-              }
-              mbar_arrive(b_info + slot);
-              if (j + 1 < nt) {
-                find(j + 1);
-                scales(j + 1);
-              }
-            }
             ok = __all_sync(full, wait(b_raw + buf, (item / kRing) & 1)) != 0;
             if (!ok) break;
-            const uint32_t raw_at = base + S::kRawAt + buf * kTok * RB + ch * 16;
-            uint8_t* const half = sm + S::kRingAt + buf * S::kTile + (ch / 4) * 16384;
-            const Slice* slices = sh_slice[lw][j & 1];
-#pragma unroll 4
-            for (int r = r0; r < kTok; r += R) {
-              uint32_t c4[4], h[8];
-              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(c4[0]), "=r"(c4[1]), "=r"(c4[2]), "=r"(c4[3]) : "r"(raw_at + r * RB));
-              const bool there = r % 16 < slices[r / 16].live;  // what lies behind may be anything
+            const uint32_t from = base + S::kRawAt + buf * kTok * RB + r0 * RB + ch * 16;
+            uint8_t* const tile = sm + S::kRingAt + buf * S::kTile;
+            // kBatch rows at a time: a load does not pass the stores before it
+            constexpr int kFull = kTok / R, kBatch = kFull % 5 == 0 ? 5 : kFull % 4 == 0 ? 4 : 2;
+            static_assert(kFull % kBatch == 0 && R * (kFull + 1) > kTok, "batches, then one row for some");
+            const Slice* slices = sh_slice[0][(n >> 1) % kFound];  // the first warp's: it wrote them before the copies
+            if (__all_sync(full, slices[lane & 7].live == 16)) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t y = !there ? S::FMT == RSSM_I8 ? 0x80808080u : 0u : S::FMT == RSSM_I8 ? c4[e] ^ 0x80808080u : c4[e];
-                codes_f16<S::FMT>(y, h[2 * e], h[2 * e + 1]);
+              for (int k0 = 0; k0 < kFull; k0 += kBatch) {
+                uint32_t c4[kBatch][4];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) fetch(c4[k], from, k0 + k);
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) store(c4[k], tile, k0 + k, true);
               }
-              *reinterpret_cast<uint4*>(half + sw(r, (2 * ch) % 8)) = make_uint4(h[0], h[1], h[2], h[3]);
-              *reinterpret_cast<uint4*>(half + sw(r, (2 * ch + 1) % 8)) = make_uint4(h[4], h[5], h[6], h[7]);
+              if (r0 + kFull * R < kTok) {
+                uint32_t c4[4];
+                fetch(c4, from, kFull);
+                store(c4, tile, kFull, true);
+              }
+            } else {
+#pragma unroll 1
+              for (int k = 0; r0 + k * R < kTok; ++k) {
+                const int r = r0 + k * R;
+                uint32_t c4[4];
+                fetch(c4, from, k);
+                store(c4, tile, k, r % 16 < slices[r / 16].live);  // what lies behind may be anything
+              }
             }
             fence_async();
             __syncwarp();
@@ -670,7 +842,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             ++fixed;
             if (!ok) break;
             uint8_t* tile = sm + S::kRingAt + buf * S::kTile + (ch / 8) * 16384;
-            const Slice* slices = sh_slice[lw][j & 1];
+            const Slice* slices = sh_slice[lw][j % kFound];
             for (int r = r0; r < kTok; r += R) {
               uint4* q = reinterpret_cast<uint4*>(tile + sw(r, ch % 8));
               if (r % 16 >= slices[r / 16].live) {
@@ -835,7 +1007,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
               }
             } else {
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) __stcg(reinterpret_cast<uint4*>(left + r * D + d0 + i), make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]));
+              for (int i = 0; i < 32; i += 4) __stcg(reinterpret_cast<uint4*>(left + piece_at<kRows, D>(r, d0 + i)), make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]));
             }
           }
           __syncwarp();  // the next load is the whole warp's
@@ -861,7 +1033,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             uint2* const q = reinterpret_cast<uint2*>(sm + (r / kQ) * S::kTile + c / 64 * 16384 + sw(r % kQ, c % 64 / 8) + c % 8 * 2);
             *q = make_uint2(bf16_pair(bf16lo(q->x) + y.x, bf16hi(q->x) + y.y), bf16_pair(bf16lo(q->y) + y.z, bf16hi(q->y) + y.w));
           } else {
-            float4* const q = reinterpret_cast<float4*>(left + r * D + c);
+            float4* const q = reinterpret_cast<float4*>(left + piece_at<kRows, D>(r, c));
             const float4 z = __ldcg(q);
             __stcg(q, make_float4(z.x + y.x, z.y + y.y, z.z + y.z, z.w + y.w));
           }
@@ -877,12 +1049,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         }
       }
     }
-    if (!p.whole && threadIdx.x == 0) sh_joint[joints & 1] = Joint{p.first, sh_line.lo - p.t1, p.tiles, p.head, p.row0, p.rows};
-    joints += !p.whole;
   }
-  __syncthreads();
-  if (ok)
-    for (int i = 0; i < joints; ++i) join_pieces<kRows, D, kThreads, 4>(a, sh_joint[i], sh_line.share, kUnit);
   // a wait that gave up: what was started ends before the memory is given back
   if (!ok && warp == kMmaWarp && lane == 0) {
     mbar_init(b_info, 1);
@@ -924,7 +1091,9 @@ cudaError_t launch(const AttnArgs& a, int grid, cudaStream_t st) {
   }
   CUtensorMap k = {}, v = {};
   if (!S::Q8 && (!page_map(a.c, false, a.box, &k) || !page_map(a.c, true, a.box, &v))) return cudaErrorInvalidValue;
-  return launch_pdl(wide_kernel<S>, dim3(grid), dim3(S::kThreads), S::kSmem, st, a, k, v);
+  e = launch_pdl(wide_kernel<S>, dim3(grid), dim3(S::kThreads), S::kSmem, st, a, k, v);
+  if (e != cudaSuccess || a.whole || grid < 2) return e;
+  return launch_join<kRows, kTok, D>(a, grid, S::Q8 ? kShift8 : 1.0f, st);
 }
 template <int D>
 cudaError_t launch_format(const AttnArgs& a, int grid, cudaStream_t st) {
