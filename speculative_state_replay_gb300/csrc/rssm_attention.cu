@@ -22,7 +22,8 @@
 // Work is cut without regard to rows: all (row, tile, head) segments in one line of
 // 64-token units, and every block takes an equal part of it.  A segment that several
 // blocks share is joined by the one that finishes last, from what the others left in
-// the scratch, in the segment's order: no block waits for another.
+// the scratch, in the segment's order: no block waits for another.  Of more than 8
+// queries a launch of its own joins them.
 #include "rssm_attention.cuh"
 
 namespace rssm {
@@ -513,7 +514,9 @@ cudaError_t run(const AttnArgs& args, int sms, cudaStream_t st) {
   }
   AttnArgs a = args;
   const int grid = S::kGrid * sms;
-  a.apart = static_cast<long long>(a.r.T) * a.group > 8;
+  // up to 8 queries the joins are short, and a launch costs as much (one row of 8192 tokens, int8: 1 token 23 us, 26 apart;
+  // 4 tokens 38, 33 apart; 8 over 32768 99, 57 apart)
+  a.apart = grid > 1 && static_cast<long long>(a.r.T) * a.group > 8;
   e = launch_pdl(attention_kernel<S>, dim3(grid), dim3(kThreads), S::kSmem, st, a);
   if (e != cudaSuccess || !a.apart) return e;
   return launch_join<S::kRows, kTile, S::D>(a, grid, S::Q8 ? kShift8 : 1.0f, st);

@@ -124,6 +124,24 @@ def test_attention(fmt, d, hq, h, page, lengths, new, is_tree):
     check_rows(cache, table, lengths, new, q, parents, out, 0.11)
 
 
+CUTS = [
+    # segments of one and of two query tiles, rows without tokens, pieces of one tile: format, query heads, lengths, new tokens, tree
+    ("I8", 8, [3000, 5, 700, 0, -1, 1900, 130], [64, 3, 33, 1, 2, 0, 48], True),
+    ("BF16", 8, [128 * 7 - 40, 2500, 0, 1], [40, 64, 64, 9], True),
+    ("E4M3", 8, [2000, 17, 640], [70, 200, 129], False),
+    ("BF16", 4, [40 * b for b in range(30)], [8 - b % 5 for b in range(30)], False),
+    ("E4M3", 2, [5000, 3], [5, 4], False),
+]
+
+
+@pytest.mark.parametrize("fmt,hq,lengths,new,is_tree", CUTS)
+@pytest.mark.parametrize("sms", [1, 2, 7, 40])
+def test_cuts(monkeypatch, sms, fmt, hq, lengths, new, is_tree):
+    """Grids of few blocks: a block has many segments, and every block's first and last are shared."""
+    monkeypatch.setenv("RSSM_SM_LIMIT", str(sms))
+    test_attention(fmt, 64 if sms == 2 else 128, hq, 2, 32, lengths, new, is_tree)
+
+
 @pytest.mark.parametrize("fmt", ["BF16", "I8", "E4M3"])
 def test_append_and_read(fmt):
     """What is written is what the format's definition says, bit for bit; nothing else changes; it reads back as the values it stands for."""
