@@ -669,8 +669,9 @@ size_t rssm_attention_scratch_bytes(const rssm_kv_cache *cache, int32_t nqheads)
  *        (multiples of 8; 16-byte aligned), heads contiguous
  *   T: most tokens of a row (at most 64 with parents);  tokens: rows of q and out
  * Scores, statistics and sums are fp32; the probabilities enter the product with
- * the values in 8 significant bits for a bf16 cache, in 11 for 8-bit ones.  Rows
- * of lengths[b] < 0 get zeros; rows past their page table get zeros and
+ * the values in 8 significant bits for a bf16 cache, in 11 for 8-bit ones (times
+ * its value's scale; below 2^-25 of the query's largest in fewer, below 2^-36 in
+ * none).  Rows of lengths[b] < 0 get zeros; rows past their page table get zeros and
  * RSSM_ERRBIT_PAGE; tokens in a page outside the cache are not seen
  * (RSSM_ERRBIT_PAGE).  Bad token counts: RSSM_ERRBIT_SEQLEN, outputs untouched, as
  * are those behind the last row.  What a token does not see does not reach it,

@@ -123,7 +123,7 @@ struct RowWork {
 // What a segment costs, in units: a tile of tokens, and what is done once.  The kernel for few queries: a tile is a unit.
 // The one for many: a tile of tokens costs about 5000 cycles where both query tiles have queries of their own (3 units),
 // 3500 where they share them (2), and a segment's queries and sums 20000 (16 ragged trees over int8: 204 us with equal
-// tiles, 159 so).  A part is at least what a tile costs, so that none between a segment's first tile and its end is
+// tiles, 145 so).  A part is at least what a tile costs, so that none between a segment's first tile and its end is
 // without one.
 template <int kRows>
 constexpr int kOnce = kRows > 32 ? 12 : 0;

@@ -364,11 +364,11 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       const float scale2 = fmaxf(fabsf(a.scale2), 1e-30f);  // (times -inf it stays that)
       {
         const bool flip = a.scale2 < 0.0f;            // the maximum is taken before the scale
-        constexpr int G = D / 8, AT = 32 / G, N = kRows / (kSoftWarps * AT);  // lanes of a row, rows of a warp; all rows on their way at a time
+        constexpr int G = D / 8, AT = 32 / G, N = 2;  // lanes of a row, rows of a warp; rows on their way at a time (all eight at once: 8 us more for 16 trees)
         const int row0 = p.row0, rows = p.rows, head = p.head;
         const long long first = p.first;
-        {
-          const int r0 = warp * AT;
+#pragma unroll 1
+        for (int r0 = warp * AT; r0 < (p.alt ? kQ : kRows); r0 += N * kSoftWarps * AT) {
           uint4 x[N];
 #pragma unroll
           for (int i = 0; i < N; ++i) {
@@ -401,8 +401,6 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       const uint32_t s_at = tm + ((warp & 3) << 21) + tile * kTok + half * kPart;
       const int n0 = p.used[tile], nt = p.nt, len = p.len, some = p.some;
       int n = n0, j = alt ? tile : 0, step = p.steps + j, pos = (p.t0 + j) * kTok + half * kPart;
-      // lanes without queries only keep step: what the products make of their lanes goes nowhere
-      const bool idle = (alt ? 0 : tile * kQ) + (warp & 3) * 32 >= p.rows;
       auto pass = [&] {
         __syncwarp();
         if (lane == 0) mbar_arrive(b_p + tile);
@@ -423,10 +421,6 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           ok = __all_sync(full, ok && wait(b_s + tile, n & 1)) != 0;
           if (!ok) break;
           tc_after();
-          if (idle) {
-            pass();
-            continue;
-          }
           uint32_t x[kPart / 32][32];
 #pragma unroll
           for (int c = 0; c < kPart / 32; ++c) tc_ld32(x[c], s_at + 32 * c);
@@ -534,10 +528,6 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           ok = __all_sync(full, ok && wait(b_s + tile, n & 1)) != 0;
           if (!ok) break;
           tc_after();
-          if (idle) {
-            pass();
-            continue;
-          }
           uint32_t x[2][32];  // of query i token 8 y + c2 + e: [i / 2][4 y + 2 (i % 2) + e]
           tc_ld64(x[0], s_at);
           tc_ld64(x[1], s_at + (16u << 16));
