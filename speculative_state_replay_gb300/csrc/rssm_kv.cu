@@ -2,6 +2,8 @@
 // reading tokens back, and the commit of a tree's accepted drafts.
 #include "rssm_kv.cuh"
 
+#include <type_traits>
+
 namespace rssm {
 namespace {
 
@@ -37,23 +39,31 @@ struct AppendArgs {
   long long k_stride, v_stride;
 };
 
+// Codes of eight values times 1 / scale.  int8 ones need no limits: no magnitude is above the head's largest, which
+// three roundings of 2^-24 take to no more than 127 (1 + 2^-22).
 template <int FMT>
 __device__ __forceinline__ uint2 quantize8(const uint4& x, float inv) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t out[2] = {0u, 0u};
+  uint32_t out[2];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const float v0 = __fmul_rn(bf16lo(w[q]), inv), v1 = __fmul_rn(bf16hi(w[q]), inv);
-    uint32_t two;
+  for (int h = 0; h < 2; ++h) {
+    float v[4];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      v[2 * q] = __fmul_rn(bf16lo(w[2 * h + q]), inv);
+      v[2 * q + 1] = __fmul_rn(bf16hi(w[2 * h + q]), inv);
+    }
     if constexpr (FMT == RSSM_I8) {
       // adding 1.5 2^23 rounds to an integer, to even; its low byte is the code
-      const float t0 = __fadd_rn(fminf(fmaxf(v0, -127.0f), 127.0f), 12582912.0f);
-      const float t1 = __fadd_rn(fminf(fmaxf(v1, -127.0f), 127.0f), 12582912.0f);
-      two = __byte_perm(__float_as_uint(t0), __float_as_uint(t1), 0x0040u) & 0xffffu;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = __fadd_rn(v[q], 12582912.0f);
+      out[h] = __byte_perm(__byte_perm(__float_as_uint(v[0]), __float_as_uint(v[1]), 0x0040u),
+                           __byte_perm(__float_as_uint(v[2]), __float_as_uint(v[3]), 0x0040u), 0x5410u);
     } else {
-      two = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(v0, v1), __NV_SATFINITE, __NV_E4M3));
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
+      out[h] = lo | hi << 16;
     }
-    out[q >> 1] |= two << (16 * (q & 1));
   }
   return make_uint2(out[0], out[1]);
 }
@@ -68,16 +78,19 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendArgs a)
   pdl_trigger();
   if (tok >= a.r.tokens) return;
   const int items = 2 * c.heads;
-  KvPlace at;
+  constexpr int ESZ = FMT == RSSM_BF16 ? 2 : 1;
+  const uint16_t* const from_k = a.k + tok * a.k_stride + part * 8;
+  const uint16_t* const from_v = a.v + tok * a.v_stride + part * 8 - c.heads * D;
+  uint8_t *to_k = nullptr, *to_v = nullptr;  // of the token's place in head 0 (to_v: of head -heads)
+  float *scale_k = nullptr, *scale_v = nullptr;
+  const unsigned stride = static_cast<unsigned>(c.page_size) * (D * ESZ);  // bytes between heads
 #pragma unroll 1
   for (int i0 = 0; i0 < items; i0 += RUN * AT_ONCE) {
     uint4 x[RUN];
 #pragma unroll
     for (int u = 0; u < RUN; ++u) {
       const int i = i0 + u * AT_ONCE + mine;
-      const bool values = i >= c.heads;
-      const uint16_t* p = values ? a.v + tok * a.v_stride + (i - c.heads) * D : a.k + tok * a.k_stride + i * D;
-      x[u] = i < items ? __ldcs(reinterpret_cast<const uint4*>(p + part * 8)) : make_uint4(0u, 0u, 0u, 0u);
+      x[u] = i < items ? __ldcs(reinterpret_cast<const uint4*>((i >= c.heads ? from_v : from_k) + i * D)) : make_uint4(0u, 0u, 0u, 0u);
     }
     if (i0 == 0) {
       const int b = find_row(a.r, tok, lane);
@@ -90,20 +103,25 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendArgs a)
       }
       const int len = a.r.lengths[b];
       if (len < 0) return;
+      KvPlace at;
       if (!kv_place(c, a.r, b, len + t, at)) {
         if (lane == 0) set_error(c.err, RSSM_ERRBIT_PAGE);
         return;
+      }
+      to_k = c.k + at.page * c.k_page + at.slot * (D * ESZ) + part * (8 * ESZ);
+      to_v = c.v + at.page * c.v_page + at.slot * (D * ESZ) + part * (8 * ESZ) - static_cast<long long>(c.heads) * stride;
+      if constexpr (FMT != RSSM_BF16) {
+        scale_k = c.ks + at.page * c.ks_page + at.slot;
+        scale_v = c.vs + at.page * c.vs_page + at.slot - static_cast<long long>(c.heads) * c.page_size;
       }
     }
 #pragma unroll
     for (int u = 0; u < RUN; ++u) {
       const int i = i0 + u * AT_ONCE + mine;
       const bool values = i >= c.heads;
-      const int head = values ? i - c.heads : i;
-      const long long row = static_cast<long long>(head) * c.page_size + at.slot;
-      uint8_t* to = (values ? c.v + at.page * c.v_page : c.k + at.page * c.k_page) + row * (D * (FMT == RSSM_BF16 ? 2 : 1));
+      uint8_t* const to = (values ? to_v : to_k) + static_cast<unsigned long long>(i) * stride;
       if constexpr (FMT == RSSM_BF16) {
-        if (i < items) *reinterpret_cast<uint4*>(to + part * 16) = x[u];
+        if (i < items) *reinterpret_cast<uint4*>(to) = x[u];
       } else {
         uint32_t m = __vmaxu2(__vmaxu2(x[u].x & 0x7fff7fffu, x[u].y & 0x7fff7fffu), __vmaxu2(x[u].z & 0x7fff7fffu, x[u].w & 0x7fff7fffu));
 #pragma unroll
@@ -116,8 +134,8 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendArgs a)
                                                                          : __fmul_rn(amax, FMT == RSSM_I8 ? 1.0f / 127.0f : 1.0f / 448.0f);
         const uint2 codes = quantize8<FMT>(x[u], __frcp_rn(scale));
         if (i < items) {
-          *reinterpret_cast<uint2*>(to + part * 8) = finite ? codes : make_uint2(0u, 0u);
-          if (part == 0) (values ? c.vs + at.page * c.vs_page : c.ks + at.page * c.ks_page)[row] = scale;
+          *reinterpret_cast<uint2*>(to) = finite ? codes : make_uint2(0u, 0u);
+          if (part == 0) (values ? scale_v : scale_k)[static_cast<long long>(i) * c.page_size] = scale;
         }
       }
     }
@@ -146,10 +164,23 @@ __device__ __forceinline__ void decode8(const uint4& x, float scale, float (&f)[
     }
   } else {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const uint32_t code = ((q < 4 ? x.x : x.y) >> (8 * (q & 3))) & 0xffu;
-      const float v = FMT == RSSM_I8 ? static_cast<float>(static_cast<int8_t>(code)) : e4m3_to_f32(static_cast<uint8_t>(code));
-      f[q] = __fmul_rn(v, scale);
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t w = h ? x.y : x.x;
+      if constexpr (FMT == RSSM_I8) {
+        // code + 128 in the low byte of 2^23: 2^23 + 128 + code
+        const uint32_t y = w ^ 0x80808080u;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          f[4 * h + q] = __fmul_rn(__fsub_rn(__uint_as_float(__byte_perm(y, 0x4b000000u, 0x7440u + q)), 8388736.0f), scale);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const __half2_raw y = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(q ? w >> 16 : w & 0xffffu), __NV_E4M3);
+          const float2 z = __half22float2(__half2(y));
+          f[4 * h + 2 * q] = __fmul_rn(z.x, scale);
+          f[4 * h + 2 * q + 1] = __fmul_rn(z.y, scale);
+        }
+      }
     }
   }
 }
@@ -190,6 +221,18 @@ __global__ void __launch_bounds__(kWarps * 32) read_kernel(const ReadArgs a) {
     if (lane == 0) set_error(c.err, RSSM_ERRBIT_PAGE);
   }
   const int items = 2 * c.heads;
+  // of the token's place in head 0 (values: of head -heads), read and written
+  const unsigned stride = static_cast<unsigned>(c.page_size) * (D * ESZ);
+  const uint8_t* const from_k = c.k + at.page * c.k_page + at.slot * (D * ESZ) + part * (8 * ESZ);
+  const uint8_t* const from_v = c.v + at.page * c.v_page + at.slot * (D * ESZ) + part * (8 * ESZ) - static_cast<long long>(c.heads) * stride;
+  const float *scale_k = nullptr, *scale_v = nullptr;
+  if constexpr (FMT != RSSM_BF16) {
+    scale_k = c.ks + at.page * c.ks_page + at.slot;
+    scale_v = c.vs + at.page * c.vs_page + at.slot - static_cast<long long>(c.heads) * c.page_size;
+  }
+  using Out = typename std::conditional<OUT == RSSM_F32, float, uint16_t>::type;
+  Out* const to_k = static_cast<Out*>(a.k) + tok * a.k_stride + part * 8;
+  Out* const to_v = static_cast<Out*>(a.v) + tok * a.v_stride + part * 8 - c.heads * D;
 #pragma unroll 1
   for (int i0 = 0; i0 < items; i0 += RUN * AT_ONCE) {
     uint4 x[RUN];
@@ -198,8 +241,7 @@ __global__ void __launch_bounds__(kWarps * 32) read_kernel(const ReadArgs a) {
     for (int u = 0; u < RUN; ++u) {
       const int i = i0 + u * AT_ONCE + mine;
       const bool values = i >= c.heads;
-      const long long row = static_cast<long long>(values ? i - c.heads : i) * c.page_size + at.slot;
-      const uint8_t* p = (values ? c.v + at.page * c.v_page : c.k + at.page * c.k_page) + row * (D * ESZ) + part * 8 * ESZ;
+      const uint8_t* p = (values ? from_v : from_k) + static_cast<unsigned long long>(i) * stride;
       x[u] = make_uint4(0u, 0u, 0u, 0u);
       scale[u] = 0.0f;
       if (have && i < items) {
@@ -209,7 +251,7 @@ __global__ void __launch_bounds__(kWarps * 32) read_kernel(const ReadArgs a) {
           const uint2 y = __ldcs(reinterpret_cast<const uint2*>(p));
           x[u].x = y.x;
           x[u].y = y.y;
-          scale[u] = (values ? c.vs + at.page * c.vs_page : c.ks + at.page * c.ks_page)[row];
+          scale[u] = (values ? scale_v : scale_k)[static_cast<long long>(i) * c.page_size];
         }
       }
     }
@@ -217,20 +259,17 @@ __global__ void __launch_bounds__(kWarps * 32) read_kernel(const ReadArgs a) {
     for (int u = 0; u < RUN; ++u) {
       const int i = i0 + u * AT_ONCE + mine;
       if (i >= items) continue;
-      const bool values = i >= c.heads;
-      const long long to = tok * (values ? a.v_stride : a.k_stride) + (values ? i - c.heads : i) * D + part * 8;
-      void* base = values ? a.v : a.k;
+      Out* const p = (i >= c.heads ? to_v : to_k) + i * D;
       float f[8];
       decode8<FMT>(x[u], scale[u], f);
       if constexpr (OUT == RSSM_F32) {
-        float* p = static_cast<float*>(base) + to;
         __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
         __stcs(reinterpret_cast<float4*>(p + 4), make_float4(f[4], f[5], f[6], f[7]));
       } else {
         uint32_t w[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) w[q] = OUT == RSSM_BF16 ? two_bf16(f[2 * q], f[2 * q + 1]) : two_f16(f[2 * q], f[2 * q + 1]);
-        __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + to), make_uint4(w[0], w[1], w[2], w[3]));
+        __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
       }
     }
   }
