@@ -7,7 +7,9 @@
 // copies into shared memory, its own statistics and sums, so that no warp waits for
 // another until the pieces are joined.
 //
-// What bounds it is the cache's read.  The scores' contraction index is permuted so
+// What bounds it is the cache's read: 64 rows of 8192 bf16 tokens, 8 heads of 128, 4
+// queries each, take 332 us, 6.5 TB/s.  8-bit codes are bound by the instructions that
+// make operands of them: the same in e4m3 225 us, 4.9 TB/s, of the issue slots 55 %.  The scores' contraction index is permuted so
 // that a lane's part of a key is 16 bytes as they lie in the cache; 8-bit codes become
 // fp16 exactly, on their way into the products.  The values' tile is read by transposing
 // loads; 8-bit ones come as pairs of neighbouring dimensions of two tokens, which two

@@ -3,8 +3,9 @@
 //
 // With 256 queries over the same tokens the products are what bounds it, and they are
 // tcgen05's: of two tiles of 128 queries, S = Q K' of 128 tokens into tensor memory,
-// the softmax in registers, a query for two threads, its weights P back into tensor memory in
-// S's place, O += P V with O in tensor memory throughout.  Keys and values come in
+// the softmax in registers, its weights P back into tensor memory in S's place (bf16: a query
+// for two threads; 8-bit: four queries for eight, each with a quarter of a half's tokens, as
+// their scales are read along), O += P V with O in tensor memory throughout.  Keys and values come in
 // turn through a ring of shared-memory buffers, 8-bit codes as fp16, exactly.  The two
 // tiles alternate: while one's scores are turned into weights the products of the other
 // run.  Where a segment has 128 queries or fewer, both take the same ones and every
@@ -15,6 +16,13 @@
 //
 // Work is cut as in rssm_attention.cu, or, where there are segments enough for all
 // blocks, a segment a block with the longest first: a prompt's late queries see more.
+//
+// Measured: the second 4096 tokens of a prompt (32 heads over 8, of 128, bf16) 390 us, 1.06
+// PFLOP/s.  A step of 256 queries over 128 tokens takes 4250 cycles, of which the tensor
+// cores are at work 2050; issuing the products takes 2600 and a tile's softmax 2500, so the
+// two tiles' softmax is what the products wait for.  16 trees of up to 48 tokens over 5000
+// int8 ones each: 145 us; a step of 256 queries takes 5000 cycles, the two warps that
+// convert codes taking 1900 for a tile of keys or values.
 #include "rssm_attention.cuh"
 #include "rssm_readout.cuh"
 #include "rssm_tcgen05.cuh"

