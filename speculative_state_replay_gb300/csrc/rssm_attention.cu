@@ -8,8 +8,8 @@
 // another until the pieces are joined.
 //
 // What bounds it is the cache's read: 64 rows of 8192 bf16 tokens, 8 heads of 128, 4
-// queries each, take 332 us, 6.5 TB/s.  8-bit codes are bound by the instructions that
-// make operands of them: the same in e4m3 225 us, 4.9 TB/s, of the issue slots 55 %.  The scores' contraction index is permuted so
+// queries each, take 328 us, 6.5 TB/s.  8-bit codes are bound by the instructions that
+// make operands of them: the same in e4m3 210 us, 5.3 TB/s, in int8 234.  The scores' contraction index is permuted so
 // that a lane's part of a key is 16 bytes as they lie in the cache; 8-bit codes become
 // fp16 exactly, on their way into the products.  The values' tile is read by transposing
 // loads; 8-bit ones come as pairs of neighbouring dimensions of two tokens, which two
@@ -17,15 +17,18 @@
 // log2, with scales a_i of keys and b_i of values,
 //   s_i = q . k_i a_i scale log2(e),  m = max (s_i + log2 b_i),  w_i = 2^(s_i + log2 b_i - m),
 //   out = (sum w_i code_i) / (sum w_i / b_i)
-// so the values' scales enter the weights, and weights are at most 1 whatever the
-// scales.  8-bit caches take the weights to fp16 times 2^14 (weights down to 2^-28 of
-// the largest keep 11 bits), bf16 ones to bf16.
+// so the values' scales enter the weights, which are at most 2^4 whatever the scales: the
+// m in use follows the true maximum only when that is more than 2^4 times past it, so that
+// the sums are rarely scaled.  8-bit caches take the weights to fp16 times 2^11 (those down
+// to 2^-25 of the largest keep 11 bits), bf16 ones to bf16.
 //
 // Work is cut without regard to rows: all (row, tile, head) segments in one line of
 // 64-token units, and every block takes an equal part of it.  A segment that several
 // blocks share is joined by the one that finishes last, from what the others left in
 // the scratch, in the segment's order: no block waits for another.  Of more than 8
 // queries a launch of its own joins them.
+#include <type_traits>
+
 #include "rssm_attention.cuh"
 
 namespace rssm {
@@ -36,7 +39,8 @@ constexpr int kSlice = 16;              // tokens of a warp's step
 constexpr int kTile = kWarps * kSlice;  // tokens of a unit of work
 constexpr int kBlocks = 3;              // an SM, at most
 constexpr int kMaxSms = 512;
-constexpr float kShift = 14.0f;         // fp16 weights are times 2^14
+constexpr float kShift = 11.0f;         // fp16 weights are times 2^11: 2^15 at most
+constexpr float kLazy = 4.0f;           // log2 of how far the true maximum may be past the one that weights are taken against
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -75,7 +79,7 @@ struct Shape {
   static constexpr int NL = NC / 4;        // chunks a lane takes of a key
   static constexpr int QS = D * 2 + (Q8 ? 16 : 64);  // bytes between queries: a quarter of a warp's reads fall on distinct banks
   // blocks an SM: 8-bit codes are bound by instructions, and eight warps issue in half of the cycles only (64 rows of 8192
-  // tokens, heads of 128, e4m3: two blocks 234 us, three 225; of 64: 187, 150); bf16 keys of 128 are bound by bytes, and three
+  // tokens, heads of 128, e4m3: two blocks 234 us, three 225, of 64: 187, 150; since then 210 and 142); bf16 keys of 128 are bound by bytes, and three
   // stages in flight of two blocks are worth more than two of three (332 us, 341)
   static constexpr int kSm = MT == 1 && D * ESZ <= 128 ? 3 : 2;
   static constexpr int STAGES = Q8 && D < 256 ? 4 : 3;
@@ -104,6 +108,7 @@ __global__ void __launch_bounds__(kThreads, S::kSm) attention_kernel(const __gri
   __shared__ unsigned long long sh_mask[kTreeT];
   __shared__ float sh_qscale[kRows];
   __shared__ int sh_odd;  // values that are not finite among the piece's new tokens
+  __shared__ __align__(16) float sh_v[kWarps][2][kSlice];  // of a slice's values' scales: logarithms, inverses
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, cc = lane & 3;
   const unsigned full = 0xffffffffu;
   uint8_t* const stages = smem + kRows * QS;
@@ -179,6 +184,10 @@ __global__ void __launch_bounds__(kThreads, S::kSm) attention_kernel(const __gri
     const uint8_t* kbase = a.c.k + static_cast<long long>(head) * a.c.page_size * RB;
     const uint8_t* vbase = a.c.v + static_cast<long long>(head) * a.c.page_size * RB;
     unsigned missing = 0;  // per stage: the slice is in no page
+    // of the next slice to ask for: its first token's place in its page, tokens from there to the last one seen
+    const int page_step = kTile % a.c.page_size;
+    int slot = static_cast<int>(static_cast<unsigned>(first) * kSlice % static_cast<unsigned>(a.c.page_size));
+    int behind = static_cast<int>(end - static_cast<long long>(first) * kSlice);
 
     // pages of the 32 slices from a multiple of 32 on, a lane each, and of the 32 after them
     auto look_up = [&](int k) {
@@ -196,29 +205,34 @@ __global__ void __launch_bounds__(kThreads, S::kSm) attention_kernel(const __gri
         const int stage = k % S::STAGES;
         const int page = __shfl_sync(full, page_now, k & 31);
         const bool have = page >= 0 && page < a.c.pages;
-        const unsigned pos = static_cast<unsigned>(first + k * kWarps) * kSlice;
-        const int slot = static_cast<int>(pos % static_cast<unsigned>(a.c.page_size));
-        const int live = have ? static_cast<int>(min(static_cast<long long>(kSlice), end - pos)) : 0;
+        const int live = have ? min(kSlice, behind) : 0;
         missing = (missing & ~(1u << stage)) | (have ? 0u : 1u << stage);
         const uint32_t to = st_at + stage * S::SB;
         const long long pg = have ? page : 0;
         const uint8_t* ksrc = kbase + pg * a.c.k_page + static_cast<long long>(slot) * RB;
         const uint8_t* vsrc = vbase + pg * a.c.v_page + static_cast<long long>(slot) * RB;
+        auto both = [&](auto all) {
 #pragma unroll
-        for (int x = 0; x < kSlice * NC / 32; ++x) {
-          const int i = lane + 32 * x, r = i / NC, ch = i % NC;
-          copy16(to + chunk_at<NC>(r, ch), ksrc + i * 16, r < live);
-        }
+          for (int x = 0; x < kSlice * NC / 32; ++x) {
+            const int i = lane + 32 * x, r = i / NC, ch = i % NC;
+            copy16(to + chunk_at<NC>(r, ch), ksrc + i * 16, all.value || r < live);
+          }
 #pragma unroll
-        for (int x = 0; x < kSlice * NC / 32; ++x) {
-          const int i = lane + 32 * x, r = i / NC, ch = i % NC;
-          copy16(to + kSlice * RB + chunk_at<NC>(r, ch), vsrc + i * 16, r < live);
-        }
+          for (int x = 0; x < kSlice * NC / 32; ++x) {
+            const int i = lane + 32 * x, r = i / NC, ch = i % NC;
+            copy16(to + kSlice * RB + chunk_at<NC>(r, ch), vsrc + i * 16, all.value || r < live);
+          }
+        };
+        if (Q8 && live == kSlice) both(std::true_type());  // (bf16 ones are not bound by instructions)
+        else both(std::false_type());
         if constexpr (Q8) {
           const int r = lane & 15;
           const long long row = static_cast<long long>(head) * a.c.page_size + slot + r;
           copy4(to + 2 * kSlice * RB + lane * 4, lane < 16 ? a.c.ks + pg * a.c.ks_page + row : a.c.vs + pg * a.c.vs_page + row, r < live);
         }
+        behind -= kTile;
+        slot += page_step;
+        if (slot >= a.c.page_size) slot -= a.c.page_size;
       }
       copy_commit();
     };
@@ -251,6 +265,16 @@ __global__ void __launch_bounds__(kThreads, S::kSm) attention_kernel(const __gri
         continue;
       }
       const bool edge = pos + kSlice > some;
+      if constexpr (Q8) {
+        // a lane's token: the logarithm (lanes 0 .. 15) or the inverse of its values' scale
+        float y;
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y) : "r"(ks + 2 * kSlice * RB + (16 + (lane & 15)) * 4) : "memory");
+        y = y < 7.7037197775489434e-34f ? 7.7037197775489434e-34f : y;  // 2^-110: a scale of 0 stands for zeros all the same
+        // a sum of 2^110 2^11 would pass fp32's range; NaN: the weight is that, or 0 if not seen
+        const float inverse = y == y ? rcp_fast(y) * kShift8 : 0.0f;
+        sh_v[warp][lane >> 4][lane & 15] = lane < 16 ? __log2f(y) : inverse;
+        __syncwarp();
+      }
 
       // scores
       float s[MT][2][4];
@@ -302,19 +326,13 @@ __global__ void __launch_bounds__(kThreads, S::kSm) attention_kernel(const __gri
       // weights
       float kf[2][2], lv[2][2], iv[2][2];
       if constexpr (Q8) {
-        const uint32_t sc = ks + 2 * kSlice * RB;
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x, y;
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(sc + (8 * n + 2 * cc + e) * 4) : "memory");
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y) : "r"(sc + (16 + 8 * n + 2 * cc + e) * 4) : "memory");
-            y = y < 7.7037197775489434e-34f ? 7.7037197775489434e-34f : y;  // 2^-110: a scale of 0 stands for zeros all the same
-            kf[n][e] = x;
-            lv[n][e] = __log2f(y);
-            iv[n][e] = y == y ? rcp_fast(y) * kShift8 : 0.0f;  // a sum of 2^110 2^14 would pass fp32's range; NaN: the weight is that, or 0 if not seen
-          }
+        for (int n = 0; n < 2; ++n) {
+          const float2 l2 = *reinterpret_cast<const float2*>(&sh_v[warp][0][8 * n + 2 * cc]), i2 = *reinterpret_cast<const float2*>(&sh_v[warp][1][8 * n + 2 * cc]);
+          asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(kf[n][0]), "=f"(kf[n][1]) : "r"(ks + 2 * kSlice * RB + (8 * n + 2 * cc) * 4) : "memory");
+          lv[n][0] = l2.x, lv[n][1] = l2.y;
+          iv[n][0] = i2.x, iv[n][1] = i2.y;
+        }
       }
       uint32_t pa[MT][4];
 #pragma unroll
@@ -346,10 +364,10 @@ __global__ void __launch_bounds__(kThreads, S::kSm) attention_kernel(const __gri
           float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
           top = fmaxf(top, __shfl_xor_sync(full, top, 1));
           top = fmaxf(top, __shfl_xor_sync(full, top, 2));
-          const float now = fmaxf(m[x][h], top);
-          const float ref = now == -INFINITY ? 0.0f : now;  // nothing seen yet
-          const float alpha = exp2_fast(m[x][h] - ref);
-          if (__any_sync(full, alpha != 1.0f)) {
+          if (__any_sync(full, top > m[x][h] + kLazy)) {
+            const float now = fmaxf(m[x][h], top);
+            const float alpha = now == -INFINITY ? 1.0f : exp2_fast(m[x][h] - now);
+            m[x][h] = now;
             l[x][h] *= alpha;
 #pragma unroll
             for (int y = 0; y < D / 8; ++y) {
@@ -357,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, S::kSm) attention_kernel(const __gri
               o[x][y][2 * h + 1] *= alpha;
             }
           }
-          m[x][h] = now;
+          const float ref = m[x][h] == -INFINITY ? 0.0f : m[x][h];  // nothing seen yet
           float p[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) p[y] = exp2_fast(v[y] - (Q8 ? ref - kShift : ref));
