@@ -727,6 +727,7 @@ rssm_status rssm_tree_accept(const rssm_kv_cache *cache, const int32_t *pages, i
  *   vocab 1..2^18;  T 1..64: most tokens of a request;  ntok: rows of logits
  *   temperature, repetition, presence, frequency f32 [batch] or NULL (1, 1, 0, 0);
  *        a repetition of 0 or less, a temperature below 0, or one that is NaN counts as 1
+ *        (x / repetition is x times the rounded 1 / repetition)
  *   history i32 [batch][history_stride], of which a row's first history_max may be
  *        tokens; history_len, prompt_len i32 [batch]; NULL: none, no prompt.  Lengths
  *        are held to 0 .. history_max, a prompt's to its history's; ids outside the
