@@ -103,7 +103,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) logits_kernel(const LogitsA
   // where word w lies: a step's first four and last four words in planes of their own, so that a warp's 16-byte accesses neighbour
   const int plane = k.slice / 2;
   auto at = [&](int w) { return (w >> 3) * 4 + (w & 3) + (w & 4 ? plane : 0); };
-  auto holds = [&](int id) { return id >= max(base, 0) && id - base < words; };  // (an id below 0 is none)
+  // (an id may be any 32 bits: id - base of the largest would pass them where the row begins up to seven places in)
+  auto holds = [&](int id) { return id >= max(base, 0) && id < base + words; };
 
   // ---- the first logits, asked for early
   uint4 raw[kAhead][PIECES];

@@ -1,0 +1,36 @@
+"""rssm_logits: ids at the ends of their type."""
+import random
+
+import pytest
+import torch
+
+import test_gpu_logits as L
+from test_gpu_logits import _api, check, ints, make  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+ODD_IDS = [2**31 - 1 - i for i in range(9)] + [-(2**31), -(2**31) + 1, -1, -7, -8]
+
+
+@pytest.mark.parametrize("V,dtype", [(100, torch.bfloat16), (4099, torch.float32), (40000, torch.float16)])
+@pytest.mark.parametrize("off", [0, 1, 3, 7])
+def test_ids_at_the_ends_of_their_type_are_not_counted(V, dtype, off):
+    """Rows that begin up to seven values behind a 16-byte boundary: the id of a block's first word is then below 0."""
+    c = make(V, [2, 1, 3], 30, off, tree=True, bias=20, dtype=dtype)
+    odd = ODD_IDS + [V, V + 1]
+    rng = random.Random(V)
+    for h in c["history"]:
+        h += odd
+    for b in c["bias"]:
+        b += [(i, 1e6) for i in odd]
+    c["tokens"][1], c["tokens"][3], c["tokens"][5] = 2**31 - 1, -(2**31), rng.choice(odd)
+    wide = torch.zeros(6, V + 9, dtype=dtype, device="cuda")
+    wide[:, off : off + V] = c["x"]
+    c["x"] = wide[:, off : off + V]
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for probs in (True, False):
+        out = torch.zeros(6, V, device="cuda")
+        L.call(c, out, probs=probs, error_word=word)
+        check(c, out, probs)
+    assert int(word) == 0
