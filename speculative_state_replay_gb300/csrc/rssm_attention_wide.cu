@@ -201,7 +201,8 @@ struct Piece {
   int t0, nt, t1;                    // its steps of tokens: from t0 on nt that any query sees, of t1 - t0
   int end, some;                     // the last token seen by any of its queries; from `some` on not every query sees all
   int items, steps, used[2], done[2], number;  // how often things came round so far: the ring, steps, by tile scores and sums, pieces
-  int fixed;                         // and tiles whose values were looked at
+  int fixed[2];                      // and tiles whose values were looked at: where piece n finds them, n % 2, and leaves them for the
+                                     // next (one place would be written while a late warp still has to read it)
   bool alt, whole, fine, over;       // both tiles have the same queries, and every other step; the whole segment; the row's tree; no piece
 };
 
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     mbar_init(b_q, kSoft);
     fence_barrier_init();
     Piece& p = sh_piece;
-    p.items = p.steps = p.used[0] = p.used[1] = p.done[0] = p.done[1] = p.number = p.fixed = 0;
+    p.items = p.steps = p.used[0] = p.used[1] = p.done[0] = p.done[1] = p.number = p.fixed[0] = p.fixed[1] = 0;
     p.nt = 0;
     p.alt = p.over = false;
   }
@@ -819,7 +820,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           }
         }
       } else {
-        int n = 0, fixed = p.fixed;
+        int n = 0, fixed = p.fixed[p.number & 1];
 #pragma unroll 1
         for (; n < 2 * nt; ++n) {
           const int item = items + n, buf = item % kRing, j = n >> 1;
@@ -858,7 +859,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           }
           if (lane == 0 && (fix || lw != 0)) mbar_arrive(b_full + buf);
         }
-        if (lw == 0 && lane == 0) sh_piece.fixed = fixed;  // (the others have read it: each item takes them all)
+        if (lw == 0 && lane == 0) sh_piece.fixed[(p.number + 1) & 1] = fixed;
         if (!ok && lw == 0)  // no copy is in flight at the end
           for (int i = max(0, n - kRing); i < n; ++i) mbar_wait(b_full + (items + i) % kRing, ((items + i) / kRing) & 1);
       }

@@ -1,0 +1,51 @@
+"""rssm_tree_attention on rows and calls where its kernels can go wrong; both kernels, and both ways in which the one for many
+queries cuts its work."""
+import pytest
+import torch
+
+from test_gpu_attention import check_rows, make_cache, offsets
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _api():
+    import test_gpu_attention as A
+    from speculative_state_replay_gb300 import api
+
+    A.api = api
+
+
+def api():
+    import test_gpu_attention as A
+
+    return A.api
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def tensors(gen, n, hq, h, d):
+    return (torch.randn(n, x, d, generator=gen, device="cuda").bfloat16() for x in (hq, h, h))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sms", [1, 5, None])
+def test_many_short_pieces(monkeypatch, sms, d):
+    """Rows of one to three steps of tokens, all of which some query does not see, by blocks that take many of them in turn."""
+    if sms:
+        monkeypatch.setenv("RSSM_SM_LIMIT", str(sms))
+    h, hq, T, lengths = 2, 8, 40, [0, 90, 200, 128, 1, 300, 88, 87] * 8
+    new = [T - b % 3 for b in range(len(lengths))]
+    cache, table, gen = make_cache(api().BF16, d, h, 16, lengths, new)
+    q, k, v = tensors(gen, sum(new), hq, h, d)
+    ln, cu = ints(lengths), offsets(new)
+    api().rssm_kv_append(cache, k, v, table, ln, T, cu_seqlens=cu)
+    scratch, first = api().alloc_attention_scratch(cache, hq), torch.zeros_like(q)
+    api().rssm_tree_attention(cache, q, table, ln, T, first, scratch, cu_seqlens=cu)
+    out = torch.zeros_like(q)
+    for _ in range(60):
+        api().rssm_tree_attention(cache, q, table, ln, T, out, scratch, cu_seqlens=cu)
+    assert int(cache.error_word) == 0 and torch.equal(out, first)
+    check_rows(cache, table, lengths[:8], new[:8], q, None, out, d**-0.5)
