@@ -834,10 +834,12 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           }
           const uint32_t to = base + S::kRingAt + buf * S::kTile;
           // values that not every query sees are looked at before the product gets them, and what lies behind the last is zero
+          // (two barriers in turn: the ring lets the first warp be up to two such tiles ahead of another, which has
+          // to find the phase that it waits for, and not the one after)
           const bool fix = (n & 1) && ((t0 + j + 1) * kTok > p.some || missing);
-          if (lw == 0) copy(n, fix ? b_raw : b_full + buf, to);
+          if (lw == 0) copy(n, fix ? b_raw + (fixed & 1) : b_full + buf, to);
           if (fix) {
-            ok = __all_sync(full, ok && wait(b_raw, fixed & 1)) != 0;
+            ok = __all_sync(full, ok && wait(b_raw + (fixed & 1), (fixed >> 1) & 1)) != 0;
             ++fixed;
             if (!ok) break;
             uint8_t* tile = sm + S::kRingAt + buf * S::kTile + (ch / 8) * 16384;
