@@ -367,13 +367,15 @@ rssm_status rssm_eval_spec_math(const float *in, float *out_exp, float *out_soft
 /*
  * Diagnostics: a self-test of the bounded waits every pipeline kernel uses
  * (a wait that gives up records RSSM_ERRBIT_TIMEOUT and the kernel returns
- * instead of hanging; the pages have no counterpart to this call).  Launches
- * one warp that waits on an mbarrier told to expect 256 bytes of transactions
+ * instead of hanging; the pages have no counterpart to this call).  Launches a
+ * warp that waits on an mbarrier told to expect 256 bytes of transactions
  * no copy will bring, with the library's wait bounded to about wait_ms
  * milliseconds (1..10000); the wait runs out, RSSM_ERRBIT_TIMEOUT is set in
  * *error_word (device, 4-byte aligned) and the kernel returns.  A genuine
  * bulk copy issued next to it is waited for in full, so nothing is in flight
- * when the kernel ends and the context stays usable.
+ * when the kernel ends and the context stays usable.  Two more warps that meet,
+ * as pairs of the attention kernel do, show that one which gives up does not
+ * keep the other.
  */
 rssm_status rssm_selftest_wait_timeout(uint32_t *error_word, int32_t wait_ms, void *stream);
 

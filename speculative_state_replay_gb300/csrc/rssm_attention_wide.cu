@@ -39,6 +39,7 @@ constexpr int kInfo = 5;                // places of what goes with a step of to
 constexpr float kLazy = 4.0f;           // log2 of how far the true maximum may be past the one in use
 constexpr float kShift = 11.0f;         // fp16 weights are times 2^11: 2^15 at most
 constexpr int kTmem = 512;              // columns: two of S, two of O
+constexpr int kPairs = 2;               // named barriers from here on: of the two warps with the same queries
 
 struct Wait {  // a wait that gives up is for all of the block
   volatile int* dead;
@@ -191,7 +192,6 @@ template <int N>
 __device__ __forceinline__ void soft_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void pair_sync(int pair) { asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory"); }  // of the two warps with the same queries
 
 // A block's part of a segment: what its warps have to know, in shared memory, so that their loops have the registers.
 struct Piece {
@@ -428,7 +428,10 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           const int slot = step % kInfo;
           ok = ok && wait(b_info + slot, (step / kInfo) & 1);
           ok = __all_sync(full, ok && wait(b_s + tile, n & 1)) != 0;
-          if (!ok) break;
+          if (!ok) {
+            pair_leave(kPairs + (warp & 3 | tile << 2));
+            break;
+          }
           tc_after();
           uint32_t x[kPart / 32][32];
 #pragma unroll
@@ -463,7 +466,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           // the other half's; after this the other half's scores are in registers too, and P may take their place
           sh_top[tile][half][mine] = top;
           tc_before();
-          pair_sync(warp & 3 | tile << 2);
+          pair_sync(kPairs + (warp & 3 | tile << 2));
           tc_after();
           top = fmaxf(top, sh_top[tile][half ^ 1][mine]);
           // the maximum in use follows where it has to; the products before this step's are done (its scores came after them)
@@ -535,7 +538,10 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           const int slot = step % kInfo;
           ok = ok && wait(b_info + slot, (step / kInfo) & 1);
           ok = __all_sync(full, ok && wait(b_s + tile, n & 1)) != 0;
-          if (!ok) break;
+          if (!ok) {
+            pair_leave(kPairs + (warp & 3 | tile << 2));
+            break;
+          }
           tc_after();
           uint32_t x[2][32];  // of query i token 8 y + c2 + e: [i / 2][4 y + 2 (i % 2) + e]
           tc_ld64(x[0], s_at);
@@ -590,7 +596,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           }
           // the other half's; after this the other half's scores are in registers too, and P may take their place
           tc_before();
-          pair_sync(warp & 3 | tile << 2);
+          pair_sync(kPairs + (warp & 3 | tile << 2));
           tc_after();
 #pragma unroll
           for (int i = 0; i < 4; ++i) {

@@ -763,12 +763,14 @@ __global__ void spec_math_kernel(const float* in, float* oexp, float* osp, long 
 }
 
 // ---------------------------------------------------------------------------
-// self-test of the bounded mbarrier wait: one warp.  Barrier `lost` is told to
+// self-test of the bounded mbarrier wait: three warps.  Barrier `lost` is told to
 // expect 256 bytes of transactions that no copy will bring (the state a stage
 // barrier is in when a copy it counts on never lands); its wait runs out after
 // `tries` tests and the kernel sets RSSM_ERRBIT_TIMEOUT, as the pipeline
 // kernels do.  Barrier `real` counts one genuine 256-byte bulk copy, waited
-// for in full, so no copy is in flight when the kernel returns.
+// for in full, so no copy is in flight when the kernel returns.  The second and
+// third warps are a pair: the second's wait for `lost` runs out and it leaves,
+// the third's for `real` does not, and it gets past the pair's meeting.
 // ---------------------------------------------------------------------------
 __device__ __align__(16) unsigned char g_wait_probe_src[256];
 
@@ -782,7 +784,17 @@ __global__ void wait_timeout_kernel(unsigned* err, unsigned tries) {
     mbar_init(real, 1);
     fence_barrier_init();
   }
-  __syncwarp();
+  __syncthreads();
+  if (threadIdx.x >= 64) {
+    if (mbar_wait(real, 0u)) pair_sync(1);
+    else pair_leave(1);
+    return;
+  }
+  if (threadIdx.x >= 32) {
+    if (mbar_wait(lost, 0u, tries)) pair_sync(1);
+    else pair_leave(1);
+    return;
+  }
   if (threadIdx.x != 0) return;
   mbar_arrive_expect_tx(lost, 256u);  // nothing will ever complete these bytes
   mbar_arrive_expect_tx(real, 256u);
@@ -793,7 +805,7 @@ __global__ void wait_timeout_kernel(unsigned* err, unsigned tries) {
 }
 
 int launch_wait_timeout(unsigned* err, unsigned tries, void* stream) {
-  wait_timeout_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(err, tries);
+  wait_timeout_kernel<<<1, 96, 0, static_cast<cudaStream_t>(stream)>>>(err, tries);
   return cudaGetLastError();
 }
 

@@ -49,3 +49,20 @@ def test_many_short_pieces(monkeypatch, sms, d):
         api().rssm_tree_attention(cache, q, table, ln, T, out, scratch, cu_seqlens=cu)
     assert int(cache.error_word) == 0 and torch.equal(out, first)
     check_rows(cache, table, lengths[:8], new[:8], q, None, out, d**-0.5)
+
+
+def test_a_warp_that_gives_up_does_not_keep_its_partner():
+    """Of two warps that meet in every step one's wait runs out, the other's does not: the kernel ends, and calls go on as before."""
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for ms in (1, 20):
+        api().rssm_selftest_wait_timeout(word, wait_ms=ms)
+        torch.cuda.synchronize()
+        assert int(word) == api().ERRBIT_TIMEOUT
+    lengths, new, d, h, hq = [200, 3], [40, 40], 64, 2, 8
+    cache, table, gen = make_cache(api().I8, d, h, 16, lengths, new)
+    q, k, v = tensors(gen, 80, hq, h, d)
+    api().rssm_kv_append(cache, k, v, table, ints(lengths), 40)
+    out = torch.zeros_like(q)
+    api().rssm_tree_attention(cache, q, table, ints(lengths), 40, out, api().alloc_attention_scratch(cache, hq))
+    assert int(cache.error_word) == 0
+    check_rows(cache, table, lengths, new, q, None, out, d**-0.5)
