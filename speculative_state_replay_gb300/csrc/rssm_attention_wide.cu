@@ -868,8 +868,10 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           if (lane == 0 && (fix || lw != 0)) mbar_arrive(b_full + buf);
         }
         if (lw == 0 && lane == 0) sh_piece.fixed[(p.number + 1) & 1] = fixed;
-        if (!ok && lw == 0)  // no copy is in flight at the end
+        if (!ok && lw == 0) {  // no copy is in flight at the end, that of a tile to be looked at neither
           for (int i = max(0, n - kRing); i < n; ++i) mbar_wait(b_full + (items + i) % kRing, ((items + i) / kRing) & 1);
+          if (fixed > 0) mbar_wait(b_raw + ((fixed - 1) & 1), ((fixed - 1) >> 1) & 1);
+        }
       }
     } else {
       // ---- products
