@@ -1027,6 +1027,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         }
       }
       tc_before();
+      fence_async();  // the next piece's copies come into the ring, where the second tile's sums were
       if (!Q8 && sh_odd == p.number) {
         // values that are not finite, to those queries that see them
         soft_sync<kSoft>();
