@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       const int most = max(0, end - 1);
       auto page_id = [&](int j) {
         const unsigned at = min(most, (t0 + j) * kTok + 16 * (lane & 7));
-        return end > 0 ? __ldg(table + at / static_cast<unsigned>(a.c.page_size)) : 0;
+        return end > 0 ? table[at / static_cast<unsigned>(a.c.page_size)] : 0;
       };
       int next_id = page_id(0);
       unsigned missing = 0u;
@@ -738,8 +738,10 @@ __global__ void __launch_bounds__(S::kThreads, 1)
               for (int e = 0; e < 4; ++e) {
                 const Slice& sl = sh_slice[0][j % kFound][lane / 16 + 2 * e];
                 const long long row = static_cast<long long>(head) * a.c.page_size + sl.place + (lane & 15);
-                ksv[e] = __ldg(a.c.ks + sl.page * a.c.ks_page + row);  // (of page 0 where there is none: such a token's weight is 0)
-                vsv[e] = __ldg(a.c.vs + sl.page * a.c.vs_page + row);
+                // (of page 0 where there is none: such a token's weight is 0.  Ordinary loads: this kernel may have begun before
+                // the append that writes these ended, so they are not constant while it runs)
+                ksv[e] = a.c.ks[sl.page * a.c.ks_page + row];
+                vsv[e] = a.c.vs[sl.page * a.c.vs_page + row];
               }
             }
             ok = __all_sync(full, ok && (item < kRing || wait(b_free + buf, (item / kRing - 1) & 1))) != 0;
