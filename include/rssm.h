@@ -624,7 +624,8 @@ typedef struct {
  *   cu_seqlens [batch+1] i32 or NULL (T tokens a row);  T: most tokens of a row
  *   tokens: token rows of k and v;  max_pages: entries of a row of `pages`
  * Tokens behind the last row are not written.  Token counts that are negative or
- * more than T, and bounds past `tokens`: RSSM_ERRBIT_SEQLEN, the row is skipped.
+ * more than T, and bounds past `tokens`: RSSM_ERRBIT_SEQLEN, the row is skipped, the
+ * others are written (a token that lies in two of them, where bounds fall, for both).
  * Positions past the page table and pages outside the cache: RSSM_ERRBIT_PAGE,
  * the token is skipped.  Two tokens of a call must not meet in one place of a page.
  */
@@ -642,7 +643,8 @@ rssm_status rssm_kv_append(const rssm_kv_cache *cache, int32_t layer, const void
  * Rows of starts[b] < 0 are padding: their outputs and those of tokens that lie
  * past the page table or in no page (RSSM_ERRBIT_PAGE) are zeros.  Outputs behind
  * the last row, and those of rows whose bounds fall or pass `tokens`
- * (RSSM_ERRBIT_SEQLEN), stay as they are.
+ * (RSSM_ERRBIT_SEQLEN), stay as they are; an output that lies in two other rows,
+ * where bounds fall, gets values of either.
  */
 rssm_status rssm_kv_read(const rssm_kv_cache *cache, int32_t layer, const int32_t *pages, int64_t pages_stride,
                          int32_t max_pages, const int32_t *starts, const int32_t *cu_seqlens, int32_t batch,

@@ -14,6 +14,15 @@ struct KvPlace {
   int slot;
 };
 
+// Whether the bounds of all rows are sound, by a whole block; sets the error bit if not.
+__device__ __forceinline__ bool bounds_sound(const KvRows& r, unsigned* err) {
+  int bad = 0;
+  for (int b = threadIdx.x; b < r.batch; b += blockDim.x) bad |= row_span(r, b).count < 0;
+  if (!__syncthreads_or(bad)) return true;
+  if (threadIdx.x == 0) set_error(err, RSSM_ERRBIT_SEQLEN);
+  return false;
+}
+
 // Where position `pos` of row b is: false if it is past the row's table or in no page.
 __device__ __forceinline__ bool kv_place(const KvView& c, const KvRows& r, int b, long long pos, KvPlace& at) {
   if (pos >= static_cast<long long>(r.max_pages) * c.page_size) return false;
@@ -30,7 +39,10 @@ __device__ __forceinline__ bool kv_place(const KvView& c, const KvRows& r, int b
 // (they do not depend on where the token goes, so the first four leave before the
 // token's row and page are looked up).  The largest magnitude of a head is found on
 // the bits: magnitudes order as integers, and what is not finite is at 0x7f80 and above.
-// Measured: 16411 tokens of 8 heads of 128 as int8, 102 MB, 22.5 us, 4.5 TB/s; issue slots
+// A token's row is found by the rows' ends, which order where all bounds are sound.  The
+// first block looks whether they are, and goes over the sound rows itself if not, since
+// some of their tokens may then have been found in no row, or in another.
+// Measured: 16411 tokens of 8 heads of 128 as int8, 102 MB, 22.7 us, 4.5 TB/s; issue slots
 // are 70 % taken, and the two ends of so short a launch are in it.
 // --------------------------------------------------------------------------
 struct AppendArgs {
@@ -70,15 +82,12 @@ __device__ __forceinline__ uint2 quantize8(const uint4& x, float inv) {
   return make_uint2(out[0], out[1]);
 }
 
-template <int D, int FMT>
-__global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendArgs a) {
-  constexpr int G = D / 8, AT_ONCE = 32 / G, RUN = 4;
+// token `tok`, of row `row` or (-1) of the one that it is found in, by a warp; RUN heads' loads of a lane on their way at a time
+template <int D, int FMT, int RUN>
+__device__ __forceinline__ void append_token(const AppendArgs& a, long long tok, int row) {
+  constexpr int G = D / 8, AT_ONCE = 32 / G;
   const KvView& c = a.c;
   const int lane = threadIdx.x & 31, mine = lane / G, part = lane % G;
-  const long long tok = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  pdl_wait();
-  pdl_trigger();
-  if (tok >= a.r.tokens) return;
   const int items = 2 * c.heads;
   constexpr int ESZ = FMT == RSSM_BF16 ? 2 : 1;
   const uint16_t* const from_k = a.k + tok * a.k_stride + part * 8;
@@ -95,14 +104,11 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendArgs a)
       x[u] = i < items ? __ldcs(reinterpret_cast<const uint4*>((i >= c.heads ? from_v : from_k) + i * D)) : make_uint4(0u, 0u, 0u, 0u);
     }
     if (i0 == 0) {
-      const int b = find_row(a.r, tok, lane);
+      const int b = row < 0 ? find_row(a.r, tok, lane) : row;
       if (b < 0) return;
       const RowSpan s = row_span(a.r, b);
       const long long t = tok - s.first;
-      if (t < 0 || t >= s.count) {
-        if (s.count < 0 && lane == 0) set_error(c.err, RSSM_ERRBIT_SEQLEN);
-        return;
-      }
+      if (t < 0 || t >= s.count) return;  // (bounds that are not sound: the first block says so)
       const int len = a.r.lengths[b];
       if (len < 0) return;
       KvPlace at;
@@ -143,10 +149,26 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(const AppendArgs a)
     }
   }
 }
+template <int D, int FMT>
+__global__ void __launch_bounds__(kWarps * 32) append_kernel(const __grid_constant__ AppendArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5;
+  if (a.r.cu && blockIdx.x == 0) {
+    if (bounds_sound(a.r, a.c.err)) return;
+    for (int b = 0; b < a.r.batch; ++b) {
+      const RowSpan s = row_span(a.r, b);
+      for (int t = warp; t < s.count; t += kWarps) append_token<D, FMT, 1>(a, s.first + t, b);
+    }
+    return;
+  }
+  const long long tok = static_cast<long long>(blockIdx.x - (a.r.cu ? 1 : 0)) * kWarps + warp;
+  if (tok < a.r.tokens) append_token<D, FMT, 4>(a, tok, -1);
+}
 
 // --------------------------------------------------------------------------
 // Reading back: the same cut, the other way.  51584 tokens of 8 heads of 128, e4m3 to
-// bf16, 320 MB: 52.5 us, 6.1 TB/s (90 % of a copy).
+// bf16, 320 MB: 51.0 us, 6.3 TB/s (92 % of a copy).
 // --------------------------------------------------------------------------
 struct ReadArgs {
   KvView c;
@@ -199,23 +221,17 @@ __device__ __forceinline__ uint32_t two_f16(float lo, float hi) {
   return r;
 }
 
-template <int D, int FMT, int OUT>
-__global__ void __launch_bounds__(kWarps * 32) read_kernel(const ReadArgs a) {
-  constexpr int G = D / 8, AT_ONCE = 32 / G, RUN = 4, ESZ = FMT == RSSM_BF16 ? 2 : 1;
+// (as append_token)
+template <int D, int FMT, int OUT, int RUN>
+__device__ __forceinline__ void read_token(const ReadArgs& a, long long tok, int row) {
+  constexpr int G = D / 8, AT_ONCE = 32 / G, ESZ = FMT == RSSM_BF16 ? 2 : 1;
   const KvView& c = a.c;
   const int lane = threadIdx.x & 31, mine = lane / G, part = lane % G;
-  const long long tok = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  pdl_wait();
-  pdl_trigger();
-  if (tok >= a.r.tokens) return;
-  const int b = find_row(a.r, tok, lane);
+  const int b = row < 0 ? find_row(a.r, tok, lane) : row;
   if (b < 0) return;
   const RowSpan s = row_span(a.r, b);
   const long long t = tok - s.first;
-  if (t < 0 || t >= s.count) {
-    if (s.count < 0 && lane == 0) set_error(c.err, RSSM_ERRBIT_SEQLEN);
-    return;
-  }
+  if (t < 0 || t >= s.count) return;
   const int start = a.r.lengths ? a.r.lengths[b] : 0;
   KvPlace at = {0, 0};
   bool have = start >= 0;
@@ -276,6 +292,22 @@ __global__ void __launch_bounds__(kWarps * 32) read_kernel(const ReadArgs a) {
       }
     }
   }
+}
+template <int D, int FMT, int OUT>
+__global__ void __launch_bounds__(kWarps * 32) read_kernel(const __grid_constant__ ReadArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5;
+  if (blockIdx.x == 0) {
+    if (bounds_sound(a.r, a.c.err)) return;
+    for (int b = 0; b < a.r.batch; ++b) {
+      const RowSpan s = row_span(a.r, b);
+      for (int t = warp; t < s.count; t += kWarps) read_token<D, FMT, OUT, 1>(a, s.first + t, b);
+    }
+    return;
+  }
+  const long long tok = static_cast<long long>(blockIdx.x - 1) * kWarps + warp;
+  if (tok < a.r.tokens) read_token<D, FMT, OUT, 4>(a, tok, -1);
 }
 
 // --------------------------------------------------------------------------
@@ -421,11 +453,11 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptArgs
 
 bool al(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-cudaError_t launch(void (*kernel)(AppendArgs), const AppendArgs& a, cudaStream_t st) {
-  return launch_pdl(kernel, dim3(static_cast<unsigned>((a.r.tokens + kWarps - 1) / kWarps)), dim3(kWarps * 32), 0, st, a);
-}
-cudaError_t launch(void (*kernel)(ReadArgs), const ReadArgs& a, cudaStream_t st) {
-  return launch_pdl(kernel, dim3(static_cast<unsigned>((a.r.tokens + kWarps - 1) / kWarps)), dim3(kWarps * 32), 0, st, a);
+// a warp a token, and a block for the bounds, if there are any
+template <typename A>
+cudaError_t launch(void (*kernel)(A), const A& a, cudaStream_t st) {
+  const unsigned blocks = static_cast<unsigned>((a.r.tokens + kWarps - 1) / kWarps) + (a.r.cu ? 1u : 0u);
+  return launch_pdl(kernel, dim3(blocks), dim3(kWarps * 32), 0, st, a);
 }
 
 template <int D>
