@@ -112,7 +112,7 @@ __device__ __forceinline__ bool take_out_odd(uint4& x) {
 
 struct RowWork {
   RowSpan s;
-  int len;    // committed tokens; < 0: nothing to see, zeros (-2: past the page table)
+  int len;    // committed tokens; < 0: nothing to see, zeros (-1: padding, -2: past the page table)
   int tiles;  // of tokens
   int mtiles; // of queries
   int cost;   // of a tile of tokens, in units
@@ -145,7 +145,7 @@ __device__ __forceinline__ RowWork row_work(const AttnArgs& a, int b) {
   w.units = 0;
   w.len = -1;
   if (w.s.count <= 0) return w;
-  w.len = a.r.lengths[b];
+  w.len = max(a.r.lengths[b], -1);  // (any below 0 is padding)
   w.tiles = 1;
   w.mtiles = static_cast<int>((static_cast<long long>(w.s.count) * a.group + kRows - 1) / kRows);
   if (w.len >= 0) {

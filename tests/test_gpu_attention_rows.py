@@ -66,3 +66,19 @@ def test_a_warp_that_gives_up_does_not_keep_its_partner():
     api().rssm_tree_attention(cache, q, table, ints(lengths), 40, out, api().alloc_attention_scratch(cache, hq))
     assert int(cache.error_word) == 0
     check_rows(cache, table, lengths, new, q, None, out, d**-0.5)
+
+
+@pytest.mark.parametrize("T,sms", [(2, None), (40, None), (40, 1)])  # few queries; many; many, a segment a block
+def test_any_negative_length_is_padding(monkeypatch, T, sms):
+    if sms:
+        monkeypatch.setenv("RSSM_SM_LIMIT", str(sms))
+    d, h, hq, lengths = 64, 2, 4, [-2, 30, -1, -(2**31), 0, -3]
+    new = [T] * len(lengths)
+    cache, table, gen = make_cache(api().BF16, d, h, 16, lengths, new)
+    q, k, v = tensors(gen, sum(new), hq, h, d)
+    ln, cu = ints(lengths), offsets(new)
+    api().rssm_kv_append(cache, k, v, table, ln, T, cu_seqlens=cu)
+    out = torch.full_like(q, 7.0)
+    api().rssm_tree_attention(cache, q, table, ln, T, out, api().alloc_attention_scratch(cache, hq), cu_seqlens=cu)
+    assert int(cache.error_word) == 0
+    check_rows(cache, table, lengths, new, q, None, out, d**-0.5)
