@@ -841,10 +841,11 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             mbar_arrive(b_info + slot);
           }
           const uint32_t to = base + S::kRingAt + buf * S::kTile;
-          // values that not every query sees are looked at before the product gets them, and what lies behind the last is zero
+          // values that not every query sees are looked at before the product gets them, and what lies behind the last or in no
+          // page is zero
           // (two barriers in turn: the ring lets the first warp be up to two such tiles ahead of another, which has
           // to find the phase that it waits for, and not the one after)
-          const bool fix = (n & 1) && ((t0 + j + 1) * kTok > p.some || missing);
+          const bool unseen = (t0 + j + 1) * kTok > p.some, fix = (n & 1) && (unseen || missing);
           if (lw == 0) copy(n, fix ? b_raw + (fixed & 1) : b_full + buf, to);
           if (fix) {
             ok = __all_sync(full, ok && wait(b_raw + (fixed & 1), (fixed >> 1) & 1)) != 0;
@@ -858,6 +859,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
                 *q = make_uint4(0u, 0u, 0u, 0u);
                 continue;
               }
+              if (!unseen) continue;  // every query sees the others, whatever they are
               uint4 y = *q;
               if (take_out_odd(y)) {
                 *q = y;

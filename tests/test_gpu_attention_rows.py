@@ -1,5 +1,7 @@
 """rssm_tree_attention on rows and calls where its kernels can go wrong; both kernels, and both ways in which the one for many
 queries cuts its work."""
+import math
+
 import pytest
 import torch
 
@@ -82,3 +84,25 @@ def test_any_negative_length_is_padding(monkeypatch, T, sms):
     api().rssm_tree_attention(cache, q, table, ln, T, out, api().alloc_attention_scratch(cache, hq), cu_seqlens=cu)
     assert int(cache.error_word) == 0
     check_rows(cache, table, lengths, new, q, None, out, d**-0.5)
+
+
+@pytest.mark.parametrize("T", [2, 40])
+def test_what_is_not_finite_beside_a_missing_page(T):
+    """A row of three hundred tokens without its second page: NaN and infinities in the other pages reach all queries, which see them."""
+    d, h, hq, lengths, new = 64, 2, 4, [300, 300], [T, T]
+    cache, table, gen = make_cache(api().BF16, d, h, 16, lengths, new)
+    q, k, v = tensors(gen, sum(new), hq, h, d)
+    ln, cu = ints(lengths), offsets(new)
+    api().rssm_kv_append(cache, k, v, table, ln, T, cu_seqlens=cu)
+    cache.v[0, int(table[0, 3]), 0, 5, 11] = math.inf
+    cache.v[0, int(table[0, 3]), 1, 7, 60] = math.nan
+    holes = table.clone()
+    holes[0, 1] = -1
+    out = torch.zeros_like(q)
+    api().rssm_tree_attention(cache, q, holes, ln, T, out, api().alloc_attention_scratch(cache, hq), cu_seqlens=cu)
+    assert int(cache.error_word) == api().ERRBIT_PAGE
+    got = out[:T].float().cpu().view(T, h, hq // h, d)
+    assert bool((got[:, 0, :, 11] == math.inf).all()) and bool(got[:, 1, :, 60].isnan().all())
+    got[:, 0, :, 11] = got[:, 1, :, 60] = 0.0
+    assert bool(got.isfinite().all())
+    check_rows(cache, table[1:], lengths[1:], new[1:], q[T:], None, out[T:], d**-0.5)
