@@ -592,7 +592,8 @@ rssm_status rssm_residual_norm(const void *x, int64_t x_stride, const void *resi
  * it is below 2^-100), and code = nearest of x * (1 / scale), ties to even, each
  * operation and constant rounded to fp32.  A token's head
  * with a value that is not finite gets the scale NaN and the codes 0: it reads
- * back as NaN throughout.  e4m3 codes that a caller writes must not be NaN.
+ * back as NaN throughout.  e4m3 codes that a caller writes must not be NaN, and its
+ * scales not negative.
  *
  * Rows find their pages in a table, pages [batch][pages_stride] i32, whose first
  * max_pages entries of a row are its pages in order: the token at position i is

@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, S::kSm) attention_kernel(const __gri
         float y;
         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y) : "r"(ks + 2 * kSlice * RB + (16 + (lane & 15)) * 4) : "memory");
         y = y < 7.7037197775489434e-34f ? 7.7037197775489434e-34f : y;  // 2^-110: a scale of 0 stands for zeros all the same
-        // a sum of 2^110 2^11 would pass fp32's range; NaN: the weight is that, or 0 if not seen
+        // NaN: the weight is that, or 0 if not seen
         const float inverse = y == y ? rcp_fast(y) * kShift8 : 0.0f;
         sh_v[warp][lane >> 4][lane & 15] = lane < 16 ? __log2f(y) : inverse;
         __syncwarp();

@@ -10,7 +10,9 @@
 
 namespace rssm {
 
-constexpr float kShift8 = 9.3132257461547852e-10f;  // 2^-30: 1 / (a value's scale) is summed times this
+// 1 / (a value's scale) is summed times this, 2^-16.  Scales are at least 2^-109 (2^-100 / 448), at most 2^121 (bf16's largest
+// / 127): the inverse of the largest keeps 12 bits, and 2^20 tokens of the smallest with weights of 2^15 stay in range.
+constexpr float kShift8 = 1.52587890625e-05f;
 
 struct AttnArgs {
   KvView c;

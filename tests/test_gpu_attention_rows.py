@@ -106,3 +106,26 @@ def test_what_is_not_finite_beside_a_missing_page(T):
     got[:, 0, :, 11] = got[:, 1, :, 60] = 0.0
     assert bool(got.isfinite().all())
     check_rows(cache, table[1:], lengths[1:], new[1:], q[T:], None, out[T:], d**-0.5)
+
+
+@pytest.mark.parametrize("fmt", ["I8", "E4M3"])
+@pytest.mark.parametrize("T", [3, 40])
+@pytest.mark.parametrize("power", [-96, 100, 118, 126])
+def test_values_of_any_size(fmt, T, power):
+    """Values up to the largest of bf16, whose scales pass 2^118, and as small as the cache's scales go."""
+    d, h, hq, lengths, new = 64, 2, 8, [200, 9], [T, T]
+    cache, table, gen = make_cache(getattr(api(), fmt), d, h, 16, lengths, new)
+    q, k, _ = tensors(gen, 2 * T, hq, h, d)
+    ln, cu = ints(lengths), offsets(new)
+    draw = lambda n: ((torch.rand(n, h, d, generator=gen, device="cuda") * 2 - 1) * 2.0**power).bfloat16()  # noqa: E731
+    old = draw(sum(lengths))
+    kk = torch.randn(sum(lengths), h, d, generator=gen, device="cuda").bfloat16()
+    api().rssm_kv_append(cache, kk, old, table, ints([0, 0]), max(lengths), cu_seqlens=offsets(lengths))
+    api().rssm_kv_append(cache, k, draw(2 * T), table, ln, T, cu_seqlens=cu)
+    out = torch.zeros_like(q)
+    api().rssm_tree_attention(cache, q, table, ln, T, out, api().alloc_attention_scratch(cache, hq), cu_seqlens=cu)
+    assert int(cache.error_word) == 0
+    # check_rows has the output's rounding and the weights'; what a weight of an 8-bit cache is off by below the fp16 range (2^-36 of
+    # the largest p_j b_j) times codes of at most 448.  Scales are at most 2^power / 127 (1 + 2^-8), and the tokens 240.  The inverse
+    # of the largest scale, 2^119, has 14 bits left in the sum's unit: 2^-15 of a weight, within the 2^-12 that are counted.
+    check_rows(cache, table, lengths, new, q, None, out, d**-0.5, 2.0**-36 * 448 * (max(lengths) + T) * 2.0**power / 126)
