@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_attention import check_rows, make_cache, offsets
+from test_gpu_attention import check_rows, make_cache, offsets, tree
 
 pytestmark = pytest.mark.gpu
 
@@ -129,3 +129,33 @@ def test_values_of_any_size(fmt, T, power):
     # the largest p_j b_j) times codes of at most 448.  Scales are at most 2^power / 127 (1 + 2^-8), and the tokens 240.  The inverse
     # of the largest scale, 2^119, has 14 bits left in the sum's unit: 2^-15 of a weight, within the 2^-12 that are counted.
     check_rows(cache, table, lengths, new, q, None, out, d**-0.5, 2.0**-36 * 448 * (max(lengths) + T) * 2.0**power / 126)
+
+
+REPEAT = [
+    # format, head_dim, query heads, lengths, new tokens, tree
+    ("BF16", 128, 8, [3000, 5, 700, 0, -1, 1900], [4, 3, 1, 1, 2, 4], False),
+    ("E4M3", 64, 4, [4000, 17], [5, 5], False),
+    ("I8", 128, 8, [2500, 5, 700, 0], [64, 3, 33, 1], True),
+    ("BF16", 128, 8, [2500, 130, 0, 90], [64, 40, 64, 9], True),
+    ("E4M3", 64, 8, [2000, 17, 640], [70, 200, 129], False),
+    ("BF16", 256, 4, [1500, 3], [12, 5], True),
+]
+
+
+@pytest.mark.parametrize("fmt,d,hq,lengths,new,is_tree", REPEAT)
+@pytest.mark.parametrize("sms", [None, 2, 7])
+def test_the_same_call_gives_the_same_bits(monkeypatch, sms, fmt, d, hq, lengths, new, is_tree):
+    if sms:
+        monkeypatch.setenv("RSSM_SM_LIMIT", str(sms))
+    cache, table, gen = make_cache(getattr(api(), fmt), d, 2, 32, lengths, new)
+    q, k, v = tensors(gen, sum(new), hq, 2, d)
+    ln, cu = ints(lengths), offsets(new)
+    api().rssm_kv_append(cache, k, v, table, ln, max(new), cu_seqlens=cu)
+    parents = [p for b, m in enumerate(new) for p in tree(m, b)] if is_tree else None
+    scratch = api().alloc_attention_scratch(cache, hq)
+    outs = torch.full((12, *q.shape), 7.0, dtype=torch.bfloat16, device="cuda")
+    for out in outs:
+        api().rssm_tree_attention(cache, q, table, ln, max(new), out, scratch, parents=None if parents is None else ints(parents), cu_seqlens=cu)
+    assert int(cache.error_word) == 0
+    assert all(torch.equal(out.view(torch.int16), outs[0].view(torch.int16)) for out in outs[1:])
+    check_rows(cache, table, lengths, new, q, parents, outs[0], d**-0.5)
