@@ -120,6 +120,18 @@ __global__ void __launch_bounds__(kThreads, kBlocks) logits_kernel(const LogitsA
   };
   ask(0);
 
+  // a request's parents, whatever its penalties
+  if (a.parents && t == 0 && rank == 0 && warp == 0) {
+    bool fine = true;
+#pragma unroll
+    for (int i = lane; i < kTreeT; i += 32)
+      if (i < n) {
+        const int up = a.parents[first + i];
+        fine = fine && up >= -1 && up < i;
+      }
+    if (!__all_sync(full, fine) && lane == 0) set_error(a.error_word, RSSM_ERRBIT_TREE);
+  }
+
   float temp = a.temperature ? a.temperature[b] : 1.0f;
   if (!(temp >= 0.0f)) temp = 1.0f;
   float rep = a.repetition ? a.repetition[b] : 1.0f;
@@ -147,7 +159,6 @@ __global__ void __launch_bounds__(kThreads, kBlocks) logits_kernel(const LogitsA
           mask = t < 32 ? m0 : m1;
         } else {
           mask = 1ull << t;
-          if (lane == 0 && rank == 0) set_error(a.error_word, RSSM_ERRBIT_TREE);
         }
       }
 #pragma unroll

@@ -1,4 +1,4 @@
-"""rssm_logits: ids at the ends of their type."""
+"""rssm_logits: ids at the ends of their type, and parents that are looked at whatever the penalties."""
 import random
 
 import pytest
@@ -34,3 +34,24 @@ def test_ids_at_the_ends_of_their_type_are_not_counted(V, dtype, off):
         L.call(c, out, probs=probs, error_word=word)
         check(c, out, probs)
     assert int(word) == 0
+
+
+@pytest.mark.parametrize("options", [{}, dict(temperature=None, repetition=None, presence=None, frequency=None)])
+@pytest.mark.parametrize("with_tokens", [True, False])
+def test_bad_parents_set_their_bit(options, with_tokens):
+    c = make(300, [3, 4, 2], 20, 1, tree=True)
+    c["parents"] = [-1, 0, 1, -1, 0, 2, 1, -1, 0]  # token 2 of the second row follows itself
+    if options:
+        n = len(c["lens"])
+        for name, x in (("temperature", 1.0), ("repetition", 1.0), ("presence", 0.0), ("frequency", 0.0)):
+            c[name] = torch.full((n,), x, device="cuda")
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.zeros(9, 300, device="cuda")
+    L.call(c, out, error_word=word, **options, **({} if with_tokens else dict(tokens=None)))
+    assert int(word) == L.api.ERRBIT_TREE
+    word.zero_()
+    c["parents"][5] = 1
+    L.call(c, out, error_word=word, **options, **({} if with_tokens else dict(tokens=None)))
+    assert int(word) == 0
+    if with_tokens:
+        check(c, out)
