@@ -764,7 +764,8 @@ def rssm_logits(logits, T, out, temperature=None, repetition=None, presence=None
         _f32(fn, "bias_value", bias_value, biases)
     sm = 0
     if mask is not None:
-        if mask.dtype is not torch.int32 or mask.dim() != 2 or mask.shape[0] < ntok or 32 * mask.shape[1] < vocab or mask.stride(1) != 1:
+        if mask.dtype is not torch.int32 or mask.dim() != 2 or mask.shape[0] < ntok or 32 * mask.shape[1] < vocab or \
+                (mask.shape[1] > 1 and mask.stride(1) != 1):
             _refuse(fn, f"mask must be int32 [{ntok}, {(vocab + 31) // 32}] with contiguous rows")
         sm = mask.stride(0) if mask.shape[0] > 1 else mask.shape[1]
     if error_word is not None and (error_word.element_size() != 4 or error_word.numel() < 1):
