@@ -605,10 +605,10 @@ class KVCache:
         return self._ref
 
 
-def _table(fn, pages, batch):
-    """Entries between the rows of a page table, and of a row."""
+def _table(fn, pages, batch, name="pages"):
+    """Entries between the rows of a page table (or of another int32 table), and of a row."""
     if pages.dtype is not torch.int32 or pages.dim() != 2 or pages.shape[0] < batch or (pages.shape[1] > 1 and pages.stride(1) != 1):
-        _refuse(fn, f"pages must be int32 [{batch}, pages of a row] with contiguous rows")
+        _refuse(fn, f"{name} must be int32 [{batch}, entries of a row] with contiguous rows")
     n = pages.shape[1]
     return (pages.stride(0) if pages.shape[0] > 1 else n), n
 
@@ -747,7 +747,7 @@ def rssm_logits(logits, T, out, temperature=None, repetition=None, presence=None
     if history is not None:
         if history_len is None:
             _refuse(fn, "history needs history_len")
-        sh, width = _table(fn, history, batch)
+        sh, width = _table(fn, history, batch, "history")
         _ids(fn, "history_len", history_len, batch)
         if prompt_len is not None:
             _ids(fn, "prompt_len", prompt_len, batch)

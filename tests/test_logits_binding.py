@@ -22,3 +22,12 @@ def test_a_mask_of_one_column_is_taken_whatever_its_stride():
             call(mask=mask)
     with pytest.raises(ValueError, match="mask must be"):
         call(mask=words[:, ::2])
+
+
+def test_a_message_names_the_argument_at_fault():
+    history, length = torch.zeros(2, 9, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for bad in (history.long(), history[:1], history.t(), history[0]):
+        with pytest.raises(ValueError, match=r"history must be int32 \[2, "):
+            call(history=bad, history_len=length)
+    with pytest.raises(ValueError, match=DEVICE):
+        call(history=history, history_len=length)
