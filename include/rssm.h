@@ -629,6 +629,7 @@ typedef struct {
  * others are written (a token that lies in two of them, where bounds fall, for both).
  * Positions past the page table and pages outside the cache: RSSM_ERRBIT_PAGE,
  * the token is skipped.  Two tokens of a call must not meet in one place of a page.
+ * A call with `tokens` 0 returns at once and looks at nothing.
  */
 rssm_status rssm_kv_append(const rssm_kv_cache *cache, int32_t layer, const void *k, int64_t k_stride, const void *v,
                            int64_t v_stride, const int32_t *pages, int64_t pages_stride, int32_t max_pages,

@@ -730,7 +730,8 @@ def rssm_logits(logits, T, out, temperature=None, repetition=None, presence=None
     """Penalties, biases, grammar masks and temperature on logits [tok, vocab]; out: the probabilities that rssm_verify takes, or
     (probs False) the processed logits.  `temperature` .. `frequency` [batch] f32; `history` [batch, most] int32 with `history_len`
     and `prompt_len` [batch]; `tokens`, `parents` [tok]; biases by request: `bias_start` [batch + 1], `bias_id`, `bias_value`;
-    `mask` [tok, words of 32 ids] int32.  Without cu_seqlens and `batch`, requests of T tokens each."""
+    `mask` [tok, words of 32 ids] int32.  Without cu_seqlens and `batch`, requests of T tokens each; rows
+    behind the last whole one belong to none and are left as they are (as rows behind the last request always are)."""
     fn = "rssm_logits"
     ntok, vocab = logits.shape
     if logits.dtype not in _DTYPE or out.dtype not in _DTYPE:

@@ -55,3 +55,14 @@ def test_bad_parents_set_their_bit(options, with_tokens):
     assert int(word) == 0
     if with_tokens:
         check(c, out)
+
+
+def test_rows_behind_the_last_request_are_left():
+    """Seven rows in requests of three tokens: two requests, and a row that belongs to none; the same with their number given."""
+    x = torch.randn(7, 50, generator=torch.Generator(device="cuda").manual_seed(0), device="cuda")
+    for kw, whole in ((dict(), 6), (dict(batch=1), 3), (dict(cu_seqlens=ints([0, 2, 5])), 5)):
+        out = torch.full((7, 50), 9.0, device="cuda")
+        L.api.rssm_logits(x, 3, out, **kw)
+        assert bool((out[whole:] == 9.0).all())
+        # expf of at most 12 off by 2^-23 (1 + 12), the sum of 50 and its reciprocal
+        assert (out[:whole].double() - torch.softmax(x[:whole].double(), -1)).abs().max() <= 2.0**-23 * 13 + 52 * 2.0**-24
