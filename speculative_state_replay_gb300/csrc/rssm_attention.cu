@@ -8,9 +8,10 @@
 // another until the pieces are joined.
 //
 // What bounds it is the cache's read: 64 rows of 8192 bf16 tokens, 8 heads of 128, 4
-// queries each, take 328 us, 6.5 TB/s.  8-bit codes are bound by the instructions that
-// make operands of them: the same in e4m3 210 us, 5.3 TB/s, in int8 234.  The scores' contraction index is permuted so
-// that a lane's part of a key is 16 bytes as they lie in the cache; 8-bit codes become
+// queries each, take 311 us, 6.9 TB/s.  8-bit codes are bound by the instructions that
+// make operands of them: the same in e4m3 197 us, 5.6 TB/s, in int8 223.  The scores'
+// contraction index is permuted so that a lane's part of a key is 16 bytes as they lie
+// in the cache; 8-bit codes become
 // fp16 exactly, on their way into the products.  The values' tile is read by transposing
 // loads; 8-bit ones come as pairs of neighbouring dimensions of two tokens, which two
 // byte permutations turn into the even and the odd dimension's operands.  In units of
@@ -78,9 +79,10 @@ struct Shape {
   static constexpr int NC = RB / 16;       // and its 16-byte chunks
   static constexpr int NL = NC / 4;        // chunks a lane takes of a key
   static constexpr int QS = D * 2 + (Q8 ? 16 : 64);  // bytes between queries: a quarter of a warp's reads fall on distinct banks
-  // blocks an SM: 8-bit codes are bound by instructions, and eight warps issue in half of the cycles only (64 rows of 8192
-  // tokens, heads of 128, e4m3: two blocks 234 us, three 225, of 64: 187, 150; since then 210 and 142); bf16 keys of 128 are bound by bytes, and three
-  // stages in flight of two blocks are worth more than two of three (332 us, 341)
+  // blocks an SM: 8-bit codes are bound by instructions, and eight warps issue in half of the
+  // cycles only (64 rows of 8192 tokens, one query token, e4m3, heads of 128: two blocks 227 us,
+  // three 197, of 64: 195, 133); bf16 keys of 128 are bound by bytes, and two blocks of three
+  // stages are what fits (three of two stages took 341 us where these took 332)
   static constexpr int kSm = MT == 1 && D * ESZ <= 128 ? 3 : 2;
   static constexpr int STAGES = Q8 && D < 256 ? 4 : 3;
   static constexpr int SB = 2 * kSlice * RB + (Q8 ? 2 * kSlice * 4 : 0);  // bytes of a stage: keys, values, their scales
@@ -534,8 +536,8 @@ cudaError_t run(const AttnArgs& args, int sms, cudaStream_t st) {
   }
   AttnArgs a = args;
   const int grid = S::kGrid * sms;
-  // up to 8 queries the joins are short, and a launch costs as much (one row of 8192 tokens, int8: 1 token 23 us, 26 apart;
-  // 4 tokens 38, 33 apart; 8 over 32768 99, 57 apart)
+  // up to 8 queries a head the joins are short, and a launch costs as much (one row of 8192 int8 tokens,
+  // heads of 128: 4 queries 20 us, 25 apart; 8 queries 25, 26 apart; 16 34, 32 apart; 32 81, 40 apart)
   a.apart = grid > 1 && static_cast<long long>(a.r.T) * a.group > 8;
   e = launch_pdl(attention_kernel<S>, dim3(grid), dim3(kThreads), S::kSmem, st, a);
   if (e != cudaSuccess || !a.apart) return e;

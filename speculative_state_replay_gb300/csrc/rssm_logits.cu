@@ -9,9 +9,9 @@
 // exponential.  Each block takes them against its own maximum; maxima and sums meet once
 // through the cluster's shared memory.  Rows of any alignment are read 16 bytes a lane:
 // places are counted from the 16-byte boundary before the row's first value.  252 rows
-// of 131073 bf16 values, 132 MB: 55 us without options, 105 us with a history of 8192
+// of 131073 bf16 values, 132 MB: 52 us without options, 106 us with a history of 8192
 // tokens (25 us: every block reads all of it), a mask and 100 biases a request.  Threads
-// a block: 256 take 50 us where 128 take 69 and 512 take 72 (no options, 131072 values).
+// a block: 256 take 52 us where 128 take 71 and 512 take 78 (no options, 131072 values).
 #include <cooperative_groups.h>
 
 #include "rssm_kv.cuh"
